@@ -132,7 +132,8 @@ def work(c):
 # the 4-bit layout, in torch: pages of 16-token tiles, per (page, kv head, tile) the bytes
 #   K codes [16][d/2], V codes [16][d/2], K scales bf16 [16][d/32], V scales bf16 [16][d/32]
 # a K row's 32-bit word c*G+g holds values 32g+8c.. (8 codes), a V row's 16-bit word i*G+g values 32g+4i.. (4 codes),
-# G = d/32; the V row of token t of its tile is row (t%2)*8 + t//2; codes are value+8 in [1, 15], low nibble first
+# G = d/32, low nibble first; the V row of token t of its tile is row (t%2)*8 + t//2; in each group of four nibbles, nibble n
+# has the magnitude of code n in its three low bits and the sign of code n ^ 2 in its high bit
 # ---------------------------------------------------------------------------------------------------------------
 def _nibbles_to_bytes(u):
     return u[..., 0::2] | (u[..., 1::2] << 4)
@@ -142,13 +143,28 @@ def _bytes_to_nibbles(b):
     return torch.stack((b & 15, b >> 4), -1).flatten(-2)
 
 
+def _other_sign(x):
+    """Entries n ^ 2 of each four."""
+    return x.unflatten(-1, (-1, 2, 2)).flip(-2).flatten(-3)
+
+
+def _codes_to_nibbles(c):
+    """Codes in -7 .. 7, in the order of the layout's words."""
+    return c.abs().to(torch.uint8) | (_other_sign(c < 0).to(torch.uint8) << 3)
+
+
+def _nibbles_to_codes(u):
+    c = (u & 7).float()
+    return torch.where(_other_sign(u) > 7, -c, c)
+
+
 def _quantise(x):
-    """fp32 [..., d] -> (codes + 8 as uint8 [..., d], scales bf16 [..., d/32])."""
+    """fp32 [..., d] -> (codes in fp32 [..., d], scales bf16 [..., d/32])."""
     g = x.unflatten(-1, (-1, GROUP))
     s = (g.abs().amax(-1) / 7).to(torch.bfloat16)
     sf = s.float().unsqueeze(-1)
     code = torch.where(sf > 0, (g / sf).round().clamp(-7, 7), torch.zeros_like(g))
-    return (code + 8).to(torch.uint8).flatten(-2), s
+    return code.flatten(-2), s
 
 
 def _pack(k, v):
@@ -160,7 +176,7 @@ def _pack(k, v):
         u, s = _quantise(x)
         u = u.permute(0, 2, 1, 3).reshape(np_, H, nt, 16, *inner).transpose(-3, -2).reshape(np_, H, nt, 16, d)
         s = s.permute(0, 2, 1, 3).reshape(np_, H, nt, 16 * G).contiguous().view(torch.uint8)
-        out.append((_nibbles_to_bytes(u), s))
+        out.append((_nibbles_to_bytes(_codes_to_nibbles(u)), s))
     (ku, ks), (vu, vs) = out
     vu = vu.unflatten(3, (8, 2)).transpose(3, 4).flatten(3, 4)
     return torch.cat((ku.flatten(3), vu.flatten(3), ks, vs), -1).reshape(np_, H, P, 9 * d // 8).contiguous()
@@ -176,8 +192,8 @@ def _unpack(rec, d):
     sc = t[..., 2 * half:].contiguous().view(torch.bfloat16).float().reshape(n, H, nt, 2, 16, G)
     got = []
     for j, (u, inner) in enumerate(((ku, (4, G, 8)), (vu, (8, G, 4)))):
-        c = _bytes_to_nibbles(u).reshape(n, H, nt, 16, *inner).transpose(-3, -2).reshape(n, H, nt, 16, G, GROUP)
-        x = (c.float() - 8) * sc[:, :, :, j].unsqueeze(-1)
+        c = _nibbles_to_codes(_bytes_to_nibbles(u)).reshape(n, H, nt, 16, *inner).transpose(-3, -2)
+        x = c.reshape(n, H, nt, 16, G, GROUP) * sc[:, :, :, j].unsqueeze(-1)
         got.append(x.reshape(n, H, P, d).transpose(1, 2))
     return got
 
@@ -440,7 +456,7 @@ def _store(s):
         k, v = s["k16"].flatten(0, 1)[to], s["v16"].flatten(0, 1)[to]
     for x, back in ((k, s["k_back"]), (v, s["v_back"])):
         u, sc = _quantise(x.float())
-        y = (u.float() - 8).unflatten(-1, (-1, GROUP)) * sc.float().unsqueeze(-1)
+        y = u.unflatten(-1, (-1, GROUP)) * sc.float().unsqueeze(-1)
         back.flatten(0, 1)[to] = y.flatten(-2).to(torch.bfloat16)
     return [s["k_back"], s["v_back"]]
 
@@ -531,9 +547,13 @@ def _exact_values(cache, pages, n, d):
     G = d // GROUP
     got = []
     for nib, base, row, sbase in ((kn, 0, t, 16 * d), (vn, 8 * d, (t % 2) * 8 + t // 2, 16 * d + 32 * G)):
-        byte = base + row[:, None] * (d // 2) + nib // 2
-        b = rows.gather(2, byte[:, None, :].expand(-1, rows.shape[1], -1))
-        code = torch.where((nib % 2).bool(), b >> 4, b & 15).double() - 8
+        def nibble(n):
+            byte = base + row[:, None] * (d // 2) + n // 2
+            b = rows.gather(2, byte[:, None, :].expand(-1, rows.shape[1], -1))
+            return torch.where((n % 2).bool(), b >> 4, b & 15).double()
+
+        sign = 1 - 2 * torch.floor(nibble(nib ^ 2) / 8)
+        code = torch.remainder(nibble(nib), 8) * sign
         at = sbase + t[:, None] * 2 * G + torch.arange(G, device=DEV) * 2
         lo = rows.gather(2, at[:, None, :].expand(-1, rows.shape[1], -1)).int()
         hi = rows.gather(2, at[:, None, :].expand(-1, rows.shape[1], -1) + 1).int()
