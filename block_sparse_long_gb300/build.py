@@ -1,9 +1,10 @@
-"""Build libcosa.so (the C-ABI library of the CUDA path) in-tree for sm_103a.
+"""Build libcosa.so (the C-ABI library of the CUDA path) and libcosa_kv.so (what stands around it: include/cosa_kv.h)
+in-tree for sm_103a.
 
 Compiles the translation units under csrc/ in parallel with nvcc and links them into
-block_sparse_long_gb300/libcosa.so.  The CUDA runtime is linked statically and the driver
-API is reached through the runtime's entry-point query, so the library loads on a machine
-without a GPU (its calls then fail with COSA_ERR_CUDA).
+block_sparse_long_gb300/libcosa.so and libcosa_kv.so.  The CUDA runtime is linked statically and the driver
+API is reached through the runtime's entry-point query, so the libraries load on a machine
+without a GPU (their calls then fail with COSA_ERR_CUDA).
 
     python -m block_sparse_long_gb300.build [--force] [--verbose]
 """
@@ -23,6 +24,9 @@ LIB = os.path.join(HERE, "libcosa.so")
 SOURCES = ["api.cu", "osk.cu", "osk_p16.cu", "osk_p32.cu", "osk_p64.cu", "osk_p128.cu", "osk_union_d64.cu",
            "osk_union_d128.cu", "kap.cu"]
 HEADERS = ["ptx.cuh", "internal.h", "osk_kernel.cuh", "osk_union_kernel.cuh"]
+KV_LIB = os.path.join(HERE, "libcosa_kv.so")
+KV_SOURCES = ["kv_api.cu", "kv_rope.cu", "kv_convert.cu", "kv_attention.cu", "kv_evict.cu"]
+KV_HEADERS = ["ptx.cuh", "kv_internal.h", "kv_layout.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-std=c++17", "-O3", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall", "--expt-relaxed-constexpr"]
 
@@ -34,23 +38,32 @@ def nvcc() -> str:
     return cand
 
 
-def _inputs():
-    files = [os.path.join(CSRC, s) for s in SOURCES + HEADERS]
-    files.append(os.path.join(ROOT, "include", "cosa.h"))
+def _inputs(sources, headers, public):
+    files = [os.path.join(CSRC, s) for s in sources + headers]
+    files += [os.path.join(ROOT, "include", h) for h in public]
     files.append(os.path.abspath(__file__))
     return files
 
 
+# library, its translation units, the headers they include
+LIBRARIES = ((LIB, SOURCES, HEADERS, ["cosa.h"]), (KV_LIB, KV_SOURCES, KV_HEADERS, ["cosa.h", "cosa_kv.h"]))
+
+
+def _stale(lib, sources, headers, public) -> bool:
+    if not os.path.exists(lib):
+        return True
+    t = os.path.getmtime(lib)
+    return any(os.path.getmtime(f) > t for f in _inputs(sources, headers, public))
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
-        return False
-    t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(f) <= t for f in _inputs())
+    return not any(_stale(*entry) for entry in LIBRARIES)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile and link libcosa.so if any input changed; returns its path."""
-    if not force and up_to_date():
+    """Compile and link the libraries whose inputs changed; returns the path of libcosa.so."""
+    todo = [entry for entry in LIBRARIES if force or _stale(*entry)]
+    if not todo:
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     cc = nvcc()
@@ -67,14 +80,16 @@ def build(force: bool = False, verbose: bool = False) -> str:
             sys.stderr.write(r.stdout + r.stderr)
         return obj
 
-    with ThreadPoolExecutor(len(SOURCES)) as ex:
-        objs = list(ex.map(compile_one, SOURCES))
-    tmp = LIB + ".tmp"
-    cmd = [cc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, LIB)
+    sources = [src for _, srcs, _, _ in todo for src in srcs]
+    with ThreadPoolExecutor(len(sources)) as ex:
+        objs = dict(zip(sources, ex.map(compile_one, sources)))
+    for lib, srcs, _, _ in todo:
+        tmp = lib + ".tmp"
+        cmd = [cc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *(objs[src] for src in srcs)]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+        os.replace(tmp, lib)
     return LIB
 
 

@@ -1,0 +1,67 @@
+// Host-side declarations of libcosa_kv: launch records shared by the C-ABI layer (kv_api.cu) and the
+// kernel files.
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "cosa_kv.h"
+
+namespace cosa_kv {
+
+struct RopeLaunch {
+  const uint16_t *q, *k, *v, *q_weight, *k_weight;
+  const double* inv_freq;
+  const int32_t *positions, *cu_seqlens, *start, *page_table;
+  uint16_t *q_out, *k_out, *k_cache, *v_cache;
+  int32_t* status;
+  int64_t q_stride, k_stride, v_stride;
+  int num_reqs, num_q_heads, num_kv_heads, head_dim, page_size, total_tokens, max_seqlen, num_pages, max_pages_per_req;
+  int rotary_dim, interleaved;
+  float eps;
+};
+cudaError_t launch_rope(const RopeLaunch& L, cudaStream_t stream);
+
+struct ConvertLaunch {
+  // store: k, v are the source (rows or pages); load: k_cache, v_cache the destination
+  const uint16_t *k, *v;
+  uint16_t *k_cache, *v_cache;
+  uint8_t* cache;
+  const int32_t *page_table, *other_table, *cu_seqlens, *start, *kv_len;
+  int32_t* status;
+  int64_t k_stride, v_stride;
+  int num_reqs, num_kv_heads, head_dim, page_size, total_tokens, max_seqlen, num_pages, num_kv4_pages, max_pages_per_req;
+};
+cudaError_t launch_store_rows(const ConvertLaunch& L, cudaStream_t stream);
+cudaError_t launch_store_pages(const ConvertLaunch& L, cudaStream_t stream);
+cudaError_t launch_load(const ConvertLaunch& L, cudaStream_t stream);
+
+struct AttnLaunch {
+  const uint16_t* q;
+  const int32_t *cu_seqlens, *page_table, *kv_len;
+  const uint8_t* cache;
+  uint16_t* out;
+  float* weights;
+  void* workspace;
+  int32_t* status;
+  int num_reqs, num_q_heads, num_kv_heads, head_dim, page_size, total_tokens, max_seqlen, num_kv4_pages, max_pages_per_req;
+  int max_new_tokens;
+  float scale_log2;      // sm_scale * log2(e)
+};
+size_t attn_workspace_bytes(int num_q_heads, int head_dim, int total_tokens, int max_seqlen, bool with_weights);
+cudaError_t launch_attention(const AttnLaunch& L, cudaStream_t stream);
+
+struct EvictLaunch {
+  uint8_t* cache;
+  const int32_t *page_table, *kv_len, *dst_page_table;
+  const float* weights;
+  int32_t *new_len, *kept;
+  float* weights_out;
+  int32_t* status;
+  int num_reqs, num_kv_heads, head_dim, page_size, max_seqlen, num_kv4_pages, max_pages_per_req, max_dst_pages;
+  int budget, sink, recent;
+};
+cudaError_t launch_evict(const EvictLaunch& L, cudaStream_t stream);
+
+}  // namespace cosa_kv
