@@ -1,10 +1,11 @@
 // K and V into the 4-bit cache and back (layout: include/cosa_kv.h).
 //
-// Per group of 32 values:  s = bf16(max|x| / 7),  c = clamp(rint(x / s), -7, 7).  Eight values of a
-// token's head are a lane's work: lane (g, c) of the D / 8 lanes of a row holds values 32 g + 8 c .. + 7,
-// which are one 32-bit word of the K layout and two 16-bit words of the V layout; the four lanes of a group
-// share their largest magnitude by two shuffles.  Both directions are memory bound: 4 d bytes of bf16
-// and 9/8 d bytes of cache per token and kv head.
+// Per group of 32 values:  s = bf16(max|x| / 7),  c = clamp(rint(x / s), -7, 7).  Four lanes have a row (token,
+// head): lane c of them holds values 32 g + 8 c .. + 7 of every group g, of K and of V, which are 16 (d = 128) or
+// 8 (d = 64) neighbouring bytes of the row's K codes and of its V codes; the four lanes of a group share its
+// largest magnitude by two shuffles.  Both directions are memory bound: 4 d bytes of bf16 and
+// 9/8 d bytes of cache per token and kv head.
+#include <algorithm>
 #include <cstdint>
 
 #include "cosa_kv.h"
@@ -15,34 +16,66 @@ namespace cosa_kv {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kTokens = 8;     // tokens of a CTA
+constexpr int kMaxTokens = 16;     // tokens of a CTA (a storage tile: its slots share their pages)
 
-// Codes of a lane's eight values, lowest nibble first, and the bits of their group's scale.  Nibble n of each
-// half has the magnitude of value n, and the sign of value n ^ 2 in its high bit.  Every lane of the warp calls it.
-__device__ __forceinline__ uint32_t quantise8(const uint4& u, uint32_t& scale_bits) {
+// Codes of eight values, lowest nibble first: nibble n of each half has the magnitude of value n, and the sign of
+// value n ^ 2 in its high bit.
+//
+// rint(x / s) without a division: |x| / s is formed to 2^-22 by the reciprocal and rounded to a multiple of 2^-10 by
+// the addition of 1.5 * 2^13.  Significands of 8 bits make a quotient that lies on a border k + 1/2 or at least 1/512
+// from it (2 X 2^e - (2 k + 1) S is a whole multiple of 1/2 where it is not zero, over 2 S <= 510), so the first
+// rounding puts every tie on its border exactly and moves nothing across one; the second addition rounds to even.
+__device__ __forceinline__ uint32_t codes8(const uint4& u, float s, float inv) {
   float x[8];
   unpack8(u, x);
-  // the magnitudes as integers keep their order, with infinities and NaN above every number
-  uint32_t m = 0;
+  uint32_t w = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(x[i]) & 0x7FFFFFFFu);
-  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-  m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-  if (m >= 0x7F800000u) {
-    scale_bits = 0x7FC0u;
-    return 0u;
+  for (int i = 0; i < 8; ++i) {
+    const float y = fmaf(fabsf(x[i]), inv, 12288.0f) - 12288.0f;
+    const uint32_t m = __float_as_uint(y + 12582912.0f) & 15u;
+    w |= m << (4 * i);
+    if (m != 0u && x[i] < 0.f) w |= 8u << (4 * (i ^ 2));
   }
-  const float s = __uint_as_float(cosa::pack_bf16x2(0.f, __uint_as_float(m) / 7.0f) & 0xFFFF0000u);
-  scale_bits = __float_as_uint(s) >> 16;
-  if (s == 0.f) return 0u;
+  return w;
+}
+
+// The same by the division, for scales whose reciprocal or codes leave the range (near the ends of bf16's).
+__device__ __noinline__ uint32_t codes8_slow(uint4 u, float s) {
+  float x[8];
+  unpack8(u, x);
   uint32_t w = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int c = static_cast<int>(fminf(fmaxf(rintf(x[i] / s), -7.f), 7.f));
     w |= static_cast<uint32_t>(abs(c)) << (4 * i);
-    w |= c < 0 ? 8u << (4 * (i ^ 2)) : 0u;
+    if (c < 0) w |= 8u << (4 * (i ^ 2));
   }
   return w;
+}
+
+// Codes of a lane's values, a word per group, and the bits of the groups' scales.  Every lane of the warp calls it.
+template <int G>
+__device__ __forceinline__ void quantise(const uint4 (&u)[G], uint32_t (&w)[G], uint32_t (&scale)[G]) {
+#pragma unroll
+  for (int g = 0; g < G; ++g) {
+    // two magnitudes at a time as integers: they keep their order, with infinities and NaN above every number
+    uint32_t m = __vmaxu2(__vmaxu2(u[g].x & 0x7FFF7FFFu, u[g].y & 0x7FFF7FFFu), __vmaxu2(u[g].z & 0x7FFF7FFFu, u[g].w & 0x7FFF7FFFu));
+    m = max(m & 0xFFFFu, m >> 16);
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    if (m >= 0x7F80u) {
+      scale[g] = 0x7FC0u;
+      w[g] = 0u;
+      continue;
+    }
+    const uint32_t bits = cosa::pack_bf16x2(__uint_as_float(m << 16) / 7.0f, 0.f) & 0xFFFFu;
+    const float s = __uint_as_float(bits << 16);
+    scale[g] = bits;
+    if (bits >= 0x0400u && bits < 0x7C00u)        // 2^-119 <= s < 2^121
+      w[g] = codes8(u[g], s, 1.0f / s);
+    else
+      w[g] = bits == 0u ? 0u : codes8_slow(u[g], s);
+  }
 }
 
 // Eight values from their codes: the products are exact in fp32 and rounded once.
@@ -56,18 +89,70 @@ __device__ __forceinline__ uint4 dequantise8(uint32_t w, float s) {
   return pack8(x);
 }
 
+// A lane's share of a row of K codes is one piece of the row; of a row of V codes too.
 template <int D>
-__device__ __forceinline__ void put(uint8_t* tile, int t, int lane, uint32_t kw, uint32_t ks, uint32_t vw, uint32_t vs) {
-  using T = Tile<D>;
-  const int g = lane / 4, c = lane % 4;
-  *reinterpret_cast<uint32_t*>(tile + t * T::kRow + (c * T::G + g) * 4) = kw;
-  uint16_t* v = reinterpret_cast<uint16_t*>(tile + T::kVCodes + v_row(t) * T::kRow);
-  v[(2 * c) * T::G + g] = static_cast<uint16_t>(vw);
-  v[(2 * c + 1) * T::G + g] = static_cast<uint16_t>(vw >> 16);
-  if (c == 0) {
-    *reinterpret_cast<uint16_t*>(tile + T::kKScales + (t * T::G + g) * 2) = static_cast<uint16_t>(ks);
-    *reinterpret_cast<uint16_t*>(tile + T::kVScales + (t * T::G + g) * 2) = static_cast<uint16_t>(vs);
+__device__ __forceinline__ void store_piece(uint8_t* at, const uint32_t (&w)[Tile<D>::G]) {
+  if constexpr (Tile<D>::G == 4)
+    *reinterpret_cast<uint4*>(at) = make_uint4(w[0], w[1], w[2], w[3]);
+  else
+    *reinterpret_cast<uint2*>(at) = make_uint2(w[0], w[1]);
+}
+
+template <int D>
+__device__ __forceinline__ void load_piece(const uint8_t* at, uint32_t (&w)[Tile<D>::G]) {
+  if constexpr (Tile<D>::G == 4) {
+    const uint4 u = *reinterpret_cast<const uint4*>(at);
+    w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
+  } else {
+    const uint2 u = *reinterpret_cast<const uint2*>(at);
+    w[0] = u.x; w[1] = u.y;
   }
+}
+
+// Between a word per group and the V order: 16-bit words i * G + g for i = 2c, then for i = 2c + 1.
+template <int G>
+__device__ __forceinline__ void to_v_order(const uint32_t (&w)[G], uint32_t (&v)[G]) {
+#pragma unroll
+  for (int g = 0; g < G; g += 2) {
+    v[g / 2] = __byte_perm(w[g], w[g + 1], 0x5410);
+    v[G / 2 + g / 2] = __byte_perm(w[g], w[g + 1], 0x7632);
+  }
+}
+template <int G>
+__device__ __forceinline__ void from_v_order(const uint32_t (&v)[G], uint32_t (&w)[G]) {
+#pragma unroll
+  for (int g = 0; g < G; g += 2) {
+    w[g] = __byte_perm(v[g / 2], v[G / 2 + g / 2], 0x5410);
+    w[g + 1] = __byte_perm(v[g / 2], v[G / 2 + g / 2], 0x7632);
+  }
+}
+
+// A row's codes and scales into token t of its tile (lane c of the row's four).
+template <int D>
+__device__ __forceinline__ void put(uint8_t* tile, int t, int c, const uint32_t (&kw)[Tile<D>::G], const uint32_t (&ks)[Tile<D>::G],
+                                    const uint32_t (&vw)[Tile<D>::G], const uint32_t (&vs)[Tile<D>::G]) {
+  using T = Tile<D>;
+  constexpr int G = T::G;
+  store_piece<D>(tile + t * T::kRow + c * 4 * G, kw);
+  uint32_t v[G];
+  to_v_order<G>(vw, v);
+  store_piece<D>(tile + T::kVCodes + v_row(t) * T::kRow + c * 4 * G, v);
+  if (c < 2) {                                 // lane 0 writes the K scales, lane 1 the V scales
+    uint8_t* at = tile + (c ? T::kVScales : T::kKScales) + t * G * 2;
+    uint32_t two[G / 2];
+#pragma unroll
+    for (int g = 0; g < G; g += 2) two[g / 2] = c ? vs[g] | (vs[g + 1] << 16) : ks[g] | (ks[g + 1] << 16);
+    if constexpr (G == 4)
+      *reinterpret_cast<uint2*>(at) = make_uint2(two[0], two[1]);
+    else
+      *reinterpret_cast<uint32_t*>(at) = two[0];
+  }
+}
+
+template <int G>
+__device__ __forceinline__ void load_row(const uint16_t* src, int c, bool in, uint4 (&u)[G]) {
+#pragma unroll
+  for (int g = 0; g < G; ++g) u[g] = in ? *reinterpret_cast<const uint4*>(src + 32 * g + 8 * c) : make_uint4(0, 0, 0, 0);
 }
 
 // Slots first .. end - 1 of request b; a contradiction gives an empty range and the status.
@@ -82,20 +167,20 @@ __device__ __forceinline__ int page_of(const int32_t* table, const ConvertLaunch
   return phys >= 0 && phys < pages ? phys : -1;
 }
 
-// Rows packed by cu_seqlens; a CTA takes kTokens tokens of the batch.
+// Rows packed by cu_seqlens; a CTA takes `tokens` tokens of the batch.
 template <int D>
-__global__ void __launch_bounds__(kThreads) store_rows_kernel(const ConvertLaunch L) {
-  constexpr int kLanes = D / 8;
-  __shared__ int s_slot[kTokens], s_phys[kTokens];
+__global__ void __launch_bounds__(kThreads) store_rows_kernel(const ConvertLaunch L, const int tokens) {
+  constexpr int G = Tile<D>::G;
+  __shared__ int s_slot[kMaxTokens], s_phys[kMaxTokens];
   const int tid = threadIdx.x;
-  const int t0 = blockIdx.x * kTokens;
+  const int t0 = blockIdx.x * tokens;
   const int last = L.cu_seqlens[L.num_reqs];
   if (blockIdx.x == 0 && tid == 0 && (L.cu_seqlens[0] != 0 || last > L.total_tokens))
     cosa::report_status(L.status, cosa::kStatusBadInput);
-  const int ntok = min(kTokens, min(last, L.total_tokens) - t0);
+  const int ntok = min(tokens, min(last, L.total_tokens) - t0);
   if (ntok <= 0) return;
-  if (tid / 32 < ntok) {
-    const int t = t0 + tid / 32, lane = tid % 32;
+  for (int j = tid / 32; j < ntok; j += blockDim.x / 32) {
+    const int t = t0 + j, lane = tid % 32;
     int b = 0;
     for (int i = lane; i < L.num_reqs; i += 32) b += L.cu_seqlens[i + 1] <= t;
     b = __reduce_add_sync(0xffffffffu, b);
@@ -104,110 +189,129 @@ __global__ void __launch_bounds__(kThreads) store_rows_kernel(const ConvertLaunc
       const int64_t slot = off < 0 ? -1 : static_cast<int64_t>(off) + (L.start ? L.start[b] : 0);
       const bool fits = slot >= 0 && slot < L.max_seqlen;
       if (!fits) cosa::report_status(L.status, cosa::kStatusBadInput);
-      s_slot[tid / 32] = fits ? static_cast<int>(slot) : 0;
-      s_phys[tid / 32] = fits ? page_of(L.page_table, L, b, static_cast<int>(slot), L.num_kv4_pages) : -1;
+      s_slot[j] = fits ? static_cast<int>(slot) : 0;
+      s_phys[j] = fits ? page_of(L.page_table, L, b, static_cast<int>(slot), L.num_kv4_pages) : -1;
     }
   }
   __syncthreads();
-  const int lane = tid % kLanes;
+  const int c = tid % 4;
   const int rows = ntok * L.num_kv_heads;
-  for (int r0 = 0; r0 < rows; r0 += kThreads / kLanes) {     // uniform: the shuffles need every lane
-    const int r = r0 + tid / kLanes;
+  for (int r0 = 0; r0 < rows; r0 += blockDim.x / 4) {     // uniform: the shuffles need every lane
+    const int r = r0 + tid / 4;
     const bool in = r < rows;
     const int j = in ? r / L.num_kv_heads : 0;
     const int h = in ? r - j * L.num_kv_heads : 0;
     const int64_t t = t0 + j;
-    uint4 ku = make_uint4(0, 0, 0, 0), vu = ku;
-    if (in) {
-      ku = *reinterpret_cast<const uint4*>(L.k + t * L.k_stride + static_cast<int64_t>(h) * D + 8 * lane);
-      vu = *reinterpret_cast<const uint4*>(L.v + t * L.v_stride + static_cast<int64_t>(h) * D + 8 * lane);
-    }
-    uint32_t ks, vs;
-    const uint32_t kw = quantise8(ku, ks), vw = quantise8(vu, vs);
+    uint4 ku[G], vu[G];
+    load_row<G>(L.k + t * L.k_stride + static_cast<int64_t>(h) * D, c, in, ku);
+    load_row<G>(L.v + t * L.v_stride + static_cast<int64_t>(h) * D, c, in, vu);
+    uint32_t kw[G], ks[G], vw[G], vs[G];
+    quantise<G>(ku, kw, ks);
+    quantise<G>(vu, vw, vs);
     if (in && s_phys[j] >= 0)
-      put<D>(L.cache + tile_offset<D>(s_phys[j], h, s_slot[j], L.num_kv_heads, L.page_size), s_slot[j] % kTile, lane, kw,
-             ks, vw, vs);
+      put<D>(L.cache + tile_offset<D>(s_phys[j], h, s_slot[j], L.num_kv_heads, L.page_size), s_slot[j] % kTile, c, kw, ks,
+             vw, vs);
   }
 }
 
-// Pages to pages; a CTA takes kTokens slots of request blockIdx.y.  LOAD: from the cache to bf16 pages.
+// Pages to pages: the CTAs of request blockIdx.y take `tokens` slots at a time.  LOAD: from the cache to bf16 pages.
 template <int D, bool LOAD>
-__global__ void __launch_bounds__(kThreads) pages_kernel(const ConvertLaunch L) {
+__global__ void __launch_bounds__(kThreads) pages_kernel(const ConvertLaunch L, const int tokens) {
   using T = Tile<D>;
-  constexpr int kLanes = D / 8;
+  constexpr int G = T::G;
   const int tid = threadIdx.x;
   const int b = blockIdx.y;
   const Range range = slots_of(L, b, L.kv_len[b], L.start ? L.start[b] : 0);
   if (!range.ok && blockIdx.x == 0 && tid == 0) cosa::report_status(L.status, cosa::kStatusBadInput);
+  const int c = tid % 4;
+  const int rows = tokens * L.num_kv_heads;
   // from the tile boundary at or before the first slot
-  const int64_t s0 = static_cast<int64_t>(range.first / kTile * kTile) + static_cast<int64_t>(blockIdx.x) * kTokens;
-  if (s0 >= range.end) return;
-  const int slot0 = static_cast<int>(s0);
-  // kTokens divides 16, so the slots of a CTA share their pages
-  const int p4 = page_of(L.page_table, L, b, slot0, L.num_kv4_pages);
-  const int p16 = page_of(L.other_table, L, b, slot0, L.num_pages);
-  if (p4 < 0 || p16 < 0) return;
-  const int lane = tid % kLanes;
-  const int rows = kTokens * L.num_kv_heads;
-  for (int r0 = 0; r0 < rows; r0 += kThreads / kLanes) {     // uniform: the shuffles need every lane
-    const int r = r0 + tid / kLanes;
-    const int j = r < rows ? r / L.num_kv_heads : 0;
-    const int h = r < rows ? r - j * L.num_kv_heads : 0;
-    const int slot = slot0 + j;
-    const bool in = r < rows && slot >= range.first && slot < range.end;
-    const size_t at = ((static_cast<size_t>(p16) * L.page_size + slot % L.page_size) * L.num_kv_heads + h) * D + 8 * lane;
-    uint8_t* tile = L.cache + tile_offset<D>(p4, h, slot, L.num_kv_heads, L.page_size);
-    const int t = slot % kTile;
-    if (LOAD) {
-      if (!in) continue;
-      const int g = lane / 4, c = lane % 4;
-      const uint32_t kw = *reinterpret_cast<const uint32_t*>(tile + t * T::kRow + (c * T::G + g) * 4);
-      const uint16_t* v = reinterpret_cast<const uint16_t*>(tile + T::kVCodes + v_row(t) * T::kRow);
-      const uint32_t vw = v[(2 * c) * T::G + g] | (static_cast<uint32_t>(v[(2 * c + 1) * T::G + g]) << 16);
-      const float ks = bf16_lo(*reinterpret_cast<const uint16_t*>(tile + T::kKScales + (t * T::G + g) * 2));
-      const float vs = bf16_lo(*reinterpret_cast<const uint16_t*>(tile + T::kVScales + (t * T::G + g) * 2));
-      *reinterpret_cast<uint4*>(L.k_cache + at) = dequantise8(kw, ks);
-      *reinterpret_cast<uint4*>(L.v_cache + at) = dequantise8(vw, vs);
-    } else {
-      uint4 ku = make_uint4(0, 0, 0, 0), vu = ku;
-      if (in) {
-        ku = *reinterpret_cast<const uint4*>(L.k + at);
-        vu = *reinterpret_cast<const uint4*>(L.v + at);
+  for (int64_t s0 = range.first / kTile * kTile + static_cast<int64_t>(blockIdx.x) * tokens; s0 < range.end;
+       s0 += static_cast<int64_t>(gridDim.x) * tokens) {
+    const int slot0 = static_cast<int>(s0);
+    const int p4 = page_of(L.page_table, L, b, slot0, L.num_kv4_pages);
+    const int p16 = page_of(L.other_table, L, b, slot0, L.num_pages);
+    if (p4 < 0 || p16 < 0) continue;
+    for (int r0 = 0; r0 < rows; r0 += blockDim.x / 4) {     // uniform: the shuffles need every lane
+      const int r = r0 + tid / 4;
+      const int j = r < rows ? r / L.num_kv_heads : 0;
+      const int h = r < rows ? r - j * L.num_kv_heads : 0;
+      const int slot = slot0 + j;
+      const bool in = r < rows && slot >= range.first && slot < range.end;
+      const size_t at = ((static_cast<size_t>(p16) * L.page_size + slot % L.page_size) * L.num_kv_heads + h) * D;
+      uint8_t* tile = L.cache + tile_offset<D>(p4, h, slot, L.num_kv_heads, L.page_size);
+      const int t = slot % kTile;
+      if (LOAD) {
+        if (!in) continue;
+        uint32_t kw[G], v[G], vw[G];
+        load_piece<D>(tile + t * T::kRow + c * 4 * G, kw);
+        load_piece<D>(tile + T::kVCodes + v_row(t) * T::kRow + c * 4 * G, v);
+        from_v_order<G>(v, vw);
+        const uint32_t* ks = reinterpret_cast<const uint32_t*>(tile + T::kKScales + t * G * 2);
+        const uint32_t* vs = reinterpret_cast<const uint32_t*>(tile + T::kVScales + t * G * 2);
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          *reinterpret_cast<uint4*>(L.k_cache + at + 32 * g + 8 * c) = dequantise8(kw[g], g % 2 ? bf16_hi(ks[g / 2]) : bf16_lo(ks[g / 2]));
+          *reinterpret_cast<uint4*>(L.v_cache + at + 32 * g + 8 * c) = dequantise8(vw[g], g % 2 ? bf16_hi(vs[g / 2]) : bf16_lo(vs[g / 2]));
+        }
+      } else {
+        uint4 ku[G], vu[G];
+        load_row<G>(L.k + at, c, in, ku);
+        load_row<G>(L.v + at, c, in, vu);
+        uint32_t kw[G], ks[G], vw[G], vs[G];
+        quantise<G>(ku, kw, ks);
+        quantise<G>(vu, vw, vs);
+        if (in) put<D>(tile, t, c, kw, ks, vw, vs);
       }
-      uint32_t ks, vs;
-      const uint32_t kw = quantise8(ku, ks), vw = quantise8(vu, vs);
-      if (in) put<D>(tile, t, lane, kw, ks, vw, vs);
     }
   }
 }
 
 }  // namespace
 
+namespace {
+
+// Four threads per row: a CTA of tokens that fill 256 of them where the heads are few.
+struct Shape {
+  int tokens, threads;
+  explicit Shape(int heads) : tokens(heads >= 8 ? 8 : kMaxTokens), threads((std::min(kThreads, 4 * tokens * heads) + 31) / 32 * 32) {}
+};
+
+// CTAs per request: one for each group of tokens, but no more than 32 per SM over the batch, so that requests much
+// shorter than max_seqlen (or a late `start`) leave few CTAs without work (0.6 ns each).
+dim3 pages_grid(const ConvertLaunch& L, int tokens) {
+  const int64_t most = std::max<int64_t>(1, 32 * 152 / L.num_reqs);
+  return dim3(static_cast<unsigned>(std::min<int64_t>(most, (static_cast<int64_t>(L.max_seqlen) + tokens - 1) / tokens)),
+              static_cast<unsigned>(L.num_reqs));
+}
+
+template <bool LOAD>
+cudaError_t launch_pages(const ConvertLaunch& L, cudaStream_t stream) {
+  const Shape s(L.num_kv_heads);
+  if (L.head_dim == 128)
+    pages_kernel<128, LOAD><<<pages_grid(L, s.tokens), s.threads, 0, stream>>>(L, s.tokens);
+  else
+    pages_kernel<64, LOAD><<<pages_grid(L, s.tokens), s.threads, 0, stream>>>(L, s.tokens);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
 cudaError_t launch_store_rows(const ConvertLaunch& L, cudaStream_t stream) {
-  const unsigned grid = static_cast<unsigned>((L.total_tokens + kTokens - 1) / kTokens);
+  const Shape s(L.num_kv_heads);
+  // few rows: a token per CTA
+  const int tokens = L.total_tokens <= 8 * 152 ? 1 : s.tokens;
+  const int threads = std::min(s.threads, (4 * tokens * L.num_kv_heads + 31) / 32 * 32);
+  const unsigned grid = static_cast<unsigned>((static_cast<int64_t>(L.total_tokens) + tokens - 1) / tokens);
   if (L.head_dim == 128)
-    store_rows_kernel<128><<<grid, kThreads, 0, stream>>>(L);
+    store_rows_kernel<128><<<grid, threads, 0, stream>>>(L, tokens);
   else
-    store_rows_kernel<64><<<grid, kThreads, 0, stream>>>(L);
+    store_rows_kernel<64><<<grid, threads, 0, stream>>>(L, tokens);
   return cudaGetLastError();
 }
 
-cudaError_t launch_store_pages(const ConvertLaunch& L, cudaStream_t stream) {
-  const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(L.max_seqlen) + kTokens - 1) / kTokens), static_cast<unsigned>(L.num_reqs));
-  if (L.head_dim == 128)
-    pages_kernel<128, false><<<grid, kThreads, 0, stream>>>(L);
-  else
-    pages_kernel<64, false><<<grid, kThreads, 0, stream>>>(L);
-  return cudaGetLastError();
-}
+cudaError_t launch_store_pages(const ConvertLaunch& L, cudaStream_t stream) { return launch_pages<false>(L, stream); }
 
-cudaError_t launch_load(const ConvertLaunch& L, cudaStream_t stream) {
-  const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(L.max_seqlen) + kTokens - 1) / kTokens), static_cast<unsigned>(L.num_reqs));
-  if (L.head_dim == 128)
-    pages_kernel<128, true><<<grid, kThreads, 0, stream>>>(L);
-  else
-    pages_kernel<64, true><<<grid, kThreads, 0, stream>>>(L);
-  return cudaGetLastError();
-}
+cudaError_t launch_load(const ConvertLaunch& L, cudaStream_t stream) { return launch_pages<true>(L, stream); }
 
 }  // namespace cosa_kv
