@@ -3,11 +3,18 @@
 // Per (request, kv head): of the slots that exist, the first `sink` and last `recent` ones, then those with the
 // largest weights (ties: the lowest slot), `budget` in all; kept slots move in order into other pages.
 //
-// A slot's weight becomes a 32-bit key that sorts as the weight does (missing pages 0, NaN 1, kept in any
-// case the largest), so the K-th largest key is found by a radix select and everything above it is
-// kept, with the lowest slots among the equal ones.  The move copies whole rows of codes and scales.
-// Work: 4 bytes per slot and 9/4 d bytes per kept slot, memory bound.
+// A slot's weight becomes a 32-bit key that sorts as the weight does (missing pages 0, NaN 1, kept in any case the
+// largest).  A cluster of one to eight CTAs has the slots of one (request, kv head), a run each, their keys in shared
+// memory.  The K-th largest key is found by a radix select, 11 bits at a time from the top: every CTA counts its
+// keys' digits, sums its share of the bins over the cluster through distributed shared memory, and looks the
+// digit up among the sums.  Everything above the K-th key is kept, and the lowest slots among the equal ones; the
+// numbers of both in the earlier CTAs and threads give each kept slot its place.  The move then copies whole rows
+// of codes and scales.  Work: 8 bytes per slot and 9/4 d bytes per kept slot, memory bound; the select is bound by
+// the latency of its few cluster barriers.
+#include <algorithm>
 #include <cstdint>
+
+#include <cooperative_groups.h>
 
 #include "cosa_kv.h"
 #include "kv_internal.h"
@@ -16,7 +23,13 @@
 namespace cosa_kv {
 namespace {
 
-constexpr int kSelectThreads = 1024;
+namespace cg = cooperative_groups;
+
+constexpr int kSelectThreads = 512;
+constexpr int kWarps = kSelectThreads / 32;
+constexpr int kCluster = 8;             // CTAs of a cluster at most
+constexpr int kBins = 2048;
+constexpr int kMaxKeys = 16384;         // keys that a CTA holds; longer runs are formed again for each pass
 constexpr uint32_t kMissing = 0u, kNan = 1u, kAlways = 0xFFFFFFFFu;
 
 __device__ __forceinline__ uint32_t key_of(float w) {
@@ -35,102 +48,185 @@ __device__ __forceinline__ int page_of(const int32_t* table, int pitch, const Ev
   return phys >= 0 && phys < L.num_kv4_pages ? phys : -1;
 }
 
-// Exclusive prefix of a flag over the CTA and the CTA's total.
-__device__ __forceinline__ int block_prefix(bool flag, int* s_warp, int& total) {
-  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  const unsigned m = __ballot_sync(0xffffffffu, flag);
-  __syncthreads();
-  if (lane == 0) s_warp[warp] = __popc(m);
-  __syncthreads();
-  int v = s_warp[lane];          // kSelectThreads / 32 = 32 warps
-  const int own = v;
+// Inclusive sum over a warp's lanes.
+__device__ __forceinline__ int warp_scan(int v) {
+  const int lane = threadIdx.x % 32;
 #pragma unroll
   for (int k = 1; k < 32; k *= 2) {
     const int x = __shfl_up_sync(0xffffffffu, v, k);
     if (lane >= k) v += x;
   }
-  total = __shfl_sync(0xffffffffu, v, 31);
-  return __shfl_sync(0xffffffffu, v - own, warp) + __popc(m & ((1u << lane) - 1u));
+  return v;
 }
 
+// Exclusive sum over the CTA's threads, and the CTA's total.  Ends with the CTA synchronised.
+__device__ __forceinline__ int block_scan(int v, int* s_warp, int& total) {
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const int end = warp_scan(v);
+  if (lane == 31) s_warp[warp] = end;
+  __syncthreads();
+  const int w = lane < kWarps ? s_warp[lane] : 0;
+  const int sums = warp_scan(w);
+  total = __shfl_sync(0xffffffffu, sums, kWarps - 1);
+  const int before = __shfl_sync(0xffffffffu, sums - w, warp);
+  __syncthreads();
+  return before + end - v;
+}
+
+struct SelectSmem {
+  int hist[kBins];                // this CTA's digits
+  int sums[kBins];                // this CTA's share of the bins over the cluster: kBins / ctas of them
+  int share_total;                // their total
+  int counts[2];                  // keep and want of the passes; then this CTA's keys above the K-th, and equal to it
+  int warp[32];
+  uint32_t digit;
+};
+
+// HELD: the run's keys fit in shared memory.  They are padded so that threads that walk neighbouring runs of keys do
+// not meet in a bank.
+__host__ __device__ constexpr int padded(int i) { return i + i / 32; }
+
+template <bool HELD>
 __global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictLaunch L) {
-  __shared__ int s_hist[256];
-  __shared__ int s_warp[32];
-  __shared__ uint32_t s_prefix;
-  __shared__ int s_want, s_keep;
+  extern __shared__ uint32_t s_keys[];
+  __shared__ SelectSmem sm;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int ctas = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
   const int tid = threadIdx.x;
-  const int b = blockIdx.x / L.num_kv_heads, h = blockIdx.x % L.num_kv_heads;
+  const int item = static_cast<int>(blockIdx.x) / ctas;
+  const int b = item / L.num_kv_heads, h = item % L.num_kv_heads;
   const int n = length_of(L, b);
-  if (tid == 0 && h == 0 && n != L.kv_len[b]) cosa::report_status(L.status, cosa::kStatusBadInput);
+  if (tid == 0 && rank == 0 && h == 0 && n != L.kv_len[b]) cosa::report_status(L.status, cosa::kStatusBadInput);
   const size_t row = static_cast<size_t>(b) * L.num_kv_heads + h;
   const float* w = L.weights + row * L.max_seqlen;
-  auto key = [&](int s) -> uint32_t {
+  // this CTA's run of slots, and this thread's part of it
+  const int run = (n + ctas - 1) / ctas;
+  const int lo = min(n, rank * run), hi = min(n, lo + run);
+  const int per = (run + kSelectThreads - 1) / kSelectThreads;
+
+  auto form = [&](int s) -> uint32_t {
     if (page_of(L.page_table, L.max_pages_per_req, L, b, s) < 0) return kMissing;
     if (s < L.sink || s >= n - L.recent) return kAlways;
     return key_of(w[s]);
   };
+  auto key = [&](int s) -> uint32_t { return HELD ? s_keys[padded(s - lo)] : form(s); };
+  if (HELD) {
+    for (int s = lo + tid; s < hi; s += kSelectThreads) s_keys[padded(s - lo)] = form(s);
+  }
 
-  // the K-th largest key, eight bits at a time from the top
-  uint32_t prefix = 0;
-  int want = 0, keep = 0;
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    if (tid < 256) s_hist[tid] = 0;
+  const int share = kBins / ctas;
+  uint32_t prefix = 0;              // the digits found so far
+  int want = 0, keep = 0;           // how many keys with this prefix are kept; how many keys in all
+  int used = 0;                     // bits of the prefix
+#pragma unroll 1
+  for (int pass = 0; pass < 3; ++pass) {
+    const int bits = pass == 2 ? 10 : 11, shift = 32 - used - bits;
+    for (int i = tid; i < kBins; i += kSelectThreads) sm.hist[i] = 0;
     __syncthreads();
-    for (int s = tid; s < n; s += kSelectThreads) {
+    for (int s = lo + tid; s < hi; s += kSelectThreads) {
       const uint32_t k = key(s);
-      if (k != kMissing && (shift == 24 || (k >> (shift + 8)) == prefix)) atomicAdd(&s_hist[(k >> shift) & 255u], 1);
+      if (k != kMissing && (pass == 0 || (k >> (shift + bits)) == prefix)) atomicAdd(&sm.hist[(k >> shift) & ((1u << bits) - 1u)], 1);
+    }
+    cluster.sync();
+    // this CTA's share of the bins, summed over the cluster
+    for (int i = tid; i < share; i += kSelectThreads) {
+      int v = 0;
+      for (int r = 0; r < ctas; ++r) v += cluster.map_shared_rank(sm.hist, r)[rank * share + i];
+      sm.sums[i] = v;
     }
     __syncthreads();
-    if (tid < 32) {          // lane l has bins 255 - 8 l down to 248 - 8 l
-      int mine = 0;
-      for (int j = 0; j < 8; ++j) mine += s_hist[255 - 8 * tid - j];
-      int end = mine;
-#pragma unroll
-      for (int k = 1; k < 32; k *= 2) {
-        const int x = __shfl_up_sync(0xffffffffu, end, k);
-        if (tid >= k) end += x;
-      }
-      if (shift == 24) {
+    if (tid < 32) {
+      int v = 0;
+      for (int i = tid; i < share; i += 32) v += sm.sums[i];
+      v = __reduce_add_sync(0xffffffffu, v);
+      if (tid == 0) sm.share_total = v;
+    }
+    cluster.sync();
+    // the digit: shares from the top, then the bins of the share that has it (a warp, in every CTA alike)
+    if (tid < 32) {
+      const int r = ctas - 1 - tid;                   // lane 0 has the top share
+      const int mine = r >= 0 ? *cluster.map_shared_rank(&sm.share_total, r) : 0;
+      int end = warp_scan(mine);
+      if (pass == 0) {
         keep = min(L.budget, __shfl_sync(0xffffffffu, end, 31));
         want = keep;
-        if (tid == 0) s_keep = keep;
+      } else {
+        keep = sm.counts[0];
+        want = sm.counts[1];
       }
-      const unsigned past = __ballot_sync(0xffffffffu, end >= want);
-      if (want > 0 && tid == __ffs(past) - 1) {
-        int before = end - mine, j = 0;
-        while (before + s_hist[255 - 8 * tid - j] < want) before += s_hist[255 - 8 * tid - j++];
-        s_prefix = (prefix << 8) | static_cast<uint32_t>(255 - 8 * tid - j);
-        s_want = want - before;
+      const int at = __ffs(__ballot_sync(0xffffffffu, end >= want)) - 1;      // want <= the total: there is one
+      const int owner = ctas - 1 - at;
+      int before = __shfl_sync(0xffffffffu, end - mine, at);
+      const int* sums = cluster.map_shared_rank(sm.sums, max(owner, 0));
+      uint32_t digit = 0;
+      for (int i0 = share - 1; owner >= 0; i0 -= 32) {                        // ends in the share: its total reaches want
+        const int i = i0 - tid;
+        const int v = i >= 0 ? sums[i] : 0;
+        const int e = warp_scan(v);
+        const unsigned hit = __ballot_sync(0xffffffffu, before + e >= want);
+        if (hit || i0 < 32) {
+          const int lane = hit ? __ffs(hit) - 1 : 0;
+          digit = static_cast<uint32_t>(owner * share + i0 - lane);
+          before += __shfl_sync(0xffffffffu, e - v, lane);
+          break;
+        }
+        before += __shfl_sync(0xffffffffu, e, 31);
+      }
+      if (tid == 0) {
+        sm.digit = digit;
+        sm.counts[0] = keep;
+        sm.counts[1] = want - before;
       }
     }
     __syncthreads();
-    keep = s_keep;
-    if (keep == 0) break;    // uniform: nothing exists
-    prefix = s_prefix;
-    want = s_want;
+    keep = sm.counts[0];
+    want = sm.counts[1];
+    prefix = (prefix << bits) | sm.digit;
+    used += bits;
+    if (keep == 0) break;           // the same in the whole cluster: no slot exists
   }
+  // here `prefix` is the K-th largest key and `want` the number of its equals that are kept
 
-  // kept slots in ascending order
   int32_t* kept = L.kept + row * L.budget;
-  int out = 0, ties = 0;
-  for (int s0 = 0; keep > 0 && s0 < n; s0 += kSelectThreads) {
-    const int s = s0 + tid;
-    const uint32_t k = s < n ? key(s) : kMissing;
-    int total;
-    const int tie = ties + block_prefix(k == prefix && k != kMissing, s_warp, total);
-    ties += total;
-    const bool in = k != kMissing && (k > prefix || (k == prefix && tie < want));
-    const int at = out + block_prefix(in, s_warp, total);
-    out += total;
-    if (in) kept[at] = s;
+  if (keep > 0) {
+    // thread tid has slots lo + tid * per ..; padded() keeps the threads of a warp apart
+    const int first = lo + tid * per, last = min(hi, first + per);
+    int above = 0, equal = 0;
+    for (int s = first; s < last; ++s) {
+      const uint32_t k = key(s);
+      above += k > prefix;
+      equal += k == prefix;
+    }
+    int total_above, total_equal;
+    above = block_scan(above, sm.warp, total_above);
+    equal = block_scan(equal, sm.warp, total_equal);
+    cluster.sync();                 // nobody reads the counts of the passes any more
+    if (tid == 0) {
+      sm.counts[0] = total_above;
+      sm.counts[1] = total_equal;
+    }
+    cluster.sync();
+    for (int r = 0; r < rank; ++r) {
+      const int* c = cluster.map_shared_rank(sm.counts, r);
+      above += c[0];
+      equal += c[1];
+    }
+    int at = above + min(equal, want);
+    for (int s = first; s < last; ++s) {
+      const uint32_t k = key(s);
+      if (k > prefix || (k == prefix && equal++ < want)) {
+        kept[at] = s;
+        if (L.weights_out) L.weights_out[row * L.max_seqlen + at] = w[s];
+        ++at;
+      }
+    }
   }
-  for (int j = keep + tid; j < L.budget; j += kSelectThreads) kept[j] = -1;
-  if (tid == 0 && h == 0) L.new_len[b] = keep;
-  if (L.weights_out) {
-    __syncthreads();
-    float* o = L.weights_out + row * L.max_seqlen;
-    for (int j = tid; j < L.max_seqlen; j += kSelectThreads) o[j] = j < keep ? w[kept[j]] : 0.f;
-  }
+  for (int j = keep + rank * kSelectThreads + tid; j < L.budget; j += ctas * kSelectThreads) kept[j] = -1;
+  if (L.weights_out)
+    for (int j = keep + rank * kSelectThreads + tid; j < L.max_seqlen; j += ctas * kSelectThreads)
+      L.weights_out[row * L.max_seqlen + j] = 0.f;
+  if (tid == 0 && rank == 0 && h == 0) L.new_len[b] = keep;
+  cluster.sync();                   // a CTA's shared memory lives until its neighbours have read it
 }
 
 // One destination tile of 16 slots per CTA.
@@ -173,11 +269,36 @@ __global__ void __launch_bounds__(128) move_kernel(const EvictLaunch L) {
   }
 }
 
+// A cluster of as many CTAs as give each about 4096 slots: below that, the pass over the keys costs less than the
+// barriers that sharing it takes.
+cudaError_t launch_select(const EvictLaunch& L, cudaStream_t stream) {
+  int ctas = 1;
+  while (ctas < kCluster && static_cast<int64_t>(ctas) * 4096 < L.max_seqlen) ctas *= 2;
+  const int run = (L.max_seqlen - 1) / ctas + 1;
+  const bool held = run <= kMaxKeys;
+  cudaLaunchConfig_t c{};
+  c.gridDim = dim3(static_cast<unsigned>(L.num_reqs * L.num_kv_heads * ctas));
+  c.blockDim = dim3(kSelectThreads);
+  c.dynamicSmemBytes = held ? static_cast<size_t>(padded(run)) * 4 : 0;
+  c.stream = stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = static_cast<unsigned>(ctas);
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  c.attrs = &attr;
+  c.numAttrs = 1;
+  auto* kernel = held ? select_kernel<true> : select_kernel<false>;
+  if (held) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, padded(kMaxKeys) * 4);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaLaunchKernelEx(&c, kernel, L);
+}
+
 }  // namespace
 
 cudaError_t launch_evict(const EvictLaunch& L, cudaStream_t stream) {
-  select_kernel<<<static_cast<unsigned>(L.num_reqs * L.num_kv_heads), kSelectThreads, 0, stream>>>(L);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e = launch_select(L, stream);
   if (e != cudaSuccess) return e;
   const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(L.budget) + kTile - 1) / kTile), static_cast<unsigned>(L.num_kv_heads),
                   static_cast<unsigned>(L.num_reqs));
