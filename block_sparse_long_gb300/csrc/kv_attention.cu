@@ -19,7 +19,9 @@
 // run of it, whatever the lengths are.  A CTA that has all of a (request, kv head, row tile) writes its
 // output; otherwise it leaves its maximum, sum and unnormalised output in the workspace (a CTA has at
 // most two unfinished ones, the first and the last of its run) and kv4_combine_kernel joins them in order.
+#include <algorithm>
 #include <cstdint>
+#include <type_traits>
 
 #include "cosa_kv.h"
 #include "kv_internal.h"
@@ -49,6 +51,7 @@ struct Args {
   float* logits;      // [Hkv][T * g][pitch]: logits as the first product leaves them, with weights only
   int64_t pitch;
   int group;          // Hq / Hkv
+  int page_shift;     // log2(P)
 };
 
 struct Request {
@@ -232,18 +235,19 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attention_kernel(co
     uint32_t there = 0;               // per stage: the tile's page exists
     auto page_at = [&](int t) -> int {
       if (t >= t_end || t * kTile >= r.len) return -1;
-      const int phys = table[t * kTile / L.page_size];
+      const int phys = table[(t * kTile) >> a.page_shift];
       return phys < L.num_kv4_pages ? phys : -1;
     };
+    const uint8_t* head = L.cache + (static_cast<size_t>(h) << (a.page_shift - 4)) * T::kBytes + lane * 16;
+    const size_t page_bytes = (static_cast<size_t>(L.num_kv_heads) << (a.page_shift - 4)) * T::kBytes;
+    const int tile_mask = (1 << (a.page_shift - 4)) - 1;
     auto issue = [&](int t, int stage, int phys) {
       if (phys >= 0) {
-        const uint8_t* src = L.cache + tile_offset<D>(phys, h, t * kTile, L.num_kv_heads, L.page_size);
-        const uint32_t dst = cosa::smem_u32(sm.ring[warp][stage]);
+        const uint8_t* src = head + phys * page_bytes + (t & tile_mask) * T::kBytes;
+        const uint32_t dst = cosa::smem_u32(sm.ring[warp][stage]) + lane * 16;
 #pragma unroll
-        for (int k = 0; k < (T::kBytes + 511) / 512; ++k) {
-          const int at16 = (k * 32 + lane) * 16;
-          if (at16 < T::kBytes) copy16(dst + at16, src + at16);
-        }
+        for (int k = 0; k < (T::kBytes + 511) / 512; ++k)
+          if (k < T::kBytes / 512 || lane * 16 < T::kBytes % 512) copy16(dst + k * 512, src + k * 512);
         there |= 1u << stage;
       } else {
         there &= ~(1u << stage);
@@ -377,32 +381,39 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attention_kernel(co
           vw[k][0] = *reinterpret_cast<const uint32_t*>(src);
         }
       }
+      auto product = [&](auto all) {
 #pragma unroll
-      for (int g = 0; g < G; ++g) {
-        uint32_t pb[NT][2];
+        for (int g = 0; g < G; ++g) {
+          uint32_t pb[NT][2];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const float s0 = g % 2 ? bf16_hi(vs[j][g / 2]) : bf16_lo(vs[j][g / 2]);
-          const float s1 = g % 2 ? bf16_hi(vs[j][G / 2 + g / 2]) : bf16_lo(vs[j][G / 2 + g / 2]);
+          for (int j = 0; j < 2; ++j) {
+            const float s0 = g % 2 ? bf16_hi(vs[j][g / 2]) : bf16_lo(vs[j][g / 2]);
+            const float s1 = g % 2 ? bf16_hi(vs[j][G / 2 + g / 2]) : bf16_lo(vs[j][G / 2 + g / 2]);
+#pragma unroll
+            for (int x = 0; x < NT; ++x) {
+              float y0 = p[x][2 * j] * s0, y1 = p[x][2 * j + 1] * s1;
+              if constexpr (!decltype(all)::value) {      // an unseen token adds nothing, whatever its scale is
+                if (!((seen >> (4 * x + 2 * j)) & 1u)) y0 = 0.f;
+                if (!((seen >> (4 * x + 2 * j + 1)) & 1u)) y1 = 0.f;
+              }
+              pb[x][j] = cosa::pack_bf16x2(y0, y1);
+            }
+          }
+          // the group's codes of both tokens of a pair, and the same with the bytes exchanged
+          const uint32_t sel = g % 2 ? 0x7632 : 0x5410, swp = g % 2 ? 0x6723 : 0x4501;
+          const uint32_t w0 = __byte_perm(vw[0][g / 2], vw[1][g / 2], sel), z0 = __byte_perm(vw[0][g / 2], vw[1][g / 2], swp);
+          const uint32_t w1 = __byte_perm(vw[2][g / 2], vw[3][g / 2], sel), z1 = __byte_perm(vw[2][g / 2], vw[3][g / 2], swp);
 #pragma unroll
           for (int x = 0; x < NT; ++x) {
-            float y0 = p[x][2 * j] * s0, y1 = p[x][2 * j + 1] * s1;
-            // an unseen token adds nothing, whatever its scale is
-            if (!((seen >> (4 * x + 2 * j)) & 1u)) y0 = 0.f;
-            if (!((seen >> (4 * x + 2 * j + 1)) & 1u)) y1 = 0.f;
-            pb[x][j] = cosa::pack_bf16x2(y0, y1);
+            mma_bf16(o[x][2 * g], codes<0>(w0, z0), codes<1>(w0, z0), codes<0>(w1, z1), codes<1>(w1, z1), pb[x][0], pb[x][1]);
+            mma_bf16(o[x][2 * g + 1], codes<2>(w0, z0), codes<3>(w0, z0), codes<2>(w1, z1), codes<3>(w1, z1), pb[x][0], pb[x][1]);
           }
         }
-        // the group's codes of both tokens of a pair, and the same with the bytes exchanged
-        const uint32_t sel = g % 2 ? 0x7632 : 0x5410, swp = g % 2 ? 0x6723 : 0x4501;
-        const uint32_t w0 = __byte_perm(vw[0][g / 2], vw[1][g / 2], sel), z0 = __byte_perm(vw[0][g / 2], vw[1][g / 2], swp);
-        const uint32_t w1 = __byte_perm(vw[2][g / 2], vw[3][g / 2], sel), z1 = __byte_perm(vw[2][g / 2], vw[3][g / 2], swp);
-#pragma unroll
-        for (int x = 0; x < NT; ++x) {
-          mma_bf16(o[x][2 * g], codes<0>(w0, z0), codes<1>(w0, z0), codes<0>(w1, z1), codes<1>(w1, z1), pb[x][0], pb[x][1]);
-          mma_bf16(o[x][2 * g + 1], codes<2>(w0, z0), codes<3>(w0, z0), codes<2>(w1, z1), codes<3>(w1, z1), pb[x][0], pb[x][1]);
-        }
-      }
+      };
+      if (clear)
+        product(std::true_type{});
+      else
+        product(std::false_type{});
 
       __syncwarp();                   // every lane has read the stage
       issue(t + kStages * kWarps, stage, next_phys);
@@ -481,52 +492,97 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attention_kernel(co
   if (tid == 0) a.owner[me] = own;
 }
 
-// Joins the parts of the items that no CTA had whole: block (owner CTA, row), a thread per value.
+// Joins the parts of the items that no CTA had whole: block (x, row) goes through the owner CTAs x, x + gridDim.x, ...
+// The parts' maxima and sums are read at once, then their outputs, eight in flight per thread.
 template <int D, int NT, bool WEIGHTS>
-__global__ void __launch_bounds__(D) combine_kernel(const Args a) {
+__global__ void __launch_bounds__(D) combine_kernel(const Args a, const int ctas) {
   constexpr int kRows = 8 * NT;
-  const Owner own = a.owner[blockIdx.x];
-  if (own.b < 0) return;
-  const Request r = request_of(a, own.b, kRows, false);
-  const int row = own.rt * kRows + static_cast<int>(blockIdx.y);
-  if (row >= static_cast<int64_t>(r.n) * a.group) return;
-  const int d = threadIdx.x;
-  float M = -INFINITY, sum = 0.f, v = 0.f;
-  for (int j = blockIdx.x; j <= own.last; ++j) {
-    const size_t at = (static_cast<size_t>(j) * 2 + (j == static_cast<int>(blockIdx.x) ? 1 : 0)) * 16 + blockIdx.y;
-    const float mj = a.part_ml[at * 2], sj = a.part_ml[at * 2 + 1], oj = a.part_o[at * D + d];
-    const float m_new = fmaxf(M, mj);
-    const float f = M == -INFINITY ? 1.f : cosa::ex2_approx(M - m_new), fj = mj == -INFINITY ? 1.f : cosa::ex2_approx(mj - m_new);
-    sum = sum * f + sj * fj;
-    v = v * f + oj * fj;
-    M = m_new;
-  }
-  const int tok = row / a.group, head = row - tok * a.group;
-  const float y = sum == 0.f ? 0.f : v * (kDown / (sum * (1.0f / kUp)));
-  a.L.out[((static_cast<int64_t>(r.tok0) + tok) * a.L.num_q_heads + own.h * a.group + head) * D + d] =
-      static_cast<uint16_t>(cosa::pack_bf16x2(y, y));
-  if (WEIGHTS && d == 0) {
-    float* st = a.stats + ((static_cast<int64_t>(own.h) * a.L.total_tokens + r.tok0) * a.group + row) * 2;
-    st[0] = M;
-    st[1] = sum * (1.0f / kUp);
+  __shared__ float s_factor[kMaxCtas];
+  __shared__ float s_red[2][D / 32];
+  const int d = threadIdx.x, warp = d / 32, lane = d % 32;
+  for (int first = blockIdx.x; first < ctas; first += gridDim.x) {
+    const Owner own = a.owner[first];
+    if (own.b < 0) continue;
+    const Request r = request_of(a, own.b, kRows, false);
+    const int row = own.rt * kRows + static_cast<int>(blockIdx.y);
+    if (row >= static_cast<int64_t>(r.n) * a.group) continue;
+    // part j: the second place of the owner, the first of every later CTA
+    auto place = [&](int j) { return (static_cast<size_t>(first + j) * 2 + (j == 0 ? 1 : 0)) * 16 + blockIdx.y; };
+    const int parts = own.last - first + 1;
+    float M = -INFINITY;
+    for (int j = d; j < parts; j += D) M = fmaxf(M, a.part_ml[place(j) * 2]);
+#pragma unroll
+    for (int m = 16; m > 0; m /= 2) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, m));
+    if (lane == 0) s_red[0][warp] = M;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < D / 32; ++w) M = fmaxf(M, s_red[0][w]);
+    float sum = 0.f;
+    for (int j = d; j < parts; j += D) {
+      const float m = a.part_ml[place(j) * 2];
+      const float f = m == -INFINITY ? 1.f : cosa::ex2_approx(m - M);     // nothing seen: sums of zero, or NaN
+      s_factor[j] = f;
+      sum = fmaf(f, a.part_ml[place(j) * 2 + 1], sum);
+    }
+#pragma unroll
+    for (int m = 16; m > 0; m /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+    if (lane == 0) s_red[1][warp] = sum;
+    __syncthreads();
+    sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < D / 32; ++w) sum += s_red[1][w];
+    float v = 0.f;
+#pragma unroll 8
+    for (int j = 0; j < parts; ++j) v = fmaf(s_factor[j], a.part_o[place(j) * D + d], v);
+    const int tok = row / a.group, head = row - tok * a.group;
+    const float y = sum == 0.f ? 0.f : v * (kDown / (sum * (1.0f / kUp)));
+    a.L.out[((static_cast<int64_t>(r.tok0) + tok) * a.L.num_q_heads + own.h * a.group + head) * D + d] =
+        static_cast<uint16_t>(cosa::pack_bf16x2(y, y));
+    if (WEIGHTS && d == 0) {
+      float* st = a.stats + ((static_cast<int64_t>(own.h) * a.L.total_tokens + r.tok0) * a.group + row) * 2;
+      st[0] = M;
+      st[1] = sum * (1.0f / kUp);
+    }
+    __syncthreads();
   }
 }
 
-// weights[b, h, s] += sum over the rows of exp2(scale * logit - M) / sum, rows in order.
-__global__ void __launch_bounds__(256) weights_kernel(const Args a, int rows_per_tile) {
+// weights[b, h, s] += sum over the rows of exp2(scale * logit - M) / sum, rows in order; four slots per thread.
+constexpr int kWeightRows = 32;       // rows whose maxima and sums a CTA holds at a time
+__global__ void __launch_bounds__(256) weights_kernel(const Args a, const int rows_per_tile) {
+  __shared__ float2 s_stat[kWeightRows];
   const int b = blockIdx.z, h = blockIdx.y;
   const Request r = request_of(a, b, rows_per_tile, false);
-  const int slot = static_cast<int>(blockIdx.x) * 256 + threadIdx.x;
-  if (slot >= r.len) return;
+  const int slot = (static_cast<int>(blockIdx.x) * 256 + threadIdx.x) * 4;
+  if (static_cast<int>(blockIdx.x) * 1024 >= r.len || r.n == 0) return;
+  const bool in = slot < r.len;
   const int64_t row0 = (static_cast<int64_t>(h) * a.L.total_tokens + r.tok0) * a.group;
-  const int rows = r.n * a.group;
-  float w = 0.f;
-  for (int i = 0; i < rows; ++i) {
-    const float M = a.stats[(row0 + i) * 2], sum = a.stats[(row0 + i) * 2 + 1];
-    const float s = a.logits[(row0 + i) * a.pitch + slot];
-    if (sum != 0.f && s != -INFINITY) w += cosa::ex2_approx(fmaf(s, a.L.scale_log2, -M)) / sum;
+  const int64_t rows = static_cast<int64_t>(r.n) * a.group;
+  float w[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int64_t i0 = 0; i0 < rows; i0 += kWeightRows) {
+    const int n = static_cast<int>(min(static_cast<int64_t>(kWeightRows), rows - i0));    // unseen slots have -inf
+    __syncthreads();
+    if (threadIdx.x < n) {
+      const float2 st = *reinterpret_cast<const float2*>(a.stats + (row0 + i0 + threadIdx.x) * 2);
+      s_stat[threadIdx.x] = make_float2(-st.x, 1.0f / st.y);
+    }
+    __syncthreads();
+    if (!in) continue;
+#pragma unroll 8
+    for (int i = 0; i < n; ++i) {
+      const float2 st = s_stat[i];
+      const float4 s = *reinterpret_cast<const float4*>(a.logits + (row0 + i0 + i) * a.pitch + slot);
+      w[0] += s.x == -INFINITY ? 0.f : cosa::ex2_approx(fmaf(s.x, a.L.scale_log2, st.x)) * st.y;
+      w[1] += s.y == -INFINITY ? 0.f : cosa::ex2_approx(fmaf(s.y, a.L.scale_log2, st.x)) * st.y;
+      w[2] += s.z == -INFINITY ? 0.f : cosa::ex2_approx(fmaf(s.z, a.L.scale_log2, st.x)) * st.y;
+      w[3] += s.w == -INFINITY ? 0.f : cosa::ex2_approx(fmaf(s.w, a.L.scale_log2, st.x)) * st.y;
+    }
   }
-  a.L.weights[(static_cast<int64_t>(b) * a.L.num_kv_heads + h) * a.L.max_seqlen + slot] += w;
+  if (!in) return;
+  float* dst = a.L.weights + (static_cast<int64_t>(b) * a.L.num_kv_heads + h) * a.L.max_seqlen + slot;
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    if (slot + k < r.len) dst[k] += w[k];
 }
 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
@@ -541,10 +597,10 @@ cudaError_t launch(const Args& a, cudaStream_t stream) {
   constexpr int kCtas = kMaxCtas / NT;
   kernel<<<kCtas, kThreads, smem, stream>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  combine_kernel<D, NT, WEIGHTS><<<dim3(kCtas, 8 * NT), D, 0, stream>>>(a);
+  combine_kernel<D, NT, WEIGHTS><<<dim3(std::min(kCtas, 64), 8 * NT), D, 0, stream>>>(a, kCtas);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   if (WEIGHTS) {
-    const dim3 grid(static_cast<unsigned>((a.L.max_seqlen + 255LL) / 256), static_cast<unsigned>(a.L.num_kv_heads),
+    const dim3 grid(static_cast<unsigned>((a.L.max_seqlen + 1023LL) / 1024), static_cast<unsigned>(a.L.num_kv_heads),
                     static_cast<unsigned>(a.L.num_reqs));
     weights_kernel<<<grid, 256, 0, stream>>>(a, 8 * NT);
     e = cudaGetLastError();
@@ -570,6 +626,7 @@ cudaError_t launch_attention(const AttnLaunch& L, cudaStream_t stream) {
   a.L = L;
   a.L.scale_log2 = L.scale_log2 * kDown;      // of the logits as the first product leaves them
   a.group = L.num_q_heads / L.num_kv_heads;
+  for (a.page_shift = 4; (1 << a.page_shift) < L.page_size;) ++a.page_shift;
   a.pitch = (static_cast<int64_t>(L.max_seqlen) + kTile - 1) / kTile * kTile;
   uint8_t* w = static_cast<uint8_t*>(L.workspace);
   a.owner = reinterpret_cast<Owner*>(w);
