@@ -284,6 +284,7 @@ int cosa_kv4_evict(const cosa_kv_params* p, void* kv4_cache, const int32_t* page
   L.budget = p->budget;
   L.sink = p->sink;
   L.recent = p->recent;
+  for (L.page_shift = 4; (1 << L.page_shift) < p->page_size;) ++L.page_shift;
   return done(cosa_kv::launch_evict(L, static_cast<cudaStream_t>(stream)));
 }
 

@@ -2,10 +2,12 @@
 //
 // Per (request, kv head) the rows are the request's query tokens times the Hq / Hkv query heads of the
 // kv head, eight or sixteen of them at a time:  o = softmax(scale q K^T) V with K = c_k s_k, V = c_v s_v.
-// Both products run on mma.sync m16n8k16 with bf16 operands and fp32 sums:
-//   q K^T   A = q (exact), B = the codes of 8 tokens; the codes of one scale group (32 values = two
-//           products) are summed apart and then multiplied by the token's scale in fp32;
-//   p V     A = V^T codes (16 values of the head by 16 tokens), B = p * s per scale group in bf16.
+// Both products run on mma.sync m16n8k16 with bf16 operands and fp32 sums, the tokens or the head's values as the
+// sixteen rows and the query rows as the eight columns, so that no part of an instruction is empty for eight rows:
+//   K q^T   A = the codes of 16 tokens, B = q (exact); the codes of one scale group (32 values = two products) are
+//           summed apart and then multiplied by the token's scale in fp32;
+//   V^T p   A = the codes of 16 values of the head by 16 tokens, B = p * s per scale group in bf16, turned from the
+//           first product's layout (tokens down) to the second's (tokens across) by movmatrix.
 // A code of magnitude m becomes the subnormal bf16 number +-m 2^-129 (three bits of significand and the sign
 // bit where the layout has them), two codes by a shift and an AND; matrix instructions take subnormal
 // operands exactly.  The other operands carry 2^96 to keep the products normal: q is multiplied by it, and
@@ -30,16 +32,19 @@
 namespace cosa_kv {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kStages = 4;        // tiles in flight per warp
-constexpr int kMaxCtas = 304;     // two per SM; one with sixteen rows to a tile, which take twice the registers
-constexpr int kMinTiles = 8;      // tiles per CTA at least: one per warp
+constexpr int kSms = 152;
+constexpr int kMaxCtas = 3 * kSms;
+constexpr int kMinTiles = 8;      // tiles per CTA at least, where a request is shared between CTAs
+constexpr int kWholeTiles = 16;   // tiles of an item that one CTA takes alone
+constexpr int kFewItems = 64;     // items up to which the join has a block per row
 
 // What a CTA leaves about the unfinished (request, kv head, row tile) that begins in its run.
 struct Owner {
-  int b, h, rt;     // b < 0: none
+  int rows;         // query rows of the tile; 0: none
   int last;         // last CTA that has a part of it
+  int tok0, h, rt;  // first row of q of the request, kv head, row tile
 };
 
 struct Args {
@@ -73,45 +78,78 @@ __device__ __forceinline__ Request request_of(const Args& a, int b, int rows, bo
   return r;
 }
 
-__device__ __forceinline__ int64_t warp_sum(int64_t v) {
-#pragma unroll
-  for (int m = 16; m > 0; m /= 2) v += __shfl_xor_sync(0xffffffffu, v, m);
-  return v;
+// A quotient of numbers that are not negative, with the 32-bit division where it is enough (a fifth of the 64-bit one's
+// time, and there are several in a row before a CTA's first load).
+__device__ __forceinline__ int64_t quotient(int64_t x, int64_t y) {
+  if (((x | y) >> 32) == 0) return static_cast<uint32_t>(x) / static_cast<uint32_t>(y);
+  return x / y;
 }
 
-// All units of the batch (whole warp).
-__device__ __forceinline__ int64_t total_units(const Args& a, int rows, bool tell) {
-  int64_t u = 0;
-  for (int b = threadIdx.x % 32; b < a.L.num_reqs; b += 32) {
-    const Request r = request_of(a, b, rows, tell);
-    u += r.tiles * r.rts * a.L.num_kv_heads;
+// The units of the batch in even shares: the first `more` CTAs have one more than `each`.
+struct Shares {
+  int64_t units, items, each, more;
+  int ctas;
+  __device__ __forceinline__ int64_t begin(int64_t cta) const { return cta * each + min(cta, more); }
+  __device__ __forceinline__ int owner(int64_t unit) const {
+    const int64_t big = more * (each + 1);
+    return static_cast<int>(unit < big ? quotient(unit, each + 1) : more + quotient(unit - big, each));
   }
-  return warp_sum(u);
+};
+
+// This lane's request of the 32 from b0, its units, and their sum up to and with it (whole warp).
+struct LaneUnits {
+  int64_t own, end, items;
+};
+__device__ __forceinline__ LaneUnits lane_units(const Args& a, int rows, int b0, bool tell) {
+  const int lane = threadIdx.x % 32;
+  LaneUnits u{0, 0, 0};
+  if (b0 + lane < a.L.num_reqs) {
+    const Request r = request_of(a, b0 + lane, rows, tell);
+    u.items = r.rts * a.L.num_kv_heads;
+    u.own = r.tiles * u.items;
+  }
+  u.end = u.own;
+#pragma unroll
+  for (int m = 1; m < 32; m *= 2) {
+    const int64_t v = __shfl_up_sync(0xffffffffu, u.end, m);
+    if (lane >= m) u.end += v;
+  }
+  return u;
 }
 
-// Request that holds unit `at`, and the unit at which it begins (whole warp).
-__device__ __forceinline__ int find_request(const Args& a, int rows, int64_t at, int64_t& begin) {
-  const int lane = threadIdx.x % 32;
+// The batch's shares (whole warp).  `first`: what the lanes have of the first 32 requests, for find_request.
+__device__ __forceinline__ Shares shares_of(const Args& a, int rows, int grid, bool tell, LaneUnits& first) {
+  Shares s{0, 0, 0, 0, 0};
+  for (int b0 = 0; b0 < a.L.num_reqs; b0 += 32) {
+    const LaneUnits u = lane_units(a, rows, b0, tell);
+    if (b0 == 0) first = u;
+    s.units += __shfl_sync(0xffffffffu, u.end, 31);
+    int64_t n = u.items;
+#pragma unroll
+    for (int m = 16; m > 0; m /= 2) n += __shfl_xor_sync(0xffffffffu, n, m);
+    s.items += n;
+  }
+  // Short contexts stay whole: with up to kWholeTiles tiles in the average item, a CTA takes at least one item, and no
+  // parts are left to join.  Else at least a tile for each warp.
+  const int64_t fit = s.units <= kWholeTiles * s.items ? s.items : max(s.items, quotient(s.units, kMinTiles));
+  s.ctas = static_cast<int>(max(static_cast<int64_t>(1), min(static_cast<int64_t>(grid), fit)));
+  s.each = quotient(s.units, s.ctas);
+  s.more = s.units - s.each * s.ctas;
+  return s;
+}
+
+// Request that holds unit `at`, and the unit at which it begins (whole warp; `at` is below the batch's units).
+__device__ __forceinline__ int find_request(const Args& a, int rows, int64_t at, const LaneUnits& first, int64_t& begin) {
   int64_t base = 0;
   for (int b0 = 0; b0 < a.L.num_reqs; b0 += 32) {
-    int64_t u = 0;
-    if (b0 + lane < a.L.num_reqs) {
-      const Request r = request_of(a, b0 + lane, rows, false);
-      u = r.tiles * r.rts * a.L.num_kv_heads;
-    }
-    int64_t end = u;
-#pragma unroll
-    for (int m = 1; m < 32; m *= 2) {
-      const int64_t v = __shfl_up_sync(0xffffffffu, end, m);
-      if (lane >= m) end += v;
-    }
-    const unsigned past = __ballot_sync(0xffffffffu, base + end > at);
+    const LaneUnits u = b0 == 0 ? first : lane_units(a, rows, b0, false);
+    const unsigned past = __ballot_sync(0xffffffffu, base + u.end > at);
     if (past) {
-      const int first = __ffs(past) - 1;
-      begin = base + __shfl_sync(0xffffffffu, end - u, first);
-      return b0 + first;
+      const int lane = __ffs(past) - 1;
+      begin = base + __shfl_sync(0xffffffffu, u.end - u.own, lane);
+      return b0 + lane;
     }
-    base += __shfl_sync(0xffffffffu, end, 31);
+    base += __shfl_sync(0xffffffffu, u.end, 31);
   }
   begin = base;
   return a.L.num_reqs;
@@ -122,6 +160,14 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
   asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The same with a sum that begins at zero.
+__device__ __forceinline__ void mma_bf16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                               uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
@@ -137,41 +183,75 @@ __device__ __forceinline__ uint32_t codes(uint32_t w, uint32_t swapped) {
   return (P % 2 ? x : x << 4) & 0x80708070u;
 }
 
+// An 8 x 8 matrix of 16-bit values, a row in four lanes, transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ void fma2(float& d0, float& d1, float a0, float a1, float b0, float b1) {      // d += a * b
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 d, {%0, %1};\n\t"
+      "fma.rn.f32x2 d, a, b, d;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "+f"(d0), "+f"(d1)
+      : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+__device__ __forceinline__ void mul2(float& d0, float& d1, float a0, float a1, float b0, float b1) {
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d0), "=f"(d1)
+      : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+
 constexpr float kUp = 79228162514264337593543950336.0f;      // 2^96
 constexpr float kDown = 8589934592.0f;                       // 2^33
+
+// The kernels after the first are launched while it runs; this waits until the grid before has ended and its
+// writes are visible.  Every thread calls it first of all.
+__device__ __forceinline__ void wait_for_grid_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// A warp takes TP tiles at a time: with eight rows two, whose chains of dependent instructions fill each other's gaps (one
+// tile alone has too few independent ones); with sixteen rows one, for the registers.
+template <int NT>
+struct Steps {
+  static constexpr int TP = NT == 1 ? 2 : 1;
+  static constexpr int kStages = NT == 1 ? 2 : 4;      // steps in flight per warp
+  static constexpr int kCtas = NT == 1 ? 3 : 2;        // CTAs of an SM: 168 or 255 registers a thread
+};
 
 template <int D, int NT>
 struct AttnSmem {
   static constexpr int kRows = 8 * NT;
-  alignas(16) uint8_t ring[kWarps][kStages][Tile<D>::kBytes];
+  alignas(16) uint8_t ring[kWarps][Steps<NT>::kStages][Steps<NT>::TP * Tile<D>::kBytes];
   alignas(16) float o[kWarps][kRows][D];
   float ml[kWarps][kRows][2];
 };
 
-// Rows of a warp's accumulators: lane = 4 i + c.  In q K^T a lane holds rows i (and i + 8) and tokens
-// 2c, 2c + 1 of each 8-token half; in p V it holds rows 2c, 2c + 1 (of each 8-row half) and of every scale
-// group g the values 32 g + 4 i .. + 3.
+// A warp's accumulators: lane = 4 i + c has query rows 2c and 2c + 1 of each eight; of the logits the tokens i and i + 8,
+// of the output the values 32 g + 4 i .. + 3 of every scale group g.
 template <int D, int NT, bool WEIGHTS>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attention_kernel(const Args a) {
+__global__ void __launch_bounds__(kThreads, Steps<NT>::kCtas) attention_kernel(const Args a) {
   using T = Tile<D>;
   constexpr int G = T::G;
   constexpr int kRows = 8 * NT;
+  constexpr int TP = Steps<NT>::TP, kStages = Steps<NT>::kStages, kStep = TP * kWarps;
   extern __shared__ __align__(16) uint8_t smem_raw[];
   AttnSmem<D, NT>& sm = *reinterpret_cast<AttnSmem<D, NT>*>(smem_raw);
   const AttnLaunch& L = a.L;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, i = lane / 4, c = lane % 4;
 
-  const int64_t units = total_units(a, kRows, blockIdx.x == 0 && warp == 0);
-  const int64_t ctas = min(static_cast<int64_t>(gridDim.x), max(static_cast<int64_t>(1), units / kMinTiles));
-  const int64_t me = blockIdx.x;
-  Owner own{-1, 0, 0, 0};
-  if (me >= ctas || units == 0) {
+  LaneUnits first;
+  const Shares sh = shares_of(a, kRows, static_cast<int>(gridDim.x), blockIdx.x == 0 && warp == 0, first);
+  const int me = static_cast<int>(blockIdx.x);
+  Owner own{0, 0, 0, 0, 0};
+  if (me >= sh.ctas || sh.units == 0) {
     if (tid == 0) a.owner[me] = own;
     return;
   }
-  const int64_t lo = units * me / ctas, hi = units * (me + 1) / ctas;
-  int64_t at = lo, req_begin;
-  int b = find_request(a, kRows, at, req_begin);
+  const int64_t hi = sh.begin(me + 1);
+  int64_t at = sh.begin(me), req_begin;
+  int b = find_request(a, kRows, at, first, req_begin);
 
   while (at < hi) {
     const Request r = request_of(a, b, kRows, false);
@@ -181,24 +261,67 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attention_kernel(co
       ++b;
       continue;
     }
-    const int64_t item = (at - req_begin) / r.tiles;          // (kv head, row tile)
-    const int h = static_cast<int>(item / r.rts), rt = static_cast<int>(item % r.rts);
+    const int64_t item = quotient(at - req_begin, r.tiles);   // (kv head, row tile)
+    const int h = static_cast<int>(quotient(item, r.rts)), rt = static_cast<int>(item - h * r.rts);
     const int64_t item_begin = req_begin + item * r.tiles, item_end = item_begin + r.tiles;
     const int t_begin = static_cast<int>(at - item_begin);
     const int t_end = static_cast<int>(min(hi, item_end) - item_begin);
     const int nrows = static_cast<int>(min(static_cast<int64_t>(kRows), static_cast<int64_t>(r.n) * a.group - static_cast<int64_t>(rt) * kRows));
 
-    // ---- this lane's rows of q: A operands ----
-    uint32_t qa[NT][2 * G][2];        // [row half][product][k half]
-    int limit[NT];                    // slots that the row sees
+    // ---- the warp's steps of TP tiles: from t_begin + TP * warp, kStep on ----
+    const int32_t* table = L.page_table + static_cast<size_t>(b) * L.max_pages_per_req;
+    uint32_t there = 0;               // bit stage * TP + u: the page of the stage's tile u exists
+    auto page_at = [&](int t) -> int {
+      if (t >= t_end || t * kTile >= r.len) return -1;
+      const int phys = table[(t * kTile) >> a.page_shift];
+      return phys < L.num_kv4_pages ? phys : -1;
+    };
+    const uint8_t* head = L.cache + (static_cast<size_t>(h) << (a.page_shift - 4)) * T::kBytes + lane * 16;
+    const size_t page_bytes = (static_cast<size_t>(L.num_kv_heads) << (a.page_shift - 4)) * T::kBytes;
+    const int tile_mask = (1 << (a.page_shift - 4)) - 1;
+    int phys[TP];                     // pages of the step that is asked for next
+    auto look_up = [&](int t) {
+#pragma unroll
+      for (int u = 0; u < TP; ++u) phys[u] = page_at(t + u);
+    };
+    auto issue = [&](int t, int stage) {
+#pragma unroll
+      for (int u = 0; u < TP; ++u) {
+        const uint32_t bit = 1u << (stage * TP + u);
+        if (phys[u] >= 0) {
+          const uint8_t* src = head + phys[u] * page_bytes + ((t + u) & tile_mask) * T::kBytes;
+          const uint32_t dst = cosa::smem_u32(sm.ring[warp][stage]) + u * T::kBytes + lane * 16;
+#pragma unroll
+          for (int k = 0; k < (T::kBytes + 511) / 512; ++k)
+            if (k < T::kBytes / 512 || lane * 16 < T::kBytes % 512) copy16(dst + k * 512, src + k * 512);
+          there |= bit;
+        } else {
+          there &= ~bit;
+        }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    const int t_first = t_begin + TP * warp;
+#pragma unroll
+    for (int s = 0; s < kStages; ++s) {
+      look_up(t_first + s * kStep);
+      issue(t_first + s * kStep, s);
+    }
+    look_up(t_first + kStages * kStep);
+
+    // ---- this lane's row of q: B operands ----
+    uint32_t qb[NT][2 * G][2];        // row 8 x + i: [eight rows][product][k half]
+    int limit[NT][2];                 // slots that rows 8 x + 2c and + 1 see
     int all_see = r.len;              // slots that every row sees
 #pragma unroll
     for (int x = 0; x < NT; ++x) {
       const int row = rt * kRows + 8 * x + i;
       const bool in = 8 * x + i < nrows;
       const int tok = in ? row / a.group : 0, head = in ? row - tok * a.group : 0;
-      limit[x] = in ? max(0, r.len - r.n + tok + 1) : 0;
-      if (in) all_see = min(all_see, limit[x]);
+      const int sees = in ? max(0, r.len - r.n + tok + 1) : 0;
+      if (in) all_see = min(all_see, sees);
+      limit[x][0] = __shfl_sync(0xffffffffu, sees, 8 * c);
+      limit[x][1] = __shfl_sync(0xffffffffu, sees, 8 * c + 4);
       const uint16_t* src = L.q + ((static_cast<int64_t>(r.tok0) + tok) * L.num_q_heads + h * a.group + head) * D + 8 * c;
 #pragma unroll
       for (int g = 0; g < G; ++g) {
@@ -209,204 +332,208 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attention_kernel(co
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] *= kUp;
         // values e and e + 4 meet in a pair of codes
-        qa[x][2 * g][0] = cosa::pack_bf16x2(v[0], v[4]);
-        qa[x][2 * g][1] = cosa::pack_bf16x2(v[1], v[5]);
-        qa[x][2 * g + 1][0] = cosa::pack_bf16x2(v[2], v[6]);
-        qa[x][2 * g + 1][1] = cosa::pack_bf16x2(v[3], v[7]);
+        qb[x][2 * g][0] = cosa::pack_bf16x2(v[0], v[4]);
+        qb[x][2 * g][1] = cosa::pack_bf16x2(v[1], v[5]);
+        qb[x][2 * g + 1][0] = cosa::pack_bf16x2(v[2], v[6]);
+        qb[x][2 * g + 1][1] = cosa::pack_bf16x2(v[3], v[7]);
       }
     }
 #pragma unroll
     for (int m = 4; m < 32; m *= 2) all_see = min(all_see, __shfl_xor_sync(0xffffffffu, all_see, m));
 
-    float o[NT][2 * G][4];            // [row half][m tile]
-    float m2[NT], l[NT];              // running maximum (scaled, base 2) and this lane's part of the sum
+    float o[NT][2 * G][4];            // [eight rows][m tile]
+    float m2[NT][2], l[NT][2];        // rows 8 x + 2c and + 1: running maximum (scaled, base 2), this lane's part of the sum
 #pragma unroll
     for (int x = 0; x < NT; ++x) {
-      m2[x] = -INFINITY;
-      l[x] = 0.f;
+      m2[x][0] = m2[x][1] = -INFINITY;
+      l[x][0] = l[x][1] = 0.f;
 #pragma unroll
       for (int mt = 0; mt < 2 * G; ++mt)
 #pragma unroll
         for (int k = 0; k < 4; ++k) o[x][mt][k] = 0.f;
     }
 
-    // ---- the warp's tiles: t_begin + warp, + 8, ... ----
-    const int32_t* table = L.page_table + static_cast<size_t>(b) * L.max_pages_per_req;
-    uint32_t there = 0;               // per stage: the tile's page exists
-    auto page_at = [&](int t) -> int {
-      if (t >= t_end || t * kTile >= r.len) return -1;
-      const int phys = table[(t * kTile) >> a.page_shift];
-      return phys < L.num_kv4_pages ? phys : -1;
-    };
-    const uint8_t* head = L.cache + (static_cast<size_t>(h) << (a.page_shift - 4)) * T::kBytes + lane * 16;
-    const size_t page_bytes = (static_cast<size_t>(L.num_kv_heads) << (a.page_shift - 4)) * T::kBytes;
-    const int tile_mask = (1 << (a.page_shift - 4)) - 1;
-    auto issue = [&](int t, int stage, int phys) {
-      if (phys >= 0) {
-        const uint8_t* src = head + phys * page_bytes + (t & tile_mask) * T::kBytes;
-        const uint32_t dst = cosa::smem_u32(sm.ring[warp][stage]) + lane * 16;
-#pragma unroll
-        for (int k = 0; k < (T::kBytes + 511) / 512; ++k)
-          if (k < T::kBytes / 512 || lane * 16 < T::kBytes % 512) copy16(dst + k * 512, src + k * 512);
-        there |= 1u << stage;
-      } else {
-        there &= ~(1u << stage);
-      }
-      asm volatile("cp.async.commit_group;" ::: "memory");
-    };
-#pragma unroll
-    for (int s = 0; s < kStages; ++s) {
-      const int t = t_begin + warp + s * kWarps;
-      issue(t, s, page_at(t));
-    }
     int stage = 0;
-    int next_phys = page_at(t_begin + warp + kStages * kWarps);
-    for (int t = t_begin + warp; t < t_end; t += kWarps) {
+    for (int t = t_first; t < t_end; t += kStep) {
       asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
       __syncwarp();
-      const uint8_t* tile = sm.ring[warp][stage];
-      const bool exists = (there >> stage) & 1u;
-      const int slot0 = t * kTile;
-      const bool clear = exists && slot0 + kTile <= all_see;   // every row sees every token of the tile
+      const uint8_t* tiles = sm.ring[warp][stage];
+      const uint32_t exists = there >> (stage * TP);           // bit u
+      // every row sees every token of the step
+      const bool clear = (exists & ((1u << TP) - 1u)) == (1u << TP) - 1u && (t + TP) * kTile <= all_see;
 
-      // q K^T: logits of 16 tokens
-      float s[2][4];                  // [8-token half][row i: 2c, 2c + 1; row i + 8: 2c, 2c + 1]
+      // K q^T: logits of 16 TP tokens
+      float s[TP][NT][4];             // [tile][eight rows][token i: rows 2c, 2c + 1; token i + 8: rows 2c, 2c + 1]
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        uint32_t kw[G], sc[G];        // sc: scales of tokens 2c and 2c + 1, two groups to a word
-        if constexpr (G == 4) {
-          const uint4 u = *reinterpret_cast<const uint4*>(tile + (8 * j + i) * T::kRow + 16 * c);
-          kw[0] = u.x; kw[1] = u.y; kw[2] = u.z; kw[3] = u.w;
-          const uint4 v = *reinterpret_cast<const uint4*>(tile + T::kKScales + (8 * j + 2 * c) * G * 2);
-          sc[0] = v.x; sc[1] = v.y; sc[2] = v.z; sc[3] = v.w;
-        } else {
-          const uint2 u = *reinterpret_cast<const uint2*>(tile + (8 * j + i) * T::kRow + 8 * c);
-          kw[0] = u.x; kw[1] = u.y;
-          const uint2 v = *reinterpret_cast<const uint2*>(tile + T::kKScales + (8 * j + 2 * c) * G * 2);
-          sc[0] = v.x; sc[1] = v.y;
-        }
+      for (int u = 0; u < TP; ++u) {
+        const uint8_t* tile = tiles + u * T::kBytes;
+        uint32_t kw[2][G], sc[2][G / 2];      // tokens i and i + 8: codes, and scales two groups to a word
 #pragma unroll
-        for (int k = 0; k < 4; ++k) s[j][k] = 0.f;
-#pragma unroll
-        for (int g = 0; g < G; ++g) {
-          const uint32_t w = kw[g], z = swap_bytes(w);
-          float acc[4] = {0.f, 0.f, 0.f, 0.f};
-          mma_bf16(acc, qa[0][2 * g][0], NT == 2 ? qa[NT - 1][2 * g][0] : 0u, qa[0][2 * g][1],
-                   NT == 2 ? qa[NT - 1][2 * g][1] : 0u, codes<0>(w, z), codes<1>(w, z));
-          mma_bf16(acc, qa[0][2 * g + 1][0], NT == 2 ? qa[NT - 1][2 * g + 1][0] : 0u, qa[0][2 * g + 1][1],
-                   NT == 2 ? qa[NT - 1][2 * g + 1][1] : 0u, codes<2>(w, z), codes<3>(w, z));
-          const float s0 = g % 2 ? bf16_hi(sc[g / 2]) : bf16_lo(sc[g / 2]);
-          const float s1 = g % 2 ? bf16_hi(sc[G / 2 + g / 2]) : bf16_lo(sc[G / 2 + g / 2]);
-          s[j][0] = fmaf(acc[0], s0, s[j][0]);
-          s[j][1] = fmaf(acc[1], s1, s[j][1]);
-          if (NT == 2) {
-            s[j][2] = fmaf(acc[2], s0, s[j][2]);
-            s[j][3] = fmaf(acc[3], s1, s[j][3]);
+        for (int j = 0; j < 2; ++j) {
+          if constexpr (G == 4) {
+            const uint4 w = *reinterpret_cast<const uint4*>(tile + (8 * j + i) * T::kRow + 16 * c);
+            kw[j][0] = w.x; kw[j][1] = w.y; kw[j][2] = w.z; kw[j][3] = w.w;
+            const uint2 v = *reinterpret_cast<const uint2*>(tile + T::kKScales + (8 * j + i) * G * 2);
+            sc[j][0] = v.x; sc[j][1] = v.y;
+          } else {
+            const uint2 w = *reinterpret_cast<const uint2*>(tile + (8 * j + i) * T::kRow + 8 * c);
+            kw[j][0] = w.x; kw[j][1] = w.y;
+            sc[j][0] = *reinterpret_cast<const uint32_t*>(tile + T::kKScales + (8 * j + i) * G * 2);
           }
         }
-      }
-      uint32_t seen = 0xFFu;          // bit 4 x + 2 j + e: row half x sees token 8 j + 2 c + e
-      if (!clear) {
-        seen = 0;
 #pragma unroll
         for (int x = 0; x < NT; ++x)
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
+          for (int k = 0; k < 4; ++k) s[u][x][k] = 0.f;
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              if (exists && slot0 + 8 * j + 2 * c + e < limit[x])
-                seen |= 1u << (4 * x + 2 * j + e);
+        for (int g = 0; g < G; ++g) {
+          const uint32_t w0 = kw[0][g], z0 = swap_bytes(w0), w1 = kw[1][g], z1 = swap_bytes(w1);
+          const uint32_t a0 = codes<0>(w0, z0), a1 = codes<0>(w1, z1), a2 = codes<1>(w0, z0), a3 = codes<1>(w1, z1);
+          const uint32_t e0 = codes<2>(w0, z0), e1 = codes<2>(w1, z1), e2 = codes<3>(w0, z0), e3 = codes<3>(w1, z1);
+          const float s0 = g % 2 ? bf16_hi(sc[0][g / 2]) : bf16_lo(sc[0][g / 2]);
+          const float s1 = g % 2 ? bf16_hi(sc[1][g / 2]) : bf16_lo(sc[1][g / 2]);
+#pragma unroll
+          for (int x = 0; x < NT; ++x) {
+            float acc[4];
+            mma_bf16_first(acc, a0, a1, a2, a3, qb[x][2 * g][0], qb[x][2 * g][1]);
+            mma_bf16(acc, e0, e1, e2, e3, qb[x][2 * g + 1][0], qb[x][2 * g + 1][1]);
+            fma2(s[u][x][0], s[u][x][1], acc[0], acc[1], s0, s0);
+            fma2(s[u][x][2], s[u][x][3], acc[2], acc[3], s1, s1);
+          }
+        }
+      }
+      // bit 4 (NT u + x) + k: the row of s[u][x][k] sees its token
+      uint32_t seen = ~0u;
+      if (!clear) {
+        seen = 0;
+#pragma unroll
+        for (int u = 0; u < TP; ++u)
+#pragma unroll
+          for (int x = 0; x < NT; ++x)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              if (((exists >> u) & 1u) && (t + u) * kTile + i + 8 * (k / 2) < limit[x][k % 2])
+                seen |= 1u << (4 * (NT * u + x) + k);
               else
-                s[j][2 * x + e] = -INFINITY;
+                s[u][x][k] = -INFINITY;
             }
       }
       if (WEIGHTS) {
 #pragma unroll
         for (int x = 0; x < NT; ++x)
-          if (8 * x + i < nrows) {
-            const int64_t row = (static_cast<int64_t>(h) * L.total_tokens + r.tok0) * a.group + rt * kRows + 8 * x + i;
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
-              *reinterpret_cast<float2*>(a.logits + row * a.pitch + slot0 + 8 * j + 2 * c) = make_float2(s[j][2 * x], s[j][2 * x + 1]);
-          }
+          for (int e = 0; e < 2; ++e)
+            if (8 * x + 2 * c + e < nrows) {
+              const int64_t row = (static_cast<int64_t>(h) * L.total_tokens + r.tok0) * a.group + rt * kRows + 8 * x + 2 * c + e;
+              float* dst = a.logits + row * a.pitch + t * kTile + i;
+#pragma unroll
+              for (int u = 0; u < TP; ++u)
+                if (u == 0 || t + u < t_end) {       // the next tile may be another CTA's
+                  dst[16 * u] = s[u][x][e];
+                  dst[16 * u + 8] = s[u][x][2 + e];
+                }
+            }
       }
 
-      // running maximum; the sums so far are rescaled where it grows
-      float p[NT][4];                 // [row half][2 j + e]
+      // Running maximum.  The lanes of a row agree on it, so whether any of them has a larger logit is one vote; only
+      // then is the maximum found and are the sums so far rescaled.
+      float top[NT][2];
+      bool grows = false;
 #pragma unroll
-      for (int x = 0; x < NT; ++x) {
-        float mx = fmaxf(fmaxf(s[0][2 * x], s[0][2 * x + 1]), fmaxf(s[1][2 * x], s[1][2 * x + 1]));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2)) * L.scale_log2;
-        if (__any_sync(0xffffffffu, mx > m2[x])) {
-          const float m_new = fmaxf(m2[x], mx);
-          const float f = m2[x] == -INFINITY ? 0.f : cosa::ex2_approx(m2[x] - m_new);
-          m2[x] = m_new;
-          l[x] *= f;
-          // rows 2c and 2c + 1 of the output accumulators live in the lanes whose i is that row
-          const float f0 = __shfl_sync(0xffffffffu, f, 8 * c), f1 = __shfl_sync(0xffffffffu, f, 8 * c + 4);
+      for (int x = 0; x < NT; ++x)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float mx = fmaxf(s[0][x][e], s[0][x][2 + e]);
+#pragma unroll
+          for (int u = 1; u < TP; ++u) mx = fmaxf(mx, fmaxf(s[u][x][e], s[u][x][2 + e]));
+          top[x][e] = mx * L.scale_log2;
+          grows |= top[x][e] > m2[x][e];
+        }
+      if (__any_sync(0xffffffffu, grows)) {
+#pragma unroll
+        for (int x = 0; x < NT; ++x) {
+          float f[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float mx = top[x][e];
+#pragma unroll
+            for (int m = 4; m < 32; m *= 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, m));
+            const float m_new = fmaxf(m2[x][e], mx);
+            f[e] = m2[x][e] == -INFINITY ? 0.f : cosa::ex2_approx(m2[x][e] - m_new);
+            m2[x][e] = m_new;
+            l[x][e] *= f[e];
+          }
 #pragma unroll
           for (int mt = 0; mt < 2 * G; ++mt) {
-            o[x][mt][0] *= f0; o[x][mt][1] *= f1; o[x][mt][2] *= f0; o[x][mt][3] *= f1;
+            o[x][mt][0] *= f[0]; o[x][mt][1] *= f[1]; o[x][mt][2] *= f[0]; o[x][mt][3] *= f[1];
           }
         }
-        const float up = 96.f - (m2[x] == -INFINITY ? 0.f : m2[x]);
+      }
+      float p[TP][NT][4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          p[x][k] = cosa::ex2_approx(fmaf(s[k / 2][2 * x + k % 2], L.scale_log2, up));
-          l[x] += p[x][k];
-        }
+      for (int x = 0; x < NT; ++x) {
+        const float up[2] = {96.f - (m2[x][0] == -INFINITY ? 0.f : m2[x][0]), 96.f - (m2[x][1] == -INFINITY ? 0.f : m2[x][1])};
+#pragma unroll
+        for (int u = 0; u < TP; ++u)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            p[u][x][k] = cosa::ex2_approx(fmaf(s[u][x][k], L.scale_log2, up[k % 2]));
+            l[x][k % 2] += p[u][x][k];
+          }
       }
 
-      // p V
-      uint32_t vs[2][G];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        if constexpr (G == 4) {
-          const uint4 v = *reinterpret_cast<const uint4*>(tile + T::kVScales + (8 * j + 2 * c) * G * 2);
-          vs[j][0] = v.x; vs[j][1] = v.y; vs[j][2] = v.z; vs[j][3] = v.w;
-        } else {
-          const uint2 v = *reinterpret_cast<const uint2*>(tile + T::kVScales + (8 * j + 2 * c) * G * 2);
-          vs[j][0] = v.x; vs[j][1] = v.y;
-        }
-      }
-      uint32_t vw[4][G / 2];          // tokens 2c, 2c + 1, 8 + 2c, 9 + 2c: rows c, 8 + c, 4 + c, 12 + c
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const uint8_t* src = tile + T::kVCodes + (c + 8 * (k % 2) + 4 * (k / 2)) * T::kRow + i * (2 * G);
-        if constexpr (G == 4) {
-          const uint2 u = *reinterpret_cast<const uint2*>(src);
-          vw[k][0] = u.x; vw[k][1] = u.y;
-        } else {
-          vw[k][0] = *reinterpret_cast<const uint32_t*>(src);
-        }
-      }
+      // V^T p
       auto product = [&](auto all) {
 #pragma unroll
-        for (int g = 0; g < G; ++g) {
-          uint32_t pb[NT][2];
+        for (int u = 0; u < TP; ++u) {
+          const uint8_t* tile = tiles + u * T::kBytes;
+          uint32_t sc[2][G / 2];      // tokens i and i + 8
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const float s0 = g % 2 ? bf16_hi(vs[j][g / 2]) : bf16_lo(vs[j][g / 2]);
-            const float s1 = g % 2 ? bf16_hi(vs[j][G / 2 + g / 2]) : bf16_lo(vs[j][G / 2 + g / 2]);
-#pragma unroll
-            for (int x = 0; x < NT; ++x) {
-              float y0 = p[x][2 * j] * s0, y1 = p[x][2 * j + 1] * s1;
-              if constexpr (!decltype(all)::value) {      // an unseen token adds nothing, whatever its scale is
-                if (!((seen >> (4 * x + 2 * j)) & 1u)) y0 = 0.f;
-                if (!((seen >> (4 * x + 2 * j + 1)) & 1u)) y1 = 0.f;
-              }
-              pb[x][j] = cosa::pack_bf16x2(y0, y1);
+            if constexpr (G == 4) {
+              const uint2 v = *reinterpret_cast<const uint2*>(tile + T::kVScales + (8 * j + i) * G * 2);
+              sc[j][0] = v.x; sc[j][1] = v.y;
+            } else {
+              sc[j][0] = *reinterpret_cast<const uint32_t*>(tile + T::kVScales + (8 * j + i) * G * 2);
             }
           }
-          // the group's codes of both tokens of a pair, and the same with the bytes exchanged
-          const uint32_t sel = g % 2 ? 0x7632 : 0x5410, swp = g % 2 ? 0x6723 : 0x4501;
-          const uint32_t w0 = __byte_perm(vw[0][g / 2], vw[1][g / 2], sel), z0 = __byte_perm(vw[0][g / 2], vw[1][g / 2], swp);
-          const uint32_t w1 = __byte_perm(vw[2][g / 2], vw[3][g / 2], sel), z1 = __byte_perm(vw[2][g / 2], vw[3][g / 2], swp);
+          uint32_t vw[4][G / 2];      // tokens 2c, 2c + 1, 8 + 2c, 9 + 2c: rows c, 8 + c, 4 + c, 12 + c
 #pragma unroll
-          for (int x = 0; x < NT; ++x) {
-            mma_bf16(o[x][2 * g], codes<0>(w0, z0), codes<1>(w0, z0), codes<0>(w1, z1), codes<1>(w1, z1), pb[x][0], pb[x][1]);
-            mma_bf16(o[x][2 * g + 1], codes<2>(w0, z0), codes<3>(w0, z0), codes<2>(w1, z1), codes<3>(w1, z1), pb[x][0], pb[x][1]);
+          for (int k = 0; k < 4; ++k) {
+            const uint8_t* src = tile + T::kVCodes + (c + 8 * (k % 2) + 4 * (k / 2)) * T::kRow + i * (2 * G);
+            if constexpr (G == 4) {
+              const uint2 w = *reinterpret_cast<const uint2*>(src);
+              vw[k][0] = w.x; vw[k][1] = w.y;
+            } else {
+              vw[k][0] = *reinterpret_cast<const uint32_t*>(src);
+            }
+          }
+#pragma unroll
+          for (int g = 0; g < G; ++g) {
+            uint32_t pb[NT][2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const float sj = g % 2 ? bf16_hi(sc[j][g / 2]) : bf16_lo(sc[j][g / 2]);
+#pragma unroll
+              for (int x = 0; x < NT; ++x) {
+                float y0, y1;
+                mul2(y0, y1, p[u][x][2 * j], p[u][x][2 * j + 1], sj, sj);
+                if constexpr (!decltype(all)::value) {      // an unseen token adds nothing, whatever its scale is
+                  if (!((seen >> (4 * (NT * u + x) + 2 * j)) & 1u)) y0 = 0.f;
+                  if (!((seen >> (4 * (NT * u + x) + 2 * j + 1)) & 1u)) y1 = 0.f;
+                }
+                pb[x][j] = transpose8(cosa::pack_bf16x2(y0, y1));
+              }
+            }
+            // the group's codes of both tokens of a pair, and the same with the bytes exchanged
+            const uint32_t sel = g % 2 ? 0x7632 : 0x5410, swp = g % 2 ? 0x6723 : 0x4501;
+            const uint32_t w0 = __byte_perm(vw[0][g / 2], vw[1][g / 2], sel), z0 = __byte_perm(vw[0][g / 2], vw[1][g / 2], swp);
+            const uint32_t w1 = __byte_perm(vw[2][g / 2], vw[3][g / 2], sel), z1 = __byte_perm(vw[2][g / 2], vw[3][g / 2], swp);
+#pragma unroll
+            for (int x = 0; x < NT; ++x) {
+              mma_bf16(o[x][2 * g], codes<0>(w0, z0), codes<1>(w0, z0), codes<0>(w1, z1), codes<1>(w1, z1), pb[x][0], pb[x][1]);
+              mma_bf16(o[x][2 * g + 1], codes<2>(w0, z0), codes<3>(w0, z0), codes<2>(w1, z1), codes<3>(w1, z1), pb[x][0], pb[x][1]);
+            }
           }
         }
       };
@@ -416,8 +543,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attention_kernel(co
         product(std::false_type{});
 
       __syncwarp();                   // every lane has read the stage
-      issue(t + kStages * kWarps, stage, next_phys);
-      next_phys = page_at(t + (kStages + 1) * kWarps);
+      issue(t + kStages * kStep, stage);
+      look_up(t + (kStages + 1) * kStep);
       stage = stage + 1 == kStages ? 0 : stage + 1;
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
@@ -425,11 +552,14 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attention_kernel(co
     // ---- join the warps ----
 #pragma unroll
     for (int x = 0; x < NT; ++x) {
-      l[x] += __shfl_xor_sync(0xffffffffu, l[x], 1);
-      l[x] += __shfl_xor_sync(0xffffffffu, l[x], 2);
-      if (c == 0) {
-        sm.ml[warp][8 * x + i][0] = m2[x];
-        sm.ml[warp][8 * x + i][1] = l[x];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int m = 4; m < 32; m *= 2) l[x][e] += __shfl_xor_sync(0xffffffffu, l[x][e], m);
+        if (i == 0) {
+          sm.ml[warp][8 * x + 2 * c + e][0] = m2[x][e];
+          sm.ml[warp][8 * x + 2 * c + e][1] = l[x][e];
+        }
       }
 #pragma unroll
       for (int g = 0; g < G; ++g) {
@@ -480,11 +610,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attention_kernel(co
       }
     }
     if (!whole && t_begin == 0) {
-      // the CTA that has the item's last unit
-      int64_t j = (item_end - 1) * ctas / units;
-      while (units * (j + 1) / ctas <= item_end - 1) ++j;
-      while (units * j / ctas > item_end - 1) --j;
-      own = Owner{b, h, rt, static_cast<int>(j)};
+      own = Owner{nrows, sh.owner(item_end - 1), r.tok0, h, rt};
     }
     __syncthreads();
     at = item_begin + t_end;
@@ -492,58 +618,127 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attention_kernel(co
   if (tid == 0) a.owner[me] = own;
 }
 
-// Joins the parts of the items that no CTA had whole: block (x, row) goes through the owner CTAs x, x + gridDim.x, ...
-// The parts' maxima and sums are read at once, then their outputs, eight in flight per thread.
-template <int D, int NT, bool WEIGHTS>
-__global__ void __launch_bounds__(D) combine_kernel(const Args a, const int ctas) {
-  constexpr int kRows = 8 * NT;
+// Joins the parts of the items that no CTA had whole, for few items of many parts.  Block (x, y) goes through the owner
+// CTAs x, x + gridDim.x, ..., and through rows y, y + gridDim.y, ... of theirs.  A thread has four values of the row and
+// every kJoin-th part, all of which are asked for before the first is needed.
+constexpr int kJoinThreads = 256;
+template <int D, bool WEIGHTS>
+__global__ void __launch_bounds__(kJoinThreads) combine_wide_kernel(const Args a, const int ctas, const int tile_rows) {
+  constexpr int kLanes = D / 4, kJoin = kJoinThreads / kLanes, kDeep = 8;
+  constexpr int kWarpsHere = kJoinThreads / 32;
   __shared__ float s_factor[kMaxCtas];
-  __shared__ float s_red[2][D / 32];
-  const int d = threadIdx.x, warp = d / 32, lane = d % 32;
+  __shared__ float s_red[2][kWarpsHere];
+  __shared__ float4 s_o[kJoin][kLanes];
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, d4 = tid % kLanes, part0 = tid / kLanes;
+  wait_for_grid_before();
   for (int first = blockIdx.x; first < ctas; first += gridDim.x) {
     const Owner own = a.owner[first];
-    if (own.b < 0) continue;
-    const Request r = request_of(a, own.b, kRows, false);
-    const int row = own.rt * kRows + static_cast<int>(blockIdx.y);
-    if (row >= static_cast<int64_t>(r.n) * a.group) continue;
-    // part j: the second place of the owner, the first of every later CTA
-    auto place = [&](int j) { return (static_cast<size_t>(first + j) * 2 + (j == 0 ? 1 : 0)) * 16 + blockIdx.y; };
+    for (int row = blockIdx.y; row < own.rows; row += gridDim.y) {
+      // part j: the second place of the owner, the first of every later CTA
+      auto place = [&](int j) { return (static_cast<size_t>(first + j) * 2 + (j == 0 ? 1 : 0)) * 16 + row; };
+      const int parts = own.last - first + 1;
+      float4 o[kDeep];
+#pragma unroll
+      for (int k = 0; k < kDeep; ++k) {
+        const int j = part0 + k * kJoin;
+        o[k] = j < parts ? *reinterpret_cast<const float4*>(a.part_o + place(j) * D + 4 * d4) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+      float M = -INFINITY;
+      for (int j = tid; j < parts; j += kJoinThreads) M = fmaxf(M, a.part_ml[place(j) * 2]);
+#pragma unroll
+      for (int m = 16; m > 0; m /= 2) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, m));
+      if (lane == 0) s_red[0][warp] = M;
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < kWarpsHere; ++w) M = fmaxf(M, s_red[0][w]);
+      float sum = 0.f;
+      for (int j = tid; j < parts; j += kJoinThreads) {
+        const float m = a.part_ml[place(j) * 2];
+        const float f = m == -INFINITY ? 1.f : cosa::ex2_approx(m - M);     // nothing seen: sums of zero, or NaN
+        s_factor[j] = f;
+        sum = fmaf(f, a.part_ml[place(j) * 2 + 1], sum);
+      }
+#pragma unroll
+      for (int m = 16; m > 0; m /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+      if (lane == 0) s_red[1][warp] = sum;
+      __syncthreads();
+      sum = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarpsHere; ++w) sum += s_red[1][w];
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      auto add = [&](int j, const float4& x) {
+        const float f = s_factor[j];
+        v.x = fmaf(f, x.x, v.x); v.y = fmaf(f, x.y, v.y); v.z = fmaf(f, x.z, v.z); v.w = fmaf(f, x.w, v.w);
+      };
+#pragma unroll
+      for (int k = 0; k < kDeep; ++k)
+        if (part0 + k * kJoin < parts) add(part0 + k * kJoin, o[k]);
+      for (int j = part0 + kDeep * kJoin; j < parts; j += kJoin) add(j, *reinterpret_cast<const float4*>(a.part_o + place(j) * D + 4 * d4));
+      s_o[part0][d4] = v;
+      __syncthreads();
+      if (part0 == 0) {
+#pragma unroll
+        for (int k = 1; k < kJoin; ++k) {
+          const float4 x = s_o[k][d4];
+          v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
+        }
+        const int rr = own.rt * tile_rows + row;
+        const int tok = rr / a.group, head = rr - tok * a.group;
+        const float inv = sum == 0.f ? 0.f : kDown / (sum * (1.0f / kUp));
+        uint16_t* dst = a.L.out + ((static_cast<int64_t>(own.tok0) + tok) * a.L.num_q_heads + own.h * a.group + head) * D + 4 * d4;
+        *reinterpret_cast<uint2*>(dst) = make_uint2(cosa::pack_bf16x2(v.x * inv, v.y * inv), cosa::pack_bf16x2(v.z * inv, v.w * inv));
+        if (WEIGHTS && d4 == 0) {
+          float* st = a.stats + ((static_cast<int64_t>(own.h) * a.L.total_tokens + own.tok0) * a.group + rr) * 2;
+          st[0] = M;
+          st[1] = sum * (1.0f / kUp);
+        }
+      }
+      __syncthreads();
+    }
+  }
+}
+
+// The same for many items of few parts: a block per owner CTA, a warp per row.
+template <int D, bool WEIGHTS>
+__global__ void __launch_bounds__(kJoinThreads) combine_kernel(const Args a, const int tile_rows) {
+  constexpr int V = D / 32;          // values of a lane
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int first = blockIdx.x;
+  wait_for_grid_before();
+  const Owner own = a.owner[first];
+  for (int row = warp; row < own.rows; row += kJoinThreads / 32) {
+    auto place = [&](int j) { return (static_cast<size_t>(first + j) * 2 + (j == 0 ? 1 : 0)) * 16 + row; };
     const int parts = own.last - first + 1;
     float M = -INFINITY;
-    for (int j = d; j < parts; j += D) M = fmaxf(M, a.part_ml[place(j) * 2]);
+    for (int j = lane; j < parts; j += 32) M = fmaxf(M, a.part_ml[place(j) * 2]);
 #pragma unroll
     for (int m = 16; m > 0; m /= 2) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, m));
-    if (lane == 0) s_red[0][warp] = M;
-    __syncthreads();
+    float sum = 0.f, v[V];
 #pragma unroll
-    for (int w = 0; w < D / 32; ++w) M = fmaxf(M, s_red[0][w]);
-    float sum = 0.f;
-    for (int j = d; j < parts; j += D) {
+    for (int k = 0; k < V; ++k) v[k] = 0.f;
+#pragma unroll 4
+    for (int j = 0; j < parts; ++j) {
       const float m = a.part_ml[place(j) * 2];
-      const float f = m == -INFINITY ? 1.f : cosa::ex2_approx(m - M);     // nothing seen: sums of zero, or NaN
-      s_factor[j] = f;
+      const float f = m == -INFINITY ? 1.f : cosa::ex2_approx(m - M);       // nothing seen: sums of zero, or NaN
       sum = fmaf(f, a.part_ml[place(j) * 2 + 1], sum);
+#pragma unroll
+      for (int k = 0; k < V; k += 2) {
+        const float2 x = *reinterpret_cast<const float2*>(a.part_o + place(j) * D + V * lane + k);
+        v[k] = fmaf(f, x.x, v[k]);
+        v[k + 1] = fmaf(f, x.y, v[k + 1]);
+      }
     }
+    const int rr = own.rt * tile_rows + row;
+    const int tok = rr / a.group, head = rr - tok * a.group;
+    const float inv = sum == 0.f ? 0.f : kDown / (sum * (1.0f / kUp));
+    uint16_t* dst = a.L.out + ((static_cast<int64_t>(own.tok0) + tok) * a.L.num_q_heads + own.h * a.group + head) * D + V * lane;
 #pragma unroll
-    for (int m = 16; m > 0; m /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, m);
-    if (lane == 0) s_red[1][warp] = sum;
-    __syncthreads();
-    sum = 0.f;
-#pragma unroll
-    for (int w = 0; w < D / 32; ++w) sum += s_red[1][w];
-    float v = 0.f;
-#pragma unroll 8
-    for (int j = 0; j < parts; ++j) v = fmaf(s_factor[j], a.part_o[place(j) * D + d], v);
-    const int tok = row / a.group, head = row - tok * a.group;
-    const float y = sum == 0.f ? 0.f : v * (kDown / (sum * (1.0f / kUp)));
-    a.L.out[((static_cast<int64_t>(r.tok0) + tok) * a.L.num_q_heads + own.h * a.group + head) * D + d] =
-        static_cast<uint16_t>(cosa::pack_bf16x2(y, y));
-    if (WEIGHTS && d == 0) {
-      float* st = a.stats + ((static_cast<int64_t>(own.h) * a.L.total_tokens + r.tok0) * a.group + row) * 2;
+    for (int k = 0; k < V; k += 2) *reinterpret_cast<uint32_t*>(dst + k) = cosa::pack_bf16x2(v[k] * inv, v[k + 1] * inv);
+    if (WEIGHTS && lane == 0) {
+      float* st = a.stats + ((static_cast<int64_t>(own.h) * a.L.total_tokens + own.tok0) * a.group + rr) * 2;
       st[0] = M;
       st[1] = sum * (1.0f / kUp);
     }
-    __syncthreads();
   }
 }
 
@@ -551,6 +746,7 @@ __global__ void __launch_bounds__(D) combine_kernel(const Args a, const int ctas
 constexpr int kWeightRows = 32;       // rows whose maxima and sums a CTA holds at a time
 __global__ void __launch_bounds__(256) weights_kernel(const Args a, const int rows_per_tile) {
   __shared__ float2 s_stat[kWeightRows];
+  wait_for_grid_before();
   const int b = blockIdx.z, h = blockIdx.y;
   const Request r = request_of(a, b, rows_per_tile, false);
   const int slot = (static_cast<int>(blockIdx.x) * 256 + threadIdx.x) * 4;
@@ -594,16 +790,33 @@ cudaError_t launch(const Args& a, cudaStream_t stream) {
   auto* kernel = attention_kernel<D, NT, WEIGHTS>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  constexpr int kCtas = kMaxCtas / NT;
+  constexpr int kCtas = Steps<NT>::kCtas * kSms;
   kernel<<<kCtas, kThreads, smem, stream>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  combine_kernel<D, NT, WEIGHTS><<<dim3(std::min(kCtas, 64), 8 * NT), D, 0, stream>>>(a, kCtas);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t c{};
+  c.blockDim = dim3(kJoinThreads);
+  c.stream = stream;
+  c.attrs = &early;
+  c.numAttrs = 1;
+  // How many items there are, as far as max_new_tokens tells (either kernel is right for any number).
+  const int64_t rows = static_cast<int64_t>(a.L.max_new_tokens) * a.group;
+  const int64_t items = static_cast<int64_t>(a.L.num_reqs) * a.L.num_kv_heads * ((rows + 8 * NT - 1) / (8 * NT));
+  if (items <= kFewItems) {
+    c.gridDim = dim3(64, static_cast<unsigned>(std::min<int64_t>(8 * NT, rows)));
+    e = cudaLaunchKernelEx(&c, combine_wide_kernel<D, WEIGHTS>, a, kCtas, 8 * NT);
+  } else {
+    c.gridDim = dim3(kCtas);
+    e = cudaLaunchKernelEx(&c, combine_kernel<D, WEIGHTS>, a, 8 * NT);
+  }
+  if (e != cudaSuccess) return e;
   if (WEIGHTS) {
-    const dim3 grid(static_cast<unsigned>((a.L.max_seqlen + 1023LL) / 1024), static_cast<unsigned>(a.L.num_kv_heads),
-                    static_cast<unsigned>(a.L.num_reqs));
-    weights_kernel<<<grid, 256, 0, stream>>>(a, 8 * NT);
-    e = cudaGetLastError();
+    c.gridDim = dim3(static_cast<unsigned>((a.L.max_seqlen + 1023LL) / 1024), static_cast<unsigned>(a.L.num_kv_heads),
+                     static_cast<unsigned>(a.L.num_reqs));
+    c.blockDim = dim3(256);
+    e = cudaLaunchKernelEx(&c, weights_kernel, a, 8 * NT);
   }
   return e;
 }

@@ -21,22 +21,26 @@ constexpr int kMaxTokens = 16;     // tokens of a CTA (a storage tile: its slots
 // Codes of eight values, lowest nibble first: nibble n of each half has the magnitude of value n, and the sign of
 // value n ^ 2 in its high bit.
 //
-// rint(x / s) without a division: |x| / s is formed to 2^-22 by the reciprocal and rounded to a multiple of 2^-10 by
-// the addition of 1.5 * 2^13.  Significands of 8 bits make a quotient that lies on a border k + 1/2 or at least 1/512
-// from it (2 X 2^e - (2 k + 1) S is a whole multiple of 1/2 where it is not zero, over 2 S <= 510), so the first
-// rounding puts every tie on its border exactly and moves nothing across one; the second addition rounds to even.
-__device__ __forceinline__ uint32_t codes8(const uint4& u, float s, float inv) {
+// rint(x / s) without a division: x / s is formed to 2^-21 by the reciprocal and rounded to a multiple of 2^-10 by
+// being added to 1.5 * 2^13.  Significands of 8 bits make a quotient that lies on a border k + 1/2 or at least 1/512
+// from it (2 X 2^e - (2 k + 1) S is a whole multiple of 1/2 where it is not zero, over 2 S <= 510), so this first
+// rounding puts every tie on its border exactly and moves nothing across one.  A second addition, to 1.5 * 2^23
+// in all, rounds to even and leaves the code in the low bits; the eight words are summed with weights 16^i.
+__device__ __forceinline__ uint32_t codes8(const uint4& u, float inv) {
   float x[8];
   unpack8(u, x);
-  uint32_t w = 0;
+  uint32_t sum = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float y = fmaf(fabsf(x[i]), inv, 12288.0f) - 12288.0f;
-    const uint32_t m = __float_as_uint(y + 12582912.0f) & 15u;
-    w |= m << (4 * i);
-    if (m != 0u && x[i] < 0.f) w |= 8u << (4 * (i ^ 2));
-  }
-  return w;
+  for (int i = 0; i < 8; ++i)
+    sum += __float_as_uint(fmaf(x[i], inv, 12288.0f) + (12582912.0f - 12288.0f)) << (4 * i);
+  // sum_i (0x4B400000 + c_i) 16^i: without the constant, and with 8 in each nibble, the nibbles are c + 8
+  uint32_t bias = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) bias += 0x4B400000u << (4 * i);
+  const uint32_t c = (sum - bias + 0x88888888u) ^ 0x88888888u;       // two's complement in each nibble
+  const uint32_t neg = (c >> 3) & 0x11111111u;
+  const uint32_t mag = (c ^ (neg * 15u)) + neg;                       // no carry: the codes are -7 .. 7
+  return mag | __byte_perm(neg << 3, 0, 0x2301);                      // the bytes of a half hold nibbles 0, 1 and 2, 3
 }
 
 // The same by the division, for scales whose reciprocal or codes leave the range (near the ends of bf16's).
@@ -72,21 +76,37 @@ __device__ __forceinline__ void quantise(const uint4 (&u)[G], uint32_t (&w)[G], 
     const float s = __uint_as_float(bits << 16);
     scale[g] = bits;
     if (bits >= 0x0400u && bits < 0x7C00u)        // 2^-119 <= s < 2^121
-      w[g] = codes8(u[g], s, 1.0f / s);
+      w[g] = codes8(u[g], 1.0f / s);
     else
       w[g] = bits == 0u ? 0u : codes8_slow(u[g], s);
   }
 }
 
-// Eight values from their codes: the products are exact in fp32 and rounded once.
-__device__ __forceinline__ uint4 dequantise8(uint32_t w, float s) {
-  float x[8];
+__device__ __forceinline__ uint32_t sub_bf16x2(uint32_t x, uint32_t y) {
+  uint32_t r;
+  asm("sub.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+  return r;
+}
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t x, uint32_t y) {
+  uint32_t r;
+  asm("mul.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+  return r;
+}
+
+// Eight values from their codes and `scale` (the bf16 scale in both halves).  The two magnitudes of a byte become the
+// bf16 numbers 128 + m (low bits of the significand) and 8 + m (high bits), less 128 and 8; the product with the scale is
+// rounded once.
+__device__ __forceinline__ uint4 dequantise8(uint32_t w, uint32_t scale) {
+  uint32_t y[4];
+  const uint32_t w4 = w << 4;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float m = static_cast<float>((w >> (4 * i)) & 7u) * s;
-    x[i] = (w >> (4 * (i ^ 2))) & 8u ? -m : m;
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t x = (__byte_perm(w, 0, k | (4 << 4) | (k << 8) | (4 << 12)) & 0x00700007u) | 0x41004300u;
+    // signs of values 2k and 2k + 1: bits 3 and 7 of byte k ^ 1
+    const uint32_t sign = __byte_perm(w4, w, ((k ^ 1) << 4) | ((4 + (k ^ 1)) << 12)) & 0x80008000u;
+    y[k] = mul_bf16x2(sub_bf16x2(x, 0x41004300u), scale) ^ sign;
   }
-  return pack8(x);
+  return make_uint4(y[0], y[1], y[2], y[3]);
 }
 
 // A lane's share of a row of K codes is one piece of the row; of a row of V codes too.
@@ -251,8 +271,8 @@ __global__ void __launch_bounds__(kThreads) pages_kernel(const ConvertLaunch L, 
         const uint32_t* vs = reinterpret_cast<const uint32_t*>(tile + T::kVScales + t * G * 2);
 #pragma unroll
         for (int g = 0; g < G; ++g) {
-          *reinterpret_cast<uint4*>(L.k_cache + at + 32 * g + 8 * c) = dequantise8(kw[g], g % 2 ? bf16_hi(ks[g / 2]) : bf16_lo(ks[g / 2]));
-          *reinterpret_cast<uint4*>(L.v_cache + at + 32 * g + 8 * c) = dequantise8(vw[g], g % 2 ? bf16_hi(vs[g / 2]) : bf16_lo(vs[g / 2]));
+          *reinterpret_cast<uint4*>(L.k_cache + at + 32 * g + 8 * c) = dequantise8(kw[g], __byte_perm(ks[g / 2], 0, g % 2 ? 0x3232 : 0x1010));
+          *reinterpret_cast<uint4*>(L.v_cache + at + 32 * g + 8 * c) = dequantise8(vw[g], __byte_perm(vs[g / 2], 0, g % 2 ? 0x3232 : 0x1010));
         }
       } else {
         uint4 ku[G], vu[G];

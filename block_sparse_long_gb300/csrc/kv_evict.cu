@@ -44,7 +44,7 @@ __device__ __forceinline__ int length_of(const EvictLaunch& L, int b) {
 }
 
 __device__ __forceinline__ int page_of(const int32_t* table, int pitch, const EvictLaunch& L, int b, int slot) {
-  const int phys = table[static_cast<size_t>(b) * pitch + slot / L.page_size];
+  const int phys = table[static_cast<size_t>(b) * pitch + (slot >> L.page_shift)];
   return phys >= 0 && phys < L.num_kv4_pages ? phys : -1;
 }
 
@@ -104,14 +104,29 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictLaunc
   const int lo = min(n, rank * run), hi = min(n, lo + run);
   const int per = (run + kSelectThreads - 1) / kSelectThreads;
 
-  auto form = [&](int s) -> uint32_t {
-    if (page_of(L.page_table, L.max_pages_per_req, L, b, s) < 0) return kMissing;
-    if (s < L.sink || s >= n - L.recent) return kAlways;
-    return key_of(w[s]);
+  const int32_t* table = L.page_table + static_cast<size_t>(b) * L.max_pages_per_req;
+  auto form = [&](int s, int phys, float weight) -> uint32_t {
+    if (phys < 0 || phys >= L.num_kv4_pages) return kMissing;
+    return s < L.sink || s >= n - L.recent ? kAlways : key_of(weight);
   };
-  auto key = [&](int s) -> uint32_t { return HELD ? s_keys[padded(s - lo)] : form(s); };
+  auto key = [&](int s) -> uint32_t { return HELD ? s_keys[padded(s - lo)] : form(s, table[s >> L.page_shift], w[s]); };
   if (HELD) {
-    for (int s = lo + tid; s < hi; s += kSelectThreads) s_keys[padded(s - lo)] = form(s);
+    constexpr int kDeep = 8;          // loads in flight per thread
+    for (int s0 = lo + tid; s0 < hi; s0 += kDeep * kSelectThreads) {
+      float weight[kDeep];
+      int phys[kDeep];
+#pragma unroll
+      for (int k = 0; k < kDeep; ++k) {
+        const int s = s0 + k * kSelectThreads;
+        weight[k] = s < hi ? w[s] : 0.f;
+        phys[k] = s < hi ? table[s >> L.page_shift] : -1;
+      }
+#pragma unroll
+      for (int k = 0; k < kDeep; ++k) {
+        const int s = s0 + k * kSelectThreads;
+        if (s < hi) s_keys[padded(s - lo)] = form(s, phys[k], weight[k]);
+      }
+    }
   }
 
   const int share = kBins / ctas;
@@ -214,11 +229,7 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictLaunc
     int at = above + min(equal, want);
     for (int s = first; s < last; ++s) {
       const uint32_t k = key(s);
-      if (k > prefix || (k == prefix && equal++ < want)) {
-        kept[at] = s;
-        if (L.weights_out) L.weights_out[row * L.max_seqlen + at] = w[s];
-        ++at;
-      }
+      if (k > prefix || (k == prefix && equal++ < want)) kept[at++] = s;
     }
   }
   for (int j = keep + rank * kSelectThreads + tid; j < L.budget; j += ctas * kSelectThreads) kept[j] = -1;
@@ -229,44 +240,61 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictLaunc
   cluster.sync();                   // a CTA's shared memory lives until its neighbours have read it
 }
 
-// One destination tile of 16 slots per CTA.
+// A destination tile of 16 slots per warp, all of whose pieces are in flight at once.
+constexpr int kMoveWarps = 8;
 template <int D>
-__global__ void __launch_bounds__(128) move_kernel(const EvictLaunch L) {
+__global__ void __launch_bounds__(32 * kMoveWarps) move_kernel(const EvictLaunch L) {
   using T = Tile<D>;
-  const int tid = threadIdx.x;
-  const int b = blockIdx.z, h = blockIdx.y, slot0 = blockIdx.x * kTile;
+  constexpr int kChunks = T::kRow / 16;      // 16-byte pieces of a row of codes
+  constexpr int kSteps = kChunks / 2;        // pieces of the tile's codes per lane, of K and of V
+  const int lane = threadIdx.x % 32;
+  const int b = blockIdx.z, h = blockIdx.y;
+  const int slot0 = static_cast<int>(blockIdx.x * kMoveWarps + threadIdx.x / 32) * kTile;
   const int rows = min(kTile, L.new_len[b] - slot0);
   if (rows <= 0) return;
+  const size_t row = static_cast<size_t>(b) * L.num_kv_heads + h;
+  // lane t < 16 looks up the source of slot t
+  size_t from = 0;                           // its tile
+  int at = 0;                                // its row there
+  if (lane < rows) {
+    const int s = L.kept[row * L.budget + slot0 + lane];
+    const int phys = L.page_table[static_cast<size_t>(b) * L.max_pages_per_req + (s >> L.page_shift)];
+    from = tile_offset<D>(phys, h, s, L.num_kv_heads, L.page_size);
+    at = s % kTile;
+    if (L.weights_out) L.weights_out[row * L.max_seqlen + slot0 + lane] = L.weights[row * L.max_seqlen + s];
+  }
   const int dst_phys = page_of(L.dst_page_table, L.max_dst_pages, L, b, slot0);
   if (dst_phys < 0) return;
-  __shared__ const uint8_t* s_src[kTile];
-  __shared__ int s_row[kTile];
-  if (tid < rows) {
-    const int s = L.kept[(static_cast<size_t>(b) * L.num_kv_heads + h) * L.budget + slot0 + tid];
-    s_src[tid] = L.cache + tile_offset<D>(page_of(L.page_table, L.max_pages_per_req, L, b, s), h, s, L.num_kv_heads, L.page_size);
-    s_row[tid] = s % kTile;
-  }
-  __syncthreads();
   uint8_t* dst = L.cache + tile_offset<D>(dst_phys, h, slot0, L.num_kv_heads, L.page_size);
-  constexpr int kChunks = T::kRow / 16;      // 16-byte pieces of a row of codes
-  for (int k = tid; k < rows * (2 * kChunks + 2); k += 128) {
-    const int t = k / (2 * kChunks + 2), j = k % (2 * kChunks + 2);
-    const uint8_t* src = s_src[t];
-    const int from = s_row[t];
-    if (j < kChunks) {
-      *reinterpret_cast<uint4*>(dst + t * T::kRow + 16 * j) = *reinterpret_cast<const uint4*>(src + from * T::kRow + 16 * j);
-    } else if (j < 2 * kChunks) {
-      const int x = 16 * (j - kChunks);
-      *reinterpret_cast<uint4*>(dst + T::kVCodes + v_row(t) * T::kRow + x) =
-          *reinterpret_cast<const uint4*>(src + T::kVCodes + v_row(from) * T::kRow + x);
-    } else {
-      const int base = j == 2 * kChunks ? T::kKScales : T::kVScales;
-      if constexpr (T::G == 4)
-        *reinterpret_cast<uint2*>(dst + base + t * 8) = *reinterpret_cast<const uint2*>(src + base + from * 8);
-      else
-        *reinterpret_cast<uint32_t*>(dst + base + t * 4) = *reinterpret_cast<const uint32_t*>(src + base + from * 4);
+  uint4 k[kSteps], v[kSteps];
+#pragma unroll
+  for (int i = 0; i < kSteps; ++i) {
+    const int t = (i * 32 + lane) / kChunks, x = 16 * (lane % kChunks);
+    const uint8_t* src = L.cache + __shfl_sync(0xffffffffu, from, t) + x;
+    const int r = __shfl_sync(0xffffffffu, at, t);
+    if (t < rows) {
+      k[i] = *reinterpret_cast<const uint4*>(src + r * T::kRow);
+      v[i] = *reinterpret_cast<const uint4*>(src + T::kVCodes + v_row(r) * T::kRow);
     }
   }
+  // scales: lanes 0 to 15 of K, 16 to 31 of V
+  const int t = lane % kTile, base = lane < kTile ? T::kKScales : T::kVScales;
+  const uint8_t* src = L.cache + __shfl_sync(0xffffffffu, from, t) + base + __shfl_sync(0xffffffffu, at, t) * (2 * T::G);
+  uint32_t sc[T::G / 2];
+  if (t < rows)
+#pragma unroll
+    for (int g = 0; g < T::G / 2; ++g) sc[g] = reinterpret_cast<const uint32_t*>(src)[g];
+#pragma unroll
+  for (int i = 0; i < kSteps; ++i) {
+    const int t = (i * 32 + lane) / kChunks, x = 16 * (lane % kChunks);
+    if (t < rows) {
+      *reinterpret_cast<uint4*>(dst + t * T::kRow + x) = k[i];
+      *reinterpret_cast<uint4*>(dst + T::kVCodes + v_row(t) * T::kRow + x) = v[i];
+    }
+  }
+  if (t < rows)
+#pragma unroll
+    for (int g = 0; g < T::G / 2; ++g) reinterpret_cast<uint32_t*>(dst + base + t * (2 * T::G))[g] = sc[g];
 }
 
 // A cluster of as many CTAs as give each about 4096 slots: below that, the pass over the keys costs less than the
@@ -300,12 +328,13 @@ cudaError_t launch_select(const EvictLaunch& L, cudaStream_t stream) {
 cudaError_t launch_evict(const EvictLaunch& L, cudaStream_t stream) {
   cudaError_t e = launch_select(L, stream);
   if (e != cudaSuccess) return e;
-  const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(L.budget) + kTile - 1) / kTile), static_cast<unsigned>(L.num_kv_heads),
+  const int64_t most = std::min(L.budget, L.max_seqlen);
+  const dim3 grid(static_cast<unsigned>((most + kMoveWarps * kTile - 1) / (kMoveWarps * kTile)), static_cast<unsigned>(L.num_kv_heads),
                   static_cast<unsigned>(L.num_reqs));
   if (L.head_dim == 128)
-    move_kernel<128><<<grid, 128, 0, stream>>>(L);
+    move_kernel<128><<<grid, 32 * kMoveWarps, 0, stream>>>(L);
   else
-    move_kernel<64><<<grid, 128, 0, stream>>>(L);
+    move_kernel<64><<<grid, 32 * kMoveWarps, 0, stream>>>(L);
   return cudaGetLastError();
 }
 

@@ -61,6 +61,7 @@ struct EvictLaunch {
   int32_t* status;
   int num_reqs, num_kv_heads, head_dim, page_size, max_seqlen, num_kv4_pages, max_pages_per_req, max_dst_pages;
   int budget, sink, recent;
+  int page_shift;        // log2(page_size)
 };
 cudaError_t launch_evict(const EvictLaunch& L, cudaStream_t stream);
 
