@@ -31,6 +31,7 @@ receives errors found on the device.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 from typing import Optional, Tuple
@@ -126,19 +127,29 @@ def kv_required_numel(p: CosaKvParams) -> dict:
             "kept": p.num_reqs * p.num_kv_heads * p.budget, "status": 1}
 
 
+@functools.lru_cache(maxsize=256)
+def _sizes(params: bytes) -> dict:
+    """kv_required_numel by the parameters' values."""
+    return kv_required_numel(CosaKvParams.from_buffer_copy(params))
+
+
 class _Call:
     """Checks of one call's tensors and its stream.  The first tensor sets the device."""
 
+    __slots__ = ("p", "need", "index")
+
     def __init__(self, p: CosaKvParams):
-        self.p, self.need, self.device = p, kv_required_numel(p), None
+        self.p, self.need, self.index = p, _sizes(bytes(p)), None
 
     def on_device(self, t: torch.Tensor, name: str) -> None:
+        index = t.get_device()
+        if index == self.index:
+            return
         if not t.is_cuda:
             raise ValueError(f"{name} must be a CUDA tensor")
-        if self.device is None:
-            self.device = t.device
-        elif t.device != self.device:
-            raise ValueError(f"{name} is on {t.device}, the other tensors on {self.device}")
+        if self.index is not None:
+            raise ValueError(f"{name} is on {t.device}, the other tensors on cuda:{self.index}")
+        self.index = index
 
     def dense(self, t: Optional[torch.Tensor], name: str, dtype: torch.dtype, need: Optional[str] = None):
         """Address of a contiguous tensor of at least the size that the parameters imply."""
@@ -151,7 +162,8 @@ class _Call:
         least = self.need[need or name]
         if t.numel() < least:
             raise ValueError(f"{name} holds {t.numel()} elements; the parameters need at least {least}")
-        self.on_device(t, name)
+        if t.get_device() != self.index or self.index < 0:
+            self.on_device(t, name)
         return t.data_ptr()
 
     def rows(self, t: torch.Tensor, name: str, heads: int):
@@ -159,13 +171,13 @@ class _Call:
         p = self.p
         if t.dtype != torch.bfloat16:
             raise ValueError(f"{name} must be torch.bfloat16, got {t.dtype}")
-        shape = t.shape
-        if len(shape) != 3 or shape[1] != heads or shape[2] != p.head_dim:
-            raise ValueError(f"{name} must be [total_tokens, {heads}, {p.head_dim}], got {list(shape)}")
+        shape, d = t.shape, p.head_dim
+        if len(shape) != 3 or shape[1] != heads or shape[2] != d:
+            raise ValueError(f"{name} must be [total_tokens, {heads}, {d}], got {list(shape)}")
         if shape[0] < p.total_tokens:
             raise ValueError(f"{name} holds {shape[0]} tokens; the parameters need at least {p.total_tokens}")
         st = t.stride()
-        if shape[0] and (st[2] != 1 or (heads > 1 and st[1] != p.head_dim)):
+        if shape[0] and (st[2] != 1 or (heads > 1 and st[1] != d)):
             raise ValueError(f"{name}: the heads of a token must be contiguous")
         self.on_device(t, name)
         # the stride of a single token says nothing
@@ -180,22 +192,22 @@ class _Call:
 
     def run(self, name: str, p: CosaKvParams, args, status: Optional[torch.Tensor], stream) -> None:
         st = self.dense(status, "status", torch.int32)
-        s = stream if stream is not None else torch.cuda.current_stream(self.device)
-        f = getattr(kv_library(), name)
-        if torch.cuda.current_device() == self.device.index:
-            rc = f(ctypes.byref(p), *args, st, s.cuda_stream)
+        s = stream.cuda_stream if stream is not None else torch.cuda.current_stream(self.index).cuda_stream
+        f = getattr(_lib or kv_library(), name)
+        if torch.cuda.current_device() == self.index:
+            rc = f(p, *args, st, s)
         else:
-            with torch.cuda.device(self.device):
-                rc = f(ctypes.byref(p), *args, st, s.cuda_stream)
+            with torch.cuda.device(self.index):
+                rc = f(p, *args, st, s)
         if rc != COSA_OK:
             raise CosaError(rc, name)
 
     def empty(self, shape, dtype: torch.dtype, stream) -> torch.Tensor:
         """Memory for an output or workspace, tied to the stream that the call runs on."""
         if stream is None:
-            return torch.empty(shape, dtype=dtype, device=self.device)
+            return torch.empty(shape, dtype=dtype, device=torch.device("cuda", self.index))
         with torch.cuda.stream(stream):
-            return torch.empty(shape, dtype=dtype, device=self.device)
+            return torch.empty(shape, dtype=dtype, device=torch.device("cuda", self.index))
 
 
 def cosa_qk_norm_rope(p: CosaKvParams, q: torch.Tensor, k: torch.Tensor, cu_seqlens: torch.Tensor, inv_freq: torch.Tensor,
