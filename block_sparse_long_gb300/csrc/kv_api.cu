@@ -256,7 +256,7 @@ int cosa_kv4_evict(const cosa_kv_params* p, void* kv4_cache, const int32_t* page
   if (static_cast<int64_t>(p->sink) + p->recent > p->budget) return COSA_ERR_INVALID_ARG;
   if (p->budget > kMaxTokens) return COSA_ERR_UNSUPPORTED;
   if (p->max_dst_pages < ceil_div(p->budget, p->page_size)) return COSA_ERR_INVALID_ARG;
-  if (static_cast<int64_t>(p->num_reqs) * p->num_kv_heads > INT32_MAX / 8) return COSA_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(p->num_reqs) * p->num_kv_heads > INT32_MAX / 16) return COSA_ERR_UNSUPPORTED;
   if (!kv4_cache || !page_table || !kv_len || !weights || !dst_page_table || !new_len || !kept) return COSA_ERR_INVALID_ARG;
   if (weights_out == weights || dst_page_table == page_table) return COSA_ERR_INVALID_ARG;   // moved into other memory
   if (!aligned(kv4_cache, 16) || !aligned(page_table, 4) || !aligned(kv_len, 4) || !aligned(weights, 4) ||

@@ -207,10 +207,6 @@ __device__ __forceinline__ void mul2(float& d0, float& d1, float a0, float a1, f
 constexpr float kUp = 79228162514264337593543950336.0f;      // 2^96
 constexpr float kDown = 8589934592.0f;                       // 2^33
 
-// The kernels after the first are launched while it runs; this waits until the grid before has ended and its
-// writes are visible.  Every thread calls it first of all.
-__device__ __forceinline__ void wait_for_grid_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 // A warp takes TP tiles at a time: with eight rows two, whose chains of dependent instructions fill each other's gaps (one
 // tile alone has too few independent ones); with sixteen rows one, for the registers.
 template <int NT>
@@ -241,6 +237,8 @@ __global__ void __launch_bounds__(kThreads, Steps<NT>::kCtas) attention_kernel(c
   const AttnLaunch& L = a.L;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, i = lane / 4, c = lane % 4;
 
+  wait_for_stream();
+  let_next_start();
   LaneUnits first;
   const Shares sh = shares_of(a, kRows, static_cast<int>(gridDim.x), blockIdx.x == 0 && warp == 0, first);
   const int me = static_cast<int>(blockIdx.x);
@@ -630,7 +628,8 @@ __global__ void __launch_bounds__(kJoinThreads) combine_wide_kernel(const Args a
   __shared__ float s_red[2][kWarpsHere];
   __shared__ float4 s_o[kJoin][kLanes];
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, d4 = tid % kLanes, part0 = tid / kLanes;
-  wait_for_grid_before();
+  wait_for_stream();
+  let_next_start();
   for (int first = blockIdx.x; first < ctas; first += gridDim.x) {
     const Owner own = a.owner[first];
     for (int row = blockIdx.y; row < own.rows; row += gridDim.y) {
@@ -704,7 +703,8 @@ __global__ void __launch_bounds__(kJoinThreads) combine_kernel(const Args a, con
   constexpr int V = D / 32;          // values of a lane
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int first = blockIdx.x;
-  wait_for_grid_before();
+  wait_for_stream();
+  let_next_start();
   const Owner own = a.owner[first];
   for (int row = warp; row < own.rows; row += kJoinThreads / 32) {
     auto place = [&](int j) { return (static_cast<size_t>(first + j) * 2 + (j == 0 ? 1 : 0)) * 16 + row; };
@@ -746,7 +746,7 @@ __global__ void __launch_bounds__(kJoinThreads) combine_kernel(const Args a, con
 constexpr int kWeightRows = 32;       // rows whose maxima and sums a CTA holds at a time
 __global__ void __launch_bounds__(256) weights_kernel(const Args a, const int rows_per_tile) {
   __shared__ float2 s_stat[kWeightRows];
-  wait_for_grid_before();
+  wait_for_stream();
   const int b = blockIdx.z, h = blockIdx.y;
   const Request r = request_of(a, b, rows_per_tile, false);
   const int slot = (static_cast<int>(blockIdx.x) * 256 + threadIdx.x) * 4;
@@ -791,34 +791,19 @@ cudaError_t launch(const Args& a, cudaStream_t stream) {
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
   constexpr int kCtas = Steps<NT>::kCtas * kSms;
-  kernel<<<kCtas, kThreads, smem, stream>>>(a);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  cudaLaunchAttribute early{};
-  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  early.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t c{};
-  c.blockDim = dim3(kJoinThreads);
-  c.stream = stream;
-  c.attrs = &early;
-  c.numAttrs = 1;
+  if ((e = launch_after(kernel, dim3(kCtas), kThreads, smem, stream, 1, a)) != cudaSuccess) return e;
   // How many items there are, as far as max_new_tokens tells (either kernel is right for any number).
   const int64_t rows = static_cast<int64_t>(a.L.max_new_tokens) * a.group;
   const int64_t items = static_cast<int64_t>(a.L.num_reqs) * a.L.num_kv_heads * ((rows + 8 * NT - 1) / (8 * NT));
-  if (items <= kFewItems) {
-    c.gridDim = dim3(64, static_cast<unsigned>(std::min<int64_t>(8 * NT, rows)));
-    e = cudaLaunchKernelEx(&c, combine_wide_kernel<D, WEIGHTS>, a, kCtas, 8 * NT);
-  } else {
-    c.gridDim = dim3(kCtas);
-    e = cudaLaunchKernelEx(&c, combine_kernel<D, WEIGHTS>, a, 8 * NT);
-  }
-  if (e != cudaSuccess) return e;
-  if (WEIGHTS) {
-    c.gridDim = dim3(static_cast<unsigned>((a.L.max_seqlen + 1023LL) / 1024), static_cast<unsigned>(a.L.num_kv_heads),
-                     static_cast<unsigned>(a.L.num_reqs));
-    c.blockDim = dim3(256);
-    e = cudaLaunchKernelEx(&c, weights_kernel, a, 8 * NT);
-  }
-  return e;
+  if (items <= kFewItems)
+    e = launch_after(combine_wide_kernel<D, WEIGHTS>, dim3(64, static_cast<unsigned>(std::min<int64_t>(8 * NT, rows))), kJoinThreads, 0,
+                     stream, 1, a, kCtas, 8 * NT);
+  else
+    e = launch_after(combine_kernel<D, WEIGHTS>, dim3(kCtas), kJoinThreads, 0, stream, 1, a, 8 * NT);
+  if (e != cudaSuccess || !WEIGHTS) return e;
+  const dim3 grid(static_cast<unsigned>((a.L.max_seqlen + 1023LL) / 1024), static_cast<unsigned>(a.L.num_kv_heads),
+                  static_cast<unsigned>(a.L.num_reqs));
+  return launch_after(weights_kernel, grid, 256, 0, stream, 1, a, 8 * NT);
 }
 
 }  // namespace

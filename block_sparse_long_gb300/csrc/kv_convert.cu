@@ -57,6 +57,12 @@ __device__ __noinline__ uint32_t codes8_slow(uint4 u, float s) {
   return w;
 }
 
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // Codes of a lane's values, a word per group, and the bits of the groups' scales.  Every lane of the warp calls it.
 template <int G>
 __device__ __forceinline__ void quantise(const uint4 (&u)[G], uint32_t (&w)[G], uint32_t (&scale)[G]) {
@@ -72,13 +78,16 @@ __device__ __forceinline__ void quantise(const uint4 (&u)[G], uint32_t (&w)[G], 
       w[g] = 0u;
       continue;
     }
-    const uint32_t bits = cosa::pack_bf16x2(__uint_as_float(m << 16) / 7.0f, 0.f) & 0xFFFFu;
-    const float s = __uint_as_float(bits << 16);
+    // max|x| / 7 by the reciprocal: the quotient of an 8-bit significand is never halfway between two bf16 numbers (7 times
+    // an odd 9-bit one is odd and above 255), nor nearer to it than 2^-12 of itself, so the product's 2^-23 does not matter
+    uint32_t bits = cosa::pack_bf16x2(__uint_as_float(m << 16) * (1.0f / 7.0f), 0.f) & 0xFFFFu;
+    if (bits >= 0x0400u && bits < 0x7C00u) {      // 2^-119 <= s < 2^121
+      w[g] = codes8(u[g], rcp_approx(__uint_as_float(bits << 16)));
+    } else {                                      // near the ends of the range, subnormal scales among them
+      bits = cosa::pack_bf16x2(__uint_as_float(m << 16) / 7.0f, 0.f) & 0xFFFFu;
+      w[g] = bits == 0u ? 0u : codes8_slow(u[g], __uint_as_float(bits << 16));
+    }
     scale[g] = bits;
-    if (bits >= 0x0400u && bits < 0x7C00u)        // 2^-119 <= s < 2^121
-      w[g] = codes8(u[g], 1.0f / s);
-    else
-      w[g] = bits == 0u ? 0u : codes8_slow(u[g], s);
   }
 }
 
@@ -193,6 +202,7 @@ __global__ void __launch_bounds__(kThreads) store_rows_kernel(const ConvertLaunc
   constexpr int G = Tile<D>::G;
   __shared__ int s_slot[kMaxTokens], s_phys[kMaxTokens];
   const int tid = threadIdx.x;
+  wait_for_stream();
   const int t0 = blockIdx.x * tokens;
   const int last = L.cu_seqlens[L.num_reqs];
   if (blockIdx.x == 0 && tid == 0 && (L.cu_seqlens[0] != 0 || last > L.total_tokens))
@@ -241,6 +251,7 @@ __global__ void __launch_bounds__(kThreads) pages_kernel(const ConvertLaunch L, 
   constexpr int G = T::G;
   const int tid = threadIdx.x;
   const int b = blockIdx.y;
+  wait_for_stream();
   const Range range = slots_of(L, b, L.kv_len[b], L.start ? L.start[b] : 0);
   if (!range.ok && blockIdx.x == 0 && tid == 0) cosa::report_status(L.status, cosa::kStatusBadInput);
   const int c = tid % 4;
@@ -308,11 +319,8 @@ dim3 pages_grid(const ConvertLaunch& L, int tokens) {
 template <bool LOAD>
 cudaError_t launch_pages(const ConvertLaunch& L, cudaStream_t stream) {
   const Shape s(L.num_kv_heads);
-  if (L.head_dim == 128)
-    pages_kernel<128, LOAD><<<pages_grid(L, s.tokens), s.threads, 0, stream>>>(L, s.tokens);
-  else
-    pages_kernel<64, LOAD><<<pages_grid(L, s.tokens), s.threads, 0, stream>>>(L, s.tokens);
-  return cudaGetLastError();
+  return launch_after(L.head_dim == 128 ? pages_kernel<128, LOAD> : pages_kernel<64, LOAD>, pages_grid(L, s.tokens), s.threads, 0,
+                      stream, 1, L, s.tokens);
 }
 
 }  // namespace
@@ -323,11 +331,7 @@ cudaError_t launch_store_rows(const ConvertLaunch& L, cudaStream_t stream) {
   const int tokens = L.total_tokens <= 8 * 152 ? 1 : s.tokens;
   const int threads = std::min(s.threads, (4 * tokens * L.num_kv_heads + 31) / 32 * 32);
   const unsigned grid = static_cast<unsigned>((static_cast<int64_t>(L.total_tokens) + tokens - 1) / tokens);
-  if (L.head_dim == 128)
-    store_rows_kernel<128><<<grid, threads, 0, stream>>>(L, tokens);
-  else
-    store_rows_kernel<64><<<grid, threads, 0, stream>>>(L, tokens);
-  return cudaGetLastError();
+  return launch_after(L.head_dim == 128 ? store_rows_kernel<128> : store_rows_kernel<64>, dim3(grid), threads, 0, stream, 1, L, tokens);
 }
 
 cudaError_t launch_store_pages(const ConvertLaunch& L, cudaStream_t stream) { return launch_pages<false>(L, stream); }

@@ -4,7 +4,7 @@
 // largest weights (ties: the lowest slot), `budget` in all; kept slots move in order into other pages.
 //
 // A slot's weight becomes a 32-bit key that sorts as the weight does (missing pages 0, NaN 1, kept in any case the
-// largest).  A cluster of one to eight CTAs has the slots of one (request, kv head), a run each, their keys in shared
+// largest).  A cluster of one to sixteen CTAs has the slots of one (request, kv head), a run each, their keys in shared
 // memory.  The K-th largest key is found by a radix select, 11 bits at a time from the top: every CTA counts its
 // keys' digits, sums its share of the bins over the cluster through distributed shared memory, and looks the
 // digit up among the sums.  Everything above the K-th key is kept, and the lowest slots among the equal ones; the
@@ -27,7 +27,7 @@ namespace cg = cooperative_groups;
 
 constexpr int kSelectThreads = 512;
 constexpr int kWarps = kSelectThreads / 32;
-constexpr int kCluster = 8;             // CTAs of a cluster at most
+constexpr int kCluster = 16;            // CTAs of a cluster at most
 constexpr int kBins = 2048;
 constexpr int kMaxKeys = 16384;         // keys that a CTA holds; longer runs are formed again for each pass
 constexpr uint32_t kMissing = 0u, kNan = 1u, kAlways = 0xFFFFFFFFu;
@@ -77,7 +77,8 @@ struct SelectSmem {
   int hist[kBins];                // this CTA's digits
   int sums[kBins];                // this CTA's share of the bins over the cluster: kBins / ctas of them
   int share_total;                // their total
-  int counts[2];                  // keep and want of the passes; then this CTA's keys above the K-th, and equal to it
+  int counts[2];                  // keep and want of the passes
+  int mine[2];                    // this CTA's keys above the K-th, and equal to it
   int warp[32];
   uint32_t digit;
 };
@@ -95,6 +96,8 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictLaunc
   const int tid = threadIdx.x;
   const int item = static_cast<int>(blockIdx.x) / ctas;
   const int b = item / L.num_kv_heads, h = item % L.num_kv_heads;
+  wait_for_stream();
+  let_next_start();
   const int n = length_of(L, b);
   if (tid == 0 && rank == 0 && h == 0 && n != L.kv_len[b]) cosa::report_status(L.status, cosa::kStatusBadInput);
   const size_t row = static_cast<size_t>(b) * L.num_kv_heads + h;
@@ -215,17 +218,20 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictLaunc
     int total_above, total_equal;
     above = block_scan(above, sm.warp, total_above);
     equal = block_scan(equal, sm.warp, total_equal);
-    cluster.sync();                 // nobody reads the counts of the passes any more
     if (tid == 0) {
-      sm.counts[0] = total_above;
-      sm.counts[1] = total_equal;
+      sm.mine[0] = total_above;
+      sm.mine[1] = total_equal;
     }
     cluster.sync();
-    for (int r = 0; r < rank; ++r) {
-      const int* c = cluster.map_shared_rank(sm.counts, r);
-      above += c[0];
-      equal += c[1];
+    // what the CTAs before this one have: a lane for each
+    int before_above = 0, before_equal = 0;
+    if (tid % 32 < rank) {
+      const int* c = cluster.map_shared_rank(sm.mine, tid % 32);
+      before_above = c[0];
+      before_equal = c[1];
     }
+    above += __reduce_add_sync(0xffffffffu, before_above);
+    equal += __reduce_add_sync(0xffffffffu, before_equal);
     int at = above + min(equal, want);
     for (int s = first; s < last; ++s) {
       const uint32_t k = key(s);
@@ -250,6 +256,7 @@ __global__ void __launch_bounds__(32 * kMoveWarps) move_kernel(const EvictLaunch
   const int lane = threadIdx.x % 32;
   const int b = blockIdx.z, h = blockIdx.y;
   const int slot0 = static_cast<int>(blockIdx.x * kMoveWarps + threadIdx.x / 32) * kTile;
+  wait_for_stream();
   const int rows = min(kTile, L.new_len[b] - slot0);
   if (rows <= 0) return;
   const size_t row = static_cast<size_t>(b) * L.num_kv_heads + h;
@@ -297,45 +304,33 @@ __global__ void __launch_bounds__(32 * kMoveWarps) move_kernel(const EvictLaunch
     for (int g = 0; g < T::G / 2; ++g) reinterpret_cast<uint32_t*>(dst + base + t * (2 * T::G))[g] = sc[g];
 }
 
-// A cluster of as many CTAs as give each about 4096 slots: below that, the pass over the keys costs less than the
-// barriers that sharing it takes.
+// Clusters of as many CTAs as fill the card, while each still has 2048 slots (with fewer, the pass over the keys costs less
+// than the barriers that sharing it takes), and as many as it takes to hold the keys.
 cudaError_t launch_select(const EvictLaunch& L, cudaStream_t stream) {
+  const int64_t items = static_cast<int64_t>(L.num_reqs) * L.num_kv_heads;
   int ctas = 1;
-  while (ctas < kCluster && static_cast<int64_t>(ctas) * 4096 < L.max_seqlen) ctas *= 2;
+  while (ctas < kCluster && ((items * ctas < 152 && static_cast<int64_t>(ctas) * 2048 < L.max_seqlen) ||
+                             static_cast<int64_t>(ctas) * kMaxKeys < L.max_seqlen))
+    ctas *= 2;
   const int run = (L.max_seqlen - 1) / ctas + 1;
   const bool held = run <= kMaxKeys;
-  cudaLaunchConfig_t c{};
-  c.gridDim = dim3(static_cast<unsigned>(L.num_reqs * L.num_kv_heads * ctas));
-  c.blockDim = dim3(kSelectThreads);
-  c.dynamicSmemBytes = held ? static_cast<size_t>(padded(run)) * 4 : 0;
-  c.stream = stream;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = static_cast<unsigned>(ctas);
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  c.attrs = &attr;
-  c.numAttrs = 1;
   auto* kernel = held ? select_kernel<true> : select_kernel<false>;
-  if (held) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, padded(kMaxKeys) * 4);
-    if (e != cudaSuccess) return e;
-  }
-  return cudaLaunchKernelEx(&c, kernel, L);
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess && held) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, padded(kMaxKeys) * 4);
+  if (e != cudaSuccess) return e;
+  return launch_after(kernel, dim3(static_cast<unsigned>(items * ctas)), kSelectThreads, held ? static_cast<size_t>(padded(run)) * 4 : 0,
+                      stream, ctas, L);
 }
 
 }  // namespace
 
 cudaError_t launch_evict(const EvictLaunch& L, cudaStream_t stream) {
-  cudaError_t e = launch_select(L, stream);
+  const cudaError_t e = launch_select(L, stream);
   if (e != cudaSuccess) return e;
   const int64_t most = std::min(L.budget, L.max_seqlen);
   const dim3 grid(static_cast<unsigned>((most + kMoveWarps * kTile - 1) / (kMoveWarps * kTile)), static_cast<unsigned>(L.num_kv_heads),
                   static_cast<unsigned>(L.num_reqs));
-  if (L.head_dim == 128)
-    move_kernel<128><<<grid, 32 * kMoveWarps, 0, stream>>>(L);
-  else
-    move_kernel<64><<<grid, 32 * kMoveWarps, 0, stream>>>(L);
-  return cudaGetLastError();
+  return launch_after(L.head_dim == 128 ? move_kernel<128> : move_kernel<64>, grid, 32 * kMoveWarps, 0, stream, 1, L);
 }
 
 }  // namespace cosa_kv

@@ -10,6 +10,26 @@
 
 namespace cosa_kv {
 
+// Launch of a kernel that begins with wait_for_stream() (kv_layout.cuh), in clusters of `cluster` CTAs where it is not 1.
+template <typename... Params, typename... Args>
+cudaError_t launch_after(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t stream, int cluster,
+                         const Args&... args) {
+  cudaLaunchAttribute attrs[2]{};
+  attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attrs[0].val.programmaticStreamSerializationAllowed = 1;
+  attrs[1].id = cudaLaunchAttributeClusterDimension;
+  attrs[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attrs[1].val.clusterDim.y = attrs[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t c{};
+  c.gridDim = grid;
+  c.blockDim = dim3(static_cast<unsigned>(threads));
+  c.dynamicSmemBytes = smem;
+  c.stream = stream;
+  c.attrs = attrs;
+  c.numAttrs = cluster == 1 ? 1 : 2;
+  return cudaLaunchKernelEx(&c, kernel, args...);
+}
+
 struct RopeLaunch {
   const uint16_t *q, *k, *v, *q_weight, *k_weight;
   const double* inv_freq;

@@ -47,6 +47,12 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
                     cosa::pack_bf16x2(x[6], x[7]));
 }
 
+// Kernels of this library are launched while the kernel before them on the stream still runs (its last CTAs, or all of
+// it where it allows), so that their launch costs no time of its own.  wait_for_stream() ends when that kernel has ended
+// and its writes are visible; every thread calls it before anything else.  let_next_start() allows it to the next one.
+__device__ __forceinline__ void wait_for_stream() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 struct Range {
   int first, end;
   bool ok;

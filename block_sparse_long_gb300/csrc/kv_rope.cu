@@ -28,6 +28,7 @@ __global__ void __launch_bounds__(kThreads, 4) rope_kernel(const RopeLaunch L, c
   constexpr int kRows = 32 / kLanes;       // rows of a warp at a time
   constexpr unsigned kAll = 0xffffffffu;
   const int tid = threadIdx.x, lane = tid % 32, l = lane % kLanes, sub = lane / kLanes;
+  wait_for_stream();
   const int64_t unit = (static_cast<int64_t>(blockIdx.x) * kThreads + tid) / 32;
   const int last = L.cu_seqlens[L.num_reqs];
   if (blockIdx.x == 0 && tid == 0 && (L.cu_seqlens[0] != 0 || last > L.total_tokens))
@@ -172,11 +173,7 @@ cudaError_t launch_rope(const RopeLaunch& L, cudaStream_t stream) {
   int split = 1;
   while (2 * split <= steps && static_cast<int64_t>(L.total_tokens) * split < 152 * 32) split *= 2;
   const unsigned grid = static_cast<unsigned>((static_cast<int64_t>(L.total_tokens) * split * 32 + kThreads - 1) / kThreads);
-  if (L.head_dim == 128)
-    rope_kernel<128><<<grid, kThreads, 0, stream>>>(L, split);
-  else
-    rope_kernel<64><<<grid, kThreads, 0, stream>>>(L, split);
-  return cudaGetLastError();
+  return launch_after(L.head_dim == 128 ? rope_kernel<128> : rope_kernel<64>, dim3(grid), kThreads, 0, stream, 1, L, split);
 }
 
 }  // namespace cosa_kv
