@@ -18,6 +18,12 @@ bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) %
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+int shift_of(int page_size) {
+  int s = 4;
+  while ((1 << s) < page_size) ++s;
+  return s;
+}
+
 // What every call asks of the parameters.
 int check_common(const cosa_kv_params* p) {
   if (p == nullptr) return COSA_ERR_INVALID_ARG;
@@ -114,6 +120,7 @@ int cosa_qk_norm_rope(const cosa_kv_params* p, const void* q, const void* k, con
   L.num_kv_heads = p->num_kv_heads;
   L.head_dim = p->head_dim;
   L.page_size = p->page_size;
+  L.page_shift = shift_of(p->page_size);
   L.total_tokens = p->total_tokens;
   L.max_seqlen = p->max_seqlen;
   L.num_pages = p->num_pages;
@@ -160,6 +167,7 @@ int cosa_kv4_store(const cosa_kv_params* p, const void* k, const void* v, const 
   L.page_size = p->page_size;
   L.max_seqlen = p->max_seqlen;
   L.num_pages = p->num_pages;
+  L.page_shift = shift_of(p->page_size);
   L.num_kv4_pages = p->num_kv4_pages;
   L.max_pages_per_req = p->max_pages_per_req;
   if (pages) {
@@ -196,6 +204,7 @@ int cosa_kv4_load(const cosa_kv_params* p, const void* kv4_cache, const int32_t*
   L.page_size = p->page_size;
   L.max_seqlen = p->max_seqlen;
   L.num_pages = p->num_pages;
+  L.page_shift = shift_of(p->page_size);
   L.num_kv4_pages = p->num_kv4_pages;
   L.max_pages_per_req = p->max_pages_per_req;
   return done(cosa_kv::launch_load(L, static_cast<cudaStream_t>(stream)));
@@ -284,7 +293,7 @@ int cosa_kv4_evict(const cosa_kv_params* p, void* kv4_cache, const int32_t* page
   L.budget = p->budget;
   L.sink = p->sink;
   L.recent = p->recent;
-  for (L.page_shift = 4; (1 << L.page_shift) < p->page_size;) ++L.page_shift;
+  L.page_shift = shift_of(p->page_size);
   return done(cosa_kv::launch_evict(L, static_cast<cudaStream_t>(stream)));
 }
 

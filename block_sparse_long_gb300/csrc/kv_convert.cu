@@ -63,31 +63,42 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return y;
 }
 
-// Codes of a lane's values, a word per group, and the bits of the groups' scales.  Every lane of the warp calls it.
+// The larger magnitudes of two pairs of bf16 numbers (NaN above every number; the signs mean nothing).
+__device__ __forceinline__ uint32_t max_abs2(uint32_t x, uint32_t y) {
+  uint32_t r;
+  asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+  return r;
+}
+
+// Codes of eight values of a group whose largest magnitude has the bits m, and the bits of its scale.
+__device__ __forceinline__ uint32_t quantise8(const uint4& u, uint32_t m, uint32_t& scale) {
+  if (m >= 0x7F80u) {
+    scale = 0x7FC0u;
+    return 0u;
+  }
+  // max|x| / 7 by the reciprocal: the quotient of an 8-bit significand is never halfway between two bf16 numbers (7 times
+  // an odd 9-bit one is odd and above 255), nor nearer to it than 2^-12 of itself, so the product's 2^-23 does not matter
+  scale = cosa::pack_bf16x2(__uint_as_float(m << 16) * (1.0f / 7.0f), 0.f) & 0xFFFFu;
+  if (scale >= 0x0400u && scale < 0x7C00u) return codes8(u, rcp_approx(__uint_as_float(scale << 16)));     // 2^-119 <= s < 2^121
+  // near the ends of the range, subnormal scales among them
+  scale = cosa::pack_bf16x2(__uint_as_float(m << 16) / 7.0f, 0.f) & 0xFFFFu;
+  return scale == 0u ? 0u : codes8_slow(u, __uint_as_float(scale << 16));
+}
+
+// Codes of a lane's values of K and V, a word per group, and the bits of the groups' scales.  Every lane of the warp calls
+// it: the four lanes of a group find its largest magnitude, of K in the low half of a word and of V in the high half.
 template <int G>
-__device__ __forceinline__ void quantise(const uint4 (&u)[G], uint32_t (&w)[G], uint32_t (&scale)[G]) {
+__device__ __forceinline__ void quantise(const uint4 (&ku)[G], const uint4 (&vu)[G], uint32_t (&kw)[G], uint32_t (&ks)[G],
+                                         uint32_t (&vw)[G], uint32_t (&vs)[G]) {
 #pragma unroll
   for (int g = 0; g < G; ++g) {
-    // two magnitudes at a time as integers: they keep their order, with infinities and NaN above every number
-    uint32_t m = __vmaxu2(__vmaxu2(u[g].x & 0x7FFF7FFFu, u[g].y & 0x7FFF7FFFu), __vmaxu2(u[g].z & 0x7FFF7FFFu, u[g].w & 0x7FFF7FFFu));
-    m = max(m & 0xFFFFu, m >> 16);
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-    if (m >= 0x7F80u) {
-      scale[g] = 0x7FC0u;
-      w[g] = 0u;
-      continue;
-    }
-    // max|x| / 7 by the reciprocal: the quotient of an 8-bit significand is never halfway between two bf16 numbers (7 times
-    // an odd 9-bit one is odd and above 255), nor nearer to it than 2^-12 of itself, so the product's 2^-23 does not matter
-    uint32_t bits = cosa::pack_bf16x2(__uint_as_float(m << 16) * (1.0f / 7.0f), 0.f) & 0xFFFFu;
-    if (bits >= 0x0400u && bits < 0x7C00u) {      // 2^-119 <= s < 2^121
-      w[g] = codes8(u[g], rcp_approx(__uint_as_float(bits << 16)));
-    } else {                                      // near the ends of the range, subnormal scales among them
-      bits = cosa::pack_bf16x2(__uint_as_float(m << 16) / 7.0f, 0.f) & 0xFFFFu;
-      w[g] = bits == 0u ? 0u : codes8_slow(u[g], __uint_as_float(bits << 16));
-    }
-    scale[g] = bits;
+    const uint32_t k = max_abs2(max_abs2(ku[g].x, ku[g].y), max_abs2(ku[g].z, ku[g].w));
+    const uint32_t v = max_abs2(max_abs2(vu[g].x, vu[g].y), max_abs2(vu[g].z, vu[g].w));
+    uint32_t m = max_abs2(__byte_perm(k, v, 0x5410), __byte_perm(k, v, 0x7632));
+    m = max_abs2(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = max_abs2(m, __shfl_xor_sync(0xffffffffu, m, 2)) & 0x7FFF7FFFu;
+    kw[g] = quantise8(ku[g], m & 0xFFFFu, ks[g]);
+    vw[g] = quantise8(vu[g], m >> 16, vs[g]);
   }
 }
 
@@ -192,7 +203,7 @@ __device__ __forceinline__ Range slots_of(const ConvertLaunch& L, int b, int len
 }
 
 __device__ __forceinline__ int page_of(const int32_t* table, const ConvertLaunch& L, int b, int slot, int pages) {
-  const int phys = table[static_cast<size_t>(b) * L.max_pages_per_req + slot / L.page_size];
+  const int phys = table[static_cast<size_t>(b) * L.max_pages_per_req + (slot >> L.page_shift)];
   return phys >= 0 && phys < pages ? phys : -1;
 }
 
@@ -236,10 +247,9 @@ __global__ void __launch_bounds__(kThreads) store_rows_kernel(const ConvertLaunc
     load_row<G>(L.k + t * L.k_stride + static_cast<int64_t>(h) * D, c, in, ku);
     load_row<G>(L.v + t * L.v_stride + static_cast<int64_t>(h) * D, c, in, vu);
     uint32_t kw[G], ks[G], vw[G], vs[G];
-    quantise<G>(ku, kw, ks);
-    quantise<G>(vu, vw, vs);
+    quantise<G>(ku, vu, kw, ks, vw, vs);
     if (in && s_phys[j] >= 0)
-      put<D>(L.cache + tile_offset<D>(s_phys[j], h, s_slot[j], L.num_kv_heads, L.page_size), s_slot[j] % kTile, c, kw, ks,
+      put<D>(L.cache + tile_offset<D>(s_phys[j], h, s_slot[j], L.num_kv_heads, L.page_shift), s_slot[j] % kTile, c, kw, ks,
              vw, vs);
   }
 }
@@ -269,8 +279,8 @@ __global__ void __launch_bounds__(kThreads) pages_kernel(const ConvertLaunch L, 
       const int h = r < rows ? r - j * L.num_kv_heads : 0;
       const int slot = slot0 + j;
       const bool in = r < rows && slot >= range.first && slot < range.end;
-      const size_t at = ((static_cast<size_t>(p16) * L.page_size + slot % L.page_size) * L.num_kv_heads + h) * D;
-      uint8_t* tile = L.cache + tile_offset<D>(p4, h, slot, L.num_kv_heads, L.page_size);
+      const size_t at = ((static_cast<size_t>(p16) * L.page_size + (slot & ((1 << L.page_shift) - 1))) * L.num_kv_heads + h) * D;
+      uint8_t* tile = L.cache + tile_offset<D>(p4, h, slot, L.num_kv_heads, L.page_shift);
       const int t = slot % kTile;
       if (LOAD) {
         if (!in) continue;
@@ -290,8 +300,7 @@ __global__ void __launch_bounds__(kThreads) pages_kernel(const ConvertLaunch L, 
         load_row<G>(L.k + at, c, in, ku);
         load_row<G>(L.v + at, c, in, vu);
         uint32_t kw[G], ks[G], vw[G], vs[G];
-        quantise<G>(ku, kw, ks);
-        quantise<G>(vu, vw, vs);
+        quantise<G>(ku, vu, kw, ks, vw, vs);
         if (in) put<D>(tile, t, c, kw, ks, vw, vs);
       }
     }

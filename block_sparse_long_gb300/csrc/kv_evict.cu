@@ -146,25 +146,32 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictLaunc
       if (k != kMissing && (pass == 0 || (k >> (shift + bits)) == prefix)) atomicAdd(&sm.hist[(k >> shift) & ((1u << bits) - 1u)], 1);
     }
     cluster.sync();
-    // this CTA's share of the bins, summed over the cluster
-    for (int i = tid; i < share; i += kSelectThreads) {
-      int v = 0;
-      for (int r = 0; r < ctas; ++r) v += cluster.map_shared_rank(sm.hist, r)[rank * share + i];
-      sm.sums[i] = v;
-    }
+    // (the cluster has read the sums of the pass before)
+    for (int i = tid; i < share; i += kSelectThreads) sm.sums[i] = 0;
+    if (tid == 0) sm.share_total = 0;
     __syncthreads();
-    if (tid < 32) {
-      int v = 0;
-      for (int i = tid; i < share; i += 32) v += sm.sums[i];
-      v = __reduce_add_sync(0xffffffffu, v);
-      if (tid == 0) sm.share_total = v;
+    // This CTA's share of the bins, summed over the cluster: a thread per bin and per four CTAs, whose loads go together.
+    int total = 0;
+    for (int i = tid; i < share * ((ctas + 3) / 4); i += kSelectThreads) {
+      const int bin = i & (share - 1), r0 = i / share * 4;
+      int v[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = r0 + k < ctas ? cluster.map_shared_rank(sm.hist, r0 + k)[rank * share + bin] : 0;
+      const int sum = (v[0] + v[1]) + (v[2] + v[3]);
+      total += sum;
+      if (ctas > 4)
+        atomicAdd(&sm.sums[bin], sum);
+      else
+        sm.sums[bin] = sum;
     }
+    total = __reduce_add_sync(0xffffffffu, total);
+    if (tid % 32 == 0) atomicAdd(&sm.share_total, total);
     cluster.sync();
-    // the digit: shares from the top, then the bins of the share that has it (a warp, in every CTA alike)
+    // The digit: shares from the top, then the bins of the share that has it (a warp, in every CTA alike).
     if (tid < 32) {
       const int r = ctas - 1 - tid;                   // lane 0 has the top share
       const int mine = r >= 0 ? *cluster.map_shared_rank(&sm.share_total, r) : 0;
-      int end = warp_scan(mine);
+      const int end = warp_scan(mine);
       if (pass == 0) {
         keep = min(L.budget, __shfl_sync(0xffffffffu, end, 31));
         want = keep;
@@ -173,23 +180,27 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictLaunc
         want = sm.counts[1];
       }
       const int at = __ffs(__ballot_sync(0xffffffffu, end >= want)) - 1;      // want <= the total: there is one
-      const int owner = ctas - 1 - at;
+      const int owner = max(ctas - 1 - at, 0);
       int before = __shfl_sync(0xffffffffu, end - mine, at);
-      const int* sums = cluster.map_shared_rank(sm.sums, max(owner, 0));
-      uint32_t digit = 0;
-      for (int i0 = share - 1; owner >= 0; i0 -= 32) {                        // ends in the share: its total reaches want
-        const int i = i0 - tid;
-        const int v = i >= 0 ? sums[i] : 0;
-        const int e = warp_scan(v);
-        const unsigned hit = __ballot_sync(0xffffffffu, before + e >= want);
-        if (hit || i0 < 32) {
-          const int lane = hit ? __ffs(hit) - 1 : 0;
-          digit = static_cast<uint32_t>(owner * share + i0 - lane);
-          before += __shfl_sync(0xffffffffu, e - v, lane);
-          break;
+      // lane l has the bins from share - 1 - l * each downwards
+      const int each = share / 32;
+      const int* sums = cluster.map_shared_rank(sm.sums, owner) + share - (tid + 1) * each;
+      int own = 0;
+#pragma unroll 4
+      for (int i = 0; i < each; ++i) own += sums[i];
+      const int upto = warp_scan(own);
+      const unsigned hit = __ballot_sync(0xffffffffu, before + upto >= want);
+      const int lane = hit ? __ffs(hit) - 1 : 31;
+      before += __shfl_sync(0xffffffffu, upto - own, lane);
+      int i = each - 1;
+      if (tid == lane)
+        for (int v = sums[i]; i > 0 && before + v < want; v = sums[i]) {
+          before += v;
+          --i;
         }
-        before += __shfl_sync(0xffffffffu, e, 31);
-      }
+      before = __shfl_sync(0xffffffffu, before, lane);
+      i = __shfl_sync(0xffffffffu, i, lane);
+      const uint32_t digit = static_cast<uint32_t>(owner * share + share - (lane + 1) * each + i);
       if (tid == 0) {
         sm.digit = digit;
         sm.counts[0] = keep;
@@ -266,13 +277,13 @@ __global__ void __launch_bounds__(32 * kMoveWarps) move_kernel(const EvictLaunch
   if (lane < rows) {
     const int s = L.kept[row * L.budget + slot0 + lane];
     const int phys = L.page_table[static_cast<size_t>(b) * L.max_pages_per_req + (s >> L.page_shift)];
-    from = tile_offset<D>(phys, h, s, L.num_kv_heads, L.page_size);
+    from = tile_offset<D>(phys, h, s, L.num_kv_heads, L.page_shift);
     at = s % kTile;
     if (L.weights_out) L.weights_out[row * L.max_seqlen + slot0 + lane] = L.weights[row * L.max_seqlen + s];
   }
   const int dst_phys = page_of(L.dst_page_table, L.max_dst_pages, L, b, slot0);
   if (dst_phys < 0) return;
-  uint8_t* dst = L.cache + tile_offset<D>(dst_phys, h, slot0, L.num_kv_heads, L.page_size);
+  uint8_t* dst = L.cache + tile_offset<D>(dst_phys, h, slot0, L.num_kv_heads, L.page_shift);
   uint4 k[kSteps], v[kSteps];
 #pragma unroll
   for (int i = 0; i < kSteps; ++i) {

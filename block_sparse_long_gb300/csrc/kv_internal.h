@@ -39,6 +39,7 @@ struct RopeLaunch {
   int64_t q_stride, k_stride, v_stride;
   int num_reqs, num_q_heads, num_kv_heads, head_dim, page_size, total_tokens, max_seqlen, num_pages, max_pages_per_req;
   int rotary_dim, interleaved;
+  int page_shift;        // log2(page_size)
   float eps;
 };
 cudaError_t launch_rope(const RopeLaunch& L, cudaStream_t stream);
@@ -52,6 +53,7 @@ struct ConvertLaunch {
   int32_t* status;
   int64_t k_stride, v_stride;
   int num_reqs, num_kv_heads, head_dim, page_size, total_tokens, max_seqlen, num_pages, num_kv4_pages, max_pages_per_req;
+  int page_shift;        // log2(page_size)
 };
 cudaError_t launch_store_rows(const ConvertLaunch& L, cudaStream_t stream);
 cudaError_t launch_store_pages(const ConvertLaunch& L, cudaStream_t stream);

@@ -28,9 +28,9 @@ __device__ __forceinline__ int v_row(int t) { return (t & 1) * 8 + (t >> 1); }
 
 // First byte of the tile of `slot` of (physical page, kv head).
 template <int D>
-__device__ __forceinline__ size_t tile_offset(int phys, int kvh, int slot, int num_kv_heads, int page_size) {
-  const int tiles = page_size / kTile;
-  return ((static_cast<size_t>(phys) * num_kv_heads + kvh) * tiles + (slot % page_size) / kTile) * Tile<D>::kBytes;
+__device__ __forceinline__ size_t tile_offset(int phys, int kvh, int slot, int num_kv_heads, int page_shift) {
+  const int tile = (slot & ((1 << page_shift) - 1)) / kTile;
+  return (((static_cast<size_t>(phys) * num_kv_heads + kvh) << (page_shift - 4)) + tile) * Tile<D>::kBytes;
 }
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }

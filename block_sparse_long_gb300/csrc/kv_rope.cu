@@ -23,7 +23,7 @@ constexpr int kBatch = 3;      // rows per lane in flight
 // lane: chunks l and l + rotary_dim / 16 of the rotated part, then what is left of the head two by two.
 // (Interleaved pairs are neighbours: any choice.)
 template <int D>
-__global__ void __launch_bounds__(kThreads, 4) rope_kernel(const RopeLaunch L, const int split) {
+__global__ void __launch_bounds__(kThreads, 4) rope_kernel(const RopeLaunch L, const int split_log2) {
   constexpr int kLanes = D / 16;
   constexpr int kRows = 32 / kLanes;       // rows of a warp at a time
   constexpr unsigned kAll = 0xffffffffu;
@@ -33,9 +33,10 @@ __global__ void __launch_bounds__(kThreads, 4) rope_kernel(const RopeLaunch L, c
   const int last = L.cu_seqlens[L.num_reqs];
   if (blockIdx.x == 0 && tid == 0 && (L.cu_seqlens[0] != 0 || last > L.total_tokens))
     cosa::report_status(L.status, cosa::kStatusBadInput);
-  const int64_t t = unit / split;
+  const int split = 1 << split_log2;
+  const int64_t t = unit >> split_log2;
   if (t >= min(last, L.total_tokens)) return;
-  const int part = static_cast<int>(unit - t * split);
+  const int part = static_cast<int>(unit) & (split - 1);
 
   const int rot_chunks = L.rotary_dim / 8;        // chunks of eight rotated values
   const bool turned = l < rot_chunks / 2;         // this lane's chunks are rotated (both or neither)
@@ -71,9 +72,9 @@ __global__ void __launch_bounds__(kThreads, 4) rope_kernel(const RopeLaunch L, c
   size_t page_row = 0;                            // (token, kv head 0) of the bf16 caches
   bool paged = false;
   if (L.k_cache) {
-    const int phys = L.page_table[static_cast<size_t>(b) * L.max_pages_per_req + slot / L.page_size];
+    const int phys = L.page_table[static_cast<size_t>(b) * L.max_pages_per_req + (slot >> L.page_shift)];
     paged = phys >= 0 && phys < L.num_pages;
-    page_row = (static_cast<size_t>(max(phys, 0)) * L.page_size + slot % L.page_size) * L.num_kv_heads;
+    page_row = ((static_cast<size_t>(max(phys, 0)) << L.page_shift) + (slot & ((1 << L.page_shift) - 1))) * L.num_kv_heads;
   }
 
   // The lane's eight angles.  An angle is formed in turns and in 64 bits, less its whole turns; the rest is at most
@@ -170,9 +171,9 @@ __global__ void __launch_bounds__(kThreads, 4) rope_kernel(const RopeLaunch L, c
 cudaError_t launch_rope(const RopeLaunch& L, cudaStream_t stream) {
   // a token's heads on several warps while the tokens alone do not fill the card (152 SMs of 32 warps)
   const int steps = (L.num_q_heads + 2 * L.num_kv_heads) / (L.head_dim == 128 ? 4 : 8);
-  int split = 1;
-  while (2 * split <= steps && static_cast<int64_t>(L.total_tokens) * split < 152 * 32) split *= 2;
-  const unsigned grid = static_cast<unsigned>((static_cast<int64_t>(L.total_tokens) * split * 32 + kThreads - 1) / kThreads);
+  int split = 0;       // log2
+  while ((2 << split) <= steps && (static_cast<int64_t>(L.total_tokens) << split) < 152 * 32) ++split;
+  const unsigned grid = static_cast<unsigned>(((static_cast<int64_t>(L.total_tokens) << split) * 32 + kThreads - 1) / kThreads);
   return launch_after(L.head_dim == 128 ? rope_kernel<128> : rope_kernel<64>, dim3(grid), kThreads, 0, stream, 1, L, split);
 }
 
