@@ -75,7 +75,7 @@ __device__ __forceinline__ int block_scan(int v, int* s_warp, int& total) {
 
 struct SelectSmem {
   int hist[kBins];                // this CTA's digits
-  int sums[kBins];                // this CTA's share of the bins over the cluster: kBins / ctas of them
+  alignas(16) int sums[kBins];    // this CTA's share of the bins over the cluster, from the top: kBins / ctas of them
   int share_total;                // their total
   int counts[2];                  // keep and want of the passes
   int mine[2];                    // this CTA's keys above the K-th, and equal to it
@@ -88,7 +88,7 @@ struct SelectSmem {
 __host__ __device__ constexpr int padded(int i) { return i + i / 32; }
 
 template <bool HELD>
-__global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictLaunch L) {
+__global__ void __launch_bounds__(kSelectThreads, 3) select_kernel(const EvictLaunch L) {
   extern __shared__ uint32_t s_keys[];
   __shared__ SelectSmem sm;
   cg::cluster_group cluster = cg::this_cluster();
@@ -114,7 +114,7 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictLaunc
   };
   auto key = [&](int s) -> uint32_t { return HELD ? s_keys[padded(s - lo)] : form(s, table[s >> L.page_shift], w[s]); };
   if (HELD) {
-    constexpr int kDeep = 8;          // loads in flight per thread
+    constexpr int kDeep = 8;          // slots in flight per thread
     for (int s0 = lo + tid; s0 < hi; s0 += kDeep * kSelectThreads) {
       float weight[kDeep];
       int phys[kDeep];
@@ -148,24 +148,33 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictLaunc
     cluster.sync();
     // (the cluster has read the sums of the pass before)
     for (int i = tid; i < share; i += kSelectThreads) sm.sums[i] = 0;
-    if (tid == 0) sm.share_total = 0;
     __syncthreads();
     // This CTA's share of the bins, summed over the cluster: a thread per bin and per four CTAs, whose loads go together.
-    int total = 0;
     for (int i = tid; i < share * ((ctas + 3) / 4); i += kSelectThreads) {
       const int bin = i & (share - 1), r0 = i / share * 4;
       int v[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) v[k] = r0 + k < ctas ? cluster.map_shared_rank(sm.hist, r0 + k)[rank * share + bin] : 0;
-      const int sum = (v[0] + v[1]) + (v[2] + v[3]);
-      total += sum;
-      if (ctas > 4)
-        atomicAdd(&sm.sums[bin], sum);
-      else
-        sm.sums[bin] = sum;
+      atomicAdd(&sm.sums[share - 1 - bin], (v[0] + v[1]) + (v[2] + v[3]));
     }
-    total = __reduce_add_sync(0xffffffffu, total);
-    if (tid % 32 == 0) atomicAdd(&sm.share_total, total);
+    __syncthreads();
+    // then, from the top bin down, the number of keys in the bins so far; a thread has up to four neighbouring bins
+    {
+      const int each = max(1, share / kSelectThreads);
+      int v[kBins / kSelectThreads], own = 0, total;
+#pragma unroll
+      for (int k = 0; k < kBins / kSelectThreads; ++k) {
+        v[k] = k < each && tid * each < share ? sm.sums[tid * each + k] : 0;
+        own += v[k];
+      }
+      int upto = block_scan(own, sm.warp, total);
+#pragma unroll
+      for (int k = 0; k < kBins / kSelectThreads; ++k) {
+        upto += v[k];
+        if (k < each && tid * each < share) sm.sums[tid * each + k] = upto;
+      }
+      if (tid == 0) sm.share_total = total;
+    }
     cluster.sync();
     // The digit: shares from the top, then the bins of the share that has it (a warp, in every CTA alike).
     if (tid < 32) {
@@ -182,25 +191,19 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictLaunc
       const int at = __ffs(__ballot_sync(0xffffffffu, end >= want)) - 1;      // want <= the total: there is one
       const int owner = max(ctas - 1 - at, 0);
       int before = __shfl_sync(0xffffffffu, end - mine, at);
-      // lane l has the bins from share - 1 - l * each downwards
-      const int each = share / 32;
-      const int* sums = cluster.map_shared_rank(sm.sums, owner) + share - (tid + 1) * each;
-      int own = 0;
+      // the bins above the digit are those with which the sum stays below `want`
+      const int4* sums = reinterpret_cast<const int4*>(cluster.map_shared_rank(sm.sums, owner));
+      int above = 0, most = 0;
 #pragma unroll 4
-      for (int i = 0; i < each; ++i) own += sums[i];
-      const int upto = warp_scan(own);
-      const unsigned hit = __ballot_sync(0xffffffffu, before + upto >= want);
-      const int lane = hit ? __ffs(hit) - 1 : 31;
-      before += __shfl_sync(0xffffffffu, upto - own, lane);
-      int i = each - 1;
-      if (tid == lane)
-        for (int v = sums[i]; i > 0 && before + v < want; v = sums[i]) {
-          before += v;
-          --i;
-        }
-      before = __shfl_sync(0xffffffffu, before, lane);
-      i = __shfl_sync(0xffffffffu, i, lane);
-      const uint32_t digit = static_cast<uint32_t>(owner * share + share - (lane + 1) * each + i);
+      for (int i = tid; i < share / 4; i += 32) {
+        const int4 v = sums[i];
+        above += (before + v.x < want) + (before + v.y < want) + (before + v.z < want) + (before + v.w < want);
+        most = max(most, max(max(before + v.x < want ? v.x : 0, before + v.y < want ? v.y : 0),
+                             max(before + v.z < want ? v.z : 0, before + v.w < want ? v.w : 0)));
+      }
+      above = min(__reduce_add_sync(0xffffffffu, above), share - 1);
+      before += __reduce_max_sync(0xffffffffu, most);
+      const uint32_t digit = static_cast<uint32_t>(owner * share + share - 1 - above);
       if (tid == 0) {
         sm.digit = digit;
         sm.counts[0] = keep;
@@ -227,8 +230,18 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictLaunc
       equal += k == prefix;
     }
     int total_above, total_equal;
-    above = block_scan(above, sm.warp, total_above);
-    equal = block_scan(equal, sm.warp, total_equal);
+    if (HELD) {                     // both in one word: neither is above kMaxKeys
+      static_assert(kMaxKeys < 32768, "two counts in a word");
+      int total;
+      const int both = block_scan(above | (equal << 16), sm.warp, total);
+      above = both & 0xFFFF;
+      equal = both >> 16;
+      total_above = total & 0xFFFF;
+      total_equal = total >> 16;
+    } else {
+      above = block_scan(above, sm.warp, total_above);
+      equal = block_scan(equal, sm.warp, total_equal);
+    }
     if (tid == 0) {
       sm.mine[0] = total_above;
       sm.mine[1] = total_equal;
@@ -243,6 +256,7 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictLaunc
     }
     above += __reduce_add_sync(0xffffffffu, before_above);
     equal += __reduce_add_sync(0xffffffffu, before_equal);
+    cluster.barrier_arrive();       // this thread reads no other CTA's shared memory any more
     int at = above + min(equal, want);
     for (int s = first; s < last; ++s) {
       const uint32_t k = key(s);
@@ -254,7 +268,9 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictLaunc
     for (int j = keep + rank * kSelectThreads + tid; j < L.max_seqlen; j += ctas * kSelectThreads)
       L.weights_out[row * L.max_seqlen + j] = 0.f;
   if (tid == 0 && rank == 0 && h == 0) L.new_len[b] = keep;
-  cluster.sync();                   // a CTA's shared memory lives until its neighbours have read it
+  // a CTA's shared memory lives until its neighbours have read it
+  if (keep == 0) cluster.barrier_arrive();
+  cluster.barrier_wait();
 }
 
 // A destination tile of 16 slots per warp, all of whose pieces are in flight at once.
