@@ -29,7 +29,7 @@ int check_common(const cosa_kv_params* p) {
   if (p == nullptr) return COSA_ERR_INVALID_ARG;
   if (p->num_reqs < 1 || p->num_q_heads < 1 || p->num_kv_heads < 1) return COSA_ERR_INVALID_ARG;
   if (p->num_q_heads % p->num_kv_heads != 0) return COSA_ERR_INVALID_ARG;
-  if ((p->flags & ~COSA_KV_FLAG_INTERLEAVED) != 0 || p->reserved != 0) return COSA_ERR_INVALID_ARG;
+  if ((p->flags & ~(COSA_KV_FLAG_INTERLEAVED | COSA_KV_FLAG_TEST_STALL)) != 0 || p->reserved != 0) return COSA_ERR_INVALID_ARG;
   if (p->head_dim != 64 && p->head_dim != 128) return COSA_ERR_UNSUPPORTED;
   if (p->page_size != 16 && p->page_size != 32 && p->page_size != 64 && p->page_size != 128) return COSA_ERR_UNSUPPORTED;
   if (p->num_reqs > kMaxReqs || p->num_q_heads > kMaxHeads) return COSA_ERR_UNSUPPORTED;
@@ -252,6 +252,7 @@ int cosa_kv4_attention(const cosa_kv_params* p, const void* q, const int32_t* cu
   L.num_kv4_pages = p->num_kv4_pages;
   L.max_pages_per_req = p->max_pages_per_req;
   L.max_new_tokens = p->max_new_tokens;
+  L.stall = (p->flags & COSA_KV_FLAG_TEST_STALL) != 0;
   L.scale_log2 = static_cast<float>(p->sm_scale * 1.4426950408889634074);
   return done(cosa_kv::launch_attention(L, static_cast<cudaStream_t>(stream)));
 }

@@ -17,8 +17,8 @@
 // behind, the issue slots that unpack the codes.  So a warp works alone on tiles of 16 tokens out of its own
 // ring in shared memory, and nothing is shared between warps until the end of the CTA's part of a request.
 //
-// The work is the list of all (request, kv head, row tile, 16-token tile); every CTA takes an equal
-// run of it, whatever the lengths are.  A CTA that has all of a (request, kv head, row tile) writes its
+// The work is the list of all (request, kv head, row tile, unit of 32 or 16 tokens); every CTA takes an equal run
+// of it, whatever the lengths are.  A CTA that has all of a (request, kv head, row tile) writes its
 // output; otherwise it leaves its maximum, sum and unnormalised output in the workspace (a CTA has at
 // most two unfinished ones, the first and the last of its run) and kv4_combine_kernel joins them in order.
 #include <algorithm>
@@ -36,8 +36,8 @@ constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kSms = 152;
 constexpr int kMaxCtas = 3 * kSms;
-constexpr int kMinTiles = 8;      // tiles per CTA at least, where a request is shared between CTAs
-constexpr int kWholeTiles = 16;   // tiles of an item that one CTA takes alone
+constexpr int kMinUnits = 4;     // units per CTA at least, where a request is shared between CTAs: one per warp
+constexpr int kWholeUnits = 8;   // units of an item that one CTA takes alone
 constexpr int kFewItems = 64;     // items up to which the join has a block per row
 
 // What a CTA leaves about the unfinished (request, kv head, row tile) that begins in its run.
@@ -57,14 +57,16 @@ struct Args {
   int64_t pitch;
   int group;          // Hq / Hkv
   int page_shift;     // log2(P)
+  bool stall;         // test hook: no copy is issued
 };
 
 struct Request {
   int tok0, n, len;   // first row of q, query tokens, cache length
-  int64_t tiles, rts; // 16-token tiles (one at least, to write an empty request's zeros), row tiles
+  int64_t units, rts; // units of tokens (one at least, to write an empty request's zeros), row tiles
 };
 
-__device__ __forceinline__ Request request_of(const Args& a, int b, int rows, bool tell) {
+// `rows`: query rows of a row tile, `tokens`: of a unit.
+__device__ __forceinline__ Request request_of(const Args& a, int b, int rows, int tokens, bool tell) {
   Request r;
   r.tok0 = a.L.cu_seqlens[b];
   r.n = a.L.cu_seqlens[b + 1] - r.tok0;
@@ -73,7 +75,7 @@ __device__ __forceinline__ Request request_of(const Args& a, int b, int rows, bo
     if (tell) cosa::report_status(a.L.status, cosa::kStatusBadInput);
     r.n = r.len = 0;
   }
-  r.tiles = max(1, (r.len + kTile - 1) / kTile);
+  r.units = max(1, (r.len + tokens - 1) / tokens);
   r.rts = (static_cast<int64_t>(r.n) * a.group + rows - 1) / rows;
   return r;
 }
@@ -100,13 +102,13 @@ struct Shares {
 struct LaneUnits {
   int64_t own, end, items;
 };
-__device__ __forceinline__ LaneUnits lane_units(const Args& a, int rows, int b0, bool tell) {
+__device__ __forceinline__ LaneUnits lane_units(const Args& a, int rows, int tokens, int b0, bool tell) {
   const int lane = threadIdx.x % 32;
   LaneUnits u{0, 0, 0};
   if (b0 + lane < a.L.num_reqs) {
-    const Request r = request_of(a, b0 + lane, rows, tell);
+    const Request r = request_of(a, b0 + lane, rows, tokens, tell);
     u.items = r.rts * a.L.num_kv_heads;
-    u.own = r.tiles * u.items;
+    u.own = r.units * u.items;
   }
   u.end = u.own;
 #pragma unroll
@@ -118,10 +120,10 @@ __device__ __forceinline__ LaneUnits lane_units(const Args& a, int rows, int b0,
 }
 
 // The batch's shares (whole warp).  `first`: what the lanes have of the first 32 requests, for find_request.
-__device__ __forceinline__ Shares shares_of(const Args& a, int rows, int grid, bool tell, LaneUnits& first) {
+__device__ __forceinline__ Shares shares_of(const Args& a, int rows, int tokens, int grid, bool tell, LaneUnits& first) {
   Shares s{0, 0, 0, 0, 0};
   for (int b0 = 0; b0 < a.L.num_reqs; b0 += 32) {
-    const LaneUnits u = lane_units(a, rows, b0, tell);
+    const LaneUnits u = lane_units(a, rows, tokens, b0, tell);
     if (b0 == 0) first = u;
     s.units += __shfl_sync(0xffffffffu, u.end, 31);
     int64_t n = u.items;
@@ -129,9 +131,9 @@ __device__ __forceinline__ Shares shares_of(const Args& a, int rows, int grid, b
     for (int m = 16; m > 0; m /= 2) n += __shfl_xor_sync(0xffffffffu, n, m);
     s.items += n;
   }
-  // Short contexts stay whole: with up to kWholeTiles tiles in the average item, a CTA takes at least one item, and no
-  // parts are left to join.  Else at least a tile for each warp.
-  const int64_t fit = s.units <= kWholeTiles * s.items ? s.items : max(s.items, quotient(s.units, kMinTiles));
+  // Short contexts stay whole: with up to kWholeUnits units in the average item, a CTA takes at least one item, and few
+  // parts are left to join.  Else at least a unit for each warp.
+  const int64_t fit = s.units <= kWholeUnits * s.items ? s.items : max(s.items, quotient(s.units, kMinUnits));
   s.ctas = static_cast<int>(max(static_cast<int64_t>(1), min(static_cast<int64_t>(grid), fit)));
   s.each = quotient(s.units, s.ctas);
   s.more = s.units - s.each * s.ctas;
@@ -139,10 +141,10 @@ __device__ __forceinline__ Shares shares_of(const Args& a, int rows, int grid, b
 }
 
 // Request that holds unit `at`, and the unit at which it begins (whole warp; `at` is below the batch's units).
-__device__ __forceinline__ int find_request(const Args& a, int rows, int64_t at, const LaneUnits& first, int64_t& begin) {
+__device__ __forceinline__ int find_request(const Args& a, int rows, int tokens, int64_t at, const LaneUnits& first, int64_t& begin) {
   int64_t base = 0;
   for (int b0 = 0; b0 < a.L.num_reqs; b0 += 32) {
-    const LaneUnits u = b0 == 0 ? first : lane_units(a, rows, b0, false);
+    const LaneUnits u = b0 == 0 ? first : lane_units(a, rows, tokens, b0, false);
     const unsigned past = __ballot_sync(0xffffffffu, base + u.end > at);
     if (past) {
       const int lane = __ffs(past) - 1;
@@ -170,8 +172,11 @@ __device__ __forceinline__ void mma_bf16_first(float (&d)[4], uint32_t a0, uint3
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+// `bytes` neighbouring bytes into shared memory (both ends 16-byte aligned), counted by a barrier of this CTA.
+__device__ __forceinline__ void copy_bulk(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(cosa::smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(cosa::smem_u32(bar))
+               : "memory");
 }
 
 // Nibbles P of both halves of a word as bf16 pairs; `swapped` is the word with the bytes of each half exchanged,
@@ -190,29 +195,15 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   return y;
 }
 
-// Two fp32 operations in one instruction.
-__device__ __forceinline__ void fma2(float& d0, float& d1, float a0, float a1, float b0, float b1) {      // d += a * b
-  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 d, {%0, %1};\n\t"
-      "fma.rn.f32x2 d, a, b, d;\n\tmov.b64 {%0, %1}, d;\n\t}"
-      : "+f"(d0), "+f"(d1)
-      : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
-}
-__device__ __forceinline__ void mul2(float& d0, float& d1, float a0, float a1, float b0, float b1) {
-  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
-      "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
-      : "=f"(d0), "=f"(d1)
-      : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
-}
-
 constexpr float kUp = 79228162514264337593543950336.0f;      // 2^96
 constexpr float kDown = 8589934592.0f;                       // 2^33
 
-// A warp takes TP tiles at a time: with eight rows two, whose chains of dependent instructions fill each other's gaps (one
-// tile alone has too few independent ones); with sixteen rows one, for the registers.
+// A unit is TP tiles: with eight rows two, whose chains of dependent instructions fill each other's gaps (one tile alone
+// has too few independent ones); with sixteen rows one, for the registers.
 template <int NT>
 struct Steps {
   static constexpr int TP = NT == 1 ? 2 : 1;
-  static constexpr int kStages = NT == 1 ? 2 : 4;      // steps in flight per warp
+  static constexpr int kStages = NT == 1 ? 2 : 4;      // units in flight per warp
   static constexpr int kCtas = NT == 1 ? 3 : 2;        // CTAs of an SM: 168 or 255 registers a thread
 };
 
@@ -222,6 +213,7 @@ struct AttnSmem {
   alignas(16) uint8_t ring[kWarps][Steps<NT>::kStages][Steps<NT>::TP * Tile<D>::kBytes];
   alignas(16) float o[kWarps][kRows][D];
   float ml[kWarps][kRows][2];
+  alignas(8) uint64_t full[kWarps][Steps<NT>::kStages];
 };
 
 // A warp's accumulators: lane = 4 i + c has query rows 2c and 2c + 1 of each eight; of the logits the tokens i and i + 8,
@@ -231,7 +223,7 @@ __global__ void __launch_bounds__(kThreads, Steps<NT>::kCtas) attention_kernel(c
   using T = Tile<D>;
   constexpr int G = T::G;
   constexpr int kRows = 8 * NT;
-  constexpr int TP = Steps<NT>::TP, kStages = Steps<NT>::kStages, kStep = TP * kWarps;
+  constexpr int TP = Steps<NT>::TP, kStages = Steps<NT>::kStages, kUnit = TP * kTile;
   extern __shared__ __align__(16) uint8_t smem_raw[];
   AttnSmem<D, NT>& sm = *reinterpret_cast<AttnSmem<D, NT>*>(smem_raw);
   const AttnLaunch& L = a.L;
@@ -240,72 +232,96 @@ __global__ void __launch_bounds__(kThreads, Steps<NT>::kCtas) attention_kernel(c
   wait_for_stream();
   let_next_start();
   LaneUnits first;
-  const Shares sh = shares_of(a, kRows, static_cast<int>(gridDim.x), blockIdx.x == 0 && warp == 0, first);
+  const Shares sh = shares_of(a, kRows, kUnit, static_cast<int>(gridDim.x), blockIdx.x == 0 && warp == 0, first);
   const int me = static_cast<int>(blockIdx.x);
   Owner own{0, 0, 0, 0, 0};
+  if (lane == 0) {
+#pragma unroll
+    for (int k = 0; k < kStages; ++k) cosa::mbar_init(&sm.full[warp][k], 1);
+    cosa::fence_mbarrier_init();
+    cosa::fence_proxy_async_smem();
+  }
+  __syncwarp();
+  uint32_t phase = 0;               // bit k: parity of the next completion of stage k's barrier
+  bool alive = true;                // no wait of this warp has run out
   if (me >= sh.ctas || sh.units == 0) {
     if (tid == 0) a.owner[me] = own;
     return;
   }
   const int64_t hi = sh.begin(me + 1);
   int64_t at = sh.begin(me), req_begin;
-  int b = find_request(a, kRows, at, first, req_begin);
+  int b = find_request(a, kRows, kUnit, at, first, req_begin);
 
   while (at < hi) {
-    const Request r = request_of(a, b, kRows, false);
-    const int64_t req_units = r.tiles * r.rts * L.num_kv_heads;
+    const Request r = request_of(a, b, kRows, kUnit, false);
+    const int64_t req_units = r.units * r.rts * L.num_kv_heads;
     if (at >= req_begin + req_units) {     // the next request that has units
       req_begin += req_units;
       ++b;
       continue;
     }
-    const int64_t item = quotient(at - req_begin, r.tiles);   // (kv head, row tile)
+    const int64_t item = quotient(at - req_begin, r.units);   // (kv head, row tile)
     const int h = static_cast<int>(quotient(item, r.rts)), rt = static_cast<int>(item - h * r.rts);
-    const int64_t item_begin = req_begin + item * r.tiles, item_end = item_begin + r.tiles;
+    const int64_t item_begin = req_begin + item * r.units, item_end = item_begin + r.units;
     const int t_begin = static_cast<int>(at - item_begin);
     const int t_end = static_cast<int>(min(hi, item_end) - item_begin);
     const int nrows = static_cast<int>(min(static_cast<int64_t>(kRows), static_cast<int64_t>(r.n) * a.group - static_cast<int64_t>(rt) * kRows));
 
-    // ---- the warp's steps of TP tiles: from t_begin + TP * warp, kStep on ----
+    // ---- the warp's units: t_begin + warp, + kWarps, ... ----
     const int32_t* table = L.page_table + static_cast<size_t>(b) * L.max_pages_per_req;
     uint32_t there = 0;               // bit stage * TP + u: the page of the stage's tile u exists
-    auto page_at = [&](int t) -> int {
-      if (t >= t_end || t * kTile >= r.len) return -1;
-      const int phys = table[(t * kTile) >> a.page_shift];
-      return phys < L.num_kv4_pages ? phys : -1;
-    };
-    const uint8_t* head = L.cache + (static_cast<size_t>(h) << (a.page_shift - 4)) * T::kBytes + lane * 16;
-    const size_t page_bytes = (static_cast<size_t>(L.num_kv_heads) << (a.page_shift - 4)) * T::kBytes;
-    const int tile_mask = (1 << (a.page_shift - 4)) - 1;
-    int phys[TP];                     // pages of the step that is asked for next
+    int phys[TP];                     // pages of the unit that is asked for next (one, where a page holds a unit)
+    const bool one_page = TP == 1 || a.page_shift >= 5;
     auto look_up = [&](int t) {
 #pragma unroll
-      for (int u = 0; u < TP; ++u) phys[u] = page_at(t + u);
+      for (int u = 0; u < TP; ++u) {
+        if (u > 0 && one_page) {
+          phys[u] = phys[0];
+          continue;
+        }
+        const int slot = t * kUnit + u * kTile;
+        phys[u] = -1;
+        if (t < t_end && slot < r.len) {
+          const int page = table[slot >> a.page_shift];
+          if (page < L.num_kv4_pages) phys[u] = page;
+        }
+      }
     };
+    const uint8_t* head = L.cache + (static_cast<size_t>(h) << (a.page_shift - 4)) * T::kBytes;
+    const size_t page_bytes = (static_cast<size_t>(L.num_kv_heads) << (a.page_shift - 4)) * T::kBytes;
+    const int tile_mask = (1 << (a.page_shift - 4)) - 1;
+    // one copy per page that the unit lies on, all counted by the stage's barrier
     auto issue = [&](int t, int stage) {
+      if (t >= t_end || !alive) return;
 #pragma unroll
       for (int u = 0; u < TP; ++u) {
         const uint32_t bit = 1u << (stage * TP + u);
-        if (phys[u] >= 0) {
-          const uint8_t* src = head + phys[u] * page_bytes + ((t + u) & tile_mask) * T::kBytes;
-          const uint32_t dst = cosa::smem_u32(sm.ring[warp][stage]) + u * T::kBytes + lane * 16;
-#pragma unroll
-          for (int k = 0; k < (T::kBytes + 511) / 512; ++k)
-            if (k < T::kBytes / 512 || lane * 16 < T::kBytes % 512) copy16(dst + k * 512, src + k * 512);
-          there |= bit;
+        there = phys[u] >= 0 ? there | bit : there & ~bit;
+      }
+      if (lane == 0 && !a.stall) {
+        uint64_t* bar = &sm.full[warp][stage];
+        uint8_t* dst = sm.ring[warp][stage];
+        if (one_page) {
+          cosa::mbar_arrive_expect_tx(bar, phys[0] >= 0 ? TP * T::kBytes : 0);
+          if (phys[0] >= 0) copy_bulk(dst, head + phys[0] * page_bytes + (t * TP & tile_mask) * T::kBytes, TP * T::kBytes, bar);
         } else {
-          there &= ~bit;
+          int bytes = 0;
+#pragma unroll
+          for (int u = 0; u < TP; ++u) bytes += phys[u] >= 0 ? T::kBytes : 0;
+          cosa::mbar_arrive_expect_tx(bar, bytes);
+#pragma unroll
+          for (int u = 0; u < TP; ++u)
+            if (phys[u] >= 0) copy_bulk(dst + u * T::kBytes, head + phys[u] * page_bytes, T::kBytes, bar);
         }
       }
-      asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    const int t_first = t_begin + TP * warp;
+    const int t_first = t_begin + warp;
 #pragma unroll
     for (int s = 0; s < kStages; ++s) {
-      look_up(t_first + s * kStep);
-      issue(t_first + s * kStep, s);
+      look_up(t_first + s * kWarps);
+      issue(t_first + s * kWarps, s);
     }
-    look_up(t_first + kStages * kStep);
+    look_up(t_first + kStages * kWarps);
 
     // ---- this lane's row of q: B operands ----
     uint32_t qb[NT][2 * G][2];        // row 8 x + i: [eight rows][product][k half]
@@ -352,13 +368,19 @@ __global__ void __launch_bounds__(kThreads, Steps<NT>::kCtas) attention_kernel(c
     }
 
     int stage = 0;
-    for (int t = t_first; t < t_end; t += kStep) {
-      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
-      __syncwarp();
+    for (int t = t_first; alive && t < t_end; t += kWarps) {
+      if (!cosa::wait_parity_bounded(&sm.full[warp][stage], (phase >> stage) & 1u, nullptr, L.status)) {
+        // give the copies in flight time to land before the CTA's memory is anyone else's; what follows is undefined
+        for (int k = 0; k < kStages; ++k) cosa::wait_parity_bounded(&sm.full[warp][k], (phase >> k) & 1u, nullptr, L.status);
+        alive = false;
+      }
+      alive = __all_sync(0xffffffffu, alive);
+      if (!alive) break;
+      phase ^= 1u << stage;
       const uint8_t* tiles = sm.ring[warp][stage];
       const uint32_t exists = there >> (stage * TP);           // bit u
-      // every row sees every token of the step
-      const bool clear = (exists & ((1u << TP) - 1u)) == (1u << TP) - 1u && (t + TP) * kTile <= all_see;
+      // every row sees every token of the unit
+      const bool clear = (exists & ((1u << TP) - 1u)) == (1u << TP) - 1u && (t + 1) * kUnit <= all_see;
 
       // K q^T: logits of 16 TP tokens
       float s[TP][NT][4];             // [tile][eight rows][token i: rows 2c, 2c + 1; token i + 8: rows 2c, 2c + 1]
@@ -380,10 +402,6 @@ __global__ void __launch_bounds__(kThreads, Steps<NT>::kCtas) attention_kernel(c
           }
         }
 #pragma unroll
-        for (int x = 0; x < NT; ++x)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) s[u][x][k] = 0.f;
-#pragma unroll
         for (int g = 0; g < G; ++g) {
           const uint32_t w0 = kw[0][g], z0 = swap_bytes(w0), w1 = kw[1][g], z1 = swap_bytes(w1);
           const uint32_t a0 = codes<0>(w0, z0), a1 = codes<0>(w1, z1), a2 = codes<1>(w0, z0), a3 = codes<1>(w1, z1);
@@ -395,8 +413,11 @@ __global__ void __launch_bounds__(kThreads, Steps<NT>::kCtas) attention_kernel(c
             float acc[4];
             mma_bf16_first(acc, a0, a1, a2, a3, qb[x][2 * g][0], qb[x][2 * g][1]);
             mma_bf16(acc, e0, e1, e2, e3, qb[x][2 * g + 1][0], qb[x][2 * g + 1][1]);
-            fma2(s[u][x][0], s[u][x][1], acc[0], acc[1], s0, s0);
-            fma2(s[u][x][2], s[u][x][3], acc[2], acc[3], s1, s1);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float sk = k < 2 ? s0 : s1;
+              s[u][x][k] = g == 0 ? acc[k] * sk : fmaf(acc[k], sk, s[u][x][k]);
+            }
           }
         }
       }
@@ -410,7 +431,7 @@ __global__ void __launch_bounds__(kThreads, Steps<NT>::kCtas) attention_kernel(c
           for (int x = 0; x < NT; ++x)
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              if (((exists >> u) & 1u) && (t + u) * kTile + i + 8 * (k / 2) < limit[x][k % 2])
+              if (((exists >> u) & 1u) && t * kUnit + u * kTile + i + 8 * (k / 2) < limit[x][k % 2])
                 seen |= 1u << (4 * (NT * u + x) + k);
               else
                 s[u][x][k] = -INFINITY;
@@ -423,13 +444,12 @@ __global__ void __launch_bounds__(kThreads, Steps<NT>::kCtas) attention_kernel(c
           for (int e = 0; e < 2; ++e)
             if (8 * x + 2 * c + e < nrows) {
               const int64_t row = (static_cast<int64_t>(h) * L.total_tokens + r.tok0) * a.group + rt * kRows + 8 * x + 2 * c + e;
-              float* dst = a.logits + row * a.pitch + t * kTile + i;
+              float* dst = a.logits + row * a.pitch + t * kUnit + i;
 #pragma unroll
-              for (int u = 0; u < TP; ++u)
-                if (u == 0 || t + u < t_end) {       // the next tile may be another CTA's
-                  dst[16 * u] = s[u][x][e];
-                  dst[16 * u + 8] = s[u][x][2 + e];
-                }
+              for (int u = 0; u < TP; ++u) {
+                dst[16 * u] = s[u][x][e];
+                dst[16 * u + 8] = s[u][x][2 + e];
+              }
             }
       }
 
@@ -514,8 +534,7 @@ __global__ void __launch_bounds__(kThreads, Steps<NT>::kCtas) attention_kernel(c
               const float sj = g % 2 ? bf16_hi(sc[j][g / 2]) : bf16_lo(sc[j][g / 2]);
 #pragma unroll
               for (int x = 0; x < NT; ++x) {
-                float y0, y1;
-                mul2(y0, y1, p[u][x][2 * j], p[u][x][2 * j + 1], sj, sj);
+                float y0 = p[u][x][2 * j] * sj, y1 = p[u][x][2 * j + 1] * sj;
                 if constexpr (!decltype(all)::value) {      // an unseen token adds nothing, whatever its scale is
                   if (!((seen >> (4 * (NT * u + x) + 2 * j)) & 1u)) y0 = 0.f;
                   if (!((seen >> (4 * (NT * u + x) + 2 * j + 1)) & 1u)) y1 = 0.f;
@@ -541,11 +560,10 @@ __global__ void __launch_bounds__(kThreads, Steps<NT>::kCtas) attention_kernel(c
         product(std::false_type{});
 
       __syncwarp();                   // every lane has read the stage
-      issue(t + kStages * kStep, stage);
-      look_up(t + (kStages + 1) * kStep);
+      issue(t + kStages * kWarps, stage);
+      look_up(t + (kStages + 1) * kWarps);
       stage = stage + 1 == kStages ? 0 : stage + 1;
     }
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
 
     // ---- join the warps ----
 #pragma unroll
@@ -569,7 +587,7 @@ __global__ void __launch_bounds__(kThreads, Steps<NT>::kCtas) attention_kernel(c
       }
     }
     __syncthreads();
-    const bool whole = t_begin == 0 && t_end == r.tiles;
+    const bool whole = t_begin == 0 && t_end == r.units;
     const int slot_of_part = t_begin == 0 ? 1 : 0;
     for (int k = tid; k < nrows * (D / 4); k += kThreads) {
       const int row = k / (D / 4), d0 = 4 * (k % (D / 4));
@@ -744,11 +762,11 @@ __global__ void __launch_bounds__(kJoinThreads) combine_kernel(const Args a, con
 
 // weights[b, h, s] += sum over the rows of exp2(scale * logit - M) / sum, rows in order; four slots per thread.
 constexpr int kWeightRows = 32;       // rows whose maxima and sums a CTA holds at a time
-__global__ void __launch_bounds__(256) weights_kernel(const Args a, const int rows_per_tile) {
+__global__ void __launch_bounds__(256) weights_kernel(const Args a) {
   __shared__ float2 s_stat[kWeightRows];
   wait_for_stream();
   const int b = blockIdx.z, h = blockIdx.y;
-  const Request r = request_of(a, b, rows_per_tile, false);
+  const Request r = request_of(a, b, 8, kTile, false);
   const int slot = (static_cast<int>(blockIdx.x) * 256 + threadIdx.x) * 4;
   if (static_cast<int>(blockIdx.x) * 1024 >= r.len || r.n == 0) return;
   const bool in = slot < r.len;
@@ -781,6 +799,9 @@ __global__ void __launch_bounds__(256) weights_kernel(const Args a, const int ro
     if (slot + k < r.len) dst[k] += w[k];
 }
 
+// Row pitch of the logits: whole units, of which the last is written to its end.
+int64_t logits_pitch(int max_seqlen) { return (static_cast<int64_t>(max_seqlen) + 31) / 32 * 32; }
+
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
 template <int D, int NT, bool WEIGHTS>
@@ -803,7 +824,7 @@ cudaError_t launch(const Args& a, cudaStream_t stream) {
   if (e != cudaSuccess || !WEIGHTS) return e;
   const dim3 grid(static_cast<unsigned>((a.L.max_seqlen + 1023LL) / 1024), static_cast<unsigned>(a.L.num_kv_heads),
                   static_cast<unsigned>(a.L.num_reqs));
-  return launch_after(weights_kernel, grid, 256, 0, stream, 1, a, 8 * NT);
+  return launch_after(weights_kernel, grid, 256, 0, stream, 1, a);
 }
 
 }  // namespace
@@ -813,8 +834,7 @@ size_t attn_workspace_bytes(int num_q_heads, int head_dim, int total_tokens, int
              align256(size_t(kMaxCtas) * 2 * 16 * head_dim * 4);
   if (with_weights) {
     const size_t rows = static_cast<size_t>(total_tokens) * num_q_heads;
-    const size_t pitch = (static_cast<size_t>(max_seqlen) + kTile - 1) / kTile * kTile;
-    n += align256(rows * 8) + align256(rows * pitch * 4);
+    n += align256(rows * 8) + align256(rows * logits_pitch(max_seqlen) * 4);
   }
   return n;
 }
@@ -825,7 +845,8 @@ cudaError_t launch_attention(const AttnLaunch& L, cudaStream_t stream) {
   a.L.scale_log2 = L.scale_log2 * kDown;      // of the logits as the first product leaves them
   a.group = L.num_q_heads / L.num_kv_heads;
   for (a.page_shift = 4; (1 << a.page_shift) < L.page_size;) ++a.page_shift;
-  a.pitch = (static_cast<int64_t>(L.max_seqlen) + kTile - 1) / kTile * kTile;
+  a.pitch = logits_pitch(L.max_seqlen);
+  a.stall = L.stall;
   uint8_t* w = static_cast<uint8_t*>(L.workspace);
   a.owner = reinterpret_cast<Owner*>(w);
   w += align256(kMaxCtas * sizeof(Owner));

@@ -70,6 +70,7 @@ struct AttnLaunch {
   int num_reqs, num_q_heads, num_kv_heads, head_dim, page_size, total_tokens, max_seqlen, num_kv4_pages, max_pages_per_req;
   int max_new_tokens;
   float scale_log2;      // sm_scale * log2(e)
+  bool stall;            // COSA_KV_FLAG_TEST_STALL
 };
 size_t attn_workspace_bytes(int num_q_heads, int head_dim, int total_tokens, int max_seqlen, bool with_weights);
 cudaError_t launch_attention(const AttnLaunch& L, cudaStream_t stream);

@@ -47,6 +47,7 @@ KV_LIB_PATH = os.path.join(_HERE, "libcosa_kv.so")
 KV_EXPORTS = ("cosa_kv_version", "cosa_qk_norm_rope", "cosa_kv4_store", "cosa_kv4_load",
               "cosa_kv4_attention_workspace_size", "cosa_kv4_attention", "cosa_kv4_evict")
 COSA_KV_FLAG_INTERLEAVED = 1
+COSA_KV_FLAG_TEST_STALL = 4   # test hook of cosa_kv4_attention: every in-kernel wait runs out
 KV4_GROUP = 32   # values of a head that share a scale
 KV4_TILE = 16    # tokens of a storage tile
 

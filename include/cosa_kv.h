@@ -22,7 +22,8 @@
  *   - Return value: COSA_OK, or a negative status for an error found on the host before anything is
  *     enqueued, or COSA_ERR_CUDA for a failed launch.  Lengths that contradict `p` are found on the
  *     device: *device_status (an int32 the caller zeroes; may be NULL) becomes COSA_ERR_BAD_INPUT and
- *     the request concerned is treated as empty.
+ *     the request concerned is treated as empty.  A bounded wait inside the attention kernel that runs out gives
+ *     COSA_ERR_DEVICE_TIMEOUT; the outputs are then undefined.
  *   - Requests are packed by cu_seqlens int32 [num_reqs + 1] (cu_seqlens[0] = 0, non-decreasing, last
  *     entry <= total_tokens); rows behind the last request are neither read nor written.
  *   - A cache slot is a token's place in its request: slot s of request b is row s % P of logical page
@@ -67,6 +68,9 @@ extern "C" {
 
 /* cosa_kv_params.flags */
 #define COSA_KV_FLAG_INTERLEAVED 1 /* rotation pairs are (2i, 2i+1); default (i, i + rotary_dim/2) */
+/* Test hook for the bounded waits of cosa_kv4_attention: no copy of the cache is issued, so every wait in the kernel runs
+   out after its 2 s budget, the kernel ends, *device_status becomes COSA_ERR_DEVICE_TIMEOUT and out is undefined. */
+#define COSA_KV_FLAG_TEST_STALL 4
 
 typedef struct cosa_kv_params {
   int32_t num_reqs;          /* B >= 1                                                          */

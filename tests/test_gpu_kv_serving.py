@@ -330,6 +330,25 @@ def test_shared_prefix_pages_are_read_by_both():
     assert torch.equal(out[0], out[1])
 
 
+def test_waits_that_run_out_end_the_kernel():
+    """With no copy issued, every wait of the attention runs out: the call ends by itself and reports it, and the next call is
+    as good as ever."""
+    s, _ = calls(15)
+    q1 = bf(s.rng, 2, s.Hq, s.d)
+    args = (q1, cu_of([1, 1]), s.cache, i32(s.pt4), i32(s.lens))
+    want = C.cosa_kv4_attention(s.p1, *args)
+    torch.cuda.synchronize()
+    p = C.CosaKvParams.from_buffer_copy(s.p1)
+    p.flags |= C.COSA_KV_FLAG_TEST_STALL
+    st = new_status()
+    C.cosa_kv4_attention(p, *args, status=st)
+    torch.cuda.synchronize()
+    assert int(st.item()) == cosa.COSA_ERR_DEVICE_TIMEOUT
+    st = new_status()
+    assert torch.equal(C.cosa_kv4_attention(s.p1, *args, status=st), want)
+    ok(st)
+
+
 def test_binding_refusals_on_the_device():
     s, _ = calls(14)
     ok_args = dict(cu=cu_of([1, 1]), pt=i32(s.pt4), lens=i32(s.lens))
