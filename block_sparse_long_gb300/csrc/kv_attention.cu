@@ -10,8 +10,8 @@
 //           first product's layout (tokens down) to the second's (tokens across) by movmatrix.
 // A code of magnitude m becomes the subnormal bf16 number +-m 2^-129 (three bits of significand and the sign
 // bit where the layout has them), two codes by a shift and an AND; matrix instructions take subnormal
-// operands exactly.  The other operands carry 2^96 to keep the products normal: q is multiplied by it, and
-// the exponent of p is raised by 96.  What is left, 2^-33, goes into the softmax scale and the last division.
+// operands exactly.  The other operands, q and p * s, carry 2^96 to keep the products normal; what is
+// left, 2^-33, goes into the softmax scale and the last division.
 //
 // What bounds it: 9 d / 8 bytes of cache per token and kv head (144 at d = 128, K and V) against HBM; close
 // behind, the issue slots that unpack the codes.  So a warp works alone on tiles of 16 tokens out of its own
@@ -173,10 +173,18 @@ __device__ __forceinline__ void mma_bf16_first(float (&d)[4], uint32_t a0, uint3
 }
 
 // `bytes` neighbouring bytes into shared memory (both ends 16-byte aligned), counted by a barrier of this CTA.
-__device__ __forceinline__ void copy_bulk(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(cosa::smem_u32(dst)),
-               "l"(src), "r"(bytes), "r"(cosa::smem_u32(bar))
+__device__ __forceinline__ void copy_bulk(void* dst, const void* src, uint32_t bytes, uint64_t* bar, uint64_t policy) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(
+                   cosa::smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(cosa::smem_u32(bar)), "l"(policy)
                : "memory");
+}
+
+// Cache policy for bytes that a call reads once: they make room in L2 first (the logits, which are read again, stay).
+__device__ __forceinline__ uint64_t read_once() {
+  uint64_t policy;
+  asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
+  return policy;
 }
 
 // Nibbles P of both halves of a word as bf16 pairs; `swapped` is the word with the bytes of each half exchanged,
@@ -198,8 +206,9 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
 constexpr float kUp = 79228162514264337593543950336.0f;      // 2^96
 constexpr float kDown = 8589934592.0f;                       // 2^33
 
-// A unit is TP tiles: with eight rows two, whose chains of dependent instructions fill each other's gaps (one tile alone
-// has too few independent ones); with sixteen rows one, for the registers.
+// A unit is TP tiles that a warp takes at a time: with eight rows two, whose chains of dependent instructions fill each
+// other's gaps; with sixteen rows one, for the registers.  (One 128K context with TP = 1, 2, 4: 49, 39 and 38 us; 48 ragged
+// ones with weights: 149, 130 and 134 us; a context of 777 tokens: 12, 11.5 and 14.5 us.)
 template <int NT>
 struct Steps {
   static constexpr int TP = NT == 1 ? 2 : 1;
@@ -207,11 +216,15 @@ struct Steps {
   static constexpr int kCtas = NT == 1 ? 3 : 2;        // CTAs of an SM: 168 or 255 registers a thread
 };
 
+// A warp's part of the output before the join lies where its units were.
 template <int D, int NT>
 struct AttnSmem {
-  static constexpr int kRows = 8 * NT;
-  alignas(16) uint8_t ring[kWarps][Steps<NT>::kStages][Steps<NT>::TP * Tile<D>::kBytes];
-  alignas(16) float o[kWarps][kRows][D];
+  static constexpr int kRows = 8 * NT, TP = Steps<NT>::TP;
+  union Ring {
+    uint8_t unit[Steps<NT>::kStages][TP * Tile<D>::kBytes];
+    float o[kRows][D];
+  };
+  alignas(16) Ring ring[kWarps];
   float ml[kWarps][kRows][2];
   alignas(8) uint64_t full[kWarps][Steps<NT>::kStages];
 };
@@ -225,7 +238,7 @@ __global__ void __launch_bounds__(kThreads, Steps<NT>::kCtas) attention_kernel(c
   constexpr int kRows = 8 * NT;
   constexpr int TP = Steps<NT>::TP, kStages = Steps<NT>::kStages, kUnit = TP * kTile;
   extern __shared__ __align__(16) uint8_t smem_raw[];
-  AttnSmem<D, NT>& sm = *reinterpret_cast<AttnSmem<D, NT>*>(smem_raw);
+  auto& sm = *reinterpret_cast<AttnSmem<D, NT>*>(smem_raw);
   const AttnLaunch& L = a.L;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, i = lane / 4, c = lane % 4;
 
@@ -244,6 +257,7 @@ __global__ void __launch_bounds__(kThreads, Steps<NT>::kCtas) attention_kernel(c
   __syncwarp();
   uint32_t phase = 0;               // bit k: parity of the next completion of stage k's barrier
   bool alive = true;                // no wait of this warp has run out
+  const uint64_t once = read_once();
   if (me >= sh.ctas || sh.units == 0) {
     if (tid == 0) a.owner[me] = own;
     return;
@@ -270,13 +284,15 @@ __global__ void __launch_bounds__(kThreads, Steps<NT>::kCtas) attention_kernel(c
     // ---- the warp's units: t_begin + warp, + kWarps, ... ----
     const int32_t* table = L.page_table + static_cast<size_t>(b) * L.max_pages_per_req;
     uint32_t there = 0;               // bit stage * TP + u: the page of the stage's tile u exists
-    int phys[TP];                     // pages of the unit that is asked for next (one, where a page holds a unit)
-    const bool one_page = TP == 1 || a.page_shift >= 5;
+    const bool copies = lane == 0 && !a.stall;
+    int phys[TP];                     // pages of the tiles of the unit that is asked for next
+    const bool one_page = kUnit <= (1 << a.page_shift);
+    const int page_tiles = 1 << (a.page_shift - 4);
     auto look_up = [&](int t) {
 #pragma unroll
       for (int u = 0; u < TP; ++u) {
-        if (u > 0 && one_page) {
-          phys[u] = phys[0];
+        if (u > 0 && (one_page || (u & (page_tiles - 1)))) {
+          phys[u] = phys[u - 1];
           continue;
         }
         const int slot = t * kUnit + u * kTile;
@@ -288,8 +304,7 @@ __global__ void __launch_bounds__(kThreads, Steps<NT>::kCtas) attention_kernel(c
       }
     };
     const uint8_t* head = L.cache + (static_cast<size_t>(h) << (a.page_shift - 4)) * T::kBytes;
-    const size_t page_bytes = (static_cast<size_t>(L.num_kv_heads) << (a.page_shift - 4)) * T::kBytes;
-    const int tile_mask = (1 << (a.page_shift - 4)) - 1;
+    const uint32_t page_bytes = (static_cast<uint32_t>(L.num_kv_heads) << (a.page_shift - 4)) * T::kBytes;   // below 2^31
     // one copy per page that the unit lies on, all counted by the stage's barrier
     auto issue = [&](int t, int stage) {
       if (t >= t_end || !alive) return;
@@ -298,20 +313,22 @@ __global__ void __launch_bounds__(kThreads, Steps<NT>::kCtas) attention_kernel(c
         const uint32_t bit = 1u << (stage * TP + u);
         there = phys[u] >= 0 ? there | bit : there & ~bit;
       }
-      if (lane == 0 && !a.stall) {
+      if (copies) {
         uint64_t* bar = &sm.full[warp][stage];
-        uint8_t* dst = sm.ring[warp][stage];
+        uint8_t* dst = sm.ring[warp].unit[stage];
         if (one_page) {
           cosa::mbar_arrive_expect_tx(bar, phys[0] >= 0 ? TP * T::kBytes : 0);
-          if (phys[0] >= 0) copy_bulk(dst, head + phys[0] * page_bytes + (t * TP & tile_mask) * T::kBytes, TP * T::kBytes, bar);
+          if (phys[0] >= 0)
+            copy_bulk(dst, head + static_cast<uint64_t>(static_cast<uint32_t>(phys[0])) * page_bytes + (t * TP & (page_tiles - 1)) * T::kBytes, TP * T::kBytes, bar, once);
         } else {
-          int bytes = 0;
+          int tiles = 0;
 #pragma unroll
-          for (int u = 0; u < TP; ++u) bytes += phys[u] >= 0 ? T::kBytes : 0;
-          cosa::mbar_arrive_expect_tx(bar, bytes);
+          for (int u = 0; u < TP; ++u) tiles += phys[u] >= 0;
+          cosa::mbar_arrive_expect_tx(bar, tiles * T::kBytes);
 #pragma unroll
           for (int u = 0; u < TP; ++u)
-            if (phys[u] >= 0) copy_bulk(dst + u * T::kBytes, head + phys[u] * page_bytes, T::kBytes, bar);
+            if (phys[u] >= 0 && (u & (page_tiles - 1)) == 0)
+              copy_bulk(dst + u * T::kBytes, head + static_cast<uint64_t>(static_cast<uint32_t>(phys[u])) * page_bytes, page_tiles * T::kBytes, bar, once);
         }
       }
     };
@@ -355,11 +372,14 @@ __global__ void __launch_bounds__(kThreads, Steps<NT>::kCtas) attention_kernel(c
 #pragma unroll
     for (int m = 4; m < 32; m *= 2) all_see = min(all_see, __shfl_xor_sync(0xffffffffu, all_see, m));
 
+    const int clear_units = all_see / kUnit;
     float o[NT][2 * G][4];            // [eight rows][m tile]
-    float m2[NT][2], l[NT][2];        // rows 8 x + 2c and + 1: running maximum (scaled, base 2), this lane's part of the sum
+    // rows 8 x + 2c and + 1: running maximum (unscaled), minus the scaled one (0 for none), this lane's part of the sum
+    float top[NT][2], off[NT][2], l[NT][2];
 #pragma unroll
     for (int x = 0; x < NT; ++x) {
-      m2[x][0] = m2[x][1] = -INFINITY;
+      top[x][0] = top[x][1] = -INFINITY;
+      off[x][0] = off[x][1] = 0.f;
       l[x][0] = l[x][1] = 0.f;
 #pragma unroll
       for (int mt = 0; mt < 2 * G; ++mt)
@@ -377,10 +397,10 @@ __global__ void __launch_bounds__(kThreads, Steps<NT>::kCtas) attention_kernel(c
       alive = __all_sync(0xffffffffu, alive);
       if (!alive) break;
       phase ^= 1u << stage;
-      const uint8_t* tiles = sm.ring[warp][stage];
+      const uint8_t* tiles = sm.ring[warp].unit[stage];
       const uint32_t exists = there >> (stage * TP);           // bit u
       // every row sees every token of the unit
-      const bool clear = (exists & ((1u << TP) - 1u)) == (1u << TP) - 1u && (t + 1) * kUnit <= all_see;
+      const bool clear = (exists & ((1u << TP) - 1u)) == (1u << TP) - 1u && t < clear_units;
 
       // K q^T: logits of 16 TP tokens
       float s[TP][NT][4];             // [tile][eight rows][token i: rows 2c, 2c + 1; token i + 8: rows 2c, 2c + 1]
@@ -455,17 +475,16 @@ __global__ void __launch_bounds__(kThreads, Steps<NT>::kCtas) attention_kernel(c
 
       // Running maximum.  The lanes of a row agree on it, so whether any of them has a larger logit is one vote; only
       // then is the maximum found and are the sums so far rescaled.
-      float top[NT][2];
+      float mx[NT][2];
       bool grows = false;
 #pragma unroll
       for (int x = 0; x < NT; ++x)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float mx = fmaxf(s[0][x][e], s[0][x][2 + e]);
+          mx[x][e] = fmaxf(s[0][x][e], s[0][x][2 + e]);
 #pragma unroll
-          for (int u = 1; u < TP; ++u) mx = fmaxf(mx, fmaxf(s[u][x][e], s[u][x][2 + e]));
-          top[x][e] = mx * L.scale_log2;
-          grows |= top[x][e] > m2[x][e];
+          for (int u = 1; u < TP; ++u) mx[x][e] = fmaxf(mx[x][e], fmaxf(s[u][x][e], s[u][x][2 + e]));
+          grows |= mx[x][e] > top[x][e];
         }
       if (__any_sync(0xffffffffu, grows)) {
 #pragma unroll
@@ -473,12 +492,14 @@ __global__ void __launch_bounds__(kThreads, Steps<NT>::kCtas) attention_kernel(c
           float f[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float mx = top[x][e];
+            float m = mx[x][e];
 #pragma unroll
-            for (int m = 4; m < 32; m *= 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, m));
-            const float m_new = fmaxf(m2[x][e], mx);
-            f[e] = m2[x][e] == -INFINITY ? 0.f : cosa::ex2_approx(m2[x][e] - m_new);
-            m2[x][e] = m_new;
+            for (int k = 4; k < 32; k *= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
+            m = fmaxf(top[x][e], m);
+            const float now = m == -INFINITY ? 0.f : -m * L.scale_log2;
+            f[e] = top[x][e] == -INFINITY ? 0.f : cosa::ex2_approx(now - off[x][e]);
+            top[x][e] = m;
+            off[x][e] = now;
             l[x][e] *= f[e];
           }
 #pragma unroll
@@ -489,16 +510,15 @@ __global__ void __launch_bounds__(kThreads, Steps<NT>::kCtas) attention_kernel(c
       }
       float p[TP][NT][4];
 #pragma unroll
-      for (int x = 0; x < NT; ++x) {
-        const float up[2] = {96.f - (m2[x][0] == -INFINITY ? 0.f : m2[x][0]), 96.f - (m2[x][1] == -INFINITY ? 0.f : m2[x][1])};
+      for (int x = 0; x < NT; ++x)
 #pragma unroll
         for (int u = 0; u < TP; ++u)
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            p[u][x][k] = cosa::ex2_approx(fmaf(s[u][x][k], L.scale_log2, up[k % 2]));
-            l[x][k % 2] += p[u][x][k];
+            const float e = cosa::ex2_approx(fmaf(s[u][x][k], L.scale_log2, off[x][k % 2]));
+            l[x][k % 2] += e;
+            p[u][x][k] = e * kUp;
           }
-      }
 
       // V^T p
       auto product = [&](auto all) {
@@ -573,16 +593,16 @@ __global__ void __launch_bounds__(kThreads, Steps<NT>::kCtas) attention_kernel(c
 #pragma unroll
         for (int m = 4; m < 32; m *= 2) l[x][e] += __shfl_xor_sync(0xffffffffu, l[x][e], m);
         if (i == 0) {
-          sm.ml[warp][8 * x + 2 * c + e][0] = m2[x][e];
+          sm.ml[warp][8 * x + 2 * c + e][0] = top[x][e] == -INFINITY ? -INFINITY : -off[x][e];
           sm.ml[warp][8 * x + 2 * c + e][1] = l[x][e];
         }
       }
 #pragma unroll
       for (int g = 0; g < G; ++g) {
         // m tile 2g: values +0 (first half) and +1, m tile 2g + 1: +2 and +3
-        *reinterpret_cast<float4*>(&sm.o[warp][8 * x + 2 * c][32 * g + 4 * i]) =
+        *reinterpret_cast<float4*>(&sm.ring[warp].o[8 * x + 2 * c][32 * g + 4 * i]) =
             make_float4(o[x][2 * g][0], o[x][2 * g][2], o[x][2 * g + 1][0], o[x][2 * g + 1][2]);
-        *reinterpret_cast<float4*>(&sm.o[warp][8 * x + 2 * c + 1][32 * g + 4 * i]) =
+        *reinterpret_cast<float4*>(&sm.ring[warp].o[8 * x + 2 * c + 1][32 * g + 4 * i]) =
             make_float4(o[x][2 * g][1], o[x][2 * g][3], o[x][2 * g + 1][1], o[x][2 * g + 1][3]);
       }
     }
@@ -602,19 +622,19 @@ __global__ void __launch_bounds__(kThreads, Steps<NT>::kCtas) attention_kernel(c
         // a warp that saw nothing has sums of zero, or of NaN where a logit was NaN: then so is its factor's product
         const float f = mw == -INFINITY ? 1.f : cosa::ex2_approx(mw - M);
         sum = fmaf(f, sm.ml[w][row][1], sum);
-        const float4 u = *reinterpret_cast<const float4*>(&sm.o[w][row][d0]);
+        const float4 u = *reinterpret_cast<const float4*>(&sm.ring[w].o[row][d0]);
         v.x = fmaf(f, u.x, v.x); v.y = fmaf(f, u.y, v.y); v.z = fmaf(f, u.z, v.z); v.w = fmaf(f, u.w, v.w);
       }
       if (whole) {
         const int rr = rt * kRows + row;
         const int tok = rr / a.group, head = rr - tok * a.group;
-        const float inv = sum == 0.f ? 0.f : kDown / (sum * (1.0f / kUp));
+        const float inv = sum == 0.f ? 0.f : kDown / sum;
         uint16_t* dst = L.out + ((static_cast<int64_t>(r.tok0) + tok) * L.num_q_heads + h * a.group + head) * D + d0;
         *reinterpret_cast<uint2*>(dst) = make_uint2(cosa::pack_bf16x2(v.x * inv, v.y * inv), cosa::pack_bf16x2(v.z * inv, v.w * inv));
         if (WEIGHTS && d0 == 0) {
           float* st = a.stats + ((static_cast<int64_t>(h) * L.total_tokens + r.tok0) * a.group + rr) * 2;
           st[0] = M;
-          st[1] = sum * (1.0f / kUp);
+          st[1] = sum;
         }
       } else {
         const size_t at_part = (static_cast<size_t>(me) * 2 + slot_of_part) * 16 + row;
@@ -628,6 +648,7 @@ __global__ void __launch_bounds__(kThreads, Steps<NT>::kCtas) attention_kernel(c
     if (!whole && t_begin == 0) {
       own = Owner{nrows, sh.owner(item_end - 1), r.tok0, h, rt};
     }
+    cosa::fence_proxy_async_smem();   // the rings are free for copies again
     __syncthreads();
     at = item_begin + t_end;
   }
@@ -701,13 +722,13 @@ __global__ void __launch_bounds__(kJoinThreads) combine_wide_kernel(const Args a
         }
         const int rr = own.rt * tile_rows + row;
         const int tok = rr / a.group, head = rr - tok * a.group;
-        const float inv = sum == 0.f ? 0.f : kDown / (sum * (1.0f / kUp));
+        const float inv = sum == 0.f ? 0.f : kDown / sum;
         uint16_t* dst = a.L.out + ((static_cast<int64_t>(own.tok0) + tok) * a.L.num_q_heads + own.h * a.group + head) * D + 4 * d4;
         *reinterpret_cast<uint2*>(dst) = make_uint2(cosa::pack_bf16x2(v.x * inv, v.y * inv), cosa::pack_bf16x2(v.z * inv, v.w * inv));
         if (WEIGHTS && d4 == 0) {
           float* st = a.stats + ((static_cast<int64_t>(own.h) * a.L.total_tokens + own.tok0) * a.group + rr) * 2;
           st[0] = M;
-          st[1] = sum * (1.0f / kUp);
+          st[1] = sum;
         }
       }
       __syncthreads();
@@ -748,14 +769,14 @@ __global__ void __launch_bounds__(kJoinThreads) combine_kernel(const Args a, con
     }
     const int rr = own.rt * tile_rows + row;
     const int tok = rr / a.group, head = rr - tok * a.group;
-    const float inv = sum == 0.f ? 0.f : kDown / (sum * (1.0f / kUp));
+    const float inv = sum == 0.f ? 0.f : kDown / sum;
     uint16_t* dst = a.L.out + ((static_cast<int64_t>(own.tok0) + tok) * a.L.num_q_heads + own.h * a.group + head) * D + V * lane;
 #pragma unroll
     for (int k = 0; k < V; k += 2) *reinterpret_cast<uint32_t*>(dst + k) = cosa::pack_bf16x2(v[k] * inv, v[k + 1] * inv);
     if (WEIGHTS && lane == 0) {
       float* st = a.stats + ((static_cast<int64_t>(own.h) * a.L.total_tokens + own.tok0) * a.group + rr) * 2;
       st[0] = M;
-      st[1] = sum * (1.0f / kUp);
+      st[1] = sum;
     }
   }
 }
@@ -807,7 +828,7 @@ size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 template <int D, int NT, bool WEIGHTS>
 cudaError_t launch(const Args& a, cudaStream_t stream) {
   constexpr size_t smem = sizeof(AttnSmem<D, NT>);
-  static_assert(smem <= 227 * 1024, "shared memory of a CTA");
+  static_assert(Steps<NT>::kCtas * (smem + 1024) <= 228 * 1024, "shared memory of an SM");
   auto* kernel = attention_kernel<D, NT, WEIGHTS>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
