@@ -161,6 +161,7 @@ __global__ void __launch_bounds__(kThreads, 4) rope_kernel(const RopeLaunch L, c
   for (int r0 = part * kRows; r0 < rows; r0 += kBatch * split * kRows) {    // uniform over the warp
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) finish(r0 + k * split * kRows + sub, u[k][0], u[k][1]);
+    if (r0 + kBatch * split * kRows >= rows) break;
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) load(r0 + (kBatch + k) * split * kRows + sub, u[k][0], u[k][1]);
   }
