@@ -152,20 +152,26 @@ class _Call:
             raise ValueError(f"{name} is on {t.device}, the other tensors on cuda:{self.index}")
         self.index = index
 
-    def dense(self, t: Optional[torch.Tensor], name: str, dtype: torch.dtype, need: Optional[str] = None):
-        """Address of a contiguous tensor of at least the size that the parameters imply."""
-        if t is None:
-            return None
-        if t.dtype != dtype:
-            raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-        least = self.need[need or name]
-        if t.numel() < least:
-            raise ValueError(f"{name} holds {t.numel()} elements; the parameters need at least {least}")
-        if t.get_device() != self.index or self.index < 0:
-            self.on_device(t, name)
-        return t.data_ptr()
+    def dense(self, *wanted) -> list:
+        """Addresses of contiguous tensors (tensor or None, name, dtype[, key of the size]) of at least the sizes that the
+        parameters imply."""
+        out, need, index = [], self.need, self.index
+        for t, name, dtype, *key in wanted:
+            if t is None:
+                out.append(None)
+                continue
+            if t.dtype != dtype:
+                raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+            if not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous")
+            least = need[key[0] if key else name]
+            if t.numel() < least:
+                raise ValueError(f"{name} holds {t.numel()} elements; the parameters need at least {least}")
+            if index is None or t.get_device() != index:
+                self.on_device(t, name)
+                index = self.index
+            out.append(t.data_ptr())
+        return out
 
     def rows(self, t: torch.Tensor, name: str, heads: int):
         """Address and token stride of rows [total_tokens, heads, d], whose tokens may lie apart."""
@@ -192,14 +198,15 @@ class _Call:
         return p
 
     def run(self, name: str, p: CosaKvParams, args, status: Optional[torch.Tensor], stream) -> None:
-        st = self.dense(status, "status", torch.int32)
+        if status is not None:
+            (status,) = self.dense((status, "status", torch.int32))
         s = stream.cuda_stream if stream is not None else torch.cuda.current_stream(self.index).cuda_stream
         f = getattr(_lib or kv_library(), name)
         if torch.cuda.current_device() == self.index:
-            rc = f(p, *args, st, s)
+            rc = f(p, *args, status, s)
         else:
             with torch.cuda.device(self.index):
-                rc = f(p, *args, st, s)
+                rc = f(p, *args, status, s)
         if rc != COSA_OK:
             raise CosaError(rc, name)
 
@@ -230,12 +237,10 @@ def cosa_qk_norm_rope(p: CosaKvParams, q: torch.Tensor, k: torch.Tensor, cu_seql
     if k_out is None and k_cache is None:
         k_out = c.empty((p.total_tokens, p.num_kv_heads, p.head_dim), torch.bfloat16, stream)
     bf, i32 = torch.bfloat16, torch.int32
-    args = (qp, kp, vp, c.dense(q_weight, "q_weight", bf), c.dense(k_weight, "k_weight", bf),
-            c.dense(inv_freq, "inv_freq", torch.float64), c.dense(positions, "positions", i32),
-            c.dense(cu_seqlens, "cu_seqlens", i32), c.dense(start, "start", i32), c.dense(q_out, "q_out", bf),
-            c.dense(k_out, "k_out", bf), c.dense(k_cache, "k_cache", bf), c.dense(v_cache, "v_cache", bf),
-            c.dense(page_table, "page_table", i32))
-    c.run("cosa_qk_norm_rope", c.params(q_stride=qs, k_stride=ks, v_stride=vs), args, status, stream)
+    args = c.dense((q_weight, "q_weight", bf), (k_weight, "k_weight", bf), (inv_freq, "inv_freq", torch.float64),
+                   (positions, "positions", i32), (cu_seqlens, "cu_seqlens", i32), (start, "start", i32), (q_out, "q_out", bf),
+                   (k_out, "k_out", bf), (k_cache, "k_cache", bf), (v_cache, "v_cache", bf), (page_table, "page_table", i32))
+    c.run("cosa_qk_norm_rope", c.params(q_stride=qs, k_stride=ks, v_stride=vs), (qp, kp, vp, *args), status, stream)
     return q_out, k_out
 
 
@@ -255,11 +260,10 @@ def cosa_kv4_store(p: CosaKvParams, kv4_cache: torch.Tensor, page_table: torch.T
     else:
         if kv_len is None:
             raise ValueError("pages need kv_len")
-        kp, vp, ks, vs = c.dense(k, "k", bf, "k_cache"), c.dense(v, "v", bf, "v_cache"), 0, 0
-    args = (kp, vp, c.dense(cu_seqlens, "cu_seqlens", i32), c.dense(src_page_table, "src_page_table", i32),
-            c.dense(start, "start", i32), c.dense(kv_len, "kv_len", i32), c.dense(kv4_cache, "kv4_cache", torch.uint8),
-            c.dense(page_table, "page_table", i32))
-    c.run("cosa_kv4_store", c.params(k_stride=ks, v_stride=vs), args, status, stream)
+        (kp, vp), ks, vs = c.dense((k, "k", bf, "k_cache"), (v, "v", bf, "v_cache")), 0, 0
+    args = c.dense((cu_seqlens, "cu_seqlens", i32), (src_page_table, "src_page_table", i32), (start, "start", i32),
+                   (kv_len, "kv_len", i32), (kv4_cache, "kv4_cache", torch.uint8), (page_table, "page_table", i32))
+    c.run("cosa_kv4_store", c.params(k_stride=ks, v_stride=vs), (kp, vp, *args), status, stream)
 
 
 def cosa_kv4_load(p: CosaKvParams, kv4_cache: torch.Tensor, page_table: torch.Tensor, k_cache: torch.Tensor,
@@ -269,9 +273,9 @@ def cosa_kv4_load(p: CosaKvParams, kv4_cache: torch.Tensor, page_table: torch.Te
     """Slots start[b] .. kv_len[b] - 1 of the 4-bit cache into the bf16 pages of dst_page_table."""
     c = _Call(p)
     bf, i32 = torch.bfloat16, torch.int32
-    args = (c.dense(kv4_cache, "kv4_cache", torch.uint8), c.dense(page_table, "page_table", i32),
-            c.dense(start, "start", i32), c.dense(kv_len, "kv_len", i32), c.dense(k_cache, "k_cache", bf),
-            c.dense(v_cache, "v_cache", bf), c.dense(dst_page_table, "dst_page_table", i32))
+    args = c.dense((kv4_cache, "kv4_cache", torch.uint8), (page_table, "page_table", i32), (start, "start", i32),
+                   (kv_len, "kv_len", i32), (k_cache, "k_cache", bf), (v_cache, "v_cache", bf),
+                   (dst_page_table, "dst_page_table", i32))
     c.run("cosa_kv4_load", p, args, status, stream)
 
 
@@ -288,9 +292,8 @@ def cosa_kv4_attention(p: CosaKvParams, q: torch.Tensor, cu_seqlens: torch.Tenso
     qp, qs = c.rows(q, "q", p.num_q_heads)
     if out is None:
         out = c.empty((p.total_tokens, p.num_q_heads, p.head_dim), bf, stream)
-    args = [qp, c.dense(cu_seqlens, "cu_seqlens", i32), c.dense(kv4_cache, "kv4_cache", torch.uint8),
-            c.dense(page_table, "page_table", i32), c.dense(kv_len, "kv_len", i32), c.dense(out, "out", bf),
-            c.dense(weights, "weights", torch.float32)]
+    args = c.dense((cu_seqlens, "cu_seqlens", i32), (kv4_cache, "kv4_cache", torch.uint8), (page_table, "page_table", i32),
+                   (kv_len, "kv_len", i32), (out, "out", bf), (weights, "weights", torch.float32))
     if workspace is None:
         size = cosa_kv4_attention_workspace_size(p, weights is not None)
         workspace = c.empty(max(size, 256), torch.uint8, stream)
@@ -298,7 +301,7 @@ def cosa_kv4_attention(p: CosaKvParams, q: torch.Tensor, cu_seqlens: torch.Tenso
     if not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
     args += [workspace.data_ptr(), workspace.numel() * workspace.element_size()]
-    c.run("cosa_kv4_attention", c.params(q_stride=qs) if qs else p, args, status, stream)
+    c.run("cosa_kv4_attention", c.params(q_stride=qs) if qs else p, (qp, *args), status, stream)
     return out
 
 
@@ -310,16 +313,15 @@ def cosa_kv4_evict(p: CosaKvParams, kv4_cache: torch.Tensor, page_table: torch.T
     of the same cache that hold none of the sources).  Returns (new_len [B], kept [B, Hkv, budget], weights_out)."""
     c = _Call(p)
     i32 = torch.int32
-    kv4 = c.dense(kv4_cache, "kv4_cache", torch.uint8)
+    (kv4,) = c.dense((kv4_cache, "kv4_cache", torch.uint8))
     if new_len is None:
         new_len = c.empty((p.num_reqs,), i32, stream)
     if kept is None:
         kept = c.empty((p.num_reqs, p.num_kv_heads, p.budget), i32, stream)
     if weights_out is None:
         weights_out = c.empty((p.num_reqs, p.num_kv_heads, p.max_seqlen), torch.float32, stream)
-    args = (kv4, c.dense(page_table, "page_table", i32), c.dense(kv_len, "kv_len", i32),
-            c.dense(weights, "weights", torch.float32), c.dense(dst_page_table, "dst_page_table", i32, "evict_page_table"),
-            c.dense(new_len, "new_len", i32), c.dense(kept, "kept", i32),
-            c.dense(weights_out, "weights_out", torch.float32))
-    c.run("cosa_kv4_evict", p, args, status, stream)
+    args = c.dense((page_table, "page_table", i32), (kv_len, "kv_len", i32), (weights, "weights", torch.float32),
+                   (dst_page_table, "dst_page_table", i32, "evict_page_table"), (new_len, "new_len", i32), (kept, "kept", i32),
+                   (weights_out, "weights_out", torch.float32))
+    c.run("cosa_kv4_evict", p, (kv4, *args), status, stream)
     return new_len, kept, weights_out

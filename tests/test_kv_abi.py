@@ -168,13 +168,13 @@ def test_binding_refuses_before_the_library(C):
     c = C._Call(p)
     i32 = torch.int32
     with pytest.raises(ValueError, match="page_table holds 5"):
-        c.dense(meta(5, dtype=i32), "page_table", i32)
+        c.dense((meta(5, dtype=i32), "page_table", i32))
     with pytest.raises(ValueError, match="must be torch.int32"):
-        c.dense(meta(6, dtype=torch.int64), "page_table", i32)
+        c.dense((meta(6, dtype=torch.int64), "page_table", i32))
     with pytest.raises(ValueError, match="contiguous"):
-        c.dense(meta(6, 2, dtype=i32)[:, 0], "page_table", i32)
+        c.dense((meta(6, 2, dtype=i32)[:, 0], "page_table", i32))
     with pytest.raises(ValueError, match="CUDA"):
-        c.dense(meta(6, dtype=i32), "page_table", i32)
+        c.dense((meta(6, dtype=i32), "page_table", i32))
     with pytest.raises(ValueError, match="6"):
         c.rows(meta(5, 4, 64), "q", 4)
     with pytest.raises(ValueError, match="must be"):
