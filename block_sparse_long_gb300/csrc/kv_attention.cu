@@ -18,12 +18,14 @@
 // ring in shared memory, and nothing is shared between warps until the end of the CTA's part of a request.
 //
 // The work is the list of all (request, kv head, row tile, unit of 32 or 16 tokens); every CTA takes an equal run
-// of it, whatever the lengths are.  A CTA that has all of a (request, kv head, row tile) writes its
+// of it, whatever the lengths are (or a cluster takes each item, where that is quicker).  A CTA that has all of a (request, kv head, row tile) writes its
 // output; otherwise it leaves its maximum, sum and unnormalised output in the workspace (a CTA has at
 // most two unfinished ones, the first and the last of its run) and kv4_combine_kernel joins them in order.
 #include <algorithm>
 #include <cstdint>
 #include <type_traits>
+
+#include <cooperative_groups.h>
 
 #include "cosa_kv.h"
 #include "kv_internal.h"
@@ -32,12 +34,21 @@
 namespace cosa_kv {
 namespace {
 
+namespace cg = cooperative_groups;
+
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kSms = 152;
 constexpr int kMaxCtas = 3 * kSms;
+constexpr int kMaxRows = 24;     // query rows of a row tile: 8, 16 or 24
 constexpr int kMinUnits = 4;     // units per CTA at least, where a request is shared between CTAs: one per warp
 constexpr int kWholeUnits = 8;   // units of an item that one CTA takes alone
+constexpr int kMaxCluster = 16;  // CTAs of a cluster
+// Tokens per warp up to which items go to clusters.  No list of the batch to make before the first load and no second kernel
+// after the last: a context of 777 tokens takes 5.8 us instead of 11.4, 7 x 14K with 2 kv heads 17.5 instead of 18.7, 15 x 6K
+// 14.3 instead of 21.6; but shares are even only within an item and the clusters may fill the card badly: one of 32K takes
+// 23.8 us instead of 19.0.
+constexpr int kClusterTokens = 256;
 constexpr int kFewItems = 64;     // items up to which the join has a block per row
 
 // What a CTA leaves about the unfinished (request, kv head, row tile) that begins in its run.
@@ -50,14 +61,15 @@ struct Owner {
 struct Args {
   AttnLaunch L;
   Owner* owner;       // [kMaxCtas]
-  float* part_ml;     // [kMaxCtas][2][16][2]
-  float* part_o;      // [kMaxCtas][2][16][d]
+  float* part_ml;     // [kMaxCtas][2][kMaxRows][2]
+  float* part_o;      // [kMaxCtas][2][kMaxRows][d]
   float* stats;       // [Hkv][T * g][2]: maximum (scaled) and sum of a row, with weights only
   float* logits;      // [Hkv][T * g][pitch]: logits as the first product leaves them, with weights only
   int64_t pitch;
   int group;          // Hq / Hkv
   int page_shift;     // log2(P)
   bool stall;         // test hook: no copy is issued
+  int row_tiles;      // row tiles of a request, as far as max_new_tokens tells
 };
 
 struct Request {
@@ -207,13 +219,14 @@ constexpr float kUp = 79228162514264337593543950336.0f;      // 2^96
 constexpr float kDown = 8589934592.0f;                       // 2^33
 
 // A unit is TP tiles that a warp takes at a time: with eight rows two, whose chains of dependent instructions fill each
-// other's gaps; with sixteen rows one, for the registers.  (One 128K context with TP = 1, 2, 4: 49, 39 and 38 us; 48 ragged
+// other's gaps; with more rows one, for the registers.  (One 128K context with TP = 1, 2, 4: 49, 39 and 38 us; 48 ragged
 // ones with weights: 149, 130 and 134 us; a context of 777 tokens: 12, 11.5 and 14.5 us.)
 template <int NT>
 struct Steps {
   static constexpr int TP = NT == 1 ? 2 : 1;
   static constexpr int kStages = NT == 1 ? 2 : 4;      // units in flight per warp
   static constexpr int kCtas = NT == 1 ? 3 : 2;        // CTAs of an SM: 168 or 255 registers a thread
+  static constexpr int kResident = kCtas * kSms;
 };
 
 // A warp's part of the output before the join lies where its units were.
@@ -226,12 +239,16 @@ struct AttnSmem {
   };
   alignas(16) Ring ring[kWarps];
   float ml[kWarps][kRows][2];
+  alignas(8) float joined[kRows][2];
   alignas(8) uint64_t full[kWarps][Steps<NT>::kStages];
 };
 
 // A warp's accumulators: lane = 4 i + c has query rows 2c and 2c + 1 of each eight; of the logits the tokens i and i + 8,
 // of the output the values 32 g + 4 i .. + 3 of every scale group g.
-template <int D, int NT, bool WEIGHTS>
+//
+// CLUSTERED: a cluster has one (request, kv head, row tile) at a time, its CTAs even shares of the units, and joins its parts
+// through distributed shared memory.  Else every CTA has a run of the whole list, and a second kernel joins the parts.
+template <int D, int NT, bool WEIGHTS, bool CLUSTERED>
 __global__ void __launch_bounds__(kThreads, Steps<NT>::kCtas) attention_kernel(const Args a) {
   using T = Tile<D>;
   constexpr int G = T::G;
@@ -244,10 +261,6 @@ __global__ void __launch_bounds__(kThreads, Steps<NT>::kCtas) attention_kernel(c
 
   wait_for_stream();
   let_next_start();
-  LaneUnits first;
-  const Shares sh = shares_of(a, kRows, kUnit, static_cast<int>(gridDim.x), blockIdx.x == 0 && warp == 0, first);
-  const int me = static_cast<int>(blockIdx.x);
-  Owner own{0, 0, 0, 0, 0};
   if (lane == 0) {
 #pragma unroll
     for (int k = 0; k < kStages; ++k) cosa::mbar_init(&sm.full[warp][k], 1);
@@ -258,27 +271,58 @@ __global__ void __launch_bounds__(kThreads, Steps<NT>::kCtas) attention_kernel(c
   uint32_t phase = 0;               // bit k: parity of the next completion of stage k's barrier
   bool alive = true;                // no wait of this warp has run out
   const uint64_t once = read_once();
-  if (me >= sh.ctas || sh.units == 0) {
-    if (tid == 0) a.owner[me] = own;
-    return;
-  }
-  const int64_t hi = sh.begin(me + 1);
-  int64_t at = sh.begin(me), req_begin;
-  int b = find_request(a, kRows, kUnit, at, first, req_begin);
 
-  while (at < hi) {
-    const Request r = request_of(a, b, kRows, kUnit, false);
-    const int64_t req_units = r.units * r.rts * L.num_kv_heads;
-    if (at >= req_begin + req_units) {     // the next request that has units
-      req_begin += req_units;
-      ++b;
-      continue;
+  const int me = static_cast<int>(blockIdx.x);
+  cg::cluster_group cluster = cg::this_cluster();
+  const int ctas = CLUSTERED ? static_cast<int>(cluster.num_blocks()) : 1;
+  const int rank = CLUSTERED ? static_cast<int>(cluster.block_rank()) : 0;
+  Request r;                        // the request at hand
+  int b, h, rt;                     // and the kv head and row tile
+  int t_begin, t_end;               // this CTA's units of it
+  Shares sh;
+  int64_t hi = 0, at = 0, req_begin = 0, item_end = 0;
+  Owner own{0, 0, 0, 0, 0};
+  if (CLUSTERED) {
+    const int item = me / ctas;
+    rt = item % a.row_tiles;
+    h = item / a.row_tiles % L.num_kv_heads;
+    b = item / a.row_tiles / L.num_kv_heads;
+    r = request_of(a, b, kRows, kUnit, rank == 0 && h == 0 && rt == 0 && tid == 0);
+    t_begin = static_cast<int>(r.units * rank / ctas);
+    t_end = static_cast<int>(r.units * (rank + 1) / ctas);
+  } else {
+    LaneUnits first;
+    sh = shares_of(a, kRows, kUnit, static_cast<int>(gridDim.x), blockIdx.x == 0 && warp == 0, first);
+    if (me >= sh.ctas || sh.units == 0) {
+      if (tid == 0) a.owner[me] = own;
+      return;
     }
-    const int64_t item = quotient(at - req_begin, r.units);   // (kv head, row tile)
-    const int h = static_cast<int>(quotient(item, r.rts)), rt = static_cast<int>(item - h * r.rts);
-    const int64_t item_begin = req_begin + item * r.units, item_end = item_begin + r.units;
-    const int t_begin = static_cast<int>(at - item_begin);
-    const int t_end = static_cast<int>(min(hi, item_end) - item_begin);
+    hi = sh.begin(me + 1);
+    at = sh.begin(me);
+    b = find_request(a, kRows, kUnit, at, first, req_begin);
+  }
+
+  for (;;) {
+    if (CLUSTERED) {
+      if (rt >= r.rts) break;        // the same in the whole cluster
+    } else {
+      if (at >= hi) break;
+      r = request_of(a, b, kRows, kUnit, false);
+      const int64_t req_units = r.units * r.rts * L.num_kv_heads;
+      if (at >= req_begin + req_units) {     // the next request that has units
+        req_begin += req_units;
+        ++b;
+        continue;
+      }
+      const int64_t item = quotient(at - req_begin, r.units);   // (kv head, row tile)
+      h = static_cast<int>(quotient(item, r.rts));
+      rt = static_cast<int>(item - h * r.rts);
+      const int64_t item_begin = req_begin + item * r.units;
+      item_end = item_begin + r.units;
+      t_begin = static_cast<int>(at - item_begin);
+      t_end = static_cast<int>(min(hi, item_end) - item_begin);
+      at = item_begin + t_end;
+    }
     const int nrows = static_cast<int>(min(static_cast<int64_t>(kRows), static_cast<int64_t>(r.n) * a.group - static_cast<int64_t>(rt) * kRows));
 
     // ---- the warp's units: t_begin + warp, + kWarps, ... ----
@@ -607,8 +651,20 @@ __global__ void __launch_bounds__(kThreads, Steps<NT>::kCtas) attention_kernel(c
       }
     }
     __syncthreads();
-    const bool whole = t_begin == 0 && t_end == r.units;
-    const int slot_of_part = t_begin == 0 ? 1 : 0;
+    // four values of a row whose maximum is M: the output, and what the weights need
+    auto finish = [&](int row, int d0, float M, float sum, const float4& v) {
+      const int rr = rt * kRows + row;
+      const int tok = rr / a.group, head = rr - tok * a.group;
+      const float inv = sum == 0.f ? 0.f : kDown / sum;
+      uint16_t* dst = L.out + ((static_cast<int64_t>(r.tok0) + tok) * L.num_q_heads + h * a.group + head) * D + d0;
+      *reinterpret_cast<uint2*>(dst) = make_uint2(cosa::pack_bf16x2(v.x * inv, v.y * inv), cosa::pack_bf16x2(v.z * inv, v.w * inv));
+      if (WEIGHTS && d0 == 0) {
+        float* st = a.stats + ((static_cast<int64_t>(h) * L.total_tokens + r.tok0) * a.group + rr) * 2;
+        st[0] = M;
+        st[1] = sum;
+      }
+    };
+    const bool whole = CLUSTERED ? ctas == 1 : t_begin == 0 && t_end == r.units;
     for (int k = tid; k < nrows * (D / 4); k += kThreads) {
       const int row = k / (D / 4), d0 = 4 * (k % (D / 4));
       float M = -INFINITY;
@@ -626,18 +682,15 @@ __global__ void __launch_bounds__(kThreads, Steps<NT>::kCtas) attention_kernel(c
         v.x = fmaf(f, u.x, v.x); v.y = fmaf(f, u.y, v.y); v.z = fmaf(f, u.z, v.z); v.w = fmaf(f, u.w, v.w);
       }
       if (whole) {
-        const int rr = rt * kRows + row;
-        const int tok = rr / a.group, head = rr - tok * a.group;
-        const float inv = sum == 0.f ? 0.f : kDown / sum;
-        uint16_t* dst = L.out + ((static_cast<int64_t>(r.tok0) + tok) * L.num_q_heads + h * a.group + head) * D + d0;
-        *reinterpret_cast<uint2*>(dst) = make_uint2(cosa::pack_bf16x2(v.x * inv, v.y * inv), cosa::pack_bf16x2(v.z * inv, v.w * inv));
-        if (WEIGHTS && d0 == 0) {
-          float* st = a.stats + ((static_cast<int64_t>(h) * L.total_tokens + r.tok0) * a.group + rr) * 2;
-          st[0] = M;
-          st[1] = sum;
+        finish(row, d0, M, sum, v);
+      } else if (CLUSTERED) {
+        *reinterpret_cast<float4*>(&sm.ring[0].o[row][d0]) = v;      // which only this thread has read
+        if (d0 == 0) {
+          sm.joined[row][0] = M;
+          sm.joined[row][1] = sum;
         }
       } else {
-        const size_t at_part = (static_cast<size_t>(me) * 2 + slot_of_part) * 16 + row;
+        const size_t at_part = (static_cast<size_t>(me) * 2 + (t_begin == 0 ? 1 : 0)) * kMaxRows + row;
         *reinterpret_cast<float4*>(a.part_o + at_part * D + d0) = v;
         if (d0 == 0) {
           a.part_ml[at_part * 2] = M;
@@ -645,14 +698,34 @@ __global__ void __launch_bounds__(kThreads, Steps<NT>::kCtas) attention_kernel(c
         }
       }
     }
-    if (!whole && t_begin == 0) {
-      own = Owner{nrows, sh.owner(item_end - 1), r.tok0, h, rt};
+    if (CLUSTERED && !whole) {
+      cluster.sync();
+      for (int k = rank * kThreads + tid; k < nrows * (D / 4); k += ctas * kThreads) {
+        const int row = k / (D / 4), d0 = 4 * (k % (D / 4));
+        float M = -INFINITY, sum = 0.f;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int j = 0; j < ctas; ++j) M = fmaxf(M, *cluster.map_shared_rank(&sm.joined[row][0], j));
+#pragma unroll 4
+        for (int j = 0; j < ctas; ++j) {
+          const float2 ml = *reinterpret_cast<const float2*>(cluster.map_shared_rank(&sm.joined[row][0], j));
+          const float4 u = *reinterpret_cast<const float4*>(cluster.map_shared_rank(&sm.ring[0].o[row][d0], j));
+          const float f = ml.x == -INFINITY ? 1.f : cosa::ex2_approx(ml.x - M);
+          sum = fmaf(f, ml.y, sum);
+          v.x = fmaf(f, u.x, v.x); v.y = fmaf(f, u.y, v.y); v.z = fmaf(f, u.z, v.z); v.w = fmaf(f, u.w, v.w);
+        }
+        finish(row, d0, M, sum, v);
+      }
+      cosa::fence_proxy_async_smem();
+      cluster.sync();                  // the cluster's memory has been read
+    } else {
+      if (!CLUSTERED && !whole && t_begin == 0) own = Owner{nrows, sh.owner(item_end - 1), r.tok0, h, rt};
+      cosa::fence_proxy_async_smem();  // the rings are free for copies again
+      __syncthreads();
     }
-    cosa::fence_proxy_async_smem();   // the rings are free for copies again
-    __syncthreads();
-    at = item_begin + t_end;
+    if (CLUSTERED) rt += a.row_tiles;
   }
-  if (tid == 0) a.owner[me] = own;
+  if (!CLUSTERED && tid == 0) a.owner[me] = own;
 }
 
 // Joins the parts of the items that no CTA had whole, for few items of many parts.  Block (x, y) goes through the owner
@@ -673,7 +746,7 @@ __global__ void __launch_bounds__(kJoinThreads) combine_wide_kernel(const Args a
     const Owner own = a.owner[first];
     for (int row = blockIdx.y; row < own.rows; row += gridDim.y) {
       // part j: the second place of the owner, the first of every later CTA
-      auto place = [&](int j) { return (static_cast<size_t>(first + j) * 2 + (j == 0 ? 1 : 0)) * 16 + row; };
+      auto place = [&](int j) { return (static_cast<size_t>(first + j) * 2 + (j == 0 ? 1 : 0)) * kMaxRows + row; };
       const int parts = own.last - first + 1;
       float4 o[kDeep];
 #pragma unroll
@@ -746,7 +819,7 @@ __global__ void __launch_bounds__(kJoinThreads) combine_kernel(const Args a, con
   let_next_start();
   const Owner own = a.owner[first];
   for (int row = warp; row < own.rows; row += kJoinThreads / 32) {
-    auto place = [&](int j) { return (static_cast<size_t>(first + j) * 2 + (j == 0 ? 1 : 0)) * 16 + row; };
+    auto place = [&](int j) { return (static_cast<size_t>(first + j) * 2 + (j == 0 ? 1 : 0)) * kMaxRows + row; };
     const int parts = own.last - first + 1;
     float M = -INFINITY;
     for (int j = lane; j < parts; j += 32) M = fmaxf(M, a.part_ml[place(j) * 2]);
@@ -826,33 +899,59 @@ int64_t logits_pitch(int max_seqlen) { return (static_cast<int64_t>(max_seqlen) 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
 template <int D, int NT, bool WEIGHTS>
-cudaError_t launch(const Args& a, cudaStream_t stream) {
+cudaError_t launch(Args a, cudaStream_t stream) {
+  using S = Steps<NT>;
   constexpr size_t smem = sizeof(AttnSmem<D, NT>);
-  static_assert(Steps<NT>::kCtas * (smem + 1024) <= 228 * 1024, "shared memory of an SM");
-  auto* kernel = attention_kernel<D, NT, WEIGHTS>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-  if (e != cudaSuccess) return e;
-  constexpr int kCtas = Steps<NT>::kCtas * kSms;
-  if ((e = launch_after(kernel, dim3(kCtas), kThreads, smem, stream, 1, a)) != cudaSuccess) return e;
-  // How many items there are, as far as max_new_tokens tells (either kernel is right for any number).
+  static_assert(S::kCtas * (smem + 1024) <= 228 * 1024, "shared memory of an SM");
   const int64_t rows = static_cast<int64_t>(a.L.max_new_tokens) * a.group;
-  const int64_t items = static_cast<int64_t>(a.L.num_reqs) * a.L.num_kv_heads * ((rows + 8 * NT - 1) / (8 * NT));
-  if (items <= kFewItems)
-    e = launch_after(combine_wide_kernel<D, WEIGHTS>, dim3(64, static_cast<unsigned>(std::min<int64_t>(8 * NT, rows))), kJoinThreads, 0,
-                     stream, 1, a, kCtas, 8 * NT);
-  else
-    e = launch_after(combine_kernel<D, WEIGHTS>, dim3(kCtas), kJoinThreads, 0, stream, 1, a, 8 * NT);
+  const int64_t row_tiles = std::min<int64_t>((rows + 8 * NT - 1) / (8 * NT), INT32_MAX);
+  // how many (request, kv head, row tile) there are and how many units they have, as far as the parameters tell (either way
+  // of sharing them is right for any number)
+  const int64_t items = static_cast<int64_t>(a.L.num_reqs) * a.L.num_kv_heads * row_tiles;
+  const int64_t units = (static_cast<int64_t>(a.L.max_seqlen) + S::TP * kTile - 1) / (S::TP * kTile);
+  int ctas = 1;
+  while (ctas < kMaxCluster && 2 * ctas * items <= S::kResident && ctas * kWarps < units) ctas *= 2;
+  cudaError_t e;
+  // Clusters where a warp has few tokens: up to 512 of them where the clusters fill half of the card, else up to 256.
+  const int64_t tokens = (units + ctas * kWarps - 1) / (ctas * kWarps) * (S::TP * kTile);
+  if (ctas * items <= S::kResident && tokens <= (2 * ctas * items >= S::kResident ? 2 * kClusterTokens : kClusterTokens)) {
+    auto* kernel = attention_kernel<D, NT, WEIGHTS, true>;
+    a.row_tiles = static_cast<int>(row_tiles);
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess) e = launch_after(kernel, dim3(static_cast<unsigned>(items * ctas)), kThreads, smem, stream, ctas, a);
+  } else {
+    auto* kernel = attention_kernel<D, NT, WEIGHTS, false>;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e == cudaSuccess) e = launch_after(kernel, dim3(S::kResident), kThreads, smem, stream, 1, a);
+    if (e != cudaSuccess) return e;
+    if (items <= kFewItems)
+      e = launch_after(combine_wide_kernel<D, WEIGHTS>, dim3(64, static_cast<unsigned>(std::min<int64_t>(8 * NT, rows))), kJoinThreads, 0,
+                       stream, 1, a, S::kResident, 8 * NT);
+    else
+      e = launch_after(combine_kernel<D, WEIGHTS>, dim3(S::kResident), kJoinThreads, 0, stream, 1, a, 8 * NT);
+  }
   if (e != cudaSuccess || !WEIGHTS) return e;
   const dim3 grid(static_cast<unsigned>((a.L.max_seqlen + 1023LL) / 1024), static_cast<unsigned>(a.L.num_kv_heads),
                   static_cast<unsigned>(a.L.num_reqs));
   return launch_after(weights_kernel, grid, 256, 0, stream, 1, a);
 }
 
+// Row tiles of 8, 16 or 24 rows: the smallest that has all of a request's rows, else the larger if it leaves fewer tiles
+// (each of which reads the cache again).
+template <int D, bool WEIGHTS>
+cudaError_t launch(const Args& a, cudaStream_t stream) {
+  const int64_t rows = static_cast<int64_t>(a.L.max_new_tokens) * a.group;
+  if (rows <= 8) return launch<D, 1, WEIGHTS>(a, stream);
+  if (rows <= 16 || (rows + 23) / 24 == (rows + 15) / 16) return launch<D, 2, WEIGHTS>(a, stream);
+  return launch<D, 3, WEIGHTS>(a, stream);
+}
+
 }  // namespace
 
 size_t attn_workspace_bytes(int num_q_heads, int head_dim, int total_tokens, int max_seqlen, bool with_weights) {
-  size_t n = align256(kMaxCtas * sizeof(Owner)) + align256(size_t(kMaxCtas) * 2 * 16 * 2 * 4) +
-             align256(size_t(kMaxCtas) * 2 * 16 * head_dim * 4);
+  size_t n = align256(kMaxCtas * sizeof(Owner)) + align256(size_t(kMaxCtas) * 2 * kMaxRows * 2 * 4) +
+             align256(size_t(kMaxCtas) * 2 * kMaxRows * head_dim * 4);
   if (with_weights) {
     const size_t rows = static_cast<size_t>(total_tokens) * num_q_heads;
     n += align256(rows * 8) + align256(rows * logits_pitch(max_seqlen) * 4);
@@ -872,22 +971,16 @@ cudaError_t launch_attention(const AttnLaunch& L, cudaStream_t stream) {
   a.owner = reinterpret_cast<Owner*>(w);
   w += align256(kMaxCtas * sizeof(Owner));
   a.part_ml = reinterpret_cast<float*>(w);
-  w += align256(size_t(kMaxCtas) * 2 * 16 * 2 * 4);
+  w += align256(size_t(kMaxCtas) * 2 * kMaxRows * 2 * 4);
   a.part_o = reinterpret_cast<float*>(w);
-  w += align256(size_t(kMaxCtas) * 2 * 16 * L.head_dim * 4);
+  w += align256(size_t(kMaxCtas) * 2 * kMaxRows * L.head_dim * 4);
   if (L.weights) {
     a.stats = reinterpret_cast<float*>(w);
     w += align256(static_cast<size_t>(L.total_tokens) * L.num_q_heads * 8);
     a.logits = reinterpret_cast<float*>(w);
   }
-  const bool wide = static_cast<int64_t>(L.max_new_tokens) * a.group > 8;
-  const bool d128 = L.head_dim == 128;
-  if (L.weights) {
-    if (d128) return wide ? launch<128, 2, true>(a, stream) : launch<128, 1, true>(a, stream);
-    return wide ? launch<64, 2, true>(a, stream) : launch<64, 1, true>(a, stream);
-  }
-  if (d128) return wide ? launch<128, 2, false>(a, stream) : launch<128, 1, false>(a, stream);
-  return wide ? launch<64, 2, false>(a, stream) : launch<64, 1, false>(a, stream);
+  if (L.head_dim == 128) return L.weights ? launch<128, true>(a, stream) : launch<128, false>(a, stream);
+  return L.weights ? launch<64, true>(a, stream) : launch<64, false>(a, stream);
 }
 
 }  // namespace cosa_kv

@@ -85,7 +85,7 @@ typedef struct cosa_kv_params {
   int32_t max_pages_per_req; /* row pitch of the page tables, >= ceil(max_seqlen / P)           */
   int32_t rotary_dim;        /* rotated values per head: a multiple of 16, <= d                 */
   int32_t max_new_tokens;    /* attention: query tokens per request to tile for (any value >= 1
-                                gives the same results; the largest request's is fastest)       */
+                                is right; the largest request's is fastest)                     */
   int32_t budget;            /* evict: slots kept per request and kv head                       */
   int32_t sink;              /* evict: first slots always kept                                  */
   int32_t recent;            /* evict: last slots always kept, sink + recent <= budget          */

@@ -292,8 +292,12 @@ def test_store_and_load_report_contradictions():
 # ---------------------------------------------------------------------------------------------------------------
 # attention
 # ---------------------------------------------------------------------------------------------------------------
-def attend(rng, lens, new, Hq, Hkv, d, P, *, weights=False, missing=(), edit=None, hint=None, scale=None, q_scale=1.5, spare=2):
+def attend(rng, lens, new, Hq, Hkv, d, P, *, weights=False, missing=(), edit=None, hint=None, scale=None, q_scale=1.5, spare=2, wide=False):
     cache, t, ks, vs = packed(rng, lens, Hkv, P, d, missing=missing, edit=edit)
+    if wide:          # a max_seqlen far above the lengths: the batch is shared as one list instead of by clusters
+        more = np.full((len(lens), -(-20000 // P)), -1, np.int32)
+        more[:, :t.shape[1]] = t
+        t = more
     T = sum(new)
     q = bf(rng, T + spare, Hq, d, scale=q_scale)
     pages = t.shape[1]
@@ -336,32 +340,35 @@ def run_attention(c, **kw):
     return out
 
 
-@pytest.mark.parametrize("weights", [False, True])
+@pytest.mark.parametrize("weights,wide", [(False, False), (True, False), (True, True)])
 @pytest.mark.parametrize("Hq,Hkv,d,P", [(32, 8, 128, 64), (4, 4, 64, 16), (7, 1, 128, 128), (8, 1, 64, 64), (16, 1, 128, 16),
                                         (12, 4, 128, 32), (24, 1, 64, 32), (9, 3, 64, 128)])
-def test_attention_lengths(Hq, Hkv, d, P, weights):
+def test_attention_lengths(Hq, Hkv, d, P, weights, wide):
     """One token per request; lengths from zero to several tiles; pages that end inside the tile; missing pages."""
     lens = [1, 15, 16, 17, 0, 64, 130, 300, 2, P + 1]
     c = attend(np.random.default_rng(Hq * 7 + d + P), lens, [1] * len(lens), Hq, Hkv, d, P, weights=weights,
-               missing=[(7, 0), (6, min(1, 130 // P)), (2, 0)])
+               missing=[(7, 0), (6, min(1, 130 // P)), (2, 0)], wide=wide)
     run_attention(c)
 
 
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("Hq,Hkv,d,new,hint", [(8, 2, 128, [3, 0, 1, 5, 2], None), (8, 2, 128, [3, 0, 1, 5, 2], 1), (4, 4, 64, [9, 1, 0, 20, 2], None),
-                                               (16, 2, 64, [2, 0, 1, 3, 2], 2), (6, 2, 128, [40, 0, 1, 2, 2], 100), (5, 5, 128, [8, 8, 8, 8, 2], 3)])
-def test_attention_several_tokens(Hq, Hkv, d, new, hint):
+                                               (16, 2, 64, [2, 0, 1, 3, 2], 2), (6, 2, 128, [40, 0, 1, 2, 2], 100), (5, 5, 128, [8, 8, 8, 8, 2], 3), (7, 1, 64, [3, 1, 1, 2, 0], None),
+                                               (6, 1, 128, [4, 0, 1, 8, 1], None), (12, 1, 128, [2, 2, 2, 2, 2], 1)])
+def test_attention_several_tokens(Hq, Hkv, d, new, hint, wide):
     """Causal at the end; more rows than a row tile has; requests without queries; query tokens that see nothing (more
     queries than slots); any hint gives the same."""
     lens = [100, 50, 1, 7, 1]
-    c = attend(np.random.default_rng(sum(new) + d), lens, new, Hq, Hkv, d, 16, weights=True, hint=hint)
+    c = attend(np.random.default_rng(sum(new) + d), lens, new, Hq, Hkv, d, 16, weights=True, hint=hint, wide=wide)
     run_attention(c)
 
 
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("L,B,Hkv", [(1000, 1, 8), (5000, 1, 1), (2500, 2, 2), (333, 5, 3)])
-def test_attention_split_over_ctas(L, B, Hkv):
+def test_attention_split_over_ctas(L, B, Hkv, wide):
     """Long contexts: a (request, kv head) is shared by many CTAs and joined; a run of a CTA spans requests."""
     rng = np.random.default_rng(L)
-    run_attention(attend(rng, [L - 37 * b for b in range(B)], [1] * B, 4 * Hkv, Hkv, 64, 64, weights=True, missing=[(0, 2)]))
+    run_attention(attend(rng, [L - 37 * b for b in range(B)], [1] * B, 4 * Hkv, Hkv, 64, 64, weights=True, missing=[(0, 2)], wide=wide))
 
 
 def test_attention_large_logits_and_scale():
