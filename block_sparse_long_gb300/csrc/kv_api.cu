@@ -225,6 +225,7 @@ int cosa_kv4_attention(const cosa_kv_params* p, const void* q, const int32_t* cu
   if (!(p->sm_scale > 0.0) || !std::isfinite(p->sm_scale)) return COSA_ERR_INVALID_ARG;
   const int64_t dense = static_cast<int64_t>(p->num_q_heads) * p->head_dim;
   if (p->q_stride != 0 && p->q_stride != dense) return COSA_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(p->total_tokens) * (p->num_q_heads / p->num_kv_heads) > INT32_MAX) return COSA_ERR_UNSUPPORTED;
   if (p->total_tokens == 0) return COSA_OK;
   if (!q || !cu_seqlens || !kv4_cache || !page_table || !kv_len || !out) return COSA_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(cu_seqlens, 4) || !aligned(kv4_cache, 16) || !aligned(page_table, 4) ||

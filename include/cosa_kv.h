@@ -155,7 +155,9 @@ int cosa_kv4_load(const cosa_kv_params* p, const void* kv4_cache, const int32_t*
  *   workspace at least cosa_kv4_attention_workspace_size(p, weights != NULL) bytes, 256-byte aligned;
  *             its content on entry does not matter.
  * Logits, softmax and sums are fp32; q and the codes enter the products exactly, and p * s is rounded
- * to bf16 for the second one.  |q| and the scales are below 2^31 (beyond, the result is not finite).
+ * to bf16 for the second one.  |q| and the scales are below 2^31 (beyond, the result is not finite), and values
+ * smaller than 2^-90 lose precision.  Results do not depend on the run; another max_seqlen, max_new_tokens or batch may
+ * round differently.
  */
 size_t cosa_kv4_attention_workspace_size(const cosa_kv_params* p, int with_weights);
 int cosa_kv4_attention(const cosa_kv_params* p, const void* q, const int32_t* cu_seqlens, const void* kv4_cache,

@@ -120,6 +120,39 @@ def test_rope_to_rows_far_positions(T):
         near(got, y, m * 2.0 ** -16)
 
 
+@pytest.mark.parametrize("Hq,Hkv,d,rot,T,inter,paged", [(3, 1, 64, 64, 20001, False, False), (2, 1, 64, 32, 20003, True, True),
+                                                        (5, 1, 64, 64, 12345, False, True), (2, 2, 128, 128, 9999, False, False),
+                                                        (3, 1, 128, 48, 9731, True, True)])
+def test_rope_several_tokens_per_warp(Hq, Hkv, d, rot, T, inter, paged):
+    """Few heads and many tokens: a warp's tokens lie in different requests, empty ones between them, and the last warp has
+    fewer."""
+    lens = [1, 0, 0, 2, 1, 1, 0, 5, 3, 1, 1, 1, 0, T - 16]
+    starts = [(5 * b) % 13 for b in range(len(lens))]
+    c = rope_case(T, lens, starts, Hq, Hkv, d, 128, rot, inter, spare_rows=2)
+    st = new_status()
+    args = dict(q_weight=c["wq"], k_weight=c["wk"], positions=i32(c["pos"]), start=i32(starts), status=st)
+    (yq, mq), (yk, mk) = rope_want(c)
+    if not paged:
+        q_out, k_out = C.cosa_qk_norm_rope(c["p"], c["q"], c["k"], cu_of(lens), c["inv"], **args)
+        ok(st)
+        near(k_out[:c["T"]], yk, mk * 2.0 ** -16)
+    else:
+        kc = torch.zeros(c["p"].num_pages, 128, Hkv, d, dtype=torch.bfloat16, device=DEV)
+        vc = torch.zeros_like(kc)
+        q_out, _ = C.cosa_qk_norm_rope(c["p"], c["q"], c["k"], cu_of(lens), c["inv"], v=c["v"], k_cache=kc, v_cache=vc,
+                                       page_table=i32(c["t"]), **args)
+        ok(st)
+        slots = np.concatenate([np.arange(s, s + n) for s, n in zip(starts, lens)])
+        reqs = np.repeat(np.arange(len(lens)), lens)
+        at = c["t"][reqs, slots // 128].astype(np.int64) * 128 + slots % 128
+        near(ref.to_f64(kc).reshape(-1, Hkv, d)[at], yk, mk * 2.0 ** -16)
+        assert torch.equal(vc.flatten(0, 1)[torch.from_numpy(at).to(DEV)], c["v"][:c["T"]])
+        rest = np.ones(c["p"].num_pages * 128, bool)
+        rest[at] = False
+        assert not bool(kc.flatten(0, 1)[torch.from_numpy(rest).to(DEV)].any())
+    near(q_out[:c["T"]], yq, mq * 2.0 ** -16)
+
+
 def test_rope_positions_default_to_slots_and_both_outputs():
     lens, starts = [4, 9], [30, 2]
     c = rope_case(5, lens, starts, 4, 2, 64, 16, 32, False, spare_rows=0)
@@ -496,6 +529,12 @@ def test_evict_ties_signs_and_special_weights():
 def test_evict_long(n, budget):
     rng = np.random.default_rng(n)
     run_evict(rng, [n, n // 3], 1, 64, 64, budget, 0, 0)
+
+
+def test_evict_keys_that_no_cluster_holds():
+    """More slots than the shared memory of sixteen CTAs has keys for: they are formed again for every pass."""
+    rng = np.random.default_rng(31)
+    run_evict(rng, [270001, 7], 1, 64, 128, 300, 2, 50, missing=[(0, 5), (0, 2000)])
 
 
 def test_evict_reports_contradictions():

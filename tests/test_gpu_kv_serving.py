@@ -330,6 +330,50 @@ def test_shared_prefix_pages_are_read_by_both():
     assert torch.equal(out[0], out[1])
 
 
+def test_pages_beyond_32_bits():
+    """Caches of more than 2^32 bytes whose used pages are the last ones: every call gives what it gives on small caches."""
+    H, d, P, lens = 8, 128, 64, [130, 65]
+    rng = np.random.default_rng(33)
+    near, pages, room = 12, 3, 2
+    far16 = (1 << 32) // (P * H * d * 2) + 100          # bf16 pages: 4 GiB and some
+    far4 = (1 << 32) // (P * H * d * 9 // 8) + 100
+    T = sum(lens)
+    qkv = bf(rng, T, 4 * H + 2 * H, d)
+    inv = torch.from_numpy(1e4 ** (-np.arange(d // 2) / (d // 2))).to(DEV)
+    w = torch.rand(2, H, pages * P, device=DEV)
+    t16, t4 = table(rng, 2, pages, near), table(rng, 2, pages + room, near)
+    q1 = bf(rng, 2, 4 * H, d)
+    got = []
+    for n16, n4 in ((near, near), (far16, far4)):
+        a, b = t16 + (n16 - near), t4 + (n4 - near)
+        src, dst = i32(np.ascontiguousarray(b[:, :pages])), i32(np.ascontiguousarray(b[:, pages:]))
+        kw = dict(num_reqs=2, num_q_heads=4 * H, num_kv_heads=H, head_dim=d, page_size=P, max_seqlen=pages * P, num_pages=n16,
+                  num_kv4_pages=n4, max_pages_per_req=pages, budget=100, sink=1, recent=9, max_dst_pages=room)
+        p = C.make_kv_params(total_tokens=T, **kw)
+        kc, vc = (torch.zeros(n16, P, H, d, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+        cache = torch.zeros(C.kv4_cache_shape(n4, H, P, d), dtype=torch.uint8, device=DEV)
+        st = new_status()
+        q_out, _ = C.cosa_qk_norm_rope(p, qkv[:, :4 * H], qkv[:, 4 * H:5 * H], cu_of(lens), inv, v=qkv[:, 5 * H:], k_cache=kc,
+                                       v_cache=vc, page_table=i32(a), status=st)
+        C.cosa_kv4_store(p, cache, src, kc, vc, src_page_table=i32(a), kv_len=i32(lens), status=st)
+        C.cosa_kv4_store(p, cache, src, qkv[:, 4 * H:5 * H], qkv[:, 5 * H:], cu_seqlens=i32([0, 1, 2]), start=i32([7, 64]), status=st)
+        acc = w.clone()
+        out = C.cosa_kv4_attention(C.make_kv_params(total_tokens=2, **kw), q1, cu_of([1, 1]), cache, src, i32(lens), weights=acc, status=st)
+        new_len, kept, wo = C.cosa_kv4_evict(p, cache, src, i32(lens), w, dst, status=st)
+        kb, vb = torch.zeros_like(kc), torch.zeros_like(vc)
+        C.cosa_kv4_load(C.make_kv_params(**{**kw, "max_seqlen": room * P, "max_pages_per_req": room}), cache, dst, kb, vb,
+                        i32(np.ascontiguousarray(a[:, :room])), kv_len=new_len, status=st)
+        ok(st)
+        got.append([q_out, out, acc, new_len, kept, wo, kc[n16 - near:], vc[n16 - near:], cache[n4 - near:], kb[n16 - near:], vb[n16 - near:]])
+        if n16 > near:
+            assert not bool(kc[:n16 - near].any()) and not bool(cache[:n4 - near].any()) and not bool(vb[:n16 - near].any())
+        got[-1] = [x.clone() for x in got[-1]]
+        del kc, vc, cache, kb, vb
+    for x, y in zip(*got):
+        assert torch.equal(x, y)
+    assert bool(got[0][-1].any()) and bool(got[0][1].any())
+
+
 def test_waits_that_run_out_end_the_kernel():
     """With no copy issued, every wait of the attention runs out: the call ends by itself and reports it, and the next call is
     as good as ever."""

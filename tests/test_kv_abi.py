@@ -132,6 +132,7 @@ def test_attention_refusals(C):
     for kw in (dict(sm_scale=0.0), dict(sm_scale=float("nan")), dict(max_new_tokens=0), dict(total_tokens=-1)):
         assert attend(C, params(C, **kw)) == inv, kw
     assert attend(C, params(C, q_stride=2048)) == uns
+    assert attend(C, params(C, total_tokens=1 << 30, num_q_heads=8, num_kv_heads=1)) == uns        # rows beyond 32 bits
     assert attend(C, params(C), q=None) == inv and attend(C, params(C), q=ODD) == inv and attend(C, params(C), n=None) == inv
     p = params(C)
     size = C.cosa_kv4_attention_workspace_size(p)
