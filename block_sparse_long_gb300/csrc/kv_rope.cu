@@ -8,6 +8,10 @@
 // time, a row on d / 16 lanes.  The angles of a lane are the same in every row, so they are formed once and stay in
 // registers; nothing is shared between warps, and each has three rows per lane in flight.  Where a token has few rows, a
 // warp has two or four tokens, each on its share of the rows.
+//
+// Measured: 128K tokens of 32 + 8 + 8 heads of 128 into pages, 489 us, 3.22 GB at 6.6 TB/s (97 % of the measured copy rate);
+// 64 tokens, 4.8 us, bound by the chain of loads (request, position, frequencies).  Runs of tokens on a warp, with the
+// frequencies kept, took 593 us and more for the 128K tokens (each warp then walks memory alone, in 12 KB pieces).
 #include <cstdint>
 
 #include "cosa_kv.h"

@@ -40,6 +40,9 @@ import torch
 
 from .cosa import COSA_OK, CosaError
 
+# Handle of the current stream of a device (the public way makes a Stream object for it, a microsecond per call).
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
 _HERE = os.path.dirname(os.path.abspath(__file__))
 KV_LIB_PATH = os.path.join(_HERE, "libcosa_kv.so")
 
@@ -200,7 +203,7 @@ class _Call:
     def run(self, name: str, p: CosaKvParams, args, status: Optional[torch.Tensor], stream) -> None:
         if status is not None:
             (status,) = self.dense((status, "status", torch.int32))
-        s = stream.cuda_stream if stream is not None else torch.cuda.current_stream(self.index).cuda_stream
+        s = stream.cuda_stream if stream is not None else _current_stream(self.index)
         f = getattr(_lib or kv_library(), name)
         if torch.cuda.current_device() == self.index:
             rc = f(p, *args, status, s)
