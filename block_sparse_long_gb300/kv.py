@@ -189,6 +189,8 @@ class _Call:
         st = t.stride()
         if shape[0] and (st[2] != 1 or (heads > 1 and st[1] != d)):
             raise ValueError(f"{name}: the heads of a token must be contiguous")
+        if shape[0] > 1 and st[0] < heads * d:
+            raise ValueError(f"{name}: tokens are {st[0]} elements apart, a token has {heads * d}")
         self.on_device(t, name)
         # the stride of a single token says nothing
         return t.data_ptr(), (st[0] if shape[0] > 1 else 0)

@@ -184,6 +184,10 @@ def test_binding_refuses_before_the_library(C):
         c.rows(meta(6, 4, 64, dtype=torch.float16), "q", 4)
     with pytest.raises(ValueError, match="heads of a token"):
         c.rows(meta(4, 6, 64).transpose(0, 1), "q", 4)
+    with pytest.raises(ValueError, match="0 elements apart"):         # the library takes 0 for dense rows
+        c.rows(meta(1, 4, 64).expand(6, 4, 64), "q", 4)
+    with pytest.raises(ValueError, match="CUDA"):
+        c.rows(meta(1, 4, 64).expand(6, 4, 64).contiguous(), "q", 4)
     with pytest.raises(ValueError, match="CUDA"):
         c.rows(meta(6, 8, 64)[:, :4], "q", 4)                         # a slice of a fused projection is fine
     with pytest.raises(ValueError, match="cu_seqlens"):
