@@ -270,6 +270,7 @@ int cosa_kv4_evict(const cosa_kv_params* p, void* kv4_cache, const int32_t* page
   if (static_cast<int64_t>(p->num_reqs) * p->num_kv_heads > INT32_MAX / 16) return COSA_ERR_UNSUPPORTED;
   if (!kv4_cache || !page_table || !kv_len || !weights || !dst_page_table || !new_len || !kept) return COSA_ERR_INVALID_ARG;
   if (weights_out == weights || dst_page_table == page_table) return COSA_ERR_INVALID_ARG;   // moved into other memory
+  if (new_len == kv_len) return COSA_ERR_INVALID_ARG;     // the heads of a request read the one while the other is written
   if (!aligned(kv4_cache, 16) || !aligned(page_table, 4) || !aligned(kv_len, 4) || !aligned(weights, 4) ||
       !aligned(dst_page_table, 4) || !aligned(new_len, 4) || !aligned(kept, 4) || !aligned(weights_out, 4) ||
       !aligned(device_status, 4))

@@ -171,7 +171,7 @@ int cosa_kv4_attention(const cosa_kv_params* p, const void* q, const int32_t* cu
  * of dst_page_table in the same cache.  The source pages are not changed, and no destination page may
  * be a source page of the call.
  *   weights      float32 [num_reqs, Hkv, max_seqlen]
- *   new_len      out: int32 [num_reqs], slots kept (equal for all kv heads of a request)
+ *   new_len      out: int32 [num_reqs], slots kept (equal for all kv heads of a request); not `kv_len` itself
  *   kept         out: int32 [num_reqs, Hkv, budget], the old slot of every new one, then -1
  *   weights_out  out, or NULL: float32 [num_reqs, Hkv, max_seqlen], the kept slots' weights, then 0;
  *                not `weights` itself

@@ -75,8 +75,8 @@ def attend(C, p, q=F, w=None, ws=F, size=1 << 40, n=F):
     return C.kv_library().cosa_kv4_attention(ctypes.byref(p), q, F, F, F, n, F, w, ws, size, None, None)
 
 
-def evict(C, p, w=F, dst=ctypes.c_void_p(8192), wout=None, n=F, kept=F):
-    return C.kv_library().cosa_kv4_evict(ctypes.byref(p), F, F, n, w, dst, F, kept, wout, None, None)
+def evict(C, p, w=F, dst=ctypes.c_void_p(8192), wout=None, n=F, kept=F, new=ctypes.c_void_p(8192)):
+    return C.kv_library().cosa_kv4_evict(ctypes.byref(p), F, F, n, w, dst, new, kept, wout, None, None)
 
 
 def test_parameters_refused_by_every_call(C):
@@ -150,6 +150,7 @@ def test_evict_refusals(C):
     assert evict(C, params(C), w=None) == inv and evict(C, params(C), n=None) == inv and evict(C, params(C), kept=None) == inv
     assert evict(C, params(C), dst=F) == inv          # the source table
     assert evict(C, params(C), wout=F) == inv         # the weights themselves
+    assert evict(C, params(C), new=F) == inv          # the old lengths
 
 
 def meta(*shape, dtype=torch.bfloat16):
