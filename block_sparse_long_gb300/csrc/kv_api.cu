@@ -233,6 +233,7 @@ int cosa_kv4_attention(const cosa_kv_params* p, const void* q, const int32_t* cu
     return COSA_ERR_INVALID_ARG;
   if (!workspace || !aligned(workspace, 256) || workspace_bytes < cosa_kv4_attention_workspace_size(p, weights != nullptr))
     return COSA_ERR_WORKSPACE;
+  if (out == q) return COSA_ERR_INVALID_ARG;      // CTAs that share an item write its rows while others read theirs
   cosa_kv::AttnLaunch L{};
   L.q = static_cast<const uint16_t*>(q);
   L.cu_seqlens = cu_seqlens;

@@ -149,7 +149,7 @@ int cosa_kv4_load(const cosa_kv_params* p, const void* kv4_cache, const int32_t*
  * Attention over the 4-bit cache.  Request b has n = cu_seqlens[b+1] - cu_seqlens[b] query tokens, the
  * last n of its kv_len[b] cache slots: token i attends to slots 0 .. kv_len[b] - n + i that exist.
  * A row that sees nothing gives 0.  Query head h reads kv head h / (Hq / Hkv).
- *   q, out    bf16 [total_tokens, Hq, d], both dense
+ *   q, out    bf16 [total_tokens, Hq, d], both dense; out is not q itself
  *   weights   float32 [num_reqs, Hkv, max_seqlen], or NULL: weights[b, j, s] += the sum, over the request's
  *             query tokens and the heads of kv head j, of the softmax weight of slot s (s < kv_len[b]).
  *   workspace at least cosa_kv4_attention_workspace_size(p, weights != NULL) bytes, 256-byte aligned;

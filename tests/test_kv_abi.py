@@ -71,8 +71,8 @@ def load(C, p, n=F, kc=F, c=F):
     return C.kv_library().cosa_kv4_load(ctypes.byref(p), c, F, None, n, kc, F, F, None, None)
 
 
-def attend(C, p, q=F, w=None, ws=F, size=1 << 40, n=F):
-    return C.kv_library().cosa_kv4_attention(ctypes.byref(p), q, F, F, F, n, F, w, ws, size, None, None)
+def attend(C, p, q=F, w=None, ws=F, size=1 << 40, n=F, out=ctypes.c_void_p(8192)):
+    return C.kv_library().cosa_kv4_attention(ctypes.byref(p), q, F, F, F, n, out, w, ws, size, None, None)
 
 
 def evict(C, p, w=F, dst=ctypes.c_void_p(8192), wout=None, n=F, kept=F, new=ctypes.c_void_p(8192)):
@@ -141,6 +141,7 @@ def test_attention_refusals(C):
     assert attend(C, p, size=size - 1) == wsp and attend(C, p, w=F, size=more - 1) == wsp
     assert attend(C, p, ws=None) == wsp and attend(C, p, ws=ctypes.c_void_p(4096 + 128)) == wsp
     assert attend(C, params(C, total_tokens=0), q=None) == 0
+    assert attend(C, p, out=F) == inv                  # q itself
 
 
 def test_evict_refusals(C):
