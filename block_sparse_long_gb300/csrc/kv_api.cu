@@ -76,7 +76,7 @@ int cosa_qk_norm_rope(const cosa_kv_params* p, const void* q, const void* k, con
   COSA_TRY(check_common(p));
   COSA_TRY(check_tokens(p));
   if (p->rotary_dim < 16 || p->rotary_dim > p->head_dim || p->rotary_dim % 16 != 0) return COSA_ERR_INVALID_ARG;
-  if (!(p->norm_eps >= 0.0) || !std::isfinite(p->norm_eps)) return COSA_ERR_INVALID_ARG;
+  if (p->norm_eps != 0.0 && !(p->norm_eps >= 0x1p-126 && p->norm_eps <= 0x1p126)) return COSA_ERR_INVALID_ARG;
   if (p->total_tokens == 0) return COSA_OK;     // empty tensors have no address
   if (!q || !k || !inv_freq || !cu_seqlens || !q_out) return COSA_ERR_INVALID_ARG;
   const bool paged = k_cache != nullptr;
@@ -222,7 +222,7 @@ int cosa_kv4_attention(const cosa_kv_params* p, const void* q, const int32_t* cu
   COSA_TRY(check_tokens(p));
   COSA_TRY(check_slots(p));
   if (p->num_kv4_pages < 1 || p->max_new_tokens < 1) return COSA_ERR_INVALID_ARG;
-  if (!(p->sm_scale > 0.0) || !std::isfinite(p->sm_scale)) return COSA_ERR_INVALID_ARG;
+  if (!(p->sm_scale >= 0x1p-100 && p->sm_scale <= 0x1p60)) return COSA_ERR_INVALID_ARG;      // fp32 carries it times 2^33
   const int64_t dense = static_cast<int64_t>(p->num_q_heads) * p->head_dim;
   if (p->q_stride != 0 && p->q_stride != dense) return COSA_ERR_UNSUPPORTED;
   if (static_cast<int64_t>(p->total_tokens) * (p->num_q_heads / p->num_kv_heads) > INT32_MAX) return COSA_ERR_UNSUPPORTED;

@@ -95,8 +95,8 @@ typedef struct cosa_kv_params {
   int64_t q_stride;          /* elements between tokens of q, k, v; 0 for dense rows            */
   int64_t k_stride;
   int64_t v_stride;
-  double sm_scale;           /* attention: logit scale, normally 1/sqrt(d)                      */
-  double norm_eps;           /* norm: added to the mean square                                  */
+  double sm_scale;           /* attention: logit scale, normally 1/sqrt(d); 2^-100 to 2^60      */
+  double norm_eps;           /* norm: added to the mean square; 0, or 2^-126 to 2^126           */
 } cosa_kv_params;
 
 /* Library version, (major << 16) | minor. */

@@ -100,7 +100,7 @@ def test_parameters_refused_by_every_call(C):
 def test_rope_refusals(C):
     inv = -1
     for kw in (dict(rotary_dim=0), dict(rotary_dim=24), dict(rotary_dim=144), dict(norm_eps=-1.0), dict(norm_eps=float("nan")),
-               dict(norm_eps=float("inf")), dict(total_tokens=-1), dict(q_stride=1023), dict(q_stride=1028), dict(k_stride=-256),
+               dict(norm_eps=float("inf")), dict(norm_eps=1e-40), dict(norm_eps=1e300), dict(total_tokens=-1), dict(q_stride=1023), dict(q_stride=1028), dict(k_stride=-256),
                dict(v_stride=8), dict(num_pages=0), dict(max_seqlen=0)):
         assert rope(C, params(C, **kw)) == inv, kw
     for kw in (dict(q=None), dict(k=None), dict(v=None), dict(q_out=None), dict(inv=None), dict(cu=None), dict(kc=None),
@@ -129,7 +129,7 @@ def test_store_and_load_refusals(C):
 
 def test_attention_refusals(C):
     inv, uns, wsp = -1, -2, -5
-    for kw in (dict(sm_scale=0.0), dict(sm_scale=float("nan")), dict(max_new_tokens=0), dict(total_tokens=-1)):
+    for kw in (dict(sm_scale=0.0), dict(sm_scale=float("nan")), dict(sm_scale=1e-40), dict(sm_scale=1e30), dict(max_new_tokens=0), dict(total_tokens=-1)):
         assert attend(C, params(C, **kw)) == inv, kw
     assert attend(C, params(C, q_stride=2048)) == uns
     assert attend(C, params(C, total_tokens=1 << 30, num_q_heads=8, num_kv_heads=1)) == uns        # rows beyond 32 bits
