@@ -970,6 +970,7 @@ size_t attn_workspace_bytes(int num_q_heads, int head_dim, int total_tokens, int
 cudaError_t launch_attention(const AttnLaunch& L, cudaStream_t stream) {
   Args a{};
   a.L = L;
+  a.L.max_new_tokens = std::min(L.max_new_tokens, L.total_tokens);
   a.L.scale_log2 = L.scale_log2 * kDown;      // of the logits as the first product leaves them
   a.group = L.num_q_heads / L.num_kv_heads;
   for (a.page_shift = 4; (1 << a.page_shift) < L.page_size;) ++a.page_shift;

@@ -184,13 +184,7 @@ __global__ void __launch_bounds__(kSelectThreads, 3) select_kernel(const EvictLa
       const int r = ctas - 1 - tid;                   // lane 0 has the top share
       const int mine = r >= 0 ? *cluster.map_shared_rank(&sm.share_total, r) : 0;
       const int end = warp_scan(mine);
-      if (pass == 0) {
-        keep = min(L.budget, __shfl_sync(0xffffffffu, end, 31));
-        want = keep;
-      } else {
-        keep = sm.counts[0];
-        want = sm.counts[1];
-      }
+      if (pass == 0) want = keep = min(L.budget, __shfl_sync(0xffffffffu, end, 31));
       const int at = __ffs(__ballot_sync(0xffffffffu, end >= want)) - 1;      // want <= the total: there is one
       const int owner = max(ctas - 1 - at, 0);
       int before = __shfl_sync(0xffffffffu, end - mine, at);

@@ -205,7 +205,12 @@ class _Call:
     def run(self, name: str, p: CosaKvParams, args, status: Optional[torch.Tensor], stream) -> None:
         if status is not None:
             (status,) = self.dense((status, "status", torch.int32))
-        s = stream.cuda_stream if stream is not None else _current_stream(self.index)
+        if stream is None:
+            s = _current_stream(self.index)
+        elif stream.device.index == self.index:
+            s = stream.cuda_stream
+        else:
+            raise ValueError(f"stream is on {stream.device}, the tensors on cuda:{self.index}")
         f = getattr(_lib or kv_library(), name)
         if torch.cuda.current_device() == self.index:
             rc = f(p, *args, status, s)

@@ -404,6 +404,15 @@ def test_attention_split_over_ctas(L, B, Hkv, wide):
     run_attention(attend(rng, [L - 37 * b for b in range(B)], [1] * B, 4 * Hkv, Hkv, 64, 64, weights=True, missing=[(0, 2)], wide=wide))
 
 
+@pytest.mark.parametrize("wide", [False, True])
+def test_attention_any_hint(wide):
+    """A hint far above the tokens that there are is as good as their number."""
+    c = attend(np.random.default_rng(23), [700, 3, 90], [2, 0, 3], 8, 2, 128, 16, weights=True, wide=wide, hint=7)
+    acc0, out = c["acc"].clone(), run_attention(c)
+    acc1, c["acc"], c["p"].max_new_tokens, c["rng"] = c["acc"], acc0, 2 ** 31 - 1, np.random.default_rng(24)
+    assert torch.equal(run_attention(c)[:c["T"]], out[:c["T"]]) and torch.equal(c["acc"], acc1)
+
+
 def test_attention_large_logits_and_scale():
     """A maximum that moves late by hundreds: the running rescale; one slot takes nearly all of the weight."""
     def edit(b, k, v):

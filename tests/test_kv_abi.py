@@ -3,6 +3,7 @@ import ctypes
 import os
 import re
 import subprocess
+import types
 
 import pytest
 import torch
@@ -192,6 +193,9 @@ def test_binding_refuses_before_the_library(C):
         c.rows(meta(1, 4, 64).expand(6, 4, 64).contiguous(), "q", 4)
     with pytest.raises(ValueError, match="CUDA"):
         c.rows(meta(6, 8, 64)[:, :4], "q", 4)                         # a slice of a fused projection is fine
+    c.index = 0
+    with pytest.raises(ValueError, match="stream is on cuda:1"):
+        c.run("cosa_kv4_load", p, (), None, types.SimpleNamespace(device=torch.device("cuda", 1), cuda_stream=0))
     with pytest.raises(ValueError, match="cu_seqlens"):
         C.cosa_kv4_store(p, None, None, None, None)
     with pytest.raises(ValueError, match="kv_len"):
