@@ -1,7 +1,7 @@
 // Attention of the newest tokens of each request over the paged 4-bit cache.
 //
 // Per (request, kv head) the rows are the request's query tokens times the Hq / Hkv query heads of the
-// kv head, eight or sixteen of them at a time:  o = softmax(scale q K^T) V with K = c_k s_k, V = c_v s_v.
+// kv head, eight, sixteen or twenty-four of them at a time:  o = softmax(scale q K^T) V with K = c_k s_k, V = c_v s_v.
 // Both products run on mma.sync m16n8k16 with bf16 operands and fp32 sums, the tokens or the head's values as the
 // sixteen rows and the query rows as the eight columns, so that no part of an instruction is empty for eight rows:
 //   K q^T   A = the codes of 16 tokens, B = q (exact); the codes of one scale group (32 values = two products) are
@@ -19,14 +19,14 @@
 // warps until the end of the CTA's part of a request.
 //
 // Two ways to share the work.  As one list of all (request, kv head, row tile, unit), of which every CTA takes an equal run
-// whatever the lengths are: a CTA that has all of a (request, kv head, row tile) writes its output, otherwise it leaves its
-// maximum, sum and unnormalised output in the workspace (a CTA has at most two unfinished ones, the first and the last of its
-// run) and a second kernel joins them in order.  Or, where warps have few tokens, a cluster to each (request, kv head,
-// row tile), whose CTAs join their parts through distributed shared memory.
+// whatever the lengths are (with an allowance for the ends of its pieces): a CTA that has all of a (request, kv head, row
+// tile) writes its output, otherwise it leaves its maximum, sum and unnormalised output in the workspace (a CTA has at most
+// two unfinished ones, the first and the last of its run) and a second kernel joins them in order.  Or, where warps have
+// few tokens, a cluster to each (request, kv head, row tile), whose CTAs join their parts through distributed shared memory.
 //
-// Measured (32 query and 8 kv heads of 128, one new token): one context of 131072 tokens, 39 us, 151 MB at 3.9 TB/s (57 % of the
+// Measured (32 query and 8 kv heads of 128, one new token): one context of 131072 tokens, 37 us, 151 MB at 4.0 TB/s (59 % of the
 // measured copy rate; 27 us of it stream at 5.6 TB/s, the rest is the first loads, the CTAs' uneven ends and the join);
-// one of 777 tokens, 5.8 us; 48 ragged contexts (417K tokens), two new tokens and weights, 130 us, of which the weights'
+// one of 777 tokens, 5.8 us; 48 ragged contexts (417K tokens), two new tokens and weights, 125 us, of which the weights'
 // logits (107 MB written and read) take about 35.
 
 #include <algorithm>
@@ -49,15 +49,26 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kSms = 152;
 constexpr int kMaxCtas = 3 * kSms;
 constexpr int kMaxRows = 24;     // query rows of a row tile: 8, 16 or 24
-constexpr int kMinUnits = 4;     // units per CTA at least, where a request is shared between CTAs: one per warp
-constexpr int kWholeUnits = 8;   // units of an item that one CTA takes alone
+// Units per CTA at least (with kPiece), where an item is shared between CTAs.  A context of 1500 tokens and 8 kv heads, one of
+// 6000, three of 3000 with 2 kv heads: with 2 units 10.9, 12.4 and 10.1 us, with 4 10.2, 10.9 and 10.6, with 8 11.3, 12.1
+// and 11.8.
+constexpr int kMinUnits = 4;
+// Units of an average item up to which one CTA takes it alone: 16 contexts of 200 tokens in tables for 32K, 7.7 us instead of
+// 11.4 (with none); with 32 units nothing changes for those, and 8 contexts of 250 tokens take 10.8 us instead of 10.7.
+constexpr int kWholeUnits = 8;
+// What the beginning and the end of a CTA's part of an item cost, in units: a CTA whose run crosses into a next item has so many
+// fewer.  With none, 4 and 12: a context of 128K 38.5, 37.5 and 37.1 us, 48 ragged ones with weights 127.9, 126.8 and 123.1 us,
+// one of 1500 tokens 12.3, 11.3 and 10.2 us.
+constexpr int kPiece = 12;
 constexpr int kMaxCluster = 16;  // CTAs of a cluster
 // Tokens per warp up to which items go to clusters.  No list of the batch to make before the first load and no second kernel
 // after the last: a context of 777 tokens takes 5.8 us instead of 11.4, 7 x 14K with 2 kv heads 17.5 instead of 18.7, 15 x 6K
 // 14.3 instead of 21.6; but shares are even only within an item and the clusters may fill the card badly: one of 32K takes
 // 23.8 us instead of 19.0.
 constexpr int kClusterTokens = 256;
-constexpr int kFewItems = 64;     // items up to which the join has a block per row
+// Items up to which the join has a block per row: a context of 128K takes 45.1 us so, 55.4 with a warp per row, 48 ragged ones
+// 153.3 and 135.5.
+constexpr int kFewItems = 64;
 
 // What a CTA leaves about the unfinished (request, kv head, row tile) that begins in its run.
 struct Owner {
@@ -107,7 +118,7 @@ __device__ __forceinline__ int64_t quotient(int64_t x, int64_t y) {
   return x / y;
 }
 
-// The units of the batch in even shares: the first `more` CTAs have one more than `each`.
+// The units of the batch, kPiece added to every item's, in even shares: the first `more` CTAs have one more than `each`.
 struct Shares {
   int64_t units, items, each, more;
   int ctas;
@@ -128,7 +139,7 @@ __device__ __forceinline__ LaneUnits lane_units(const Args& a, int rows, int tok
   if (b0 + lane < a.L.num_reqs) {
     const Request r = request_of(a, b0 + lane, rows, tokens, tell);
     u.items = r.rts * a.L.num_kv_heads;
-    u.own = r.units * u.items;
+    u.own = (r.units + kPiece) * u.items;
   }
   u.end = u.own;
 #pragma unroll
@@ -152,8 +163,8 @@ __device__ __forceinline__ Shares shares_of(const Args& a, int rows, int tokens,
     s.items += n;
   }
   // Short contexts stay whole: with up to kWholeUnits units in the average item, a CTA takes at least one item, and few
-  // parts are left to join.  Else at least a unit for each warp.
-  const int64_t fit = s.units <= kWholeUnits * s.items ? s.items : max(s.items, quotient(s.units, kMinUnits));
+  // parts are left to join.
+  const int64_t fit = s.units <= (kWholeUnits + kPiece) * s.items ? s.items : max(s.items, quotient(s.units, kMinUnits));
   s.ctas = static_cast<int>(max(static_cast<int64_t>(1), min(static_cast<int64_t>(grid), fit)));
   s.each = quotient(s.units, s.ctas);
   s.more = s.units - s.each * s.ctas;
@@ -226,14 +237,15 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
 constexpr float kUp = 79228162514264337593543950336.0f;      // 2^96
 constexpr float kDown = 8589934592.0f;                       // 2^33
 
-// A unit is TP tiles that a warp takes at a time: with eight rows two, whose chains of dependent instructions fill each
-// other's gaps; with more rows one, for the registers.  (One 128K context with TP = 1, 2, 4: 49, 39 and 38 us; 48 ragged
-// ones with weights: 149, 130 and 134 us; a context of 777 tokens: 12, 11.5 and 14.5 us.)
+// A unit is TP tiles that a warp takes at a time: with eight and sixteen rows two, whose chains of dependent instructions fill
+// each other's gaps; with more rows one, for the registers.  (Eight rows, one 128K context with TP = 1, 2, 4: 49, 39 and 38 us;
+// 48 ragged ones with weights: 149, 130 and 134 us; a context of 777 tokens: 12, 11.5 and 14.5 us.  Sixteen rows, 8 contexts
+// of 16K: with TP = 1 on two and on three CTAs an SM 70 and 77 us, with TP = 2 on two 59.)
 template <int NT>
 struct Steps {
-  static constexpr int TP = NT == 1 ? 2 : 1;
-  static constexpr int kStages = NT == 1 ? 2 : 4;      // units in flight per warp
-  static constexpr int kCtas = NT == 1 ? 3 : 2;        // CTAs of an SM: 168 or 255 registers a thread
+  static constexpr int TP = NT <= 2 ? 2 : 1;
+  static constexpr int kStages = NT <= 2 ? 2 : 4;        // units in flight per warp
+  static constexpr int kCtas = NT == 1 ? 3 : 2;          // CTAs of an SM: 168 or 255 registers a thread
   static constexpr int kResident = kCtas * kSms;
 };
 
@@ -316,22 +328,24 @@ __global__ void __launch_bounds__(kThreads, Steps<NT>::kCtas) attention_kernel(c
     } else {
       if (at >= hi) break;
       r = request_of(a, b, kRows, kUnit, false);
-      const int64_t req_units = r.units * r.rts * L.num_kv_heads;
+      const int64_t item_units = r.units + kPiece, req_units = item_units * r.rts * L.num_kv_heads;
       if (at >= req_begin + req_units) {     // the next request that has units
         req_begin += req_units;
         ++b;
         continue;
       }
-      const int64_t item = quotient(at - req_begin, r.units);   // (kv head, row tile)
+      const int64_t item = quotient(at - req_begin, item_units);   // (kv head, row tile)
       h = static_cast<int>(quotient(item, r.rts));
       rt = static_cast<int>(item - h * r.rts);
-      const int64_t item_begin = req_begin + item * r.units;
+      const int64_t item_begin = req_begin + item * item_units;
       item_end = item_begin + r.units;
       t_begin = static_cast<int>(at - item_begin);
       t_end = static_cast<int>(min(hi, item_end) - item_begin);
-      at = item_begin + t_end;
+      at = item_end + kPiece;
+      if (t_begin >= r.units) continue;
     }
-    const int nrows = static_cast<int>(min(static_cast<int64_t>(kRows), static_cast<int64_t>(r.n) * a.group - static_cast<int64_t>(rt) * kRows));
+    const int nrows = static_cast<int>(
+        min(static_cast<int64_t>(kRows), static_cast<int64_t>(r.n) * a.group - static_cast<int64_t>(rt) * kRows));
 
     // ---- the warp's units: t_begin + warp, + kWarps, ... ----
     const int32_t* table = L.page_table + static_cast<size_t>(b) * L.max_pages_per_req;
@@ -368,10 +382,10 @@ __global__ void __launch_bounds__(kThreads, Steps<NT>::kCtas) attention_kernel(c
       if (copies) {
         uint64_t* bar = &sm.full[warp][stage];
         uint8_t* dst = sm.ring[warp].unit[stage];
+        auto page = [&](int u) { return head + static_cast<uint64_t>(static_cast<uint32_t>(phys[u])) * page_bytes; };
         if (one_page) {
           cosa::mbar_arrive_expect_tx(bar, phys[0] >= 0 ? TP * T::kBytes : 0);
-          if (phys[0] >= 0)
-            copy_bulk(dst, head + static_cast<uint64_t>(static_cast<uint32_t>(phys[0])) * page_bytes + (t * TP & (page_tiles - 1)) * T::kBytes, TP * T::kBytes, bar, once);
+          if (phys[0] >= 0) copy_bulk(dst, page(0) + (t * TP & (page_tiles - 1)) * T::kBytes, TP * T::kBytes, bar, once);
         } else {
           int tiles = 0;
 #pragma unroll
@@ -380,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, Steps<NT>::kCtas) attention_kernel(c
 #pragma unroll
           for (int u = 0; u < TP; ++u)
             if (phys[u] >= 0 && (u & (page_tiles - 1)) == 0)
-              copy_bulk(dst + u * T::kBytes, head + static_cast<uint64_t>(static_cast<uint32_t>(phys[u])) * page_bytes, page_tiles * T::kBytes, bar, once);
+              copy_bulk(dst + u * T::kBytes, page(u), page_tiles * T::kBytes, bar, once);
         }
       }
     };
@@ -792,7 +806,8 @@ __global__ void __launch_bounds__(kJoinThreads) combine_wide_kernel(const Args a
 #pragma unroll
       for (int k = 0; k < kDeep; ++k)
         if (part0 + k * kJoin < parts) add(part0 + k * kJoin, o[k]);
-      for (int j = part0 + kDeep * kJoin; j < parts; j += kJoin) add(j, *reinterpret_cast<const float4*>(a.part_o + place(j) * D + 4 * d4));
+      for (int j = part0 + kDeep * kJoin; j < parts; j += kJoin)
+        add(j, *reinterpret_cast<const float4*>(a.part_o + place(j) * D + 4 * d4));
       s_o[part0][d4] = v;
       __syncthreads();
       if (part0 == 0) {
@@ -934,8 +949,8 @@ cudaError_t launch(Args a, cudaStream_t stream) {
     if (e == cudaSuccess) e = launch_after(kernel, dim3(S::kResident), kThreads, smem, stream, 1, a);
     if (e != cudaSuccess) return e;
     if (items <= kFewItems)
-      e = launch_after(combine_wide_kernel<D, WEIGHTS>, dim3(64, static_cast<unsigned>(std::min<int64_t>(8 * NT, rows))), kJoinThreads, 0,
-                       stream, 1, a, S::kResident, 8 * NT);
+      e = launch_after(combine_wide_kernel<D, WEIGHTS>, dim3(64, static_cast<unsigned>(std::min<int64_t>(8 * NT, rows))),
+                       kJoinThreads, 0, stream, 1, a, S::kResident, 8 * NT);
     else
       e = launch_after(combine_kernel<D, WEIGHTS>, dim3(S::kResident), kJoinThreads, 0, stream, 1, a, 8 * NT);
   }
@@ -945,14 +960,14 @@ cudaError_t launch(Args a, cudaStream_t stream) {
   return launch_after(weights_kernel, grid, 256, 0, stream, 1, a);
 }
 
-// Row tiles of 8, 16 or 24 rows: the smallest that has all of a request's rows, else the larger if it leaves fewer tiles
-// (each of which reads the cache again).
+// Row tiles of 8, 16 or 24 rows: the smallest that has all of a request's rows, else of 16, the least time per row.  Tiles of
+// 8 / 16 / 24 rows, 8 contexts of 16K with 8 kv heads: 12 rows 62 / 57 / - us, 16 rows 63 / 59 / - us, 32 rows 113 / 91 / -
+// us, 64 rows 213 / 166 / 203 us; 17 contexts of 4K with 20 rows 53 / 55 / 46 us.
 template <int D, bool WEIGHTS>
 cudaError_t launch(const Args& a, cudaStream_t stream) {
   const int64_t rows = static_cast<int64_t>(a.L.max_new_tokens) * a.group;
   if (rows <= 8) return launch<D, 1, WEIGHTS>(a, stream);
-  if (rows <= 16 || (rows + 23) / 24 == (rows + 15) / 16) return launch<D, 2, WEIGHTS>(a, stream);
-  return launch<D, 3, WEIGHTS>(a, stream);
+  return rows > 16 && rows <= 24 ? launch<D, 3, WEIGHTS>(a, stream) : launch<D, 2, WEIGHTS>(a, stream);
 }
 
 }  // namespace
