@@ -8,12 +8,14 @@
 // memory.  The K-th largest key is found by a radix select, 11 bits at a time from the top: every CTA counts its
 // keys' digits, sums its share of the bins over the cluster through distributed shared memory, and looks the
 // digit up among the sums.  Everything above the K-th key is kept, and the lowest slots among the equal ones; the
-// numbers of both in the earlier CTAs and threads give each kept slot its place.  The move then copies whole rows
-// of codes and scales.
+// numbers of both in the earlier CTAs and warps, and votes within 32 neighbouring keys, give each kept slot its place.  The
+// move then copies whole rows of codes and scales.
 //
-// Work: 8 bytes per slot and 9/4 d bytes per kept slot.  Measured, 131072 slots of 8 heads of 128 to 16384: the select takes 22 us,
-// bound by the latency of its chain (forming the keys 4, a pass 4 to 5, the places 4; sixteen CTAs a head); the move takes
-// 13 us for 38 MB, of which the scattered rows make 50 MB of reads.  One CTA a head, from global memory, took 400 us.
+// Work: 8 bytes per slot and 9/4 d bytes per kept slot.  Measured, 131072 slots of 8 heads of 128 to 16384: 28 us, of which the
+// select takes about 16, bound by the latency of its chain of loads, counts and barriers (sixteen CTAs a head), and the move 13
+// for 38 MB, of which the scattered rows make 50 MB of reads.  24 requests of 16000 to 4000: 80 us, 221 MB moved; the
+// select's 30 us are the issue slots of two CTAs on an SM.  A run of keys per thread instead of per warp took 33 and 90 us; one CTA
+// a head, from global memory, 400 us.
 #include <algorithm>
 #include <cstdint>
 
@@ -86,10 +88,15 @@ struct SelectSmem {
   uint32_t digit;
 };
 
-// HELD: the run's keys fit in shared memory.  They are padded so that threads that walk neighbouring runs of keys do
-// not meet in a bank.
-__host__ __device__ constexpr int padded(int i) { return i + i / 32; }
+// Slots in flight per thread while the keys are formed; the keys' number is rounded up to whole steps (with kMissing).
+constexpr int kDeep = 8;
+__host__ __device__ constexpr int whole_steps(int run) {
+  constexpr int kStep = kDeep * kSelectThreads;
+  return (run + kStep - 1) / kStep * kStep;
+}
+static_assert(kMaxKeys == whole_steps(kMaxKeys), "held keys");
 
+// HELD: the run's keys fit in shared memory.
 template <bool HELD>
 __global__ void __launch_bounds__(kSelectThreads, 3) select_kernel(const EvictLaunch L) {
   extern __shared__ uint32_t s_keys[];
@@ -105,32 +112,38 @@ __global__ void __launch_bounds__(kSelectThreads, 3) select_kernel(const EvictLa
   if (tid == 0 && rank == 0 && h == 0 && n != L.kv_len[b]) cosa::report_status(L.status, cosa::kStatusBadInput);
   const size_t row = static_cast<size_t>(b) * L.num_kv_heads + h;
   const float* w = L.weights + row * L.max_seqlen;
-  // this CTA's run of slots, and this thread's part of it
+  // this CTA's run of slots
   const int run = (n + ctas - 1) / ctas;
-  const int lo = min(n, rank * run), hi = min(n, lo + run);
-  const int per = (run + kSelectThreads - 1) / kSelectThreads;
+  const int lo = min(n, rank * run), len = min(n, lo + run) - lo;
 
   const int32_t* table = L.page_table + static_cast<size_t>(b) * L.max_pages_per_req;
   auto form = [&](int s, int phys, float weight) -> uint32_t {
     if (phys < 0 || phys >= L.num_kv4_pages) return kMissing;
     return s < L.sink || s >= n - L.recent ? kAlways : key_of(weight);
   };
-  auto key = [&](int s) -> uint32_t { return HELD ? s_keys[padded(s - lo)] : form(s, table[s >> L.page_shift], w[s]); };
-  if (HELD) {
-    constexpr int kDeep = 8;          // slots in flight per thread
-    for (int s0 = lo + tid; s0 < hi; s0 += kDeep * kSelectThreads) {
+  // key of slot lo + i; kMissing behind the run
+  auto key = [&](int i) -> uint32_t {
+    if (HELD) return s_keys[i];
+    return i < len ? form(lo + i, table[(lo + i) >> L.page_shift], w[lo + i]) : kMissing;
+  };
+  for (int i = tid; i < kBins; i += kSelectThreads) sm.hist[i] = 0;
+  __syncthreads();
+  if (HELD) {                         // the first pass counts the keys as they are formed
+    for (int i0 = tid; i0 - tid < len; i0 += kDeep * kSelectThreads) {
       float weight[kDeep];
       int phys[kDeep];
 #pragma unroll
       for (int k = 0; k < kDeep; ++k) {
-        const int s = s0 + k * kSelectThreads;
-        weight[k] = s < hi ? w[s] : 0.f;
-        phys[k] = s < hi ? table[s >> L.page_shift] : -1;
+        const int i = i0 + k * kSelectThreads;
+        weight[k] = i < len ? w[lo + i] : 0.f;
+        phys[k] = i < len ? table[(lo + i) >> L.page_shift] : -1;
       }
 #pragma unroll
       for (int k = 0; k < kDeep; ++k) {
-        const int s = s0 + k * kSelectThreads;
-        if (s < hi) s_keys[padded(s - lo)] = form(s, phys[k], weight[k]);
+        const int i = i0 + k * kSelectThreads;
+        const uint32_t x = form(lo + i, phys[k], weight[k]);
+        s_keys[i] = x;
+        if (x != kMissing) atomicAdd(&sm.hist[x >> 21], 1);
       }
     }
   }
@@ -142,11 +155,21 @@ __global__ void __launch_bounds__(kSelectThreads, 3) select_kernel(const EvictLa
 #pragma unroll 1
   for (int pass = 0; pass < 3; ++pass) {
     const int bits = pass == 2 ? 10 : 11, shift = 32 - used - bits;
-    for (int i = tid; i < kBins; i += kSelectThreads) sm.hist[i] = 0;
-    __syncthreads();
-    for (int s = lo + tid; s < hi; s += kSelectThreads) {
-      const uint32_t k = key(s);
-      if (k != kMissing && (pass == 0 || (k >> (shift + bits)) == prefix)) atomicAdd(&sm.hist[(k >> shift) & ((1u << bits) - 1u)], 1);
+    if (pass > 0) {
+      for (int i = tid; i < kBins; i += kSelectThreads) sm.hist[i] = 0;
+      __syncthreads();
+    }
+    if (!HELD || pass > 0) {
+      constexpr int kBatch = 4;       // keys asked for together: a count could be to their address, for all the compiler knows
+      for (int i0 = tid; i0 - tid < len; i0 += kBatch * kSelectThreads) {
+        uint32_t x[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) x[k] = key(i0 + k * kSelectThreads);
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k)
+          if (x[k] != kMissing && (pass == 0 || (x[k] >> (shift + bits)) == prefix))
+            atomicAdd(&sm.hist[(x[k] >> shift) & ((1u << bits) - 1u)], 1);
+      }
     }
     cluster.sync();
     // (the cluster has read the sums of the pass before)
@@ -218,27 +241,29 @@ __global__ void __launch_bounds__(kSelectThreads, 3) select_kernel(const EvictLa
 
   int32_t* kept = L.kept + row * L.budget;
   if (keep > 0) {
-    // thread tid has slots lo + tid * per ..; padded() keeps the threads of a warp apart
-    const int first = lo + tid * per, last = min(hi, first + per);
+    // Neighbouring keys to neighbouring lanes, a run of them to every warp: within 32 keys the places come from votes.
+    const int lane = tid % 32, warp = tid / 32;
+    const int per = (len + kSelectThreads - 1) / kSelectThreads * 32;
+    const int first = warp * per, last = min(len, first + per);
     int above = 0, equal = 0;
-    for (int s = first; s < last; ++s) {
-      const uint32_t k = key(s);
-      above += k > prefix;
-      equal += k == prefix;
+#pragma unroll 4
+    for (int i = first + lane; i - lane < last; i += 32) {
+      const uint32_t x = key(i);
+      above += x > prefix;
+      equal += x == prefix;           // (the K-th key is a slot's: not kMissing)
     }
-    int total_above, total_equal;
-    if (HELD) {                     // both in one word: neither is above kMaxKeys
-      static_assert(kMaxKeys < 32768, "two counts in a word");
-      int total;
-      const int both = block_scan(above | (equal << 16), sm.warp, total);
-      above = both & 0xFFFF;
-      equal = both >> 16;
-      total_above = total & 0xFFFF;
-      total_equal = total >> 16;
-    } else {
-      above = block_scan(above, sm.warp, total_above);
-      equal = block_scan(equal, sm.warp, total_equal);
+    above = __reduce_add_sync(0xffffffffu, above);
+    equal = __reduce_add_sync(0xffffffffu, equal);
+    if (lane == 0) {
+      sm.warp[warp] = above;
+      sm.warp[kWarps + warp] = equal;
     }
+    __syncthreads();
+    above = lane < kWarps ? sm.warp[lane] : 0;
+    equal = lane < kWarps ? sm.warp[kWarps + lane] : 0;
+    const int total_above = __reduce_add_sync(0xffffffffu, above), total_equal = __reduce_add_sync(0xffffffffu, equal);
+    above = __reduce_add_sync(0xffffffffu, lane < warp ? above : 0);
+    equal = __reduce_add_sync(0xffffffffu, lane < warp ? equal : 0);
     if (tid == 0) {
       sm.mine[0] = total_above;
       sm.mine[1] = total_equal;
@@ -246,18 +271,23 @@ __global__ void __launch_bounds__(kSelectThreads, 3) select_kernel(const EvictLa
     cluster.sync();
     // what the CTAs before this one have: a lane for each
     int before_above = 0, before_equal = 0;
-    if (tid % 32 < rank) {
-      const int* c = cluster.map_shared_rank(sm.mine, tid % 32);
+    if (lane < rank) {
+      const int* c = cluster.map_shared_rank(sm.mine, lane);
       before_above = c[0];
       before_equal = c[1];
     }
     above += __reduce_add_sync(0xffffffffu, before_above);
     equal += __reduce_add_sync(0xffffffffu, before_equal);
     cluster.barrier_arrive();       // this thread reads no other CTA's shared memory any more
-    int at = above + min(equal, want);
-    for (int s = first; s < last; ++s) {
-      const uint32_t k = key(s);
-      if (k > prefix || (k == prefix && equal++ < want)) kept[at++] = s;
+    const unsigned before = (1u << lane) - 1u;
+#pragma unroll 4
+    for (int i = first + lane; i - lane < last; i += 32) {
+      const uint32_t x = key(i);
+      const unsigned a = __ballot_sync(0xffffffffu, x > prefix), e = __ballot_sync(0xffffffffu, x == prefix);
+      const int place = equal + __popc(e & before);
+      if (x > prefix || (x == prefix && place < want)) kept[above + __popc(a & before) + min(place, want)] = lo + i;
+      above += __popc(a);
+      equal += __popc(e);
     }
   }
   for (int j = keep + rank * kSelectThreads + tid; j < L.budget; j += ctas * kSelectThreads) kept[j] = -1;
@@ -328,8 +358,10 @@ __global__ void __launch_bounds__(32 * kMoveWarps) move_kernel(const EvictLaunch
     for (int g = 0; g < T::G / 2; ++g) reinterpret_cast<uint32_t*>(dst + base + t * (2 * T::G))[g] = sc[g];
 }
 
-// Clusters of as many CTAs as fill the card, while each still has 2048 slots (with fewer, the pass over the keys costs less
-// than the barriers that sharing it takes), and as many as it takes to hold the keys.
+// Clusters of as many CTAs as fill the card (24 requests of 16K, 8 heads: 192 of one CTA 81 us, 384 of two 80, 768 of four 91),
+// while each still has 2048 slots: with fewer, the pass over the keys costs less than the barriers that sharing it takes (8000
+// slots of 8 heads with 512 / 2048 / 4096 slots a CTA: 18.5 / 14.3 / 16.4 us); and as many as it takes to hold the keys (131072
+// slots: sixteen CTAs a head 53.8 us, eight 57.1).
 cudaError_t launch_select(const EvictLaunch& L, cudaStream_t stream) {
   const int64_t items = static_cast<int64_t>(L.num_reqs) * L.num_kv_heads;
   int ctas = 1;
@@ -340,9 +372,9 @@ cudaError_t launch_select(const EvictLaunch& L, cudaStream_t stream) {
   const bool held = run <= kMaxKeys;
   auto* kernel = held ? select_kernel<true> : select_kernel<false>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  if (e == cudaSuccess && held) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, padded(kMaxKeys) * 4);
+  if (e == cudaSuccess && held) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxKeys * 4);
   if (e != cudaSuccess) return e;
-  return launch_after(kernel, dim3(static_cast<unsigned>(items * ctas)), kSelectThreads, held ? static_cast<size_t>(padded(run)) * 4 : 0,
+  return launch_after(kernel, dim3(static_cast<unsigned>(items * ctas)), kSelectThreads, held ? whole_steps(run) * 4 : 0,
                       stream, ctas, L);
 }
 
