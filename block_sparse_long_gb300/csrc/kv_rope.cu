@@ -9,10 +9,11 @@
 // registers; nothing is shared between warps, and each has three rows per lane in flight.  Where a token has few rows, a
 // warp has two or four tokens, each on its share of the rows.
 //
-// Measured: 128K tokens of 32 + 8 + 8 heads of 128 into pages, 489 us, 3.22 GB at 6.6 TB/s (97 % of the measured copy rate);
-// 64 tokens, 4.8 us, bound by the chain of loads (request, position, frequencies).  Runs of tokens on a warp, with the
+// Measured: 128K tokens of 32 + 8 + 8 heads of 128 into pages, 487 us, 3.22 GB at 6.6 TB/s (97 % of the measured copy rate);
+// 64 tokens, 4.2 us, bound by the chain of loads (request, position, frequencies).  Runs of tokens on a warp, with the
 // frequencies kept, took 593 us and more for the 128K tokens (each warp then walks memory alone, in 12 KB pieces).
 #include <cstdint>
+#include <type_traits>
 
 #include "cosa_kv.h"
 #include "kv_internal.h"
@@ -23,6 +24,39 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kBatch = 3;      // rows per lane in flight
+
+// The angle pos * freq less its whole turns, in half turns (-1 to 1), by the double multiplication.
+__device__ __forceinline__ float half_turns(int64_t pos, double freq) {
+  constexpr double kInvTwoPi = 0.15915494309189533577;
+  const double turns = static_cast<double>(pos) * freq * kInvTwoPi;
+  return 2.0f * static_cast<float>(turns - rint(turns));
+}
+
+// The same in integers, for the frequencies of ordinary rotations, since the SM has few units for doubles: 51K tokens of 3 + 1
+// heads of 64 take 19.9 us instead of 25.6, 64 tokens of 32 + 8 heads 4.2 instead of 4.8.  freq = m 2^(e - 1075) has a
+// significand m of 53 bits; m times round(2^66 / 2 pi), shifted, is the turns of one position in units of 2^-64, whole
+// turns dropped; times the position it is good to 2^-32 of a turn.
+__device__ __forceinline__ bool ordinary(double freq) {       // 2^-36 <= |freq| < 2^10
+  const int e = static_cast<int>(static_cast<uint64_t>(__double_as_longlong(freq)) >> 52) & 0x7FF;
+  return e >= 1023 - 36 && e < 1023 + 10;
+}
+__device__ __forceinline__ uint64_t turn_of(double freq) {
+  const uint64_t bits = static_cast<uint64_t>(__double_as_longlong(freq));
+  const int right = (1077 - (static_cast<int>(bits >> 52) & 0x7FF)) & 127;      // 45 to 90 where it is ordinary
+  const uint64_t m = (bits & ((1ull << 52) - 1)) | (1ull << 52);
+  constexpr uint64_t kTurn = 11743562013128004906ull;
+  const uint64_t hi = __umul64hi(m, kTurn), lo = m * kTurn;
+  const uint64_t turn = right < 64 ? (hi << (64 - right)) | (lo >> right) : hi >> (right - 64);
+  return bits >> 63 ? 0 - turn : turn;
+}
+__device__ __forceinline__ float half_turns(int64_t pos, uint64_t turn) {
+  const uint64_t angle = turn * static_cast<uint64_t>(pos);
+  const bool neg = angle >> 63;
+  const uint64_t size = neg ? 0 - angle : angle;
+  const float hi = __uint2float_rn(static_cast<uint32_t>(size >> 32)), lo = __uint2float_rn(static_cast<uint32_t>(size));
+  const float x = fmaf(hi, 0x1p-31f, lo * 0x1p-63f);
+  return neg ? -x : x;
+}
 
 // Lane l of a row has two chunks of eight values, chosen so that both halves of every rotation pair are in one
 // lane: chunks l and l + rotary_dim / 16 of the rotated part, then what is left of the head two by two.
@@ -87,25 +121,33 @@ __global__ void __launch_bounds__(kThreads, 4) rope_kernel(const RopeLaunch L, c
     page_row = ((static_cast<size_t>(max(phys, 0)) << L.page_shift) + (slot & ((1 << L.page_shift) - 1))) * L.num_kv_heads;
   }
 
-  // The lane's eight angles.  An angle is formed in turns and in 64 bits, less its whole turns; the rest is at most
-  // half a turn, which fp32 holds to 2^-25 of a turn.  (Far positions have angles of 10^5 and more: fp32 would lose
-  // them.)  The rows of the warp share the work: sub-row s forms angles s, s + kRows, ...
+  // The lane's eight angles, formed in 64 bits: far positions have angles of 10^5 and more, which fp32 would lose.  The rows
+  // of the warp share the work: sub-row s forms angles s, s + kRows, ...
   float cs[8], sn[8];
-  const double pos = L.positions ? static_cast<double>(L.positions[t]) : static_cast<double>(slot);
+  const int64_t pos = L.positions ? L.positions[t] : slot;
+  auto angles = [&](auto in_doubles) {            // whether all of them were formed
+    bool all = true;
 #pragma unroll
-  for (int i0 = 0; i0 < 8; i0 += kRows) {
-    const int i = i0 + sub;
-    const int f = L.interleaved ? 4 * (i < 4 ? c0 : c1) + i % 4 : 8 * c0 + i;
-    constexpr double kInvTwoPi = 0.15915494309189533577;
-    const double turns = turned ? pos * L.inv_freq[f] * kInvTwoPi : 0.0;
-    float s, c;
-    sincospif(2.0f * static_cast<float>(turns - rint(turns)), &s, &c);
+    for (int i0 = 0; i0 < 8; i0 += kRows) {
+      const int i = i0 + sub;
+      const double freq = turned ? L.inv_freq[L.interleaved ? 4 * (i < 4 ? c0 : c1) + i % 4 : 8 * c0 + i] : 1.0;
+      float x, s, c;
+      if constexpr (decltype(in_doubles)::value) {
+        x = half_turns(pos, freq);
+      } else {
+        all &= ordinary(freq);
+        x = half_turns(pos, turn_of(freq));
+      }
+      sincospif(turned ? x : 0.f, &s, &c);
 #pragma unroll
-    for (int k = 0; k < kRows; ++k) {
-      cs[i0 + k] = __shfl_sync(kAll, c, (own * kRows + k) * kLanes + l);
-      sn[i0 + k] = __shfl_sync(kAll, s, (own * kRows + k) * kLanes + l);
+      for (int k = 0; k < kRows; ++k) {
+        cs[i0 + k] = __shfl_sync(kAll, c, (own * kRows + k) * kLanes + l);
+        sn[i0 + k] = __shfl_sync(kAll, s, (own * kRows + k) * kLanes + l);
+      }
     }
-  }
+    return all;
+  };
+  if (!__all_sync(kAll, angles(std::false_type{}))) angles(std::true_type{});
 
   auto finish = [&](int row, const uint4& u0, const uint4& u1) {
     const bool query = row < L.num_q_heads, value = row >= L.num_q_heads + L.num_kv_heads;
@@ -189,7 +231,7 @@ cudaError_t launch_rope(const RopeLaunch& L, cudaStream_t stream) {
   int split = 0;       // log2
   while ((2 << split) <= rows / at_once && (static_cast<int64_t>(L.total_tokens) << split) < 152 * 8) ++split;
   // several tokens on a warp, if they fill the card so and a batch still has all of a token's rows: 3 + 1 heads of 64 for 51K
-  // tokens take 25.6 us instead of 44.7
+  // tokens take 25.6 us instead of 44.7 (with the angles in doubles)
   int tokens = 1;
   while (split == 0 && tokens < at_once / 2 && L.total_tokens >= 2 * tokens * kWarps &&
          rows <= at_once / (2 * tokens) * kBatch)

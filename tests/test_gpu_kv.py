@@ -120,6 +120,34 @@ def test_rope_to_rows_far_positions(T):
         near(got, y, m * 2.0 ** -16)
 
 
+@pytest.mark.parametrize("inter", [False, True])
+def test_rope_any_frequency(inter):
+    """Zero, negative, far larger and far smaller frequencies than usual, at both sides of where their arithmetic changes, and
+    negative positions; what is not finite gives NaN.  (Up to 2^53 the double of position * frequency in the reference is
+    exact to half a step: the positions here leave it 2^-20 of a radian at worst, in the 2^-16's shadow.)"""
+    c = rope_case(31, [900], [0], 4, 2, 128, 16, 128, inter, spare_rows=0)
+    rng = np.random.default_rng(32)
+    inv = np.concatenate([[0.0, -0.0, 1.0, -1.0, 0.5, 2.0 ** -36, -2.0 ** -37, 2.0 ** -60, 5e-324, 1024.0, 1023.9999, -1024.5, 5000.0],
+                          (2.0 ** rng.uniform(-40, 11, 51)) * rng.choice([-1, 1], 51)])
+    c["inv"] = torch.from_numpy(inv).to(DEV)
+    c["pos"] = np.concatenate([[0, 1, -1, 2 ** 20, -2 ** 20], rng.integers(-2 ** 20, 2 ** 20, 895)])
+    for scale in (1, 2 ** 10):                                      # with small frequencies, the farthest positions
+        if scale > 1:
+            c["inv"], c["pos"] = c["inv"] / 2 ** 14, np.clip(c["pos"] * 2 ** 11, -2 ** 31, 2 ** 31 - 1)
+        st = new_status()
+        got = C.cosa_qk_norm_rope(c["p"], c["q"], c["k"], cu_of([900]), c["inv"], q_weight=c["wq"], k_weight=c["wk"],
+                                  positions=i32(c["pos"]), status=st)
+        ok(st)
+        for x, (y, m) in zip(got, rope_want(c)):
+            near(x, y, m * 2.0 ** -16)
+    c["inv"][[0, 5, 9]] = torch.tensor([float("nan"), float("inf"), -float("inf")], dtype=torch.float64, device=DEV)
+    got = C.cosa_qk_norm_rope(c["p"], c["q"], c["k"], cu_of([900]), c["inv"], q_weight=c["wq"], k_weight=c["wk"],
+                              positions=i32(c["pos"]))[0]
+    bad = [2 * f + e for f in (0, 5, 9) for e in (0, 1)] if inter else [f + e for f in (0, 5, 9) for e in (0, 64)]
+    assert (torch.isnan(got).sum((0, 1)) == 0).nonzero().flatten().tolist() == [i for i in range(128) if i not in bad]
+    assert torch.isnan(got[..., bad]).all()
+
+
 @pytest.mark.parametrize("Hq,Hkv,d,rot,T,inter,paged", [(3, 1, 64, 64, 20001, False, False), (2, 1, 64, 32, 20003, True, True),
                                                         (5, 1, 64, 64, 12345, False, True), (2, 2, 128, 128, 9999, False, False),
                                                         (3, 1, 128, 48, 9731, True, True)])
