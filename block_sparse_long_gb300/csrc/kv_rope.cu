@@ -10,7 +10,7 @@
 // warp has two or four tokens, each on its share of the rows.
 //
 // Measured: 128K tokens of 32 + 8 + 8 heads of 128 into pages, 487 us, 3.22 GB at 6.6 TB/s (97 % of the measured copy rate);
-// 64 tokens, 4.2 us, bound by the chain of loads (request, position, frequencies).  Runs of tokens on a warp, with the
+// 64 tokens, 3.8 us, bound by the chain of loads (request, position, frequencies).  Runs of tokens on a warp, with the
 // frequencies kept, took 593 us and more for the 128K tokens (each warp then walks memory alone, in 12 KB pieces).
 #include <cstdint>
 #include <type_traits>
@@ -61,8 +61,8 @@ __device__ __forceinline__ float half_turns(int64_t pos, uint64_t turn) {
 // Lane l of a row has two chunks of eight values, chosen so that both halves of every rotation pair are in one
 // lane: chunks l and l + rotary_dim / 16 of the rotated part, then what is left of the head two by two.
 // (Interleaved pairs are neighbours: any choice.)
-template <int D, int TOKENS>
-__global__ void __launch_bounds__(kThreads, 4) rope_kernel(const RopeLaunch L, const int split_log2) {
+template <int D, int TOKENS, int CTAS>
+__global__ void __launch_bounds__(kThreads, CTAS) rope_kernel(const RopeLaunch L, const int split_log2) {
   constexpr int kLanes = D / 16;
   constexpr int kRows = 32 / kLanes / TOKENS;       // rows of a token at a time
   constexpr unsigned kAll = 0xffffffffu;
@@ -238,8 +238,13 @@ cudaError_t launch_rope(const RopeLaunch& L, cudaStream_t stream) {
     tokens *= 2;
   const int64_t warps = ((static_cast<int64_t>(L.total_tokens) + tokens - 1) / tokens) << split;
   const unsigned grid = static_cast<unsigned>((warps * 32 + kThreads - 1) / kThreads);
-  auto* kernel = L.head_dim == 128 ? (tokens == 1 ? rope_kernel<128, 1> : rope_kernel<128, 2>)
-                                   : (tokens == 1 ? rope_kernel<64, 1> : tokens == 2 ? rope_kernel<64, 2> : rope_kernel<64, 4>);
+  // Three CTAs an SM have the registers that four have to save and load; with four more loads are in flight.  With three / four: 64
+  // tokens of 40 heads of 128 take 3.8 / 4.3 us, 1000 6.3 / 6.9, 4000 17.8 / 18.7, but 9.6K of 16 heads of 64 (8 CTAs an SM) 17.2 / 15.8
+  // and 128K of 48 into pages 499 / 487.
+  const bool few = grid <= 6 * 152;
+  auto* kernel = L.head_dim == 128 ? (tokens > 1 ? rope_kernel<128, 2, 4> : few ? rope_kernel<128, 1, 3> : rope_kernel<128, 1, 4>)
+                 : tokens > 1      ? (tokens == 2 ? rope_kernel<64, 2, 4> : rope_kernel<64, 4, 4>)
+                                   : (few ? rope_kernel<64, 1, 3> : rope_kernel<64, 1, 4>);
   return launch_after(kernel, dim3(grid), kThreads, 0, stream, 1, L, split);
 }
 
