@@ -13,8 +13,8 @@
 //
 // Work: 8 bytes per slot and 9/4 d bytes per kept slot.  Measured, 131072 slots of 8 heads of 128 to 16384: 28 us, of which the
 // select takes about 16, bound by the latency of its chain of loads, counts and barriers (sixteen CTAs a head), and the move 13
-// for 38 MB, of which the scattered rows make 50 MB of reads.  24 requests of 16000 to 4000: 80 us, 221 MB moved; the
-// select's 30 us are the issue slots of two CTAs on an SM.  A run of keys per thread instead of per warp took 33 and 90 us; one CTA
+// for 38 MB, of which the scattered rows make 50 MB of reads.  24 requests of 16000 to 4000: 76 us, 221 MB moved; the
+// select's 25 us are a CTA a head, two on some SMs.  A run of keys per thread instead of per warp took 33 and 90 us; one CTA
 // a head, from global memory, 400 us.
 #include <algorithm>
 #include <cstdint>
@@ -172,25 +172,27 @@ __global__ void __launch_bounds__(kSelectThreads, 3) select_kernel(const EvictLa
       }
     }
     cluster.sync();
-    // (the cluster has read the sums of the pass before)
-    for (int i = tid; i < share; i += kSelectThreads) sm.sums[i] = 0;
-    __syncthreads();
-    // This CTA's share of the bins, summed over the cluster: a thread per bin and per four CTAs, whose loads go together.
-    for (int i = tid; i < share * ((ctas + 3) / 4); i += kSelectThreads) {
-      const int bin = i & (share - 1), r0 = i / share * 4;
-      int v[4];
+    if (ctas > 1) {                 // (the cluster has read the sums of the pass before; a CTA alone takes its own bins)
+      for (int i = tid; i < share; i += kSelectThreads) sm.sums[i] = 0;
+      __syncthreads();
+      // This CTA's share of the bins, summed over the cluster: a thread per bin and per four CTAs, whose loads go together.
+      for (int i = tid; i < share * ((ctas + 3) / 4); i += kSelectThreads) {
+        const int bin = i & (share - 1), r0 = i / share * 4;
+        int v[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) v[k] = r0 + k < ctas ? cluster.map_shared_rank(sm.hist, r0 + k)[rank * share + bin] : 0;
-      atomicAdd(&sm.sums[share - 1 - bin], (v[0] + v[1]) + (v[2] + v[3]));
+        for (int k = 0; k < 4; ++k) v[k] = r0 + k < ctas ? cluster.map_shared_rank(sm.hist, r0 + k)[rank * share + bin] : 0;
+        atomicAdd(&sm.sums[share - 1 - bin], (v[0] + v[1]) + (v[2] + v[3]));
+      }
+      __syncthreads();
     }
-    __syncthreads();
     // then, from the top bin down, the number of keys in the bins so far; a thread has up to four neighbouring bins
     {
       const int each = max(1, share / kSelectThreads);
       int v[kBins / kSelectThreads], own = 0, total;
 #pragma unroll
       for (int k = 0; k < kBins / kSelectThreads; ++k) {
-        v[k] = k < each && tid * each < share ? sm.sums[tid * each + k] : 0;
+        const int i = tid * each + k;
+        v[k] = k < each && tid * each < share ? (ctas > 1 ? sm.sums[i] : sm.hist[kBins - 1 - i]) : 0;
         own += v[k];
       }
       int upto = block_scan(own, sm.warp, total);
@@ -358,7 +360,7 @@ __global__ void __launch_bounds__(32 * kMoveWarps) move_kernel(const EvictLaunch
     for (int g = 0; g < T::G / 2; ++g) reinterpret_cast<uint32_t*>(dst + base + t * (2 * T::G))[g] = sc[g];
 }
 
-// Clusters of as many CTAs as fill the card (24 requests of 16K, 8 heads: 192 of one CTA 81 us, 384 of two 80, 768 of four 91),
+// Clusters of as many CTAs as fill the card (24 requests of 16K, 8 heads: 192 of one CTA 76 us, 384 of two 80, 768 of four 91),
 // while each still has 2048 slots: with fewer, the pass over the keys costs less than the barriers that sharing it takes (8000
 // slots of 8 heads with 512 / 2048 / 4096 slots a CTA: 18.5 / 14.3 / 16.4 us); and as many as it takes to hold the keys (131072
 // slots: sixteen CTAs a head 53.8 us, eight 57.1).
