@@ -155,26 +155,31 @@ class _Call:
             raise ValueError(f"{name} is on {t.device}, the other tensors on cuda:{self.index}")
         self.index = index
 
-    def dense(self, *wanted) -> list:
-        """Addresses of contiguous tensors (tensor or None, name, dtype[, key of the size]) of at least the sizes that the
-        parameters imply."""
+    def dense(self, *wanted, **keys) -> list:
+        """Addresses of contiguous tensors (tensor or None, name, dtype) of at least the sizes that the parameters imply
+        (`keys`: names whose size stands under another one)."""
         out, need, index = [], self.need, self.index
-        for t, name, dtype, *key in wanted:
+        if keys:
+            need = {**need, **{name: need[key] for name, key in keys.items()}}
+        for t, name, dtype in wanted:
             if t is None:
                 out.append(None)
                 continue
-            if t.dtype != dtype:
-                raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-            if not t.is_contiguous():
-                raise ValueError(f"{name} must be contiguous")
-            least = need[key[0] if key else name]
-            if t.numel() < least:
-                raise ValueError(f"{name} holds {t.numel()} elements; the parameters need at least {least}")
-            if index is None or t.get_device() != index:
-                self.on_device(t, name)
+            if t.dtype is not dtype or not t.is_contiguous() or t.numel() < need[name] or t.get_device() != index:
+                self.look(t, name, dtype, need[name])
                 index = self.index
             out.append(t.data_ptr())
         return out
+
+    def look(self, t: torch.Tensor, name: str, dtype: torch.dtype, least: int) -> None:
+        """What is wrong with a tensor, unless it is the first one on a device."""
+        if t.dtype != dtype:
+            raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        if t.numel() < least:
+            raise ValueError(f"{name} holds {t.numel()} elements; the parameters need at least {least}")
+        self.on_device(t, name)
 
     def rows(self, t: torch.Tensor, name: str, heads: int):
         """Address and token stride of rows [total_tokens, heads, d], whose tokens may lie apart."""
@@ -270,7 +275,7 @@ def cosa_kv4_store(p: CosaKvParams, kv4_cache: torch.Tensor, page_table: torch.T
     else:
         if kv_len is None:
             raise ValueError("pages need kv_len")
-        (kp, vp), ks, vs = c.dense((k, "k", bf, "k_cache"), (v, "v", bf, "v_cache")), 0, 0
+        (kp, vp), ks, vs = c.dense((k, "k", bf), (v, "v", bf), k="k_cache", v="v_cache"), 0, 0
     args = c.dense((cu_seqlens, "cu_seqlens", i32), (src_page_table, "src_page_table", i32), (start, "start", i32),
                    (kv_len, "kv_len", i32), (kv4_cache, "kv4_cache", torch.uint8), (page_table, "page_table", i32))
     c.run("cosa_kv4_store", c.params(k_stride=ks, v_stride=vs), (kp, vp, *args), status, stream)
@@ -331,7 +336,7 @@ def cosa_kv4_evict(p: CosaKvParams, kv4_cache: torch.Tensor, page_table: torch.T
     if weights_out is None:
         weights_out = c.empty((p.num_reqs, p.num_kv_heads, p.max_seqlen), torch.float32, stream)
     args = c.dense((page_table, "page_table", i32), (kv_len, "kv_len", i32), (weights, "weights", torch.float32),
-                   (dst_page_table, "dst_page_table", i32, "evict_page_table"), (new_len, "new_len", i32), (kept, "kept", i32),
-                   (weights_out, "weights_out", torch.float32))
+                   (dst_page_table, "dst_page_table", i32), (new_len, "new_len", i32), (kept, "kept", i32),
+                   (weights_out, "weights_out", torch.float32), dst_page_table="evict_page_table")
     c.run("cosa_kv4_evict", p, (kv4, *args), status, stream)
     return new_len, kept, weights_out
