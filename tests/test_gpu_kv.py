@@ -150,10 +150,11 @@ def test_rope_any_frequency(inter):
 
 @pytest.mark.parametrize("Hq,Hkv,d,rot,T,inter,paged", [(3, 1, 64, 64, 20001, False, False), (2, 1, 64, 32, 20003, True, True),
                                                         (5, 1, 64, 64, 12345, False, True), (2, 2, 128, 128, 9999, False, False),
-                                                        (3, 1, 128, 48, 9731, True, True)])
+                                                        (3, 1, 128, 48, 9731, True, True), (6, 2, 128, 128, 8001, False, True),
+                                                        (13, 1, 64, 48, 8003, True, False)])
 def test_rope_several_tokens_per_warp(Hq, Hkv, d, rot, T, inter, paged):
-    """Few heads and many tokens: a warp's tokens lie in different requests, empty ones between them, and the last warp has
-    fewer."""
+    """Many tokens, the first five with so few heads that a warp has several: they lie in different requests, empty ones
+    between them, and the last warp has fewer."""
     lens = [1, 0, 0, 2, 1, 1, 0, 5, 3, 1, 1, 1, 0, T - 16]
     starts = [(5 * b) % 13 for b in range(len(lens))]
     c = rope_case(T, lens, starts, Hq, Hkv, d, 128, rot, inter, spare_rows=2)
@@ -403,7 +404,7 @@ def run_attention(c, **kw):
 
 @pytest.mark.parametrize("weights,wide", [(False, False), (True, False), (True, True)])
 @pytest.mark.parametrize("Hq,Hkv,d,P", [(32, 8, 128, 64), (4, 4, 64, 16), (7, 1, 128, 128), (8, 1, 64, 64), (16, 1, 128, 16),
-                                        (12, 4, 128, 32), (24, 1, 64, 32), (9, 3, 64, 128)])
+                                        (12, 4, 128, 32), (24, 1, 64, 32), (9, 3, 64, 128), (20, 1, 128, 32), (33, 1, 128, 64)])
 def test_attention_lengths(Hq, Hkv, d, P, weights, wide):
     """One token per request; lengths from zero to several tiles; pages that end inside the tile; missing pages."""
     lens = [1, 15, 16, 17, 0, 64, 130, 300, 2, P + 1]
