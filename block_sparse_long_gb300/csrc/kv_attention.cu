@@ -211,6 +211,12 @@ __device__ __forceinline__ void copy_bulk(void* dst, const void* src, uint32_t b
                : "memory");
 }
 
+// Waits for a barrier as long as a bounded wait that began at `since` (cosa::global_timer_ns) may take.
+__device__ __forceinline__ void wait_until(uint64_t* bar, uint32_t parity, uint64_t since) {
+  while (!cosa::mbar_try_wait(bar, parity) && cosa::global_timer_ns() - since <= COSA_WAIT_BUDGET_NS) {
+  }
+}
+
 // Cache policy for bytes that a call reads once: they make room in L2 first (the logits, which are read again, stay).
 __device__ __forceinline__ uint64_t read_once() {
   uint64_t policy;
@@ -456,8 +462,14 @@ __global__ void __launch_bounds__(kThreads, Steps<NT>::kCtas) attention_kernel(c
     int stage = 0;
     for (int t = t_first; alive && t < t_end; t += kWarps) {
       if (!cosa::wait_parity_bounded(&sm.full[warp][stage], (phase >> stage) & 1u, nullptr, L.status)) {
-        // give the copies in flight time to land before the CTA's memory is anyone else's; what follows is undefined
-        for (int k = 0; k < kStages; ++k) cosa::wait_parity_bounded(&sm.full[warp][k], (phase >> k) & 1u, nullptr, L.status);
+        // The copies in flight have one more budget together to land before the CTA's memory is anyone else's; what follows is
+        // undefined.  The stage j places ahead has unit t + j kWarps; no copy was made for it if none of its pages exists.
+        const uint64_t since = cosa::global_timer_ns();
+        for (int j = 0; j < kStages; ++j) {
+          const int k = (stage + j) % kStages;
+          if (!a.stall && t + j * kWarps < t_end && ((there >> (k * TP)) & ((1u << TP) - 1u)))
+            wait_until(&sm.full[warp][k], (phase >> k) & 1u, since);
+        }
         alive = false;
       }
       alive = __all_sync(0xffffffffu, alive);
@@ -672,7 +684,8 @@ __global__ void __launch_bounds__(kThreads, Steps<NT>::kCtas) attention_kernel(c
             make_float4(o[x][2 * g][1], o[x][2 * g][3], o[x][2 * g + 1][1], o[x][2 * g + 1][3]);
       }
     }
-    __syncthreads();
+    // a warp whose wait ran out ends the others' work too: their next waits would come one after the other
+    alive = __syncthreads_and(alive);
     // four values of a row whose maximum is M: the output, and what the weights need
     auto finish = [&](int row, int d0, float M, float sum, const float4& v) {
       const int rr = rt * kRows + row;

@@ -22,8 +22,9 @@
  *   - Return value: COSA_OK, or a negative status for an error found on the host before anything is
  *     enqueued, or COSA_ERR_CUDA for a failed launch.  Lengths that contradict `p` are found on the
  *     device: *device_status (an int32 the caller zeroes; may be NULL) becomes COSA_ERR_BAD_INPUT and
- *     the request concerned is treated as empty.  A bounded wait inside the attention kernel that runs out gives
- *     COSA_ERR_DEVICE_TIMEOUT; the outputs are then undefined.
+ *     the request concerned is treated as empty.  A wait inside the attention kernel that runs out after
+ *     2 s gives COSA_ERR_DEVICE_TIMEOUT; the kernel ends once the copies in flight have landed, after 2 s more
+ *     at the latest, and the outputs are then undefined.
  *   - Requests are packed by cu_seqlens int32 [num_reqs + 1] (cu_seqlens[0] = 0, non-decreasing, last
  *     entry <= total_tokens); rows behind the last request are neither read nor written.
  *   - A cache slot is a token's place in its request: slot s of request b is row s % P of logical page

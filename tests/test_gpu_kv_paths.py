@@ -1,0 +1,50 @@
+"""The calls of include/cosa_kv.h on the paths that small shapes do not reach: the attention's list of the whole batch with its
+join, whichever way its waits end, long contexts, many rows."""
+import time
+
+import numpy as np
+import pytest
+import torch
+
+from block_sparse_long_gb300 import cosa, kv as C
+from tests import kv_paths, test_gpu_kv as base
+from tests.kv_helpers import cu_of, i32, new_status, ok
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    from block_sparse_long_gb300 import build
+    build.build()
+
+
+# ---------------------------------------------------------------------------------------------------------------
+# waits that run out
+# ---------------------------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("listed", [False, True])
+@pytest.mark.parametrize("Hq,Hkv", [(8, 1), (16, 1), (24, 1), (30, 1)])
+def test_waits_that_run_out_take_four_seconds_at_most(Hq, Hkv, listed):
+    """Nothing is copied, so the first wait of every warp runs out, 2 s after it began; no copy is in flight to be waited for.
+    The requests have one unit to four, so that in a list the warps of a CTA come to their first wait in different items."""
+    lens = [10, 30, 50, 70, 20, 100, 128, 1, 15]
+    c = base.attend(np.random.default_rng(Hq), lens, [1] * len(lens), Hq, Hkv, 64, 16, spare=0)
+    if listed:
+        kv_paths.widened(c)
+    assert kv_paths.shares_a_list(c["p"]) == listed
+    out = base.run_attention(c).clone()
+    p = C.CosaKvParams.from_buffer_copy(c["p"])
+    p.flags |= C.COSA_KV_FLAG_TEST_STALL
+    st = new_status()
+    args = (c["q"], cu_of(c["new"]), c["cache"], i32(c["t"]), i32(c["lens"]))
+    torch.cuda.synchronize()
+    t0 = time.monotonic()
+    C.cosa_kv4_attention(p, *args, status=st)
+    torch.cuda.synchronize()
+    took = time.monotonic() - t0
+    assert int(st.item()) == cosa.COSA_ERR_DEVICE_TIMEOUT
+    assert 1.9 < took < 4.0, took
+    st = new_status()
+    assert torch.equal(C.cosa_kv4_attention(c["p"], *args, status=st), out)      # and the next call is as good as ever
+    ok(st)
