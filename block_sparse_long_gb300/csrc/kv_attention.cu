@@ -287,6 +287,7 @@ __global__ void __launch_bounds__(kThreads, Steps<NT>::kCtas) attention_kernel(c
 
   wait_for_stream();
   let_next_start();
+  if (blockIdx.x == 0 && tid == 0 && L.cu_seqlens[0] != 0) cosa::report_status(L.status, cosa::kStatusBadInput);
   if (lane == 0) {
 #pragma unroll
     for (int k = 0; k < kStages; ++k) cosa::mbar_init(&sm.full[warp][k], 1);

@@ -48,3 +48,22 @@ def test_waits_that_run_out_take_four_seconds_at_most(Hq, Hkv, listed):
     st = new_status()
     assert torch.equal(C.cosa_kv4_attention(c["p"], *args, status=st), out)      # and the next call is as good as ever
     ok(st)
+
+
+# ---------------------------------------------------------------------------------------------------------------
+# contradictions
+# ---------------------------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("listed", [False, True])
+def test_attention_reports_rows_before_the_first_request(listed):
+    """cu_seqlens that begin behind row 0: reported, the rows in front left as they were, the requests served."""
+    c = base.attend(np.random.default_rng(41), [30, 50, 9], [1, 2, 1], 4, 2, 64, 16, spare=1)
+    if listed:
+        kv_paths.widened(c)
+    assert kv_paths.shares_a_list(c["p"]) == listed
+    want = base.run_attention(c)
+    shifted = torch.cat([c["q"][-1:], c["q"][:-1]])
+    st, out = new_status(), torch.full_like(shifted, 7.0)
+    C.cosa_kv4_attention(c["p"], shifted, cu_of(c["new"]) + 1, c["cache"], i32(c["t"]), i32(c["lens"]), out=out, status=st)
+    torch.cuda.synchronize()
+    assert int(st.item()) == cosa.COSA_ERR_BAD_INPUT
+    assert (out[0] == 7).all() and torch.equal(out[1:], want[:-1])
