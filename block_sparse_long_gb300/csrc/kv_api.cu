@@ -226,13 +226,14 @@ int cosa_kv4_attention(const cosa_kv_params* p, const void* q, const int32_t* cu
   const int64_t dense = static_cast<int64_t>(p->num_q_heads) * p->head_dim;
   if (p->q_stride != 0 && p->q_stride != dense) return COSA_ERR_UNSUPPORTED;
   if (static_cast<int64_t>(p->total_tokens) * (p->num_q_heads / p->num_kv_heads) > INT32_MAX) return COSA_ERR_UNSUPPORTED;
+  const size_t need = cosa_kv4_attention_workspace_size(p, weights != nullptr);
+  if (need == 0) return COSA_ERR_UNSUPPORTED;
   if (p->total_tokens == 0) return COSA_OK;
   if (!q || !cu_seqlens || !kv4_cache || !page_table || !kv_len || !out) return COSA_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(cu_seqlens, 4) || !aligned(kv4_cache, 16) || !aligned(page_table, 4) ||
       !aligned(kv_len, 4) || !aligned(out, 16) || !aligned(weights, 4) || !aligned(device_status, 4))
     return COSA_ERR_INVALID_ARG;
-  if (!workspace || !aligned(workspace, 256) || workspace_bytes < cosa_kv4_attention_workspace_size(p, weights != nullptr))
-    return COSA_ERR_WORKSPACE;
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < need) return COSA_ERR_WORKSPACE;
   if (out == q) return COSA_ERR_INVALID_ARG;      // CTAs that share an item write its rows while others read theirs
   cosa_kv::AttnLaunch L{};
   L.q = static_cast<const uint16_t*>(q);

@@ -986,11 +986,13 @@ cudaError_t launch(const Args& a, cudaStream_t stream) {
 
 }  // namespace
 
+// 0 if it passes 2^61 bytes (the logits of rows and slots that no memory holds).
 size_t attn_workspace_bytes(int num_q_heads, int head_dim, int total_tokens, int max_seqlen, bool with_weights) {
   size_t n = align256(kMaxCtas * sizeof(Owner)) + align256(size_t(kMaxCtas) * 2 * kMaxRows * 2 * 4) +
              align256(size_t(kMaxCtas) * 2 * kMaxRows * head_dim * 4);
   if (with_weights) {
     const size_t rows = static_cast<size_t>(total_tokens) * num_q_heads;
+    if (rows > (size_t(1) << 61) / (logits_pitch(max_seqlen) * 4)) return 0;
     n += align256(rows * 8) + align256(rows * logits_pitch(max_seqlen) * 4);
   }
   return n;
