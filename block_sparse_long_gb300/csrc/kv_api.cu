@@ -8,6 +8,12 @@
 #include "cosa_kv.h"
 #include "kv_internal.h"
 
+#define COSA_TRY(x)                    \
+  do {                                 \
+    const int rc_ = (x);               \
+    if (rc_ != COSA_OK) return rc_;    \
+  } while (0)
+
 namespace {
 
 constexpr int kMaxReqs = 65535;      // grid dimension
@@ -55,13 +61,19 @@ int64_t stride_of(int64_t given, int64_t dense) {
   return given >= dense && given % 8 == 0 && given <= (int64_t(1) << 31) ? given : -1;
 }
 
-int done(cudaError_t e) { return e == cudaSuccess ? COSA_OK : COSA_ERR_CUDA; }
+// What the attention asks of the parameters; the size of its workspace is 0 where it refuses them.
+int check_attention(const cosa_kv_params* p) {
+  COSA_TRY(check_common(p));
+  COSA_TRY(check_tokens(p));
+  COSA_TRY(check_slots(p));
+  if (p->num_kv4_pages < 1 || p->max_new_tokens < 1) return COSA_ERR_INVALID_ARG;
+  if (!(p->sm_scale >= 0x1p-100 && p->sm_scale <= 0x1p60)) return COSA_ERR_INVALID_ARG;      // fp32 carries it times 2^33
+  if (p->q_stride != 0 && p->q_stride != static_cast<int64_t>(p->num_q_heads) * p->head_dim) return COSA_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(p->total_tokens) * (p->num_q_heads / p->num_kv_heads) > INT32_MAX) return COSA_ERR_UNSUPPORTED;
+  return COSA_OK;
+}
 
-#define COSA_TRY(x)                    \
-  do {                                 \
-    const int rc_ = (x);               \
-    if (rc_ != COSA_OK) return rc_;    \
-  } while (0)
+int done(cudaError_t e) { return e == cudaSuccess ? COSA_OK : COSA_ERR_CUDA; }
 
 }  // namespace
 
@@ -211,21 +223,14 @@ int cosa_kv4_load(const cosa_kv_params* p, const void* kv4_cache, const int32_t*
 }
 
 size_t cosa_kv4_attention_workspace_size(const cosa_kv_params* p, int with_weights) {
-  if (check_common(p) != COSA_OK || check_tokens(p) != COSA_OK || check_slots(p) != COSA_OK) return 0;
+  if (check_attention(p) != COSA_OK) return 0;
   return cosa_kv::attn_workspace_bytes(p->num_q_heads, p->head_dim, p->total_tokens, p->max_seqlen, with_weights != 0);
 }
 
 int cosa_kv4_attention(const cosa_kv_params* p, const void* q, const int32_t* cu_seqlens, const void* kv4_cache,
                        const int32_t* page_table, const int32_t* kv_len, void* out, float* weights,
                        void* workspace, size_t workspace_bytes, int32_t* device_status, void* stream) {
-  COSA_TRY(check_common(p));
-  COSA_TRY(check_tokens(p));
-  COSA_TRY(check_slots(p));
-  if (p->num_kv4_pages < 1 || p->max_new_tokens < 1) return COSA_ERR_INVALID_ARG;
-  if (!(p->sm_scale >= 0x1p-100 && p->sm_scale <= 0x1p60)) return COSA_ERR_INVALID_ARG;      // fp32 carries it times 2^33
-  const int64_t dense = static_cast<int64_t>(p->num_q_heads) * p->head_dim;
-  if (p->q_stride != 0 && p->q_stride != dense) return COSA_ERR_UNSUPPORTED;
-  if (static_cast<int64_t>(p->total_tokens) * (p->num_q_heads / p->num_kv_heads) > INT32_MAX) return COSA_ERR_UNSUPPORTED;
+  COSA_TRY(check_attention(p));
   const size_t need = cosa_kv4_attention_workspace_size(p, weights != nullptr);
   if (need == 0) return COSA_ERR_UNSUPPORTED;
   if (p->total_tokens == 0) return COSA_OK;

@@ -154,7 +154,7 @@ int cosa_kv4_load(const cosa_kv_params* p, const void* kv4_cache, const int32_t*
  *   weights   float32 [num_reqs, Hkv, max_seqlen], or NULL: weights[b, j, s] += the sum, over the request's
  *             query tokens and the heads of kv head j, of the softmax weight of slot s (s < kv_len[b]).
  *   workspace at least cosa_kv4_attention_workspace_size(p, weights != NULL) bytes, 256-byte aligned;
- *             its content on entry does not matter.
+ *             its content on entry does not matter.  The size is 0 where the call refuses p.
  * Logits, softmax and sums are fp32; q and the codes enter the products exactly, and p * s is rounded
  * to bf16 for the second one.  |q| and the scales are below 2^31 (beyond, the result is not finite), and values
  * smaller than 2^-90 lose precision.  Results do not depend on the run; another max_seqlen, max_new_tokens or batch may

@@ -26,3 +26,14 @@ def test_workspace_of_more_bytes_than_64_bits_number(C):
     size = C.cosa_kv4_attention_workspace_size(huge(C, total, heads), with_weights=True)
     assert size > total * heads * (1 << 30) * 4
     assert attend(C, huge(C, total, heads), w=F, size=1 << 40) == WORKSPACE
+
+
+def test_no_workspace_for_parameters_that_the_attention_refuses(C):
+    assert C.cosa_kv4_attention_workspace_size(params(C)) > 0
+    for kw in (dict(max_new_tokens=0), dict(num_kv4_pages=0), dict(sm_scale=0.0), dict(sm_scale=float("nan")), dict(sm_scale=1e30),
+               dict(q_stride=2048), dict(total_tokens=-1), dict(max_seqlen=0), dict(max_pages_per_req=15), dict(num_q_heads=7),
+               dict(total_tokens=1 << 30, num_q_heads=8, num_kv_heads=1), dict(flags=2)):
+        p = params(C, **kw)
+        assert attend(C, p) in (INVALID, UNSUPPORTED), kw
+        for weights in (False, True):
+            assert C.cosa_kv4_attention_workspace_size(p, with_weights=weights) == 0, kw
