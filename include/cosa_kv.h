@@ -21,10 +21,13 @@
  *     that can run at the same time need two workspaces.
  *   - Return value: COSA_OK, or a negative status for an error found on the host before anything is
  *     enqueued, or COSA_ERR_CUDA for a failed launch.  Lengths that contradict `p` are found on the
- *     device: *device_status (an int32 the caller zeroes; may be NULL) becomes COSA_ERR_BAD_INPUT and
- *     the request concerned is treated as empty.  A wait inside the attention kernel that runs out after
- *     2 s gives COSA_ERR_DEVICE_TIMEOUT; the kernel ends once the copies in flight have landed, after 2 s more
- *     at the latest, and the outputs are then undefined.
+ *     device: *device_status (an int32 the caller zeroes; may be NULL) becomes COSA_ERR_BAD_INPUT.  The
+ *     attention, the eviction and the calls from pages to pages then treat the request concerned as empty;
+ *     cosa_qk_norm_rope and cosa_kv4_store from rows leave out (write nothing of) the tokens of no request
+ *     and those whose slot is negative or, where a cache is written, not below max_seqlen; the other tokens of
+ *     the request are written.  A wait inside the attention kernel that runs out after 2 s gives
+ *     COSA_ERR_DEVICE_TIMEOUT; the kernel ends once the copies in flight have landed, after 2 s more at the
+ *     latest, and the outputs are then undefined.
  *   - Requests are packed by cu_seqlens int32 [num_reqs + 1] (cu_seqlens[0] = 0, non-decreasing, last
  *     entry <= total_tokens); rows behind the last request are neither read nor written.
  *   - A cache slot is a token's place in its request: slot s of request b is row s % P of logical page

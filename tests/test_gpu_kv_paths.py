@@ -67,3 +67,39 @@ def test_attention_reports_rows_before_the_first_request(listed):
     torch.cuda.synchronize()
     assert int(st.item()) == cosa.COSA_ERR_BAD_INPUT
     assert (out[0] == 7).all() and torch.equal(out[1:], want[:-1])
+
+
+@pytest.mark.parametrize("paged", [False, True])
+@pytest.mark.parametrize("cu,start,dropped,reported", [
+    ([0, 4, 9], [0, 0], [], (True, True)),             # a row more than there are
+    ([0, 4, 8], [0, 13], [7], (True, False)),          # slots 13 to 16 of 16: without caches a slot is only a position
+    ([0, 4, 8], [-2, 0], [0, 1], (True, True)),        # slots from -2
+    ([1, 4, 8], [0, 0], [0], (True, True))])           # a row of no request
+def test_rope_leaves_out_the_tokens_that_do_not_fit(cu, start, dropped, reported, paged):
+    """Contradictions are reported; the tokens concerned are left out, all others of the request are written."""
+    c = base.rope_case(43, [4, 4], [0, 0], 4, 2, 64, 16, 64, False, spare_rows=0)
+    total, rng = c["p"].num_pages, c["rng"]
+    kc, vc = (base.bf(rng, total, 16, 2, 64) for _ in range(2))
+    q_out, k_out = base.bf(rng, 8, 4, 64), base.bf(rng, 8, 2, 64)
+    before = [x.clone() for x in (q_out, k_out, kc, vc)]
+    more = dict(v=c["v"], k_cache=kc, v_cache=vc, page_table=i32(c["t"])) if paged else {}
+    st = new_status()
+    C.cosa_qk_norm_rope(c["p"], c["q"], c["k"], i32(cu), c["inv"], q_weight=c["wq"], k_weight=c["wk"], start=i32(start), q_out=q_out,
+                        k_out=k_out, status=st, **more)
+    torch.cuda.synchronize()
+    if not paged and not reported[1]:
+        dropped = []
+    assert int(st.item()) == (cosa.COSA_ERR_BAD_INPUT if reported[0 if paged else 1] else 0)
+    slots = np.array([t - cu[int(t >= cu[1])] + start[int(t >= cu[1])] for t in range(8)])
+    c["pos"] = np.maximum(slots, 0)
+    (yq, mq), (yk, mk) = base.rope_want(c)
+    kept = [t for t in range(8) if t not in dropped]
+    base.near(q_out[kept], yq[kept], mq[kept] * 2.0 ** -16)
+    base.near(k_out[kept], yk[kept], mk[kept] * 2.0 ** -16)
+    assert torch.equal(q_out[dropped], before[0][dropped]) and torch.equal(k_out[dropped], before[1][dropped])
+    want_k, want_v = before[2], before[3]
+    if paged:
+        for t in kept:
+            page = int(c["t"][int(t >= cu[1]), 0])
+            want_k[page, slots[t]], want_v[page, slots[t]] = k_out[t], c["v"][t]
+    assert torch.equal(kc, want_k) and torch.equal(vc, want_v)
