@@ -32,6 +32,17 @@ def shares_a_list(p) -> bool:
     return not (ctas * n <= resident and tokens <= (512 if 2 * ctas * n >= resident else 256))
 
 
+def parts_of_the_longest(p, lens) -> int:
+    """CTAs that share the longest request's first item in a list, at least (equal shares of the items' units, each item with 12
+    more than its own; a CTA has four units or more)."""
+    nt = row_groups(p)
+    unit, resident = (32 if nt <= 2 else 16), SMS * (3 if nt == 1 else 2)
+    own = [max(1, -(-n // unit)) for n in lens]
+    total = sum(u + 12 for u in own) * p.num_kv_heads
+    each = -(-total // max(1, min(resident, total // 4)))
+    return max(own) // each
+
+
 def widened(c, tokens=40000):
     """A case of tests/test_gpu_kv.py's attend() with page tables for `tokens`, more than any cluster takes."""
     p, P = c["p"], c["P"]

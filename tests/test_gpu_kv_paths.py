@@ -7,8 +7,8 @@ import pytest
 import torch
 
 from block_sparse_long_gb300 import cosa, kv as C
-from tests import kv_paths, test_gpu_kv as base
-from tests.kv_helpers import cu_of, i32, new_status, ok
+from tests import kv_bulk, kv_paths, kv_reference as ref, test_gpu_kv as base
+from tests.kv_helpers import bf, cu_of, i32, new_status, ok
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -103,3 +103,133 @@ def test_rope_leaves_out_the_tokens_that_do_not_fit(cu, start, dropped, reported
             page = int(c["t"][int(t >= cu[1]), 0])
             want_k[page, slots[t]], want_v[page, slots[t]] = k_out[t], c["v"][t]
     assert torch.equal(kc, want_k) and torch.equal(vc, want_v)
+
+
+# ---------------------------------------------------------------------------------------------------------------
+# the list of the whole batch and its join
+# ---------------------------------------------------------------------------------------------------------------
+def attend_listed(rng, lens, new, Hq, Hkv, d, P, *, weights=False, missing=(), edit=None, hint=None, scale=None, q_scale=1.5, spare=2):
+    """A case for base.run_attention whose batch is shared as one list."""
+    cache, t, ks, vs = kv_bulk.packed(rng, lens, Hkv, P, d, missing=missing, edit=edit)
+    T, pages = sum(new), t.shape[1]
+    p = C.make_kv_params(num_reqs=len(lens), num_q_heads=Hq, num_kv_heads=Hkv, head_dim=d, page_size=P, total_tokens=T + spare,
+                         max_seqlen=pages * P, num_kv4_pages=cache.shape[0], max_pages_per_req=pages,
+                         max_new_tokens=max(1, max(new)) if hint is None else hint, sm_scale=scale)
+    acc = torch.from_numpy(rng.random((len(lens), Hkv, pages * P)).astype(np.float32)).to(DEV) if weights else None
+    c = dict(p=p, q=bf(rng, T + spare, Hq, d, scale=q_scale), cache=cache, t=t, ks=ks, vs=vs, lens=lens, new=new, acc=acc, T=T, P=P, rng=rng)
+    return kv_paths.widened(c, max(40000, max(lens)))
+
+
+@pytest.mark.parametrize("weights", [False, True])
+@pytest.mark.parametrize("Hq,Hkv,d,P", [(32, 8, 128, 64), (4, 4, 64, 16), (7, 1, 128, 128), (8, 1, 64, 64), (12, 4, 128, 32), (9, 3, 64, 128),
+                                        (16, 1, 128, 16), (16, 1, 64, 32), (9, 1, 64, 128), (24, 1, 64, 32), (20, 1, 128, 32),
+                                        (24, 1, 128, 128), (33, 1, 128, 64), (40, 1, 64, 16)])
+def test_listed_lengths(Hq, Hkv, d, P, weights):
+    """One token per request; lengths from zero to several tiles; pages that end inside the tile; missing pages."""
+    lens = [1, 15, 16, 17, 0, 64, 130, 300, 2, P + 1]
+    base.run_attention(attend_listed(np.random.default_rng(Hq * 7 + d + P), lens, [1] * len(lens), Hq, Hkv, d, P, weights=weights,
+                                     missing=[(7, 0), (6, min(1, 130 // P)), (2, 0)]))
+
+
+@pytest.mark.parametrize("weights", [False, True])
+@pytest.mark.parametrize("Hq,Hkv,d,new,hint", [(8, 2, 128, [3, 0, 1, 5, 2], None), (8, 2, 128, [3, 0, 1, 5, 2], 1), (4, 4, 64, [9, 1, 0, 20, 2], None),
+                                               (16, 2, 64, [2, 0, 1, 3, 2], 2), (6, 2, 128, [40, 0, 1, 2, 2], 100), (5, 5, 128, [8, 8, 8, 8, 2], 3),
+                                               (7, 1, 64, [3, 1, 1, 2, 0], None), (6, 1, 128, [4, 0, 1, 8, 1], None), (12, 1, 128, [2, 2, 2, 2, 2], 1)])
+def test_listed_several_tokens(Hq, Hkv, d, new, hint, weights):
+    """Causal at the end; several row tiles; requests without queries; queries that see nothing; hints too small and too large."""
+    base.run_attention(attend_listed(np.random.default_rng(sum(new) + d), [100, 50, 1, 7, 1], new, Hq, Hkv, d, 16, weights=weights, hint=hint))
+
+
+@pytest.mark.parametrize("weights", [False, True])
+@pytest.mark.parametrize("Hq,Hkv,d,lens,new", [
+    (32, 8, 64, [3000, 1, 0, 700, 33, 2048, 5, 900, 260], 1), (16, 8, 128, [1500, 64, 1, 31, 32, 700, 0, 90, 400, 17], 1),
+    (36, 4, 64, [2000 - 111 * b for b in range(17)], 1), (20, 4, 64, [1200 - 60 * b for b in range(18)], 4),
+    (8, 8, 128, [5] * 70, 1)])
+def test_listed_many_items(Hq, Hkv, d, lens, new, weights):
+    """More than 64 items: the join with a warp per row; CTAs' runs end inside items and span them."""
+    c = attend_listed(np.random.default_rng(len(lens) + d), lens, [min(new, n) for n in lens], Hq, Hkv, d, 64, weights=weights,
+                      missing=[(0, 3)] if max(lens) > 256 else [])
+    assert kv_paths.items(c["p"]) > 64
+    base.run_attention(c)
+
+
+@pytest.mark.parametrize("weights", [False, True])
+@pytest.mark.parametrize("Hq,Hkv,d,lens", [(4, 1, 64, [25001]), (8, 1, 128, [12001]), (5, 1, 64, [70001]), (12, 1, 64, [40007]),
+                                           (20, 1, 128, [12345]), (6, 2, 128, [31000, 4])])
+def test_listed_long_contexts(Hq, Hkv, d, lens, weights):
+    """Few items of very many parts: a thread of the join has more parts of a row than it asks for at once (128 of them for heads of
+    64, 64 for 128)."""
+    c = attend_listed(np.random.default_rng(lens[0]), lens, [1] * len(lens), Hq, Hkv, d, 128, weights=weights, missing=[(0, 2), (0, 40)])
+    assert kv_paths.items(c["p"]) <= 64 and kv_paths.parts_of_the_longest(c["p"], lens) > (128 if d == 64 else 64)
+    base.run_attention(c)
+
+
+def test_listed_any_hint():
+    c = attend_listed(np.random.default_rng(23), [700, 3, 90], [2, 0, 3], 8, 2, 128, 16, weights=True, hint=7)
+    acc0, out = c["acc"].clone(), base.run_attention(c)
+    acc1, c["acc"], c["p"].max_new_tokens, c["rng"] = c["acc"], acc0, 2 ** 31 - 1, np.random.default_rng(24)
+    assert kv_paths.shares_a_list(c["p"])
+    assert torch.equal(base.run_attention(c)[:c["T"]], out[:c["T"]]) and torch.equal(c["acc"], acc1)
+
+
+def test_listed_large_logits_and_scale():
+    """A maximum that moves late by hundreds, within a CTA's part and from part to part."""
+    def edit(b, k, v):
+        for s in range(0, len(k), 97):
+            k[s] = ref.bf16(k[s] * (1 + s / 100))
+    base.run_attention(attend_listed(np.random.default_rng(11), [1700, 190], [1, 2], 4, 2, 128, 16, weights=True, edit=edit, scale=0.02, q_scale=4.0))
+
+
+def test_listed_keeps_nan_where_it_is_seen():
+    """A NaN group of a key, of a value, in one part of many: rows that see the slot give NaN (for a value, in its 32
+    channels), the others do not."""
+    def edit(b, k, v):
+        if b == 0:
+            k[1010, 0, 3] = np.nan
+        if b == 1:
+            v[1499, 1, 40] = np.inf
+    c = attend_listed(np.random.default_rng(12), [1500, 1500, 1500], [1, 2, 1], 4, 2, 64, 16, edit=edit)
+    out = torch.zeros_like(c["q"])
+    C.cosa_kv4_attention(c["p"], c["q"], cu_of(c["new"]), c["cache"], i32(c["t"]), i32(c["lens"]), out=out)
+    o = ref.to_f64(out)
+    assert np.isnan(o[0, :2]).all() and np.isfinite(o[0, 2:]).all()
+    assert np.isfinite(o[1]).all()                                               # request 1's first token does not see slot 1499
+    assert np.isfinite(o[2, :2]).all() and np.isfinite(o[2, 2:, :32]).all() and np.isnan(o[2, 2:, 32:]).all()
+    assert np.isfinite(o[3]).all()
+
+
+def test_listed_reports_contradictions():
+    """The request concerned is empty (its rows stay as they were), the others are served; by other CTAs than without it, which
+    may round differently: the reference decides."""
+    c = attend_listed(np.random.default_rng(13), [900, 30, 700], [1, 1, 1], 2, 1, 64, 16, spare=0)
+    top, q = c["p"].max_seqlen, ref.to_f64(c["q"])
+    for cu, lens, served in (([0, 1, 2, 3], [900, top + 1, 700], (0, 2)), ([0, 1, 2, 3], [900, -1, 700], (0, 2)),
+                             ([0, 1, 2, 4], [900, 30, 700], (0, 1)), ([0, 1, 4, 3], [900, 30, 700], (0,))):
+        st, out = new_status(), torch.full_like(c["q"], 7.0)
+        C.cosa_kv4_attention(c["p"], c["q"], i32(cu), c["cache"], i32(c["t"]), i32(lens), out=out, status=st)
+        torch.cuda.synchronize()
+        assert int(st.item()) == cosa.COSA_ERR_BAD_INPUT
+        for b in range(3):
+            if b not in served:
+                assert (out[b] == 7).all()
+                continue
+            k, v = c["ks"][b], c["vs"][b]
+            want, mag, _ = ref.attention(q[b:b + 1], k, v, np.ones(len(k), bool), c["p"].sm_scale)
+            base.near(out[b:b + 1], want, mag * (2.0 ** -8 + 2.0 ** -17 + 2.1 * ref.logit_error(q[b:b + 1], k, c["p"].sm_scale)))
+
+
+@pytest.mark.parametrize("weights", [False, True])
+@pytest.mark.parametrize("lens", [[900, 40, 333], [200 + 37 * b for b in range(20)]])
+def test_listed_whatever_the_workspace_holds(lens, weights):
+    """Owners and parts lie in the workspace: its content on entry, NaN and an earlier call's among them, changes nothing."""
+    new = [1 + b % 2 for b in range(len(lens))]
+    c = attend_listed(np.random.default_rng(14), lens, new, 8, 4, 128, 64, weights=weights)
+    ws = torch.empty(C.cosa_kv4_attention_workspace_size(c["p"], weights), dtype=torch.uint8, device=DEV)
+    args, acc0, outs = (c["p"], c["q"], cu_of(new), c["cache"], i32(c["t"]), i32(lens)), c["acc"], []
+    for fill in (0, 255, 127, 7, None):                                          # None: as the call before it left it
+        if fill is not None:
+            ws.fill_(fill)
+        acc = acc0.clone() if weights else None
+        outs.append((C.cosa_kv4_attention(*args, weights=acc, workspace=ws)[:c["T"]].clone(), acc))
+    for o, a in outs[1:]:
+        assert torch.equal(o, outs[0][0]) and (not weights or torch.equal(a, outs[0][1]))
