@@ -233,3 +233,90 @@ def test_listed_whatever_the_workspace_holds(lens, weights):
         outs.append((C.cosa_kv4_attention(*args, weights=acc, workspace=ws)[:c["T"]].clone(), acc))
     for o, a in outs[1:]:
         assert torch.equal(o, outs[0][0]) and (not weights or torch.equal(a, outs[0][1]))
+
+
+# ---------------------------------------------------------------------------------------------------------------
+# many tokens into the cache and back
+# ---------------------------------------------------------------------------------------------------------------
+def placed(t, lens, starts, P, total):
+    """(physical page, row, token) of the tokens whose pages exist, requests after each other."""
+    b = np.repeat(np.arange(len(lens)), lens)
+    slot = np.concatenate([np.arange(s, s + n) for s, n in zip(starts, lens)])
+    phys = t[b, slot // P].astype(np.int64)
+    there = np.nonzero((phys >= 0) & (phys < total))[0]
+    return phys[there], (slot % P)[there], there
+
+
+@pytest.mark.parametrize("H,d,P", [(8, 128, 64), (9, 64, 16), (2, 64, 32), (3, 128, 128), (1, 64, 128), (12, 128, 16)])
+def test_bulk_rows(H, d, P):
+    """More rows than go one to a CTA: CTAs of 8 or 16 tokens that cross requests (some of them empty) and pages, a last CTA with
+    fewer, rows behind the last request."""
+    rng = np.random.default_rng(H + d + P)
+    lens, starts = [1, 0, 5, 1013, 0, 0, 2, 1, 1, 1, 700, 3, 0, 411, 9], [0, 4, P - 2, 7, 1, 0, 2 * P + 1, 3, 3, 0, P, 1, 0, 15, 16]
+    T, pages = sum(lens), max(-(-(s + n) // P) for s, n in zip(starts, lens))
+    assert T % 16 and T % 8 and T > 8 * 152
+    kv = base.bf(rng, T + 3, 2 * H * d + 8)
+    k, v = kv[:, :H * d].unflatten(1, (H, d)), kv[:, H * d:2 * H * d].unflatten(1, (H, d))
+    base.special(rng, k[30:])
+    base.special(rng, v[900:])
+    total = len(lens) * pages + 1
+    t = base.table(rng, len(lens), pages, total, missing=[(3, 1), (10, 2), (6, 2)])
+    cache = base.noise_cache(rng, total, H, P, d)
+    want = cache.cpu().numpy().copy()
+    p = C.make_kv_params(num_reqs=len(lens), num_q_heads=H, num_kv_heads=H, head_dim=d, page_size=P, total_tokens=T + 3,
+                         max_seqlen=pages * P, num_kv4_pages=total, max_pages_per_req=pages)
+    st = new_status()
+    C.cosa_kv4_store(p, cache, i32(t), k, v, cu_seqlens=cu_of(lens), start=i32(starts), status=st)
+    ok(st)
+    phys, row, tok = placed(t, lens, starts, P, total)
+    kv_bulk.put(want, phys, row, ref.to_f64(k)[tok], ref.to_f64(v)[tok])
+    assert np.array_equal(cache.cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("H,d,P,B,long", [(8, 64, 64, 64, 1500), (2, 128, 128, 64, 3000), (3, 64, 16, 64, 4001), (1, 64, 16, 5000, 60), (9, 64, 32, 1, 45000)])
+def test_pages_of_requests_longer_than_a_turn_of_their_CTAs(H, d, P, B, long):
+    """A request's CTAs (4864 over the batch) take up to 16 slots each at a time and come round again: store and load, from a
+    start inside a tile; pages without a counterpart on either side."""
+    tokens, most = (8 if H >= 8 else 16), max(1, 32 * 152 // B)
+    assert long - 37 > tokens * most
+    rng = np.random.default_rng(H + d + P + B)
+    ends = [long] + [int(n) for n in rng.integers(0, min(long, 40) + 1, B - 1)]
+    starts = [37] + [int(n) for n in rng.integers(0, 20, B - 1)]
+    lens = [max(0, e - s) for s, e in zip(starts, ends)]
+    pages = -(-long // P)
+    # the long request's pages, and one or three for each other: the rest of the tables points nowhere
+    few = min(pages, -(-40 // P))
+    total = pages + (B - 1) * few + 2
+    def tables():
+        perm = rng.permutation(total).astype(np.int32)
+        t = np.full((B, pages), -1, np.int32)
+        t[0], t[1:, :few] = perm[:pages], perm[pages:pages + (B - 1) * few].reshape(B - 1, few)
+        t[0, int(rng.integers(1, pages))] = total + 5
+        return t
+    t4, t16 = tables(), tables()
+    k, v = base.bf(rng, total, P, H, d), base.bf(rng, total, P, H, d)
+    base.special(rng, k[:, 3])
+    cache = base.noise_cache(rng, total, H, P, d)
+    want = cache.cpu().numpy().copy()
+    p = C.make_kv_params(num_reqs=B, num_q_heads=H, num_kv_heads=H, head_dim=d, page_size=P, max_seqlen=pages * P, num_pages=total,
+                         num_kv4_pages=total, max_pages_per_req=pages)
+    st = new_status()
+    C.cosa_kv4_store(p, cache, i32(t4), k, v, src_page_table=i32(t16), start=i32(starts), kv_len=i32(ends), status=st)
+    ok(st)
+    b = np.repeat(np.arange(B), lens)
+    slot = np.concatenate([np.arange(s, s + n) for s, n in zip(starts, lens)])
+    a, z = t16[b, slot // P].astype(np.int64), t4[b, slot // P].astype(np.int64)
+    both = (a >= 0) & (a < total) & (z >= 0) & (z < total)
+    a, z, row = a[both], z[both], (slot % P)[both]
+    assert both.sum() > long // 2 and not both.all()
+    kv_bulk.put(want, z, row, ref.to_f64(k)[a, row], ref.to_f64(v)[a, row])
+    assert np.array_equal(cache.cpu().numpy(), want)
+
+    # and back into other contents of the same pages
+    kb, vb = base.bf(rng, total, P, H, d), base.bf(rng, total, P, H, d)
+    want_k, want_v = ref.to_f64(kb), ref.to_f64(vb)
+    C.cosa_kv4_load(p, cache, i32(t4), kb, vb, i32(t16), kv_len=i32(ends), start=i32(starts), status=st)
+    ok(st)
+    x, y = kv_bulk.get(want, z, row, d)
+    want_k[a, row], want_v[a, row] = ref.bf16(x), ref.bf16(y)
+    assert np.array_equal(ref.to_f64(kb), want_k, equal_nan=True) and np.array_equal(ref.to_f64(vb), want_v, equal_nan=True)
