@@ -320,3 +320,42 @@ def test_pages_of_requests_longer_than_a_turn_of_their_CTAs(H, d, P, B, long):
     x, y = kv_bulk.get(want, z, row, d)
     want_k[a, row], want_v[a, row] = ref.bf16(x), ref.bf16(y)
     assert np.array_equal(ref.to_f64(kb), want_k, equal_nan=True) and np.array_equal(ref.to_f64(vb), want_v, equal_nan=True)
+
+
+# ---------------------------------------------------------------------------------------------------------------
+# memory that the binding allocates
+# ---------------------------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("which", ["rope", "attention", "attention with weights", "evict"])
+def test_allocated_memory_belongs_to_the_streams_pool(monkeypatch, which):
+    """What the binding allocates for a call on a given stream is that stream's memory: freed at once while the call still waits,
+    none of it is handed out to the current stream."""
+    c = attend_listed(np.random.default_rng(51), [700, 90], [1, 1], 8, 2, 64, 16, weights=which.endswith("weights"), spare=0)
+    p, inv = c["p"], torch.from_numpy(1e4 ** (-np.arange(32) / 32)).to(DEV)
+    p.budget, p.max_dst_pages = 16, 1
+    cu, t, lens, k = cu_of([1, 1]), i32(c["t"]), i32(c["lens"]), bf(c["rng"], 2, 2, 64)
+    room, few = i32(np.setdiff1d(np.arange(c["cache"].shape[0]), c["t"])[:2].reshape(2, 1)), i32([8, 9])
+    w = torch.rand(2, 2, p.max_seqlen, device=DEV)
+    call = {"rope": lambda st: C.cosa_qk_norm_rope(p, c["q"], k, cu, inv, stream=st),
+            "evict": lambda st: C.cosa_kv4_evict(p, c["cache"], t, few, w, room, stream=st)}.get(
+                which, lambda st: C.cosa_kv4_attention(p, c["q"], cu, c["cache"], t, lens, weights=c["acc"], stream=st))
+    call(None)                                # loads the kernels
+    blocks, empty = [], C._Call.empty
+
+    def recorded(self, shape, dtype, stream):
+        got = empty(self, shape, dtype, stream)
+        blocks.append((got.data_ptr(), got.shape, got.dtype))
+        return got
+
+    monkeypatch.setattr(C._Call, "empty", recorded)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(200_000_000)        # the stream is busy: the call waits
+    call(side)                                # what it returns is let go
+    again = [torch.empty(shape, dtype=dtype, device=DEV) for _, shape, dtype in blocks for _ in range(3)]
+    busy = not side.query()
+    torch.cuda.synchronize()
+    assert busy, "the stream ended too soon for the check to mean anything"
+    assert len(blocks) == {"rope": 2, "evict": 3}.get(which, 2)
+    assert not {a for a, _, _ in blocks} & {x.data_ptr() for x in again}
