@@ -287,7 +287,6 @@ __global__ void __launch_bounds__(kThreads, Steps<NT>::kCtas) attention_kernel(c
 
   wait_for_stream();
   let_next_start();
-  if (blockIdx.x == 0 && tid == 0 && L.cu_seqlens[0] != 0) cosa::report_status(L.status, cosa::kStatusBadInput);
   if (lane == 0) {
 #pragma unroll
     for (int k = 0; k < kStages; ++k) cosa::mbar_init(&sm.full[warp][k], 1);
@@ -315,10 +314,12 @@ __global__ void __launch_bounds__(kThreads, Steps<NT>::kCtas) attention_kernel(c
     h = item / a.row_tiles % L.num_kv_heads;
     b = item / a.row_tiles / L.num_kv_heads;
     r = request_of(a, b, kRows, kUnit, rank == 0 && h == 0 && rt == 0 && tid == 0);
+    if (me == 0 && tid == 0 && r.tok0 != 0) cosa::report_status(L.status, cosa::kStatusBadInput);
     t_begin = static_cast<int>(r.units * rank / ctas);
     t_end = static_cast<int>(r.units * (rank + 1) / ctas);
   } else {
     LaneUnits first;
+    if (me == 0 && tid == 0 && L.cu_seqlens[0] != 0) cosa::report_status(L.status, cosa::kStatusBadInput);
     sh = shares_of(a, kRows, kUnit, static_cast<int>(gridDim.x), blockIdx.x == 0 && warp == 0, first);
     if (me >= sh.ctas || sh.units == 0) {
       if (tid == 0) a.owner[me] = own;

@@ -67,6 +67,10 @@ def test_attention_reports_rows_before_the_first_request(listed):
     torch.cuda.synchronize()
     assert int(st.item()) == cosa.COSA_ERR_BAD_INPUT
     assert (out[0] == 7).all() and torch.equal(out[1:], want[:-1])
+    st = new_status()                                            # and where no request has a query
+    C.cosa_kv4_attention(c["p"], shifted, i32([2, 2, 2, 2]), c["cache"], i32(c["t"]), i32(c["lens"]), out=out, status=st)
+    torch.cuda.synchronize()
+    assert int(st.item()) == cosa.COSA_ERR_BAD_INPUT and torch.equal(out[1:], want[:-1])
 
 
 @pytest.mark.parametrize("paged", [False, True])
