@@ -363,3 +363,24 @@ def test_allocated_memory_belongs_to_the_streams_pool(monkeypatch, which):
     assert busy, "the stream ended too soon for the check to mean anything"
     assert len(blocks) == {"rope": 2, "evict": 3}.get(which, 2)
     assert not {a for a, _, _ in blocks} & {x.data_ptr() for x in again}
+
+
+def test_evict_without_weights_out():
+    """The C call makes weights_out optional: the same slots, kept numbers and moved rows without it."""
+    rng = np.random.default_rng(61)
+    cache, t, _, _ = kv_bulk.packed(rng, [300, 40], 2, 16, 64)
+    pages, room = t.shape[1], 3
+    dst = np.setdiff1d(np.arange(cache.shape[0] + 2 * room), t)[-2 * room:].reshape(2, room)
+    cache = torch.cat([cache, torch.zeros_like(cache[:2 * room])])
+    p = C.make_kv_params(num_reqs=2, num_q_heads=2, num_kv_heads=2, head_dim=64, page_size=16, max_seqlen=pages * 16, num_kv4_pages=cache.shape[0],
+                         max_pages_per_req=pages, budget=40, sink=2, recent=5, max_dst_pages=room)
+    w = torch.from_numpy(rng.exponential(size=(2, 2, pages * 16)).astype(np.float32)).to(DEV)
+    table, lens, to = i32(t), i32([300, 40]), i32(dst)
+    other = cache.clone()
+    new_len, kept, _ = C.cosa_kv4_evict(p, cache, table, lens, w, to)
+    n2, k2, st = torch.zeros_like(new_len), torch.zeros_like(kept), new_status()
+    rc = C.kv_library().cosa_kv4_evict(p, other.data_ptr(), table.data_ptr(), lens.data_ptr(), w.data_ptr(), to.data_ptr(), n2.data_ptr(),
+                                       k2.data_ptr(), None, st.data_ptr(), torch.cuda.current_stream().cuda_stream)
+    assert rc == 0
+    ok(st)
+    assert torch.equal(n2, new_len) and torch.equal(k2, kept) and torch.equal(other, cache) and new_len.tolist() == [40, 40]
