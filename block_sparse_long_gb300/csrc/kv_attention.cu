@@ -13,10 +13,17 @@
 // operands exactly.  The other operands, q and p * s, carry 2^96 to keep the products normal; what is
 // left, 2^-33, goes into the softmax scale and the last division.
 //
-// Work: 9/8 d bytes of cache per token and kv head (144 at d = 128) and 4 d operations per row.  Bound by the issue slots
-// that unpack the codes (320 instructions of a warp per 16 tokens at d = 128) together with the memory: a warp works alone on
+// The one rounding to fewer bits than fp32: p * s becomes a bf16 operand.  It is off by 2^-8 of a term at most and by much less
+// in their sum: outputs are 1.7e-3 to 1.8e-3 from a 64-bit form, where their own rounding to bf16 alone makes 1.6e-3 to 1.7e-3.
+// A second operand with what is cut off would double the second product and the turns of its layout, eight more of each, and
+// takes about 40 other instructions beside the 320 per 16 tokens, for an error that the output's rounding hides.  The accumulated weights are
+// formed from fp32 logits and take no part in it.
+//
+// Work: 9/8 d bytes of cache per token and kv head (144 at d = 128) and 4 d operations per row.  A warp works alone on
 // units of 16 or 32 tokens, one bulk copy each, out of its own ring in shared memory, and nothing is shared between
-// warps until the end of the CTA's part of a request.
+// warps until the end of the CTA's part of a request.  No unit of the card is full: over a context of 131072 tokens the issue slots
+// are 55 % busy (320 instructions of a warp per 16 tokens at d = 128, most of them unpacking), the ALU pipe 48 %, the memory 54 %,
+// the matrix pipe 22 %.  It streams at 5.6 TB/s; what is lost are the first loads, the CTAs' uneven ends and the join.
 //
 // Two ways to share the work.  As one list of all (request, kv head, row tile, unit), of which every CTA takes an equal run
 // whatever the lengths are (with an allowance for the ends of its pieces): a CTA that has all of a (request, kv head, row
@@ -25,9 +32,10 @@
 // few tokens, a cluster to each (request, kv head, row tile), whose CTAs join their parts through distributed shared memory.
 //
 // Measured (32 query and 8 kv heads of 128, one new token): one context of 131072 tokens, 37 us, 151 MB at 4.0 TB/s (59 % of the
-// measured copy rate; 27 us of it stream at 5.6 TB/s, the rest is the first loads, the CTAs' uneven ends and the join);
+// measured copy rate, 27 us of it streaming);
 // one of 777 tokens, 5.8 us; 48 ragged contexts (417K tokens), two new tokens and weights, 125 us, of which the weights'
-// logits (107 MB written and read) take about 35.
+// logits (107 MB written and read) take about 35.  Heads of 64: 27 us and 5.3 us.  A row tile streams and unpacks the cache for
+// itself: 8 contexts of 16K (151 MB) take 58, 60, 93 and 170 us with 12, 16, 32 and 64 rows.
 
 #include <algorithm>
 #include <cstdint>

@@ -2,7 +2,7 @@
 //
 // Per head x of d values:  y = x * rsqrt(mean(x^2) + eps) * w, then for each of the rotary_dim / 2 pairs (a, b):
 // (y_a cos t - y_b sin t, y_b cos t + y_a sin t) with t = position * inv_freq[i].  A value is read once and written
-// once (4 bytes), for about ten operations: memory bound.
+// once (4 bytes), for about ten operations: bound by the memory where a token has many rows.
 //
 // A warp has a token, or a part of its heads where the tokens are few: four rows (d = 128; eight for d = 64) at a
 // time, a row on d / 16 lanes.  The angles of a lane are the same in every row, so they are formed once and stay in
@@ -10,7 +10,9 @@
 // warp has two or four tokens, each on its share of the rows.
 //
 // Measured: 128K tokens of 32 + 8 + 8 heads of 128 into pages, 487 us, 3.22 GB at 6.6 TB/s (97 % of the measured copy rate);
-// 64 tokens, 3.8 us, bound by the chain of loads (request, position, frequencies).  Runs of tokens on a warp, with the
+// 64 tokens, 3.8 us, bound by the chain of loads (request, position, frequencies); 9.6K tokens of 12 + 4 + 4 heads of 64, 15.8 us,
+// 49 MB at 3.1 TB/s: the same chain and the angles are paid per token for 2.5 KB of rows each way (issue slots 59 % busy, warps wait
+// for loads more than for anything else).  Runs of tokens on a warp, with the
 // frequencies kept, took 593 us and more for the 128K tokens (each warp then walks memory alone, in 12 KB pieces).
 #include <cstdint>
 #include <type_traits>
@@ -35,7 +37,7 @@ __device__ __forceinline__ float half_turns(int64_t pos, double freq) {
 // The same in integers, for the frequencies of ordinary rotations, since the SM has few units for doubles: 51K tokens of 3 + 1
 // heads of 64 take 19.9 us instead of 25.6, 64 tokens of 32 + 8 heads 4.2 instead of 4.8.  freq = m 2^(e - 1075) has a
 // significand m of 53 bits; m times round(2^66 / 2 pi), shifted, is the turns of one position in units of 2^-64, whole
-// turns dropped; times the position it is good to 2^-32 of a turn.
+// turns dropped; times the position it is good to 2^-31 of a turn (for frequencies up to 2^6 to 2^-33).
 __device__ __forceinline__ bool ordinary(double freq) {       // 2^-36 <= |freq| < 2^10
   const int e = static_cast<int>(static_cast<uint64_t>(__double_as_longlong(freq)) >> 52) & 0x7FF;
   return e >= 1023 - 36 && e < 1023 + 10;

@@ -70,7 +70,7 @@
 extern "C" {
 #endif
 
-/* cosa_kv_params.flags */
+/* cosa_kv_params.flags.  Flags and fields that a call has no use for are ignored by it: one set of parameters serves all. */
 #define COSA_KV_FLAG_INTERLEAVED 1 /* rotation pairs are (2i, 2i+1); default (i, i + rotary_dim/2) */
 /* Test hook for the bounded waits of cosa_kv4_attention: no copy of the cache is issued, so every wait in the kernel runs
    out after its 2 s budget, the kernel ends, *device_status becomes COSA_ERR_DEVICE_TIMEOUT and out is undefined. */
