@@ -7,7 +7,7 @@ import pytest
 import torch
 
 from block_sparse_long_gb300 import cosa, kv as C
-from tests import kv_bulk, kv_paths, kv_reference as ref, test_gpu_kv as base
+from tests import kv_bulk, kv_paths, kv_reference as ref, test_gpu_kv as base, test_gpu_kv_serving as serving
 from tests.kv_helpers import bf, cu_of, i32, new_status, ok
 
 pytestmark = pytest.mark.gpu
@@ -384,3 +384,72 @@ def test_evict_without_weights_out():
     assert rc == 0
     ok(st)
     assert torch.equal(n2, new_len) and torch.equal(k2, kept) and torch.equal(other, cache) and new_len.tolist() == [40, 40]
+
+
+# ---------------------------------------------------------------------------------------------------------------
+# calls of one program on two streams
+# ---------------------------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("listed", [False, True])
+def test_decode_over_two_streams_and_captured(listed):
+    """Norm and rotation on one stream, append and attention on another behind an event, torch's kernels and fills between them, the
+    eviction back on the first: the results of one stream, run by run and replayed from a graph.  (Kernels of the library start
+    before the one in front of them has ended, and wait.)"""
+    s = serving.Loop(71)
+    s.prefill()
+    ok(s.status)
+    B, d = 2, s.d
+    pages = 2500 if listed else s.pages
+    pt4 = np.full((B, pages), -1, np.int32)
+    pt4[:, :s.pages] = s.pt4
+    p1 = C.make_kv_params(total_tokens=B, **{**s.common, "max_seqlen": pages * s.P, "max_pages_per_req": pages})
+    assert kv_paths.shares_a_list(p1) == listed
+    table, dst, cu1, before, after = i32(pt4), i32(s.dst), cu_of([1] * B), i32(s.lens), i32([n + 1 for n in s.lens])
+    pos, x, cache0 = i32(s.pos), s.steps[0], s.cache.clone()
+    e = lambda *a, dtype=torch.bfloat16: torch.zeros(a, dtype=dtype, device=DEV)  # noqa: E731
+    q1, k1, v1, out = e(B, s.Hq, d), e(B, s.Hkv, d), e(B, s.Hkv, d), e(B, s.Hq, d)
+    acc, acc_out = (e(B, s.Hkv, pages * s.P, dtype=torch.float32) for _ in range(2))
+    n, kept, ws = e(B, dtype=torch.int32), e(B, s.Hkv, s.budget, dtype=torch.int32), torch.empty(
+        C.cosa_kv4_attention_workspace_size(p1, True), dtype=torch.uint8, device=DEV)
+    outs = [q1, k1, out, acc, n, kept, acc_out, s.cache]
+
+    def step(main, side):
+        with torch.cuda.stream(main):
+            s.cache.copy_(cache0)
+            q, k, v = s.split(x)
+            C.cosa_qk_norm_rope(p1, q, k, cu1, s.inv, q_weight=s.wq, k_weight=s.wk, positions=pos, q_out=q1, k_out=k1)
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            acc.zero_()
+            v1.copy_(v)
+            C.cosa_kv4_store(p1, s.cache, table, k1, v1, cu_seqlens=cu1, start=before)
+            C.cosa_kv4_attention(p1, q1, cu1, s.cache, table, after, out=out, weights=acc, workspace=ws)
+            acc.mul_(0.5)
+            C.cosa_kv4_attention(p1, q1, cu1, s.cache, table, after, out=out, weights=acc, workspace=ws)
+        main.wait_stream(side)
+        with torch.cuda.stream(main):
+            C.cosa_kv4_evict(p1, s.cache, table, after, acc, dst, new_len=n, kept=kept, weights_out=acc_out)
+
+    one, two = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    step(one, one)
+    torch.cuda.synchronize()
+    want = [t.clone() for t in outs]
+    assert all(bool((t != 0).any()) for t in want)
+    for _ in range(10):
+        for t in outs[:-1]:
+            t.zero_()
+        torch.cuda.synchronize()
+        step(one, two)
+        torch.cuda.synchronize()
+        assert all(torch.equal(t, w) for t, w in zip(outs, want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=one):
+        step(one, two)
+    for _ in range(3):
+        for t in outs[:-1]:
+            t.zero_()
+        torch.cuda.synchronize()
+        graph.replay()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(t, w) for t, w in zip(outs, want))
