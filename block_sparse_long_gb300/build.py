@@ -1,8 +1,8 @@
-"""Build libcosa.so (the C-ABI library of the CUDA path) and libcosa_kv.so (what stands around it: include/cosa_kv.h)
-in-tree for sm_103a.
+"""Build libcosa.so (the C-ABI library of the CUDA path), libcosa_kv.so (what stands around it: include/cosa_kv.h) and
+libcosa_attn.so (dense attention beside it: include/cosa_attn.h) in-tree for sm_103a.
 
 Compiles the translation units under csrc/ in parallel with nvcc and links them into
-block_sparse_long_gb300/libcosa.so and libcosa_kv.so.  The CUDA runtime is linked statically and the driver
+block_sparse_long_gb300/libcosa.so, libcosa_kv.so and libcosa_attn.so.  The CUDA runtime is linked statically and the driver
 API is reached through the runtime's entry-point query, so the libraries load on a machine
 without a GPU (their calls then fail with COSA_ERR_CUDA).
 
@@ -26,7 +26,10 @@ SOURCES = ["api.cu", "osk.cu", "osk_p16.cu", "osk_p32.cu", "osk_p64.cu", "osk_p1
 HEADERS = ["ptx.cuh", "internal.h", "osk_kernel.cuh", "osk_union_kernel.cuh"]
 KV_LIB = os.path.join(HERE, "libcosa_kv.so")
 KV_SOURCES = ["kv_api.cu", "kv_rope.cu", "kv_convert.cu", "kv_attention.cu", "kv_evict.cu"]
-KV_HEADERS = ["ptx.cuh", "kv_internal.h", "kv_layout.cuh"]
+KV_HEADERS = ["ptx.cuh", "kv_internal.h", "kv_layout.cuh", "kv_angles.cuh"]
+ATTN_LIB = os.path.join(HERE, "libcosa_attn.so")
+ATTN_SOURCES = ["attn_api.cu", "attn_rope.cu", "attn_commit.cu", "attn_paged.cu", "attn_prefill.cu"]
+ATTN_HEADERS = KV_HEADERS + ["attn_internal.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-std=c++17", "-O3", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall", "--expt-relaxed-constexpr"]
 
@@ -46,7 +49,8 @@ def _inputs(sources, headers, public):
 
 
 # library, its translation units, the headers they include
-LIBRARIES = ((LIB, SOURCES, HEADERS, ["cosa.h"]), (KV_LIB, KV_SOURCES, KV_HEADERS, ["cosa.h", "cosa_kv.h"]))
+LIBRARIES = ((LIB, SOURCES, HEADERS, ["cosa.h"]), (KV_LIB, KV_SOURCES, KV_HEADERS, ["cosa.h", "cosa_kv.h"]),
+             (ATTN_LIB, ATTN_SOURCES, ATTN_HEADERS, ["cosa.h", "cosa_kv.h", "cosa_attn.h"]))
 
 
 def _stale(lib, sources, headers, public) -> bool:
