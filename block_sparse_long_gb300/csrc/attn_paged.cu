@@ -1,93 +1,971 @@
-// Attention of each request's newest tokens over pages: the tree attention's keys and values, or latent vectors.
+// Attention of each request's newest tokens over pages: the tree attention's keys and values, or latent vectors (one key
+// head whose first values are the value).
 //
-// A warp has a query row (token, head) and walks the slots, 32-bit sums in registers, with the running maximum and sum of the
-// softmax.
+//     s = k . q (slot by row),  p = exp2(s * scale - m_row),  o = sum p v,  l = sum p
+//
+// A row is a (new token, query head of the kv head): R = n * Hq / Hkv of them share every key, one to some hundreds.  With so few
+// the cache is read once and the memory bounds the call, so the matrix instructions are set up for what there is plenty of:
+// the 128 slots of a tile, or 128 values of the output, are the 128 rows of a tcgen05.mma, and the N = 16 to 128 query rows
+// its columns.  S^T = K Q^T has a slot per TMEM lane, O^T = V^T P^T a value per lane; K comes as it lies in its page, and as V
+// read the other way (values contiguous), so latent vectors are loaded once for both products.
+//
+// A CTA per SM.  The tiles of all (request, kv head, row tile) items stand in one list, which the CTAs share evenly, one unit per
+// tile and one per item; a CTA's piece of an item that others have too leaves m, l and o (32 bits) in the workspace and
+// join_kernel puts them together.
+//
+// Warp roles:
+//   warp 0     producer: looks up the pages of a tile and copies them by TMA into a ring of 32 KB slots (two 128-byte wide
+//              columns of 128 slots), 160 KB in flight at most.
+//   warp 1     issues S^T of every tile into one of two TMEM buffers.
+//   warp 2     issues O^T += V^T P^T; clears rows of V that no slot has, and in the tile of the new tokens what is not finite.
+//   warp 3     owns the TMEM.
+//   warps 4-   softmax: a thread has a slot and 16 to 64 query rows.  The reference m of a row is that of an earlier tile until some
+//              logit exceeds it by 2^8, so that most tiles need no maximum over the slots: one vote, the exponentials,
+//              and P^T to shared memory as bf16 (2^-9 of each term; l sums the unrounded ones).
+#include <cmath>
 #include <cstdint>
 
+#include <cuda.h>
+#include <cuda_runtime.h>
+
 #include "attn_internal.h"
+#include "attn_tma.h"
 #include "kv_internal.h"
 #include "kv_layout.cuh"
 
 namespace cosa_attn {
 namespace {
 
-constexpr int kThreads = 128;
+using cosa::fence_proxy_async_smem;
+using cosa::mbar_arrive;
+using cosa::mbar_arrive_expect_tx;
+using cosa::mbar_init;
+using cosa::named_bar_red_or;
+using cosa::named_bar_sync;
+using cosa::smem_u32;
+using cosa::tc_fence_after;
+using cosa::tc_fence_before;
+using cosa::umma_commit;
+using cosa::umma_ss;
+using cosa::wait_parity_bounded;
+
+constexpr int kTile = 128;                 // slots
+constexpr int kCtas = 152;
+constexpr int kColumn = kTile * 128;       // bytes of a 64-value wide column of a tile
+constexpr int kPair = 2 * kColumn;
+constexpr float kNone = -3e38f;            // reference of a row that has seen nothing
+constexpr float kRescaleLog2 = 8.0f;
+constexpr float kLn2 = 0.69314718055994531f;
 constexpr unsigned kAll = 0xffffffffu;
 
-__device__ __forceinline__ float value(const uint16_t* p) { return __uint_as_float(static_cast<uint32_t>(*p) << 16); }
+// DK, DV: values of a key and a value.  kLatent: the value is the key's first DV values.  N: query rows of a row tile.
+template <int DK_, int DV_, bool LATENT, int N_>
+struct Shape {
+  static constexpr int DK = DK_, DV = DV_, N = N_;
+  static constexpr bool kLatent = LATENT;
+  static constexpr int kGroups = N == 128 ? 2 : 1;               // warpgroups of the softmax
+  static constexpr int NC = N / kGroups;                         // query rows of a softmax thread
+  static constexpr int kThreads = 128 + 128 * kGroups;
+  static constexpr int kBlocks = DV > 128 ? DV / 128 : 1;        // of 128 output values
+  static constexpr int kPairs = LATENT ? DV / 128 : DK == 128 ? 2 : 1;      // ring slots of a tile; 64 + 64: K and V in one
+  static constexpr int kQBytes = N * DK * 2;
+  static constexpr int kPBytes = N * kTile * 2;
+  // The widest latent rows leave no room for P: it goes over the rotated part of the keys, which S^T has used by then.
+  static constexpr bool kAlias = LATENT && DV == 512 && N == 64;
+  static constexpr int kPBufs = kAlias ? 0 : (LATENT && DV == 512 && N == 32) || N == 128 ? 1 : 2;
+  static constexpr int kRopes = LATENT && DV + N <= 528 ? 2 : 1;      // (1, unused, without latent vectors)
+  static constexpr int kSmall = 2048 + N * 40;
+  static constexpr int kRoom = 227 * 1024 - 1024 - kSmall - kQBytes - kPBufs * kPBytes - (LATENT ? kRopes * kColumn : 1024);
+  static constexpr int kSlots = kRoom / kPair < 6 ? kRoom / kPair : 6;
+  static_assert(kSlots >= kPairs, "a tile fits the ring");
+  static constexpr uint32_t kTmemO = 0, kTmemS = kBlocks * N;
+  static_assert(kTmemS + 2 * N <= 512, "TMEM columns");
+  // P^T: rows of 32, 64 or 128 bytes per slot, swizzled at that width
+  static constexpr int kPRow = N >= 64 ? 128 : 2 * N;
+};
 
-template <int DK, int DV, bool kLatent>
-__global__ void __launch_bounds__(kThreads) row_kernel(const PagedLaunch L) {
-  cosa_kv::wait_for_stream();
+template <class S>
+struct alignas(1024) Smem {
+  uint8_t ring[S::kSlots][kPair];
+  uint8_t rope[S::kRopes][S::kLatent ? kColumn : 1024];
+  uint8_t q[S::kQBytes];
+  uint8_t p[S::kPBufs ? S::kPBufs : 1][S::kPBufs ? S::kPBytes : 16];
+  uint64_t full[S::kSlots], empty[S::kSlots];
+  uint64_t rope_full[2], rope_empty[2];
+  uint64_t q_ready, s_full[2], s_empty[2], p_full[2], pv_done[2], cleanup;
+  uint64_t mask[S::N];               // tree mask of a row's token
+  float base[S::N], alpha[S::N];     // reference of a row (log2 units), and its last change
+  float part[4][S::N];               // maxima and sums of the four warps
+  int32_t row[S::N];                 // output row, or -1
+  int32_t node[S::N];                // token of the request
+  int64_t total, before;             // units of the batch, units before this CTA's first request
+  int32_t first_req;
+  int32_t odd_values;                // something among the new tokens' values is not finite
+  uint32_t tmem_base;
+  int32_t abort_flag;
+};
+
+struct Args {
+  const uint16_t *q, *q_rope, *k_cache, *v_cache;
+  const int32_t *cu_seqlens, *page_table, *kv_len;
+  const int64_t* tree_mask;
+  uint16_t* out;
+  float *lse, *part_o, *part_ml;
+  int32_t* status;
+  int64_t q_stride, q_rope_stride;
+  int num_reqs, num_q_heads, num_kv_heads, group, page_shift, total_tokens, max_seqlen, num_pages, max_pages_per_req;
+  float scale_log2;
+  int stall;
+};
+
+// A request: its tokens, rows, tiles.  Without keys (lengths that contradict each other) it has no tiles, but its rows are written.
+struct Request {
+  int tok0, n, len, tiles, row_tiles;
+  bool bad;
+};
+
+template <int N>
+__device__ __forceinline__ Request request_of(const Args& a, int b) {
+  Request r;
+  r.tok0 = a.cu_seqlens[b];
+  const int64_t n = static_cast<int64_t>(a.cu_seqlens[b + 1]) - r.tok0;
+  r.bad = r.tok0 < 0 || n < 0 || r.tok0 + n > a.total_tokens;
+  r.n = r.bad ? 0 : static_cast<int>(n);
+  r.len = a.kv_len[b];
+  if (r.n > 0 && (r.len < r.n || r.len > a.max_seqlen || (a.tree_mask && r.n > COSA_ATTN_MAX_TREE))) r.bad = true;
+  if (r.bad || r.n == 0) r.len = 0;
+  r.tiles = (r.len + kTile - 1) / kTile;
+  r.row_tiles = static_cast<int>((static_cast<int64_t>(r.n) * a.group + N - 1) / N);
+  return r;
+}
+
+__device__ __forceinline__ int64_t units_of(const Args& a, const Request& r) {
+  return static_cast<int64_t>(a.num_kv_heads) * r.row_tiles * (r.tiles + 1);
+}
+
+// First unit of a CTA.  With fewer units than CTAs the first ones have one each: every CTA up to the last with any has some.
+__device__ __forceinline__ int64_t share(int64_t total, int cta) { return total < kCtas ? min(static_cast<int64_t>(cta), total) : total * cta / kCtas; }
+
+// What a CTA does of one item: tiles t0 .. t1 - 1.
+struct Piece {
+  Request r;
+  int b, head, row_tile, t0, t1;
+  int slot;          // of the workspace, or -1: all of the item
+};
+
+// The pieces of a CTA in order; every role walks them by itself.
+template <int N>
+struct Pieces {
+  int64_t pos, first, end, before, units;
+  int b, cta;
+  Request r;
+
+  __device__ Pieces(const Args& a, int cta_, int64_t total, int first_req, int64_t before_) : before(before_), units(0), b(first_req - 1), cta(cta_) {
+    first = pos = share(total, cta);
+    end = share(total, cta + 1);
+  }
+  __device__ bool next(const Args& a, Piece& p) {
+    if (pos >= end) return false;
+    while (pos >= before + units) {
+      before += units;
+      r = request_of<N>(a, ++b);
+      units = units_of(a, r);
+    }
+    const int64_t local = pos - before;
+    const int per = r.tiles + 1;
+    const int64_t item = local / per;
+    const int u = static_cast<int>(local - item * per);
+    const int take = static_cast<int>(min(static_cast<int64_t>(per - u), end - pos));
+    p.r = r;
+    p.b = b;
+    p.head = static_cast<int>(item / r.row_tiles);
+    p.row_tile = static_cast<int>(item % r.row_tiles);
+    p.t0 = max(u - 1, 0);
+    p.t1 = u + take - 1;
+    p.slot = take == per ? -1 : 2 * cta + (pos != first);
+    pos += take;
+    return true;
+  }
+};
+
+// Units of all requests, and the request with unit `at`: by one warp.
+template <int N>
+__device__ __forceinline__ int64_t total_units(const Args& a, bool report) {
   const int lane = threadIdx.x % 32;
-  const int64_t row = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) / 32;
-  const int64_t t = row / L.num_q_heads;
-  const int h = static_cast<int>(row % L.num_q_heads);
-  if (t >= L.total_tokens) return;
-  int b = 0;
-  while (b < L.num_reqs && L.cu_seqlens[b + 1] <= t) ++b;
-  if (b == L.num_reqs) return;
-  const int first = L.cu_seqlens[b], n = L.cu_seqlens[b + 1] - first, i = static_cast<int>(t) - first;
-  if (i < 0 || first < 0 || L.cu_seqlens[b + 1] > L.total_tokens) {
-    cosa::report_status(L.status, cosa::kStatusBadInput);
-    return;
+  int64_t sum = 0;
+  for (int b = lane; b < a.num_reqs; b += 32) {
+    const Request r = request_of<N>(a, b);
+    if (r.bad && report) cosa::report_status(a.status, cosa::kStatusBadInput);
+    sum += units_of(a, r);
   }
-  int len = L.kv_len[b];
-  if (len < n || len > L.max_seqlen || (L.tree_mask && n > COSA_ATTN_MAX_TREE)) {
-    cosa::report_status(L.status, cosa::kStatusBadInput);
-    len = 0;
+#pragma unroll
+  for (int m = 1; m < 32; m *= 2) sum += __shfl_xor_sync(kAll, sum, m);
+  return sum;
+}
+
+template <int N>
+__device__ __forceinline__ void find_request(const Args& a, int64_t at, int& first_req, int64_t& before) {
+  const int lane = threadIdx.x % 32;
+  int64_t sum = 0;
+  for (int b0 = 0;; b0 += 32) {
+    const int64_t mine = b0 + lane < a.num_reqs ? units_of(a, request_of<N>(a, b0 + lane)) : 0;
+    int64_t upto = mine;
+#pragma unroll
+    for (int m = 1; m < 32; m *= 2) {
+      const int64_t x = __shfl_up_sync(kAll, upto, m);
+      if (lane >= m) upto += x;
+    }
+    const unsigned past = __ballot_sync(kAll, sum + upto > at);
+    if (past || b0 + 32 >= a.num_reqs) {
+      const int l = past ? __ffs(past) - 1 : 31;
+      first_req = b0 + l;
+      before = sum + __shfl_sync(kAll, upto - mine, l);
+      return;
+    }
+    sum += __shfl_sync(kAll, upto, 31);
   }
-  const uint64_t mask = L.tree_mask ? static_cast<uint64_t>(L.tree_mask[t]) : 0;
-  float q[DK / 32];
+}
+
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status) {
+  return __all_sync(kAll, wait_parity_bounded(bar, parity, abort_flag, status));
+}
+
+// Shared-memory matrix descriptor; layout 2, 4, 6: 128-, 64-, 32-byte swizzle.
+__device__ __forceinline__ uint64_t smem_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo, int layout) {
+  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16 |
+         static_cast<uint64_t>((sbo >> 4) & 0x3FFFu) << 32 | static_cast<uint64_t>(1) << 46 | static_cast<uint64_t>(layout) << 61;
+}
+
+// Where 16-byte piece c of row t of P^T goes (the swizzle of rows of kRow bytes).
+template <int kRow>
+__device__ __forceinline__ int p_offset(int t, int c) {
+  const int x = kRow == 128 ? t & 7 : kRow == 64 ? t >> 1 & 3 : t >> 2 & 1;
+  return t * kRow + ((c ^ x) << 4);
+}
+
+template <int NC>
+__device__ __forceinline__ void load_columns(uint32_t taddr, float (&x)[NC]) {
+  uint32_t r[NC];
+  if constexpr (NC == 16) {
+    cosa::tmem_ld16(taddr, r);
+  } else {
 #pragma unroll
-  for (int e = 0; e < DK / 32; ++e) {
-    const int d = e * 32 + lane;
-    if (kLatent && d >= DV)
-      q[e] = value(L.q_rope + t * L.q_rope_stride + h * (DK - DV) + d - DV);
-    else
-      q[e] = value(L.q + t * L.q_stride + h * DV + d);
+    for (int i = 0; i < NC; i += 32) cosa::tmem_ld32(taddr + i, *reinterpret_cast<uint32_t(*)[32]>(&r[i]));
   }
-  float o[DV / 32] = {}, m = -INFINITY, l = 0.f;
-  const int kvh = h / (L.num_q_heads / L.num_kv_heads);
-  for (int s = 0; s < len; ++s) {
-    const int j = s - (len - n);
-    if (j >= 0 && (L.tree_mask ? !(mask >> j & 1) : j > i)) continue;
-    const int phys = L.page_table[static_cast<size_t>(b) * L.max_pages_per_req + (s >> L.page_shift)];
-    if (phys < 0 || phys >= L.num_pages) continue;
-    const int64_t place = (static_cast<int64_t>(phys) << L.page_shift) + (s & (L.page_size - 1));
-    const uint16_t* k = L.k_cache + (kLatent ? place : place * L.num_kv_heads + kvh) * DK;
-    const uint16_t* v = kLatent ? k : L.v_cache + (place * L.num_kv_heads + kvh) * DV;
-    float x = 0.f;
+  cosa::tmem_wait_ld();
 #pragma unroll
-    for (int e = 0; e < DK / 32; ++e) x = fmaf(q[e], value(k + e * 32 + lane), x);
-#pragma unroll
-    for (int w = 1; w < 32; w *= 2) x += __shfl_xor_sync(kAll, x, w);
-    x *= L.scale_log2;
-    const float top = fmaxf(m, x), keep = m == top ? 1.f : exp2f(m - top), p = exp2f(x - top);
-    m = top;
-    l = l * keep + p;
-#pragma unroll
-    for (int e = 0; e < DV / 32; ++e) o[e] = o[e] * keep + p * value(v + e * 32 + lane);
+  for (int i = 0; i < NC; ++i) x[i] = __uint_as_float(r[i]);
+}
+
+// The largest value of a warp; NaN counts as nothing.
+__device__ __forceinline__ float warp_max(float x) {
+  if (x != x) x = -INFINITY;
+  int i = __float_as_int(x);
+  i ^= (i >> 31) & 0x7fffffff;
+  i = __reduce_max_sync(kAll, i);
+  i ^= (i >> 31) & 0x7fffffff;
+  return __int_as_float(i);
+}
+
+__device__ __forceinline__ bool odd(uint32_t two) {        // either bf16 is not finite
+  return (two & 0x7F80u) == 0x7F80u || (two & 0x7F800000u) == 0x7F800000u;
+}
+
+template <class S>
+__global__ void __launch_bounds__(S::kThreads, 1)
+    paged_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const __grid_constant__ Args a) {
+  constexpr int N = S::N, NC = S::NC, DV = S::DV;
+  extern __shared__ uint8_t smem_raw[];
+  Smem<S>& sm = *reinterpret_cast<Smem<S>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, cta = blockIdx.x;
+  volatile int* abort_flag = &sm.abort_flag;
+  cosa_kv::wait_for_stream();
+  cosa_kv::let_next_start();
+
+  if (warp == 0) {
+    const int64_t total = total_units<N>(a, cta == 0);
+    int first_req;
+    int64_t before;
+    find_request<N>(a, share(total, cta), first_req, before);
+    if (lane == 0) {
+      sm.total = total;
+      sm.first_req = first_req;
+      sm.before = before;
+      if (cta == 0 && (a.cu_seqlens[0] != 0 || a.cu_seqlens[a.num_reqs] > a.total_tokens)) cosa::report_status(a.status, cosa::kStatusBadInput);
+    }
+  } else if (warp == 1 && lane == 0) {
+    for (int s = 0; s < S::kSlots; ++s) {
+      mbar_init(&sm.full[s], 1);
+      mbar_init(&sm.empty[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&sm.rope_full[s], 1);
+      mbar_init(&sm.rope_empty[s], 1);
+      mbar_init(&sm.s_full[s], 1);
+      mbar_init(&sm.s_empty[s], 4 * S::kGroups);
+      mbar_init(&sm.p_full[s], 4 * S::kGroups);
+      mbar_init(&sm.pv_done[s], 2);       // the products, and the issuing warp's own arrival
+    }
+    mbar_init(&sm.q_ready, 1);
+    mbar_init(&sm.cleanup, 2);
+    sm.abort_flag = 0;
+    sm.odd_values = 0;
+    cosa::fence_mbarrier_init();
+  } else if (warp == 3) {
+    cosa::tmem_alloc(&sm.tmem_base, 512);
+    cosa::tmem_relinquish();
   }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem_base;
+  Pieces<N> pieces(a, cta, sm.total, sm.first_req, sm.before);
+  Piece pc;
+  const int pages_per_tile = kTile >> a.page_shift;
+
+  if (warp == 0) {
+    // =========================== producer ===========================
+    if (lane == 0) {
+      cosa::tma_prefetch_desc(&kmap);
+      cosa::tma_prefetch_desc(&vmap);
+    }
+    int64_t pair = 0;      // ring slots taken so far
+    int ropes = 0;
+    bool ok = !a.stall;
+    while (ok && pieces.next(a, pc)) {
+      const int32_t* table = a.page_table + static_cast<size_t>(pc.b) * a.max_pages_per_req;
+      auto look_up = [&](int t) {
+        const int64_t page = static_cast<int64_t>(t) * pages_per_tile + lane;
+        return t < pc.t1 && lane < pages_per_tile && (page << a.page_shift) < pc.r.len ? table[page] : -1;
+      };
+      int phys_next = look_up(pc.t0);
+      for (int t = pc.t0; t < pc.t1 && ok; ++t) {
+        const int phys = phys_next;
+        phys_next = look_up(t + 1);
+        const unsigned there = __ballot_sync(kAll, phys >= 0 && phys < a.num_pages);
+        const uint32_t bytes = static_cast<uint32_t>(__popc(there)) << a.page_shift << 7;      // of a 64-value column
+        const int page = lane & (pages_per_tile - 1), column = lane / pages_per_tile;
+        const int place = __shfl_sync(kAll, phys, page) << a.page_shift;
+        const bool copies = there >> page & 1;
+        const int to = (page << a.page_shift) * 128;
+        auto rotated = [&] {
+          const int s = ropes % S::kRopes;
+          if (ropes >= S::kRopes) ok = warp_wait(&sm.rope_empty[s], (ropes / S::kRopes - 1) & 1, abort_flag, a.status);
+          if (!ok) return;
+          if (lane == 0) mbar_arrive_expect_tx(&sm.rope_full[s], bytes);
+          __syncwarp();
+          if (column == 0 && copies) cosa::tma_load_4d(&sm.rope[s][to], &kmap, &sm.rope_full[s], 0, place, DV / 64, 0);
+          ++ropes;
+        };
+        if constexpr (S::kLatent && !S::kAlias) rotated();
+        if (!ok) break;
+        for (int i = 0; i < S::kPairs; ++i, ++pair) {
+          const int s = static_cast<int>(pair % S::kSlots);
+          if (pair >= S::kSlots) ok = warp_wait(&sm.empty[s], (pair / S::kSlots - 1) & 1, abort_flag, a.status);
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect_tx(&sm.full[s], 2 * bytes);
+          __syncwarp();
+          if (column < 2 && copies) {
+            uint8_t* dst = &sm.ring[s][column * kColumn + to];
+            if (S::kLatent)
+              cosa::tma_load_4d(dst, &kmap, &sm.full[s], 0, place, 2 * i + column, 0);
+            else if (S::DK == 128)
+              cosa::tma_load_4d(dst, i ? &vmap : &kmap, &sm.full[s], 0, place, column, pc.head);
+            else
+              cosa::tma_load_4d(dst, column ? &vmap : &kmap, &sm.full[s], 0, place, 0, pc.head);
+          }
+        }
+        if constexpr (S::kAlias) {
+          if (ok) rotated();
+        }
+      }
+    }
+    // every copy lands before the CTA ends
+    if (lane == 0) {
+      for (int s = 0; s < S::kSlots; ++s) {
+        const int64_t issued = (pair - s + S::kSlots - 1) / S::kSlots;
+        if (issued > 0) wait_parity_bounded(&sm.full[s], (issued - 1) & 1, nullptr, nullptr);
+      }
+      for (int s = 0; s < S::kRopes; ++s) {
+        const int issued = (ropes - s + S::kRopes - 1) / S::kRopes;
+        if (issued > 0) wait_parity_bounded(&sm.rope_full[s], (issued - 1) & 1, nullptr, nullptr);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // =========================== S^T = K Q^T ===========================
+    if (lane == 0) {
+      constexpr uint32_t idesc = cosa::idesc_bf16_f32(128, N, false, false);
+      const uint64_t qd = smem_desc(smem_u32(sm.q), 16, 1024, 2), kd = smem_desc(smem_u32(sm.ring), 16, 1024, 2);
+      const uint64_t rd = smem_desc(smem_u32(sm.rope), 16, 1024, 2);
+      int tile = 0, turn = 0;
+      bool ok = true;
+      while (ok && pieces.next(a, pc)) {
+        if (pc.t0 == pc.t1) continue;
+        ok = wait_parity_bounded(&sm.q_ready, turn++ & 1, abort_flag, a.status);
+        for (int t = pc.t0; t < pc.t1 && ok; ++t, ++tile) {
+          const int sb = tile & 1;
+          if (tile >= 2) ok = wait_parity_bounded(&sm.s_empty[sb], (tile / 2 - 1) & 1, abort_flag, a.status);
+          const uint32_t d = tmem + S::kTmemS + sb * N;
+          // the rotated part comes last where P^T goes over it, else first
+          auto rotated = [&] {
+            const int s = tile % S::kRopes;
+            ok = ok && wait_parity_bounded(&sm.rope_full[s], (tile / S::kRopes) & 1, abort_flag, a.status);
+            if (!ok) return;
+            tc_fence_after();
 #pragma unroll
-  for (int e = 0; e < DV / 32; ++e)
-    L.out[(t * L.num_q_heads + h) * DV + e * 32 + lane] = static_cast<uint16_t>(cosa::pack_bf16x2(o[e] * inv, 0.f));
-  if (L.lse && lane == 0) L.lse[t * L.num_q_heads + h] = (m + log2f(l)) * 0.69314718055994531f;
+            for (int k = 0; k < 4; ++k)
+              umma_ss(d, rd + ((s * kColumn + k * 32) >> 4), qd + ((DV / 64 * N * 128 + k * 32) >> 4), idesc, S::kAlias || k > 0);
+            if (!S::kAlias) umma_commit(&sm.rope_empty[s]);
+          };
+          if constexpr (S::kLatent && !S::kAlias) rotated();
+          constexpr int kKeys = S::kLatent ? S::kPairs : 1;      // ring slots with keys
+#pragma unroll 1
+          for (int i = 0; i < kKeys; ++i) {
+            const int64_t pair = static_cast<int64_t>(tile) * S::kPairs + i;
+            const int s = static_cast<int>(pair % S::kSlots);
+            ok = ok && wait_parity_bounded(&sm.full[s], (pair / S::kSlots) & 1, abort_flag, a.status);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < (S::DK == 64 ? 4 : 8); ++k)
+              umma_ss(d, kd + ((s * kPair + (k / 4) * kColumn + (k % 4) * 32) >> 4),
+                      qd + (((2 * i + k / 4) * N * 128 + (k % 4) * 32) >> 4), idesc, (S::kLatent && !S::kAlias) || i > 0 || k > 0);
+            if (!S::kLatent && S::DK == 128) umma_commit(&sm.empty[s]);
+          }
+          if constexpr (S::kAlias) rotated();
+          if (ok) umma_commit(&sm.s_full[sb]);
+        }
+      }
+      umma_commit(&sm.cleanup);
+      wait_parity_bounded(&sm.cleanup, 0, nullptr, nullptr);
+    }
+    __syncwarp();
+  } else if (warp == 2) {
+    // =========================== O^T += V^T P^T ===========================
+    constexpr uint32_t idesc = cosa::idesc_bf16_f32(128, N, true, true);
+    constexpr int kLayout = S::kPRow == 128 ? 2 : S::kPRow == 64 ? 4 : 6;
+    const uint64_t vd = smem_desc(smem_u32(sm.ring), kColumn, 1024, 2);
+    const uint64_t pd = smem_desc(S::kAlias ? smem_u32(sm.rope) : smem_u32(sm.p), kColumn, 8 * S::kPRow, kLayout);
+    int tile = 0;
+    bool ok = true;
+    while (ok && pieces.next(a, pc)) {
+      const int32_t* table = a.page_table + static_cast<size_t>(pc.b) * a.max_pages_per_req;
+      const int ctx = pc.r.len - pc.r.n;
+      const bool differ = pc.r.n > 1 || a.tree_mask;      // the rows may differ in what they see
+      for (int t = pc.t0; t < pc.t1 && ok; ++t, ++tile) {
+        // bit i: lane's slots 4 * lane + i are empty (their values must be 0: 0 times what is not finite is not)
+        unsigned empty = 0;
+        int looked = -2, phys = -1;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int slot = t * kTile + 4 * lane + i;
+          if (slot < pc.r.len && slot >> a.page_shift != looked) {
+            looked = slot >> a.page_shift;
+            phys = table[looked];
+          }
+          if (slot >= pc.r.len || phys < 0 || phys >= a.num_pages) empty |= 1u << i;
+        }
+        const bool holes = __any_sync(kAll, empty);
+        const int tail0 = differ ? max(ctx - t * kTile, 0) : kTile, tail1 = min(pc.r.len - t * kTile, kTile);
+        const int pb = S::kPBufs == 2 ? tile & 1 : 0, uses = S::kPBufs == 2 ? tile / 2 : tile;
+        if (!warp_wait(&sm.p_full[pb], uses & 1, abort_flag, a.status)) { ok = false; break; }
+        bool found = false;
+#pragma unroll 1
+        for (int m = 0; m < S::kBlocks; ++m) {
+          const int64_t pair = static_cast<int64_t>(tile) * S::kPairs + (S::kLatent ? m : S::kPairs - 1);
+          const int s = static_cast<int>(pair % S::kSlots);
+          if (!warp_wait(&sm.full[s], (pair / S::kSlots) & 1, abort_flag, a.status)) { ok = false; break; }
+          constexpr int kFirst = S::DK == 64 ? 1 : 0;      // columns of the slot that are values
+          if (holes) {
+            for (int i = 0; i < 4; ++i)
+              if (empty >> i & 1)
+                for (int c = kFirst; c < 2; ++c)
+                  for (int e = 0; e < 8; ++e)
+                    *reinterpret_cast<uint4*>(&sm.ring[s][c * kColumn + (4 * lane + i) * 128 + e * 16]) = make_uint4(0, 0, 0, 0);
+          }
+          for (int e = tail0 * 16 + lane; e < tail1 * 16; e += 32) {      // 16-byte pieces of the new tokens' values
+            if ((e & 15) < 8 * kFirst) continue;
+            uint4* at = reinterpret_cast<uint4*>(&sm.ring[s][(e & 15) / 8 * kColumn + (e >> 4) * 128 + (e & 7) * 16]);
+            uint4 x = *at;
+            if (odd(x.x) || odd(x.y) || odd(x.z) || odd(x.w)) {
+              found = true;
+              uint32_t* w = reinterpret_cast<uint32_t*>(&x);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                if ((w[i] & 0x7F80u) == 0x7F80u) w[i] &= 0xFFFF0000u;
+                if ((w[i] & 0x7F800000u) == 0x7F800000u) w[i] &= 0xFFFFu;
+              }
+              *at = x;
+            }
+          }
+          if (holes || tail0 < tail1) {
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+          if (lane == 0) {
+            tc_fence_after();
+            const uint64_t vs = vd + ((s * kPair) >> 4), ps = pd + ((pb * S::kPBytes) >> 4);
+#pragma unroll
+            for (int k = 0; k < kTile / 16; ++k)
+              umma_ss(tmem + S::kTmemO + m * N, vs + ((k * 2048) >> 4), ps + ((k * 16 * S::kPRow) >> 4), idesc, t > pc.t0 || k > 0);
+            umma_commit(&sm.empty[s]);
+          }
+          __syncwarp();
+        }
+        if (!ok) break;
+        found = __any_sync(kAll, found);
+        if (lane == 0) {
+          if (found) sm.odd_values = 1;
+          if (S::kAlias) umma_commit(&sm.rope_empty[0]);
+          umma_commit(&sm.pv_done[tile & 1]);
+          mbar_arrive(&sm.pv_done[tile & 1]);
+        }
+        __syncwarp();
+      }
+    }
+    if (lane == 0) {
+      umma_commit(&sm.cleanup);
+      wait_parity_bounded(&sm.cleanup, 0, nullptr, nullptr);
+    }
+    __syncwarp();
+  } else if (warp >= 4) {
+    // =========================== softmax ===========================
+    const int g = warp / 4 - 1, quarter = warp % 4, tid = threadIdx.x - 128;
+    const int at = quarter * 32 + lane;                // TMEM lane: slot of the tile, value of an output block
+    const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+    const int c0 = g * NC;
+    constexpr int kAllBar = 3, kSoftmax = 128 * S::kGroups;
+    const int my_bar = 1 + g;
+    const float scale = a.scale_log2;
+    int tile = 0;
+    bool ok = true;
+    while (ok && pieces.next(a, pc)) {
+      const Request& r = pc.r;
+      const int rows = r.n * a.group;      // fits 32 bits: total_tokens * Hq does
+      const int row0 = pc.row_tile * N;
+      named_bar_sync(kAllBar, kSoftmax);   // the last piece is done with what follows
+      if (tid < N) {
+        const int row = row0 + tid, node = min(row, rows - 1) / a.group;
+        sm.row[tid] = row < rows ? (r.tok0 + node) * a.num_q_heads + pc.head * a.group + row % a.group : -1;
+        sm.node[tid] = node;
+        sm.mask[tid] = a.tree_mask ? static_cast<uint64_t>(a.tree_mask[r.tok0 + node]) : 0;
+        sm.base[tid] = kNone;
+      }
+      if (pc.t0 < pc.t1) {
+        // queries into rows of 128 bytes per 64 values, swizzled; rows behind the last are 0
+        constexpr int kPieces16 = S::DK / 8;
+        for (int e = tid; e < N * kPieces16; e += kSoftmax) {
+          const int row = e / kPieces16, c = e % kPieces16;
+          uint4 x = make_uint4(0, 0, 0, 0);
+          if (row0 + row < rows) {
+            const int64_t tok = r.tok0 + (row0 + row) / a.group;
+            const int head = pc.head * a.group + (row0 + row) % a.group;
+            const uint16_t* src = S::kLatent && c >= DV / 8 ? a.q_rope + tok * a.q_rope_stride + head * (S::DK - DV) + c * 8 - DV
+                                                            : a.q + tok * a.q_stride + head * DV + c * 8;
+            x = *reinterpret_cast<const uint4*>(src);
+          }
+          *reinterpret_cast<uint4*>(&sm.q[c / 8 * N * 128 + row * 128 + ((c ^ row) & 7) * 16]) = x;
+        }
+        fence_proxy_async_smem();
+      }
+      named_bar_sync(kAllBar, kSoftmax);
+      if (tid == 0 && pc.t0 < pc.t1) mbar_arrive(&sm.q_ready);
+
+      const int32_t* table = a.page_table + static_cast<size_t>(pc.b) * a.max_pages_per_req;
+      const int ctx = r.len - r.n;
+      float l[NC];
+#pragma unroll
+      for (int i = 0; i < NC; ++i) l[i] = 0.f;
+      for (int t = pc.t0; t < pc.t1; ++t, ++tile) {
+        const int sb = tile & 1, slot = t * kTile + at;
+        bool there = slot < r.len;
+        if (there) {
+          const int phys = table[slot >> a.page_shift];
+          there = phys >= 0 && phys < a.num_pages;
+        }
+        bool fail = !warp_wait(&sm.s_full[sb], (tile / 2) & 1, abort_flag, a.status);
+        float x[NC];
+        if (!fail) {
+          tc_fence_after();
+          load_columns<NC>(tmem + lanes + S::kTmemS + sb * N + c0, x);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.s_empty[sb]);
+        }
+        if (!there) {
+#pragma unroll
+          for (int i = 0; i < NC; ++i) x[i] = -INFINITY;
+        } else if (slot >= ctx) {
+          const int j = slot - ctx;
+#pragma unroll
+          for (int i = 0; i < NC; ++i)
+            if (a.tree_mask ? !(sm.mask[c0 + i] >> j & 1) : j > sm.node[c0 + i]) x[i] = -INFINITY;
+        }
+        bool high = false;
+#pragma unroll
+        for (int i = 0; i < NC; ++i) high |= fmaf(x[i], scale, -sm.base[c0 + i]) > kRescaleLog2;
+        if (named_bar_red_or(my_bar, 128, high || fail)) {
+          if (named_bar_red_or(my_bar, 128, fail)) { ok = false; break; }
+          // some logit is far above its row's reference: the rows' maxima over the tile
+          float mine = 0.f, mine2 = 0.f;
+#pragma unroll
+          for (int i = 0; i < NC; ++i) {
+            const float top = warp_max(x[i]);
+            if (i < 32) mine = lane == i ? top : mine;
+            else mine2 = lane == i - 32 ? top : mine2;
+          }
+          if (lane < NC) sm.part[quarter][c0 + lane] = mine;
+          if (NC > 32) sm.part[quarter][c0 + 32 + lane] = mine2;
+          named_bar_sync(my_bar, 128);
+          if (at < NC) {
+            const int c = c0 + at;
+            const float top = fmaxf(fmaxf(sm.part[0][c], sm.part[1][c]), fmaxf(sm.part[2][c], sm.part[3][c]));
+            const float was = sm.base[c], now = top == -INFINITY ? was : fmaxf(was, top * scale);
+            sm.base[c] = now;
+            sm.alpha[c] = now == was ? 1.f : cosa::ex2_approx(was - now);
+          }
+          named_bar_sync(my_bar, 128);
+#pragma unroll
+          for (int i = 0; i < NC; ++i) l[i] *= sm.alpha[c0 + i];
+          if (t > pc.t0) {
+            fail = !warp_wait(&sm.pv_done[(tile - 1) & 1], ((tile - 1) / 2) & 1, abort_flag, a.status);
+            if (!fail) {
+              tc_fence_after();
+#pragma unroll 1
+              for (int m = 0; m < S::kBlocks; ++m) {
+#pragma unroll 1
+                for (int i = 0; i < NC; i += 16) {
+                  const uint32_t o = tmem + lanes + S::kTmemO + m * N + c0 + i;
+                  uint32_t v[16];
+                  cosa::tmem_ld16(o, v);
+                  cosa::tmem_wait_ld();
+#pragma unroll
+                  for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * sm.alpha[c0 + i + e]);
+                  cosa::tmem_st16(o, v);
+                }
+              }
+              cosa::tmem_wait_st();
+              tc_fence_before();
+            }
+          }
+        }
+        // P^T's buffer is free once the product before (or before that) has read it
+        constexpr int kBack = S::kPBufs == 2 ? 2 : 1;
+        if (!fail && tile >= kBack)
+          fail = !warp_wait(&sm.pv_done[(tile - kBack) & 1], ((tile - kBack) / 2) & 1, abort_flag, a.status);
+        if (!fail) {
+          uint8_t* p = S::kAlias ? sm.rope[0] : sm.p[S::kPBufs == 2 ? tile & 1 : 0];
+          if (S::kGroups == 2) p += g * kColumn;
+#pragma unroll
+          for (int i = 0; i < NC; i += 8) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) {
+              const float p0 = cosa::ex2_approx(fmaf(x[i + e], scale, -sm.base[c0 + i + e]));
+              const float p1 = cosa::ex2_approx(fmaf(x[i + e + 1], scale, -sm.base[c0 + i + e + 1]));
+              l[i + e] += p0;
+              l[i + e + 1] += p1;
+              w[e / 2] = cosa::pack_bf16x2(p0, p1);
+            }
+            *reinterpret_cast<uint4*>(p + p_offset<S::kPRow>(at, i / 8)) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.p_full[S::kPBufs == 2 ? tile & 1 : 0]);
+        }
+        // a wait that ran out has set the abort flag: the next wait ends too, and its vote stops the group
+      }
+      if (!ok) break;
+      // ---------------- the piece's end ----------------
+      bool fail = false;
+      if (pc.t0 < pc.t1) fail = !warp_wait(&sm.pv_done[(tile - 1) & 1], ((tile - 1) / 2) & 1, abort_flag, a.status);
+      {
+        float mine = 0.f, mine2 = 0.f;
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+          float s = l[i];
+#pragma unroll
+          for (int m = 1; m < 32; m *= 2) s += __shfl_xor_sync(kAll, s, m);
+          if (i < 32) mine = lane == i ? s : mine;
+          else mine2 = lane == i - 32 ? s : mine2;
+        }
+        if (lane < NC) sm.part[quarter][c0 + lane] = mine;
+        if (NC > 32) sm.part[quarter][c0 + 32 + lane] = mine2;
+      }
+      if (named_bar_red_or(my_bar, 128, fail)) { ok = false; break; }
+      if (at < NC) {
+        const int c = c0 + at;
+        const float sum = (sm.part[0][c] + sm.part[1][c]) + (sm.part[2][c] + sm.part[3][c]), m = sm.base[c];
+        if (pc.slot >= 0) {
+          float* ml = a.part_ml + (static_cast<int64_t>(pc.slot) * N + c) * 2;
+          ml[0] = m == kNone ? -INFINITY : m;
+          ml[1] = sum;
+        } else {
+          sm.alpha[c] = sum == 0.f ? 0.f : 1.f / sum;
+          if (a.lse && sm.row[c] >= 0) a.lse[sm.row[c]] = m == kNone ? -INFINITY : (m + log2f(sum)) * kLn2;
+        }
+      }
+      named_bar_sync(my_bar, 128);
+      const bool odd_values = pc.t0 < pc.t1 && *reinterpret_cast<volatile int*>(&sm.odd_values);
+      tc_fence_after();
+      constexpr int kSkip = DV == 64 ? 64 : 0;         // lanes of a block that are keys
+      if (pc.t0 < pc.t1 || pc.slot < 0) {
+#pragma unroll 1
+        for (int m = 0; m < S::kBlocks; ++m) {
+          const int d = m * 128 + at - kSkip;
+#pragma unroll 1
+          for (int i = 0; i < NC; i += 16) {
+            float o[16] = {};
+            if (pc.t0 < pc.t1) load_columns<16>(tmem + lanes + S::kTmemO + m * N + c0 + i, o);
+            if (odd_values && d >= 0) {
+              // what was not finite among the new tokens' values, for the rows that see it
+              for (int s = max(ctx, pc.t0 * kTile); s < min(r.len, pc.t1 * kTile); ++s) {
+                const int phys = table[s >> a.page_shift];
+                if (phys < 0 || phys >= a.num_pages) continue;
+                const int64_t place = (static_cast<int64_t>(phys) << a.page_shift) + (s & ((1 << a.page_shift) - 1));
+                const uint16_t v = S::kLatent ? a.k_cache[place * S::DK + d] : a.v_cache[(place * a.num_kv_heads + pc.head) * DV + d];
+                if ((v & 0x7F80) != 0x7F80) continue;
+                const int j = s - ctx;
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                  if (a.tree_mask ? sm.mask[c0 + i + e] >> j & 1 : j <= sm.node[c0 + i + e]) o[e] += __uint_as_float(static_cast<uint32_t>(v) << 16);
+              }
+            }
+            if (d < 0) continue;
+            if (pc.slot >= 0) {
+              float* to = a.part_o + (static_cast<int64_t>(pc.slot) * N + c0 + i) * DV + d;
+#pragma unroll
+              for (int e = 0; e < 16; ++e) to[e * DV] = o[e];
+            } else {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                const int row = sm.row[c0 + i + e];
+                if (row >= 0)
+                  a.out[static_cast<int64_t>(row) * DV + d] = static_cast<uint16_t>(cosa::pack_bf16x2(o[e] * sm.alpha[c0 + i + e], 0.f));
+              }
+            }
+          }
+        }
+      }
+      tc_fence_before();
+      if (odd_values) {        // the other threads have read it
+        named_bar_sync(kAllBar, kSoftmax);
+        if (tid == 0) sm.odd_values = 0;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 3) {
+    tc_fence_after();
+    cosa::tmem_dealloc(tmem, 512);
+  }
+}
+
+// Joins the parts of the items that several CTAs had: out = sum 2^(m_i - m) o_i / sum 2^(m_i - m) l_i.  blockIdx.x is an item (few
+// items), or a CTA whose share ends inside an item that it began; a block has eight rows of 128 values, or (kWide, where an
+// item has many parts) one row, its warps a part each.
+constexpr int kJoinThreads = 256;
+
+template <int N, int DV, bool kWide>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ Args a, const int by_item) {
+  constexpr int kSeg = DV < 128 ? DV : 128, kSegs = DV / kSeg, kVec = kSeg / 32;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  cosa_kv::wait_for_stream();
+  const int64_t total = total_units<N>(a, false);
+  // the item that holds unit `at`, or item number `at`
+  int b;
+  int64_t before, start;
+  Request r;
+  int64_t item;
+  if (by_item) {
+    int64_t left = blockIdx.x, sum = 0;
+    for (b = 0; b < a.num_reqs; ++b) {
+      r = request_of<N>(a, b);
+      const int64_t items = static_cast<int64_t>(a.num_kv_heads) * r.row_tiles;
+      if (left < items) break;
+      left -= items;
+      sum += units_of(a, r);
+    }
+    if (b == a.num_reqs) return;
+    item = left;
+    before = sum;
+    start = before + item * (r.tiles + 1);
+  } else {
+    const int64_t at = share(total, blockIdx.x + 1);
+    if (at >= total) return;
+    find_request<N>(a, at, b, before);
+    r = request_of<N>(a, b);
+    item = (at - before) / (r.tiles + 1);
+    start = before + item * (r.tiles + 1);
+    if (start == at || start < share(total, blockIdx.x)) return;      // not cut here, or begun before this CTA
+  }
+  const int64_t end = start + r.tiles + 1;
+  // the CTAs that have the item: c0 has unit start, c1 unit end - 1
+  auto owner = [&](int64_t u) {
+    int c = static_cast<int>(total < kCtas ? u : min(static_cast<int64_t>(kCtas - 1), u * kCtas / total));
+    while (share(total, c + 1) <= u) ++c;
+    while (share(total, c) > u) --c;
+    return c;
+  };
+  const int first = owner(start), last = owner(end - 1);
+  if (first == last) return;
+  const int parts = last - first + 1;
+  const int head = static_cast<int>(item / r.row_tiles), row_tile = static_cast<int>(item % r.row_tiles);
+  const int seg = blockIdx.z;
+  const int c = kWide ? blockIdx.y : blockIdx.y * 8 + warp;      // row of the tile
+  const int64_t row = static_cast<int64_t>(row_tile) * N + c;
+  const bool live = row < static_cast<int64_t>(r.n) * a.group;
+  if (kWide ? !live : false) return;
+  auto slot = [&](int i) { return 2 * (first + i) + (i == 0 && share(total, first) < start ? 1 : 0); };
+  __shared__ float weight[kWide ? 1 : 8][kCtas + 8];
+  __shared__ float sums[8][kSeg];
+  float* w = weight[kWide ? 0 : warp];
+  // weights of the parts, by every warp of its own (kWide: all the same ones, by the first)
+  float m = -INFINITY, sum = 0.f;
+  if (live) {
+    for (int i = lane; i < parts; i += 32) m = fmaxf(m, a.part_ml[(static_cast<int64_t>(slot(i)) * N + c) * 2]);
+#pragma unroll
+    for (int k = 1; k < 32; k *= 2) m = fmaxf(m, __shfl_xor_sync(kAll, m, k));
+    for (int i = lane; i < parts; i += 32) {
+      const float* ml = a.part_ml + (static_cast<int64_t>(slot(i)) * N + c) * 2;
+      const float f = ml[0] == -INFINITY ? 0.f : exp2f(ml[0] - m);
+      // a part whose rows saw nothing may have no o; NaN is kept
+      sum += f == 0.f && ml[1] == 0.f ? 0.f : f * ml[1];
+      if (!kWide || warp == 0) w[i] = ml[0] == -INFINITY ? -1.f : f;
+    }
+#pragma unroll
+    for (int k = 1; k < 32; k *= 2) sum += __shfl_xor_sync(kAll, sum, k);
+  }
+  __syncthreads();
+  float o[kVec] = {};
+  if (live) {
+    const float* base = a.part_o + static_cast<int64_t>(c) * DV + seg * kSeg + lane * kVec;
+#pragma unroll 8
+    for (int i = kWide ? warp : 0; i < parts; i += kWide ? 8 : 1) {
+      const float f = w[i];
+      if (f < 0.f) continue;
+      const float* p = base + static_cast<int64_t>(slot(i)) * N * DV;
+      if constexpr (kVec == 4) {
+        const float4 x = *reinterpret_cast<const float4*>(p);
+        o[0] = fmaf(f, x.x, o[0]); o[1] = fmaf(f, x.y, o[1]); o[2] = fmaf(f, x.z, o[2]); o[3] = fmaf(f, x.w, o[3]);
+      } else {
+        const float2 x = *reinterpret_cast<const float2*>(p);
+        o[0] = fmaf(f, x.x, o[0]); o[1] = fmaf(f, x.y, o[1]);
+      }
+    }
+  }
+  if constexpr (kWide) {
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) sums[warp][lane * kVec + e] = o[e];
+    __syncthreads();
+    if (warp != 0) return;
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) {
+      o[e] = 0.f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) o[e] += sums[k][lane * kVec + e];
+    }
+  }
+  if (!live) return;
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  const int64_t to = (r.tok0 + row / a.group) * a.num_q_heads + head * a.group + row % a.group;
+  uint16_t* dst = a.out + to * DV + seg * kSeg + lane * kVec;
+  if constexpr (kVec == 4)
+    *reinterpret_cast<uint2*>(dst) = make_uint2(cosa::pack_bf16x2(o[0] * inv, o[1] * inv), cosa::pack_bf16x2(o[2] * inv, o[3] * inv));
+  else
+    *reinterpret_cast<uint32_t*>(dst) = cosa::pack_bf16x2(o[0] * inv, o[1] * inv);
+  if (a.lse && seg == 0 && lane == 0) a.lse[to] = m == -INFINITY && sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
+}
+
+int rows_of_tile(const PagedLaunch& L) {
+  const int64_t rows = static_cast<int64_t>(L.max_new_tokens) * (L.num_q_heads / L.num_kv_heads);
+  const int most = L.latent_dim ? 64 : 128;
+  int n = 16;
+  while (n < most && n < rows) n *= 2;
+  return n;
+}
+
+template <class S>
+cudaError_t launch_shape(const PagedLaunch& L, cudaStream_t stream) {
+  Args a{};
+  a.q = L.q;
+  a.q_rope = L.q_rope;
+  a.k_cache = L.k_cache;
+  a.v_cache = L.v_cache;
+  a.cu_seqlens = L.cu_seqlens;
+  a.page_table = L.page_table;
+  a.kv_len = L.kv_len;
+  a.tree_mask = L.tree_mask;
+  a.out = L.out;
+  a.lse = L.lse;
+  a.part_o = static_cast<float*>(L.workspace);
+  a.part_ml = a.part_o + static_cast<size_t>(2 * kCtas) * S::N * S::DV;
+  a.status = L.status;
+  a.q_stride = L.q_stride;
+  a.q_rope_stride = L.q_rope_stride;
+  a.num_reqs = L.num_reqs;
+  a.num_q_heads = L.num_q_heads;
+  a.num_kv_heads = L.num_kv_heads;
+  a.group = L.num_q_heads / L.num_kv_heads;
+  a.page_shift = L.page_shift;
+  a.total_tokens = L.total_tokens;
+  a.max_seqlen = L.max_seqlen;
+  a.num_pages = L.num_pages;
+  a.max_pages_per_req = L.max_pages_per_req;
+  a.scale_log2 = L.scale_log2;
+  a.stall = L.stall;
+  // the caches as (64 values, row of a page, 64-value column, head); a copy has the rows of a page
+  CUtensorMap kmap, vmap;
+  const uint64_t rows = static_cast<uint64_t>(L.num_pages) * L.page_size, pitch = static_cast<uint64_t>(S::kLatent ? 1 : L.num_kv_heads) * S::DK * 2;
+  const uint64_t dims[4] = {64, rows, S::DK / 64, static_cast<uint64_t>(S::kLatent ? 1 : L.num_kv_heads)};
+  const uint64_t strides[3] = {pitch, 128, S::DK * 2};
+  const uint32_t box[4] = {64, static_cast<uint32_t>(L.page_size), 1, 1};
+  if (!encode_bf16(&kmap, L.k_cache, dims, strides, box)) return cudaErrorInvalidValue;
+  if (S::kLatent) vmap = kmap;
+  else if (!encode_bf16(&vmap, L.v_cache, dims, strides, box)) return cudaErrorInvalidValue;
+
+  const size_t smem = sizeof(Smem<S>) + 1024;
+  static_assert(sizeof(Smem<S>) + 1024 <= 227 * 1024, "shared memory");
+  auto* kernel = paged_kernel<S>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  e = cosa_kv::launch_after(kernel, dim3(kCtas), S::kThreads, smem, stream, 1, kmap, vmap, a);
+  if (e != cudaSuccess) return e;
+  // at most so many items: what the tokens fill and a part of a row tile for every request
+  const int64_t items = L.num_kv_heads * ((static_cast<int64_t>(L.total_tokens) * a.group) / S::N + L.num_reqs);
+  const bool by_item = items <= kCtas;
+  const unsigned segs = S::DV < 128 ? 1 : S::DV / 128;
+  const unsigned x = static_cast<unsigned>(by_item ? items : kCtas - 1);
+  if (items <= 8)
+    return cosa_kv::launch_after(join_kernel<S::N, S::DV, true>, dim3(x, S::N, segs), kJoinThreads, 0, stream, 1, a, by_item ? 1 : 0);
+  return cosa_kv::launch_after(join_kernel<S::N, S::DV, false>, dim3(x, S::N / 8, segs), kJoinThreads, 0, stream, 1, a, by_item ? 1 : 0);
+}
+
+template <int DK, int DV, bool LATENT>
+cudaError_t launch_width(const PagedLaunch& L, cudaStream_t stream) {
+  switch (rows_of_tile(L)) {
+    case 16: return launch_shape<Shape<DK, DV, LATENT, 16>>(L, stream);
+    case 32: return launch_shape<Shape<DK, DV, LATENT, 32>>(L, stream);
+    case 64: return launch_shape<Shape<DK, DV, LATENT, 64>>(L, stream);
+    default:
+      if constexpr (!LATENT) return launch_shape<Shape<DK, DV, LATENT, 128>>(L, stream);
+      return cudaErrorInvalidValue;
+  }
 }
 
 }  // namespace
 
-size_t paged_workspace_bytes(const PagedLaunch&) { return 256; }
+size_t paged_workspace_bytes(const PagedLaunch& L) {
+  const size_t dv = static_cast<size_t>(L.latent_dim ? L.latent_dim : L.head_dim);
+  return static_cast<size_t>(2 * kCtas) * rows_of_tile(L) * (dv + 2) * sizeof(float);
+}
 
 cudaError_t launch_paged(const PagedLaunch& L, cudaStream_t stream) {
-  const int64_t rows = static_cast<int64_t>(L.total_tokens) * L.num_q_heads;
-  const unsigned grid = static_cast<unsigned>((rows * 32 + kThreads - 1) / kThreads);
-  auto* kernel = L.latent_dim == 512   ? row_kernel<576, 512, true>
-                 : L.latent_dim == 256 ? row_kernel<320, 256, true>
-                 : L.head_dim == 128   ? row_kernel<128, 128, false>
-                                       : row_kernel<64, 64, false>;
-  return cosa_kv::launch_after(kernel, dim3(grid), kThreads, 0, stream, 1, L);
+  if (L.latent_dim == 512) return launch_width<576, 512, true>(L, stream);
+  if (L.latent_dim == 256) return launch_width<320, 256, true>(L, stream);
+  return L.head_dim == 128 ? launch_width<128, 128, false>(L, stream) : launch_width<64, 64, false>(L, stream);
 }
 
 }  // namespace cosa_attn
