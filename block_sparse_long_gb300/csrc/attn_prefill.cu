@@ -1,77 +1,514 @@
-// Causal attention of packed prompts in the expanded form of latent attention.
+// Causal attention of packed prompts in the expanded form of latent attention: per head keys of d + 64 values (the last 64 shared
+// by the heads) and values of d.
 //
-// A warp has a query row (token, head) and walks its keys, 32-bit sums in registers, with the running maximum and sum of the
-// softmax.
+//     S = Q K^T,  P = exp2(S * scale - m),  O = sum P V,  l = sum P,  out = O / l
+//
+// With hundreds of queries to a key the matrix products bound it: 2 (2 d + 64) operations per visible pair.  A CTA has 256
+// queries of one head in two tiles of 128 rows, which share every block of 128 keys; while one tile's softmax runs, the
+// tensor core has the other tile's products.  All of TMEM is in use: S and O of both tiles (P goes over its S).
+//
+// Warp roles:
+//   warp 0      copies Q once, then K and V block by block (TMA).  Of the blocks on the diagonal, whose later keys some rows must
+//               not see, it clears from V what is not finite (0 times that is not 0); a row that does see such a value gets it
+//               added at the end.
+//   warps 1, 2  issue S and O of one tile each: S(j + 1) follows O(j) in the same thread's order, so P may lie over S.
+//   warp 3      owns the TMEM.
+//   warps 4-11  softmax, four warps a tile: a thread has a row.  The reference m lags the maximum by 2^8 at most, O is scaled only
+//               when it moves.
+// CTAs start with the longest rows of a head and go head by head, so that a head's keys stay in L2.
+#include <cmath>
 #include <cstdint>
 
+#include <cuda.h>
+#include <cuda_runtime.h>
+
 #include "attn_internal.h"
+#include "attn_tma.h"
 #include "kv_internal.h"
 #include "kv_layout.cuh"
 
 namespace cosa_attn {
 namespace {
 
-constexpr int kThreads = 128;
-constexpr int kRot = COSA_ATTN_ROPE_DIM;
-constexpr unsigned kAll = 0xffffffffu;
+using cosa::mbar_arrive;
+using cosa::mbar_arrive_expect_tx;
+using cosa::mbar_init;
+using cosa::smem_desc_sw128;
+using cosa::smem_u32;
+using cosa::tc_fence_after;
+using cosa::tc_fence_before;
+using cosa::umma_commit;
+using cosa::wait_parity_bounded;
 
-__device__ __forceinline__ float value(const uint16_t* p) { return __uint_as_float(static_cast<uint32_t>(*p) << 16); }
+constexpr int kThreads = 384;
+constexpr int kBlock = 128;                // keys
+constexpr int kRows = 256;                 // queries of a CTA
+constexpr int kColumn = kBlock * 128;      // bytes of a 64-value wide column of 128 rows
+constexpr float kRescaleLog2 = 8.0f;
+constexpr float kLn2 = 0.69314718055994531f;
+constexpr unsigned kAll = 0xffffffffu;
+constexpr uint32_t kTmemS = 0, kTmemO = 256;      // two of 128 columns each
+
+template <int D_>
+struct Shape {
+  static constexpr int D = D_;
+  static constexpr int kKeyColumns = D / 64 + 1, kValueColumns = D / 64;
+  static constexpr int kKeySlots = D == 128 ? 4 : 6;       // of one column
+  static constexpr int kValueSlots = D == 128 ? 2 : 3;     // of a block
+};
+
+template <class S>
+struct alignas(1024) Smem {
+  uint8_t q[2][S::kKeyColumns][kColumn];
+  uint8_t k[S::kKeySlots][kColumn];
+  uint8_t v[S::kValueSlots][S::kValueColumns][kColumn];
+  uint64_t q_full, k_full[S::kKeySlots], k_empty[S::kKeySlots], v_full[S::kValueSlots], v_empty[S::kValueSlots];
+  uint64_t v_clear[4];                     // of the blocks on the diagonal
+  uint64_t s_full[2], p_full[2], pv_done[2], cleanup;
+  int32_t req, block;                      // this CTA's request (-1: none) and its block of queries
+  int32_t odd_values;
+  uint32_t tmem_base;
+  int32_t abort_flag;
+};
+
+struct Args {
+  const int32_t *cu_seqlens, *cu_kv;
+  const uint16_t* v;
+  uint16_t* out;
+  float* lse;
+  int32_t* status;
+  int64_t v_stride, v_head_stride;
+  int num_reqs, num_heads, total_tokens, total_kv_tokens, blocks;
+  float scale_log2;
+  int stall;
+};
+
+struct Request {
+  int tok0, n;
+  int64_t from, keys;      // key rows from .. from + keys - 1
+  bool bad;                // rows are out of range (n = 0), or the keys are (keys = 0)
+};
+
+__device__ __forceinline__ Request request_of(const Args& a, int b) {
+  Request r;
+  r.tok0 = a.cu_seqlens[b];
+  const int64_t n = static_cast<int64_t>(a.cu_seqlens[b + 1]) - r.tok0;
+  r.from = a.cu_kv[b];
+  r.keys = a.cu_kv[b + 1] - r.from;
+  r.bad = r.tok0 < 0 || n < 0 || r.tok0 + n > a.total_tokens;
+  r.n = r.bad ? 0 : static_cast<int>(n);
+  if (r.n > 0 && (r.from < 0 || r.keys < n || r.from + r.keys > a.total_kv_tokens)) {
+    r.bad = true;
+    r.keys = 0;
+  }
+  return r;
+}
+
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status) {
+  return __all_sync(kAll, wait_parity_bounded(bar, parity, abort_flag, status));
+}
+
+__device__ __forceinline__ bool odd(uint32_t two) {        // either bf16 is not finite
+  return (two & 0x7F80u) == 0x7F80u || (two & 0x7F800000u) == 0x7F800000u;
+}
+
+template <class S>
+__global__ void __launch_bounds__(kThreads, 1)
+    prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap qrmap, const __grid_constant__ CUtensorMap kmap,
+                   const __grid_constant__ CUtensorMap krmap, const __grid_constant__ CUtensorMap vmap, const __grid_constant__ Args a) {
+  constexpr int D = S::D, KC = S::kKeyColumns, VC = S::kValueColumns;
+  extern __shared__ uint8_t smem_raw[];
+  Smem<S>& sm = *reinterpret_cast<Smem<S>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  volatile int* abort_flag = &sm.abort_flag;
+  cosa_kv::wait_for_stream();
+
+  const int head = blockIdx.x / a.blocks;
+  if (warp == 0) {
+    // block `at` of the list of all requests' blocks
+    int64_t at = blockIdx.x % a.blocks;
+    int req = -1;
+    for (int b0 = 0; b0 < a.num_reqs && (req < 0 || blockIdx.x == 0); b0 += 32) {
+      const Request r = request_of(a, min(b0 + lane, a.num_reqs - 1));
+      if (blockIdx.x == 0 && r.bad) cosa::report_status(a.status, cosa::kStatusBadInput);
+      const int64_t mine = b0 + lane < a.num_reqs ? (r.n + kRows - 1) / kRows : 0;
+      int64_t upto = mine;
+#pragma unroll
+      for (int m = 1; m < 32; m *= 2) {
+        const int64_t x = __shfl_up_sync(kAll, upto, m);
+        if (lane >= m) upto += x;
+      }
+      const unsigned past = __ballot_sync(kAll, upto > at);
+      if (past && req < 0) {
+        const int l = __ffs(past) - 1;
+        req = b0 + l;
+        const int64_t in = at - __shfl_sync(kAll, upto - mine, l), all = __shfl_sync(kAll, mine, l);
+        if (lane == 0) sm.block = static_cast<int>(all - 1 - in);      // the longest rows first
+      }
+      at -= __shfl_sync(kAll, upto, 31);
+    }
+    if (lane == 0) {
+      sm.req = req;
+      if (blockIdx.x == 0 && (a.cu_seqlens[0] != 0 || a.cu_seqlens[a.num_reqs] > a.total_tokens)) cosa::report_status(a.status, cosa::kStatusBadInput);
+    }
+  } else if (warp == 1 && lane == 0) {
+    mbar_init(&sm.q_full, 1);
+    for (int s = 0; s < S::kKeySlots; ++s) {
+      mbar_init(&sm.k_full[s], 1);
+      mbar_init(&sm.k_empty[s], 2);        // both tiles
+    }
+    for (int s = 0; s < S::kValueSlots; ++s) {
+      mbar_init(&sm.v_full[s], 1);
+      mbar_init(&sm.v_empty[s], 2);
+    }
+    for (int s = 0; s < 4; ++s) mbar_init(&sm.v_clear[s], 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&sm.s_full[s], 1);
+      mbar_init(&sm.p_full[s], 4);
+      mbar_init(&sm.pv_done[s], 1);
+    }
+    mbar_init(&sm.cleanup, 2);
+    sm.abort_flag = 0;
+    sm.odd_values = 0;
+    cosa::fence_mbarrier_init();
+  } else if (warp == 3) {
+    cosa::tmem_alloc(&sm.tmem_base, 512);
+    cosa::tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem_base;
+
+  if (sm.req >= 0) {
+    const Request r = request_of(a, sm.req);
+    const int q0 = sm.block * kRows;
+    const int64_t lim0 = r.keys - r.n + q0;       // last key that the first row sees
+    // blocks of keys of each tile
+    auto blocks_of = [&](int i) {
+      const int first = q0 + i * 128;
+      return r.keys == 0 || first >= r.n ? 0 : static_cast<int>((r.keys - r.n + min(first + 127, r.n - 1)) / kBlock) + 1;
+    };
+    const int nb0 = blocks_of(0), nb1 = blocks_of(1), nb = max(nb0, nb1);
+    const int diagonal = static_cast<int>((lim0 + 1) / kBlock);      // first block with keys that some row does not see
+
+    if (warp == 0) {
+      // =========================== copies ===========================
+      const int tok = r.tok0 + q0, key = static_cast<int>(r.from);
+      int64_t column = 0;
+      int values = 0;
+      bool ok = !a.stall && nb > 0;
+      if (ok && lane == 0) {
+        cosa::tma_prefetch_desc(&kmap);
+        cosa::tma_prefetch_desc(&vmap);
+        mbar_arrive_expect_tx(&sm.q_full, 2 * KC * kColumn);
+        for (int i = 0; i < 2; ++i) {
+          for (int c = 0; c < VC; ++c) cosa::tma_load_4d(sm.q[i][c], &qmap, &sm.q_full, 0, tok + i * 128, c, head);
+          cosa::tma_load_4d(sm.q[i][VC], &qrmap, &sm.q_full, 0, tok + i * 128, 0, head);
+        }
+      }
+      // what no row may multiply by 0: keys behind the request's, and what is not finite among those that some row does not see
+      auto clear = [&](int j) {
+        const int s = j % S::kValueSlots;
+        if (!warp_wait(&sm.v_full[s], (j / S::kValueSlots) & 1, abort_flag, a.status)) return false;
+        const int64_t k0 = static_cast<int64_t>(j) * kBlock;
+        const int first = static_cast<int>(max(lim0 + 1 - k0, static_cast<int64_t>(0)));
+        bool found = false;
+        for (int e = first * VC * 8 + lane; e < kBlock * VC * 8; e += 32) {
+          const int row = e / (VC * 8), c = e % (VC * 8);
+          uint4* at = reinterpret_cast<uint4*>(&sm.v[s][c / 8][row * 128 + (c & 7) * 16]);
+          uint4 x = *at;
+          if (k0 + row >= r.keys) {
+            *at = make_uint4(0, 0, 0, 0);
+          } else if (odd(x.x) || odd(x.y) || odd(x.z) || odd(x.w)) {
+            found = true;
+            uint32_t* w = reinterpret_cast<uint32_t*>(&x);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              if ((w[i] & 0x7F80u) == 0x7F80u) w[i] &= 0xFFFF0000u;
+              if ((w[i] & 0x7F800000u) == 0x7F800000u) w[i] &= 0xFFFFu;
+            }
+            *at = x;
+          }
+        }
+        cosa::fence_proxy_async_smem();
+        found = __any_sync(kAll, found);
+        if (lane == 0) {
+          if (found) sm.odd_values = 1;
+          mbar_arrive(&sm.v_clear[j - diagonal]);
+        }
+        __syncwarp();
+        return true;
+      };
+      for (int j = 0; j < nb && ok; ++j) {
+        for (int c = 0; c < KC && ok; ++c) {
+          const int s = static_cast<int>(column % S::kKeySlots);
+          if (column >= S::kKeySlots) ok = warp_wait(&sm.k_empty[s], (column / S::kKeySlots - 1) & 1, abort_flag, a.status);
+          if (!ok) break;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&sm.k_full[s], kColumn);
+            if (c < VC) cosa::tma_load_4d(sm.k[s], &kmap, &sm.k_full[s], 0, key + j * kBlock, c, head);
+            else cosa::tma_load_4d(sm.k[s], &krmap, &sm.k_full[s], 0, key + j * kBlock, 0, 0);
+          }
+          ++column;
+        }
+        const int s = j % S::kValueSlots;
+        if (ok && j >= S::kValueSlots) ok = warp_wait(&sm.v_empty[s], (j / S::kValueSlots - 1) & 1, abort_flag, a.status);
+        if (!ok) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&sm.v_full[s], VC * kColumn);
+          for (int c = 0; c < VC; ++c) cosa::tma_load_4d(sm.v[s][c], &vmap, &sm.v_full[s], 0, key + j * kBlock, c, head);
+        }
+        ++values;
+        __syncwarp();
+        if (j - 1 >= diagonal) ok = clear(j - 1);
+      }
+      if (ok && nb - 1 >= diagonal) clear(nb - 1);
+      // every copy lands before the CTA ends
+      if (lane == 0 && !a.stall && nb > 0) {
+        wait_parity_bounded(&sm.q_full, 0, nullptr, nullptr);
+        for (int s = 0; s < S::kKeySlots; ++s) {
+          const int64_t issued = (column - s + S::kKeySlots - 1) / S::kKeySlots;
+          if (issued > 0) wait_parity_bounded(&sm.k_full[s], (issued - 1) & 1, nullptr, nullptr);
+        }
+        for (int s = 0; s < S::kValueSlots; ++s) {
+          const int issued = (values - s + S::kValueSlots - 1) / S::kValueSlots;
+          if (issued > 0) wait_parity_bounded(&sm.v_full[s], (issued - 1) & 1, nullptr, nullptr);
+        }
+      }
+      __syncwarp();
+    } else if (warp == 1 || warp == 2) {
+      // =========================== products of one tile ===========================
+      if (lane == 0) {
+        const int i = warp - 1, mine = i ? nb1 : nb0;
+        constexpr uint32_t idesc_s = cosa::idesc_bf16_f32(128, kBlock, false, false), idesc_o = cosa::idesc_bf16_f32(128, D, false, true);
+        const uint64_t qd = smem_desc_sw128(smem_u32(sm.q[i]), 16, 1024), kd = smem_desc_sw128(smem_u32(sm.k), 16, 1024);
+        const uint64_t vd = smem_desc_sw128(smem_u32(sm.v), kColumn, 1024);
+        const uint32_t s_at = tmem + kTmemS + i * 128, o_at = tmem + kTmemO + i * 128;
+        int64_t column = 0;
+        bool ok = nb == 0 || wait_parity_bounded(&sm.q_full, 0, abort_flag, a.status);
+        // S of block j, or, behind the tile's last block, only the slots' release
+        auto scores = [&](int j) {
+#pragma unroll 1
+          for (int c = 0; c < KC; ++c, ++column) {
+            const int s = static_cast<int>(column % S::kKeySlots);
+            if (!wait_parity_bounded(&sm.k_full[s], (column / S::kKeySlots) & 1, abort_flag, a.status)) return false;
+            if (j >= mine) {
+              mbar_arrive(&sm.k_empty[s]);
+              continue;
+            }
+            tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              cosa::umma_ss(s_at, qd + ((c * kColumn + k * 32) >> 4), kd + ((s * kColumn + k * 32) >> 4), idesc_s, c > 0 || k > 0);
+            umma_commit(&sm.k_empty[s]);
+          }
+          if (j < mine) umma_commit(&sm.s_full[i]);
+          return true;
+        };
+        if (ok && nb > 0) ok = scores(0);
+        for (int j = 0; j < nb && ok; ++j) {
+          const int s = j % S::kValueSlots;
+          if (j < mine) ok = wait_parity_bounded(&sm.p_full[i], j & 1, abort_flag, a.status);
+          ok = ok && wait_parity_bounded(&sm.v_full[s], (j / S::kValueSlots) & 1, abort_flag, a.status);
+          if (ok && j >= diagonal) ok = wait_parity_bounded(&sm.v_clear[j - diagonal], 0, abort_flag, a.status);
+          if (!ok) break;
+          if (j < mine) {
+            tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < kBlock / 16; ++k)
+              cosa::umma_ts(o_at, s_at + k * 8, vd + ((s * VC * kColumn + k * 2048) >> 4), idesc_o, j > 0 || k > 0);
+            umma_commit(&sm.v_empty[s]);
+            umma_commit(&sm.pv_done[i]);
+          } else {
+            mbar_arrive(&sm.v_empty[s]);
+          }
+          if (j + 1 < nb) ok = scores(j + 1);
+        }
+        umma_commit(&sm.cleanup);
+        wait_parity_bounded(&sm.cleanup, 0, nullptr, nullptr);
+      }
+      __syncwarp();
+    } else if (warp >= 4) {
+      // =========================== softmax ===========================
+      const int i = warp / 4 - 1, mine = i ? nb1 : nb0;
+      const int t = (warp % 4) * 32 + lane, pos = q0 + i * 128 + t;
+      const uint32_t lanes = static_cast<uint32_t>((warp % 4) * 32) << 16;
+      const uint32_t s_at = tmem + lanes + kTmemS + i * 128, o_at = tmem + lanes + kTmemO + i * 128;
+      const int64_t lim = r.keys - r.n + pos;      // last key that the row sees
+      const float scale = a.scale_log2;
+      float ref = -INFINITY, l = 0.f;
+      bool ok = true;
+      for (int j = 0; j < mine; ++j) {
+        if (!warp_wait(&sm.s_full[i], j & 1, abort_flag, a.status)) { ok = false; break; }
+        tc_fence_after();
+        uint32_t x0[64], x1[64];
+        float top, top1;
+        cosa::tmem_ld64_max(s_at, x0, top);
+        cosa::tmem_ld64_max(s_at + 64, x1, top1);
+        cosa::tmem_wait_ld();
+        cosa::reg_after_wait(top);
+        cosa::reg_after_wait(top1);
+        top = fmaxf(top, top1);
+        const int64_t left = lim - static_cast<int64_t>(j) * kBlock;
+        if (left < kBlock - 1) {       // keys that the row does not see: the maximum again without them
+          const int last = static_cast<int>(max(left, static_cast<int64_t>(-1)));
+          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int e = 0; e < 64; ++e) {
+            if (e > last) x0[e] = 0xFF800000u;
+            if (e + 64 > last) x1[e] = 0xFF800000u;
+            m4[e & 3] = fmaxf(m4[e & 3], fmaxf(__uint_as_float(x0[e]), __uint_as_float(x1[e])));
+          }
+          top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+        }
+        top = top == -INFINITY ? top : top * scale;
+        float alpha = 1.f;
+        bool moved = false;
+        if (ref == -INFINITY) {
+          ref = top;
+        } else if (top > ref + kRescaleLog2) {
+          alpha = cosa::ex2_approx(ref - top);
+          ref = top;
+          l *= alpha;
+          moved = true;
+        }
+        const float base = ref == -INFINITY ? 0.f : ref;
+        float sum[4] = {};
+        auto weights = [&](const uint32_t(&x)[64], uint32_t to) {
+          uint32_t w[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            float a0, a1;
+            cosa::fma2_bc(a0, a1, __uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]), scale, -base);
+            const float p0 = cosa::ex2_approx(a0), p1 = cosa::ex2_approx(a1);
+            cosa::add2_acc(sum[(e & 1) * 2], sum[(e & 1) * 2 + 1], p0, p1);
+            w[e] = cosa::pack_bf16x2(p0, p1);
+          }
+          cosa::tmem_st32(to, w);
+        };
+        weights(x0, s_at);
+        weights(x1, s_at + 32);
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        cosa::tmem_wait_st();
+        if (__any_sync(kAll, moved) && j > 0) {
+          if (!warp_wait(&sm.pv_done[i], (j - 1) & 1, abort_flag, a.status)) { ok = false; break; }
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < D; c += 16) {
+            uint32_t o[16];
+            cosa::tmem_ld16(o_at + c, o);
+            cosa::tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+            cosa::tmem_st16(o_at + c, o);
+          }
+          cosa::tmem_wait_st();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.p_full[i]);
+      }
+      if (ok && mine > 0) ok = warp_wait(&sm.pv_done[i], (mine - 1) & 1, abort_flag, a.status);
+      if (ok) {
+        tc_fence_after();
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const int64_t row = static_cast<int64_t>(r.tok0 + pos) * a.num_heads + head;
+        const bool live = pos < r.n;
+        if (live && a.lse) a.lse[row] = l == 0.f ? -INFINITY : (ref + log2f(l)) * kLn2;
+        const bool odd_values = mine > 0 && *reinterpret_cast<volatile int*>(&sm.odd_values);
+#pragma unroll 1
+        for (int c = 0; c < D; c += 16) {
+          uint32_t o[16];
+          if (mine > 0) {
+            cosa::tmem_ld16(o_at + c, o);
+            cosa::tmem_wait_ld();
+          } else {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = 0;
+          }
+          if (!live) continue;
+          float f[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) f[e] = __uint_as_float(o[e]);
+          if (odd_values) {
+            // what was not finite among the values on the diagonal, for the rows that see it
+            for (int64_t s = lim0 + 1; s <= lim; ++s) {
+              const uint16_t* v = a.v + (r.from + s) * a.v_stride + head * a.v_head_stride + c;
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                if ((v[e] & 0x7F80) == 0x7F80) f[e] += __uint_as_float(static_cast<uint32_t>(v[e]) << 16);
+            }
+          }
+          uint32_t w[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) w[e] = cosa::pack_bf16x2(f[2 * e] * inv, f[2 * e + 1] * inv);
+          uint4* to = reinterpret_cast<uint4*>(a.out + row * D + c);
+          to[0] = make_uint4(w[0], w[1], w[2], w[3]);
+          to[1] = make_uint4(w[4], w[5], w[6], w[7]);
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 3) {
+    tc_fence_after();
+    cosa::tmem_dealloc(tmem, 512);
+  }
+}
 
 template <int D>
-__global__ void __launch_bounds__(kThreads) row_kernel(const PrefillLaunch L) {
-  cosa_kv::wait_for_stream();
-  const int lane = threadIdx.x % 32;
-  const int64_t row = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) / 32;
-  const int64_t t = row / L.num_heads;
-  const int h = static_cast<int>(row % L.num_heads);
-  if (t >= L.total_tokens) return;
-  int b = 0;
-  while (b < L.num_reqs && L.cu_seqlens[b + 1] <= t) ++b;
-  if (b == L.num_reqs) return;
-  const int32_t* cu_kv = L.cu_kv ? L.cu_kv : L.cu_seqlens;
-  const int first = L.cu_seqlens[b], n = L.cu_seqlens[b + 1] - first, i = static_cast<int>(t) - first;
-  if (i < 0 || first < 0 || L.cu_seqlens[b + 1] > L.total_tokens) {
-    cosa::report_status(L.status, cosa::kStatusBadInput);
-    return;
+cudaError_t launch_shape(const PrefillLaunch& L, cudaStream_t stream) {
+  using S = Shape<D>;
+  Args a{};
+  a.cu_seqlens = L.cu_seqlens;
+  a.cu_kv = L.cu_kv ? L.cu_kv : L.cu_seqlens;
+  a.v = L.v;
+  a.out = L.out;
+  a.lse = L.lse;
+  a.status = L.status;
+  a.v_stride = L.v_stride;
+  a.v_head_stride = L.v_head_stride;
+  a.num_reqs = L.num_reqs;
+  a.num_heads = L.num_heads;
+  a.total_tokens = L.total_tokens;
+  a.total_kv_tokens = L.total_kv_tokens;
+  a.scale_log2 = L.scale_log2;
+  a.stall = L.stall;
+  // at most so many blocks of queries: what the tokens fill and a part of one for every request
+  const int64_t blocks = L.total_tokens / kRows + L.num_reqs;
+  if (blocks * L.num_heads > INT32_MAX) return cudaErrorInvalidValue;
+  a.blocks = static_cast<int>(blocks);
+  // rows as (64 values, token, 64-value column, head)
+  CUtensorMap maps[5];
+  const struct {
+    const void* base;
+    int64_t tokens, width, heads, stride, head_stride;
+  } t[5] = {{L.q, L.total_tokens, D, L.num_heads, L.q_stride, L.q_head_stride},
+            {L.q_rope, L.total_tokens, 64, L.num_heads, L.q_rope_stride, L.q_rope_head_stride},
+            {L.k, L.total_kv_tokens, D, L.num_heads, L.k_stride, L.k_head_stride},
+            {L.k_rope, L.total_kv_tokens, 64, 1, L.k_rope_stride, 64},
+            {L.v, L.total_kv_tokens, D, L.num_heads, L.v_stride, L.v_head_stride}};
+  const uint32_t box[4] = {64, 128, 1, 1};
+  for (int i = 0; i < 5; ++i) {
+    const uint64_t dims[4] = {64, static_cast<uint64_t>(t[i].tokens), static_cast<uint64_t>(t[i].width / 64), static_cast<uint64_t>(t[i].heads)};
+    const uint64_t strides[3] = {static_cast<uint64_t>(t[i].stride) * 2, 128, static_cast<uint64_t>(t[i].head_stride) * 2};
+    if (!encode_bf16(&maps[i], t[i].base, dims, strides, box)) return cudaErrorInvalidValue;
   }
-  const int64_t from = cu_kv[b];
-  int64_t len = cu_kv[b + 1] - from;
-  if (from < 0 || len < n || from + len > L.total_kv_tokens) {
-    cosa::report_status(L.status, cosa::kStatusBadInput);
-    len = 0;
-  }
-  float q[D / 32], qr[kRot / 32], o[D / 32] = {}, m = -INFINITY, l = 0.f;
-#pragma unroll
-  for (int e = 0; e < D / 32; ++e) q[e] = value(L.q + t * L.q_stride + h * L.q_head_stride + e * 32 + lane);
-#pragma unroll
-  for (int e = 0; e < kRot / 32; ++e) qr[e] = value(L.q_rope + t * L.q_rope_stride + h * L.q_rope_head_stride + e * 32 + lane);
-  for (int64_t s = from; s < from + len - n + i + 1 && len; ++s) {
-    float x = 0.f;
-#pragma unroll
-    for (int e = 0; e < D / 32; ++e) x = fmaf(q[e], value(L.k + s * L.k_stride + h * L.k_head_stride + e * 32 + lane), x);
-#pragma unroll
-    for (int e = 0; e < kRot / 32; ++e) x = fmaf(qr[e], value(L.k_rope + s * L.k_rope_stride + e * 32 + lane), x);
-#pragma unroll
-    for (int w = 1; w < 32; w *= 2) x += __shfl_xor_sync(kAll, x, w);
-    x *= L.scale_log2;
-    const float top = fmaxf(m, x), keep = m == top ? 1.f : exp2f(m - top), p = exp2f(x - top);
-    m = top;
-    l = l * keep + p;
-#pragma unroll
-    for (int e = 0; e < D / 32; ++e) o[e] = o[e] * keep + p * value(L.v + s * L.v_stride + h * L.v_head_stride + e * 32 + lane);
-  }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-  for (int e = 0; e < D / 32; ++e) L.out[(t * L.num_heads + h) * D + e * 32 + lane] = static_cast<uint16_t>(cosa::pack_bf16x2(o[e] * inv, 0.f));
-  if (L.lse && lane == 0) L.lse[t * L.num_heads + h] = (m + log2f(l)) * 0.69314718055994531f;
+  const size_t smem = sizeof(Smem<S>) + 1024;
+  static_assert(sizeof(Smem<S>) + 1024 <= 227 * 1024, "shared memory");
+  auto* kernel = prefill_kernel<S>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  return cosa_kv::launch_after(kernel, dim3(static_cast<unsigned>(blocks * L.num_heads)), kThreads, smem, stream, 1, maps[0], maps[1], maps[2],
+                               maps[3], maps[4], a);
 }
 
 }  // namespace
 
 cudaError_t launch_prefill(const PrefillLaunch& L, cudaStream_t stream) {
-  const int64_t rows = static_cast<int64_t>(L.total_tokens) * L.num_heads;
-  const unsigned grid = static_cast<unsigned>((rows * 32 + kThreads - 1) / kThreads);
-  return cosa_kv::launch_after(L.head_dim == 128 ? row_kernel<128> : row_kernel<64>, dim3(grid), kThreads, 0, stream, 1, L);
+  return L.head_dim == 128 ? launch_shape<128>(L, stream) : launch_shape<64>(L, stream);
 }
 
 }  // namespace cosa_attn
