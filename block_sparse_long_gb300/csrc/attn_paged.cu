@@ -63,7 +63,7 @@ template <int DK_, int DV_, bool LATENT, int N_>
 struct Shape {
   static constexpr int DK = DK_, DV = DV_, N = N_;
   static constexpr bool kLatent = LATENT;
-  static constexpr int kGroups = N == 128 ? 2 : 1;               // warpgroups of the softmax
+  static constexpr int kGroups = N == 16 ? 1 : N == 32 ? 2 : 4;  // warpgroups of the softmax
   static constexpr int NC = N / kGroups;                         // query rows of a softmax thread
   static constexpr int kThreads = 128 + 128 * kGroups;
   static constexpr int kBlocks = DV > 128 ? DV / 128 : 1;        // of 128 output values
@@ -74,14 +74,28 @@ struct Shape {
   static constexpr bool kAlias = LATENT && DV == 512 && N == 64;
   static constexpr int kPBufs = kAlias ? 0 : (LATENT && DV == 512 && N == 32) || N == 128 ? 1 : 2;
   static constexpr int kRopes = LATENT && DV + N <= 528 ? 2 : 1;      // (1, unused, without latent vectors)
-  static constexpr int kSmall = 2048 + N * 40;
+  static constexpr int kSmall = 2048 + N * 56;
   static constexpr int kRoom = 227 * 1024 - 1024 - kSmall - kQBytes - kPBufs * kPBytes - (LATENT ? kRopes * kColumn : 1024);
-  static constexpr int kSlots = kRoom / kPair < 6 ? kRoom / kPair : 6;
+  // Keys and values in slots of their own are waited for by different warps, and a parity wait tells only two phases apart: an even
+  // number of slots has either keys or values in a slot, so that each barrier's phases are waited for by one warp, in order.
+  static constexpr int kFit = kRoom / kPair < 6 ? kRoom / kPair : 6;
+  static constexpr int kSlots = kPairs == 2 && !LATENT ? kFit / 2 * 2 : kFit;
   static_assert(kSlots >= kPairs, "a tile fits the ring");
   static constexpr uint32_t kTmemO = 0, kTmemS = kBlocks * N;
   static_assert(kTmemS + 2 * N <= 512, "TMEM columns");
   // P^T: rows of 32, 64 or 128 bytes per slot, swizzled at that width
   static constexpr int kPRow = N >= 64 ? 128 : 2 * N;
+};
+
+// Where a CTA begins in the list: units and items of the batch, and those before its first request.
+struct Start {
+  int64_t total, before, items, items_before;
+  int32_t first_req;
+};
+
+// What join_kernel has to put together: `parts` parts of an item, the first in slot `first`, the others in next, next + 2, ...
+struct Join {
+  int32_t parts, first, next, tok0, rows, head, row_tile, pad;
 };
 
 template <class S>
@@ -92,14 +106,15 @@ struct alignas(1024) Smem {
   uint8_t p[S::kPBufs ? S::kPBufs : 1][S::kPBufs ? S::kPBytes : 16];
   uint64_t full[S::kSlots], empty[S::kSlots];
   uint64_t rope_full[2], rope_empty[2];
-  uint64_t q_ready, s_full[2], s_empty[2], p_full[2], pv_done[2], cleanup;
+  uint64_t q_ready, s_full[2], s_empty[2], p_full[2], pv_done[2], groups, cleanup;
   uint64_t mask[S::N];               // tree mask of a row's token
-  float base[S::N], alpha[S::N];     // reference of a row (log2 units), and its last change
+  alignas(16) float base[S::N];      // reference of a row (log2 units), read four at a time
+  float alpha[S::N];                 // a reference's last change
   float part[4][S::N];               // maxima and sums of the four warps
   int32_t row[S::N];                 // output row, or -1
   int32_t node[S::N];                // token of the request
-  int64_t total, before;             // units of the batch, units before this CTA's first request
-  int32_t first_req;
+  int64_t q_at[S::N], r_at[S::N];    // its values in q and q_rope
+  Start start;
   int32_t odd_values;                // something among the new tokens' values is not finite
   uint32_t tmem_base;
   int32_t abort_flag;
@@ -111,9 +126,11 @@ struct Args {
   const int64_t* tree_mask;
   uint16_t* out;
   float *lse, *part_o, *part_ml;
+  Join* joins;
   int32_t* status;
   int64_t q_stride, q_rope_stride;
   int num_reqs, num_q_heads, num_kv_heads, group, page_shift, total_tokens, max_seqlen, num_pages, max_pages_per_req;
+  int join_items;      // entries of `joins` if they are by item, 0 if by CTA
   float scale_log2;
   int stall;
 };
@@ -151,79 +168,110 @@ struct Piece {
   Request r;
   int b, head, row_tile, t0, t1;
   int slot;          // of the workspace, or -1: all of the item
+  bool begins;       // it has the item's first unit
+  int64_t item;      // number of the item in the batch
+  int64_t item_end;  // behind its last unit
 };
 
 // The pieces of a CTA in order; every role walks them by itself.
 template <int N>
 struct Pieces {
-  int64_t pos, first, end, before, units;
+  int64_t pos, first, end, before, units, items;
   int b, cta;
   Request r;
 
-  __device__ Pieces(const Args& a, int cta_, int64_t total, int first_req, int64_t before_) : before(before_), units(0), b(first_req - 1), cta(cta_) {
-    first = pos = share(total, cta);
-    end = share(total, cta + 1);
+  __device__ Pieces(const Args& a, int cta_, const Start& st)
+      : before(st.before), units(0), items(st.items_before), b(st.first_req - 1), cta(cta_) {
+    first = pos = share(st.total, cta);
+    end = share(st.total, cta + 1);
+    r.row_tiles = 0;
   }
   __device__ bool next(const Args& a, Piece& p) {
     if (pos >= end) return false;
     while (pos >= before + units) {
       before += units;
+      items += static_cast<int64_t>(a.num_kv_heads) * r.row_tiles;
       r = request_of<N>(a, ++b);
       units = units_of(a, r);
     }
-    const int64_t local = pos - before;
     const int per = r.tiles + 1;
-    const int64_t item = local / per;
+    // (what follows fits 32 bits but for the longest batches)
+    const int64_t local = pos - before;
+    const int64_t item = local >> 31 ? local / per : static_cast<int64_t>(static_cast<uint32_t>(local) / static_cast<uint32_t>(per));
     const int u = static_cast<int>(local - item * per);
     const int take = static_cast<int>(min(static_cast<int64_t>(per - u), end - pos));
     p.r = r;
     p.b = b;
-    p.head = static_cast<int>(item / r.row_tiles);
-    p.row_tile = static_cast<int>(item % r.row_tiles);
+    p.head = static_cast<int>(item >> 31 ? item / r.row_tiles : static_cast<uint32_t>(item) / static_cast<uint32_t>(r.row_tiles));
+    p.row_tile = static_cast<int>(item - static_cast<int64_t>(p.head) * r.row_tiles);
     p.t0 = max(u - 1, 0);
     p.t1 = u + take - 1;
     p.slot = take == per ? -1 : 2 * cta + (pos != first);
+    p.begins = u == 0;
+    p.item = items + item;
+    p.item_end = pos + per - u;
     pos += take;
     return true;
   }
 };
 
-// Units of all requests, and the request with unit `at`: by one warp.
+// Units and items of the batch, and where this CTA begins: by one warp, a request to a lane at a time.
 template <int N>
-__device__ __forceinline__ int64_t total_units(const Args& a, bool report) {
+__device__ __forceinline__ Start find_start(const Args& a, int cta, bool report) {
   const int lane = threadIdx.x % 32;
-  int64_t sum = 0;
-  for (int b = lane; b < a.num_reqs; b += 32) {
-    const Request r = request_of<N>(a, b);
-    if (r.bad && report) cosa::report_status(a.status, cosa::kStatusBadInput);
-    sum += units_of(a, r);
-  }
-#pragma unroll
-  for (int m = 1; m < 32; m *= 2) sum += __shfl_xor_sync(kAll, sum, m);
-  return sum;
-}
-
-template <int N>
-__device__ __forceinline__ void find_request(const Args& a, int64_t at, int& first_req, int64_t& before) {
-  const int lane = threadIdx.x % 32;
-  int64_t sum = 0;
-  for (int b0 = 0;; b0 += 32) {
-    const int64_t mine = b0 + lane < a.num_reqs ? units_of(a, request_of<N>(a, b0 + lane)) : 0;
-    int64_t upto = mine;
+  Start st{};
+  int64_t units = 0, items = 0;       // of this lane's last request
+  for (int b0 = 0; b0 < a.num_reqs; b0 += 32) {
+    units = items = 0;
+    if (b0 + lane < a.num_reqs) {
+      const Request r = request_of<N>(a, b0 + lane);
+      if (r.bad && report) cosa::report_status(a.status, cosa::kStatusBadInput);
+      units = units_of(a, r);
+      items = static_cast<int64_t>(a.num_kv_heads) * r.row_tiles;
+    }
+    int64_t sum = units, sum_items = items;
 #pragma unroll
     for (int m = 1; m < 32; m *= 2) {
-      const int64_t x = __shfl_up_sync(kAll, upto, m);
-      if (lane >= m) upto += x;
+      sum += __shfl_xor_sync(kAll, sum, m);
+      sum_items += __shfl_xor_sync(kAll, sum_items, m);
     }
-    const unsigned past = __ballot_sync(kAll, sum + upto > at);
-    if (past || b0 + 32 >= a.num_reqs) {
-      const int l = past ? __ffs(past) - 1 : 31;
-      first_req = b0 + l;
-      before = sum + __shfl_sync(kAll, upto - mine, l);
-      return;
-    }
-    sum += __shfl_sync(kAll, upto, 31);
+    st.total += sum;
+    st.items += sum_items;
   }
+  const int64_t at = share(st.total, cta);
+  for (int b0 = 0; b0 < a.num_reqs; b0 += 32) {
+    if (a.num_reqs > 32) {
+      units = items = 0;
+      if (b0 + lane < a.num_reqs) {
+        const Request r = request_of<N>(a, b0 + lane);
+        units = units_of(a, r);
+        items = static_cast<int64_t>(a.num_kv_heads) * r.row_tiles;
+      }
+    }
+    int64_t upto = units, upto_items = items;
+#pragma unroll
+    for (int m = 1; m < 32; m *= 2) {
+      const int64_t x = __shfl_up_sync(kAll, upto, m), y = __shfl_up_sync(kAll, upto_items, m);
+      if (lane >= m) upto += x, upto_items += y;
+    }
+    const unsigned past = __ballot_sync(kAll, st.before + upto > at);
+    const int l = past ? __ffs(past) - 1 : 31;
+    const int64_t skip = __shfl_sync(kAll, past ? upto - units : upto, l), skip_items = __shfl_sync(kAll, past ? upto_items - items : upto_items, l);
+    st.before += skip;
+    st.items_before += skip_items;
+    st.first_req = b0 + l;
+    if (past) break;
+  }
+  return st;
+}
+
+// The CTA that has a unit.
+__device__ __forceinline__ int owner(int64_t total, int64_t u) {
+  if (total < kCtas) return static_cast<int>(u);
+  int c = static_cast<int>(min(static_cast<int64_t>(kCtas - 1), u * kCtas / total));
+  while (share(total, c + 1) <= u) ++c;
+  while (share(total, c) > u) --c;
+  return c;
 }
 
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status) {
@@ -283,14 +331,9 @@ __global__ void __launch_bounds__(S::kThreads, 1)
   cosa_kv::let_next_start();
 
   if (warp == 0) {
-    const int64_t total = total_units<N>(a, cta == 0);
-    int first_req;
-    int64_t before;
-    find_request<N>(a, share(total, cta), first_req, before);
+    const Start st = find_start<N>(a, cta, cta == 0);
     if (lane == 0) {
-      sm.total = total;
-      sm.first_req = first_req;
-      sm.before = before;
+      sm.start = st;
       if (cta == 0 && (a.cu_seqlens[0] != 0 || a.cu_seqlens[a.num_reqs] > a.total_tokens)) cosa::report_status(a.status, cosa::kStatusBadInput);
     }
   } else if (warp == 1 && lane == 0) {
@@ -307,6 +350,7 @@ __global__ void __launch_bounds__(S::kThreads, 1)
       mbar_init(&sm.pv_done[s], 2);       // the products, and the issuing warp's own arrival
     }
     mbar_init(&sm.q_ready, 1);
+    mbar_init(&sm.groups, 4 * S::kGroups);
     mbar_init(&sm.cleanup, 2);
     sm.abort_flag = 0;
     sm.odd_values = 0;
@@ -319,7 +363,7 @@ __global__ void __launch_bounds__(S::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
-  Pieces<N> pieces(a, cta, sm.total, sm.first_req, sm.before);
+  Pieces<N> pieces(a, cta, sm.start);
   Piece pc;
   const int pages_per_tile = kTile >> a.page_shift;
 
@@ -529,47 +573,85 @@ __global__ void __launch_bounds__(S::kThreads, 1)
       wait_parity_bounded(&sm.cleanup, 0, nullptr, nullptr);
     }
     __syncwarp();
-  } else if (warp >= 4) {
+  } else if (warp == 3) {
+    // =========================== what is to be joined ===========================
+    if (lane == 0) {
+      Join none{}, mine{};
+      while (pieces.next(a, pc)) {
+        if (!pc.begins) continue;
+        Join j{};
+        j.parts = 1;
+        if (pc.slot >= 0) {
+          j.parts = owner(sm.start.total, pc.item_end - 1) - cta + 1;
+          j.first = pc.slot;
+          j.next = 2 * (cta + 1);
+          j.tok0 = pc.r.tok0;
+          j.rows = pc.r.n * a.group;
+          j.head = pc.head;
+          j.row_tile = pc.row_tile;
+          mine = j;
+        }
+        if (pc.item < a.join_items) a.joins[pc.item] = j;
+      }
+      if (!a.join_items) a.joins[cta] = mine;
+      else if (cta == 0)
+        for (int64_t i = sm.start.items; i < a.join_items; ++i) a.joins[i] = none;
+    }
+    __syncwarp();
+  } else {
     // =========================== softmax ===========================
     const int g = warp / 4 - 1, quarter = warp % 4, tid = threadIdx.x - 128;
     const int at = quarter * 32 + lane;                // TMEM lane: slot of the tile, value of an output block
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
     const int c0 = g * NC;
-    constexpr int kAllBar = 3, kSoftmax = 128 * S::kGroups;
+    constexpr int kSoftmax = 128 * S::kGroups;
     const int my_bar = 1 + g;
     const float scale = a.scale_log2;
-    int tile = 0;
+    int tile = 0, meetings = 0;
     bool ok = true;
+    // All groups meet; one that gave up does not come, so the wait is bounded.
+    auto meet = [&] {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.groups);
+      return warp_wait(&sm.groups, meetings++ & 1, abort_flag, a.status);
+    };
     while (ok && pieces.next(a, pc)) {
       const Request& r = pc.r;
       const int rows = r.n * a.group;      // fits 32 bits: total_tokens * Hq does
       const int row0 = pc.row_tile * N;
-      named_bar_sync(kAllBar, kSoftmax);   // the last piece is done with what follows
+      if (!meet()) break;                  // the last piece is done with what follows
       if (tid < N) {
         const int row = row0 + tid, node = min(row, rows - 1) / a.group;
         sm.row[tid] = row < rows ? (r.tok0 + node) * a.num_q_heads + pc.head * a.group + row % a.group : -1;
         sm.node[tid] = node;
+        sm.q_at[tid] = row < rows ? (r.tok0 + node) * a.q_stride + (pc.head * a.group + row % a.group) * DV : -1;
+        if (S::kLatent) sm.r_at[tid] = (r.tok0 + node) * a.q_rope_stride + row % a.group * (S::DK - DV);
         sm.mask[tid] = a.tree_mask ? static_cast<uint64_t>(a.tree_mask[r.tok0 + node]) : 0;
         sm.base[tid] = kNone;
       }
       if (pc.t0 < pc.t1) {
         // queries into rows of 128 bytes per 64 values, swizzled; rows behind the last are 0
-        constexpr int kPieces16 = S::DK / 8;
-        for (int e = tid; e < N * kPieces16; e += kSoftmax) {
-          const int row = e / kPieces16, c = e % kPieces16;
-          uint4 x = make_uint4(0, 0, 0, 0);
-          if (row0 + row < rows) {
-            const int64_t tok = r.tok0 + (row0 + row) / a.group;
-            const int head = pc.head * a.group + (row0 + row) % a.group;
-            const uint16_t* src = S::kLatent && c >= DV / 8 ? a.q_rope + tok * a.q_rope_stride + head * (S::DK - DV) + c * 8 - DV
-                                                            : a.q + tok * a.q_stride + head * DV + c * 8;
-            x = *reinterpret_cast<const uint4*>(src);
+        if (!meet()) break;
+        constexpr int kPieces16 = S::DK / 8, kBatch = 6;
+#pragma unroll 1
+        for (int e0 = tid; e0 < N * kPieces16; e0 += kBatch * kSoftmax) {
+          uint4 x[kBatch];
+#pragma unroll
+          for (int k = 0; k < kBatch; ++k) {
+            const int e = e0 + k * kSoftmax, row = e / kPieces16, c = e % kPieces16;
+            x[k] = make_uint4(0, 0, 0, 0);
+            if (e < N * kPieces16 && sm.q_at[row] >= 0)
+              x[k] = *reinterpret_cast<const uint4*>(S::kLatent && c >= DV / 8 ? a.q_rope + sm.r_at[row] + c * 8 - DV : a.q + sm.q_at[row] + c * 8);
           }
-          *reinterpret_cast<uint4*>(&sm.q[c / 8 * N * 128 + row * 128 + ((c ^ row) & 7) * 16]) = x;
+#pragma unroll
+          for (int k = 0; k < kBatch; ++k) {
+            const int e = e0 + k * kSoftmax, row = e / kPieces16, c = e % kPieces16;
+            if (e < N * kPieces16) *reinterpret_cast<uint4*>(&sm.q[c / 8 * N * 128 + row * 128 + ((c ^ row) & 7) * 16]) = x[k];
+          }
         }
         fence_proxy_async_smem();
       }
-      named_bar_sync(kAllBar, kSoftmax);
+      if (!meet()) break;
       if (tid == 0 && pc.t0 < pc.t1) mbar_arrive(&sm.q_ready);
 
       const int32_t* table = a.page_table + static_cast<size_t>(pc.b) * a.max_pages_per_req;
@@ -604,19 +686,21 @@ __global__ void __launch_bounds__(S::kThreads, 1)
         }
         bool high = false;
 #pragma unroll
-        for (int i = 0; i < NC; ++i) high |= fmaf(x[i], scale, -sm.base[c0 + i]) > kRescaleLog2;
+        for (int i = 0; i < NC; i += 4) {
+          const float4 b = *reinterpret_cast<const float4*>(&sm.base[c0 + i]);
+          high |= fmaf(x[i], scale, -b.x) > kRescaleLog2 || fmaf(x[i + 1], scale, -b.y) > kRescaleLog2 ||
+                  fmaf(x[i + 2], scale, -b.z) > kRescaleLog2 || fmaf(x[i + 3], scale, -b.w) > kRescaleLog2;
+        }
         if (named_bar_red_or(my_bar, 128, high || fail)) {
           if (named_bar_red_or(my_bar, 128, fail)) { ok = false; break; }
           // some logit is far above its row's reference: the rows' maxima over the tile
-          float mine = 0.f, mine2 = 0.f;
+          float mine = 0.f;
 #pragma unroll
           for (int i = 0; i < NC; ++i) {
             const float top = warp_max(x[i]);
-            if (i < 32) mine = lane == i ? top : mine;
-            else mine2 = lane == i - 32 ? top : mine2;
+            mine = lane == i ? top : mine;
           }
           if (lane < NC) sm.part[quarter][c0 + lane] = mine;
-          if (NC > 32) sm.part[quarter][c0 + 32 + lane] = mine2;
           named_bar_sync(my_bar, 128);
           if (at < NC) {
             const int c = c0 + at;
@@ -655,20 +739,23 @@ __global__ void __launch_bounds__(S::kThreads, 1)
         if (!fail && tile >= kBack)
           fail = !warp_wait(&sm.pv_done[(tile - kBack) & 1], ((tile - kBack) / 2) & 1, abort_flag, a.status);
         if (!fail) {
-          uint8_t* p = S::kAlias ? sm.rope[0] : sm.p[S::kPBufs == 2 ? tile & 1 : 0];
-          if (S::kGroups == 2) p += g * kColumn;
+          uint8_t* p = (S::kAlias ? sm.rope[0] : sm.p[S::kPBufs == 2 ? tile & 1 : 0]) + c0 / 64 * kColumn;
 #pragma unroll
           for (int i = 0; i < NC; i += 8) {
             uint32_t w[4];
 #pragma unroll
-            for (int e = 0; e < 8; e += 2) {
-              const float p0 = cosa::ex2_approx(fmaf(x[i + e], scale, -sm.base[c0 + i + e]));
-              const float p1 = cosa::ex2_approx(fmaf(x[i + e + 1], scale, -sm.base[c0 + i + e + 1]));
+            for (int e = 0; e < 8; e += 4) {
+              const float4 b = *reinterpret_cast<const float4*>(&sm.base[c0 + i + e]);
+              const float p0 = cosa::ex2_approx(fmaf(x[i + e], scale, -b.x)), p1 = cosa::ex2_approx(fmaf(x[i + e + 1], scale, -b.y));
+              const float p2 = cosa::ex2_approx(fmaf(x[i + e + 2], scale, -b.z)), p3 = cosa::ex2_approx(fmaf(x[i + e + 3], scale, -b.w));
               l[i + e] += p0;
               l[i + e + 1] += p1;
+              l[i + e + 2] += p2;
+              l[i + e + 3] += p3;
               w[e / 2] = cosa::pack_bf16x2(p0, p1);
+              w[e / 2 + 1] = cosa::pack_bf16x2(p2, p3);
             }
-            *reinterpret_cast<uint4*>(p + p_offset<S::kPRow>(at, i / 8)) = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4*>(p + p_offset<S::kPRow>(at, (c0 % 64 + i) / 8)) = make_uint4(w[0], w[1], w[2], w[3]);
           }
           fence_proxy_async_smem();
           __syncwarp();
@@ -681,17 +768,15 @@ __global__ void __launch_bounds__(S::kThreads, 1)
       bool fail = false;
       if (pc.t0 < pc.t1) fail = !warp_wait(&sm.pv_done[(tile - 1) & 1], ((tile - 1) / 2) & 1, abort_flag, a.status);
       {
-        float mine = 0.f, mine2 = 0.f;
+        float mine = 0.f;
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
           float s = l[i];
 #pragma unroll
           for (int m = 1; m < 32; m *= 2) s += __shfl_xor_sync(kAll, s, m);
-          if (i < 32) mine = lane == i ? s : mine;
-          else mine2 = lane == i - 32 ? s : mine2;
+          mine = lane == i ? s : mine;
         }
         if (lane < NC) sm.part[quarter][c0 + lane] = mine;
-        if (NC > 32) sm.part[quarter][c0 + 32 + lane] = mine2;
       }
       if (named_bar_red_or(my_bar, 128, fail)) { ok = false; break; }
       if (at < NC) {
@@ -750,7 +835,7 @@ __global__ void __launch_bounds__(S::kThreads, 1)
       }
       tc_fence_before();
       if (odd_values) {        // the other threads have read it
-        named_bar_sync(kAllBar, kSoftmax);
+        if (!meet()) break;
         if (tid == 0) sm.odd_values = 0;
       }
     }
@@ -763,62 +848,23 @@ __global__ void __launch_bounds__(S::kThreads, 1)
   }
 }
 
-// Joins the parts of the items that several CTAs had: out = sum 2^(m_i - m) o_i / sum 2^(m_i - m) l_i.  blockIdx.x is an item (few
-// items), or a CTA whose share ends inside an item that it began; a block has eight rows of 128 values, or (kWide, where an
-// item has many parts) one row, its warps a part each.
+// Joins the parts of the items that several CTAs had: out = sum 2^(m_i - m) o_i / sum 2^(m_i - m) l_i.  blockIdx.x is an entry of
+// `joins`; a block has eight rows of 128 values, or (kWide, where an item has many parts) one row, its warps a part each.
 constexpr int kJoinThreads = 256;
 
 template <int N, int DV, bool kWide>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ Args a, const int by_item) {
-  constexpr int kSeg = DV < 128 ? DV : 128, kSegs = DV / kSeg, kVec = kSeg / 32;
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ Args a) {
+  constexpr int kSeg = DV < 128 ? DV : 128, kVec = kSeg / 32;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   cosa_kv::wait_for_stream();
-  const int64_t total = total_units<N>(a, false);
-  // the item that holds unit `at`, or item number `at`
-  int b;
-  int64_t before, start;
-  Request r;
-  int64_t item;
-  if (by_item) {
-    int64_t left = blockIdx.x, sum = 0;
-    for (b = 0; b < a.num_reqs; ++b) {
-      r = request_of<N>(a, b);
-      const int64_t items = static_cast<int64_t>(a.num_kv_heads) * r.row_tiles;
-      if (left < items) break;
-      left -= items;
-      sum += units_of(a, r);
-    }
-    if (b == a.num_reqs) return;
-    item = left;
-    before = sum;
-    start = before + item * (r.tiles + 1);
-  } else {
-    const int64_t at = share(total, blockIdx.x + 1);
-    if (at >= total) return;
-    find_request<N>(a, at, b, before);
-    r = request_of<N>(a, b);
-    item = (at - before) / (r.tiles + 1);
-    start = before + item * (r.tiles + 1);
-    if (start == at || start < share(total, blockIdx.x)) return;      // not cut here, or begun before this CTA
-  }
-  const int64_t end = start + r.tiles + 1;
-  // the CTAs that have the item: c0 has unit start, c1 unit end - 1
-  auto owner = [&](int64_t u) {
-    int c = static_cast<int>(total < kCtas ? u : min(static_cast<int64_t>(kCtas - 1), u * kCtas / total));
-    while (share(total, c + 1) <= u) ++c;
-    while (share(total, c) > u) --c;
-    return c;
-  };
-  const int first = owner(start), last = owner(end - 1);
-  if (first == last) return;
-  const int parts = last - first + 1;
-  const int head = static_cast<int>(item / r.row_tiles), row_tile = static_cast<int>(item % r.row_tiles);
-  const int seg = blockIdx.z;
+  const Join j = a.joins[blockIdx.x];
+  if (j.parts < 2) return;
+  const int parts = j.parts, seg = blockIdx.z;
   const int c = kWide ? blockIdx.y : blockIdx.y * 8 + warp;      // row of the tile
-  const int64_t row = static_cast<int64_t>(row_tile) * N + c;
-  const bool live = row < static_cast<int64_t>(r.n) * a.group;
-  if (kWide ? !live : false) return;
-  auto slot = [&](int i) { return 2 * (first + i) + (i == 0 && share(total, first) < start ? 1 : 0); };
+  const int64_t row = static_cast<int64_t>(j.row_tile) * N + c;
+  const bool live = row < j.rows;
+  if (kWide && !live) return;
+  auto slot = [&](int i) { return i == 0 ? j.first : j.next + 2 * (i - 1); };
   __shared__ float weight[kWide ? 1 : 8][kCtas + 8];
   __shared__ float sums[8][kSeg];
   float* w = weight[kWide ? 0 : warp];
@@ -870,7 +916,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
   }
   if (!live) return;
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  const int64_t to = (r.tok0 + row / a.group) * a.num_q_heads + head * a.group + row % a.group;
+  const int64_t to = (j.tok0 + row / a.group) * a.num_q_heads + j.head * a.group + row % a.group;
   uint16_t* dst = a.out + to * DV + seg * kSeg + lane * kVec;
   if constexpr (kVec == 4)
     *reinterpret_cast<uint2*>(dst) = make_uint2(cosa::pack_bf16x2(o[0] * inv, o[1] * inv), cosa::pack_bf16x2(o[2] * inv, o[3] * inv));
@@ -902,13 +948,17 @@ cudaError_t launch_shape(const PagedLaunch& L, cudaStream_t stream) {
   a.lse = L.lse;
   a.part_o = static_cast<float*>(L.workspace);
   a.part_ml = a.part_o + static_cast<size_t>(2 * kCtas) * S::N * S::DV;
+  a.joins = reinterpret_cast<Join*>(a.part_ml + static_cast<size_t>(2 * kCtas) * S::N * 2);
+  // at most so many items: what the tokens fill and a part of a row tile for every request
+  const int64_t group = L.num_q_heads / L.num_kv_heads, items = L.num_kv_heads * (L.total_tokens * group / S::N + L.num_reqs);
+  a.join_items = items <= kCtas ? static_cast<int>(items) : 0;
   a.status = L.status;
   a.q_stride = L.q_stride;
   a.q_rope_stride = L.q_rope_stride;
   a.num_reqs = L.num_reqs;
   a.num_q_heads = L.num_q_heads;
   a.num_kv_heads = L.num_kv_heads;
-  a.group = L.num_q_heads / L.num_kv_heads;
+  a.group = static_cast<int>(group);
   a.page_shift = L.page_shift;
   a.total_tokens = L.total_tokens;
   a.max_seqlen = L.max_seqlen;
@@ -933,14 +983,10 @@ cudaError_t launch_shape(const PagedLaunch& L, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   e = cosa_kv::launch_after(kernel, dim3(kCtas), S::kThreads, smem, stream, 1, kmap, vmap, a);
   if (e != cudaSuccess) return e;
-  // at most so many items: what the tokens fill and a part of a row tile for every request
-  const int64_t items = L.num_kv_heads * ((static_cast<int64_t>(L.total_tokens) * a.group) / S::N + L.num_reqs);
-  const bool by_item = items <= kCtas;
-  const unsigned segs = S::DV < 128 ? 1 : S::DV / 128;
-  const unsigned x = static_cast<unsigned>(by_item ? items : kCtas - 1);
-  if (items <= 8)
-    return cosa_kv::launch_after(join_kernel<S::N, S::DV, true>, dim3(x, S::N, segs), kJoinThreads, 0, stream, 1, a, by_item ? 1 : 0);
-  return cosa_kv::launch_after(join_kernel<S::N, S::DV, false>, dim3(x, S::N / 8, segs), kJoinThreads, 0, stream, 1, a, by_item ? 1 : 0);
+  const unsigned segs = S::DV < 128 ? 1 : S::DV / 128, x = static_cast<unsigned>(a.join_items ? a.join_items : kCtas);
+  if (a.join_items && a.join_items <= 16)
+    return cosa_kv::launch_after(join_kernel<S::N, S::DV, true>, dim3(x, S::N, segs), kJoinThreads, 0, stream, 1, a);
+  return cosa_kv::launch_after(join_kernel<S::N, S::DV, false>, dim3(x, S::N / 8, segs), kJoinThreads, 0, stream, 1, a);
 }
 
 template <int DK, int DV, bool LATENT>
@@ -959,7 +1005,7 @@ cudaError_t launch_width(const PagedLaunch& L, cudaStream_t stream) {
 
 size_t paged_workspace_bytes(const PagedLaunch& L) {
   const size_t dv = static_cast<size_t>(L.latent_dim ? L.latent_dim : L.head_dim);
-  return static_cast<size_t>(2 * kCtas) * rows_of_tile(L) * (dv + 2) * sizeof(float);
+  return static_cast<size_t>(2 * kCtas) * rows_of_tile(L) * (dv + 2) * sizeof(float) + kCtas * sizeof(Join);
 }
 
 cudaError_t launch_paged(const PagedLaunch& L, cudaStream_t stream) {

@@ -67,6 +67,21 @@ def test_long_contexts_are_shared(latent):
     run_and_check(c)
 
 
+@pytest.mark.parametrize("latent,d", [(0, 64), (0, 128), (256, 128), (512, 128)])
+@pytest.mark.parametrize("new", [1, 3, 7, 15])
+def test_many_tiles_to_a_cta(latent, d, new):
+    """Every width of row tiles (8 rows a token: 16 to 128), with tens of tiles and several items to a CTA."""
+    heads = 8 if latent else 16
+    c = Paged(new + d + latent, [9000, 30011, 140, 20000], [new, 1, min(new, 4), new], heads, 1 if latent else 2, d, 64, latent=latent, tree=True)
+    for _ in range(3):
+        out, lse = c.buffers()
+        st = new_status()
+        for _ in range(4):
+            c.call(out=out, lse=lse, status=st)
+        ok(st)
+    c.check(out, lse)
+
+
 @pytest.mark.parametrize("latent", [0, 256])
 def test_many_requests(latent):
     rng = np.random.default_rng(3)
