@@ -78,19 +78,6 @@ bool strides_of(int64_t token, int64_t head, int64_t heads, int64_t width, int64
   return *by_token >= 0 && *by_token % 8 == 0;
 }
 
-int check_paged(const cosa_attn_params* p, bool latent) {
-  COSA_TRY(check_common(p));
-  COSA_TRY(check_slots(p));
-  COSA_TRY(latent ? check_latent(p) : check_heads(p));
-  COSA_TRY(check_scale(p));
-  if (p->max_new_tokens < 1) return COSA_ERR_INVALID_ARG;
-  if (static_cast<int64_t>(p->total_tokens) * p->num_q_heads > INT32_MAX) return COSA_ERR_UNSUPPORTED;
-  const int64_t width = latent ? p->latent_dim : p->head_dim;
-  if (stride_of(p->q_stride, p->num_q_heads * width) < 0) return COSA_ERR_INVALID_ARG;
-  if (latent && stride_of(p->q_rope_stride, p->num_q_heads * kRot) < 0) return COSA_ERR_INVALID_ARG;
-  return COSA_OK;
-}
-
 cosa_attn::PagedLaunch paged_of(const cosa_attn_params* p, bool latent) {
   cosa_attn::PagedLaunch L{};
   L.num_reqs = p->num_reqs;
@@ -110,6 +97,19 @@ cosa_attn::PagedLaunch paged_of(const cosa_attn_params* p, bool latent) {
   L.scale_log2 = static_cast<float>(p->sm_scale * 1.4426950408889634074);
   L.stall = (p->flags & COSA_ATTN_FLAG_TEST_STALL) != 0;
   return L;
+}
+
+int check_paged(const cosa_attn_params* p, bool latent) {
+  COSA_TRY(check_common(p));
+  COSA_TRY(check_slots(p));
+  COSA_TRY(latent ? check_latent(p) : check_heads(p));
+  COSA_TRY(check_scale(p));
+  if (p->max_new_tokens < 1) return COSA_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(p->total_tokens) * p->num_q_heads > INT32_MAX) return COSA_ERR_UNSUPPORTED;
+  const int64_t width = latent ? p->latent_dim : p->head_dim;
+  if (stride_of(p->q_stride, p->num_q_heads * width) < 0) return COSA_ERR_INVALID_ARG;
+  if (latent && stride_of(p->q_rope_stride, p->num_q_heads * kRot) < 0) return COSA_ERR_INVALID_ARG;
+  return cosa_attn::paged_fits(paged_of(p, latent)) ? COSA_OK : COSA_ERR_UNSUPPORTED;
 }
 
 int done(cudaError_t e) { return e == cudaSuccess ? COSA_OK : COSA_ERR_CUDA; }

@@ -45,6 +45,7 @@ struct PagedLaunch {
   float scale_log2;      // sm_scale * log2(e)
   bool stall;            // COSA_ATTN_FLAG_TEST_STALL
 };
+bool paged_fits(const PagedLaunch& L);      // its tiles are numbered in 31 bits
 size_t paged_workspace_bytes(const PagedLaunch& L);
 cudaError_t launch_paged(const PagedLaunch& L, cudaStream_t stream);
 

@@ -46,7 +46,6 @@ using cosa::smem_u32;
 using cosa::tc_fence_after;
 using cosa::tc_fence_before;
 using cosa::umma_commit;
-using cosa::umma_ss;
 using cosa::wait_parity_bounded;
 
 constexpr int kTile = 128;                 // slots
@@ -54,7 +53,7 @@ constexpr int kCtas = 152;
 constexpr int kColumn = kTile * 128;       // bytes of a 64-value wide column of a tile
 constexpr int kPair = 2 * kColumn;
 constexpr float kNone = -3e38f;            // reference of a row that has seen nothing
-constexpr float kRescaleLog2 = 8.0f;
+constexpr uint32_t kHigh = 0x4380;         // 2^8 in bf16: a weight above it moves its row's reference
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr unsigned kAll = 0xffffffffu;
 
@@ -87,10 +86,10 @@ struct Shape {
   static constexpr int kPRow = N >= 64 ? 128 : 2 * N;
 };
 
-// Where a CTA begins in the list: units and items of the batch, and those before its first request.
+// Where a CTA begins in the list: units and items of the batch, and those before its first request.  (The call is refused where
+// they could pass 31 bits.)
 struct Start {
-  int64_t total, before, items, items_before;
-  int32_t first_req;
+  int32_t total, before, items, items_before, first_req;
 };
 
 // What join_kernel has to put together: `parts` parts of an item, the first in slot `first`, the others in next, next + 2, ...
@@ -108,7 +107,7 @@ struct alignas(1024) Smem {
   uint64_t rope_full[2], rope_empty[2];
   uint64_t q_ready, s_full[2], s_empty[2], p_full[2], pv_done[2], groups, cleanup;
   uint64_t mask[S::N];               // tree mask of a row's token
-  alignas(16) float base[S::N];      // reference of a row (log2 units), read four at a time
+  alignas(16) float base[S::N];      // a row's reference (log2 units), negated; read four at a time
   float alpha[S::N];                 // a reference's last change
   float part[4][S::N];               // maxima and sums of the four warps
   int32_t row[S::N];                 // output row, or -1
@@ -144,24 +143,24 @@ struct Request {
 template <int N>
 __device__ __forceinline__ Request request_of(const Args& a, int b) {
   Request r;
-  r.tok0 = a.cu_seqlens[b];
-  const int64_t n = static_cast<int64_t>(a.cu_seqlens[b + 1]) - r.tok0;
+  r.tok0 = __ldg(a.cu_seqlens + b);
+  const int64_t n = static_cast<int64_t>(__ldg(a.cu_seqlens + b + 1)) - r.tok0;
+  r.len = __ldg(a.kv_len + b);
   r.bad = r.tok0 < 0 || n < 0 || r.tok0 + n > a.total_tokens;
   r.n = r.bad ? 0 : static_cast<int>(n);
-  r.len = a.kv_len[b];
   if (r.n > 0 && (r.len < r.n || r.len > a.max_seqlen || (a.tree_mask && r.n > COSA_ATTN_MAX_TREE))) r.bad = true;
   if (r.bad || r.n == 0) r.len = 0;
   r.tiles = (r.len + kTile - 1) / kTile;
-  r.row_tiles = static_cast<int>((static_cast<int64_t>(r.n) * a.group + N - 1) / N);
+  r.row_tiles = static_cast<int>((static_cast<uint32_t>(r.n) * static_cast<uint32_t>(a.group) + N - 1) / N);     // total_tokens * Hq fits 31 bits
   return r;
 }
 
-__device__ __forceinline__ int64_t units_of(const Args& a, const Request& r) {
-  return static_cast<int64_t>(a.num_kv_heads) * r.row_tiles * (r.tiles + 1);
-}
+__device__ __forceinline__ int units_of(const Args& a, const Request& r) { return a.num_kv_heads * r.row_tiles * (r.tiles + 1); }
 
 // First unit of a CTA.  With fewer units than CTAs the first ones have one each: every CTA up to the last with any has some.
-__device__ __forceinline__ int64_t share(int64_t total, int cta) { return total < kCtas ? min(static_cast<int64_t>(cta), total) : total * cta / kCtas; }
+__device__ __forceinline__ int share(int total, int cta) {
+  return total < kCtas ? min(cta, total) : static_cast<int>(static_cast<uint64_t>(static_cast<uint32_t>(total)) * cta / kCtas);
+}
 
 // What a CTA does of one item: tiles t0 .. t1 - 1.
 struct Piece {
@@ -169,15 +168,14 @@ struct Piece {
   int b, head, row_tile, t0, t1;
   int slot;          // of the workspace, or -1: all of the item
   bool begins;       // it has the item's first unit
-  int64_t item;      // number of the item in the batch
-  int64_t item_end;  // behind its last unit
+  int item;          // number of the item in the batch
+  int item_end;      // behind its last unit
 };
 
 // The pieces of a CTA in order; every role walks them by itself.
 template <int N>
 struct Pieces {
-  int64_t pos, first, end, before, units, items;
-  int b, cta;
+  int pos, first, end, before, units, items, b, cta;
   Request r;
 
   __device__ Pieces(const Args& a, int cta_, const Start& st)
@@ -190,26 +188,22 @@ struct Pieces {
     if (pos >= end) return false;
     while (pos >= before + units) {
       before += units;
-      items += static_cast<int64_t>(a.num_kv_heads) * r.row_tiles;
+      items += a.num_kv_heads * r.row_tiles;
       r = request_of<N>(a, ++b);
       units = units_of(a, r);
     }
-    const int per = r.tiles + 1;
-    // (what follows fits 32 bits but for the longest batches)
-    const int64_t local = pos - before;
-    const int64_t item = local >> 31 ? local / per : static_cast<int64_t>(static_cast<uint32_t>(local) / static_cast<uint32_t>(per));
-    const int u = static_cast<int>(local - item * per);
-    const int take = static_cast<int>(min(static_cast<int64_t>(per - u), end - pos));
+    const uint32_t per = r.tiles + 1, item = static_cast<uint32_t>(pos - before) / per;
+    const int u = static_cast<int>(pos - before - item * per), take = min(static_cast<int>(per) - u, end - pos);
     p.r = r;
     p.b = b;
-    p.head = static_cast<int>(item >> 31 ? item / r.row_tiles : static_cast<uint32_t>(item) / static_cast<uint32_t>(r.row_tiles));
-    p.row_tile = static_cast<int>(item - static_cast<int64_t>(p.head) * r.row_tiles);
+    p.head = r.row_tiles == 1 ? item : item / static_cast<uint32_t>(r.row_tiles);
+    p.row_tile = static_cast<int>(item) - p.head * r.row_tiles;
     p.t0 = max(u - 1, 0);
     p.t1 = u + take - 1;
-    p.slot = take == per ? -1 : 2 * cta + (pos != first);
+    p.slot = take == static_cast<int>(per) ? -1 : 2 * cta + (pos != first);
     p.begins = u == 0;
-    p.item = items + item;
-    p.item_end = pos + per - u;
+    p.item = items + static_cast<int>(item);
+    p.item_end = pos + static_cast<int>(per) - u;
     pos += take;
     return true;
   }
@@ -220,45 +214,38 @@ template <int N>
 __device__ __forceinline__ Start find_start(const Args& a, int cta, bool report) {
   const int lane = threadIdx.x % 32;
   Start st{};
-  int64_t units = 0, items = 0;       // of this lane's last request
+  int units = 0, items = 0;       // of this lane's last request
   for (int b0 = 0; b0 < a.num_reqs; b0 += 32) {
     units = items = 0;
     if (b0 + lane < a.num_reqs) {
       const Request r = request_of<N>(a, b0 + lane);
       if (r.bad && report) cosa::report_status(a.status, cosa::kStatusBadInput);
       units = units_of(a, r);
-      items = static_cast<int64_t>(a.num_kv_heads) * r.row_tiles;
+      items = a.num_kv_heads * r.row_tiles;
     }
-    int64_t sum = units, sum_items = items;
-#pragma unroll
-    for (int m = 1; m < 32; m *= 2) {
-      sum += __shfl_xor_sync(kAll, sum, m);
-      sum_items += __shfl_xor_sync(kAll, sum_items, m);
-    }
-    st.total += sum;
-    st.items += sum_items;
+    st.total += __reduce_add_sync(kAll, units);
+    st.items += __reduce_add_sync(kAll, items);
   }
-  const int64_t at = share(st.total, cta);
+  const int at = share(st.total, cta);
   for (int b0 = 0; b0 < a.num_reqs; b0 += 32) {
     if (a.num_reqs > 32) {
       units = items = 0;
       if (b0 + lane < a.num_reqs) {
         const Request r = request_of<N>(a, b0 + lane);
         units = units_of(a, r);
-        items = static_cast<int64_t>(a.num_kv_heads) * r.row_tiles;
+        items = a.num_kv_heads * r.row_tiles;
       }
     }
-    int64_t upto = units, upto_items = items;
+    int upto = units, upto_items = items;
 #pragma unroll
     for (int m = 1; m < 32; m *= 2) {
-      const int64_t x = __shfl_up_sync(kAll, upto, m), y = __shfl_up_sync(kAll, upto_items, m);
+      const int x = __shfl_up_sync(kAll, upto, m), y = __shfl_up_sync(kAll, upto_items, m);
       if (lane >= m) upto += x, upto_items += y;
     }
     const unsigned past = __ballot_sync(kAll, st.before + upto > at);
     const int l = past ? __ffs(past) - 1 : 31;
-    const int64_t skip = __shfl_sync(kAll, past ? upto - units : upto, l), skip_items = __shfl_sync(kAll, past ? upto_items - items : upto_items, l);
-    st.before += skip;
-    st.items_before += skip_items;
+    st.before += __shfl_sync(kAll, past ? upto - units : upto, l);
+    st.items_before += __shfl_sync(kAll, past ? upto_items - items : upto_items, l);
     st.first_req = b0 + l;
     if (past) break;
   }
@@ -266,22 +253,51 @@ __device__ __forceinline__ Start find_start(const Args& a, int cta, bool report)
 }
 
 // The CTA that has a unit.
-__device__ __forceinline__ int owner(int64_t total, int64_t u) {
-  if (total < kCtas) return static_cast<int>(u);
-  int c = static_cast<int>(min(static_cast<int64_t>(kCtas - 1), u * kCtas / total));
+__device__ __forceinline__ int owner(int total, int u) {
+  if (total < kCtas) return u;
+  int c = min(kCtas - 1, static_cast<int>(static_cast<uint64_t>(static_cast<uint32_t>(u)) * kCtas / static_cast<uint32_t>(total)));
   while (share(total, c + 1) <= u) ++c;
   while (share(total, c) > u) --c;
   return c;
 }
 
+// A place in a ring of kCount barriers, and the parity of its use.
+template <int kCount>
+struct Ring {
+  int at = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next(int step = 1) {
+    at += step;
+    if (at >= kCount) at -= kCount, phase ^= 1;
+  }
+};
+
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status) {
   return __all_sync(kAll, wait_parity_bounded(bar, parity, abort_flag, status));
 }
 
-// Shared-memory matrix descriptor; layout 2, 4, 6: 128-, 64-, 32-byte swizzle.
-__device__ __forceinline__ uint64_t smem_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo, int layout) {
-  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16 |
-         static_cast<uint64_t>((sbo >> 4) & 0x3FFFu) << 32 | static_cast<uint64_t>(1) << 46 | static_cast<uint64_t>(layout) << 61;
+// Shared-memory matrix descriptors in two halves; layout 2, 4, 6: 128-, 64-, 32-byte swizzle.  Offsets add to the low half.
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) { return (saddr & 0x3FFFFu) >> 4 | (lbo >> 4) << 16; }
+__host__ __device__ constexpr uint32_t desc_hi(uint32_t sbo, int layout) { return sbo >> 4 | 1u << 14 | static_cast<uint32_t>(layout) << 29; }
+
+__device__ __forceinline__ void mma(uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi, uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tmov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\tsetp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d),
+      "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(static_cast<uint32_t>(accumulate))
+      : "memory");
+}
+
+// (d0, d1) = (a0, a1) * b + (c0, c1)
+__device__ __forceinline__ void fma2(float& d0, float& d1, float a0, float a1, float b, float c0, float c1) {
+  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %4};\n\tmov.b64 c, {%5, %6};\n\t"
+      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d0), "=f"(d1)
+      : "f"(a0), "f"(a1), "f"(b), "f"(c0), "f"(c1));
+}
+
+__device__ __forceinline__ void copy16(void* dst, const void* src, bool there) {      // asynchronous; zeros if there is nothing
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(there ? 16 : 0) : "memory");
 }
 
 // Where 16-byte piece c of row t of P^T goes (the swizzle of rows of kRow bytes).
@@ -373,14 +389,15 @@ __global__ void __launch_bounds__(S::kThreads, 1)
       cosa::tma_prefetch_desc(&kmap);
       cosa::tma_prefetch_desc(&vmap);
     }
-    int64_t pair = 0;      // ring slots taken so far
-    int ropes = 0;
+    Ring<S::kSlots> ring;
+    Ring<S::kRopes> rope;
+    int pairs = 0, ropes = 0;      // ring slots taken, up to the rings' sizes
     bool ok = !a.stall;
     while (ok && pieces.next(a, pc)) {
       const int32_t* table = a.page_table + static_cast<size_t>(pc.b) * a.max_pages_per_req;
       auto look_up = [&](int t) {
-        const int64_t page = static_cast<int64_t>(t) * pages_per_tile + lane;
-        return t < pc.t1 && lane < pages_per_tile && (page << a.page_shift) < pc.r.len ? table[page] : -1;
+        const int page = t * pages_per_tile + lane;
+        return t < pc.t1 && lane < pages_per_tile && page << a.page_shift < pc.r.len ? __ldg(table + page) : -1;
       };
       int phys_next = look_up(pc.t0);
       for (int t = pc.t0; t < pc.t1 && ok; ++t) {
@@ -393,19 +410,20 @@ __global__ void __launch_bounds__(S::kThreads, 1)
         const bool copies = there >> page & 1;
         const int to = (page << a.page_shift) * 128;
         auto rotated = [&] {
-          const int s = ropes % S::kRopes;
-          if (ropes >= S::kRopes) ok = warp_wait(&sm.rope_empty[s], (ropes / S::kRopes - 1) & 1, abort_flag, a.status);
+          const int s = rope.at;
+          if (ropes == S::kRopes) ok = warp_wait(&sm.rope_empty[s], rope.phase ^ 1, abort_flag, a.status);
           if (!ok) return;
           if (lane == 0) mbar_arrive_expect_tx(&sm.rope_full[s], bytes);
           __syncwarp();
           if (column == 0 && copies) cosa::tma_load_4d(&sm.rope[s][to], &kmap, &sm.rope_full[s], 0, place, DV / 64, 0);
-          ++ropes;
+          rope.next();
+          ropes = min(ropes + 1, S::kRopes);
         };
         if constexpr (S::kLatent && !S::kAlias) rotated();
         if (!ok) break;
-        for (int i = 0; i < S::kPairs; ++i, ++pair) {
-          const int s = static_cast<int>(pair % S::kSlots);
-          if (pair >= S::kSlots) ok = warp_wait(&sm.empty[s], (pair / S::kSlots - 1) & 1, abort_flag, a.status);
+        for (int i = 0; i < S::kPairs; ++i) {
+          const int s = ring.at;
+          if (pairs == S::kSlots) ok = warp_wait(&sm.empty[s], ring.phase ^ 1, abort_flag, a.status);
           if (!ok) break;
           if (lane == 0) mbar_arrive_expect_tx(&sm.full[s], 2 * bytes);
           __syncwarp();
@@ -418,67 +436,73 @@ __global__ void __launch_bounds__(S::kThreads, 1)
             else
               cosa::tma_load_4d(dst, column ? &vmap : &kmap, &sm.full[s], 0, place, 0, pc.head);
           }
+          ring.next();
+          pairs = min(pairs + 1, S::kSlots);
         }
         if constexpr (S::kAlias) {
           if (ok) rotated();
         }
       }
     }
-    // every copy lands before the CTA ends
+    // every copy lands before the CTA ends: the last use of each slot (those before it have landed, or it had not been taken)
     if (lane == 0) {
-      for (int s = 0; s < S::kSlots; ++s) {
-        const int64_t issued = (pair - s + S::kSlots - 1) / S::kSlots;
-        if (issued > 0) wait_parity_bounded(&sm.full[s], (issued - 1) & 1, nullptr, nullptr);
+      for (; pairs > 0; --pairs) {
+        ring.at = ring.at == 0 ? (ring.phase ^= 1, S::kSlots - 1) : ring.at - 1;
+        wait_parity_bounded(&sm.full[ring.at], ring.phase, nullptr, nullptr);
       }
-      for (int s = 0; s < S::kRopes; ++s) {
-        const int issued = (ropes - s + S::kRopes - 1) / S::kRopes;
-        if (issued > 0) wait_parity_bounded(&sm.rope_full[s], (issued - 1) & 1, nullptr, nullptr);
+      for (; ropes > 0; --ropes) {
+        rope.at = rope.at == 0 ? (rope.phase ^= 1, S::kRopes - 1) : rope.at - 1;
+        wait_parity_bounded(&sm.rope_full[rope.at], rope.phase, nullptr, nullptr);
       }
     }
     __syncwarp();
   } else if (warp == 1) {
     // =========================== S^T = K Q^T ===========================
     if (lane == 0) {
-      constexpr uint32_t idesc = cosa::idesc_bf16_f32(128, N, false, false);
-      const uint64_t qd = smem_desc(smem_u32(sm.q), 16, 1024, 2), kd = smem_desc(smem_u32(sm.ring), 16, 1024, 2);
-      const uint64_t rd = smem_desc(smem_u32(sm.rope), 16, 1024, 2);
+      constexpr uint32_t idesc = cosa::idesc_bf16_f32(128, N, false, false), hi = desc_hi(1024, 2);
+      const uint32_t qd = desc_lo(smem_u32(sm.q), 16), kd = desc_lo(smem_u32(sm.ring), 16), rd = desc_lo(smem_u32(sm.rope), 16);
+      Ring<S::kSlots> ring;
+      Ring<S::kRopes> rope;
+      Ring<2> sbuf;
       int tile = 0, turn = 0;
       bool ok = true;
       while (ok && pieces.next(a, pc)) {
         if (pc.t0 == pc.t1) continue;
         ok = wait_parity_bounded(&sm.q_ready, turn++ & 1, abort_flag, a.status);
-        for (int t = pc.t0; t < pc.t1 && ok; ++t, ++tile) {
-          const int sb = tile & 1;
-          if (tile >= 2) ok = wait_parity_bounded(&sm.s_empty[sb], (tile / 2 - 1) & 1, abort_flag, a.status);
-          const uint32_t d = tmem + S::kTmemS + sb * N;
+        for (int t = pc.t0; t < pc.t1 && ok; ++t) {
+          if (tile == 2) ok = wait_parity_bounded(&sm.s_empty[sbuf.at], sbuf.phase ^ 1, abort_flag, a.status);
+          else ++tile;
+          const uint32_t d = tmem + S::kTmemS + sbuf.at * N;
           // the rotated part comes last where P^T goes over it, else first
           auto rotated = [&] {
-            const int s = tile % S::kRopes;
-            ok = ok && wait_parity_bounded(&sm.rope_full[s], (tile / S::kRopes) & 1, abort_flag, a.status);
+            ok = ok && wait_parity_bounded(&sm.rope_full[rope.at], rope.phase, abort_flag, a.status);
             if (!ok) return;
             tc_fence_after();
+            const uint32_t k0 = rd + rope.at * (kColumn >> 4);
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              umma_ss(d, rd + ((s * kColumn + k * 32) >> 4), qd + ((DV / 64 * N * 128 + k * 32) >> 4), idesc, S::kAlias || k > 0);
-            if (!S::kAlias) umma_commit(&sm.rope_empty[s]);
+            for (int k = 0; k < 4; ++k) mma(d, k0 + 2 * k, hi, qd + ((DV / 64 * N * 128) >> 4) + 2 * k, hi, idesc, S::kAlias || k > 0);
+            if (!S::kAlias) umma_commit(&sm.rope_empty[rope.at]);
+            rope.next();
           };
           if constexpr (S::kLatent && !S::kAlias) rotated();
           constexpr int kKeys = S::kLatent ? S::kPairs : 1;      // ring slots with keys
-#pragma unroll 1
+#pragma unroll
           for (int i = 0; i < kKeys; ++i) {
-            const int64_t pair = static_cast<int64_t>(tile) * S::kPairs + i;
-            const int s = static_cast<int>(pair % S::kSlots);
-            ok = ok && wait_parity_bounded(&sm.full[s], (pair / S::kSlots) & 1, abort_flag, a.status);
+            ok = ok && wait_parity_bounded(&sm.full[ring.at], ring.phase, abort_flag, a.status);
             if (!ok) break;
             tc_fence_after();
+            const uint32_t k0 = kd + ring.at * (kPair >> 4);
 #pragma unroll
             for (int k = 0; k < (S::DK == 64 ? 4 : 8); ++k)
-              umma_ss(d, kd + ((s * kPair + (k / 4) * kColumn + (k % 4) * 32) >> 4),
-                      qd + (((2 * i + k / 4) * N * 128 + (k % 4) * 32) >> 4), idesc, (S::kLatent && !S::kAlias) || i > 0 || k > 0);
-            if (!S::kLatent && S::DK == 128) umma_commit(&sm.empty[s]);
+              mma(d, k0 + (k / 4) * (kColumn >> 4) + (k % 4) * 2, hi, qd + (2 * i + k / 4) * (N * 128 >> 4) + (k % 4) * 2, hi, idesc,
+                  (S::kLatent && !S::kAlias) || i > 0 || k > 0);
+            if (!S::kLatent && S::DK == 128) umma_commit(&sm.empty[ring.at]);
+            ring.next();
           }
+          if (S::kPairs > kKeys) ring.next();      // the values' slot
           if constexpr (S::kAlias) rotated();
-          if (ok) umma_commit(&sm.s_full[sb]);
+          if (ok) umma_commit(&sm.s_full[sbuf.at]);
+          sbuf.next();
         }
       }
       umma_commit(&sm.cleanup);
@@ -488,9 +512,11 @@ __global__ void __launch_bounds__(S::kThreads, 1)
   } else if (warp == 2) {
     // =========================== O^T += V^T P^T ===========================
     constexpr uint32_t idesc = cosa::idesc_bf16_f32(128, N, true, true);
-    constexpr int kLayout = S::kPRow == 128 ? 2 : S::kPRow == 64 ? 4 : 6;
-    const uint64_t vd = smem_desc(smem_u32(sm.ring), kColumn, 1024, 2);
-    const uint64_t pd = smem_desc(S::kAlias ? smem_u32(sm.rope) : smem_u32(sm.p), kColumn, 8 * S::kPRow, kLayout);
+    constexpr uint32_t v_hi = desc_hi(1024, 2), p_hi = desc_hi(8 * S::kPRow, S::kPRow == 128 ? 2 : S::kPRow == 64 ? 4 : 6);
+    constexpr int kFirst = S::DK == 64 ? 1 : 0;      // columns of a slot from here on are values
+    const uint32_t vd = desc_lo(smem_u32(sm.ring), kColumn), pd = desc_lo(S::kAlias ? smem_u32(sm.rope) : smem_u32(sm.p), kColumn);
+    Ring<S::kSlots> ring;
+    Ring<S::kPBufs == 2 ? 2 : 1> pbuf;
     int tile = 0;
     bool ok = true;
     while (ok && pieces.next(a, pc)) {
@@ -498,7 +524,7 @@ __global__ void __launch_bounds__(S::kThreads, 1)
       const int ctx = pc.r.len - pc.r.n;
       const bool differ = pc.r.n > 1 || a.tree_mask;      // the rows may differ in what they see
       for (int t = pc.t0; t < pc.t1 && ok; ++t, ++tile) {
-        // bit i: lane's slots 4 * lane + i are empty (their values must be 0: 0 times what is not finite is not)
+        // bit i: slot 4 * lane + i is empty (its values must be 0: 0 times what is not finite is not)
         unsigned empty = 0;
         int looked = -2, phys = -1;
 #pragma unroll
@@ -506,31 +532,24 @@ __global__ void __launch_bounds__(S::kThreads, 1)
           const int slot = t * kTile + 4 * lane + i;
           if (slot < pc.r.len && slot >> a.page_shift != looked) {
             looked = slot >> a.page_shift;
-            phys = table[looked];
+            phys = __ldg(table + looked);
           }
           if (slot >= pc.r.len || phys < 0 || phys >= a.num_pages) empty |= 1u << i;
         }
-        const bool holes = __any_sync(kAll, empty);
         const int tail0 = differ ? max(ctx - t * kTile, 0) : kTile, tail1 = min(pc.r.len - t * kTile, kTile);
-        const int pb = S::kPBufs == 2 ? tile & 1 : 0, uses = S::kPBufs == 2 ? tile / 2 : tile;
-        if (!warp_wait(&sm.p_full[pb], uses & 1, abort_flag, a.status)) { ok = false; break; }
+        const bool unclean = __any_sync(kAll, empty) || tail0 < tail1;
+        if (S::kPairs > 1 && !S::kLatent) ring.next();      // the keys' slot
         bool found = false;
-#pragma unroll 1
-        for (int m = 0; m < S::kBlocks; ++m) {
-          const int64_t pair = static_cast<int64_t>(tile) * S::kPairs + (S::kLatent ? m : S::kPairs - 1);
-          const int s = static_cast<int>(pair % S::kSlots);
-          if (!warp_wait(&sm.full[s], (pair / S::kSlots) & 1, abort_flag, a.status)) { ok = false; break; }
-          constexpr int kFirst = S::DK == 64 ? 1 : 0;      // columns of the slot that are values
-          if (holes) {
-            for (int i = 0; i < 4; ++i)
-              if (empty >> i & 1)
-                for (int c = kFirst; c < 2; ++c)
-                  for (int e = 0; e < 8; ++e)
-                    *reinterpret_cast<uint4*>(&sm.ring[s][c * kColumn + (4 * lane + i) * 128 + e * 16]) = make_uint4(0, 0, 0, 0);
-          }
+        // The values of a slot of the ring, as zeros where there are none or they are not finite.
+        auto clean = [&](uint8_t* values) {
+          for (int i = 0; i < 4; ++i)
+            if (empty >> i & 1)
+              for (int c = kFirst; c < 2; ++c)
+                for (int e = 0; e < 8; ++e) *reinterpret_cast<uint4*>(values + c * kColumn + (4 * lane + i) * 128 + e * 16) = make_uint4(0, 0, 0, 0);
+          __syncwarp();
           for (int e = tail0 * 16 + lane; e < tail1 * 16; e += 32) {      // 16-byte pieces of the new tokens' values
             if ((e & 15) < 8 * kFirst) continue;
-            uint4* at = reinterpret_cast<uint4*>(&sm.ring[s][(e & 15) / 8 * kColumn + (e >> 4) * 128 + (e & 7) * 16]);
+            uint4* at = reinterpret_cast<uint4*>(values + (e & 15) / 8 * kColumn + (e >> 4) * 128 + (e & 7) * 16);
             uint4 x = *at;
             if (odd(x.x) || odd(x.y) || odd(x.z) || odd(x.w)) {
               found = true;
@@ -543,29 +562,40 @@ __global__ void __launch_bounds__(S::kThreads, 1)
               *at = x;
             }
           }
-          if (holes || tail0 < tail1) {
-            fence_proxy_async_smem();
-            __syncwarp();
-          }
-          if (lane == 0) {
-            tc_fence_after();
-            const uint64_t vs = vd + ((s * kPair) >> 4), ps = pd + ((pb * S::kPBytes) >> 4);
-#pragma unroll
-            for (int k = 0; k < kTile / 16; ++k)
-              umma_ss(tmem + S::kTmemO + m * N, vs + ((k * 2048) >> 4), ps + ((k * 16 * S::kPRow) >> 4), idesc, t > pc.t0 || k > 0);
-            umma_commit(&sm.empty[s]);
-          }
+          fence_proxy_async_smem();
           __syncwarp();
+        };
+        if (unclean || lane == 0) ok = wait_parity_bounded(&sm.p_full[pbuf.at], pbuf.phase, abort_flag, a.status);
+        if (unclean) ok = __all_sync(kAll, ok);
+#pragma unroll
+        for (int m = 0; m < S::kBlocks; ++m) {
+          if (unclean) {
+            ok = ok && warp_wait(&sm.full[ring.at], ring.phase, abort_flag, a.status);
+            if (ok) clean(sm.ring[ring.at]);
+          }
+          if (lane == 0 && ok) {
+            // (the first product has waited for keys and latent vectors already)
+            if (!S::kLatent && S::DK == 128) ok = wait_parity_bounded(&sm.full[ring.at], ring.phase, abort_flag, a.status);
+            if (ok) {
+              tc_fence_after();
+              const uint32_t v0 = vd + ring.at * (kPair >> 4), p0 = pd + pbuf.at * (S::kPBytes >> 4);
+#pragma unroll
+              for (int k = 0; k < kTile / 16; ++k)
+                mma(tmem + S::kTmemO + m * N, v0 + k * (2048 >> 4), v_hi, p0 + k * (S::kPRow), p_hi, idesc, t > pc.t0 || k > 0);
+              umma_commit(&sm.empty[ring.at]);
+            }
+          }
+          ring.next();
         }
-        if (!ok) break;
-        found = __any_sync(kAll, found);
-        if (lane == 0) {
+        if (unclean) found = __any_sync(kAll, found);
+        if (lane == 0 && ok) {
           if (found) sm.odd_values = 1;
           if (S::kAlias) umma_commit(&sm.rope_empty[0]);
           umma_commit(&sm.pv_done[tile & 1]);
           mbar_arrive(&sm.pv_done[tile & 1]);
         }
-        __syncwarp();
+        pbuf.next();
+        ok = __shfl_sync(kAll, ok, 0);
       }
     }
     if (lane == 0) {
@@ -595,7 +625,7 @@ __global__ void __launch_bounds__(S::kThreads, 1)
       }
       if (!a.join_items) a.joins[cta] = mine;
       else if (cta == 0)
-        for (int64_t i = sm.start.items; i < a.join_items; ++i) a.joins[i] = none;
+        for (int i = sm.start.items; i < a.join_items; ++i) a.joins[i] = none;
     }
     __syncwarp();
   } else {
@@ -621,34 +651,27 @@ __global__ void __launch_bounds__(S::kThreads, 1)
       const int row0 = pc.row_tile * N;
       if (!meet()) break;                  // the last piece is done with what follows
       if (tid < N) {
-        const int row = row0 + tid, node = min(row, rows - 1) / a.group;
-        sm.row[tid] = row < rows ? (r.tok0 + node) * a.num_q_heads + pc.head * a.group + row % a.group : -1;
+        const int row = row0 + tid, node = static_cast<uint32_t>(min(row, rows - 1)) / static_cast<uint32_t>(a.group);
+        const int head = pc.head * a.group + row - node * a.group;
+        sm.row[tid] = row < rows ? (r.tok0 + node) * a.num_q_heads + head : -1;
         sm.node[tid] = node;
-        sm.q_at[tid] = row < rows ? (r.tok0 + node) * a.q_stride + (pc.head * a.group + row % a.group) * DV : -1;
-        if (S::kLatent) sm.r_at[tid] = (r.tok0 + node) * a.q_rope_stride + row % a.group * (S::DK - DV);
-        sm.mask[tid] = a.tree_mask ? static_cast<uint64_t>(a.tree_mask[r.tok0 + node]) : 0;
-        sm.base[tid] = kNone;
+        sm.q_at[tid] = row < rows ? (r.tok0 + node) * a.q_stride + head * DV : -1;
+        if (S::kLatent) sm.r_at[tid] = (r.tok0 + node) * a.q_rope_stride + head * (S::DK - DV);
+        sm.mask[tid] = a.tree_mask ? static_cast<uint64_t>(__ldg(a.tree_mask + r.tok0 + node)) : 0;
+        sm.base[tid] = -kNone;
       }
       if (pc.t0 < pc.t1) {
         // queries into rows of 128 bytes per 64 values, swizzled; rows behind the last are 0
         if (!meet()) break;
-        constexpr int kPieces16 = S::DK / 8, kBatch = 6;
-#pragma unroll 1
-        for (int e0 = tid; e0 < N * kPieces16; e0 += kBatch * kSoftmax) {
-          uint4 x[kBatch];
-#pragma unroll
-          for (int k = 0; k < kBatch; ++k) {
-            const int e = e0 + k * kSoftmax, row = e / kPieces16, c = e % kPieces16;
-            x[k] = make_uint4(0, 0, 0, 0);
-            if (e < N * kPieces16 && sm.q_at[row] >= 0)
-              x[k] = *reinterpret_cast<const uint4*>(S::kLatent && c >= DV / 8 ? a.q_rope + sm.r_at[row] + c * 8 - DV : a.q + sm.q_at[row] + c * 8);
-          }
-#pragma unroll
-          for (int k = 0; k < kBatch; ++k) {
-            const int e = e0 + k * kSoftmax, row = e / kPieces16, c = e % kPieces16;
-            if (e < N * kPieces16) *reinterpret_cast<uint4*>(&sm.q[c / 8 * N * 128 + row * 128 + ((c ^ row) & 7) * 16]) = x[k];
-          }
+        constexpr int kPieces16 = S::DK / 8;
+#pragma unroll 3
+        for (int e = tid; e < N * kPieces16; e += kSoftmax) {
+          const int row = e / kPieces16, c = e % kPieces16;
+          const int64_t at = sm.q_at[row];
+          const uint16_t* src = S::kLatent && c >= DV / 8 ? a.q_rope + sm.r_at[row] + c * 8 - DV : a.q + at + c * 8;
+          copy16(&sm.q[c / 8 * N * 128 + row * 128 + ((c ^ row) & 7) * 16], at < 0 ? a.q : src, at >= 0);
         }
+        asm volatile("cp.async.wait_all;" ::: "memory");
         fence_proxy_async_smem();
       }
       if (!meet()) break;
@@ -656,44 +679,69 @@ __global__ void __launch_bounds__(S::kThreads, 1)
 
       const int32_t* table = a.page_table + static_cast<size_t>(pc.b) * a.max_pages_per_req;
       const int ctx = r.len - r.n;
-      float l[NC];
+      float l[NC];                         // sums of this thread's slots
 #pragma unroll
       for (int i = 0; i < NC; ++i) l[i] = 0.f;
       for (int t = pc.t0; t < pc.t1; ++t, ++tile) {
         const int sb = tile & 1, slot = t * kTile + at;
         bool there = slot < r.len;
         if (there) {
-          const int phys = table[slot >> a.page_shift];
+          const int phys = __ldg(table + (slot >> a.page_shift));
           there = phys >= 0 && phys < a.num_pages;
         }
         bool fail = !warp_wait(&sm.s_full[sb], (tile / 2) & 1, abort_flag, a.status);
+        // P^T's buffer is free once the product before (or before that) has read it
+        constexpr int kBack = S::kPBufs == 2 ? 2 : 1;
+        if (!fail && tile >= kBack)
+          fail = !warp_wait(&sm.pv_done[(tile - kBack) & 1], ((tile - kBack) / 2) & 1, abort_flag, a.status);
+        uint8_t* p = (S::kAlias ? sm.rope[0] : sm.p[S::kPBufs == 2 ? tile & 1 : 0]) + c0 / 64 * kColumn;
         float x[NC];
+        // the tile's logits, -infinity where the row does not see the slot
+        auto logits = [&] {
+          load_columns<NC>(tmem + lanes + S::kTmemS + sb * N + c0, x);
+          if (!there) {
+#pragma unroll
+            for (int i = 0; i < NC; ++i) x[i] = -INFINITY;
+          } else if (slot >= ctx) {
+            const int j = slot - ctx;
+#pragma unroll
+            for (int i = 0; i < NC; ++i)
+              if (a.tree_mask ? !(sm.mask[c0 + i] >> j & 1) : j > sm.node[c0 + i]) x[i] = -INFINITY;
+          }
+          __syncwarp();
+        };
+        // x <- exp2(x * scale - reference), as bf16 to P^T; the largest as bf16 bits, in either half
+        auto weights = [&] {
+          uint32_t top = 0;
+#pragma unroll
+          for (int i = 0; i < NC; i += 8) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = i; e < i + 8; e += 4) {
+              const float4 b = *reinterpret_cast<const float4*>(&sm.base[c0 + e]);
+              fma2(x[e], x[e + 1], x[e], x[e + 1], scale, b.x, b.y);
+              fma2(x[e + 2], x[e + 3], x[e + 2], x[e + 3], scale, b.z, b.w);
+#pragma unroll
+              for (int k = e; k < e + 4; ++k) x[k] = cosa::ex2_approx(x[k]);
+              w[(e - i) / 2] = cosa::pack_bf16x2(x[e], x[e + 1]);
+              w[(e - i) / 2 + 1] = cosa::pack_bf16x2(x[e + 2], x[e + 3]);
+              top = __vmaxu2(top, __vmaxu2(w[(e - i) / 2], w[(e - i) / 2 + 1]));
+            }
+            *reinterpret_cast<uint4*>(p + p_offset<S::kPRow>(at, (c0 % 64 + i) / 8)) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+          return top;
+        };
+        bool high = false;
         if (!fail) {
           tc_fence_after();
-          load_columns<NC>(tmem + lanes + S::kTmemS + sb * N + c0, x);
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sm.s_empty[sb]);
-        }
-        if (!there) {
-#pragma unroll
-          for (int i = 0; i < NC; ++i) x[i] = -INFINITY;
-        } else if (slot >= ctx) {
-          const int j = slot - ctx;
-#pragma unroll
-          for (int i = 0; i < NC; ++i)
-            if (a.tree_mask ? !(sm.mask[c0 + i] >> j & 1) : j > sm.node[c0 + i]) x[i] = -INFINITY;
-        }
-        bool high = false;
-#pragma unroll
-        for (int i = 0; i < NC; i += 4) {
-          const float4 b = *reinterpret_cast<const float4*>(&sm.base[c0 + i]);
-          high |= fmaf(x[i], scale, -b.x) > kRescaleLog2 || fmaf(x[i + 1], scale, -b.y) > kRescaleLog2 ||
-                  fmaf(x[i + 2], scale, -b.z) > kRescaleLog2 || fmaf(x[i + 3], scale, -b.w) > kRescaleLog2;
+          logits();
+          const uint32_t top = weights();
+          high = (top & 0xFFFFu) > kHigh || top >> 16 > kHigh;
         }
         if (named_bar_red_or(my_bar, 128, high || fail)) {
           if (named_bar_red_or(my_bar, 128, fail)) { ok = false; break; }
-          // some logit is far above its row's reference: the rows' maxima over the tile
+          // some logit is far above its row's reference (or NaN): the rows' maxima over the tile, and the weights again
+          logits();
           float mine = 0.f;
 #pragma unroll
           for (int i = 0; i < NC; ++i) {
@@ -705,11 +753,12 @@ __global__ void __launch_bounds__(S::kThreads, 1)
           if (at < NC) {
             const int c = c0 + at;
             const float top = fmaxf(fmaxf(sm.part[0][c], sm.part[1][c]), fmaxf(sm.part[2][c], sm.part[3][c]));
-            const float was = sm.base[c], now = top == -INFINITY ? was : fmaxf(was, top * scale);
-            sm.base[c] = now;
+            const float was = -sm.base[c], now = top == -INFINITY ? was : fmaxf(was, top * scale);
+            sm.base[c] = -now;
             sm.alpha[c] = now == was ? 1.f : cosa::ex2_approx(was - now);
           }
           named_bar_sync(my_bar, 128);
+          weights();
 #pragma unroll
           for (int i = 0; i < NC; ++i) l[i] *= sm.alpha[c0 + i];
           if (t > pc.t0) {
@@ -730,36 +779,19 @@ __global__ void __launch_bounds__(S::kThreads, 1)
                 }
               }
               cosa::tmem_wait_st();
-              tc_fence_before();
             }
           }
         }
-        // P^T's buffer is free once the product before (or before that) has read it
-        constexpr int kBack = S::kPBufs == 2 ? 2 : 1;
-        if (!fail && tile >= kBack)
-          fail = !warp_wait(&sm.pv_done[(tile - kBack) & 1], ((tile - kBack) / 2) & 1, abort_flag, a.status);
         if (!fail) {
-          uint8_t* p = (S::kAlias ? sm.rope[0] : sm.p[S::kPBufs == 2 ? tile & 1 : 0]) + c0 / 64 * kColumn;
-#pragma unroll
-          for (int i = 0; i < NC; i += 8) {
-            uint32_t w[4];
-#pragma unroll
-            for (int e = 0; e < 8; e += 4) {
-              const float4 b = *reinterpret_cast<const float4*>(&sm.base[c0 + i + e]);
-              const float p0 = cosa::ex2_approx(fmaf(x[i + e], scale, -b.x)), p1 = cosa::ex2_approx(fmaf(x[i + e + 1], scale, -b.y));
-              const float p2 = cosa::ex2_approx(fmaf(x[i + e + 2], scale, -b.z)), p3 = cosa::ex2_approx(fmaf(x[i + e + 3], scale, -b.w));
-              l[i + e] += p0;
-              l[i + e + 1] += p1;
-              l[i + e + 2] += p2;
-              l[i + e + 3] += p3;
-              w[e / 2] = cosa::pack_bf16x2(p0, p1);
-              w[e / 2 + 1] = cosa::pack_bf16x2(p2, p3);
-            }
-            *reinterpret_cast<uint4*>(p + p_offset<S::kPRow>(at, (c0 % 64 + i) / 8)) = make_uint4(w[0], w[1], w[2], w[3]);
-          }
+          tc_fence_before();
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&sm.p_full[S::kPBufs == 2 ? tile & 1 : 0]);
+          if (lane == 0) {
+            mbar_arrive(&sm.p_full[S::kPBufs == 2 ? tile & 1 : 0]);
+            mbar_arrive(&sm.s_empty[sb]);
+          }
+#pragma unroll
+          for (int i = 0; i < NC; i += 2) cosa::add2_acc(l[i], l[i + 1], x[i], x[i + 1]);
         }
         // a wait that ran out has set the abort flag: the next wait ends too, and its vote stops the group
       }
@@ -781,7 +813,7 @@ __global__ void __launch_bounds__(S::kThreads, 1)
       if (named_bar_red_or(my_bar, 128, fail)) { ok = false; break; }
       if (at < NC) {
         const int c = c0 + at;
-        const float sum = (sm.part[0][c] + sm.part[1][c]) + (sm.part[2][c] + sm.part[3][c]), m = sm.base[c];
+        const float sum = (sm.part[0][c] + sm.part[1][c]) + (sm.part[2][c] + sm.part[3][c]), m = -sm.base[c];
         if (pc.slot >= 0) {
           float* ml = a.part_ml + (static_cast<int64_t>(pc.slot) * N + c) * 2;
           ml[0] = m == kNone ? -INFINITY : m;
@@ -802,6 +834,7 @@ __global__ void __launch_bounds__(S::kThreads, 1)
 #pragma unroll 1
           for (int i = 0; i < NC; i += 16) {
             float o[16] = {};
+            __syncwarp();
             if (pc.t0 < pc.t1) load_columns<16>(tmem + lanes + S::kTmemO + m * N + c0 + i, o);
             if (odd_values && d >= 0) {
               // what was not finite among the new tokens' values, for the rows that see it
@@ -933,6 +966,11 @@ int rows_of_tile(const PagedLaunch& L) {
   return n;
 }
 
+// At most so many items: what the tokens fill and a part of a row tile for every request.
+int64_t most_items(const PagedLaunch& L) {
+  return L.num_kv_heads * (L.total_tokens * static_cast<int64_t>(L.num_q_heads / L.num_kv_heads) / rows_of_tile(L) + L.num_reqs);
+}
+
 template <class S>
 cudaError_t launch_shape(const PagedLaunch& L, cudaStream_t stream) {
   Args a{};
@@ -949,8 +987,7 @@ cudaError_t launch_shape(const PagedLaunch& L, cudaStream_t stream) {
   a.part_o = static_cast<float*>(L.workspace);
   a.part_ml = a.part_o + static_cast<size_t>(2 * kCtas) * S::N * S::DV;
   a.joins = reinterpret_cast<Join*>(a.part_ml + static_cast<size_t>(2 * kCtas) * S::N * 2);
-  // at most so many items: what the tokens fill and a part of a row tile for every request
-  const int64_t group = L.num_q_heads / L.num_kv_heads, items = L.num_kv_heads * (L.total_tokens * group / S::N + L.num_reqs);
+  const int64_t group = L.num_q_heads / L.num_kv_heads, items = most_items(L);
   a.join_items = items <= kCtas ? static_cast<int>(items) : 0;
   a.status = L.status;
   a.q_stride = L.q_stride;
@@ -1002,6 +1039,8 @@ cudaError_t launch_width(const PagedLaunch& L, cudaStream_t stream) {
 }
 
 }  // namespace
+
+bool paged_fits(const PagedLaunch& L) { return most_items(L) <= INT32_MAX / (int64_t{L.max_seqlen} / kTile + 2); }
 
 size_t paged_workspace_bytes(const PagedLaunch& L) {
   const size_t dv = static_cast<size_t>(L.latent_dim ? L.latent_dim : L.head_dim);

@@ -109,6 +109,9 @@ def test_parameters_refused(C):
                      (dict(q_rope_stride=500), INV), (dict(q_rope_head_stride=32), INV), (dict(k_rope_stride=32), INV), (dict(q_head_stride=1 << 33), INV)):
         assert prefill(C, params(C, **kw)) == code, kw
     assert latent(C, params(C, q_rope_stride=500)) == INV
+    many = dict(num_reqs=60000, total_tokens=60000, max_seqlen=1 << 23, max_pages_per_req=1 << 17)     # more tiles than 31 bits number
+    assert tree(C, params(C, **many)) == latent(C, params(C, **many)) == UNS
+    assert C.cosa_tree_attention_workspace_size(params(C, **many)) == 0
     for call in ATTENTIONS:
         assert call(C, params(C, num_q_heads=1 << 14, total_tokens=1 << 18)) == UNS
 
