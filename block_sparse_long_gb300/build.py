@@ -29,7 +29,7 @@ KV_SOURCES = ["kv_api.cu", "kv_rope.cu", "kv_convert.cu", "kv_attention.cu", "kv
 KV_HEADERS = ["ptx.cuh", "kv_internal.h", "kv_layout.cuh", "kv_angles.cuh"]
 ATTN_LIB = os.path.join(HERE, "libcosa_attn.so")
 ATTN_SOURCES = ["attn_api.cu", "attn_tma.cu", "attn_rope.cu", "attn_commit.cu", "attn_paged.cu", "attn_prefill.cu"]
-ATTN_HEADERS = KV_HEADERS + ["attn_internal.h", "attn_tma.h"]
+ATTN_HEADERS = KV_HEADERS + ["attn_internal.h", "attn_tma.h", "attn_mma.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-std=c++17", "-O3", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall", "--expt-relaxed-constexpr"]
 

@@ -29,6 +29,7 @@
 #include <cuda_runtime.h>
 
 #include "attn_internal.h"
+#include "attn_mma.cuh"
 #include "attn_tma.h"
 #include "kv_internal.h"
 #include "kv_layout.cuh"
@@ -55,7 +56,6 @@ constexpr int kPair = 2 * kColumn;
 constexpr float kNone = -3e38f;            // reference of a row that has seen nothing
 constexpr uint32_t kHigh = 0x4380;         // 2^8 in bf16: a weight above it moves its row's reference
 constexpr float kLn2 = 0.69314718055994531f;
-constexpr unsigned kAll = 0xffffffffu;
 
 // DK, DV: values of a key and a value.  kLatent: the value is the key's first DV values.  N: query rows of a row tile.
 template <int DK_, int DV_, bool LATENT, int N_>
@@ -261,33 +261,6 @@ __device__ __forceinline__ int owner(int total, int u) {
   return c;
 }
 
-// A place in a ring of kCount barriers, and the parity of its use.
-template <int kCount>
-struct Ring {
-  int at = 0;
-  uint32_t phase = 0;
-  __device__ __forceinline__ void next(int step = 1) {
-    at += step;
-    if (at >= kCount) at -= kCount, phase ^= 1;
-  }
-};
-
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status) {
-  return __all_sync(kAll, wait_parity_bounded(bar, parity, abort_flag, status));
-}
-
-// Shared-memory matrix descriptors in two halves; layout 2, 4, 6: 128-, 64-, 32-byte swizzle.  Offsets add to the low half.
-__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) { return (saddr & 0x3FFFFu) >> 4 | (lbo >> 4) << 16; }
-__host__ __device__ constexpr uint32_t desc_hi(uint32_t sbo, int layout) { return sbo >> 4 | 1u << 14 | static_cast<uint32_t>(layout) << 29; }
-
-__device__ __forceinline__ void mma(uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi, uint32_t idesc, bool accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tmov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\tsetp.ne.b32 p, %6, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d),
-      "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(static_cast<uint32_t>(accumulate))
-      : "memory");
-}
-
 // (d0, d1) = (a0, a1) * b + (c0, c1)
 __device__ __forceinline__ void fma2(float& d0, float& d1, float a0, float a1, float b, float c0, float c1) {
   asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %4};\n\tmov.b64 c, {%5, %6};\n\t"
@@ -329,10 +302,6 @@ __device__ __forceinline__ float warp_max(float x) {
   i = __reduce_max_sync(kAll, i);
   i ^= (i >> 31) & 0x7fffffff;
   return __int_as_float(i);
-}
-
-__device__ __forceinline__ bool odd(uint32_t two) {        // either bf16 is not finite
-  return (two & 0x7F80u) == 0x7F80u || (two & 0x7F800000u) == 0x7F800000u;
 }
 
 template <class S>
@@ -458,53 +427,60 @@ __global__ void __launch_bounds__(S::kThreads, 1)
     __syncwarp();
   } else if (warp == 1) {
     // =========================== S^T = K Q^T ===========================
-    if (lane == 0) {
-      constexpr uint32_t idesc = cosa::idesc_bf16_f32(128, N, false, false), hi = desc_hi(1024, 2);
-      const uint32_t qd = desc_lo(smem_u32(sm.q), 16), kd = desc_lo(smem_u32(sm.ring), 16), rd = desc_lo(smem_u32(sm.rope), 16);
-      Ring<S::kSlots> ring;
-      Ring<S::kRopes> rope;
-      Ring<2> sbuf;
-      int tile = 0, turn = 0;
-      bool ok = true;
-      while (ok && pieces.next(a, pc)) {
-        if (pc.t0 == pc.t1) continue;
-        ok = wait_parity_bounded(&sm.q_ready, turn++ & 1, abort_flag, a.status);
-        for (int t = pc.t0; t < pc.t1 && ok; ++t) {
-          if (tile == 2) ok = wait_parity_bounded(&sm.s_empty[sbuf.at], sbuf.phase ^ 1, abort_flag, a.status);
-          else ++tile;
-          const uint32_t d = tmem + S::kTmemS + sbuf.at * N;
-          // the rotated part comes last where P^T goes over it, else first
-          auto rotated = [&] {
-            ok = ok && wait_parity_bounded(&sm.rope_full[rope.at], rope.phase, abort_flag, a.status);
-            if (!ok) return;
-            tc_fence_after();
-            const uint32_t k0 = rd + rope.at * (kColumn >> 4);
+    constexpr uint32_t idesc = cosa::idesc_bf16_f32(128, N, false, false), hi = desc_hi(1024, 2);
+    const uint32_t qd = desc_lo(smem_u32(sm.q), 16), kd = desc_lo(smem_u32(sm.ring), 16), rd = desc_lo(smem_u32(sm.rope), 16);
+    Ring<S::kSlots> ring;
+    Ring<S::kRopes> rope;
+    Ring<2> sbuf;
+    int tile = 0, turn = 0;
+    bool ok = true;
+    while (ok && pieces.next(a, pc)) {
+      if (pc.t0 == pc.t1) continue;
+      ok = warp_wait(&sm.q_ready, turn++ & 1, abort_flag, a.status);
+      for (int t = pc.t0; t < pc.t1 && ok; ++t) {
+        if (tile == 2) ok = warp_wait(&sm.s_empty[sbuf.at], sbuf.phase ^ 1, abort_flag, a.status);
+        else ++tile;
+        const uint32_t d = tmem + S::kTmemS + sbuf.at * N;
+        // the rotated part comes last where P^T goes over it, else first
+        auto rotated = [&] {
+          ok = ok && warp_wait(&sm.rope_full[rope.at], rope.phase, abort_flag, a.status);
+          if (!ok) return;
+          tc_fence_after();
+          const uint32_t k0 = rd + rope.at * (kColumn >> 4);
+          if (elect_one()) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) mma(d, k0 + 2 * k, hi, qd + ((DV / 64 * N * 128) >> 4) + 2 * k, hi, idesc, S::kAlias || k > 0);
+            for (int k = 0; k < 4; ++k) mma_ss(d, k0 + 2 * k, hi, qd + ((DV / 64 * N * 128) >> 4) + 2 * k, hi, idesc, S::kAlias || k > 0);
             if (!S::kAlias) umma_commit(&sm.rope_empty[rope.at]);
-            rope.next();
-          };
-          if constexpr (S::kLatent && !S::kAlias) rotated();
-          constexpr int kKeys = S::kLatent ? S::kPairs : 1;      // ring slots with keys
+          }
+          __syncwarp();
+          rope.next();
+        };
+        if constexpr (S::kLatent && !S::kAlias) rotated();
+        constexpr int kKeys = S::kLatent ? S::kPairs : 1;      // ring slots with keys
 #pragma unroll
-          for (int i = 0; i < kKeys; ++i) {
-            ok = ok && wait_parity_bounded(&sm.full[ring.at], ring.phase, abort_flag, a.status);
-            if (!ok) break;
-            tc_fence_after();
-            const uint32_t k0 = kd + ring.at * (kPair >> 4);
+        for (int i = 0; i < kKeys; ++i) {
+          ok = ok && warp_wait(&sm.full[ring.at], ring.phase, abort_flag, a.status);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t k0 = kd + ring.at * (kPair >> 4);
+          if (elect_one()) {
 #pragma unroll
             for (int k = 0; k < (S::DK == 64 ? 4 : 8); ++k)
-              mma(d, k0 + (k / 4) * (kColumn >> 4) + (k % 4) * 2, hi, qd + (2 * i + k / 4) * (N * 128 >> 4) + (k % 4) * 2, hi, idesc,
-                  (S::kLatent && !S::kAlias) || i > 0 || k > 0);
+              mma_ss(d, k0 + (k / 4) * (kColumn >> 4) + (k % 4) * 2, hi, qd + (2 * i + k / 4) * (N * 128 >> 4) + (k % 4) * 2, hi, idesc,
+                     (S::kLatent && !S::kAlias) || i > 0 || k > 0);
             if (!S::kLatent && S::DK == 128) umma_commit(&sm.empty[ring.at]);
-            ring.next();
           }
-          if (S::kPairs > kKeys) ring.next();      // the values' slot
-          if constexpr (S::kAlias) rotated();
-          if (ok) umma_commit(&sm.s_full[sbuf.at]);
-          sbuf.next();
+          __syncwarp();
+          ring.next();
         }
+        if (S::kPairs > kKeys) ring.next();      // the values' slot
+        if constexpr (S::kAlias) rotated();
+        if (ok && elect_one()) umma_commit(&sm.s_full[sbuf.at]);
+        __syncwarp();
+        sbuf.next();
       }
+    }
+    if (elect_one()) {
       umma_commit(&sm.cleanup);
       wait_parity_bounded(&sm.cleanup, 0, nullptr, nullptr);
     }
@@ -565,40 +541,37 @@ __global__ void __launch_bounds__(S::kThreads, 1)
           fence_proxy_async_smem();
           __syncwarp();
         };
-        if (unclean || lane == 0) ok = wait_parity_bounded(&sm.p_full[pbuf.at], pbuf.phase, abort_flag, a.status);
-        if (unclean) ok = __all_sync(kAll, ok);
+        ok = warp_wait(&sm.p_full[pbuf.at], pbuf.phase, abort_flag, a.status);
 #pragma unroll
         for (int m = 0; m < S::kBlocks; ++m) {
-          if (unclean) {
-            ok = ok && warp_wait(&sm.full[ring.at], ring.phase, abort_flag, a.status);
-            if (ok) clean(sm.ring[ring.at]);
-          }
-          if (lane == 0 && ok) {
-            // (the first product has waited for keys and latent vectors already)
-            if (!S::kLatent && S::DK == 128) ok = wait_parity_bounded(&sm.full[ring.at], ring.phase, abort_flag, a.status);
-            if (ok) {
-              tc_fence_after();
-              const uint32_t v0 = vd + ring.at * (kPair >> 4), p0 = pd + pbuf.at * (S::kPBytes >> 4);
+          // (the first product has waited for keys and latent vectors already)
+          if (unclean || (!S::kLatent && S::DK == 128)) ok = ok && warp_wait(&sm.full[ring.at], ring.phase, abort_flag, a.status);
+          if (!ok) break;
+          if (unclean) clean(sm.ring[ring.at]);
+          tc_fence_after();
+          const uint32_t v0 = vd + ring.at * (kPair >> 4), p0 = pd + pbuf.at * (S::kPBytes >> 4);
+          if (elect_one()) {
 #pragma unroll
-              for (int k = 0; k < kTile / 16; ++k)
-                mma(tmem + S::kTmemO + m * N, v0 + k * (2048 >> 4), v_hi, p0 + k * (S::kPRow), p_hi, idesc, t > pc.t0 || k > 0);
-              umma_commit(&sm.empty[ring.at]);
-            }
+            for (int k = 0; k < kTile / 16; ++k)
+              mma_ss(tmem + S::kTmemO + m * N, v0 + k * (2048 >> 4), v_hi, p0 + k * S::kPRow, p_hi, idesc, t > pc.t0 || k > 0);
+            umma_commit(&sm.empty[ring.at]);
           }
+          __syncwarp();
           ring.next();
         }
+        if (!ok) break;
         if (unclean) found = __any_sync(kAll, found);
-        if (lane == 0 && ok) {
+        if (elect_one()) {
           if (found) sm.odd_values = 1;
           if (S::kAlias) umma_commit(&sm.rope_empty[0]);
           umma_commit(&sm.pv_done[tile & 1]);
           mbar_arrive(&sm.pv_done[tile & 1]);
         }
+        __syncwarp();
         pbuf.next();
-        ok = __shfl_sync(kAll, ok, 0);
       }
     }
-    if (lane == 0) {
+    if (elect_one()) {
       umma_commit(&sm.cleanup);
       wait_parity_bounded(&sm.cleanup, 0, nullptr, nullptr);
     }

@@ -11,10 +11,12 @@
 //   warp 0      copies Q once, then K and V block by block (TMA).  Of the blocks on the diagonal, whose later keys some rows must
 //               not see, it clears from V what is not finite (0 times that is not 0); a row that does see such a value gets it
 //               added at the end.
-//   warps 1, 2  issue S and O of one tile each: S(j + 1) follows O(j) in the same thread's order, so P may lie over S.
+//   warp 1      issues the products, O(j) and S(j + 1) of the one tile, then of the other: the tiles take turns with the tensor
+//               core (with an issuer each they fell into step, and it idled while both had their softmax: 5600 cycles a block).
+//               In one thread's order S(j + 1) follows O(j), so P may lie over S.
 //   warp 3      owns the TMEM.
-//   warps 4-11  softmax, four warps a tile: a thread has a row.  The reference m lags the maximum by 2^8 at most, O is scaled only
-//               when it moves.
+//   warps 4-19  softmax, eight warps a tile: a thread has half a row.  The weights are taken against the row's reference of
+//               an earlier block; only if one passes 2^8 the tile stops for its maxima, scales O and takes them again.
 // CTAs start with the longest rows of a head and go head by head, so that a head's keys stay in L2.
 #include <cmath>
 #include <cstdint>
@@ -23,6 +25,7 @@
 #include <cuda_runtime.h>
 
 #include "attn_internal.h"
+#include "attn_mma.cuh"
 #include "attn_tma.h"
 #include "kv_internal.h"
 #include "kv_layout.cuh"
@@ -33,38 +36,40 @@ namespace {
 using cosa::mbar_arrive;
 using cosa::mbar_arrive_expect_tx;
 using cosa::mbar_init;
-using cosa::smem_desc_sw128;
 using cosa::smem_u32;
 using cosa::tc_fence_after;
 using cosa::tc_fence_before;
 using cosa::umma_commit;
 using cosa::wait_parity_bounded;
 
-constexpr int kThreads = 384;
+constexpr int kThreads = 640;
 constexpr int kBlock = 128;                // keys
 constexpr int kRows = 256;                 // queries of a CTA
 constexpr int kColumn = kBlock * 128;      // bytes of a 64-value wide column of 128 rows
-constexpr float kRescaleLog2 = 8.0f;
+constexpr int kHalf = kBlock / 2;          // keys of a thread's half row, and of a slot of values
+constexpr float kNone = -3e38f;            // reference of a row that has seen nothing
+constexpr uint32_t kHigh = 0x4380;         // 2^8 in bf16
 constexpr float kLn2 = 0.69314718055994531f;
-constexpr unsigned kAll = 0xffffffffu;
 constexpr uint32_t kTmemS = 0, kTmemO = 256;      // two of 128 columns each
 
 template <int D_>
 struct Shape {
   static constexpr int D = D_;
   static constexpr int kKeyColumns = D / 64 + 1, kValueColumns = D / 64;
-  static constexpr int kKeySlots = D == 128 ? 4 : 6;       // of one column
-  static constexpr int kValueSlots = D == 128 ? 2 : 3;     // of a block
+  // Slots of one column of 128 keys, and of 64 keys' values.  With heads of 128 there is room for eight columns in all; five
+  // and three leave either 20 products' time to come in.
+  static constexpr int kKeySlots = D == 128 ? 5 : 6, kValueSlots = D == 128 ? 3 : 6;
 };
 
 template <class S>
 struct alignas(1024) Smem {
   uint8_t q[2][S::kKeyColumns][kColumn];
   uint8_t k[S::kKeySlots][kColumn];
-  uint8_t v[S::kValueSlots][S::kValueColumns][kColumn];
+  uint8_t v[S::kValueSlots][S::kValueColumns][kHalf * 128];
   uint64_t q_full, k_full[S::kKeySlots], k_empty[S::kKeySlots], v_full[S::kValueSlots], v_empty[S::kValueSlots];
   uint64_t v_clear[4];                     // of the blocks on the diagonal
   uint64_t s_full[2], p_full[2], pv_done[2], cleanup;
+  float part[2][2][128];                   // of a row's halves: maxima, sums
   int32_t req, block;                      // this CTA's request (-1: none) and its block of queries
   int32_t odd_values;
   uint32_t tmem_base;
@@ -104,21 +109,18 @@ __device__ __forceinline__ Request request_of(const Args& a, int b) {
   return r;
 }
 
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status) {
-  return __all_sync(kAll, wait_parity_bounded(bar, parity, abort_flag, status));
-}
-
-__device__ __forceinline__ bool odd(uint32_t two) {        // either bf16 is not finite
-  return (two & 0x7F80u) == 0x7F80u || (two & 0x7F800000u) == 0x7F800000u;
-}
-
 template <class S>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap qrmap, const __grid_constant__ CUtensorMap kmap,
                    const __grid_constant__ CUtensorMap krmap, const __grid_constant__ CUtensorMap vmap, const __grid_constant__ Args a) {
   constexpr int D = S::D, KC = S::kKeyColumns, VC = S::kValueColumns;
-  extern __shared__ uint8_t smem_raw[];
-  Smem<S>& sm = *reinterpret_cast<Smem<S>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  // There is no room to round the address up; dynamic shared memory begins on such a border where there is no other.
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  Smem<S>& sm = *reinterpret_cast<Smem<S>*>(smem_raw);
+  if (smem_u32(smem_raw) % 1024 != 0) {
+    cosa::report_status(a.status, cosa::kStatusDeviceTimeout);
+    return;
+  }
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   volatile int* abort_flag = &sm.abort_flag;
   cosa_kv::wait_for_stream();
@@ -155,19 +157,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&sm.q_full, 1);
     for (int s = 0; s < S::kKeySlots; ++s) {
       mbar_init(&sm.k_full[s], 1);
-      mbar_init(&sm.k_empty[s], 2);        // both tiles
+      mbar_init(&sm.k_empty[s], 1);
     }
     for (int s = 0; s < S::kValueSlots; ++s) {
       mbar_init(&sm.v_full[s], 1);
-      mbar_init(&sm.v_empty[s], 2);
+      mbar_init(&sm.v_empty[s], 1);
     }
     for (int s = 0; s < 4; ++s) mbar_init(&sm.v_clear[s], 1);
     for (int s = 0; s < 2; ++s) {
       mbar_init(&sm.s_full[s], 1);
-      mbar_init(&sm.p_full[s], 4);
+      mbar_init(&sm.p_full[s], 8);
       mbar_init(&sm.pv_done[s], 1);
     }
-    mbar_init(&sm.cleanup, 2);
+    mbar_init(&sm.cleanup, 1);
     sm.abort_flag = 0;
     sm.odd_values = 0;
     cosa::fence_mbarrier_init();
@@ -195,8 +197,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 0) {
       // =========================== copies ===========================
       const int tok = r.tok0 + q0, key = static_cast<int>(r.from);
-      int64_t column = 0;
-      int values = 0;
+      Ring<S::kKeySlots> kring;
+      Ring<S::kValueSlots> vring, cring;      // copies of values, and what is cleared of them
+      int columns = 0, values = 0;            // slots taken, up to the rings' sizes
       bool ok = !a.stall && nb > 0;
       if (ok && lane == 0) {
         cosa::tma_prefetch_desc(&kmap);
@@ -209,28 +212,31 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // what no row may multiply by 0: keys behind the request's, and what is not finite among those that some row does not see
       auto clear = [&](int j) {
-        const int s = j % S::kValueSlots;
-        if (!warp_wait(&sm.v_full[s], (j / S::kValueSlots) & 1, abort_flag, a.status)) return false;
         const int64_t k0 = static_cast<int64_t>(j) * kBlock;
-        const int first = static_cast<int>(max(lim0 + 1 - k0, static_cast<int64_t>(0)));
+        const int first = j < diagonal ? kBlock : static_cast<int>(max(lim0 + 1 - k0, static_cast<int64_t>(0)));
         bool found = false;
-        for (int e = first * VC * 8 + lane; e < kBlock * VC * 8; e += 32) {
-          const int row = e / (VC * 8), c = e % (VC * 8);
-          uint4* at = reinterpret_cast<uint4*>(&sm.v[s][c / 8][row * 128 + (c & 7) * 16]);
-          uint4 x = *at;
-          if (k0 + row >= r.keys) {
-            *at = make_uint4(0, 0, 0, 0);
-          } else if (odd(x.x) || odd(x.y) || odd(x.z) || odd(x.w)) {
-            found = true;
-            uint32_t* w = reinterpret_cast<uint32_t*>(&x);
+        for (int h = 0; h < 2; ++h, cring.next()) {
+          if (!warp_wait(&sm.v_full[cring.at], cring.phase, abort_flag, a.status)) return false;
+          for (int e = max(first - h * kHalf, 0) * VC * 8 + lane; e < kHalf * VC * 8; e += 32) {
+            const int row = e / (VC * 8), c = e % (VC * 8);
+            uint4* at = reinterpret_cast<uint4*>(&sm.v[cring.at][c / 8][row * 128 + (c & 7) * 16]);
+            uint4 x = *at;
+            if (k0 + h * kHalf + row >= r.keys) {
+              *at = make_uint4(0, 0, 0, 0);
+            } else if (odd(x.x) || odd(x.y) || odd(x.z) || odd(x.w)) {
+              found = true;
+              uint32_t* w = reinterpret_cast<uint32_t*>(&x);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              if ((w[i] & 0x7F80u) == 0x7F80u) w[i] &= 0xFFFF0000u;
-              if ((w[i] & 0x7F800000u) == 0x7F800000u) w[i] &= 0xFFFFu;
+              for (int i = 0; i < 4; ++i) {
+                if ((w[i] & 0x7F80u) == 0x7F80u) w[i] &= 0xFFFF0000u;
+                if ((w[i] & 0x7F800000u) == 0x7F800000u) w[i] &= 0xFFFFu;
+              }
+              *at = x;
             }
-            *at = x;
           }
+          __syncwarp();
         }
+        if (j < diagonal) return true;
         cosa::fence_proxy_async_smem();
         found = __any_sync(kAll, found);
         if (lane == 0) {
@@ -241,185 +247,216 @@ __global__ void __launch_bounds__(kThreads, 1)
         return true;
       };
       for (int j = 0; j < nb && ok; ++j) {
-        for (int c = 0; c < KC && ok; ++c) {
-          const int s = static_cast<int>(column % S::kKeySlots);
-          if (column >= S::kKeySlots) ok = warp_wait(&sm.k_empty[s], (column / S::kKeySlots - 1) & 1, abort_flag, a.status);
+        for (int c = 0; c < KC && ok; ++c, kring.next()) {
+          if (columns == S::kKeySlots) ok = warp_wait(&sm.k_empty[kring.at], kring.phase ^ 1, abort_flag, a.status);
+          else ++columns;
           if (!ok) break;
           if (lane == 0) {
-            mbar_arrive_expect_tx(&sm.k_full[s], kColumn);
-            if (c < VC) cosa::tma_load_4d(sm.k[s], &kmap, &sm.k_full[s], 0, key + j * kBlock, c, head);
-            else cosa::tma_load_4d(sm.k[s], &krmap, &sm.k_full[s], 0, key + j * kBlock, 0, 0);
+            mbar_arrive_expect_tx(&sm.k_full[kring.at], kColumn);
+            if (c < VC) cosa::tma_load_4d(sm.k[kring.at], &kmap, &sm.k_full[kring.at], 0, key + j * kBlock, c, head);
+            else cosa::tma_load_4d(sm.k[kring.at], &krmap, &sm.k_full[kring.at], 0, key + j * kBlock, 0, 0);
           }
-          ++column;
         }
-        const int s = j % S::kValueSlots;
-        if (ok && j >= S::kValueSlots) ok = warp_wait(&sm.v_empty[s], (j / S::kValueSlots - 1) & 1, abort_flag, a.status);
-        if (!ok) break;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(&sm.v_full[s], VC * kColumn);
-          for (int c = 0; c < VC; ++c) cosa::tma_load_4d(sm.v[s][c], &vmap, &sm.v_full[s], 0, key + j * kBlock, c, head);
+        for (int h = 0; h < 2 && ok; ++h, vring.next()) {
+          if (values == S::kValueSlots) ok = warp_wait(&sm.v_empty[vring.at], vring.phase ^ 1, abort_flag, a.status);
+          else ++values;
+          if (!ok) break;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&sm.v_full[vring.at], VC * kHalf * 128);
+            for (int c = 0; c < VC; ++c)
+              cosa::tma_load_4d(sm.v[vring.at][c], &vmap, &sm.v_full[vring.at], 0, key + j * kBlock + h * kHalf, c, head);
+          }
+          __syncwarp();
+          // a block's first half is awaited, and cleared, before its slot could be wanted by the next block's second half
+          if (h == 0 && j > 0 && ok) ok = clear(j - 1);
         }
-        ++values;
-        __syncwarp();
-        if (j - 1 >= diagonal) ok = clear(j - 1);
       }
-      if (ok && nb - 1 >= diagonal) clear(nb - 1);
-      // every copy lands before the CTA ends
+      if (ok) clear(nb - 1);
+      // every copy lands before the CTA ends: the last use of each slot
       if (lane == 0 && !a.stall && nb > 0) {
         wait_parity_bounded(&sm.q_full, 0, nullptr, nullptr);
-        for (int s = 0; s < S::kKeySlots; ++s) {
-          const int64_t issued = (column - s + S::kKeySlots - 1) / S::kKeySlots;
-          if (issued > 0) wait_parity_bounded(&sm.k_full[s], (issued - 1) & 1, nullptr, nullptr);
+        for (; columns > 0; --columns) {
+          kring.back();
+          wait_parity_bounded(&sm.k_full[kring.at], kring.phase, nullptr, nullptr);
         }
-        for (int s = 0; s < S::kValueSlots; ++s) {
-          const int issued = (values - s + S::kValueSlots - 1) / S::kValueSlots;
-          if (issued > 0) wait_parity_bounded(&sm.v_full[s], (issued - 1) & 1, nullptr, nullptr);
+        for (; values > 0; --values) {
+          vring.back();
+          wait_parity_bounded(&sm.v_full[vring.at], vring.phase, nullptr, nullptr);
         }
       }
       __syncwarp();
-    } else if (warp == 1 || warp == 2) {
-      // =========================== products of one tile ===========================
-      if (lane == 0) {
-        const int i = warp - 1, mine = i ? nb1 : nb0;
-        constexpr uint32_t idesc_s = cosa::idesc_bf16_f32(128, kBlock, false, false), idesc_o = cosa::idesc_bf16_f32(128, D, false, true);
-        const uint64_t qd = smem_desc_sw128(smem_u32(sm.q[i]), 16, 1024), kd = smem_desc_sw128(smem_u32(sm.k), 16, 1024);
-        const uint64_t vd = smem_desc_sw128(smem_u32(sm.v), kColumn, 1024);
-        const uint32_t s_at = tmem + kTmemS + i * 128, o_at = tmem + kTmemO + i * 128;
-        int64_t column = 0;
-        bool ok = nb == 0 || wait_parity_bounded(&sm.q_full, 0, abort_flag, a.status);
-        // S of block j, or, behind the tile's last block, only the slots' release
-        auto scores = [&](int j) {
-#pragma unroll 1
-          for (int c = 0; c < KC; ++c, ++column) {
-            const int s = static_cast<int>(column % S::kKeySlots);
-            if (!wait_parity_bounded(&sm.k_full[s], (column / S::kKeySlots) & 1, abort_flag, a.status)) return false;
-            if (j >= mine) {
-              mbar_arrive(&sm.k_empty[s]);
-              continue;
-            }
-            tc_fence_after();
+    } else if (warp == 1) {
+      // =========================== products ===========================
+      constexpr uint32_t idesc_s = cosa::idesc_bf16_f32(128, kBlock, false, false), idesc_o = cosa::idesc_bf16_f32(128, D, false, true);
+      constexpr uint32_t hi = desc_hi(1024, 2);
+      const uint32_t qd = desc_lo(smem_u32(sm.q), 16), kd = desc_lo(smem_u32(sm.k), 16), vd = desc_lo(smem_u32(sm.v), kHalf * 128);
+      const int last = nb1 > 0 ? 1 : 0;      // the tile that is done with a block last
+      Ring<S::kKeySlots> kring[2];
+      Ring<S::kValueSlots> vring[2];
+      bool ok = nb == 0 || warp_wait(&sm.q_full, 0, abort_flag, a.status);
+      auto scores = [&](int i) {
+        const uint32_t to = tmem + kTmemS + i * 128;
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              cosa::umma_ss(s_at, qd + ((c * kColumn + k * 32) >> 4), kd + ((s * kColumn + k * 32) >> 4), idesc_s, c > 0 || k > 0);
-            umma_commit(&sm.k_empty[s]);
-          }
-          if (j < mine) umma_commit(&sm.s_full[i]);
-          return true;
-        };
-        if (ok && nb > 0) ok = scores(0);
-        for (int j = 0; j < nb && ok; ++j) {
-          const int s = j % S::kValueSlots;
-          if (j < mine) ok = wait_parity_bounded(&sm.p_full[i], j & 1, abort_flag, a.status);
-          ok = ok && wait_parity_bounded(&sm.v_full[s], (j / S::kValueSlots) & 1, abort_flag, a.status);
-          if (ok && j >= diagonal) ok = wait_parity_bounded(&sm.v_clear[j - diagonal], 0, abort_flag, a.status);
-          if (!ok) break;
-          if (j < mine) {
-            tc_fence_after();
+        for (int c = 0; c < KC; ++c) {
+          Ring<S::kKeySlots>& k = kring[i];
+          if (!warp_wait(&sm.k_full[k.at], k.phase, abort_flag, a.status)) return false;
+          tc_fence_after();
+          const uint32_t q0 = qd + (i * KC + c) * (kColumn >> 4), k0 = kd + k.at * (kColumn >> 4);
+          if (elect_one()) {
 #pragma unroll
-            for (int k = 0; k < kBlock / 16; ++k)
-              cosa::umma_ts(o_at, s_at + k * 8, vd + ((s * VC * kColumn + k * 2048) >> 4), idesc_o, j > 0 || k > 0);
-            umma_commit(&sm.v_empty[s]);
-            umma_commit(&sm.pv_done[i]);
-          } else {
-            mbar_arrive(&sm.v_empty[s]);
+            for (int s = 0; s < 4; ++s) mma_ss(to, q0 + 2 * s, hi, k0 + 2 * s, hi, idesc_s, c > 0 || s > 0);
+            if (i == last) umma_commit(&sm.k_empty[k.at]);
+            if (c == KC - 1) umma_commit(&sm.s_full[i]);
           }
-          if (j + 1 < nb) ok = scores(j + 1);
+          __syncwarp();
+          k.next();
         }
+        return true;
+      };
+      if (ok && nb0 > 0) ok = scores(0);
+      if (ok && nb1 > 0) ok = scores(1);
+      for (int j = 0; j < nb && ok; ++j) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int mine = i ? nb1 : nb0;
+          if (j >= mine || !ok) continue;
+          ok = warp_wait(&sm.p_full[i], j & 1, abort_flag, a.status);
+          if (ok && j >= diagonal) ok = warp_wait(&sm.v_clear[j - diagonal], 0, abort_flag, a.status);
+          const uint32_t p = tmem + kTmemS + i * 128, to = tmem + kTmemO + i * 128;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            Ring<S::kValueSlots>& v = vring[i];
+            ok = ok && warp_wait(&sm.v_full[v.at], v.phase, abort_flag, a.status);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t v0 = vd + v.at * (VC * kHalf * 128 >> 4);
+            if (elect_one()) {
+#pragma unroll
+              for (int s = 0; s < 4; ++s) mma_ts(to, p + h * 64 + s * 8, v0 + s * (2048 >> 4), hi, idesc_o, j > 0 || h > 0 || s > 0);
+              if (i == last) umma_commit(&sm.v_empty[v.at]);
+              if (h == 1) umma_commit(&sm.pv_done[i]);
+            }
+            __syncwarp();
+            v.next();
+          }
+          if (ok && j + 1 < mine) ok = scores(i);
+        }
+      }
+      if (elect_one()) {
         umma_commit(&sm.cleanup);
         wait_parity_bounded(&sm.cleanup, 0, nullptr, nullptr);
       }
       __syncwarp();
     } else if (warp >= 4) {
       // =========================== softmax ===========================
-      const int i = warp / 4 - 1, mine = i ? nb1 : nb0;
+      const int i = (warp - 4) / 8, half = (warp - 4) / 4 % 2, mine = i ? nb1 : nb0;
       const int t = (warp % 4) * 32 + lane, pos = q0 + i * 128 + t;
       const uint32_t lanes = static_cast<uint32_t>((warp % 4) * 32) << 16;
-      const uint32_t s_at = tmem + lanes + kTmemS + i * 128, o_at = tmem + lanes + kTmemO + i * 128;
+      const uint32_t s_at = tmem + lanes + kTmemS + i * 128 + half * kHalf, o_at = tmem + lanes + kTmemO + i * 128 + half * (D / 2);
       const int64_t lim = r.keys - r.n + pos;      // last key that the row sees
       const float scale = a.scale_log2;
-      float ref = -INFINITY, l = 0.f;
+      const int bar = 1 + i;
+      float ref = kNone, l = 0.f;                  // the row's reference; the sum of this half
       bool ok = true;
       for (int j = 0; j < mine; ++j) {
-        if (!warp_wait(&sm.s_full[i], j & 1, abort_flag, a.status)) { ok = false; break; }
-        tc_fence_after();
-        uint32_t x0[64], x1[64];
-        float top, top1;
-        cosa::tmem_ld64_max(s_at, x0, top);
-        cosa::tmem_ld64_max(s_at + 64, x1, top1);
-        cosa::tmem_wait_ld();
-        cosa::reg_after_wait(top);
-        cosa::reg_after_wait(top1);
-        top = fmaxf(top, top1);
-        const int64_t left = lim - static_cast<int64_t>(j) * kBlock;
-        if (left < kBlock - 1) {       // keys that the row does not see: the maximum again without them
-          const int last = static_cast<int>(max(left, static_cast<int64_t>(-1)));
-          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        bool fail = !warp_wait(&sm.s_full[i], j & 1, abort_flag, a.status);
+        const int64_t left = lim - static_cast<int64_t>(j) * kBlock - half * kHalf;
+        const int last = left >= kHalf - 1 ? kHalf : static_cast<int>(max(left, static_cast<int64_t>(-1)));      // last key seen of this half
+        uint32_t w[32];
+        float sum, top;
+        // exp2(S * scale - ref) as bf16 pairs; whether one is high
+        auto weights = [&](bool for_maximum) {
+          uint32_t high = 0;
+          float s4[4] = {};
+          top = -INFINITY;
 #pragma unroll
-          for (int e = 0; e < 64; ++e) {
-            if (e > last) x0[e] = 0xFF800000u;
-            if (e + 64 > last) x1[e] = 0xFF800000u;
-            m4[e & 3] = fmaxf(m4[e & 3], fmaxf(__uint_as_float(x0[e]), __uint_as_float(x1[e])));
-          }
-          top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-        }
-        top = top == -INFINITY ? top : top * scale;
-        float alpha = 1.f;
-        bool moved = false;
-        if (ref == -INFINITY) {
-          ref = top;
-        } else if (top > ref + kRescaleLog2) {
-          alpha = cosa::ex2_approx(ref - top);
-          ref = top;
-          l *= alpha;
-          moved = true;
-        }
-        const float base = ref == -INFINITY ? 0.f : ref;
-        float sum[4] = {};
-        auto weights = [&](const uint32_t(&x)[64], uint32_t to) {
-          uint32_t w[32];
-#pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            float a0, a1;
-            cosa::fma2_bc(a0, a1, __uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]), scale, -base);
-            const float p0 = cosa::ex2_approx(a0), p1 = cosa::ex2_approx(a1);
-            cosa::add2_acc(sum[(e & 1) * 2], sum[(e & 1) * 2 + 1], p0, p1);
-            w[e] = cosa::pack_bf16x2(p0, p1);
-          }
-          cosa::tmem_st32(to, w);
-        };
-        weights(x0, s_at);
-        weights(x1, s_at + 32);
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        cosa::tmem_wait_st();
-        if (__any_sync(kAll, moved) && j > 0) {
-          if (!warp_wait(&sm.pv_done[i], (j - 1) & 1, abort_flag, a.status)) { ok = false; break; }
-          tc_fence_after();
-#pragma unroll 1
-          for (int c = 0; c < D; c += 16) {
-            uint32_t o[16];
-            cosa::tmem_ld16(o_at + c, o);
+          for (int c = 0; c < 2; ++c) {
+            uint32_t x[32];
+            cosa::tmem_ld32(s_at + c * 32, x);
             cosa::tmem_wait_ld();
+            if (last < kHalf) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-            cosa::tmem_st16(o_at + c, o);
+              for (int e = 0; e < 32; ++e)
+                if (c * 32 + e > last) x[e] = 0xFF800000u;
+            }
+            if (for_maximum) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) top = fmaxf(top, __uint_as_float(x[e]));
+              continue;
+            }
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              float x0, x1;
+              cosa::fma2_bc(x0, x1, __uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]), scale, -ref);
+              const float p0 = cosa::ex2_approx(x0), p1 = cosa::ex2_approx(x1);
+              cosa::add2_acc(s4[(e & 1) * 2], s4[(e & 1) * 2 + 1], p0, p1);
+              w[c * 16 + e] = cosa::pack_bf16x2(p0, p1);
+              high = __vmaxu2(high, w[c * 16 + e]);
+            }
           }
-          cosa::tmem_wait_st();
+          sum = (s4[0] + s4[1]) + (s4[2] + s4[3]);
+          __syncwarp();
+          return (high & 0xFFFFu) > kHigh || high >> 16 > kHigh;
+        };
+        bool high = false;
+        if (!fail) {
+          tc_fence_after();
+          high = weights(false);
         }
+        if (cosa::named_bar_red_or(bar, 256, high || fail)) {
+          if (cosa::named_bar_red_or(bar, 256, fail)) { ok = false; break; }
+          // some weight is far above its row's reference (or NaN): the rows' maxima over the block, and the weights again
+          weights(true);
+          sm.part[i][half][t] = top;
+          cosa::named_bar_sync(bar, 256);
+          top = fmaxf(top, sm.part[i][half ^ 1][t]);
+          const float now = top == -INFINITY ? ref : fmaxf(ref, top * scale), alpha = now == ref ? 1.f : cosa::ex2_approx(ref - now);
+          ref = now;
+          l *= alpha;
+          weights(false);
+          if (j > 0) {
+            fail = !warp_wait(&sm.pv_done[i], (j - 1) & 1, abort_flag, a.status);
+            if (!fail) {
+              tc_fence_after();
+#pragma unroll 1
+              for (int c = 0; c < D / 2; c += 16) {
+                uint32_t o[16];
+                cosa::tmem_ld16(o_at + c, o);
+                cosa::tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                cosa::tmem_st16(o_at + c, o);
+              }
+            }
+          }
+          cosa::named_bar_sync(bar, 256);      // the maxima have been read
+        }
+        if (fail) continue;      // the abort flag is set: the next wait ends too, and its vote stops the tile
+        l += sum;
+        cosa::tmem_st32(s_at, w);
+        cosa::tmem_wait_st();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.p_full[i]);
       }
-      if (ok && mine > 0) ok = warp_wait(&sm.pv_done[i], (mine - 1) & 1, abort_flag, a.status);
+      if (ok) {
+        bool fail = false;
+        if (mine > 0) fail = !warp_wait(&sm.pv_done[i], (mine - 1) & 1, abort_flag, a.status);
+        sm.part[i][half][t] = l;
+        ok = !cosa::named_bar_red_or(bar, 256, fail);
+      }
       if (ok) {
         tc_fence_after();
+        l += sm.part[i][half ^ 1][t];
         const float inv = l == 0.f ? 0.f : 1.f / l;
         const int64_t row = static_cast<int64_t>(r.tok0 + pos) * a.num_heads + head;
         const bool live = pos < r.n;
-        if (live && a.lse) a.lse[row] = l == 0.f ? -INFINITY : (ref + log2f(l)) * kLn2;
+        if (live && a.lse && half == 0) a.lse[row] = l == 0.f ? -INFINITY : (ref + log2f(l)) * kLn2;
         const bool odd_values = mine > 0 && *reinterpret_cast<volatile int*>(&sm.odd_values);
-#pragma unroll 1
-        for (int c = 0; c < D; c += 16) {
+#pragma unroll
+        for (int c = 0; c < D / 2; c += 16) {
           uint32_t o[16];
+          __syncwarp();
           if (mine > 0) {
             cosa::tmem_ld16(o_at + c, o);
             cosa::tmem_wait_ld();
@@ -434,18 +471,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (odd_values) {
             // what was not finite among the values on the diagonal, for the rows that see it
             for (int64_t s = lim0 + 1; s <= lim; ++s) {
-              const uint16_t* v = a.v + (r.from + s) * a.v_stride + head * a.v_head_stride + c;
+              const uint16_t* v = a.v + (r.from + s) * a.v_stride + head * a.v_head_stride + half * (D / 2) + c;
 #pragma unroll
               for (int e = 0; e < 16; ++e)
                 if ((v[e] & 0x7F80) == 0x7F80) f[e] += __uint_as_float(static_cast<uint32_t>(v[e]) << 16);
             }
           }
-          uint32_t w[8];
+          uint32_t b[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) w[e] = cosa::pack_bf16x2(f[2 * e] * inv, f[2 * e + 1] * inv);
-          uint4* to = reinterpret_cast<uint4*>(a.out + row * D + c);
-          to[0] = make_uint4(w[0], w[1], w[2], w[3]);
-          to[1] = make_uint4(w[4], w[5], w[6], w[7]);
+          for (int e = 0; e < 8; ++e) b[e] = cosa::pack_bf16x2(f[2 * e] * inv, f[2 * e + 1] * inv);
+          uint4* to = reinterpret_cast<uint4*>(a.out + row * D + half * (D / 2) + c);
+          to[0] = make_uint4(b[0], b[1], b[2], b[3]);
+          to[1] = make_uint4(b[4], b[5], b[6], b[7]);
         }
       }
     }
@@ -490,14 +527,14 @@ cudaError_t launch_shape(const PrefillLaunch& L, cudaStream_t stream) {
             {L.k, L.total_kv_tokens, D, L.num_heads, L.k_stride, L.k_head_stride},
             {L.k_rope, L.total_kv_tokens, 64, 1, L.k_rope_stride, 64},
             {L.v, L.total_kv_tokens, D, L.num_heads, L.v_stride, L.v_head_stride}};
-  const uint32_t box[4] = {64, 128, 1, 1};
   for (int i = 0; i < 5; ++i) {
+    const uint32_t box[4] = {64, i == 4 ? uint32_t{kHalf} : 128u, 1, 1};
     const uint64_t dims[4] = {64, static_cast<uint64_t>(t[i].tokens), static_cast<uint64_t>(t[i].width / 64), static_cast<uint64_t>(t[i].heads)};
     const uint64_t strides[3] = {static_cast<uint64_t>(t[i].stride) * 2, 128, static_cast<uint64_t>(t[i].head_stride) * 2};
     if (!encode_bf16(&maps[i], t[i].base, dims, strides, box)) return cudaErrorInvalidValue;
   }
-  const size_t smem = sizeof(Smem<S>) + 1024;
-  static_assert(sizeof(Smem<S>) + 1024 <= 227 * 1024, "shared memory");
+  const size_t smem = sizeof(Smem<S>);
+  static_assert(sizeof(Smem<S>) <= 227 * 1024, "shared memory");
   auto* kernel = prefill_kernel<S>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
