@@ -541,27 +541,34 @@ __global__ void __launch_bounds__(S::kThreads, 1)
           fence_proxy_async_smem();
           __syncwarp();
         };
-        ok = warp_wait(&sm.p_full[pbuf.at], pbuf.phase, abort_flag, a.status);
+        // keys and values in one slot have been waited for by the first product already
+        if (unclean || (!S::kLatent && S::DK == 128)) {
+          Ring<S::kSlots> at = ring;
 #pragma unroll
-        for (int m = 0; m < S::kBlocks; ++m) {
-          // (the first product has waited for keys and latent vectors already)
-          if (unclean || (!S::kLatent && S::DK == 128)) ok = ok && warp_wait(&sm.full[ring.at], ring.phase, abort_flag, a.status);
-          if (!ok) break;
-          if (unclean) clean(sm.ring[ring.at]);
-          tc_fence_after();
-          const uint32_t v0 = vd + ring.at * (kPair >> 4), p0 = pd + pbuf.at * (S::kPBytes >> 4);
-          if (elect_one()) {
+          for (int m = 0; m < S::kBlocks; ++m, at.next()) ok = ok && warp_wait(&sm.full[at.at], at.phase, abort_flag, a.status);
+        }
+        ok = ok && warp_wait(&sm.p_full[pbuf.at], pbuf.phase, abort_flag, a.status);
+        if (!ok) break;
+        if (unclean) {
+          Ring<S::kSlots> at = ring;
+#pragma unroll 1
+          for (int m = 0; m < S::kBlocks; ++m, at.next()) clean(sm.ring[at.at]);
+        }
+        tc_fence_after();
+        const bool issue = elect_one();
+        const uint32_t p0 = pd + pbuf.at * (S::kPBytes >> 4);
+#pragma unroll
+        for (int m = 0; m < S::kBlocks; ++m, ring.next()) {
+          const uint32_t v0 = vd + ring.at * (kPair >> 4);
+          if (issue) {
 #pragma unroll
             for (int k = 0; k < kTile / 16; ++k)
               mma_ss(tmem + S::kTmemO + m * N, v0 + k * (2048 >> 4), v_hi, p0 + k * S::kPRow, p_hi, idesc, t > pc.t0 || k > 0);
             umma_commit(&sm.empty[ring.at]);
           }
-          __syncwarp();
-          ring.next();
         }
-        if (!ok) break;
         if (unclean) found = __any_sync(kAll, found);
-        if (elect_one()) {
+        if (issue) {
           if (found) sm.odd_values = 1;
           if (S::kAlias) umma_commit(&sm.rope_empty[0]);
           umma_commit(&sm.pv_done[tile & 1]);

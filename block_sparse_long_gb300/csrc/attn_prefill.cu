@@ -291,55 +291,63 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr uint32_t hi = desc_hi(1024, 2);
       const uint32_t qd = desc_lo(smem_u32(sm.q), 16), kd = desc_lo(smem_u32(sm.k), 16), vd = desc_lo(smem_u32(sm.v), kHalf * 128);
       const int last = nb1 > 0 ? 1 : 0;      // the tile that is done with a block last
-      Ring<S::kKeySlots> kring[2];
-      Ring<S::kValueSlots> vring[2];
+      Ring<S::kKeySlots> kwait, kring[2];      // what has been waited for, and the tiles' places
+      Ring<S::kValueSlots> vwait, vring[2];
       bool ok = nb == 0 || warp_wait(&sm.q_full, 0, abort_flag, a.status);
-      auto scores = [&](int i) {
+      auto wait_keys = [&] {
+#pragma unroll
+        for (int c = 0; c < KC; ++c, kwait.next()) ok = ok && warp_wait(&sm.k_full[kwait.at], kwait.phase, abort_flag, a.status);
+      };
+      auto scores = [&](int i, bool issue) {
         const uint32_t to = tmem + kTmemS + i * 128;
 #pragma unroll
-        for (int c = 0; c < KC; ++c) {
-          Ring<S::kKeySlots>& k = kring[i];
-          if (!warp_wait(&sm.k_full[k.at], k.phase, abort_flag, a.status)) return false;
-          tc_fence_after();
-          const uint32_t q0 = qd + (i * KC + c) * (kColumn >> 4), k0 = kd + k.at * (kColumn >> 4);
-          if (elect_one()) {
+        for (int c = 0; c < KC; ++c, kring[i].next()) {
+          const uint32_t q0 = qd + (i * KC + c) * (kColumn >> 4), k0 = kd + kring[i].at * (kColumn >> 4);
+          if (issue) {
 #pragma unroll
             for (int s = 0; s < 4; ++s) mma_ss(to, q0 + 2 * s, hi, k0 + 2 * s, hi, idesc_s, c > 0 || s > 0);
-            if (i == last) umma_commit(&sm.k_empty[k.at]);
-            if (c == KC - 1) umma_commit(&sm.s_full[i]);
+            if (i == last) umma_commit(&sm.k_empty[kring[i].at]);
           }
-          __syncwarp();
-          k.next();
         }
-        return true;
+        if (issue) umma_commit(&sm.s_full[i]);
       };
-      if (ok && nb0 > 0) ok = scores(0);
-      if (ok && nb1 > 0) ok = scores(1);
+      if (nb > 0) {
+        wait_keys();
+        if (ok) {
+          tc_fence_after();
+          const bool issue = elect_one();
+          if (nb0 > 0) scores(0, issue);
+          if (nb1 > 0) scores(1, issue);
+          __syncwarp();
+        }
+      }
       for (int j = 0; j < nb && ok; ++j) {
+        // all that the block's products read, but the weights: waits between products would leave gaps
+        if (j + 1 < nb) wait_keys();
+#pragma unroll
+        for (int h = 0; h < 2; ++h, vwait.next()) ok = ok && warp_wait(&sm.v_full[vwait.at], vwait.phase, abort_flag, a.status);
+        if (j >= diagonal) ok = ok && warp_wait(&sm.v_clear[j - diagonal], 0, abort_flag, a.status);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int mine = i ? nb1 : nb0;
-          if (j >= mine || !ok) continue;
-          ok = warp_wait(&sm.p_full[i], j & 1, abort_flag, a.status);
-          if (ok && j >= diagonal) ok = warp_wait(&sm.v_clear[j - diagonal], 0, abort_flag, a.status);
+          if (j >= mine) continue;
+          ok = ok && warp_wait(&sm.p_full[i], j & 1, abort_flag, a.status);
+          if (!ok) break;
+          tc_fence_after();
           const uint32_t p = tmem + kTmemS + i * 128, to = tmem + kTmemO + i * 128;
+          const bool issue = elect_one();
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            Ring<S::kValueSlots>& v = vring[i];
-            ok = ok && warp_wait(&sm.v_full[v.at], v.phase, abort_flag, a.status);
-            if (!ok) break;
-            tc_fence_after();
-            const uint32_t v0 = vd + v.at * (VC * kHalf * 128 >> 4);
-            if (elect_one()) {
+          for (int h = 0; h < 2; ++h, vring[i].next()) {
+            const uint32_t v0 = vd + vring[i].at * (VC * kHalf * 128 >> 4);
+            if (issue) {
 #pragma unroll
               for (int s = 0; s < 4; ++s) mma_ts(to, p + h * 64 + s * 8, v0 + s * (2048 >> 4), hi, idesc_o, j > 0 || h > 0 || s > 0);
-              if (i == last) umma_commit(&sm.v_empty[v.at]);
-              if (h == 1) umma_commit(&sm.pv_done[i]);
+              if (i == last) umma_commit(&sm.v_empty[vring[i].at]);
             }
-            __syncwarp();
-            v.next();
           }
-          if (ok && j + 1 < mine) ok = scores(i);
+          if (issue) umma_commit(&sm.pv_done[i]);
+          if (j + 1 < mine) scores(i, issue);
+          __syncwarp();
         }
       }
       if (elect_one()) {
