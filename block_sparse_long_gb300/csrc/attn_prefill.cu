@@ -322,15 +322,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       for (int j = 0; j < nb && ok; ++j) {
-        // all that the block's products read, but the weights: waits between products would leave gaps
-        if (j + 1 < nb) wait_keys();
 #pragma unroll
         for (int h = 0; h < 2; ++h, vwait.next()) ok = ok && warp_wait(&sm.v_full[vwait.at], vwait.phase, abort_flag, a.status);
         if (j >= diagonal) ok = ok && warp_wait(&sm.v_clear[j - diagonal], 0, abort_flag, a.status);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const int mine = i ? nb1 : nb0;
-          if (j >= mine) continue;
+          if (j >= (i ? nb1 : nb0)) continue;
           ok = ok && warp_wait(&sm.p_full[i], j & 1, abort_flag, a.status);
           if (!ok) break;
           tc_fence_after();
@@ -346,7 +343,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           if (issue) umma_commit(&sm.pv_done[i]);
-          if (j + 1 < mine) scores(i, issue);
+          __syncwarp();
+        }
+        if (j + 1 < nb && ok) {
+          wait_keys();
+          if (!ok) break;
+          tc_fence_after();
+          const bool issue = elect_one();
+          if (j + 1 < nb0) scores(0, issue);
+          if (j + 1 < nb1) scores(1, issue);
           __syncwarp();
         }
       }
