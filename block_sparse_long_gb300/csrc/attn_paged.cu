@@ -51,6 +51,7 @@ using cosa::wait_parity_bounded;
 
 constexpr int kTile = 128;                 // slots
 constexpr int kCtas = 152;
+constexpr int kMaxCluster = 8;
 constexpr int kColumn = kTile * 128;       // bytes of a 64-value wide column of a tile
 constexpr int kPair = 2 * kColumn;
 constexpr float kNone = -3e38f;            // reference of a row that has seen nothing
@@ -73,7 +74,7 @@ struct Shape {
   static constexpr bool kAlias = LATENT && DV == 512 && N == 64;
   static constexpr int kPBufs = kAlias ? 0 : (LATENT && DV == 512 && N == 32) || N == 128 ? 1 : 2;
   static constexpr int kRopes = LATENT && DV + N <= 528 ? 2 : 1;      // (1, unused, without latent vectors)
-  static constexpr int kSmall = 2048 + N * 56;
+  static constexpr int kSmall = 2048 + N * (56 + 8 * kMaxCluster);
   static constexpr int kRoom = 227 * 1024 - 1024 - kSmall - kQBytes - kPBufs * kPBytes - (LATENT ? kRopes * kColumn : 1024);
   // Keys and values in slots of their own are waited for by different warps, and a parity wait tells only two phases apart: an even
   // number of slots has either keys or values in a slot, so that each barrier's phases are waited for by one warp, in order.
@@ -86,37 +87,9 @@ struct Shape {
   static constexpr int kPRow = N >= 64 ? 128 : 2 * N;
 };
 
-// Where a CTA begins in the list: units and items of the batch, and those before its first request.  (The call is refused where
-// they could pass 31 bits.)
-struct Start {
-  int32_t total, before, items, items_before, first_req;
-};
-
 // What join_kernel has to put together: `parts` parts of an item, the first in slot `first`, the others in next, next + 2, ...
 struct Join {
   int32_t parts, first, next, tok0, rows, head, row_tile, pad;
-};
-
-template <class S>
-struct alignas(1024) Smem {
-  uint8_t ring[S::kSlots][kPair];
-  uint8_t rope[S::kRopes][S::kLatent ? kColumn : 1024];
-  uint8_t q[S::kQBytes];
-  uint8_t p[S::kPBufs ? S::kPBufs : 1][S::kPBufs ? S::kPBytes : 16];
-  uint64_t full[S::kSlots], empty[S::kSlots];
-  uint64_t rope_full[2], rope_empty[2];
-  uint64_t q_ready, s_full[2], s_empty[2], p_full[2], pv_done[2], groups, cleanup;
-  uint64_t mask[S::N];               // tree mask of a row's token
-  alignas(16) float base[S::N];      // a row's reference (log2 units), negated; read four at a time
-  float alpha[S::N];                 // a reference's last change
-  float part[4][S::N];               // maxima and sums of the four warps
-  int32_t row[S::N];                 // output row, or -1
-  int32_t node[S::N];                // token of the request
-  int64_t q_at[S::N], r_at[S::N];    // its values in q and q_rope
-  Start start;
-  int32_t odd_values;                // something among the new tokens' values is not finite
-  uint32_t tmem_base;
-  int32_t abort_flag;
 };
 
 struct Args {
@@ -130,6 +103,8 @@ struct Args {
   int64_t q_stride, q_rope_stride;
   int num_reqs, num_q_heads, num_kv_heads, group, page_shift, total_tokens, max_seqlen, num_pages, max_pages_per_req;
   int join_items;      // entries of `joins` if they are by item, 0 if by CTA
+  int whole;           // items are not cut: a unit is an item
+  int cluster;         // CTAs that share an item by its tiles and join it themselves (whole), or 1
   float scale_log2;
   int stall;
 };
@@ -155,7 +130,7 @@ __device__ __forceinline__ Request request_of(const Args& a, int b) {
   return r;
 }
 
-__device__ __forceinline__ int units_of(const Args& a, const Request& r) { return a.num_kv_heads * r.row_tiles * (r.tiles + 1); }
+__device__ __forceinline__ int units_of(const Args& a, const Request& r) { return a.num_kv_heads * r.row_tiles * (a.whole ? 1 : r.tiles + 1); }
 
 // First unit of a CTA.  With fewer units than CTAs the first ones have one each: every CTA up to the last with any has some.
 __device__ __forceinline__ int share(int total, int cta) {
@@ -172,19 +147,13 @@ struct Piece {
   int item_end;      // behind its last unit
 };
 
-// The pieces of a CTA in order; every role walks them by itself.
+// The pieces of a CTA (of a cluster) in order; every role walks them by itself.
 template <int N>
 struct Pieces {
-  int pos, first, end, before, units, items, b, cta;
+  int pos, first, end, before, units, items, b, cta;      // units and items before and of request b
   Request r;
 
-  __device__ Pieces(const Args& a, int cta_, const Start& st)
-      : before(st.before), units(0), items(st.items_before), b(st.first_req - 1), cta(cta_) {
-    first = pos = share(st.total, cta);
-    end = share(st.total, cta + 1);
-    r.row_tiles = 0;
-  }
-  __device__ bool next(const Args& a, Piece& p) {
+  __device__ __forceinline__ bool next(const Args& a, Piece& p) {
     if (pos >= end) return false;
     while (pos >= before + units) {
       before += units;
@@ -192,14 +161,19 @@ struct Pieces {
       r = request_of<N>(a, ++b);
       units = units_of(a, r);
     }
-    const uint32_t per = r.tiles + 1, item = static_cast<uint32_t>(pos - before) / per;
+    const uint32_t per = a.whole ? 1 : r.tiles + 1, item = a.whole ? pos - before : static_cast<uint32_t>(pos - before) / per;
     const int u = static_cast<int>(pos - before - item * per), take = min(static_cast<int>(per) - u, end - pos);
     p.r = r;
     p.b = b;
     p.head = r.row_tiles == 1 ? item : item / static_cast<uint32_t>(r.row_tiles);
     p.row_tile = static_cast<int>(item) - p.head * r.row_tiles;
-    p.t0 = max(u - 1, 0);
-    p.t1 = u + take - 1;
+    p.t0 = a.whole ? 0 : max(u - 1, 0);
+    p.t1 = a.whole ? r.tiles : u + take - 1;
+    if (a.cluster > 1) {
+      const int rank = blockIdx.x % a.cluster;
+      p.t1 = r.tiles * (rank + 1) / a.cluster;
+      p.t0 = r.tiles * rank / a.cluster;
+    }
     p.slot = take == static_cast<int>(per) ? -1 : 2 * cta + (pos != first);
     p.begins = u == 0;
     p.item = items + static_cast<int>(item);
@@ -209,48 +183,92 @@ struct Pieces {
   }
 };
 
-// Units and items of the batch, and where this CTA begins: by one warp, a request to a lane at a time.
+// The list's units and items, and a CTA's walk of it after its first piece.  (A call is refused where they could pass 31 bits.)
 template <int N>
-__device__ __forceinline__ Start find_start(const Args& a, int cta, bool report) {
+struct Start {
+  int32_t total, items;
+  Pieces<N> rest;
+  Piece first;
+  bool any;
+};
+
+// By one warp, a request to a lane at a time.
+template <int N>
+__device__ __forceinline__ Start<N> find_start(const Args& a, int cta, bool report) {
   const int lane = threadIdx.x % 32;
-  Start st{};
+  Start<N> st;
+  Request r{};
   int units = 0, items = 0;       // of this lane's last request
-  for (int b0 = 0; b0 < a.num_reqs; b0 += 32) {
+  auto look = [&](int b) {
     units = items = 0;
-    if (b0 + lane < a.num_reqs) {
-      const Request r = request_of<N>(a, b0 + lane);
-      if (r.bad && report) cosa::report_status(a.status, cosa::kStatusBadInput);
-      units = units_of(a, r);
-      items = a.num_kv_heads * r.row_tiles;
-    }
+    if (b >= a.num_reqs) return;
+    r = request_of<N>(a, b);
+    units = units_of(a, r);
+    items = a.num_kv_heads * r.row_tiles;
+  };
+  st.total = st.items = 0;
+  for (int b0 = 0; b0 < a.num_reqs; b0 += 32) {
+    look(b0 + lane);
+    if (b0 + lane < a.num_reqs && r.bad && report) cosa::report_status(a.status, cosa::kStatusBadInput);
     st.total += __reduce_add_sync(kAll, units);
     st.items += __reduce_add_sync(kAll, items);
   }
-  const int at = share(st.total, cta);
-  for (int b0 = 0; b0 < a.num_reqs; b0 += 32) {
-    if (a.num_reqs > 32) {
-      units = items = 0;
-      if (b0 + lane < a.num_reqs) {
-        const Request r = request_of<N>(a, b0 + lane);
-        units = units_of(a, r);
-        items = a.num_kv_heads * r.row_tiles;
-      }
-    }
+  Pieces<N>& w = st.rest;
+  w.cta = cta;
+  w.first = w.pos = share(st.total, cta);
+  w.end = share(st.total, cta + 1);
+  if (a.cluster > 1) w.end = min(w.end, w.pos + 1);
+  w.before = w.items = w.units = 0;
+  st.any = w.pos < w.end;
+  if (!st.any) return st;
+  for (int b0 = 0;; b0 += 32) {
+    if (a.num_reqs > 32) look(b0 + lane);
     int upto = units, upto_items = items;
 #pragma unroll
     for (int m = 1; m < 32; m *= 2) {
       const int x = __shfl_up_sync(kAll, upto, m), y = __shfl_up_sync(kAll, upto_items, m);
       if (lane >= m) upto += x, upto_items += y;
     }
-    const unsigned past = __ballot_sync(kAll, st.before + upto > at);
+    const unsigned past = __ballot_sync(kAll, w.before + upto > w.pos);
     const int l = past ? __ffs(past) - 1 : 31;
-    st.before += __shfl_sync(kAll, past ? upto - units : upto, l);
-    st.items_before += __shfl_sync(kAll, past ? upto_items - items : upto_items, l);
-    st.first_req = b0 + l;
-    if (past) break;
+    w.before += __shfl_sync(kAll, past ? upto - units : upto, l);
+    w.items += __shfl_sync(kAll, past ? upto_items - items : upto_items, l);
+    if (!past) continue;
+    w.b = b0 + l;
+    w.units = __shfl_sync(kAll, units, l);
+    w.r.tok0 = __shfl_sync(kAll, r.tok0, l);
+    w.r.n = __shfl_sync(kAll, r.n, l);
+    w.r.len = __shfl_sync(kAll, r.len, l);
+    w.r.tiles = __shfl_sync(kAll, r.tiles, l);
+    w.r.row_tiles = __shfl_sync(kAll, r.row_tiles, l);
+    w.r.bad = false;
+    w.next(a, st.first);
+    return st;
   }
-  return st;
 }
+
+template <class S>
+struct alignas(1024) Smem {
+  uint8_t ring[S::kSlots][kPair];
+  uint8_t rope[S::kRopes][S::kLatent ? kColumn : 1024];
+  uint8_t q[S::kQBytes];
+  uint8_t p[S::kPBufs ? S::kPBufs : 1][S::kPBufs ? S::kPBytes : 16];
+  uint64_t full[S::kSlots], empty[S::kSlots];
+  uint64_t rope_full[2], rope_empty[2];
+  uint64_t q_ready, s_full[2], s_empty[2], p_full[2], pv_done[2], groups, cleanup;
+  uint64_t mask[S::N];               // tree mask of a row's token
+  alignas(16) float base[S::N];      // a row's reference (log2 units), negated; read four at a time
+  float alpha[S::N];                 // a reference's last change
+  float part[4][S::N];               // maxima and sums of the four warps
+  int32_t row[S::N];                 // output row, or -1
+  int32_t node[S::N];                // token of the request
+  int64_t q_at[S::N], r_at[S::N];    // its values in q and q_rope
+  float2 ml[kMaxCluster][S::N];      // references and sums of the cluster's CTAs
+  Start<S::N> start;
+  int32_t odd_values;                // something among the new tokens' values is not finite
+  uint32_t tmem_base;
+  int32_t abort_flag;
+};
 
 // The CTA that has a unit.
 __device__ __forceinline__ int owner(int total, int u) {
@@ -271,6 +289,21 @@ __device__ __forceinline__ void fma2(float& d0, float& d1, float a0, float a1, f
 
 __device__ __forceinline__ void copy16(void* dst, const void* src, bool there) {      // asynchronous; zeros if there is nothing
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+
+// Shared memory of another CTA of the cluster.
+__device__ __forceinline__ uint32_t remote(const void* p, int rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void store_remote(uint32_t to, float x) { asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to), "f"(x) : "memory"); }
+__device__ __forceinline__ void store_remote(const void* to, int rank, float2 x) {
+  asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(remote(to, rank)), "f"(x.x), "f"(x.y) : "memory");
+}
+// Every thread of every CTA of the cluster arrives, whatever became of its waits before.
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
 
 // Where 16-byte piece c of row t of P^T goes (the swizzle of rows of kRow bytes).
@@ -316,7 +349,7 @@ __global__ void __launch_bounds__(S::kThreads, 1)
   cosa_kv::let_next_start();
 
   if (warp == 0) {
-    const Start st = find_start<N>(a, cta, cta == 0);
+    const Start<N> st = find_start<N>(a, cta / a.cluster, cta == 0);
     if (lane == 0) {
       sm.start = st;
       if (cta == 0 && (a.cu_seqlens[0] != 0 || a.cu_seqlens[a.num_reqs] > a.total_tokens)) cosa::report_status(a.status, cosa::kStatusBadInput);
@@ -348,8 +381,10 @@ __global__ void __launch_bounds__(S::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
-  Pieces<N> pieces(a, cta, sm.start);
-  Piece pc;
+  // for (more = ...) below: the pieces of this CTA
+  Pieces<N> pieces = sm.start.rest;
+  Piece pc = sm.start.first;
+  bool more = sm.start.any;
   const int pages_per_tile = kTile >> a.page_shift;
 
   if (warp == 0) {
@@ -362,7 +397,7 @@ __global__ void __launch_bounds__(S::kThreads, 1)
     Ring<S::kRopes> rope;
     int pairs = 0, ropes = 0;      // ring slots taken, up to the rings' sizes
     bool ok = !a.stall;
-    while (ok && pieces.next(a, pc)) {
+    for (; ok && more; more = pieces.next(a, pc)) {
       const int32_t* table = a.page_table + static_cast<size_t>(pc.b) * a.max_pages_per_req;
       auto look_up = [&](int t) {
         const int page = t * pages_per_tile + lane;
@@ -434,7 +469,7 @@ __global__ void __launch_bounds__(S::kThreads, 1)
     Ring<2> sbuf;
     int tile = 0, turn = 0;
     bool ok = true;
-    while (ok && pieces.next(a, pc)) {
+    for (; ok && more; more = pieces.next(a, pc)) {
       if (pc.t0 == pc.t1) continue;
       ok = warp_wait(&sm.q_ready, turn++ & 1, abort_flag, a.status);
       for (int t = pc.t0; t < pc.t1 && ok; ++t) {
@@ -495,7 +530,7 @@ __global__ void __launch_bounds__(S::kThreads, 1)
     Ring<S::kPBufs == 2 ? 2 : 1> pbuf;
     int tile = 0;
     bool ok = true;
-    while (ok && pieces.next(a, pc)) {
+    for (; ok && more; more = pieces.next(a, pc)) {
       const int32_t* table = a.page_table + static_cast<size_t>(pc.b) * a.max_pages_per_req;
       const int ctx = pc.r.len - pc.r.n;
       const bool differ = pc.r.n > 1 || a.tree_mask;      // the rows may differ in what they see
@@ -585,9 +620,9 @@ __global__ void __launch_bounds__(S::kThreads, 1)
     __syncwarp();
   } else if (warp == 3) {
     // =========================== what is to be joined ===========================
-    if (lane == 0) {
+    if (lane == 0 && !a.whole) {
       Join none{}, mine{};
-      while (pieces.next(a, pc)) {
+      for (; more; more = pieces.next(a, pc)) {
         if (!pc.begins) continue;
         Join j{};
         j.parts = 1;
@@ -625,7 +660,39 @@ __global__ void __launch_bounds__(S::kThreads, 1)
       if (lane == 0) mbar_arrive(&sm.groups);
       return warp_wait(&sm.groups, meetings++ & 1, abort_flag, a.status);
     };
-    while (ok && pieces.next(a, pc)) {
+    // What the products have left: `to(o, c, d)` for value d of each 16 rows from c on.
+    auto outputs = [&](bool odd_values, auto to) {
+      constexpr int kSkip = DV == 64 ? 64 : 0;         // lanes of a block that are keys
+      const int32_t* table = a.page_table + static_cast<size_t>(pc.b) * a.max_pages_per_req;
+      const int ctx = pc.r.len - pc.r.n;
+      tc_fence_after();
+#pragma unroll 1
+      for (int m = 0; m < S::kBlocks; ++m) {
+        const int d = m * 128 + at - kSkip;
+#pragma unroll
+        for (int i = 0; i < NC; i += 16) {
+          float o[16] = {};
+          __syncwarp();
+          if (pc.t0 < pc.t1) load_columns<16>(tmem + lanes + S::kTmemO + m * N + c0 + i, o);
+          if (odd_values && d >= 0) {
+            // what was not finite among the new tokens' values, for the rows that see it
+            for (int s = max(ctx, pc.t0 * kTile); s < min(pc.r.len, pc.t1 * kTile); ++s) {
+              const int phys = table[s >> a.page_shift];
+              if (phys < 0 || phys >= a.num_pages) continue;
+              const int64_t place = (static_cast<int64_t>(phys) << a.page_shift) + (s & ((1 << a.page_shift) - 1));
+              const uint16_t v = S::kLatent ? a.k_cache[place * S::DK + d] : a.v_cache[(place * a.num_kv_heads + pc.head) * DV + d];
+              if ((v & 0x7F80) != 0x7F80) continue;
+              const int j = s - ctx;
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                if (a.tree_mask ? sm.mask[c0 + i + e] >> j & 1 : j <= sm.node[c0 + i + e]) o[e] += __uint_as_float(static_cast<uint32_t>(v) << 16);
+            }
+          }
+          if (d >= 0) to(o, c0 + i, d);
+        }
+      }
+    };
+    for (; ok && more; more = pieces.next(a, pc)) {
       const Request& r = pc.r;
       const int rows = r.n * a.group;      // fits 32 bits: total_tokens * Hq does
       const int row0 = pc.row_tile * N;
@@ -711,14 +778,18 @@ __global__ void __launch_bounds__(S::kThreads, 1)
           }
           return top;
         };
-        bool high = false;
-        if (!fail) {
-          tc_fence_after();
-          logits();
-          const uint32_t top = weights();
-          high = (top & 0xFFFFu) > kHigh || top >> 16 > kHigh;
+        tc_fence_after();
+        bool redo = t == pc.t0;      // no row has a reference yet
+        if (!redo) {
+          bool high = false;
+          if (!fail) {
+            logits();
+            const uint32_t top = weights();
+            high = (top & 0xFFFFu) > kHigh || top >> 16 > kHigh;
+          }
+          redo = named_bar_red_or(my_bar, 128, high || fail);
         }
-        if (named_bar_red_or(my_bar, 128, high || fail)) {
+        if (redo) {
           if (named_bar_red_or(my_bar, 128, fail)) { ok = false; break; }
           // some logit is far above its row's reference (or NaN): the rows' maxima over the tile, and the weights again
           logits();
@@ -777,8 +848,6 @@ __global__ void __launch_bounds__(S::kThreads, 1)
       }
       if (!ok) break;
       // ---------------- the piece's end ----------------
-      bool fail = false;
-      if (pc.t0 < pc.t1) fail = !warp_wait(&sm.pv_done[(tile - 1) & 1], ((tile - 1) / 2) & 1, abort_flag, a.status);
       {
         float mine = 0.f;
 #pragma unroll
@@ -790,7 +859,18 @@ __global__ void __launch_bounds__(S::kThreads, 1)
         }
         if (lane < NC) sm.part[quarter][c0 + lane] = mine;
       }
+      bool fail = false;
+      if (pc.t0 < pc.t1) fail = !warp_wait(&sm.pv_done[(tile - 1) & 1], ((tile - 1) / 2) & 1, abort_flag, a.status);
       if (named_bar_red_or(my_bar, 128, fail)) { ok = false; break; }
+      if (a.cluster > 1) {
+        // to every CTA of the cluster; what they hold is waited for below
+        if (at < NC) {
+          const int c = c0 + at;
+          const float sum = (sm.part[0][c] + sm.part[1][c]) + (sm.part[2][c] + sm.part[3][c]), m = -sm.base[c];
+          for (int k = 0; k < a.cluster; ++k) store_remote(&sm.ml[cta % a.cluster][c], k, make_float2(m == kNone ? -INFINITY : m, sum));
+        }
+        break;
+      }
       if (at < NC) {
         const int c = c0 + at;
         const float sum = (sm.part[0][c] + sm.part[1][c]) + (sm.part[2][c] + sm.part[3][c]), m = -sm.base[c];
@@ -805,53 +885,73 @@ __global__ void __launch_bounds__(S::kThreads, 1)
       }
       named_bar_sync(my_bar, 128);
       const bool odd_values = pc.t0 < pc.t1 && *reinterpret_cast<volatile int*>(&sm.odd_values);
-      tc_fence_after();
-      constexpr int kSkip = DV == 64 ? 64 : 0;         // lanes of a block that are keys
-      if (pc.t0 < pc.t1 || pc.slot < 0) {
-#pragma unroll 1
-        for (int m = 0; m < S::kBlocks; ++m) {
-          const int d = m * 128 + at - kSkip;
-#pragma unroll 1
-          for (int i = 0; i < NC; i += 16) {
-            float o[16] = {};
-            __syncwarp();
-            if (pc.t0 < pc.t1) load_columns<16>(tmem + lanes + S::kTmemO + m * N + c0 + i, o);
-            if (odd_values && d >= 0) {
-              // what was not finite among the new tokens' values, for the rows that see it
-              for (int s = max(ctx, pc.t0 * kTile); s < min(r.len, pc.t1 * kTile); ++s) {
-                const int phys = table[s >> a.page_shift];
-                if (phys < 0 || phys >= a.num_pages) continue;
-                const int64_t place = (static_cast<int64_t>(phys) << a.page_shift) + (s & ((1 << a.page_shift) - 1));
-                const uint16_t v = S::kLatent ? a.k_cache[place * S::DK + d] : a.v_cache[(place * a.num_kv_heads + pc.head) * DV + d];
-                if ((v & 0x7F80) != 0x7F80) continue;
-                const int j = s - ctx;
+      if (pc.t0 < pc.t1 || pc.slot < 0)
+        outputs(odd_values, [&](const float(&o)[16], int c, int d) {
+          if (pc.slot >= 0) {
+            float* to = a.part_o + (static_cast<int64_t>(pc.slot) * N + c) * DV + d;
 #pragma unroll
-                for (int e = 0; e < 16; ++e)
-                  if (a.tree_mask ? sm.mask[c0 + i + e] >> j & 1 : j <= sm.node[c0 + i + e]) o[e] += __uint_as_float(static_cast<uint32_t>(v) << 16);
-              }
-            }
-            if (d < 0) continue;
-            if (pc.slot >= 0) {
-              float* to = a.part_o + (static_cast<int64_t>(pc.slot) * N + c0 + i) * DV + d;
+            for (int e = 0; e < 16; ++e) to[e * DV] = o[e];
+          } else {
 #pragma unroll
-              for (int e = 0; e < 16; ++e) to[e * DV] = o[e];
-            } else {
-#pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                const int row = sm.row[c0 + i + e];
-                if (row >= 0)
-                  a.out[static_cast<int64_t>(row) * DV + d] = static_cast<uint16_t>(cosa::pack_bf16x2(o[e] * sm.alpha[c0 + i + e], 0.f));
-              }
+            for (int e = 0; e < 16; ++e) {
+              const int row = sm.row[c + e];
+              if (row >= 0) a.out[static_cast<int64_t>(row) * DV + d] = static_cast<uint16_t>(cosa::pack_bf16x2(o[e] * sm.alpha[c + e], 0.f));
             }
           }
-        }
-      }
+        });
       tc_fence_before();
       if (odd_values) {        // the other threads have read it
         if (!meet()) break;
         if (tid == 0) sm.odd_values = 0;
       }
     }
+    if (a.cluster > 1) {
+      // The cluster joins its item: each CTA has a share of the values, to which the others send theirs, weighted.  Every thread
+      // takes both barriers; behind the first the references are there and the rings are free to receive.
+      const bool mine = sm.start.any && ok;
+      const int rank = cta % a.cluster, width = DV / a.cluster;
+      cluster_barrier();
+      float* parts = reinterpret_cast<float*>(sm.ring);      // [cluster][N][width]
+      if (mine) {
+        if (tid < N) {
+          float m = -INFINITY, sum = 0.f;
+          for (int k = 0; k < a.cluster; ++k) m = fmaxf(m, sm.ml[k][tid].x);
+          for (int k = 0; k < a.cluster; ++k) {
+            const float2 x = sm.ml[k][tid];
+            sum += x.x == -INFINITY && x.y == 0.f ? 0.f : x.y * (x.x == -INFINITY ? 1.f : exp2f(x.x - m));
+          }
+          const float own = sm.ml[rank][tid].x;
+          sm.alpha[tid] = sum == 0.f || own == -INFINITY ? (sum != sum ? sum : 0.f) : exp2f(own - m) / sum;
+          if (a.lse && rank == 0 && sm.row[tid] >= 0) a.lse[sm.row[tid]] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
+        }
+        if (meet()) {
+          const bool odd_values = pc.t0 < pc.t1 && *reinterpret_cast<volatile int*>(&sm.odd_values);
+          outputs(odd_values, [&](const float(&o)[16], int c, int d) {
+            const uint32_t to = remote(parts + (rank * N + c) * width + d % width, d / width);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) store_remote(to + e * width * 4, o[e] * sm.alpha[c + e]);
+          });
+        }
+      }
+      cluster_barrier();
+      if (mine) {
+        for (int e = tid; e < N * width / 2; e += kSoftmax) {
+          const int c = e / (width / 2), d = e % (width / 2) * 2, row = sm.row[c];
+          if (row < 0) continue;
+          float x = 0.f, y = 0.f;
+          for (int k = 0; k < a.cluster; ++k) {
+            const float2 p = *reinterpret_cast<const float2*>(parts + (k * N + c) * width + d);
+            x += p.x;
+            y += p.y;
+          }
+          *reinterpret_cast<uint32_t*>(a.out + static_cast<int64_t>(row) * DV + rank * width + d) = cosa::pack_bf16x2(x, y);
+        }
+      }
+    }
+  }
+  if (a.cluster > 1 && warp < 4) {
+    cluster_barrier();
+    cluster_barrier();
   }
   tc_fence_before();
   __syncthreads();
@@ -998,8 +1098,25 @@ cudaError_t launch_shape(const PagedLaunch& L, cudaStream_t stream) {
   auto* kernel = paged_kernel<S>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  e = cosa_kv::launch_after(kernel, dim3(kCtas), S::kThreads, smem, stream, 1, kmap, vmap, a);
-  if (e != cudaSuccess) return e;
+  a.cluster = 1;
+  // How the items are shared, by the tiles that a CTA then has at most (lengths are known to the device only: max_seqlen's): all tiles
+  // in one list, cut anywhere, and a second kernel to join (about kJoin tiles' time); whole items to a CTA; or an item to a cluster.
+  constexpr double kJoin = S::kLatent ? 2.5 : 5;
+  const double tiles = (L.max_seqlen + kTile - 1) / kTile;
+  double best = items * (tiles + 1) / kCtas + kJoin;
+  if (std::ceil(static_cast<double>(items) / kCtas) * (tiles + 1) <= best) {
+    best = std::ceil(static_cast<double>(items) / kCtas) * (tiles + 1);
+    a.whole = 1;
+  }
+  for (int c = 2; c <= kMaxCluster; c *= 2)
+    if (items * c <= kCtas && std::ceil(tiles / c) + 1 < best) {
+      best = std::ceil(tiles / c) + 1;
+      a.whole = 1;
+      a.cluster = c;
+    }
+  const unsigned ctas = static_cast<unsigned>(a.cluster > 1 ? items * a.cluster : kCtas);
+  e = cosa_kv::launch_after(kernel, dim3(ctas), S::kThreads, smem, stream, a.cluster, kmap, vmap, a);
+  if (e != cudaSuccess || a.whole) return e;
   const unsigned segs = S::DV < 128 ? 1 : S::DV / 128, x = static_cast<unsigned>(a.join_items ? a.join_items : kCtas);
   if (a.join_items && a.join_items <= 16)
     return cosa_kv::launch_after(join_kernel<S::N, S::DV, true>, dim3(x, S::N, segs), kJoinThreads, 0, stream, 1, a);
