@@ -534,29 +534,28 @@ __global__ void __launch_bounds__(S::kThreads, 1)
       const int32_t* table = a.page_table + static_cast<size_t>(pc.b) * a.max_pages_per_req;
       const int ctx = pc.r.len - pc.r.n;
       const bool differ = pc.r.n > 1 || a.tree_mask;      // the rows may differ in what they see
+      bool begun = false;
       for (int t = pc.t0; t < pc.t1 && ok; ++t, ++tile) {
-        // bit i: slot 4 * lane + i is empty (its values must be 0: 0 times what is not finite is not)
-        unsigned empty = 0;
-        int looked = -2, phys = -1;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int slot = t * kTile + 4 * lane + i;
-          if (slot < pc.r.len && slot >> a.page_shift != looked) {
-            looked = slot >> a.page_shift;
-            phys = __ldg(table + looked);
-          }
-          if (slot >= pc.r.len || phys < 0 || phys >= a.num_pages) empty |= 1u << i;
+        // The product runs over the groups of 16 slots that have any (pages are whole groups); in the last of them the values
+        // behind the sequence must be 0, since 0 times what is not finite is not.
+        const int group0 = t * kTile + 16 * lane;
+        bool has = lane < 8 && group0 < pc.r.len;
+        if (has) {
+          const int phys = __ldg(table + (group0 >> a.page_shift));
+          has = phys >= 0 && phys < a.num_pages;
         }
+        unsigned groups = __ballot_sync(kAll, has);
+        int zero0 = min(pc.r.len - t * kTile, kTile), zero1 = (zero0 + 15) & ~15;      // rows to clear
+        if (!(groups >> (zero1 / 16 - 1) & 1)) zero0 = zero1;
+        if (groups == 0 && !begun) groups = 1, zero0 = 0, zero1 = 16;      // the output starts from something
         const int tail0 = differ ? max(ctx - t * kTile, 0) : kTile, tail1 = min(pc.r.len - t * kTile, kTile);
-        const bool unclean = __any_sync(kAll, empty) || tail0 < tail1;
+        const bool unclean = zero0 < zero1 || tail0 < tail1;
         if (S::kPairs > 1 && !S::kLatent) ring.next();      // the keys' slot
         bool found = false;
-        // The values of a slot of the ring, as zeros where there are none or they are not finite.
+        // The values of a slot of the ring, as zeros where there are none or they are not finite (in the new tokens').
         auto clean = [&](uint8_t* values) {
-          for (int i = 0; i < 4; ++i)
-            if (empty >> i & 1)
-              for (int c = kFirst; c < 2; ++c)
-                for (int e = 0; e < 8; ++e) *reinterpret_cast<uint4*>(values + c * kColumn + (4 * lane + i) * 128 + e * 16) = make_uint4(0, 0, 0, 0);
+          for (int e = zero0 * 16 + lane; e < zero1 * 16; e += 32)
+            if ((e & 15) >= 8 * kFirst) *reinterpret_cast<uint4*>(values + (e & 15) / 8 * kColumn + (e >> 4) * 128 + (e & 7) * 16) = make_uint4(0, 0, 0, 0);
           __syncwarp();
           for (int e = tail0 * 16 + lane; e < tail1 * 16; e += 32) {      // 16-byte pieces of the new tokens' values
             if ((e & 15) < 8 * kFirst) continue;
@@ -598,10 +597,12 @@ __global__ void __launch_bounds__(S::kThreads, 1)
           if (issue) {
 #pragma unroll
             for (int k = 0; k < kTile / 16; ++k)
-              mma_ss(tmem + S::kTmemO + m * N, v0 + k * (2048 >> 4), v_hi, p0 + k * S::kPRow, p_hi, idesc, t > pc.t0 || k > 0);
+              if (groups >> k & 1)
+                mma_ss(tmem + S::kTmemO + m * N, v0 + k * (2048 >> 4), v_hi, p0 + k * S::kPRow, p_hi, idesc, begun || groups & ((1u << k) - 1));
             umma_commit(&sm.empty[ring.at]);
           }
         }
+        begun |= groups != 0;
         if (unclean) found = __any_sync(kAll, found);
         if (issue) {
           if (found) sm.odd_values = 1;
@@ -915,7 +916,9 @@ __global__ void __launch_bounds__(S::kThreads, 1)
       if (mine) {
         if (tid < N) {
           float m = -INFINITY, sum = 0.f;
+#pragma unroll 8
           for (int k = 0; k < a.cluster; ++k) m = fmaxf(m, sm.ml[k][tid].x);
+#pragma unroll 8
           for (int k = 0; k < a.cluster; ++k) {
             const float2 x = sm.ml[k][tid];
             sum += x.x == -INFINITY && x.y == 0.f ? 0.f : x.y * (x.x == -INFINITY ? 1.f : exp2f(x.x - m));
@@ -939,6 +942,7 @@ __global__ void __launch_bounds__(S::kThreads, 1)
           const int c = e / (width / 2), d = e % (width / 2) * 2, row = sm.row[c];
           if (row < 0) continue;
           float x = 0.f, y = 0.f;
+#pragma unroll 8
           for (int k = 0; k < a.cluster; ++k) {
             const float2 p = *reinterpret_cast<const float2*>(parts + (k * N + c) * width + d);
             x += p.x;
