@@ -24,6 +24,7 @@
 //              and P^T to shared memory as bf16 (2^-9 of each term; l sums the unrounded ones).
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -55,7 +56,7 @@ constexpr int kMaxCluster = 8;
 constexpr int kColumn = kTile * 128;       // bytes of a 64-value wide column of a tile
 constexpr int kPair = 2 * kColumn;
 constexpr float kNone = -3e38f;            // reference of a row that has seen nothing
-constexpr uint32_t kHigh = 0x4380;         // 2^8 in bf16: a weight above it moves its row's reference
+constexpr float kHigh = 8.0f;              // log2 of the weight from which on a row's reference moves
 constexpr float kLn2 = 0.69314718055994531f;
 
 // DK, DV: values of a key and a value.  kLatent: the value is the key's first DV values.  N: query rows of a row tile.
@@ -738,69 +739,62 @@ __global__ void __launch_bounds__(S::kThreads, 1)
           there = phys >= 0 && phys < a.num_pages;
         }
         bool fail = !warp_wait(&sm.s_full[sb], (tile / 2) & 1, abort_flag, a.status);
-        // P^T's buffer is free once the product before (or before that) has read it
-        constexpr int kBack = S::kPBufs == 2 ? 2 : 1;
-        if (!fail && tile >= kBack)
-          fail = !warp_wait(&sm.pv_done[(tile - kBack) & 1], ((tile - kBack) / 2) & 1, abort_flag, a.status);
-        uint8_t* p = (S::kAlias ? sm.rope[0] : sm.p[S::kPBufs == 2 ? tile & 1 : 0]) + c0 / 64 * kColumn;
-        float x[NC];
-        // the tile's logits, -infinity where the row does not see the slot
-        auto logits = [&] {
-          load_columns<NC>(tmem + lanes + S::kTmemS + sb * N + c0, x);
+        // Sixteen columns at a time: with 32 the second sixteen are read from TMEM again where they are needed again, since two more
+        // sets of registers beside the sums would be spilled (5500 cycles a tile of 128 rows instead of 2000).
+        constexpr bool kKeep = NC == 16;
+        float x[16];
+        // logits of columns i on, -infinity where the row does not see the slot
+        auto logits = [&](int i) {
+          load_columns<16>(tmem + lanes + S::kTmemS + sb * N + c0 + i, x);
           if (!there) {
 #pragma unroll
-            for (int i = 0; i < NC; ++i) x[i] = -INFINITY;
+            for (int e = 0; e < 16; ++e) x[e] = -INFINITY;
           } else if (slot >= ctx) {
             const int j = slot - ctx;
 #pragma unroll
-            for (int i = 0; i < NC; ++i)
-              if (a.tree_mask ? !(sm.mask[c0 + i] >> j & 1) : j > sm.node[c0 + i]) x[i] = -INFINITY;
+            for (int e = 0; e < 16; ++e)
+              if (a.tree_mask ? !(sm.mask[c0 + i + e] >> j & 1) : j > sm.node[c0 + i + e]) x[e] = -INFINITY;
           }
           __syncwarp();
         };
-        // x <- exp2(x * scale - reference), as bf16 to P^T; the largest as bf16 bits, in either half
-        auto weights = [&] {
-          uint32_t top = 0;
-#pragma unroll
-          for (int i = 0; i < NC; i += 8) {
-            uint32_t w[4];
-#pragma unroll
-            for (int e = i; e < i + 8; e += 4) {
-              const float4 b = *reinterpret_cast<const float4*>(&sm.base[c0 + e]);
-              fma2(x[e], x[e + 1], x[e], x[e + 1], scale, b.x, b.y);
-              fma2(x[e + 2], x[e + 3], x[e + 2], x[e + 3], scale, b.z, b.w);
-#pragma unroll
-              for (int k = e; k < e + 4; ++k) x[k] = cosa::ex2_approx(x[k]);
-              w[(e - i) / 2] = cosa::pack_bf16x2(x[e], x[e + 1]);
-              w[(e - i) / 2 + 1] = cosa::pack_bf16x2(x[e + 2], x[e + 3]);
-              top = __vmaxu2(top, __vmaxu2(w[(e - i) / 2], w[(e - i) / 2 + 1]));
-            }
-            *reinterpret_cast<uint4*>(p + p_offset<S::kPRow>(at, (c0 % 64 + i) / 8)) = make_uint4(w[0], w[1], w[2], w[3]);
-          }
-          return top;
-        };
-        tc_fence_after();
         bool redo = t == pc.t0;      // no row has a reference yet
+        if (!fail) {
+          tc_fence_after();
+          if (kKeep) logits(0);
+        }
         if (!redo) {
-          bool high = false;
+          // is some logit far above its row's reference (NaN is not: it stays what it is)
+          float top = -INFINITY;
           if (!fail) {
-            logits();
-            const uint32_t top = weights();
-            high = (top & 0xFFFFu) > kHigh || top >> 16 > kHigh;
+#pragma unroll
+            for (int i = 0; i < NC; i += 16) {
+              if (!kKeep) logits(i);
+#pragma unroll
+              for (int e = 0; e < 16; e += 4) {
+                const float4 b = *reinterpret_cast<const float4*>(&sm.base[c0 + i + e]);
+                float d[4];
+                fma2(d[0], d[1], x[e], x[e + 1], scale, b.x, b.y);
+                fma2(d[2], d[3], x[e + 2], x[e + 3], scale, b.z, b.w);
+                top = fmaxf(top, fmaxf(fmaxf(d[0], d[1]), fmaxf(d[2], d[3])));
+              }
+            }
           }
-          redo = named_bar_red_or(my_bar, 128, high || fail);
+          redo = named_bar_red_or(my_bar, 128, top > kHigh || fail);
         }
         if (redo) {
           if (named_bar_red_or(my_bar, 128, fail)) { ok = false; break; }
-          // some logit is far above its row's reference (or NaN): the rows' maxima over the tile, and the weights again
-          logits();
-          float mine = 0.f;
+          // the rows' maxima over the tile become references
 #pragma unroll
-          for (int i = 0; i < NC; ++i) {
-            const float top = warp_max(x[i]);
-            mine = lane == i ? top : mine;
+          for (int i = 0; i < NC; i += 16) {
+            if (!kKeep) logits(i);
+            float mine = 0.f;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const float top = warp_max(x[e]);
+              mine = lane == e ? top : mine;
+            }
+            if (lane < 16) sm.part[quarter][c0 + i + lane] = mine;
           }
-          if (lane < NC) sm.part[quarter][c0 + lane] = mine;
           named_bar_sync(my_bar, 128);
           if (at < NC) {
             const int c = c0 + at;
@@ -810,10 +804,9 @@ __global__ void __launch_bounds__(S::kThreads, 1)
             sm.alpha[c] = now == was ? 1.f : cosa::ex2_approx(was - now);
           }
           named_bar_sync(my_bar, 128);
-          weights();
-#pragma unroll
-          for (int i = 0; i < NC; ++i) l[i] *= sm.alpha[c0 + i];
           if (t > pc.t0) {
+#pragma unroll
+            for (int i = 0; i < NC; ++i) l[i] *= sm.alpha[c0 + i];
             fail = !warp_wait(&sm.pv_done[(tile - 1) & 1], ((tile - 1) / 2) & 1, abort_flag, a.status);
             if (!fail) {
               tc_fence_after();
@@ -834,7 +827,34 @@ __global__ void __launch_bounds__(S::kThreads, 1)
             }
           }
         }
+        // P^T's buffer is free once the product before (or before that) has read it
+        constexpr int kBack = S::kPBufs == 2 ? 2 : 1;
+        if (!fail && tile >= kBack)
+          fail = !warp_wait(&sm.pv_done[(tile - kBack) & 1], ((tile - kBack) / 2) & 1, abort_flag, a.status);
         if (!fail) {
+          // exp2(x * scale - reference), summed, and as bf16 to P^T
+          uint8_t* p = (S::kAlias ? sm.rope[0] : sm.p[S::kPBufs == 2 ? tile & 1 : 0]) + c0 / 64 * kColumn;
+#pragma unroll
+          for (int i = 0; i < NC; i += 16) {
+            if (!kKeep) logits(i);
+#pragma unroll
+            for (int h = 0; h < 16; h += 8) {
+              uint32_t w[4];
+#pragma unroll
+              for (int e = h; e < h + 8; e += 4) {
+                const float4 b = *reinterpret_cast<const float4*>(&sm.base[c0 + i + e]);
+                fma2(x[e], x[e + 1], x[e], x[e + 1], scale, b.x, b.y);
+                fma2(x[e + 2], x[e + 3], x[e + 2], x[e + 3], scale, b.z, b.w);
+#pragma unroll
+                for (int k = e; k < e + 4; ++k) x[k] = cosa::ex2_approx(x[k]);
+                cosa::add2_acc(l[i + e], l[i + e + 1], x[e], x[e + 1]);
+                cosa::add2_acc(l[i + e + 2], l[i + e + 3], x[e + 2], x[e + 3]);
+                w[(e - h) / 2] = cosa::pack_bf16x2(x[e], x[e + 1]);
+                w[(e - h) / 2 + 1] = cosa::pack_bf16x2(x[e + 2], x[e + 3]);
+              }
+              *reinterpret_cast<uint4*>(p + p_offset<S::kPRow>(at, (c0 % 64 + i + h) / 8)) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
           tc_fence_before();
           fence_proxy_async_smem();
           __syncwarp();
@@ -842,8 +862,6 @@ __global__ void __launch_bounds__(S::kThreads, 1)
             mbar_arrive(&sm.p_full[S::kPBufs == 2 ? tile & 1 : 0]);
             mbar_arrive(&sm.s_empty[sb]);
           }
-#pragma unroll
-          for (int i = 0; i < NC; i += 2) cosa::add2_acc(l[i], l[i + 1], x[i], x[i + 1]);
         }
         // a wait that ran out has set the abort flag: the next wait ends too, and its vote stops the group
       }
@@ -966,12 +984,15 @@ __global__ void __launch_bounds__(S::kThreads, 1)
 }
 
 // Joins the parts of the items that several CTAs had: out = sum 2^(m_i - m) o_i / sum 2^(m_i - m) l_i.  blockIdx.x is an entry of
-// `joins`; a block has eight rows of 128 values, or (kWide, where an item has many parts) one row, its warps a part each.
-constexpr int kJoinThreads = 256;
+// `joins`; a block has eight rows of 128 values, or (kWide, where an item has many parts) one row, which its sixteen warps share.
+constexpr int kJoinThreads = 256, kWideThreads = 512;
 
 template <int N, int DV, bool kWide>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(kWide ? kWideThreads : kJoinThreads) join_kernel(const __grid_constant__ Args a) {
   constexpr int kSeg = DV < 128 ? DV : 128, kVec = kSeg / 32;
+  constexpr int kWarps = kWide ? kWideThreads / 32 : 1;          // that share a row
+  constexpr int kAhead = kWide ? (kCtas + kWarps - 1) / kWarps : 4;      // parts of a warp in flight
+  using Vec = typename std::conditional<kVec == 4, float4, float2>::type;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   cosa_kv::wait_for_stream();
   const Join j = a.joins[blockIdx.x];
@@ -979,47 +1000,52 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
   const int parts = j.parts, seg = blockIdx.z;
   const int c = kWide ? blockIdx.y : blockIdx.y * 8 + warp;      // row of the tile
   const int64_t row = static_cast<int64_t>(j.row_tile) * N + c;
-  const bool live = row < j.rows;
-  if (kWide && !live) return;
+  if (row >= j.rows) return;                                     // (kWide: the whole block)
   auto slot = [&](int i) { return i == 0 ? j.first : j.next + 2 * (i - 1); };
-  __shared__ float weight[kWide ? 1 : 8][kCtas + 8];
-  __shared__ float sums[8][kSeg];
-  float* w = weight[kWide ? 0 : warp];
-  // weights of the parts, by every warp of its own (kWide: all the same ones, by the first)
+  const float* base = a.part_o + static_cast<int64_t>(c) * DV + seg * kSeg + lane * kVec;
+  auto load = [&](int i) { return i < parts ? *reinterpret_cast<const Vec*>(base + static_cast<int64_t>(slot(i)) * N * DV) : Vec{}; };
+  const int first = kWide ? warp : 0;
+  // all loads at once: the first values of the parts, and their references and sums (a part to a lane)
+  Vec v[kAhead];
+#pragma unroll
+  for (int k = 0; k < kAhead; ++k) v[k] = load(first + k * kWarps);
+  constexpr int kLane = (kCtas + 31) / 32;
+  float2 ml[kLane];
   float m = -INFINITY, sum = 0.f;
-  if (live) {
-    for (int i = lane; i < parts; i += 32) m = fmaxf(m, a.part_ml[(static_cast<int64_t>(slot(i)) * N + c) * 2]);
 #pragma unroll
-    for (int k = 1; k < 32; k *= 2) m = fmaxf(m, __shfl_xor_sync(kAll, m, k));
-    for (int i = lane; i < parts; i += 32) {
-      const float* ml = a.part_ml + (static_cast<int64_t>(slot(i)) * N + c) * 2;
-      const float f = ml[0] == -INFINITY ? 0.f : exp2f(ml[0] - m);
-      // a part whose rows saw nothing may have no o; NaN is kept
-      sum += f == 0.f && ml[1] == 0.f ? 0.f : f * ml[1];
-      if (!kWide || warp == 0) w[i] = ml[0] == -INFINITY ? -1.f : f;
-    }
-#pragma unroll
-    for (int k = 1; k < 32; k *= 2) sum += __shfl_xor_sync(kAll, sum, k);
+  for (int k = 0; k < kLane; ++k) {
+    const int i = lane + 32 * k;
+    ml[k] = i < parts ? *reinterpret_cast<const float2*>(a.part_ml + (static_cast<int64_t>(slot(i)) * N + c) * 2) : make_float2(-INFINITY, 0.f);
+    m = fmaxf(m, ml[k].x);
   }
-  __syncthreads();
+#pragma unroll
+  for (int k = 1; k < 32; k *= 2) m = fmaxf(m, __shfl_xor_sync(kAll, m, k));
+#pragma unroll
+  for (int k = 0; k < kLane; ++k) {
+    const bool none = ml[k].x == -INFINITY;                     // a part that saw nothing may have no values
+    sum += none ? ml[k].y : exp2f(ml[k].x - m) * ml[k].y;
+    ml[k].x = none ? -1.f : exp2f(ml[k].x - m);                  // its weight
+  }
+#pragma unroll
+  for (int k = 1; k < 32; k *= 2) sum += __shfl_xor_sync(kAll, sum, k);
   float o[kVec] = {};
-  if (live) {
-    const float* base = a.part_o + static_cast<int64_t>(c) * DV + seg * kSeg + lane * kVec;
-#pragma unroll 8
-    for (int i = kWide ? warp : 0; i < parts; i += kWide ? 8 : 1) {
-      const float f = w[i];
-      if (f < 0.f) continue;
-      const float* p = base + static_cast<int64_t>(slot(i)) * N * DV;
-      if constexpr (kVec == 4) {
-        const float4 x = *reinterpret_cast<const float4*>(p);
-        o[0] = fmaf(f, x.x, o[0]); o[1] = fmaf(f, x.y, o[1]); o[2] = fmaf(f, x.z, o[2]); o[3] = fmaf(f, x.w, o[3]);
-      } else {
-        const float2 x = *reinterpret_cast<const float2*>(p);
-        o[0] = fmaf(f, x.x, o[0]); o[1] = fmaf(f, x.y, o[1]);
-      }
+  auto add = [&](int i, const Vec& x) {
+    float f = 0.f;
+#pragma unroll
+    for (int k = 0; k < kLane; ++k) {
+      const float g = __shfl_sync(kAll, ml[k].x, i % 32);
+      f = i / 32 == k ? g : f;
     }
-  }
+    if (i >= parts || f < 0.f) return;
+    const float* y = reinterpret_cast<const float*>(&x);
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) o[e] = fmaf(f, y[e], o[e]);
+  };
+#pragma unroll
+  for (int k = 0; k < kAhead; ++k) add(first + k * kWarps, v[k]);
+  for (int i = first + kAhead * kWarps; i < parts; i += kWarps) add(i, load(i));
   if constexpr (kWide) {
+    __shared__ float sums[kWarps][kSeg];
 #pragma unroll
     for (int e = 0; e < kVec; ++e) sums[warp][lane * kVec + e] = o[e];
     __syncthreads();
@@ -1028,10 +1054,9 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
     for (int e = 0; e < kVec; ++e) {
       o[e] = 0.f;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) o[e] += sums[k][lane * kVec + e];
+      for (int k = 0; k < kWarps; ++k) o[e] += sums[k][lane * kVec + e];
     }
   }
-  if (!live) return;
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
   const int64_t to = (j.tok0 + row / a.group) * a.num_q_heads + j.head * a.group + row % a.group;
   uint16_t* dst = a.out + to * DV + seg * kSeg + lane * kVec;
@@ -1039,7 +1064,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
     *reinterpret_cast<uint2*>(dst) = make_uint2(cosa::pack_bf16x2(o[0] * inv, o[1] * inv), cosa::pack_bf16x2(o[2] * inv, o[3] * inv));
   else
     *reinterpret_cast<uint32_t*>(dst) = cosa::pack_bf16x2(o[0] * inv, o[1] * inv);
-  if (a.lse && seg == 0 && lane == 0) a.lse[to] = m == -INFINITY && sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
+  if (a.lse && seg == 0 && lane == 0) a.lse[to] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
 }
 
 int rows_of_tile(const PagedLaunch& L) {
@@ -1123,7 +1148,7 @@ cudaError_t launch_shape(const PagedLaunch& L, cudaStream_t stream) {
   if (e != cudaSuccess || a.whole) return e;
   const unsigned segs = S::DV < 128 ? 1 : S::DV / 128, x = static_cast<unsigned>(a.join_items ? a.join_items : kCtas);
   if (a.join_items && a.join_items <= 16)
-    return cosa_kv::launch_after(join_kernel<S::N, S::DV, true>, dim3(x, S::N, segs), kJoinThreads, 0, stream, 1, a);
+    return cosa_kv::launch_after(join_kernel<S::N, S::DV, true>, dim3(x, S::N, segs), kWideThreads, 0, stream, 1, a);
   return cosa_kv::launch_after(join_kernel<S::N, S::DV, false>, dim3(x, S::N / 8, segs), kJoinThreads, 0, stream, 1, a);
 }
 
