@@ -80,7 +80,10 @@ struct Shape {
   // Keys and values in slots of their own are waited for by different warps, and a parity wait tells only two phases apart: an even
   // number of slots has either keys or values in a slot, so that each barrier's phases are waited for by one warp, in order.
   static constexpr int kFit = kRoom / kPair < 6 ? kRoom / kPair : 6;
-  static constexpr int kSlots = kPairs == 2 && !LATENT ? kFit / 2 * 2 : kFit;
+  static constexpr bool kSplit = kPairs == 2 && !LATENT;
+  static constexpr int kSlots = kSplit ? kFit / 2 * 2 : kFit;
+  // A tile's place: one slot (of a pair, for kSplit: an even one for keys and the odd one behind it for values), kLatent: several.
+  static constexpr int kRing = kSplit ? kSlots / 2 : kSlots, kStep = kSplit ? 2 : 1;
   static_assert(kSlots >= kPairs, "a tile fits the ring");
   static constexpr uint32_t kTmemO = 0, kTmemS = kBlocks * N;
   static_assert(kTmemS + 2 * N <= 512, "TMEM columns");
@@ -394,69 +397,95 @@ __global__ void __launch_bounds__(S::kThreads, 1)
       cosa::tma_prefetch_desc(&kmap);
       cosa::tma_prefetch_desc(&vmap);
     }
-    Ring<S::kSlots> ring;
+    Ring<S::kRing> ring, vring;      // (vring: kSplit's values)
     Ring<S::kRopes> rope;
-    int pairs = 0, ropes = 0;      // ring slots taken, up to the rings' sizes
+    int pairs = 0, vpairs = 0, ropes = 0;      // slots taken, up to the rings' sizes
     bool ok = !a.stall;
+    const int page = lane & (pages_per_tile - 1), column = lane / pages_per_tile, to = (page << a.page_shift) * 128;
+    // The pages of a tile, a page and column to a lane.
+    struct Tile {
+      uint32_t bytes;      // of a 64-value column
+      int place, head;     // row of the lane's page in the cache, kv head
+      bool copies;
+    };
+    auto take = [&](Ring<S::kRing>& r, int& taken, int odd) {
+      if (taken == S::kRing) ok = warp_wait(&sm.empty[r.at * S::kStep + odd], r.phase ^ 1, abort_flag, a.status);
+      else ++taken;
+      return r.at * S::kStep + odd;
+    };
+    // A pair of columns from c0 on, of one cache or of both.
+    auto copy = [&](const Tile& x, int s, const CUtensorMap* first, const CUtensorMap* second, int c0, int c1) {
+      if (lane == 0) mbar_arrive_expect_tx(&sm.full[s], 2 * x.bytes);
+      __syncwarp();
+      if (column < 2 && x.copies)
+        cosa::tma_load_4d(&sm.ring[s][column * kColumn + to], column ? second : first, &sm.full[s], 0, x.place, column ? c1 : c0, x.head);
+    };
+    Tile last{};
+    bool waiting = false;      // kSplit: the last tile's values, which come behind the next tile's keys (keys are free sooner)
+    auto values = [&] {
+      const int s = take(vring, vpairs, 1);
+      if (!ok) return;
+      copy(last, s, &vmap, &vmap, 0, 1);
+      vring.next();
+      waiting = false;
+    };
     for (; ok && more; more = pieces.next(a, pc)) {
       const int32_t* table = a.page_table + static_cast<size_t>(pc.b) * a.max_pages_per_req;
       auto look_up = [&](int t) {
-        const int page = t * pages_per_tile + lane;
-        return t < pc.t1 && lane < pages_per_tile && page << a.page_shift < pc.r.len ? __ldg(table + page) : -1;
+        const int p = t * pages_per_tile + lane;
+        return t < pc.t1 && lane < pages_per_tile && p << a.page_shift < pc.r.len ? __ldg(table + p) : -1;
       };
       int phys_next = look_up(pc.t0);
       for (int t = pc.t0; t < pc.t1 && ok; ++t) {
         const int phys = phys_next;
         phys_next = look_up(t + 1);
         const unsigned there = __ballot_sync(kAll, phys >= 0 && phys < a.num_pages);
-        const uint32_t bytes = static_cast<uint32_t>(__popc(there)) << a.page_shift << 7;      // of a 64-value column
-        const int page = lane & (pages_per_tile - 1), column = lane / pages_per_tile;
-        const int place = __shfl_sync(kAll, phys, page) << a.page_shift;
-        const bool copies = there >> page & 1;
-        const int to = (page << a.page_shift) * 128;
+        Tile x;
+        x.bytes = static_cast<uint32_t>(__popc(there)) << a.page_shift << 7;
+        x.place = __shfl_sync(kAll, phys, page) << a.page_shift;
+        x.head = S::kLatent ? 0 : pc.head;
+        x.copies = there >> page & 1;
         auto rotated = [&] {
-          const int s = rope.at;
-          if (ropes == S::kRopes) ok = warp_wait(&sm.rope_empty[s], rope.phase ^ 1, abort_flag, a.status);
+          if (ropes == S::kRopes) ok = warp_wait(&sm.rope_empty[rope.at], rope.phase ^ 1, abort_flag, a.status);
+          else ++ropes;
           if (!ok) return;
-          if (lane == 0) mbar_arrive_expect_tx(&sm.rope_full[s], bytes);
+          if (lane == 0) mbar_arrive_expect_tx(&sm.rope_full[rope.at], x.bytes);
           __syncwarp();
-          if (column == 0 && copies) cosa::tma_load_4d(&sm.rope[s][to], &kmap, &sm.rope_full[s], 0, place, DV / 64, 0);
+          if (column == 0 && x.copies) cosa::tma_load_4d(&sm.rope[rope.at][to], &kmap, &sm.rope_full[rope.at], 0, x.place, DV / 64, 0);
           rope.next();
-          ropes = min(ropes + 1, S::kRopes);
         };
         if constexpr (S::kLatent && !S::kAlias) rotated();
-        if (!ok) break;
-        for (int i = 0; i < S::kPairs; ++i) {
-          const int s = ring.at;
-          if (pairs == S::kSlots) ok = warp_wait(&sm.empty[s], ring.phase ^ 1, abort_flag, a.status);
+        for (int i = 0; i < (S::kSplit ? 1 : S::kPairs) && ok; ++i) {
+          const int s = take(ring, pairs, 0);
           if (!ok) break;
-          if (lane == 0) mbar_arrive_expect_tx(&sm.full[s], 2 * bytes);
-          __syncwarp();
-          if (column < 2 && copies) {
-            uint8_t* dst = &sm.ring[s][column * kColumn + to];
-            if (S::kLatent)
-              cosa::tma_load_4d(dst, &kmap, &sm.full[s], 0, place, 2 * i + column, 0);
-            else if (S::DK == 128)
-              cosa::tma_load_4d(dst, i ? &vmap : &kmap, &sm.full[s], 0, place, column, pc.head);
-            else
-              cosa::tma_load_4d(dst, column ? &vmap : &kmap, &sm.full[s], 0, place, 0, pc.head);
-          }
+          if (S::kLatent) copy(x, s, &kmap, &kmap, 2 * i, 2 * i + 1);
+          else if (S::kSplit) copy(x, s, &kmap, &kmap, 0, 1);
+          else copy(x, s, &kmap, &vmap, 0, 0);
           ring.next();
-          pairs = min(pairs + 1, S::kSlots);
         }
         if constexpr (S::kAlias) {
           if (ok) rotated();
         }
+        if constexpr (S::kSplit) {
+          if (ok && waiting) values();
+          last = x;
+          waiting = true;
+        }
       }
     }
+    if (ok && waiting) values();
     // every copy lands before the CTA ends: the last use of each slot (those before it have landed, or it had not been taken)
     if (lane == 0) {
       for (; pairs > 0; --pairs) {
-        ring.at = ring.at == 0 ? (ring.phase ^= 1, S::kSlots - 1) : ring.at - 1;
-        wait_parity_bounded(&sm.full[ring.at], ring.phase, nullptr, nullptr);
+        ring.back();
+        wait_parity_bounded(&sm.full[ring.at * S::kStep], ring.phase, nullptr, nullptr);
+      }
+      for (; vpairs > 0; --vpairs) {
+        vring.back();
+        wait_parity_bounded(&sm.full[vring.at * S::kStep + 1], vring.phase, nullptr, nullptr);
       }
       for (; ropes > 0; --ropes) {
-        rope.at = rope.at == 0 ? (rope.phase ^= 1, S::kRopes - 1) : rope.at - 1;
+        rope.back();
         wait_parity_bounded(&sm.rope_full[rope.at], rope.phase, nullptr, nullptr);
       }
     }
@@ -465,7 +494,7 @@ __global__ void __launch_bounds__(S::kThreads, 1)
     // =========================== S^T = K Q^T ===========================
     constexpr uint32_t idesc = cosa::idesc_bf16_f32(128, N, false, false), hi = desc_hi(1024, 2);
     const uint32_t qd = desc_lo(smem_u32(sm.q), 16), kd = desc_lo(smem_u32(sm.ring), 16), rd = desc_lo(smem_u32(sm.rope), 16);
-    Ring<S::kSlots> ring;
+    Ring<S::kRing> ring;
     Ring<S::kRopes> rope;
     Ring<2> sbuf;
     int tile = 0, turn = 0;
@@ -495,21 +524,21 @@ __global__ void __launch_bounds__(S::kThreads, 1)
         constexpr int kKeys = S::kLatent ? S::kPairs : 1;      // ring slots with keys
 #pragma unroll
         for (int i = 0; i < kKeys; ++i) {
-          ok = ok && warp_wait(&sm.full[ring.at], ring.phase, abort_flag, a.status);
+          const int s = ring.at * S::kStep;
+          ok = ok && warp_wait(&sm.full[s], ring.phase, abort_flag, a.status);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t k0 = kd + ring.at * (kPair >> 4);
+          const uint32_t k0 = kd + s * (kPair >> 4);
           if (elect_one()) {
 #pragma unroll
             for (int k = 0; k < (S::DK == 64 ? 4 : 8); ++k)
               mma_ss(d, k0 + (k / 4) * (kColumn >> 4) + (k % 4) * 2, hi, qd + (2 * i + k / 4) * (N * 128 >> 4) + (k % 4) * 2, hi, idesc,
                      (S::kLatent && !S::kAlias) || i > 0 || k > 0);
-            if (!S::kLatent && S::DK == 128) umma_commit(&sm.empty[ring.at]);
+            if (S::kSplit) umma_commit(&sm.empty[s]);
           }
           __syncwarp();
           ring.next();
         }
-        if (S::kPairs > kKeys) ring.next();      // the values' slot
         if constexpr (S::kAlias) rotated();
         if (ok && elect_one()) umma_commit(&sm.s_full[sbuf.at]);
         __syncwarp();
@@ -527,7 +556,7 @@ __global__ void __launch_bounds__(S::kThreads, 1)
     constexpr uint32_t v_hi = desc_hi(1024, 2), p_hi = desc_hi(8 * S::kPRow, S::kPRow == 128 ? 2 : S::kPRow == 64 ? 4 : 6);
     constexpr int kFirst = S::DK == 64 ? 1 : 0;      // columns of a slot from here on are values
     const uint32_t vd = desc_lo(smem_u32(sm.ring), kColumn), pd = desc_lo(S::kAlias ? smem_u32(sm.rope) : smem_u32(sm.p), kColumn);
-    Ring<S::kSlots> ring;
+    Ring<S::kRing> ring;
     Ring<S::kPBufs == 2 ? 2 : 1> pbuf;
     int tile = 0;
     bool ok = true;
@@ -551,7 +580,6 @@ __global__ void __launch_bounds__(S::kThreads, 1)
         if (groups == 0 && !begun) groups = 1, zero0 = 0, zero1 = 16;      // the output starts from something
         const int tail0 = differ ? max(ctx - t * kTile, 0) : kTile, tail1 = min(pc.r.len - t * kTile, kTile);
         const bool unclean = zero0 < zero1 || tail0 < tail1;
-        if (S::kPairs > 1 && !S::kLatent) ring.next();      // the keys' slot
         bool found = false;
         // The values of a slot of the ring, as zeros where there are none or they are not finite (in the new tokens').
         auto clean = [&](uint8_t* values) {
@@ -577,30 +605,31 @@ __global__ void __launch_bounds__(S::kThreads, 1)
           __syncwarp();
         };
         // keys and values in one slot have been waited for by the first product already
-        if (unclean || (!S::kLatent && S::DK == 128)) {
-          Ring<S::kSlots> at = ring;
+        if (unclean || S::kSplit) {
+          Ring<S::kRing> at = ring;
 #pragma unroll
-          for (int m = 0; m < S::kBlocks; ++m, at.next()) ok = ok && warp_wait(&sm.full[at.at], at.phase, abort_flag, a.status);
+          for (int m = 0; m < S::kBlocks; ++m, at.next()) ok = ok && warp_wait(&sm.full[at.at * S::kStep + S::kStep - 1], at.phase, abort_flag, a.status);
         }
         ok = ok && warp_wait(&sm.p_full[pbuf.at], pbuf.phase, abort_flag, a.status);
         if (!ok) break;
         if (unclean) {
-          Ring<S::kSlots> at = ring;
+          Ring<S::kRing> at = ring;
 #pragma unroll 1
-          for (int m = 0; m < S::kBlocks; ++m, at.next()) clean(sm.ring[at.at]);
+          for (int m = 0; m < S::kBlocks; ++m, at.next()) clean(sm.ring[at.at * S::kStep + S::kStep - 1]);
         }
         tc_fence_after();
         const bool issue = elect_one();
         const uint32_t p0 = pd + pbuf.at * (S::kPBytes >> 4);
 #pragma unroll
         for (int m = 0; m < S::kBlocks; ++m, ring.next()) {
-          const uint32_t v0 = vd + ring.at * (kPair >> 4);
+          const int s = ring.at * S::kStep + S::kStep - 1;
+          const uint32_t v0 = vd + s * (kPair >> 4);
           if (issue) {
 #pragma unroll
             for (int k = 0; k < kTile / 16; ++k)
               if (groups >> k & 1)
                 mma_ss(tmem + S::kTmemO + m * N, v0 + k * (2048 >> 4), v_hi, p0 + k * S::kPRow, p_hi, idesc, begun || groups & ((1u << k) - 1));
-            umma_commit(&sm.empty[ring.at]);
+            umma_commit(&sm.empty[s]);
           }
         }
         begun |= groups != 0;
