@@ -2,7 +2,8 @@
 drafted tokens and for latent attention.
 
 Argument marshalling only, as in :mod:`block_sparse_long_gb300.kv`: every step runs in the CUDA kernels of libcosa_attn.so,
-PyTorch supplies device memory and streams, and there is no fallback.
+PyTorch supplies device memory and streams, and there is no fallback.  The checks of a call's tensors and the call itself are
+in the module _attn_call (csrc/attn_binding.cpp), which takes a third of the time that they take in Python.
 
 The functions carry the C names:
   cosa_tree_attention     attention of the newest tokens, drafted trees among them, over the prefill's bf16 pages
@@ -34,14 +35,14 @@ Every call checks the tensors' types, sizes and device on the host, runs on the 
 from __future__ import annotations
 
 import ctypes
-import functools
+import importlib
 import math
 import os
 from typing import Optional, Sequence, Tuple
 
 import torch
 
-from .kv import _Call
+from .cosa import CosaError
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 ATTN_LIB_PATH = os.path.join(_HERE, "libcosa_attn.so")
@@ -89,6 +90,24 @@ def attn_library() -> ctypes.CDLL:
     return lib
 
 
+_module = None
+
+
+def _calls():
+    """The module of checked calls, with the library's functions."""
+    global _module
+    if _module is None:
+        try:
+            module = importlib.import_module("._attn_call", __package__)
+        except ImportError as e:
+            raise RuntimeError("_attn_call is missing: build it with `python -m block_sparse_long_gb300.build`") from e
+        lib = attn_library()
+        module.bind(*(ctypes.cast(getattr(lib, "cosa_" + name), ctypes.c_void_p).value for name in (
+            "tree_attention", "latent_attention", "tree_commit", "latent_rope", "latent_prefill")))
+        _module = module
+    return _module
+
+
 def cosa_attn_version() -> int:
     return int(attn_library().cosa_attn_version())
 
@@ -132,67 +151,12 @@ def attn_required_numel(p: CosaAttnParams) -> dict:
             "tree_mask": p.total_tokens, "positions": p.total_tokens, "inv_freq": rope // 2, "weight": p.latent_dim, "status": 1}
 
 
-@functools.lru_cache(maxsize=256)
-def _sizes(params: bytes) -> dict:
-    """attn_required_numel by the parameters' values."""
-    return attn_required_numel(CosaAttnParams.from_buffer_copy(params))
-
-
-class _AttnCall(_Call):
-    """The checks of a call of this library."""
-
-    __slots__ = ()
-
-    def __init__(self, p: CosaAttnParams):
-        self.p, self.need, self.index = p, _sizes(bytes(p)), None
-
-    def strided(self, t: torch.Tensor, name: str, tokens: int, heads: Optional[int], width: int):
-        """Address, token stride and head stride of rows [tokens, heads, width] (heads None: [tokens, width]), whose tokens
-        and heads may lie apart."""
-        if t.dtype != torch.bfloat16:
-            raise ValueError(f"{name} must be torch.bfloat16, got {t.dtype}")
-        want = (width,) if heads is None else (heads, width)
-        if t.dim() != 1 + len(want) or tuple(t.shape[1:]) != want:
-            raise ValueError(f"{name} must be [tokens, {', '.join(map(str, want))}], got {list(t.shape)}")
-        if t.shape[0] < tokens:
-            raise ValueError(f"{name} holds {t.shape[0]} tokens; the parameters need at least {tokens}")
-        st, heads = t.stride(), heads or 1
-        # the stride of a single token or head says nothing
-        by_head = st[1] if len(want) == 2 and heads > 1 else width
-        by_token = st[0] if t.shape[0] > 1 else max(heads * width, (heads - 1) * by_head + width)
-        if t.shape[0]:
-            if st[-1] != 1:
-                raise ValueError(f"{name}: the values of a head must be contiguous")
-            if by_head < width:
-                raise ValueError(f"{name}: heads are {by_head} elements apart, a head has {width}")
-            if t.shape[0] > 1 and by_token < (heads - 1) * by_head + width:
-                raise ValueError(f"{name}: tokens are {by_token} elements apart, a token has {(heads - 1) * by_head + width}")
-        self.on_device(t, name)
-        if t.shape[0] <= 1:
-            by_token += -by_token % 8
-        return t.data_ptr(), by_token, by_head
-
-    def params(self, **strides) -> CosaAttnParams:
-        """The parameters with this call's strides (a copy: the caller's stay as they are)."""
-        p = CosaAttnParams.from_buffer_copy(self.p)
-        for n, s in strides.items():
-            setattr(p, n, s)
-        return p
-
-    def run(self, name: str, p: CosaAttnParams, args, status, stream) -> None:
-        super().run(name, p, args, status, stream, _lib or attn_library())
-
-    def scratch(self, workspace: Optional[torch.Tensor], size_of, stream) -> list:
-        """Address and bytes of the workspace, allocated here if there is none."""
-        if workspace is None:
-            workspace = self.empty(max(size_of(self.p), 256), torch.uint8, stream)
-        self.on_device(workspace, "workspace")
-        if not workspace.is_contiguous():
-            raise ValueError("workspace must be contiguous")
-        return [workspace.data_ptr(), workspace.numel() * workspace.element_size()]
-
-
-_BF, _I32 = torch.bfloat16, torch.int32
+def _empty(like: torch.Tensor, shape, dtype: torch.dtype, stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
+    """Memory for an output or workspace, tied to the stream that the call runs on."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
 
 
 def cosa_tree_attention(p: CosaAttnParams, q: torch.Tensor, cu_seqlens: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -204,17 +168,13 @@ def cosa_tree_attention(p: CosaAttnParams, q: torch.Tensor, cu_seqlens: torch.Te
     returns out bf16 [T, Hq, d].  Bit j of tree_mask[t] (int64): token t sees its request's token j; without it a token sees
     those up to itself.  lse, float32 [T, Hq], is written if given.  A workspace that is given must be large enough and not
     in use by another call; without one it is allocated here."""
-    c = _AttnCall(p)
-    qp, qs, qh = c.strided(q, "q", p.total_tokens, p.num_q_heads, p.head_dim)
-    if qh != p.head_dim:
-        raise ValueError("q: the heads of a token must be contiguous")
     if out is None:
-        out = c.empty((p.total_tokens, p.num_q_heads, p.head_dim), _BF, stream)
-    args = c.dense((cu_seqlens, "cu_seqlens", _I32), (k_cache, "k_cache", _BF), (v_cache, "v_cache", _BF),
-                   (page_table, "page_table", _I32), (kv_len, "kv_len", _I32), (tree_mask, "tree_mask", torch.int64),
-                   (out, "out", _BF), (lse, "lse", torch.float32))
-    args += c.scratch(workspace, cosa_tree_attention_workspace_size, stream)
-    c.run("cosa_tree_attention", c.params(q_stride=qs), (qp, *args), status, stream)
+        out = _empty(q, (p.total_tokens, p.num_q_heads, p.head_dim), torch.bfloat16, stream)
+    if workspace is None:
+        workspace = _empty(q, max(cosa_tree_attention_workspace_size(p), 256), torch.uint8, stream)
+    rc = (_module or _calls()).tree_attention(p, q, cu_seqlens, k_cache, v_cache, page_table, kv_len, tree_mask, out, lse, workspace, status, stream)
+    if rc:
+        raise CosaError(rc, "cosa_tree_attention")
     return out
 
 
@@ -224,22 +184,14 @@ def cosa_tree_commit(p: CosaAttnParams, caches: Sequence[torch.Tensor], cu_seqle
     """Moves the rows of tokens path[b, 0] < path[b, 1] < ... (path_len[b] of them) of each request's tree to the slots behind
     its context, in the one or two caches given ([pages, P, Hkv, d] keys and values, or [pages, P, latent_dim + 64]); returns
     new_len [B], the requests' lengths after it."""
-    c = _AttnCall(p)
-    caches = tuple(caches)
-    if len(caches) not in (1, 2) or any(x.dtype != _BF or x.dim() < 3 or not x.is_contiguous() for x in caches):
+    if len(caches) not in (1, 2):
         raise ValueError("caches: one or two contiguous bf16 tensors [num_pages, page_size, ...]")
-    row = math.prod(caches[0].shape[2:])
-    for x in caches:
-        if x.shape[0] < p.num_pages or x.shape[1] != p.page_size or math.prod(x.shape[2:]) != row:
-            raise ValueError(f"caches must be [{p.num_pages}, {p.page_size}, ...] with equal rows, got {list(x.shape)}")
-    for x in caches:
-        c.on_device(x, "caches")
     if new_len is None:
-        new_len = c.empty((p.num_reqs,), _I32, stream)
-    args = c.dense((cu_seqlens, "cu_seqlens", _I32), (page_table, "page_table", _I32), (kv_len, "kv_len", _I32), (path, "path", _I32),
-                   (path_len, "path_len", _I32), (new_len, "new_len", _I32))
-    second = caches[1].data_ptr() if len(caches) == 2 else None
-    c.run("cosa_tree_commit", p, (caches[0].data_ptr(), second, row, *args), status, stream)
+        new_len = _empty(caches[0], (p.num_reqs,), torch.int32, stream)
+    rc = (_module or _calls()).tree_commit(p, caches[0], caches[1] if len(caches) == 2 else None, cu_seqlens, page_table, kv_len, path, path_len,
+                                           new_len, status, stream)
+    if rc:
+        raise CosaError(rc, "cosa_tree_commit")
     return new_len
 
 
@@ -253,19 +205,15 @@ def cosa_latent_rope(p: CosaAttnParams, kv: torch.Tensor, cu_seqlens: torch.Tens
     """Norm of the latent part and rotation of the rest of kv [T, latent_dim + 64], and rotation of q [T, Hq, 64] (tokens and
     heads may lie apart, as in a slice of the query projection).  With cache and page_table they go to the pages, with c_out
     [T, latent_dim] and k_out [T, 64], or without either, to rows.  Returns (q_out, c_out, k_out), None where there is none."""
-    c = _AttnCall(p)
-    rope = COSA_ATTN_ROPE_DIM
-    kvp, kvs, _ = c.strided(kv, "kv", p.total_tokens, None, p.latent_dim + rope)
-    qp, qs, qh = (None, 0, 0) if q is None else c.strided(q, "q", p.total_tokens, p.num_q_heads, rope)
     if q is not None and q_out is None:
-        q_out = c.empty((p.total_tokens, p.num_q_heads, rope), _BF, stream)
+        q_out = _empty(kv, (p.total_tokens, p.num_q_heads, COSA_ATTN_ROPE_DIM), torch.bfloat16, stream)
     if c_out is None and k_out is None and cache is None:
-        c_out = c.empty((p.total_tokens, p.latent_dim), _BF, stream)
-        k_out = c.empty((p.total_tokens, rope), _BF, stream)
-    args = c.dense((weight, "weight", _BF), (inv_freq, "inv_freq", torch.float64), (positions, "positions", _I32),
-                   (cu_seqlens, "cu_seqlens", _I32), (start, "start", _I32), (q_out, "q_out", _BF), (c_out, "c_out", _BF),
-                   (k_out, "k_out", _BF), (cache, "latent_cache", _BF), (page_table, "page_table", _I32))
-    c.run("cosa_latent_rope", c.params(k_stride=kvs, q_rope_stride=qs, q_rope_head_stride=qh), (kvp, qp, *args), status, stream)
+        c_out = _empty(kv, (p.total_tokens, p.latent_dim), torch.bfloat16, stream)
+        k_out = _empty(kv, (p.total_tokens, COSA_ATTN_ROPE_DIM), torch.bfloat16, stream)
+    rc = (_module or _calls()).latent_rope(p, kv, q, weight, inv_freq, positions, cu_seqlens, start, q_out, c_out, k_out, cache, page_table,
+                                           status, stream)
+    if rc:
+        raise CosaError(rc, "cosa_latent_rope")
     return q_out, c_out, k_out
 
 
@@ -276,18 +224,14 @@ def cosa_latent_attention(p: CosaAttnParams, q_latent: torch.Tensor, q_rope: tor
                           status: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """Attention of the newest tokens, queries q_latent [T, Hq, latent_dim] and q_rope [T, Hq, 64], over the pages of latent
     vectors; returns out bf16 [T, Hq, latent_dim].  The rest as in cosa_tree_attention."""
-    c = _AttnCall(p)
-    qp, qs, qh = c.strided(q_latent, "q_latent", p.total_tokens, p.num_q_heads, p.latent_dim)
-    rp, rs, rh = c.strided(q_rope, "q_rope", p.total_tokens, p.num_q_heads, COSA_ATTN_ROPE_DIM)
-    if qh != p.latent_dim or rh != COSA_ATTN_ROPE_DIM:
-        raise ValueError("q_latent, q_rope: the heads of a token must be contiguous")
     if out is None:
-        out = c.empty((p.total_tokens, p.num_q_heads, p.latent_dim), _BF, stream)
-    args = c.dense((cu_seqlens, "cu_seqlens", _I32), (cache, "latent_cache", _BF), (page_table, "page_table", _I32),
-                   (kv_len, "kv_len", _I32), (tree_mask, "tree_mask", torch.int64), (out, "out", _BF), (lse, "lse", torch.float32),
-                   out="latent_out")
-    args += c.scratch(workspace, cosa_latent_attention_workspace_size, stream)
-    c.run("cosa_latent_attention", c.params(q_stride=qs, q_rope_stride=rs), (qp, rp, *args), status, stream)
+        out = _empty(q_latent, (p.total_tokens, p.num_q_heads, p.latent_dim), torch.bfloat16, stream)
+    if workspace is None:
+        workspace = _empty(q_latent, max(cosa_latent_attention_workspace_size(p), 256), torch.uint8, stream)
+    rc = (_module or _calls()).latent_attention(p, q_latent, q_rope, cu_seqlens, cache, page_table, kv_len, tree_mask, out, lse, workspace, status,
+                                                stream)
+    if rc:
+        raise CosaError(rc, "cosa_latent_attention")
     return out
 
 
@@ -298,17 +242,9 @@ def cosa_latent_prefill(p: CosaAttnParams, q_nope: torch.Tensor, q_rope: torch.T
     """Causal attention of prompts packed by cu_seqlens: queries q_nope [T, Hq, d] and q_rope [T, Hq, 64], keys k_nope
     [Tk, Hq, d] and, shared by the heads, k_rope [Tk, 64], values v [Tk, Hq, d], packed by cu_kv (without it, by cu_seqlens; a
     request's queries are the last of its keys); tokens and heads may lie apart.  Returns out bf16 [T, Hq, d]."""
-    c = _AttnCall(p)
-    H, d, rope, T, Tk = p.num_q_heads, p.head_dim, COSA_ATTN_ROPE_DIM, p.total_tokens, p.total_kv_tokens
-    qp, qs, qh = c.strided(q_nope, "q_nope", T, H, d)
-    rp, rs, rh = c.strided(q_rope, "q_rope", T, H, rope)
-    kp, ks, kh = c.strided(k_nope, "k_nope", Tk, H, d)
-    krp, krs, _ = c.strided(k_rope, "k_rope", Tk, None, rope)
-    vp, vs, vh = c.strided(v, "v", Tk, H, d)
     if out is None:
-        out = c.empty((T, H, d), _BF, stream)
-    args = c.dense((cu_seqlens, "cu_seqlens", _I32), (cu_kv, "cu_kv", _I32), (out, "out", _BF), (lse, "lse", torch.float32))
-    strides = dict(q_stride=qs, q_head_stride=qh, q_rope_stride=rs, q_rope_head_stride=rh, k_stride=ks, k_head_stride=kh,
-                   k_rope_stride=krs, v_stride=vs, v_head_stride=vh)
-    c.run("cosa_latent_prefill", c.params(**strides), (qp, rp, kp, krp, vp, *args), status, stream)
+        out = _empty(q_nope, (p.total_tokens, p.num_q_heads, p.head_dim), torch.bfloat16, stream)
+    rc = (_module or _calls()).latent_prefill(p, q_nope, q_rope, k_nope, k_rope, v, cu_seqlens, cu_kv, out, lse, status, stream)
+    if rc:
+        raise CosaError(rc, "cosa_latent_prefill")
     return out

@@ -1,5 +1,6 @@
 """Build libcosa.so (the C-ABI library of the CUDA path), libcosa_kv.so (what stands around it: include/cosa_kv.h) and
-libcosa_attn.so (dense attention beside it: include/cosa_attn.h) in-tree for sm_103a.
+libcosa_attn.so (dense attention beside it: include/cosa_attn.h) in-tree for sm_103a, and _attn_call, the Python module that
+checks a call's tensors for the latter.
 
 Compiles the translation units under csrc/ in parallel with nvcc and links them into
 block_sparse_long_gb300/libcosa.so, libcosa_kv.so and libcosa_attn.so.  The CUDA runtime is linked statically and the driver
@@ -14,6 +15,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -48,6 +50,10 @@ def _inputs(sources, headers, public):
     return files
 
 
+# host code against PyTorch's headers: its suffix names the interpreter and the machine
+CALL = os.path.join(HERE, "_attn_call" + sysconfig.get_config_var("EXT_SUFFIX"))
+CALL_SOURCES = ["attn_binding.cpp"]
+
 # library, its translation units, the headers they include
 LIBRARIES = ((LIB, SOURCES, HEADERS, ["cosa.h"]), (KV_LIB, KV_SOURCES, KV_HEADERS, ["cosa.h", "cosa_kv.h"]),
              (ATTN_LIB, ATTN_SOURCES, ATTN_HEADERS, ["cosa.h", "cosa_kv.h", "cosa_attn.h"]))
@@ -61,13 +67,32 @@ def _stale(lib, sources, headers, public) -> bool:
 
 
 def up_to_date() -> bool:
-    return not any(_stale(*entry) for entry in LIBRARIES)
+    return not any(_stale(*entry) for entry in LIBRARIES) and not _stale(CALL, CALL_SOURCES, [], ["cosa.h", "cosa_attn.h"])
+
+
+def _build_call() -> None:
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    include = [os.path.join(ROOT, "include"), os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+               sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    tmp = CALL + ".tmp"
+    cmd = ["g++", "-std=c++17", "-O2", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall", *(f"-I{d}" for d in include[:1]),
+           *(f"-isystem{d}" for d in include[1:]), *(os.path.join(CSRC, f) for f in CALL_SOURCES), "-o", tmp,
+           f"-L{os.path.join(root, 'lib')}", "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {CALL_SOURCES[0]}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, CALL)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile and link the libraries whose inputs changed; returns the path of libcosa.so."""
     todo = [entry for entry in LIBRARIES if force or _stale(*entry)]
+    call = force or _stale(CALL, CALL_SOURCES, [], ["cosa.h", "cosa_attn.h"])
     if not todo:
+        if call:
+            _build_call()
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     cc = nvcc()
@@ -85,8 +110,11 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return obj
 
     sources = [src for _, srcs, _, _ in todo for src in srcs]
-    with ThreadPoolExecutor(len(sources)) as ex:
+    with ThreadPoolExecutor(len(sources) + 1) as ex:
+        other = ex.submit(_build_call) if call else None
         objs = dict(zip(sources, ex.map(compile_one, sources)))
+        if other is not None:
+            other.result()
     for lib, srcs, _, _ in todo:
         tmp = lib + ".tmp"
         cmd = [cc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *(objs[src] for src in srcs)]

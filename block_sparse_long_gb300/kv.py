@@ -207,7 +207,7 @@ class _Call:
             setattr(p, n, s)
         return p
 
-    def run(self, name: str, p: ctypes.Structure, args, status: Optional[torch.Tensor], stream, lib: Optional[ctypes.CDLL] = None) -> None:
+    def run(self, name: str, p: CosaKvParams, args, status: Optional[torch.Tensor], stream) -> None:
         if status is not None:
             (status,) = self.dense((status, "status", torch.int32))
         if stream is None:
@@ -216,7 +216,7 @@ class _Call:
             s = stream.cuda_stream
         else:
             raise ValueError(f"stream is on {stream.device}, the tensors on cuda:{self.index}")
-        f = getattr(lib or _lib or kv_library(), name)
+        f = getattr(_lib or kv_library(), name)
         if torch.cuda.current_device() == self.index:
             rc = f(p, *args, status, s)
         else:
