@@ -164,8 +164,8 @@ def cosa_tree_attention(p: CosaAttnParams, q: torch.Tensor, cu_seqlens: torch.Te
                         out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
                         workspace: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
                         stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
-    """Attention of the newest tokens q [T, Hq, d] (request b's are the last of its kv_len[b] slots) over the bf16 pages;
-    returns out bf16 [T, Hq, d].  Bit j of tree_mask[t] (int64): token t sees its request's token j; without it a token sees
+    """Attention of the newest tokens q [T, Hq, d] (tokens and heads may lie apart; request b's are the last of its kv_len[b]
+    slots) over the bf16 pages; returns out bf16 [T, Hq, d].  Bit j of tree_mask[t] (int64): token t sees its request's token j; without it a token sees
     those up to itself.  lse, float32 [T, Hq], is written if given.  A workspace that is given must be large enough and not
     in use by another call; without one it is allocated here."""
     if out is None:

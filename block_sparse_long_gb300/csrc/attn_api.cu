@@ -71,11 +71,13 @@ int64_t stride_of(int64_t given, int64_t dense) {
   return given >= dense && given % 8 == 0 && given <= kMaxStride ? given : -1;
 }
 
-// Token and head strides of rows of `heads` times `width` values.
-bool strides_of(int64_t token, int64_t head, int64_t heads, int64_t width, int64_t* by_token, int64_t* by_head) {
-  *by_head = stride_of(head, width);
-  *by_token = *by_head < 0 ? -1 : token == 0 ? (heads - 1) * *by_head + width : stride_of(token, (heads - 1) * *by_head + width);
-  return *by_token >= 0 && *by_token % 8 == 0;
+// Token and head strides of `tokens` rows of `heads` times `width` values: heads within a token, or tokens within a head.
+bool strides_of(int64_t token, int64_t head, int64_t tokens, int64_t heads, int64_t width, int64_t* by_token, int64_t* by_head) {
+  *by_head = head == 0 ? width : head;
+  *by_token = token == 0 ? (heads - 1) * *by_head + width : token;
+  for (const int64_t s : {*by_head, *by_token})
+    if (s < width || s % 8 != 0 || s > kMaxStride) return false;
+  return *by_token >= (heads - 1) * *by_head + width || *by_head >= (tokens - 1) * *by_token + width;
 }
 
 cosa_attn::PagedLaunch paged_of(const cosa_attn_params* p, bool latent) {
@@ -85,8 +87,6 @@ cosa_attn::PagedLaunch paged_of(const cosa_attn_params* p, bool latent) {
   L.num_kv_heads = latent ? 1 : p->num_kv_heads;
   L.head_dim = latent ? 0 : p->head_dim;
   L.latent_dim = latent ? p->latent_dim : 0;
-  L.q_stride = stride_of(p->q_stride, static_cast<int64_t>(p->num_q_heads) * (latent ? p->latent_dim : p->head_dim));
-  L.q_rope_stride = latent ? stride_of(p->q_rope_stride, p->num_q_heads * kRot) : 0;
   L.page_size = p->page_size;
   L.page_shift = shift_of(p->page_size);
   L.total_tokens = p->total_tokens;
@@ -99,6 +99,12 @@ cosa_attn::PagedLaunch paged_of(const cosa_attn_params* p, bool latent) {
   return L;
 }
 
+bool query_strides(const cosa_attn_params* p, bool latent, cosa_attn::PagedLaunch* L) {
+  const int64_t T = p->total_tokens, H = p->num_q_heads;
+  return strides_of(p->q_stride, p->q_head_stride, T, H, latent ? p->latent_dim : p->head_dim, &L->q_stride, &L->q_head_stride) &&
+         (!latent || strides_of(p->q_rope_stride, p->q_rope_head_stride, T, H, kRot, &L->q_rope_stride, &L->q_rope_head_stride));
+}
+
 int check_paged(const cosa_attn_params* p, bool latent) {
   COSA_TRY(check_common(p));
   COSA_TRY(check_slots(p));
@@ -106,10 +112,9 @@ int check_paged(const cosa_attn_params* p, bool latent) {
   COSA_TRY(check_scale(p));
   if (p->max_new_tokens < 1) return COSA_ERR_INVALID_ARG;
   if (static_cast<int64_t>(p->total_tokens) * p->num_q_heads > INT32_MAX) return COSA_ERR_UNSUPPORTED;
-  const int64_t width = latent ? p->latent_dim : p->head_dim;
-  if (stride_of(p->q_stride, p->num_q_heads * width) < 0) return COSA_ERR_INVALID_ARG;
-  if (latent && stride_of(p->q_rope_stride, p->num_q_heads * kRot) < 0) return COSA_ERR_INVALID_ARG;
-  return cosa_attn::paged_fits(paged_of(p, latent)) ? COSA_OK : COSA_ERR_UNSUPPORTED;
+  cosa_attn::PagedLaunch L = paged_of(p, latent);
+  if (!query_strides(p, latent, &L)) return COSA_ERR_INVALID_ARG;
+  return cosa_attn::paged_fits(L) ? COSA_OK : COSA_ERR_UNSUPPORTED;
 }
 
 int done(cudaError_t e) { return e == cudaSuccess ? COSA_OK : COSA_ERR_CUDA; }
@@ -131,6 +136,7 @@ int run_paged(const cosa_attn_params* p, bool latent, const void* q, const void*
       !aligned(4, cu_seqlens, page_table, kv_len, lse, device_status))
     return COSA_ERR_INVALID_ARG;
   cosa_attn::PagedLaunch L = paged_of(p, latent);
+  query_strides(p, latent, &L);
   if (!workspace || !aligned(256, workspace) || workspace_bytes < cosa_attn::paged_workspace_bytes(L)) return COSA_ERR_WORKSPACE;
   if (out == q) return COSA_ERR_INVALID_ARG;      // CTAs that share a row's keys write it while others read its query
   L.q = as<uint16_t>(q);
@@ -228,7 +234,7 @@ int cosa_latent_rope(const cosa_attn_params* p, const void* kv, const void* q, c
   L.kv_stride = stride_of(p->k_stride, p->latent_dim + kRot);
   if (L.kv_stride < 0) return COSA_ERR_INVALID_ARG;
   if (q) {
-    if (!strides_of(p->q_rope_stride, p->q_rope_head_stride, p->num_q_heads, kRot, &L.q_stride, &L.q_head_stride)) return COSA_ERR_INVALID_ARG;
+    if (!strides_of(p->q_rope_stride, p->q_rope_head_stride, p->total_tokens, p->num_q_heads, kRot, &L.q_stride, &L.q_head_stride)) return COSA_ERR_INVALID_ARG;
     // in place only row for row
     if (q_out == q && (L.q_stride != p->num_q_heads * kRot || L.q_head_stride != kRot)) return COSA_ERR_INVALID_ARG;
   }
@@ -267,11 +273,11 @@ int cosa_latent_prefill(const cosa_attn_params* p, const void* q_nope, const voi
   if (p->max_new_tokens < 1 || p->total_kv_tokens < 0) return COSA_ERR_INVALID_ARG;
   if (p->total_kv_tokens > kMaxTokens || static_cast<int64_t>(p->total_tokens) * p->num_q_heads > INT32_MAX) return COSA_ERR_UNSUPPORTED;
   cosa_attn::PrefillLaunch L{};
-  const int64_t H = p->num_q_heads, d = p->head_dim;
-  if (!strides_of(p->q_stride, p->q_head_stride, H, d, &L.q_stride, &L.q_head_stride) ||
-      !strides_of(p->q_rope_stride, p->q_rope_head_stride, H, kRot, &L.q_rope_stride, &L.q_rope_head_stride) ||
-      !strides_of(p->k_stride, p->k_head_stride, H, d, &L.k_stride, &L.k_head_stride) ||
-      !strides_of(p->v_stride, p->v_head_stride, H, d, &L.v_stride, &L.v_head_stride))
+  const int64_t H = p->num_q_heads, d = p->head_dim, T = p->total_tokens, Tk = p->total_kv_tokens;
+  if (!strides_of(p->q_stride, p->q_head_stride, T, H, d, &L.q_stride, &L.q_head_stride) ||
+      !strides_of(p->q_rope_stride, p->q_rope_head_stride, T, H, kRot, &L.q_rope_stride, &L.q_rope_head_stride) ||
+      !strides_of(p->k_stride, p->k_head_stride, Tk, H, d, &L.k_stride, &L.k_head_stride) ||
+      !strides_of(p->v_stride, p->v_head_stride, Tk, H, d, &L.v_stride, &L.v_head_stride))
     return COSA_ERR_INVALID_ARG;
   L.k_rope_stride = stride_of(p->k_rope_stride, kRot);
   if (L.k_rope_stride < 0) return COSA_ERR_INVALID_ARG;

@@ -109,21 +109,20 @@ struct Call {
       Py_XDECREF(shape);
       throw Refused{};
     }
-    const int64_t n = t.size(0);
+    const int64_t n = t.size(0), h = heads ? heads : 1;
     if (n < tokens) refuse("%s holds %lld tokens; the parameters need at least %lld", name, (long long)n, (long long)tokens);
     // the stride of a single token or head says nothing
-    const int64_t head = heads > 1 ? t.stride(1) : width, span = ((heads ? heads : 1) - 1) * head + width;
-    int64_t token = n > 1 ? t.stride(0) : span;
+    int64_t head = h > 1 ? t.stride(1) : width, token = n > 1 ? t.stride(0) : (h - 1) * head + width;
     if (n > 0) {
       if (t.stride(dims - 1) != 1) refuse("%s: the values of a head must be contiguous", name);
       if (head < width) refuse("%s: heads are %lld elements apart, a head has %lld", name, (long long)head, (long long)width);
-      if (n > 1 && token < span) refuse("%s: tokens are %lld elements apart, a token has %lld", name, (long long)token, (long long)span);
+      if (n > 1 && token < (h - 1) * head + width && (token < width || head < (n - 1) * token + width))
+        refuse("%s: tokens are %lld elements apart, heads %lld: they overlap", name, (long long)token, (long long)head);
     }
     on_device(t, name);
     if (n <= 1) token += (8 - token % 8) % 8;
     *by_token = token;
     if (by_head != nullptr) *by_head = head;
-    else if (heads && head != width) refuse("%s: the heads of a token must be contiguous", name);
     return t.data_ptr();
   }
 
@@ -195,7 +194,7 @@ PyObject* tree_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     Call c(a[0]);
     cosa_attn_params& p = c.p;
     const int64_t cache = c.slots() * p.num_kv_heads * p.head_dim, rows = c.query_rows();
-    const void* q = c.rows(a[1], "q", p.total_tokens, p.num_q_heads, p.head_dim, &p.q_stride, nullptr);
+    const void* q = c.rows(a[1], "q", p.total_tokens, p.num_q_heads, p.head_dim, &p.q_stride, &p.q_head_stride);
     const int32_t* cu = c.ints(a[2], "cu_seqlens", int64_t{p.num_reqs} + 1);
     const void* k = c.bf16(a[3], "k_cache", cache);
     const void* v = c.bf16(a[4], "v_cache", cache);
@@ -217,8 +216,8 @@ PyObject* latent_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     Call c(a[0]);
     cosa_attn_params& p = c.p;
     const int64_t rows = c.query_rows();
-    const void* q = c.rows(a[1], "q_latent", p.total_tokens, p.num_q_heads, p.latent_dim, &p.q_stride, nullptr);
-    const void* r = c.rows(a[2], "q_rope", p.total_tokens, p.num_q_heads, kRot, &p.q_rope_stride, nullptr);
+    const void* q = c.rows(a[1], "q_latent", p.total_tokens, p.num_q_heads, p.latent_dim, &p.q_stride, &p.q_head_stride);
+    const void* r = c.rows(a[2], "q_rope", p.total_tokens, p.num_q_heads, kRot, &p.q_rope_stride, &p.q_rope_head_stride);
     const int32_t* cu = c.ints(a[3], "cu_seqlens", int64_t{p.num_reqs} + 1);
     const void* cache = c.bf16(a[4], "latent_cache", c.slots() * (p.latent_dim + kRot));
     const int32_t* table = c.ints(a[5], "page_table", c.tables());

@@ -39,7 +39,7 @@ struct PagedLaunch {
   float* lse;
   void* workspace;
   int32_t* status;
-  int64_t q_stride, q_rope_stride;
+  int64_t q_stride, q_head_stride, q_rope_stride, q_rope_head_stride;
   int num_reqs, num_q_heads, num_kv_heads, head_dim, latent_dim;      // latent_dim 0: the tree attention
   int page_size, page_shift, total_tokens, max_seqlen, num_pages, max_pages_per_req, max_new_tokens;
   float scale_log2;      // sm_scale * log2(e)

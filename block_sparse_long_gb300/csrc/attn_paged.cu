@@ -104,7 +104,7 @@ struct Args {
   float *lse, *part_o, *part_ml;
   Join* joins;
   int32_t* status;
-  int64_t q_stride, q_rope_stride;
+  int64_t q_stride, q_head_stride, q_rope_stride, q_rope_head_stride;
   int num_reqs, num_q_heads, num_kv_heads, group, page_shift, total_tokens, max_seqlen, num_pages, max_pages_per_req;
   int join_items;      // entries of `joins` if they are by item, 0 if by CTA
   int whole;           // items are not cut: a unit is an item
@@ -733,8 +733,8 @@ __global__ void __launch_bounds__(S::kThreads, 1)
         const int head = pc.head * a.group + row - node * a.group;
         sm.row[tid] = row < rows ? (r.tok0 + node) * a.num_q_heads + head : -1;
         sm.node[tid] = node;
-        sm.q_at[tid] = row < rows ? (r.tok0 + node) * a.q_stride + head * DV : -1;
-        if (S::kLatent) sm.r_at[tid] = (r.tok0 + node) * a.q_rope_stride + head * (S::DK - DV);
+        sm.q_at[tid] = row < rows ? (r.tok0 + node) * a.q_stride + head * a.q_head_stride : -1;
+        if (S::kLatent) sm.r_at[tid] = (r.tok0 + node) * a.q_rope_stride + head * a.q_rope_head_stride;
         sm.mask[tid] = a.tree_mask ? static_cast<uint64_t>(__ldg(a.tree_mask + r.tok0 + node)) : 0;
         sm.base[tid] = -kNone;
       }
@@ -1025,7 +1025,8 @@ __global__ void __launch_bounds__(kWide ? kWideThreads : kJoinThreads) join_kern
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   cosa_kv::wait_for_stream();
   const Join j = a.joins[blockIdx.x];
-  if (j.parts < 2) return;
+  // (the bounds hold whatever another call might have made of the workspace)
+  if (j.parts < 2 || j.parts > kCtas || j.first < 0 || j.first >= 2 * kCtas || j.next < 0 || j.next + 2 * (j.parts - 2) >= 2 * kCtas) return;
   const int parts = j.parts, seg = blockIdx.z;
   const int c = kWide ? blockIdx.y : blockIdx.y * 8 + warp;      // row of the tile
   const int64_t row = static_cast<int64_t>(j.row_tile) * N + c;
@@ -1088,6 +1089,7 @@ __global__ void __launch_bounds__(kWide ? kWideThreads : kJoinThreads) join_kern
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
   const int64_t to = (j.tok0 + row / a.group) * a.num_q_heads + j.head * a.group + row % a.group;
+  if (to < 0 || to >= static_cast<int64_t>(a.total_tokens) * a.num_q_heads) return;
   uint16_t* dst = a.out + to * DV + seg * kSeg + lane * kVec;
   if constexpr (kVec == 4)
     *reinterpret_cast<uint2*>(dst) = make_uint2(cosa::pack_bf16x2(o[0] * inv, o[1] * inv), cosa::pack_bf16x2(o[2] * inv, o[3] * inv));
@@ -1129,7 +1131,9 @@ cudaError_t launch_shape(const PagedLaunch& L, cudaStream_t stream) {
   a.join_items = items <= kCtas ? static_cast<int>(items) : 0;
   a.status = L.status;
   a.q_stride = L.q_stride;
+  a.q_head_stride = L.q_head_stride;
   a.q_rope_stride = L.q_rope_stride;
+  a.q_rope_head_stride = L.q_rope_head_stride;
   a.num_reqs = L.num_reqs;
   a.num_q_heads = L.num_q_heads;
   a.num_kv_heads = L.num_kv_heads;

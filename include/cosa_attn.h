@@ -42,7 +42,8 @@
  *     not change it.
  *     A batch whose tiles of 128 slots, by max_seqlen, times row tiles pass 31 bits is refused.
  *   - lse, float32 [total_tokens, Hq] or NULL: the natural logarithm of the sum of exp(logit) over what the row sees.
- *   - Tensors are bf16 unless noted, 16-byte aligned, strides are in elements, multiples of 8, and 0 for dense:
+ *   - Tensors are bf16 unless noted, 16-byte aligned.  Strides are in elements, multiples of 8, and 0 for dense; heads lie
+ *     within a token or tokens within a head, without overlap.
  *       k_cache, v_cache  [num_pages, P, Hkv, d] dense (the pages of cosa.h)
  *       latent_cache      [num_pages, P, latent_dim + 64] dense: c, then r
  *       page tables       int32 [num_reqs, max_pages_per_req]
@@ -90,7 +91,7 @@ typedef struct cosa_attn_params {
   int32_t flags;             /* COSA_ATTN_FLAG_*                                                */
   int32_t reserved;          /* 0                                                               */
   int64_t q_stride;          /* between tokens of q (tree), q_latent, q_nope                    */
-  int64_t q_head_stride;     /* between heads of q_nope                                         */
+  int64_t q_head_stride;     /* between heads of them                                           */
   int64_t q_rope_stride;     /* between tokens of q_rope                                        */
   int64_t q_rope_head_stride;/* between heads of q_rope                                         */
   int64_t k_stride;          /* between tokens of k_nope; of kv (rope)                          */
@@ -107,7 +108,7 @@ int cosa_attn_version(void);
 
 /*
  * Attention over the bf16 pages.  Query head h reads kv head h / (Hq / Hkv).
- *   q          [total_tokens, Hq, d], tokens q_stride apart
+ *   q          [total_tokens, Hq, d], tokens q_stride and heads q_head_stride apart
  *   tree_mask  int64 [total_tokens], or NULL
  *   out        [total_tokens, Hq, d] dense, not q itself
  *   workspace  at least cosa_tree_attention_workspace_size(p) bytes, 256-byte aligned; its content on entry does
@@ -158,8 +159,8 @@ int cosa_latent_rope(const cosa_attn_params* p, const void* kv, const void* q, c
 
 /*
  * Attention over the pages of latent vectors: logits (q_latent . c + q_rope . r) * sm_scale, output sum p c.
- *   q_latent   [total_tokens, Hq, latent_dim], tokens q_stride apart
- *   q_rope     [total_tokens, Hq, 64], tokens q_rope_stride apart
+ *   q_latent   [total_tokens, Hq, latent_dim], tokens q_stride and heads q_head_stride apart
+ *   q_rope     [total_tokens, Hq, 64], tokens q_rope_stride and heads q_rope_head_stride apart
  *   tree_mask  int64 [total_tokens], or NULL
  *   out        [total_tokens, Hq, latent_dim] dense, not q_latent itself
  *   workspace  at least cosa_latent_attention_workspace_size(p) bytes, as above

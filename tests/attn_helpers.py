@@ -86,7 +86,9 @@ class Paged:
 
         def rows(x):
             y = torch.from_numpy(np.concatenate([x, np.ones((spare, *x.shape[1:]))])).to(torch.bfloat16).to(DEV)
-            if strided:       # tokens apart, as in the slice of a fused projection
+            if strided == "heads":      # head by head, as a batched product leaves them
+                y = y.transpose(0, 1).contiguous().transpose(0, 1)
+            elif strided:     # tokens apart, as in the slice of a fused projection
                 wide = torch.zeros(y.shape[0], y[0].numel() + 48, dtype=torch.bfloat16, device=DEV)
                 wide[:, 16:16 + y[0].numel()] = y.flatten(1)
                 y = wide[:, 16:16 + y[0].numel()].unflatten(1, y.shape[1:])

@@ -100,6 +100,9 @@ def test_parameters_refused(C):
                dict(q_stride=8 * 512 + 4)):
         for call in ATTENTIONS:
             assert call(C, params(C, **kw)) == INV, (kw, call)
+    head_major = dict(q_stride=512, q_head_stride=512 * 10)        # ten tokens within a head
+    assert C.cosa_latent_attention_workspace_size(params(C, **head_major)) > 0
+    assert latent(C, params(C, q_stride=512, q_head_stride=512 * 9)) == INV
     for kw, code in ((dict(num_kv_heads=0), INV), (dict(num_kv_heads=3), INV), (dict(head_dim=96), UNS), (dict(head_dim=192), UNS)):
         assert tree(C, params(C, **kw)) == code
     for kw in (dict(latent_dim=128), dict(latent_dim=0), dict(latent_dim=640)):

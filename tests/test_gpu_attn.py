@@ -97,8 +97,9 @@ def test_chain_longer_than_a_tree(latent):
 
 
 @pytest.mark.parametrize("latent", [0, 512])
-def test_tokens_apart(latent):
-    run_and_check(Paged(9, [200, 77], [3, 2], 8, 2 if not latent else 1, 64, 32, latent=latent, strided=True))
+@pytest.mark.parametrize("strided", ["tokens", "heads"])
+def test_tokens_and_heads_apart(latent, strided):
+    run_and_check(Paged(9, [200, 77], [3, 2], 8, 2 if not latent else 1, 64, 32, latent=latent, strided=strided))
 
 
 @pytest.mark.parametrize("latent", [0, 512])
@@ -420,6 +421,14 @@ def test_prefill(H, d, fused):
 def test_prefill_lengths(n, d):
     expand_run(expand_case(n, [n], [0], 2, d))
     expand_run(expand_case(n, [n], [131], 2, d))
+
+
+def test_prefill_head_by_head():
+    """Keys and values as batched products leave them: tokens within a head."""
+    c = expand_case(4, [40, 200], [0, 9], 3, 128)
+    c["args"] = (*(x.transpose(0, 1).contiguous().transpose(0, 1) for x in c["args"][:3]), c["args"][3],
+                 c["args"][4].transpose(0, 1).contiguous().transpose(0, 1), c["args"][5])
+    expand_run(c)
 
 
 def test_prefill_without_cu_kv():
