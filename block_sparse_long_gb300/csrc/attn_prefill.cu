@@ -3,21 +3,22 @@
 //
 //     S = Q K^T,  P = exp2(S * scale - m),  O = sum P V,  l = sum P,  out = O / l
 //
-// With hundreds of queries to a key the matrix products bound it: 2 (2 d + 64) operations per visible pair.  A CTA has 256
-// queries of one head in two tiles of 128 rows, which share every block of 128 keys; while one tile's softmax runs, the
-// tensor core has the other tile's products.  All of TMEM is in use: S and O of both tiles (P goes over its S).
+// With hundreds of queries to a key the matrix products bound it: 2 (2 d + 64) operations per visible pair.  A CTA has 128
+// queries of one head and walks their keys in blocks of 128.  S is double buffered in TMEM (P goes over its S), so that the
+// softmax of one block runs under the products of its neighbours.
 //
 // Warp roles:
-//   warp 0      copies Q once, then K and V block by block (TMA).  Of the blocks on the diagonal, whose later keys some rows must
-//               not see, it clears from V what is not finite (0 times that is not 0); a row that does see such a value gets it
-//               added at the end.
-//   warp 1      issues the products, O(j) and S(j + 1) of the one tile, then of the other: the tiles take turns with the tensor
-//               core (with an issuer each they fell into step, and it idled while both had their softmax: 5600 cycles a block).
-//               In one thread's order S(j + 1) follows O(j), so P may lie over S.
-//   warp 3      owns the TMEM.
-//   warps 4-19  softmax, eight warps a tile: a thread has half a row.  The weights are taken against the row's reference of
-//               an earlier block; only if one passes 2^8 the tile stops for its maxima, scales O and takes them again.
+//   warp 0      copies Q once, then K and V block by block (TMA).
+//   warp 1      issues the products: S(j + 2) behind O(j), whose P lies in the same buffer, in one thread's order.
+//   warps 2, 3  make the values of the blocks on the diagonal, whose later keys some rows must not see, finite (0 times what is not
+//               finite is not 0); a row that does see such a value gets it added at the end.  Warp 3 owns the TMEM.
+//   warps 4-11  softmax, a thread has half a row.  The weights are taken against the row's reference of an earlier block; only if
+//               one passes 2^8 the CTA stops for its maxima, scales O and takes them again.
 // CTAs start with the longest rows of a head and go head by head, so that a head's keys stay in L2.
+//
+// Measured on the way, 16K tokens of 16 heads of 128 + 64: two tiles of 128 queries to a CTA with an issuing warp each 1.43 ms (they
+// fell into step: both softmaxes, then both products), with one issuing warp 1.37, both tiles' O before both tiles' S 1.14 (the keys'
+// slots were free for longer than a copy takes; all of TMEM and the shared memory of two tiles left no second buffer of S).
 #include <cmath>
 #include <cstdint>
 
@@ -42,34 +43,32 @@ using cosa::tc_fence_before;
 using cosa::umma_commit;
 using cosa::wait_parity_bounded;
 
-constexpr int kThreads = 640;
+constexpr int kThreads = 384;
 constexpr int kBlock = 128;                // keys
-constexpr int kRows = 256;                 // queries of a CTA
+constexpr int kRows = 128;                 // queries of a CTA
 constexpr int kColumn = kBlock * 128;      // bytes of a 64-value wide column of 128 rows
 constexpr int kHalf = kBlock / 2;          // keys of a thread's half row, and of a slot of values
 constexpr float kNone = -3e38f;            // reference of a row that has seen nothing
 constexpr uint32_t kHigh = 0x4380;         // 2^8 in bf16
 constexpr float kLn2 = 0.69314718055994531f;
-constexpr uint32_t kTmemS = 0, kTmemO = 256;      // two of 128 columns each
+constexpr uint32_t kTmemS = 0, kTmemO = 256;      // two buffers of 128 columns, and the output
 
 template <int D_>
 struct Shape {
   static constexpr int D = D_;
   static constexpr int kKeyColumns = D / 64 + 1, kValueColumns = D / 64;
-  // Slots of one column of 128 keys, and of 64 keys' values.  With heads of 128 there is room for eight columns in all; five
-  // and three leave either 20 products' time to come in.
-  static constexpr int kKeySlots = D == 128 ? 5 : 6, kValueSlots = D == 128 ? 3 : 6;
+  static constexpr int kKeySlots = 6, kValueSlots = D == 128 ? 4 : 6;      // of one column of 128 keys; of 64 keys' values
 };
 
 template <class S>
 struct alignas(1024) Smem {
-  uint8_t q[2][S::kKeyColumns][kColumn];
+  uint8_t q[S::kKeyColumns][kColumn];
   uint8_t k[S::kKeySlots][kColumn];
   uint8_t v[S::kValueSlots][S::kValueColumns][kHalf * 128];
   uint64_t q_full, k_full[S::kKeySlots], k_empty[S::kKeySlots], v_full[S::kValueSlots], v_empty[S::kValueSlots];
-  uint64_t v_clear[4];                     // of the blocks on the diagonal
-  uint64_t s_full[2], p_full[2], pv_done[2], cleanup;
-  float part[2][2][128];                   // of a row's halves: maxima, sums
+  uint64_t v_sent[4], v_clear[4];          // halves of the blocks on the diagonal: copy issued, values finite
+  uint64_t s_full[2], p_full[2], pv_done[2], cleanup;      // by block, even and odd: a parity tells two phases apart
+  float part[2][128];                      // of a row's halves: maxima, sums
   int32_t req, block;                      // this CTA's request (-1: none) and its block of queries
   int32_t odd_values;
   uint32_t tmem_base;
@@ -114,13 +113,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap qrmap, const __grid_constant__ CUtensorMap kmap,
                    const __grid_constant__ CUtensorMap krmap, const __grid_constant__ CUtensorMap vmap, const __grid_constant__ Args a) {
   constexpr int D = S::D, KC = S::kKeyColumns, VC = S::kValueColumns;
-  // There is no room to round the address up; dynamic shared memory begins on such a border where there is no other.
-  extern __shared__ __align__(1024) uint8_t smem_raw[];
-  Smem<S>& sm = *reinterpret_cast<Smem<S>*>(smem_raw);
-  if (smem_u32(smem_raw) % 1024 != 0) {
-    cosa::report_status(a.status, cosa::kStatusDeviceTimeout);
-    return;
-  }
+  extern __shared__ uint8_t smem_raw[];
+  Smem<S>& sm = *reinterpret_cast<Smem<S>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   volatile int* abort_flag = &sm.abort_flag;
   cosa_kv::wait_for_stream();
@@ -163,7 +157,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sm.v_full[s], 1);
       mbar_init(&sm.v_empty[s], 1);
     }
-    for (int s = 0; s < 4; ++s) mbar_init(&sm.v_clear[s], 1);
+    for (int s = 0; s < 4; ++s) {
+      mbar_init(&sm.v_sent[s], 1);
+      mbar_init(&sm.v_clear[s], 2);
+    }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&sm.s_full[s], 1);
       mbar_init(&sm.p_full[s], 8);
@@ -186,66 +183,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     const Request r = request_of(a, sm.req);
     const int q0 = sm.block * kRows;
     const int64_t lim0 = r.keys - r.n + q0;       // last key that the first row sees
-    // blocks of keys of each tile
-    auto blocks_of = [&](int i) {
-      const int first = q0 + i * 128;
-      return r.keys == 0 || first >= r.n ? 0 : static_cast<int>((r.keys - r.n + min(first + 127, r.n - 1)) / kBlock) + 1;
-    };
-    const int nb0 = blocks_of(0), nb1 = blocks_of(1), nb = max(nb0, nb1);
-    const int diagonal = static_cast<int>((lim0 + 1) / kBlock);      // first block with keys that some row does not see
+    // blocks of keys; the first with keys that some row does not see (two blocks at most are behind it)
+    const int nb = r.keys == 0 ? 0 : static_cast<int>((r.keys - r.n + min(q0 + kRows, r.n) - 1) / kBlock) + 1;
+    const int diagonal = nb == 0 ? 0 : static_cast<int>((lim0 + 1) / kBlock);
 
     if (warp == 0) {
       // =========================== copies ===========================
       const int tok = r.tok0 + q0, key = static_cast<int>(r.from);
       Ring<S::kKeySlots> kring;
-      Ring<S::kValueSlots> vring, cring;      // copies of values, and what is cleared of them
+      Ring<S::kValueSlots> vring;
       int columns = 0, values = 0;            // slots taken, up to the rings' sizes
       bool ok = !a.stall && nb > 0;
       if (ok && lane == 0) {
         cosa::tma_prefetch_desc(&kmap);
         cosa::tma_prefetch_desc(&vmap);
-        mbar_arrive_expect_tx(&sm.q_full, 2 * KC * kColumn);
-        for (int i = 0; i < 2; ++i) {
-          for (int c = 0; c < VC; ++c) cosa::tma_load_4d(sm.q[i][c], &qmap, &sm.q_full, 0, tok + i * 128, c, head);
-          cosa::tma_load_4d(sm.q[i][VC], &qrmap, &sm.q_full, 0, tok + i * 128, 0, head);
-        }
+        mbar_arrive_expect_tx(&sm.q_full, KC * kColumn);
+        for (int c = 0; c < VC; ++c) cosa::tma_load_4d(sm.q[c], &qmap, &sm.q_full, 0, tok, c, head);
+        cosa::tma_load_4d(sm.q[VC], &qrmap, &sm.q_full, 0, tok, 0, head);
       }
-      // what no row may multiply by 0: keys behind the request's, and what is not finite among those that some row does not see
-      auto clear = [&](int j) {
-        const int64_t k0 = static_cast<int64_t>(j) * kBlock;
-        const int first = j < diagonal ? kBlock : static_cast<int>(max(lim0 + 1 - k0, static_cast<int64_t>(0)));
-        bool found = false;
-        for (int h = 0; h < 2; ++h, cring.next()) {
-          if (!warp_wait(&sm.v_full[cring.at], cring.phase, abort_flag, a.status)) return false;
-          for (int e = max(first - h * kHalf, 0) * VC * 8 + lane; e < kHalf * VC * 8; e += 32) {
-            const int row = e / (VC * 8), c = e % (VC * 8);
-            uint4* at = reinterpret_cast<uint4*>(&sm.v[cring.at][c / 8][row * 128 + (c & 7) * 16]);
-            uint4 x = *at;
-            if (k0 + h * kHalf + row >= r.keys) {
-              *at = make_uint4(0, 0, 0, 0);
-            } else if (odd(x.x) || odd(x.y) || odd(x.z) || odd(x.w)) {
-              found = true;
-              uint32_t* w = reinterpret_cast<uint32_t*>(&x);
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                if ((w[i] & 0x7F80u) == 0x7F80u) w[i] &= 0xFFFF0000u;
-                if ((w[i] & 0x7F800000u) == 0x7F800000u) w[i] &= 0xFFFFu;
-              }
-              *at = x;
-            }
-          }
-          __syncwarp();
-        }
-        if (j < diagonal) return true;
-        cosa::fence_proxy_async_smem();
-        found = __any_sync(kAll, found);
-        if (lane == 0) {
-          if (found) sm.odd_values = 1;
-          mbar_arrive(&sm.v_clear[j - diagonal]);
-        }
-        __syncwarp();
-        return true;
-      };
       for (int j = 0; j < nb && ok; ++j) {
         for (int c = 0; c < KC && ok; ++c, kring.next()) {
           if (columns == S::kKeySlots) ok = warp_wait(&sm.k_empty[kring.at], kring.phase ^ 1, abort_flag, a.status);
@@ -265,13 +220,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_arrive_expect_tx(&sm.v_full[vring.at], VC * kHalf * 128);
             for (int c = 0; c < VC; ++c)
               cosa::tma_load_4d(sm.v[vring.at][c], &vmap, &sm.v_full[vring.at], 0, key + j * kBlock + h * kHalf, c, head);
+            if (j >= diagonal) mbar_arrive(&sm.v_sent[2 * (j - diagonal) + h]);
           }
-          __syncwarp();
-          // a block's first half is awaited, and cleared, before its slot could be wanted by the next block's second half
-          if (h == 0 && j > 0 && ok) ok = clear(j - 1);
         }
       }
-      if (ok) clear(nb - 1);
       // every copy lands before the CTA ends: the last use of each slot
       if (lane == 0 && !a.stall && nb > 0) {
         wait_parity_bounded(&sm.q_full, 0, nullptr, nullptr);
@@ -285,75 +237,113 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       __syncwarp();
+    } else if (warp == 2 || warp == 3) {
+      // =========================== values on the diagonal ===========================
+      // What no row may multiply by 0: keys behind the request's, and what is not finite among those that some row does not see.  A
+      // slot's barrier is waited for once its copy has been issued, so that its phase is the one meant.
+      bool ok = true;
+      for (int j = diagonal; j < nb && ok; ++j) {
+        const int64_t k0 = static_cast<int64_t>(j) * kBlock;
+#pragma unroll 1
+        for (int h = 0; h < 2 && ok; ++h) {
+          const int use = 2 * j + h, s = use % S::kValueSlots;
+          ok = warp_wait(&sm.v_sent[2 * (j - diagonal) + h], 0, abort_flag, a.status) &&
+               warp_wait(&sm.v_full[s], (use / S::kValueSlots) & 1, abort_flag, a.status);
+          if (!ok) break;
+          const int first = static_cast<int>(max(lim0 + 1 - k0 - h * kHalf, static_cast<int64_t>(0)));      // row of the half
+          const int64_t behind = r.keys - k0 - h * kHalf;
+          bool found = false;
+          constexpr int kBatch = 8, kRowPieces = VC * 8;
+#pragma unroll 1
+          for (int e0 = first * kRowPieces + (warp - 2) * 32 + lane; e0 < kHalf * kRowPieces; e0 += 64 * kBatch) {
+            uint4 x[kBatch];
+            auto at = [&](int k) {
+              const int e = e0 + 64 * k, row = e / kRowPieces, c = e % kRowPieces;
+              return reinterpret_cast<uint4*>(&sm.v[s][c / 8][row * 128 + (c & 7) * 16]);
+            };
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k)
+              if (e0 + 64 * k < kHalf * kRowPieces) x[k] = *at(k);
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+              if (e0 + 64 * k >= kHalf * kRowPieces) continue;
+              if ((e0 + 64 * k) / kRowPieces >= behind) {
+                *at(k) = make_uint4(0, 0, 0, 0);
+              } else if (odd(x[k].x) || odd(x[k].y) || odd(x[k].z) || odd(x[k].w)) {
+                found = true;
+                uint32_t* w = reinterpret_cast<uint32_t*>(&x[k]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  if ((w[i] & 0x7F80u) == 0x7F80u) w[i] &= 0xFFFF0000u;
+                  if ((w[i] & 0x7F800000u) == 0x7F800000u) w[i] &= 0xFFFFu;
+                }
+                *at(k) = x[k];
+              }
+            }
+          }
+          cosa::fence_proxy_async_smem();
+          found = __any_sync(kAll, found);
+          if (lane == 0) {
+            if (found) sm.odd_values = 1;
+            mbar_arrive(&sm.v_clear[2 * (j - diagonal) + h]);
+          }
+          __syncwarp();
+        }
+      }
     } else if (warp == 1) {
       // =========================== products ===========================
       constexpr uint32_t idesc_s = cosa::idesc_bf16_f32(128, kBlock, false, false), idesc_o = cosa::idesc_bf16_f32(128, D, false, true);
       constexpr uint32_t hi = desc_hi(1024, 2);
       const uint32_t qd = desc_lo(smem_u32(sm.q), 16), kd = desc_lo(smem_u32(sm.k), 16), vd = desc_lo(smem_u32(sm.v), kHalf * 128);
-      const int last = nb1 > 0 ? 1 : 0;      // the tile that is done with a block last
-      Ring<S::kKeySlots> kwait, kring[2];      // what has been waited for, and the tiles' places
-      Ring<S::kValueSlots> vwait, vring[2];
+      Ring<S::kKeySlots> kring;
+      Ring<S::kValueSlots> vring;
       bool ok = nb == 0 || warp_wait(&sm.q_full, 0, abort_flag, a.status);
-      auto wait_keys = [&] {
+      auto scores = [&](int j) {
+        // all waits before the products: between them they would leave gaps
+        Ring<S::kKeySlots> k = kring;
 #pragma unroll
-        for (int c = 0; c < KC; ++c, kwait.next()) ok = ok && warp_wait(&sm.k_full[kwait.at], kwait.phase, abort_flag, a.status);
-      };
-      auto scores = [&](int i, bool issue) {
-        const uint32_t to = tmem + kTmemS + i * 128;
+        for (int c = 0; c < KC; ++c, k.next()) ok = ok && warp_wait(&sm.k_full[k.at], k.phase, abort_flag, a.status);
+        if (!ok) return;
+        tc_fence_after();
+        const uint32_t to = tmem + kTmemS + (j & 1) * 128;
+        const bool issue = elect_one();
 #pragma unroll
-        for (int c = 0; c < KC; ++c, kring[i].next()) {
-          const uint32_t q0 = qd + (i * KC + c) * (kColumn >> 4), k0 = kd + kring[i].at * (kColumn >> 4);
+        for (int c = 0; c < KC; ++c, kring.next()) {
+          const uint32_t q0 = qd + c * (kColumn >> 4), k0 = kd + kring.at * (kColumn >> 4);
           if (issue) {
 #pragma unroll
             for (int s = 0; s < 4; ++s) mma_ss(to, q0 + 2 * s, hi, k0 + 2 * s, hi, idesc_s, c > 0 || s > 0);
-            if (i == last) umma_commit(&sm.k_empty[kring[i].at]);
+            umma_commit(&sm.k_empty[kring.at]);
           }
         }
-        if (issue) umma_commit(&sm.s_full[i]);
+        if (issue) umma_commit(&sm.s_full[j & 1]);
+        __syncwarp();
       };
-      if (nb > 0) {
-        wait_keys();
-        if (ok) {
-          tc_fence_after();
-          const bool issue = elect_one();
-          if (nb0 > 0) scores(0, issue);
-          if (nb1 > 0) scores(1, issue);
-          __syncwarp();
-        }
-      }
+      for (int j = 0; j < 2 && j < nb && ok; ++j) scores(j);
       for (int j = 0; j < nb && ok; ++j) {
+        Ring<S::kValueSlots> v = vring;
 #pragma unroll
-        for (int h = 0; h < 2; ++h, vwait.next()) ok = ok && warp_wait(&sm.v_full[vwait.at], vwait.phase, abort_flag, a.status);
-        if (j >= diagonal) ok = ok && warp_wait(&sm.v_clear[j - diagonal], 0, abort_flag, a.status);
+        for (int h = 0; h < 2; ++h, v.next()) {
+          ok = ok && warp_wait(&sm.v_full[v.at], v.phase, abort_flag, a.status);
+          if (j >= diagonal) ok = ok && warp_wait(&sm.v_clear[2 * (j - diagonal) + h], 0, abort_flag, a.status);
+        }
+        ok = ok && warp_wait(&sm.p_full[j & 1], (j / 2) & 1, abort_flag, a.status);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t p = tmem + kTmemS + (j & 1) * 128, to = tmem + kTmemO;
+        const bool issue = elect_one();
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          if (j >= (i ? nb1 : nb0)) continue;
-          ok = ok && warp_wait(&sm.p_full[i], j & 1, abort_flag, a.status);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t p = tmem + kTmemS + i * 128, to = tmem + kTmemO + i * 128;
-          const bool issue = elect_one();
+        for (int h = 0; h < 2; ++h, vring.next()) {
+          const uint32_t v0 = vd + vring.at * (VC * kHalf * 128 >> 4);
+          if (issue) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h, vring[i].next()) {
-            const uint32_t v0 = vd + vring[i].at * (VC * kHalf * 128 >> 4);
-            if (issue) {
-#pragma unroll
-              for (int s = 0; s < 4; ++s) mma_ts(to, p + h * 64 + s * 8, v0 + s * (2048 >> 4), hi, idesc_o, j > 0 || h > 0 || s > 0);
-              if (i == last) umma_commit(&sm.v_empty[vring[i].at]);
-            }
+            for (int s = 0; s < 4; ++s) mma_ts(to, p + h * 64 + s * 8, v0 + s * (2048 >> 4), hi, idesc_o, j > 0 || h > 0 || s > 0);
+            umma_commit(&sm.v_empty[vring.at]);
           }
-          if (issue) umma_commit(&sm.pv_done[i]);
-          __syncwarp();
         }
-        if (j + 1 < nb && ok) {
-          wait_keys();
-          if (!ok) break;
-          tc_fence_after();
-          const bool issue = elect_one();
-          if (j + 1 < nb0) scores(0, issue);
-          if (j + 1 < nb1) scores(1, issue);
-          __syncwarp();
-        }
+        if (issue) umma_commit(&sm.pv_done[j & 1]);
+        __syncwarp();
+        if (j + 2 < nb) scores(j + 2);
       }
       if (elect_one()) {
         umma_commit(&sm.cleanup);
@@ -362,17 +352,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
     } else if (warp >= 4) {
       // =========================== softmax ===========================
-      const int i = (warp - 4) / 8, half = (warp - 4) / 4 % 2, mine = i ? nb1 : nb0;
-      const int t = (warp % 4) * 32 + lane, pos = q0 + i * 128 + t;
+      const int half = (warp - 4) / 4, bar = 1;
+      const int t = (warp % 4) * 32 + lane, pos = q0 + t;
       const uint32_t lanes = static_cast<uint32_t>((warp % 4) * 32) << 16;
-      const uint32_t s_at = tmem + lanes + kTmemS + i * 128 + half * kHalf, o_at = tmem + lanes + kTmemO + i * 128 + half * (D / 2);
+      const uint32_t o_at = tmem + lanes + kTmemO + half * (D / 2);
       const int64_t lim = r.keys - r.n + pos;      // last key that the row sees
       const float scale = a.scale_log2;
-      const int bar = 1 + i;
       float ref = kNone, l = 0.f;                  // the row's reference; the sum of this half
       bool ok = true;
-      for (int j = 0; j < mine; ++j) {
-        bool fail = !warp_wait(&sm.s_full[i], j & 1, abort_flag, a.status);
+      for (int j = 0; j < nb; ++j) {
+        const uint32_t s_at = tmem + lanes + kTmemS + (j & 1) * 128 + half * kHalf;
+        bool fail = !warp_wait(&sm.s_full[j & 1], (j / 2) & 1, abort_flag, a.status);
         const int64_t left = lim - static_cast<int64_t>(j) * kBlock - half * kHalf;
         const int last = left >= kHalf - 1 ? kHalf : static_cast<int>(max(left, static_cast<int64_t>(-1)));      // last key seen of this half
         uint32_t w[32];
@@ -411,24 +401,25 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           return (high & 0xFFFFu) > kHigh || high >> 16 > kHigh;
         };
-        bool high = false;
-        if (!fail) {
-          tc_fence_after();
-          high = weights(false);
+        tc_fence_after();
+        bool redo = j == 0;      // no row has a reference yet
+        if (!redo) {
+          const bool high = !fail && weights(false);
+          redo = cosa::named_bar_red_or(bar, 256, high || fail);
         }
-        if (cosa::named_bar_red_or(bar, 256, high || fail)) {
+        if (redo) {
           if (cosa::named_bar_red_or(bar, 256, fail)) { ok = false; break; }
           // some weight is far above its row's reference (or NaN): the rows' maxima over the block, and the weights again
           weights(true);
-          sm.part[i][half][t] = top;
+          sm.part[half][t] = top;
           cosa::named_bar_sync(bar, 256);
-          top = fmaxf(top, sm.part[i][half ^ 1][t]);
+          top = fmaxf(top, sm.part[half ^ 1][t]);
           const float now = top == -INFINITY ? ref : fmaxf(ref, top * scale), alpha = now == ref ? 1.f : cosa::ex2_approx(ref - now);
           ref = now;
           l *= alpha;
           weights(false);
           if (j > 0) {
-            fail = !warp_wait(&sm.pv_done[i], (j - 1) & 1, abort_flag, a.status);
+            fail = !warp_wait(&sm.pv_done[(j - 1) & 1], ((j - 1) / 2) & 1, abort_flag, a.status);
             if (!fail) {
               tc_fence_after();
 #pragma unroll 1
@@ -450,27 +441,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         cosa::tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.p_full[i]);
+        if (lane == 0) mbar_arrive(&sm.p_full[j & 1]);
       }
       if (ok) {
         bool fail = false;
-        if (mine > 0) fail = !warp_wait(&sm.pv_done[i], (mine - 1) & 1, abort_flag, a.status);
-        sm.part[i][half][t] = l;
+        if (nb > 0) fail = !warp_wait(&sm.pv_done[(nb - 1) & 1], ((nb - 1) / 2) & 1, abort_flag, a.status);
+        sm.part[half][t] = l;
         ok = !cosa::named_bar_red_or(bar, 256, fail);
       }
       if (ok) {
         tc_fence_after();
-        l += sm.part[i][half ^ 1][t];
+        l += sm.part[half ^ 1][t];
         const float inv = l == 0.f ? 0.f : 1.f / l;
         const int64_t row = static_cast<int64_t>(r.tok0 + pos) * a.num_heads + head;
         const bool live = pos < r.n;
         if (live && a.lse && half == 0) a.lse[row] = l == 0.f ? -INFINITY : (ref + log2f(l)) * kLn2;
-        const bool odd_values = mine > 0 && *reinterpret_cast<volatile int*>(&sm.odd_values);
+        const bool odd_values = nb > 0 && *reinterpret_cast<volatile int*>(&sm.odd_values);
 #pragma unroll
         for (int c = 0; c < D / 2; c += 16) {
           uint32_t o[16];
           __syncwarp();
-          if (mine > 0) {
+          if (nb > 0) {
             cosa::tmem_ld16(o_at + c, o);
             cosa::tmem_wait_ld();
           } else {
@@ -546,8 +537,8 @@ cudaError_t launch_shape(const PrefillLaunch& L, cudaStream_t stream) {
     const uint64_t strides[3] = {static_cast<uint64_t>(t[i].stride) * 2, 128, static_cast<uint64_t>(t[i].head_stride) * 2};
     if (!encode_bf16(&maps[i], t[i].base, dims, strides, box)) return cudaErrorInvalidValue;
   }
-  const size_t smem = sizeof(Smem<S>);
-  static_assert(sizeof(Smem<S>) <= 227 * 1024, "shared memory");
+  const size_t smem = sizeof(Smem<S>) + 1024;
+  static_assert(sizeof(Smem<S>) + 1024 <= 227 * 1024, "shared memory");
   auto* kernel = prefill_kernel<S>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
