@@ -60,8 +60,15 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
   return __all_sync(kAll, cosa::wait_parity_bounded(bar, parity, abort_flag, status));
 }
 
-__device__ __forceinline__ bool odd(uint32_t two) {        // either bf16 is not finite
-  return (two & 0x7F80u) == 0x7F80u || (two & 0x7F800000u) == 0x7F800000u;
+// Of eight bf16 values: nonzero if one is not finite (its exponent, all ones, carries into the sign's place), and zeros for those.
+__device__ __forceinline__ uint32_t odd(const uint4& x) {
+  constexpr uint32_t kExp = 0x7F807F80u, kOne = 0x00800080u;
+  return (((x.x & kExp) + kOne) | ((x.y & kExp) + kOne) | ((x.z & kExp) + kOne) | ((x.w & kExp) + kOne)) & 0x80008000u;
 }
+__device__ __forceinline__ uint32_t finite(uint32_t two) {
+  const uint32_t bad = (((two & 0x7F807F80u) + 0x00800080u) & 0x80008000u) >> 15;      // 1 in the half that is not
+  return two & ~(bad * 0xFFFFu);
+}
+__device__ __forceinline__ uint4 finite(const uint4& x) { return make_uint4(finite(x.x), finite(x.y), finite(x.z), finite(x.w)); }
 
 }  // namespace cosa_attn

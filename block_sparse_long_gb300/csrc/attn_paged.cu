@@ -589,16 +589,10 @@ __global__ void __launch_bounds__(S::kThreads, 1)
           for (int e = tail0 * 16 + lane; e < tail1 * 16; e += 32) {      // 16-byte pieces of the new tokens' values
             if ((e & 15) < 8 * kFirst) continue;
             uint4* at = reinterpret_cast<uint4*>(values + (e & 15) / 8 * kColumn + (e >> 4) * 128 + (e & 7) * 16);
-            uint4 x = *at;
-            if (odd(x.x) || odd(x.y) || odd(x.z) || odd(x.w)) {
+            const uint4 x = *at;
+            if (odd(x)) {
               found = true;
-              uint32_t* w = reinterpret_cast<uint32_t*>(&x);
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                if ((w[i] & 0x7F80u) == 0x7F80u) w[i] &= 0xFFFF0000u;
-                if ((w[i] & 0x7F800000u) == 0x7F800000u) w[i] &= 0xFFFFu;
-              }
-              *at = x;
+              *at = finite(x);
             }
           }
           fence_proxy_async_smem();

@@ -47,7 +47,7 @@ constexpr int kThreads = 384;
 constexpr int kBlock = 128;                // keys
 constexpr int kRows = 128;                 // queries of a CTA
 constexpr int kColumn = kBlock * 128;      // bytes of a 64-value wide column of 128 rows
-constexpr int kHalf = kBlock / 2;          // keys of a thread's half row, and of a slot of values
+constexpr int kHalf = kBlock / 2;          // keys of a thread's half row
 constexpr float kNone = -3e38f;            // reference of a row that has seen nothing
 constexpr uint32_t kHigh = 0x4380;         // 2^8 in bf16
 constexpr float kLn2 = 0.69314718055994531f;
@@ -57,16 +57,16 @@ template <int D_>
 struct Shape {
   static constexpr int D = D_;
   static constexpr int kKeyColumns = D / 64 + 1, kValueColumns = D / 64;
-  static constexpr int kKeySlots = 6, kValueSlots = D == 128 ? 4 : 6;      // of one column of 128 keys; of 64 keys' values
+  static constexpr int kSlots = D == 128 ? 2 : 3;      // blocks of keys, and of values
 };
 
 template <class S>
 struct alignas(1024) Smem {
   uint8_t q[S::kKeyColumns][kColumn];
-  uint8_t k[S::kKeySlots][kColumn];
-  uint8_t v[S::kValueSlots][S::kValueColumns][kHalf * 128];
-  uint64_t q_full, k_full[S::kKeySlots], k_empty[S::kKeySlots], v_full[S::kValueSlots], v_empty[S::kValueSlots];
-  uint64_t v_sent[4], v_clear[4];          // halves of the blocks on the diagonal: copy issued, values finite
+  uint8_t k[S::kSlots][S::kKeyColumns][kColumn];
+  uint8_t v[S::kSlots][S::kValueColumns][kColumn];
+  uint64_t q_full, k_full[S::kSlots], k_empty[S::kSlots], v_full[S::kSlots], v_empty[S::kSlots];
+  uint64_t v_sent[2], v_clear[2];          // of the blocks on the diagonal: copy issued, values finite
   uint64_t s_full[2], p_full[2], pv_done[2], cleanup;      // by block, even and odd: a parity tells two phases apart
   float part[2][128];                      // of a row's halves: maxima, sums
   int32_t req, block;                      // this CTA's request (-1: none) and its block of queries
@@ -149,19 +149,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 1 && lane == 0) {
     mbar_init(&sm.q_full, 1);
-    for (int s = 0; s < S::kKeySlots; ++s) {
+    for (int s = 0; s < S::kSlots; ++s) {
       mbar_init(&sm.k_full[s], 1);
       mbar_init(&sm.k_empty[s], 1);
-    }
-    for (int s = 0; s < S::kValueSlots; ++s) {
       mbar_init(&sm.v_full[s], 1);
       mbar_init(&sm.v_empty[s], 1);
     }
-    for (int s = 0; s < 4; ++s) {
+    for (int s = 0; s < 2; ++s) {
       mbar_init(&sm.v_sent[s], 1);
       mbar_init(&sm.v_clear[s], 2);
-    }
-    for (int s = 0; s < 2; ++s) {
       mbar_init(&sm.s_full[s], 1);
       mbar_init(&sm.p_full[s], 8);
       mbar_init(&sm.pv_done[s], 1);
@@ -190,44 +186,37 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 0) {
       // =========================== copies ===========================
       const int tok = r.tok0 + q0, key = static_cast<int>(r.from);
-      Ring<S::kKeySlots> kring;
-      Ring<S::kValueSlots> vring;
-      int columns = 0, values = 0;            // slots taken, up to the rings' sizes
+      Ring<S::kSlots> kring, vring;
+      int keys = 0, values = 0;               // slots taken, up to the rings' sizes
       bool ok = !a.stall && nb > 0;
       if (ok && lane == 0) {
-        cosa::tma_prefetch_desc(&kmap);
-        cosa::tma_prefetch_desc(&vmap);
         mbar_arrive_expect_tx(&sm.q_full, KC * kColumn);
         for (int c = 0; c < VC; ++c) cosa::tma_load_4d(sm.q[c], &qmap, &sm.q_full, 0, tok, c, head);
         cosa::tma_load_4d(sm.q[VC], &qrmap, &sm.q_full, 0, tok, 0, head);
       }
-      for (int j = 0; j < nb && ok; ++j) {
-        for (int c = 0; c < KC && ok; ++c, kring.next()) {
-          if (columns == S::kKeySlots) ok = warp_wait(&sm.k_empty[kring.at], kring.phase ^ 1, abort_flag, a.status);
-          else ++columns;
-          if (!ok) break;
-          if (lane == 0) {
-            mbar_arrive_expect_tx(&sm.k_full[kring.at], kColumn);
-            if (c < VC) cosa::tma_load_4d(sm.k[kring.at], &kmap, &sm.k_full[kring.at], 0, key + j * kBlock, c, head);
-            else cosa::tma_load_4d(sm.k[kring.at], &krmap, &sm.k_full[kring.at], 0, key + j * kBlock, 0, 0);
-          }
+      for (int j = 0; j < nb && ok; ++j, kring.next(), vring.next()) {
+        if (keys == S::kSlots) ok = warp_wait(&sm.k_empty[kring.at], kring.phase ^ 1, abort_flag, a.status);
+        else ++keys;
+        if (!ok) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&sm.k_full[kring.at], KC * kColumn);
+          for (int c = 0; c < VC; ++c) cosa::tma_load_4d(sm.k[kring.at][c], &kmap, &sm.k_full[kring.at], 0, key + j * kBlock, c, head);
+          cosa::tma_load_4d(sm.k[kring.at][VC], &krmap, &sm.k_full[kring.at], 0, key + j * kBlock, 0, 0);
         }
-        for (int h = 0; h < 2 && ok; ++h, vring.next()) {
-          if (values == S::kValueSlots) ok = warp_wait(&sm.v_empty[vring.at], vring.phase ^ 1, abort_flag, a.status);
-          else ++values;
-          if (!ok) break;
-          if (lane == 0) {
-            mbar_arrive_expect_tx(&sm.v_full[vring.at], VC * kHalf * 128);
-            for (int c = 0; c < VC; ++c)
-              cosa::tma_load_4d(sm.v[vring.at][c], &vmap, &sm.v_full[vring.at], 0, key + j * kBlock + h * kHalf, c, head);
-            if (j >= diagonal) mbar_arrive(&sm.v_sent[2 * (j - diagonal) + h]);
-          }
+        if (values == S::kSlots) ok = warp_wait(&sm.v_empty[vring.at], vring.phase ^ 1, abort_flag, a.status);
+        else ++values;
+        if (!ok) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&sm.v_full[vring.at], VC * kColumn);
+          for (int c = 0; c < VC; ++c) cosa::tma_load_4d(sm.v[vring.at][c], &vmap, &sm.v_full[vring.at], 0, key + j * kBlock, c, head);
+          if (j >= diagonal) mbar_arrive(&sm.v_sent[j - diagonal]);
         }
       }
       // every copy lands before the CTA ends: the last use of each slot
       if (lane == 0 && !a.stall && nb > 0) {
         wait_parity_bounded(&sm.q_full, 0, nullptr, nullptr);
-        for (; columns > 0; --columns) {
+        if (keys > values) kring.next();      // (the values of the last block had no place)
+        for (; keys > 0; --keys) {
           kring.back();
           wait_parity_bounded(&sm.k_full[kring.at], kring.phase, nullptr, nullptr);
         }
@@ -241,107 +230,80 @@ __global__ void __launch_bounds__(kThreads, 1)
       // =========================== values on the diagonal ===========================
       // What no row may multiply by 0: keys behind the request's, and what is not finite among those that some row does not see.  A
       // slot's barrier is waited for once its copy has been issued, so that its phase is the one meant.
-      bool ok = true;
-      for (int j = diagonal; j < nb && ok; ++j) {
+      const int tid = (warp - 2) * 32 + lane;
+      for (int j = diagonal; j < nb; ++j) {
+        const int s = j % S::kSlots;
+        if (!warp_wait(&sm.v_sent[j - diagonal], 0, abort_flag, a.status) ||
+            !warp_wait(&sm.v_full[s], (j / S::kSlots) & 1, abort_flag, a.status))
+          break;
         const int64_t k0 = static_cast<int64_t>(j) * kBlock;
+        const int first = static_cast<int>(max(lim0 + 1 - k0, static_cast<int64_t>(0)));      // rows of the block
+        const int end = static_cast<int>(min(r.keys - k0, static_cast<int64_t>(kBlock)));
+        uint32_t found = 0;
+        constexpr int kBatch = 8, kPieces = VC * 8;      // 16-byte pieces of a row
+        auto at = [&](int e) { return reinterpret_cast<uint4*>(&sm.v[s][e % kPieces / 8][e / kPieces * 128 + (e & 7) * 16]); };
+        for (int e = max(first, end) * kPieces + tid; e < kBlock * kPieces; e += 64) *at(e) = make_uint4(0, 0, 0, 0);
 #pragma unroll 1
-        for (int h = 0; h < 2 && ok; ++h) {
-          const int use = 2 * j + h, s = use % S::kValueSlots;
-          ok = warp_wait(&sm.v_sent[2 * (j - diagonal) + h], 0, abort_flag, a.status) &&
-               warp_wait(&sm.v_full[s], (use / S::kValueSlots) & 1, abort_flag, a.status);
-          if (!ok) break;
-          const int first = static_cast<int>(max(lim0 + 1 - k0 - h * kHalf, static_cast<int64_t>(0)));      // row of the half
-          const int64_t behind = r.keys - k0 - h * kHalf;
-          bool found = false;
-          constexpr int kBatch = 8, kRowPieces = VC * 8;
-#pragma unroll 1
-          for (int e0 = first * kRowPieces + (warp - 2) * 32 + lane; e0 < kHalf * kRowPieces; e0 += 64 * kBatch) {
-            uint4 x[kBatch];
-            auto at = [&](int k) {
-              const int e = e0 + 64 * k, row = e / kRowPieces, c = e % kRowPieces;
-              return reinterpret_cast<uint4*>(&sm.v[s][c / 8][row * 128 + (c & 7) * 16]);
-            };
+        for (int e0 = first * kPieces + tid; e0 < end * kPieces; e0 += 64 * kBatch) {
+          uint4 x[kBatch];
+          uint32_t bad = 0;
+#pragma unroll
+          for (int k = 0; k < kBatch; ++k) x[k] = e0 + 64 * k < end * kPieces ? *at(e0 + 64 * k) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+          for (int k = 0; k < kBatch; ++k) bad |= odd(x[k]);
+          found |= bad;
+          if (bad) {
 #pragma unroll
             for (int k = 0; k < kBatch; ++k)
-              if (e0 + 64 * k < kHalf * kRowPieces) x[k] = *at(k);
-#pragma unroll
-            for (int k = 0; k < kBatch; ++k) {
-              if (e0 + 64 * k >= kHalf * kRowPieces) continue;
-              if ((e0 + 64 * k) / kRowPieces >= behind) {
-                *at(k) = make_uint4(0, 0, 0, 0);
-              } else if (odd(x[k].x) || odd(x[k].y) || odd(x[k].z) || odd(x[k].w)) {
-                found = true;
-                uint32_t* w = reinterpret_cast<uint32_t*>(&x[k]);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  if ((w[i] & 0x7F80u) == 0x7F80u) w[i] &= 0xFFFF0000u;
-                  if ((w[i] & 0x7F800000u) == 0x7F800000u) w[i] &= 0xFFFFu;
-                }
-                *at(k) = x[k];
-              }
-            }
+              if (e0 + 64 * k < end * kPieces) *at(e0 + 64 * k) = finite(x[k]);
           }
-          cosa::fence_proxy_async_smem();
-          found = __any_sync(kAll, found);
-          if (lane == 0) {
-            if (found) sm.odd_values = 1;
-            mbar_arrive(&sm.v_clear[2 * (j - diagonal) + h]);
-          }
-          __syncwarp();
         }
+        cosa::fence_proxy_async_smem();
+        const bool any = __any_sync(kAll, found != 0);
+        if (lane == 0) {
+          if (any) sm.odd_values = 1;
+          mbar_arrive(&sm.v_clear[j - diagonal]);
+        }
+        __syncwarp();
       }
     } else if (warp == 1) {
       // =========================== products ===========================
       constexpr uint32_t idesc_s = cosa::idesc_bf16_f32(128, kBlock, false, false), idesc_o = cosa::idesc_bf16_f32(128, D, false, true);
       constexpr uint32_t hi = desc_hi(1024, 2);
-      const uint32_t qd = desc_lo(smem_u32(sm.q), 16), kd = desc_lo(smem_u32(sm.k), 16), vd = desc_lo(smem_u32(sm.v), kHalf * 128);
-      Ring<S::kKeySlots> kring;
-      Ring<S::kValueSlots> vring;
+      const uint32_t qd = desc_lo(smem_u32(sm.q), 16), kd = desc_lo(smem_u32(sm.k), 16), vd = desc_lo(smem_u32(sm.v), kColumn);
+      Ring<S::kSlots> kring, vring;
       bool ok = nb == 0 || warp_wait(&sm.q_full, 0, abort_flag, a.status);
       auto scores = [&](int j) {
-        // all waits before the products: between them they would leave gaps
-        Ring<S::kKeySlots> k = kring;
-#pragma unroll
-        for (int c = 0; c < KC; ++c, k.next()) ok = ok && warp_wait(&sm.k_full[k.at], k.phase, abort_flag, a.status);
+        ok = ok && warp_wait(&sm.k_full[kring.at], kring.phase, abort_flag, a.status);
         if (!ok) return;
         tc_fence_after();
-        const uint32_t to = tmem + kTmemS + (j & 1) * 128;
-        const bool issue = elect_one();
+        const uint32_t to = tmem + kTmemS + (j & 1) * 128, k0 = kd + kring.at * (KC * kColumn >> 4);
+        if (elect_one()) {
 #pragma unroll
-        for (int c = 0; c < KC; ++c, kring.next()) {
-          const uint32_t q0 = qd + c * (kColumn >> 4), k0 = kd + kring.at * (kColumn >> 4);
-          if (issue) {
-#pragma unroll
-            for (int s = 0; s < 4; ++s) mma_ss(to, q0 + 2 * s, hi, k0 + 2 * s, hi, idesc_s, c > 0 || s > 0);
-            umma_commit(&sm.k_empty[kring.at]);
+          for (int s = 0; s < KC * 4; ++s) {
+            const int at = (s / 4) * (kColumn >> 4) + (s % 4) * 2;
+            mma_ss(to, qd + at, hi, k0 + at, hi, idesc_s, s > 0);
           }
+          umma_commit(&sm.k_empty[kring.at]);
+          umma_commit(&sm.s_full[j & 1]);
         }
-        if (issue) umma_commit(&sm.s_full[j & 1]);
         __syncwarp();
+        kring.next();
       };
       for (int j = 0; j < 2 && j < nb && ok; ++j) scores(j);
-      for (int j = 0; j < nb && ok; ++j) {
-        Ring<S::kValueSlots> v = vring;
-#pragma unroll
-        for (int h = 0; h < 2; ++h, v.next()) {
-          ok = ok && warp_wait(&sm.v_full[v.at], v.phase, abort_flag, a.status);
-          if (j >= diagonal) ok = ok && warp_wait(&sm.v_clear[2 * (j - diagonal) + h], 0, abort_flag, a.status);
-        }
+      for (int j = 0; j < nb && ok; ++j, vring.next()) {
+        ok = warp_wait(&sm.v_full[vring.at], vring.phase, abort_flag, a.status);
+        if (j >= diagonal) ok = ok && warp_wait(&sm.v_clear[j - diagonal], 0, abort_flag, a.status);
         ok = ok && warp_wait(&sm.p_full[j & 1], (j / 2) & 1, abort_flag, a.status);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t p = tmem + kTmemS + (j & 1) * 128, to = tmem + kTmemO;
-        const bool issue = elect_one();
+        const uint32_t p = tmem + kTmemS + (j & 1) * 128, v0 = vd + vring.at * (VC * kColumn >> 4);
+        if (elect_one()) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h, vring.next()) {
-          const uint32_t v0 = vd + vring.at * (VC * kHalf * 128 >> 4);
-          if (issue) {
-#pragma unroll
-            for (int s = 0; s < 4; ++s) mma_ts(to, p + h * 64 + s * 8, v0 + s * (2048 >> 4), hi, idesc_o, j > 0 || h > 0 || s > 0);
-            umma_commit(&sm.v_empty[vring.at]);
-          }
+          for (int s = 0; s < 8; ++s) mma_ts(tmem + kTmemO, p + s / 4 * 64 + s % 4 * 8, v0 + s * (2048 >> 4), hi, idesc_o, j > 0 || s > 0);
+          umma_commit(&sm.v_empty[vring.at]);
+          umma_commit(&sm.pv_done[j & 1]);
         }
-        if (issue) umma_commit(&sm.pv_done[j & 1]);
         __syncwarp();
         if (j + 2 < nb) scores(j + 2);
       }
@@ -531,8 +493,8 @@ cudaError_t launch_shape(const PrefillLaunch& L, cudaStream_t stream) {
             {L.k, L.total_kv_tokens, D, L.num_heads, L.k_stride, L.k_head_stride},
             {L.k_rope, L.total_kv_tokens, 64, 1, L.k_rope_stride, 64},
             {L.v, L.total_kv_tokens, D, L.num_heads, L.v_stride, L.v_head_stride}};
+  const uint32_t box[4] = {64, 128, 1, 1};
   for (int i = 0; i < 5; ++i) {
-    const uint32_t box[4] = {64, i == 4 ? uint32_t{kHalf} : 128u, 1, 1};
     const uint64_t dims[4] = {64, static_cast<uint64_t>(t[i].tokens), static_cast<uint64_t>(t[i].width / 64), static_cast<uint64_t>(t[i].heads)};
     const uint64_t strides[3] = {static_cast<uint64_t>(t[i].stride) * 2, 128, static_cast<uint64_t>(t[i].head_stride) * 2};
     if (!encode_bf16(&maps[i], t[i].base, dims, strides, box)) return cudaErrorInvalidValue;
