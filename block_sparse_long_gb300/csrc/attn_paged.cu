@@ -57,6 +57,7 @@ constexpr int kColumn = kTile * 128;       // bytes of a 64-value wide column of
 constexpr int kPair = 2 * kColumn;
 constexpr float kNone = -3e38f;            // reference of a row that has seen nothing
 constexpr float kHigh = 8.0f;              // log2 of the weight from which on a row's reference moves
+constexpr uint32_t kHighBits = 0x4380;     // the weight, 2^8, in bf16
 constexpr float kLn2 = 0.69314718055994531f;
 
 // DK, DV: values of a key and a value.  kLatent: the value is the key's first DV values.  N: query rows of a row tile.
@@ -64,8 +65,9 @@ template <int DK_, int DV_, bool LATENT, int N_>
 struct Shape {
   static constexpr int DK = DK_, DV = DV_, N = N_;
   static constexpr bool kLatent = LATENT;
+  static constexpr bool kRowLanes = N == 128;                    // a query row per TMEM lane: S = Q K^T, O = P V, P in TMEM
   static constexpr int kGroups = N == 16 ? 1 : N == 32 ? 2 : 4;  // warpgroups of the softmax
-  static constexpr int NC = N / kGroups;                         // query rows of a softmax thread
+  static constexpr int NC = kRowLanes ? 1 : 16;                  // query rows of a softmax thread
   static constexpr int kThreads = 128 + 128 * kGroups;
   static constexpr int kBlocks = DV > 128 ? DV / 128 : 1;        // of 128 output values
   static constexpr int kPairs = LATENT ? DV / 128 : DK == 128 ? 2 : 1;      // ring slots of a tile; 64 + 64: K and V in one
@@ -73,10 +75,11 @@ struct Shape {
   static constexpr int kPBytes = N * kTile * 2;
   // The widest latent rows leave no room for P: it goes over the rotated part of the keys, which S^T has used by then.
   static constexpr bool kAlias = LATENT && DV == 512 && N == 64;
-  static constexpr int kPBufs = kAlias ? 0 : (LATENT && DV == 512 && N == 32) || N == 128 ? 1 : 2;
+  static constexpr int kPBufs = kAlias || (LATENT && DV == 512 && N == 32) ? 1 : 2;
+  static constexpr int kPSmem = kAlias || kRowLanes ? 0 : kPBufs;    // of them in shared memory, in their own place
   static constexpr int kRopes = LATENT && DV + N <= 528 ? 2 : 1;      // (1, unused, without latent vectors)
   static constexpr int kSmall = 2048 + N * (56 + 8 * kMaxCluster);
-  static constexpr int kRoom = 227 * 1024 - 1024 - kSmall - kQBytes - kPBufs * kPBytes - (LATENT ? kRopes * kColumn : 1024);
+  static constexpr int kRoom = 227 * 1024 - 1024 - kSmall - kQBytes - kPSmem * kPBytes - (LATENT ? kRopes * kColumn : 1024);
   // Keys and values in slots of their own are waited for by different warps, and a parity wait tells only two phases apart: an even
   // number of slots has either keys or values in a slot, so that each barrier's phases are waited for by one warp, in order.
   static constexpr int kFit = kRoom / kPair < 6 ? kRoom / kPair : 6;
@@ -85,8 +88,8 @@ struct Shape {
   // A tile's place: one slot (of a pair, for kSplit: an even one for keys and the odd one behind it for values), kLatent: several.
   static constexpr int kRing = kSplit ? kSlots / 2 : kSlots, kStep = kSplit ? 2 : 1;
   static_assert(kSlots >= kPairs, "a tile fits the ring");
-  static constexpr uint32_t kTmemO = 0, kTmemS = kBlocks * N;
-  static_assert(kTmemS + 2 * N <= 512, "TMEM columns");
+  static constexpr uint32_t kTmemO = 0, kTmemS = kRowLanes ? DV : kBlocks * N, kTmemP = kTmemS + 2 * N;
+  static_assert(kTmemP + (kRowLanes ? kPBufs * kTile / 2 : 0) <= 512, "TMEM columns");
   // P^T: rows of 32, 64 or 128 bytes per slot, swizzled at that width
   static constexpr int kPRow = N >= 64 ? 128 : 2 * N;
 };
@@ -256,14 +259,14 @@ struct alignas(1024) Smem {
   uint8_t ring[S::kSlots][kPair];
   uint8_t rope[S::kRopes][S::kLatent ? kColumn : 1024];
   uint8_t q[S::kQBytes];
-  uint8_t p[S::kPBufs ? S::kPBufs : 1][S::kPBufs ? S::kPBytes : 16];
+  uint8_t p[S::kPSmem ? S::kPSmem : 1][S::kPSmem ? S::kPBytes : 16];
   uint64_t full[S::kSlots], empty[S::kSlots];
   uint64_t rope_full[2], rope_empty[2];
   uint64_t q_ready, s_full[2], s_empty[2], p_full[2], pv_done[2], groups, cleanup;
   uint64_t mask[S::N];               // tree mask of a row's token
   alignas(16) float base[S::N];      // a row's reference (log2 units), negated; read four at a time
   float alpha[S::N];                 // a reference's last change
-  float part[4][S::N];               // maxima and sums of the four warps
+  float part[4][S::N];               // maxima and sums of the four warps that have a row's slots
   int32_t row[S::N];                 // output row, or -1
   int32_t node[S::N];                // token of the request
   int64_t q_at[S::N], r_at[S::N];    // its values in q and q_rope
@@ -320,16 +323,15 @@ __device__ __forceinline__ int p_offset(int t, int c) {
 template <int NC>
 __device__ __forceinline__ void load_columns(uint32_t taddr, float (&x)[NC]) {
   uint32_t r[NC];
-  if constexpr (NC == 16) {
-    cosa::tmem_ld16(taddr, r);
-  } else {
-#pragma unroll
-    for (int i = 0; i < NC; i += 32) cosa::tmem_ld32(taddr + i, *reinterpret_cast<uint32_t(*)[32]>(&r[i]));
-  }
+  if constexpr (NC == 16) cosa::tmem_ld16(taddr, r);
+  else cosa::tmem_ld32(taddr, r);
   cosa::tmem_wait_ld();
 #pragma unroll
   for (int i = 0; i < NC; ++i) x[i] = __uint_as_float(r[i]);
 }
+
+// The first n bits.
+__device__ __forceinline__ uint32_t ones(int n) { return n <= 0 ? 0 : n >= 32 ? ~0u : (1u << n) - 1; }
 
 // The largest value of a warp; NaN counts as nothing.
 __device__ __forceinline__ float warp_max(float x) {
@@ -531,9 +533,10 @@ __global__ void __launch_bounds__(S::kThreads, 1)
           const uint32_t k0 = kd + s * (kPair >> 4);
           if (elect_one()) {
 #pragma unroll
-            for (int k = 0; k < (S::DK == 64 ? 4 : 8); ++k)
-              mma_ss(d, k0 + (k / 4) * (kColumn >> 4) + (k % 4) * 2, hi, qd + (2 * i + k / 4) * (N * 128 >> 4) + (k % 4) * 2, hi, idesc,
-                     (S::kLatent && !S::kAlias) || i > 0 || k > 0);
+            for (int k = 0; k < (S::DK == 64 ? 4 : 8); ++k) {
+              const uint32_t key = k0 + (k / 4) * (kColumn >> 4) + (k % 4) * 2, query = qd + (2 * i + k / 4) * (N * 128 >> 4) + (k % 4) * 2;
+              mma_ss(d, S::kRowLanes ? query : key, hi, S::kRowLanes ? key : query, hi, idesc, (S::kLatent && !S::kAlias) || i > 0 || k > 0);
+            }
             if (S::kSplit) umma_commit(&sm.empty[s]);
           }
           __syncwarp();
@@ -552,12 +555,12 @@ __global__ void __launch_bounds__(S::kThreads, 1)
     __syncwarp();
   } else if (warp == 2) {
     // =========================== O^T += V^T P^T ===========================
-    constexpr uint32_t idesc = cosa::idesc_bf16_f32(128, N, true, true);
+    constexpr uint32_t idesc = S::kRowLanes ? cosa::idesc_bf16_f32(128, DV, false, true) : cosa::idesc_bf16_f32(128, N, true, true);
     constexpr uint32_t v_hi = desc_hi(1024, 2), p_hi = desc_hi(8 * S::kPRow, S::kPRow == 128 ? 2 : S::kPRow == 64 ? 4 : 6);
     constexpr int kFirst = S::DK == 64 ? 1 : 0;      // columns of a slot from here on are values
     const uint32_t vd = desc_lo(smem_u32(sm.ring), kColumn), pd = desc_lo(S::kAlias ? smem_u32(sm.rope) : smem_u32(sm.p), kColumn);
     Ring<S::kRing> ring;
-    Ring<S::kPBufs == 2 ? 2 : 1> pbuf;
+    Ring<S::kPBufs> pbuf;
     int tile = 0;
     bool ok = true;
     for (; ok && more; more = pieces.next(a, pc)) {
@@ -621,8 +624,13 @@ __global__ void __launch_bounds__(S::kThreads, 1)
           if (issue) {
 #pragma unroll
             for (int k = 0; k < kTile / 16; ++k)
-              if (groups >> k & 1)
-                mma_ss(tmem + S::kTmemO + m * N, v0 + k * (2048 >> 4), v_hi, p0 + k * S::kPRow, p_hi, idesc, begun || groups & ((1u << k) - 1));
+              if (groups >> k & 1) {
+                const bool add = begun || groups & ((1u << k) - 1);
+                if constexpr (S::kRowLanes)
+                  mma_ts(tmem + S::kTmemO, tmem + S::kTmemP + pbuf.at * (kTile / 2) + k * 8, v0 + kFirst * (kColumn >> 4) + k * (2048 >> 4), v_hi, idesc, add);
+                else
+                  mma_ss(tmem + S::kTmemO + m * N, v0 + k * (2048 >> 4), v_hi, p0 + k * S::kPRow, p_hi, idesc, add);
+              }
             umma_commit(&sm.empty[s]);
           }
         }
@@ -673,9 +681,13 @@ __global__ void __launch_bounds__(S::kThreads, 1)
     const int g = warp / 4 - 1, quarter = warp % 4, tid = threadIdx.x - 128;
     const int at = quarter * 32 + lane;                // TMEM lane: slot of the tile, value of an output block
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
-    const int c0 = g * NC;
     constexpr int kSoftmax = 128 * S::kGroups;
-    const int my_bar = 1 + g;
+    // The 128 threads that share rows: a group has 16 rows (a thread a slot of the tile), or, kRowLanes, the four warps of a quarter of
+    // the lanes have 32 (a thread a quarter of the slots).
+    const int my_bar = 1 + (S::kRowLanes ? quarter : g);
+    const int c0 = S::kRowLanes ? at : g * 16;         // first row
+    const bool owns = S::kRowLanes ? g == 0 : at < 16;      // of those threads, the one that a row's reference, sum and result belong to,
+    const int own = S::kRowLanes ? at : c0 + at;            // and the row
     const float scale = a.scale_log2;
     int tile = 0, meetings = 0;
     bool ok = true;
@@ -685,35 +697,55 @@ __global__ void __launch_bounds__(S::kThreads, 1)
       if (lane == 0) mbar_arrive(&sm.groups);
       return warp_wait(&sm.groups, meetings++ & 1, abort_flag, a.status);
     };
-    // What the products have left: `to(o, c, d)` for value d of each 16 rows from c on.
+    // What the products have left: `to(o, c, d)` for value d of each 16 rows from c on (kRowLanes: values d to d + 7 of row c).
     auto outputs = [&](bool odd_values, auto to) {
-      constexpr int kSkip = DV == 64 ? 64 : 0;         // lanes of a block that are keys
       const int32_t* table = a.page_table + static_cast<size_t>(pc.b) * a.max_pages_per_req;
       const int ctx = pc.r.len - pc.r.n;
+      // what was not finite among the new tokens' values, for the rows that see it: `add(v, j)` for values d on of new token j
+      auto odd_ones = [&](int d, auto add) {
+        for (int s = max(ctx, pc.t0 * kTile); s < min(pc.r.len, pc.t1 * kTile); ++s) {
+          const int phys = table[s >> a.page_shift];
+          if (phys < 0 || phys >= a.num_pages) continue;
+          const int64_t place = (static_cast<int64_t>(phys) << a.page_shift) + (s & ((1 << a.page_shift) - 1));
+          add(S::kLatent ? a.k_cache + place * S::DK + d : a.v_cache + (place * a.num_kv_heads + pc.head) * DV + d, s - ctx);
+        }
+      };
+      auto sees = [&](int c, int j) -> bool { return a.tree_mask ? sm.mask[c] >> j & 1 : j <= sm.node[c]; };
+      auto plus = [](float& o, uint16_t v) {
+        if ((v & 0x7F80) == 0x7F80) o += __uint_as_float(static_cast<uint32_t>(v) << 16);
+      };
       tc_fence_after();
+      if constexpr (S::kRowLanes) {
 #pragma unroll 1
-      for (int m = 0; m < S::kBlocks; ++m) {
-        const int d = m * 128 + at - kSkip;
-#pragma unroll
-        for (int i = 0; i < NC; i += 16) {
+        for (int d = g * (DV / 4); d < (g + 1) * (DV / 4); d += 16) {
           float o[16] = {};
           __syncwarp();
-          if (pc.t0 < pc.t1) load_columns<16>(tmem + lanes + S::kTmemO + m * N + c0 + i, o);
-          if (odd_values && d >= 0) {
-            // what was not finite among the new tokens' values, for the rows that see it
-            for (int s = max(ctx, pc.t0 * kTile); s < min(pc.r.len, pc.t1 * kTile); ++s) {
-              const int phys = table[s >> a.page_shift];
-              if (phys < 0 || phys >= a.num_pages) continue;
-              const int64_t place = (static_cast<int64_t>(phys) << a.page_shift) + (s & ((1 << a.page_shift) - 1));
-              const uint16_t v = S::kLatent ? a.k_cache[place * S::DK + d] : a.v_cache[(place * a.num_kv_heads + pc.head) * DV + d];
-              if ((v & 0x7F80) != 0x7F80) continue;
-              const int j = s - ctx;
+          if (pc.t0 < pc.t1) load_columns<16>(tmem + lanes + S::kTmemO + d, o);
+          if (odd_values)
+            odd_ones(d, [&](const uint16_t* v, int j) {
+              if (sees(at, j))
+#pragma unroll
+                for (int e = 0; e < 16; ++e) plus(o[e], v[e]);
+            });
+#pragma unroll
+          for (int e = 0; e < 16; e += 8) to(*reinterpret_cast<const float(*)[8]>(&o[e]), at, d + e);
+        }
+      } else {
+        constexpr int kSkip = DV == 64 ? 64 : 0;       // lanes of a block that are keys
+#pragma unroll 1
+        for (int m = 0; m < S::kBlocks; ++m) {
+          const int d = m * 128 + at - kSkip;
+          float o[16] = {};
+          __syncwarp();
+          if (pc.t0 < pc.t1) load_columns<16>(tmem + lanes + S::kTmemO + m * N + c0, o);
+          if (d < 0) continue;
+          if (odd_values)
+            odd_ones(d, [&](const uint16_t* v, int j) {
 #pragma unroll
               for (int e = 0; e < 16; ++e)
-                if (a.tree_mask ? sm.mask[c0 + i + e] >> j & 1 : j <= sm.node[c0 + i + e]) o[e] += __uint_as_float(static_cast<uint32_t>(v) << 16);
-            }
-          }
-          if (d >= 0) to(o, c0 + i, d);
+                if (sees(c0 + e, j)) plus(o[e], *v);
+            });
+          to(o, c0, d);
         }
       }
     };
@@ -754,132 +786,190 @@ __global__ void __launch_bounds__(S::kThreads, 1)
       float l[NC];                         // sums of this thread's slots
 #pragma unroll
       for (int i = 0; i < NC; ++i) l[i] = 0.f;
+      float ref = kNone;                   // kRowLanes: the row's reference (log2 units)
       for (int t = pc.t0; t < pc.t1; ++t, ++tile) {
-        const int sb = tile & 1, slot = t * kTile + at;
-        bool there = slot < r.len;
-        if (there) {
-          const int phys = __ldg(table + (slot >> a.page_shift));
-          there = phys >= 0 && phys < a.num_pages;
+        const int sb = tile & 1;
+        // what the thread's slots are: one, or 32 with a bit each for those that the row sees
+        const int slot = t * kTile + (S::kRowLanes ? g * 32 : at);
+        bool there = false;
+        uint32_t seen = 0;
+        if constexpr (S::kRowLanes) {
+          const int part = slot + lane * 16;      // (pages are whole groups of 16 slots)
+          bool page = lane < 2 && part < r.len;
+          if (page) {
+            const int phys = __ldg(table + (part >> a.page_shift));
+            page = phys >= 0 && phys < a.num_pages;
+          }
+          const unsigned pages = __ballot_sync(kAll, page);
+          seen = ones(r.len - slot) & ((pages & 1 ? 0xFFFFu : 0u) | (pages & 2 ? 0xFFFF0000u : 0u));
+          const int j = slot - ctx;               // the first slot as a new token, or before them
+          if (j + 31 >= 0) {
+            uint32_t those;
+            if (a.tree_mask) those = j >= 64 ? 0u : static_cast<uint32_t>(j >= 0 ? sm.mask[at] >> j : sm.mask[at] << -j);
+            else those = ones(sm.node[at] + 1 - j);
+            seen &= those | ones(-j);
+          }
+        } else {
+          there = slot < r.len;
+          if (there) {
+            const int phys = __ldg(table + (slot >> a.page_shift));
+            there = phys >= 0 && phys < a.num_pages;
+          }
         }
         bool fail = !warp_wait(&sm.s_full[sb], (tile / 2) & 1, abort_flag, a.status);
-        // Sixteen columns at a time: with 32 the second sixteen are read from TMEM again where they are needed again, since two more
-        // sets of registers beside the sums would be spilled (5500 cycles a tile of 128 rows instead of 2000).
-        constexpr bool kKeep = NC == 16;
-        float x[16];
-        // logits of columns i on, -infinity where the row does not see the slot
-        auto logits = [&](int i) {
-          load_columns<16>(tmem + lanes + S::kTmemS + sb * N + c0 + i, x);
-          if (!there) {
+        constexpr int kHave = S::kRowLanes ? 32 : 16;
+        float x[kHave];                      // logits: the thread's row's 32 slots, or its slot's 16 rows
+        uint32_t w[16];                      // kRowLanes: weights as bf16
+        float sum = 0.f;                     // and their sum
+        // -infinity where the row does not see the slot
+        auto logits = [&] {
+          load_columns(tmem + lanes + S::kTmemS + sb * N + (S::kRowLanes ? g * 32 : c0), x);
+          if constexpr (S::kRowLanes) {
+            if (seen != ~0u) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (!(seen >> e & 1)) x[e] = -INFINITY;
+            }
+          } else if (!there) {
 #pragma unroll
             for (int e = 0; e < 16; ++e) x[e] = -INFINITY;
           } else if (slot >= ctx) {
             const int j = slot - ctx;
 #pragma unroll
             for (int e = 0; e < 16; ++e)
-              if (a.tree_mask ? !(sm.mask[c0 + i + e] >> j & 1) : j > sm.node[c0 + i + e]) x[e] = -INFINITY;
+              if (a.tree_mask ? !(sm.mask[c0 + e] >> j & 1) : j > sm.node[c0 + e]) x[e] = -INFINITY;
           }
           __syncwarp();
+        };
+        // kRowLanes: exp2(x * scale - ref); whether one is high or NaN
+        auto weights = [&] {
+          uint32_t high = 0;
+          float s4[4] = {};
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            float x0, x1;
+            cosa::fma2_bc(x0, x1, x[2 * e], x[2 * e + 1], scale, -ref);
+            const float p0 = cosa::ex2_approx(x0), p1 = cosa::ex2_approx(x1);
+            cosa::add2_acc(s4[(e & 1) * 2], s4[(e & 1) * 2 + 1], p0, p1);
+            w[e] = cosa::pack_bf16x2(p0, p1);
+            high = __vmaxu2(high, w[e]);
+          }
+          sum = (s4[0] + s4[1]) + (s4[2] + s4[3]);
+          return (high & 0xFFFFu) > kHighBits || high >> 16 > kHighBits;
         };
         bool redo = t == pc.t0;      // no row has a reference yet
         if (!fail) {
           tc_fence_after();
-          if (kKeep) logits(0);
+          logits();
         }
         if (!redo) {
           // is some logit far above its row's reference (NaN is not: it stays what it is)
-          float top = -INFINITY;
-          if (!fail) {
+          bool high = false;
+          if (fail) {
+          } else if constexpr (S::kRowLanes) {
+            high = weights();
+          } else {
+            float top = -INFINITY;
 #pragma unroll
-            for (int i = 0; i < NC; i += 16) {
-              if (!kKeep) logits(i);
-#pragma unroll
-              for (int e = 0; e < 16; e += 4) {
-                const float4 b = *reinterpret_cast<const float4*>(&sm.base[c0 + i + e]);
-                float d[4];
-                fma2(d[0], d[1], x[e], x[e + 1], scale, b.x, b.y);
-                fma2(d[2], d[3], x[e + 2], x[e + 3], scale, b.z, b.w);
-                top = fmaxf(top, fmaxf(fmaxf(d[0], d[1]), fmaxf(d[2], d[3])));
-              }
+            for (int e = 0; e < 16; e += 4) {
+              const float4 b = *reinterpret_cast<const float4*>(&sm.base[c0 + e]);
+              float d[4];
+              fma2(d[0], d[1], x[e], x[e + 1], scale, b.x, b.y);
+              fma2(d[2], d[3], x[e + 2], x[e + 3], scale, b.z, b.w);
+              top = fmaxf(top, fmaxf(fmaxf(d[0], d[1]), fmaxf(d[2], d[3])));
             }
+            high = top > kHigh;
           }
-          redo = named_bar_red_or(my_bar, 128, top > kHigh || fail);
+          redo = named_bar_red_or(my_bar, 128, high || fail);
         }
         if (redo) {
           if (named_bar_red_or(my_bar, 128, fail)) { ok = false; break; }
           // the rows' maxima over the tile become references
+          float mine = S::kRowLanes ? -INFINITY : 0.f;
+          if constexpr (S::kRowLanes) {
+            if (t > pc.t0) logits();       // (the weights were made of them: registers that live until here were spilled)
 #pragma unroll
-          for (int i = 0; i < NC; i += 16) {
-            if (!kKeep) logits(i);
-            float mine = 0.f;
+            for (int e = 0; e < 32; ++e) mine = fmaxf(mine, x[e]);
+            sm.part[g][at] = mine;
+          } else {
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
               const float top = warp_max(x[e]);
               mine = lane == e ? top : mine;
             }
-            if (lane < 16) sm.part[quarter][c0 + i + lane] = mine;
+            if (lane < 16) sm.part[quarter][c0 + lane] = mine;
           }
           named_bar_sync(my_bar, 128);
-          if (at < NC) {
-            const int c = c0 + at;
+          auto move = [&](int c, float was, float& alpha) {      // the new reference
             const float top = fmaxf(fmaxf(sm.part[0][c], sm.part[1][c]), fmaxf(sm.part[2][c], sm.part[3][c]));
-            const float was = -sm.base[c], now = top == -INFINITY ? was : fmaxf(was, top * scale);
-            sm.base[c] = -now;
-            sm.alpha[c] = now == was ? 1.f : cosa::ex2_approx(was - now);
+            const float now = top == -INFINITY ? was : fmaxf(was, top * scale);
+            alpha = now == was ? 1.f : cosa::ex2_approx(was - now);
+            return now;
+          };
+          float alpha = 1.f;               // kRowLanes: the row's
+          if constexpr (S::kRowLanes) {
+            ref = move(at, ref, alpha);
+            weights();
+          } else if (owns) {
+            sm.base[own] = -move(own, -sm.base[own], sm.alpha[own]);
           }
           named_bar_sync(my_bar, 128);
           if (t > pc.t0) {
+            if constexpr (S::kRowLanes) l[0] *= alpha;
+            else
 #pragma unroll
-            for (int i = 0; i < NC; ++i) l[i] *= sm.alpha[c0 + i];
+              for (int i = 0; i < NC; ++i) l[i] *= sm.alpha[c0 + i];
             fail = !warp_wait(&sm.pv_done[(tile - 1) & 1], ((tile - 1) / 2) & 1, abort_flag, a.status);
             if (!fail) {
               tc_fence_after();
+              constexpr int kTimes = S::kRowLanes ? DV / 4 / 16 : S::kBlocks;
 #pragma unroll 1
-              for (int m = 0; m < S::kBlocks; ++m) {
-#pragma unroll 1
-                for (int i = 0; i < NC; i += 16) {
-                  const uint32_t o = tmem + lanes + S::kTmemO + m * N + c0 + i;
-                  uint32_t v[16];
-                  cosa::tmem_ld16(o, v);
-                  cosa::tmem_wait_ld();
+              for (int m = 0; m < kTimes; ++m) {
+                const uint32_t o = tmem + lanes + S::kTmemO + (S::kRowLanes ? g * (DV / 4) + m * 16 : m * N + c0);
+                uint32_t v[16];
+                cosa::tmem_ld16(o, v);
+                cosa::tmem_wait_ld();
 #pragma unroll
-                  for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * sm.alpha[c0 + i + e]);
-                  cosa::tmem_st16(o, v);
-                }
+                for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * (S::kRowLanes ? alpha : sm.alpha[c0 + e]));
+                cosa::tmem_st16(o, v);
               }
               cosa::tmem_wait_st();
             }
           }
         }
-        // P^T's buffer is free once the product before (or before that) has read it
-        constexpr int kBack = S::kPBufs == 2 ? 2 : 1;
+        // P's buffer is free once the product before (or before that) has read it
+        constexpr int kBack = S::kPBufs;
         if (!fail && tile >= kBack)
           fail = !warp_wait(&sm.pv_done[(tile - kBack) & 1], ((tile - kBack) / 2) & 1, abort_flag, a.status);
         if (!fail) {
-          // exp2(x * scale - reference), summed, and as bf16 to P^T
-          uint8_t* p = (S::kAlias ? sm.rope[0] : sm.p[S::kPBufs == 2 ? tile & 1 : 0]) + c0 / 64 * kColumn;
-#pragma unroll
-          for (int i = 0; i < NC; i += 16) {
-            if (!kKeep) logits(i);
+          if constexpr (S::kRowLanes) {
+            l[0] += sum;
+            tc_fence_after();
+            cosa::tmem_st16(tmem + lanes + S::kTmemP + (tile & 1) * (kTile / 2) + g * 16, w);
+            cosa::tmem_wait_st();
+          } else {
+            // exp2(x * scale - reference), summed, and as bf16 to P^T
+            uint8_t* p = S::kAlias ? sm.rope[0] : sm.p[S::kPBufs == 2 ? tile & 1 : 0];
 #pragma unroll
             for (int h = 0; h < 16; h += 8) {
-              uint32_t w[4];
+              uint32_t y[4];
 #pragma unroll
               for (int e = h; e < h + 8; e += 4) {
-                const float4 b = *reinterpret_cast<const float4*>(&sm.base[c0 + i + e]);
+                const float4 b = *reinterpret_cast<const float4*>(&sm.base[c0 + e]);
                 fma2(x[e], x[e + 1], x[e], x[e + 1], scale, b.x, b.y);
                 fma2(x[e + 2], x[e + 3], x[e + 2], x[e + 3], scale, b.z, b.w);
 #pragma unroll
                 for (int k = e; k < e + 4; ++k) x[k] = cosa::ex2_approx(x[k]);
-                cosa::add2_acc(l[i + e], l[i + e + 1], x[e], x[e + 1]);
-                cosa::add2_acc(l[i + e + 2], l[i + e + 3], x[e + 2], x[e + 3]);
-                w[(e - h) / 2] = cosa::pack_bf16x2(x[e], x[e + 1]);
-                w[(e - h) / 2 + 1] = cosa::pack_bf16x2(x[e + 2], x[e + 3]);
+                cosa::add2_acc(l[e], l[e + 1], x[e], x[e + 1]);
+                cosa::add2_acc(l[e + 2], l[e + 3], x[e + 2], x[e + 3]);
+                y[(e - h) / 2] = cosa::pack_bf16x2(x[e], x[e + 1]);
+                y[(e - h) / 2 + 1] = cosa::pack_bf16x2(x[e + 2], x[e + 3]);
               }
-              *reinterpret_cast<uint4*>(p + p_offset<S::kPRow>(at, (c0 % 64 + i + h) / 8)) = make_uint4(w[0], w[1], w[2], w[3]);
+              *reinterpret_cast<uint4*>(p + p_offset<S::kPRow>(at, (c0 + h) / 8)) = make_uint4(y[0], y[1], y[2], y[3]);
             }
+            fence_proxy_async_smem();
           }
           tc_fence_before();
-          fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
             mbar_arrive(&sm.p_full[S::kPBufs == 2 ? tile & 1 : 0]);
@@ -890,7 +980,10 @@ __global__ void __launch_bounds__(S::kThreads, 1)
       }
       if (!ok) break;
       // ---------------- the piece's end ----------------
-      {
+      if constexpr (S::kRowLanes) {
+        sm.part[g][at] = l[0];
+        if (owns) sm.base[at] = -ref;
+      } else {
         float mine = 0.f;
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
@@ -906,15 +999,15 @@ __global__ void __launch_bounds__(S::kThreads, 1)
       if (named_bar_red_or(my_bar, 128, fail)) { ok = false; break; }
       if (a.cluster > 1) {
         // to every CTA of the cluster; what they hold is waited for below
-        if (at < NC) {
-          const int c = c0 + at;
+        if (owns) {
+          const int c = own;
           const float sum = (sm.part[0][c] + sm.part[1][c]) + (sm.part[2][c] + sm.part[3][c]), m = -sm.base[c];
           for (int k = 0; k < a.cluster; ++k) store_remote(&sm.ml[cta % a.cluster][c], k, make_float2(m == kNone ? -INFINITY : m, sum));
         }
         break;
       }
-      if (at < NC) {
-        const int c = c0 + at;
+      if (owns) {
+        const int c = own;
         const float sum = (sm.part[0][c] + sm.part[1][c]) + (sm.part[2][c] + sm.part[3][c]), m = -sm.base[c];
         if (pc.slot >= 0) {
           float* ml = a.part_ml + (static_cast<int64_t>(pc.slot) * N + c) * 2;
@@ -928,11 +1021,21 @@ __global__ void __launch_bounds__(S::kThreads, 1)
       named_bar_sync(my_bar, 128);
       const bool odd_values = pc.t0 < pc.t1 && *reinterpret_cast<volatile int*>(&sm.odd_values);
       if (pc.t0 < pc.t1 || pc.slot < 0)
-        outputs(odd_values, [&](const float(&o)[16], int c, int d) {
+        outputs(odd_values, [&](const auto& o, int c, int d) {
           if (pc.slot >= 0) {
             float* to = a.part_o + (static_cast<int64_t>(pc.slot) * N + c) * DV + d;
+            if constexpr (S::kRowLanes) {
+              *reinterpret_cast<float4*>(to) = make_float4(o[0], o[1], o[2], o[3]);
+              *reinterpret_cast<float4*>(to + 4) = make_float4(o[4], o[5], o[6], o[7]);
+            } else
 #pragma unroll
-            for (int e = 0; e < 16; ++e) to[e * DV] = o[e];
+              for (int e = 0; e < 16; ++e) to[e * DV] = o[e];
+          } else if constexpr (S::kRowLanes) {
+            const float f = sm.alpha[c];
+            if (sm.row[c] >= 0)
+              *reinterpret_cast<uint4*>(a.out + static_cast<int64_t>(sm.row[c]) * DV + d) =
+                  make_uint4(cosa::pack_bf16x2(o[0] * f, o[1] * f), cosa::pack_bf16x2(o[2] * f, o[3] * f), cosa::pack_bf16x2(o[4] * f, o[5] * f),
+                             cosa::pack_bf16x2(o[6] * f, o[7] * f));
           } else {
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
@@ -970,10 +1073,11 @@ __global__ void __launch_bounds__(S::kThreads, 1)
         }
         if (meet()) {
           const bool odd_values = pc.t0 < pc.t1 && *reinterpret_cast<volatile int*>(&sm.odd_values);
-          outputs(odd_values, [&](const float(&o)[16], int c, int d) {
-            const uint32_t to = remote(parts + (rank * N + c) * width + d % width, d / width);
+          outputs(odd_values, [&](const auto& o, int c, int d) {
+            const uint32_t to = remote(parts + (rank * N + c) * width + d % width, d / width);      // (8 values: of one share)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) store_remote(to + e * width * 4, o[e] * sm.alpha[c + e]);
+            for (int e = 0; e < (S::kRowLanes ? 8 : 16); ++e)
+              store_remote(to + e * (S::kRowLanes ? 1 : width) * 4, o[e] * sm.alpha[S::kRowLanes ? c : c + e]);
           });
         }
       }
