@@ -94,9 +94,9 @@ struct Shape {
   static constexpr int kPRow = N >= 64 ? 128 : 2 * N;
 };
 
-// What join_kernel has to put together: `parts` parts of an item, the first in slot `first`, the others in next, next + 2, ...
+// What join_kernel has to put together: `parts` parts of an item, the first in slot `first`, the others in next, next + step, ...
 struct Join {
-  int32_t parts, first, next, tok0, rows, head, row_tile, pad;
+  int32_t parts, first, next, step, tok0, rows, head, row_tile;
 };
 
 struct Args {
@@ -112,6 +112,7 @@ struct Args {
   int join_items;      // entries of `joins` if they are by item, 0 if by CTA
   int whole;           // items are not cut: a unit is an item
   int cluster;         // CTAs that share an item by its tiles and join it themselves (whole), or 1
+  int together;        // CTAs that walk the list as one, for as many row tiles of the same keys, or 1
   float scale_log2;
   int stall;
 };
@@ -137,14 +138,19 @@ __device__ __forceinline__ Request request_of(const Args& a, int b) {
   return r;
 }
 
-__device__ __forceinline__ int units_of(const Args& a, const Request& r) { return a.num_kv_heads * r.row_tiles * (a.whole ? 1 : r.tiles + 1); }
+// An item of the list is a (request, kv head, up to `together` row tiles).
+__device__ __forceinline__ int rounds_of(const Args& a, const Request& r) {
+  return a.together == 1 ? r.row_tiles : (r.row_tiles + a.together - 1) / a.together;
+}
+__device__ __forceinline__ int units_of(const Args& a, const Request& r) { return a.num_kv_heads * rounds_of(a, r) * (a.whole ? 1 : r.tiles + 1); }
 
-// First unit of a CTA.  With fewer units than CTAs the first ones have one each: every CTA up to the last with any has some.
-__device__ __forceinline__ int share(int total, int cta) {
-  return total < kCtas ? min(cta, total) : static_cast<int>(static_cast<uint64_t>(static_cast<uint32_t>(total)) * cta / kCtas);
+// First unit of a walker (CTA, cluster, or CTAs together).  With fewer units than walkers the first ones have one each: every one up to
+// the last with any has some.
+__device__ __forceinline__ int share(int total, int walker, int walkers) {
+  return total < walkers ? min(walker, total) : static_cast<int>(static_cast<uint64_t>(static_cast<uint32_t>(total)) * walker / walkers);
 }
 
-// What a CTA does of one item: tiles t0 .. t1 - 1.
+// What a CTA does of one item: tiles t0 .. t1 - 1 of its row tile (none if the request has fewer row tiles).
 struct Piece {
   Request r;
   int b, head, row_tile, t0, t1;
@@ -154,17 +160,17 @@ struct Piece {
   int item_end;      // behind its last unit
 };
 
-// The pieces of a CTA (of a cluster) in order; every role walks them by itself.
+// The pieces of a walker in order; every role walks them by itself.
 template <int N>
 struct Pieces {
-  int pos, first, end, before, units, items, b, cta;      // units and items before and of request b
+  int pos, first, end, before, units, items, b;      // units and items before and of request b
   Request r;
 
   __device__ __forceinline__ bool next(const Args& a, Piece& p) {
     if (pos >= end) return false;
     while (pos >= before + units) {
       before += units;
-      items += a.num_kv_heads * r.row_tiles;
+      items += a.num_kv_heads * rounds_of(a, r);
       r = request_of<N>(a, ++b);
       units = units_of(a, r);
     }
@@ -172,16 +178,18 @@ struct Pieces {
     const int u = static_cast<int>(pos - before - item * per), take = min(static_cast<int>(per) - u, end - pos);
     p.r = r;
     p.b = b;
-    p.head = r.row_tiles == 1 ? item : item / static_cast<uint32_t>(r.row_tiles);
-    p.row_tile = static_cast<int>(item) - p.head * r.row_tiles;
+    const uint32_t rounds = rounds_of(a, r);
+    p.head = rounds == 1 ? item : item / rounds;
+    p.row_tile = (static_cast<int>(item) - p.head * static_cast<int>(rounds)) * a.together + (a.together == 1 ? 0 : blockIdx.x % a.together);
     p.t0 = a.whole ? 0 : max(u - 1, 0);
     p.t1 = a.whole ? r.tiles : u + take - 1;
+    if (p.row_tile >= r.row_tiles) p.t0 = p.t1 = 0;
     if (a.cluster > 1) {
       const int rank = blockIdx.x % a.cluster;
       p.t1 = r.tiles * (rank + 1) / a.cluster;
       p.t0 = r.tiles * rank / a.cluster;
     }
-    p.slot = take == static_cast<int>(per) ? -1 : 2 * cta + (pos != first);
+    p.slot = take == static_cast<int>(per) ? -1 : 2 * static_cast<int>(blockIdx.x) + (pos != first);
     p.begins = u == 0;
     p.item = items + static_cast<int>(item);
     p.item_end = pos + static_cast<int>(per) - u;
@@ -201,7 +209,8 @@ struct Start {
 
 // By one warp, a request to a lane at a time.
 template <int N>
-__device__ __forceinline__ Start<N> find_start(const Args& a, int cta, bool report) {
+__device__ __forceinline__ Start<N> find_start(const Args& a, bool report) {
+  const int walker = blockIdx.x / (a.cluster * a.together), walkers = kCtas / a.together;
   const int lane = threadIdx.x % 32;
   Start<N> st;
   Request r{};
@@ -211,7 +220,7 @@ __device__ __forceinline__ Start<N> find_start(const Args& a, int cta, bool repo
     if (b >= a.num_reqs) return;
     r = request_of<N>(a, b);
     units = units_of(a, r);
-    items = a.num_kv_heads * r.row_tiles;
+    items = a.num_kv_heads * rounds_of(a, r);
   };
   st.total = st.items = 0;
   for (int b0 = 0; b0 < a.num_reqs; b0 += 32) {
@@ -221,9 +230,8 @@ __device__ __forceinline__ Start<N> find_start(const Args& a, int cta, bool repo
     st.items += __reduce_add_sync(kAll, items);
   }
   Pieces<N>& w = st.rest;
-  w.cta = cta;
-  w.first = w.pos = share(st.total, cta);
-  w.end = share(st.total, cta + 1);
+  w.first = w.pos = share(st.total, walker, walkers);
+  w.end = walker < walkers ? share(st.total, walker + 1, walkers) : w.pos;
   if (a.cluster > 1) w.end = min(w.end, w.pos + 1);
   w.before = w.items = w.units = 0;
   st.any = w.pos < w.end;
@@ -277,12 +285,12 @@ struct alignas(1024) Smem {
   int32_t abort_flag;
 };
 
-// The CTA that has a unit.
-__device__ __forceinline__ int owner(int total, int u) {
-  if (total < kCtas) return u;
-  int c = min(kCtas - 1, static_cast<int>(static_cast<uint64_t>(static_cast<uint32_t>(u)) * kCtas / static_cast<uint32_t>(total)));
-  while (share(total, c + 1) <= u) ++c;
-  while (share(total, c) > u) --c;
+// The walker that has a unit.
+__device__ __forceinline__ int owner(int total, int u, int walkers) {
+  if (total < walkers) return u;
+  int c = min(walkers - 1, static_cast<int>(static_cast<uint64_t>(static_cast<uint32_t>(u)) * walkers / static_cast<uint32_t>(total)));
+  while (share(total, c + 1, walkers) <= u) ++c;
+  while (share(total, c, walkers) > u) --c;
   return c;
 }
 
@@ -355,7 +363,7 @@ __global__ void __launch_bounds__(S::kThreads, 1)
   cosa_kv::let_next_start();
 
   if (warp == 0) {
-    const Start<N> st = find_start<N>(a, cta / a.cluster, cta == 0);
+    const Start<N> st = find_start<N>(a, cta == 0);
     if (lane == 0) {
       sm.start = st;
       if (cta == 0 && (a.cu_seqlens[0] != 0 || a.cu_seqlens[a.num_reqs] > a.total_tokens)) cosa::report_status(a.status, cosa::kStatusBadInput);
@@ -659,21 +667,23 @@ __global__ void __launch_bounds__(S::kThreads, 1)
         if (!pc.begins) continue;
         Join j{};
         j.parts = 1;
-        if (pc.slot >= 0) {
-          j.parts = owner(sm.start.total, pc.item_end - 1) - cta + 1;
+        if (pc.slot >= 0 && pc.row_tile < pc.r.row_tiles) {
+          j.parts = owner(sm.start.total, pc.item_end - 1, kCtas / a.together) - cta / a.together + 1;
           j.first = pc.slot;
-          j.next = 2 * (cta + 1);
+          j.next = 2 * (cta + a.together);
+          j.step = 2 * a.together;
           j.tok0 = pc.r.tok0;
           j.rows = pc.r.n * a.group;
           j.head = pc.head;
           j.row_tile = pc.row_tile;
           mine = j;
         }
-        if (pc.item < a.join_items) a.joins[pc.item] = j;
+        const int entry = pc.item * a.together + (cta - cta / a.together * a.together);
+        if (entry < a.join_items) a.joins[entry] = j;
       }
       if (!a.join_items) a.joins[cta] = mine;
       else if (cta == 0)
-        for (int i = sm.start.items; i < a.join_items; ++i) a.joins[i] = none;
+        for (int i = sm.start.items * a.together; i < a.join_items; ++i) a.joins[i] = none;
     }
     __syncwarp();
   } else {
@@ -752,6 +762,7 @@ __global__ void __launch_bounds__(S::kThreads, 1)
     for (; ok && more; more = pieces.next(a, pc)) {
       const Request& r = pc.r;
       const int rows = r.n * a.group;      // fits 32 bits: total_tokens * Hq does
+      if (pc.row_tile >= r.row_tiles) continue;
       const int row0 = pc.row_tile * N;
       if (!meet()) break;                  // the last piece is done with what follows
       if (tid < N) {
@@ -1124,12 +1135,14 @@ __global__ void __launch_bounds__(kWide ? kWideThreads : kJoinThreads) join_kern
   cosa_kv::wait_for_stream();
   const Join j = a.joins[blockIdx.x];
   // (the bounds hold whatever another call might have made of the workspace)
-  if (j.parts < 2 || j.parts > kCtas || j.first < 0 || j.first >= 2 * kCtas || j.next < 0 || j.next + 2 * (j.parts - 2) >= 2 * kCtas) return;
+  if (j.parts < 2 || j.parts > kCtas || j.first < 0 || j.first >= 2 * kCtas || j.next < 0 || j.step < 0 ||
+      j.step > 2 * kCtas || j.next + j.step * (j.parts - 2) >= 2 * kCtas)
+    return;
   const int parts = j.parts, seg = blockIdx.z;
   const int c = kWide ? blockIdx.y : blockIdx.y * 8 + warp;      // row of the tile
   const int64_t row = static_cast<int64_t>(j.row_tile) * N + c;
   if (row >= j.rows) return;                                     // (kWide: the whole block)
-  auto slot = [&](int i) { return i == 0 ? j.first : j.next + 2 * (i - 1); };
+  auto slot = [&](int i) { return i == 0 ? j.first : j.next + j.step * (i - 1); };
   const float* base = a.part_o + static_cast<int64_t>(c) * DV + seg * kSeg + lane * kVec;
   auto load = [&](int i) { return i < parts ? *reinterpret_cast<const Vec*>(base + static_cast<int64_t>(slot(i)) * N * DV) : Vec{}; };
   const int first = kWide ? warp : 0;
@@ -1204,9 +1217,17 @@ int rows_of_tile(const PagedLaunch& L) {
   return n;
 }
 
-// At most so many items: what the tokens fill and a part of a row tile for every request.
-int64_t most_items(const PagedLaunch& L) {
-  return L.num_kv_heads * (L.total_tokens * static_cast<int64_t>(L.num_q_heads / L.num_kv_heads) / rows_of_tile(L) + L.num_reqs);
+// Row tiles of the same keys that CTAs walk together, a CTA to a row tile, so that a tile of the cache is read from HBM once; the most
+// that a request has (up to 8) if the average one has more than one less, since a CTA idles through a request with fewer.
+int row_tiles_together(const PagedLaunch& L) {
+  const int64_t n = rows_of_tile(L), group = L.num_q_heads / L.num_kv_heads;
+  const int64_t most = (L.max_new_tokens * group + n - 1) / n, rounds = (most + 7) / 8;
+  return L.total_tokens * group > L.num_reqs * (most - 1) * n ? static_cast<int>((most + rounds - 1) / rounds) : 1;
+}
+
+// At most so many (request, kv head, row tile): what the tokens fill and a part of a row tile for every request, or of `together`.
+int64_t most_items(const PagedLaunch& L, int together) {
+  return L.num_kv_heads * (L.total_tokens * static_cast<int64_t>(L.num_q_heads / L.num_kv_heads) / rows_of_tile(L) + L.num_reqs * static_cast<int64_t>(together));
 }
 
 template <class S>
@@ -1225,8 +1246,7 @@ cudaError_t launch_shape(const PagedLaunch& L, cudaStream_t stream) {
   a.part_o = static_cast<float*>(L.workspace);
   a.part_ml = a.part_o + static_cast<size_t>(2 * kCtas) * S::N * S::DV;
   a.joins = reinterpret_cast<Join*>(a.part_ml + static_cast<size_t>(2 * kCtas) * S::N * 2);
-  const int64_t group = L.num_q_heads / L.num_kv_heads, items = most_items(L);
-  a.join_items = items <= kCtas ? static_cast<int>(items) : 0;
+  const int64_t group = L.num_q_heads / L.num_kv_heads, items = most_items(L, 1);
   a.status = L.status;
   a.q_stride = L.q_stride;
   a.q_head_stride = L.q_head_stride;
@@ -1274,6 +1294,9 @@ cudaError_t launch_shape(const PagedLaunch& L, cudaStream_t stream) {
       a.whole = 1;
       a.cluster = c;
     }
+  a.together = a.cluster > 1 ? 1 : row_tiles_together(L);
+  const int64_t joins = most_items(L, a.together);
+  a.join_items = joins <= kCtas ? static_cast<int>(joins) : 0;
   const unsigned ctas = static_cast<unsigned>(a.cluster > 1 ? items * a.cluster : kCtas);
   e = cosa_kv::launch_after(kernel, dim3(ctas), S::kThreads, smem, stream, a.cluster, kmap, vmap, a);
   if (e != cudaSuccess || a.whole) return e;
@@ -1297,7 +1320,7 @@ cudaError_t launch_width(const PagedLaunch& L, cudaStream_t stream) {
 
 }  // namespace
 
-bool paged_fits(const PagedLaunch& L) { return most_items(L) <= INT32_MAX / (int64_t{L.max_seqlen} / kTile + 2); }
+bool paged_fits(const PagedLaunch& L) { return most_items(L, row_tiles_together(L)) <= INT32_MAX / (int64_t{L.max_seqlen} / kTile + 2); }
 
 size_t paged_workspace_bytes(const PagedLaunch& L) {
   const size_t dv = static_cast<size_t>(L.latent_dim ? L.latent_dim : L.head_dim);

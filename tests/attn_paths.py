@@ -12,6 +12,14 @@ def row_tile(latent: int, group: int, hint: int) -> int:
     return n
 
 
+def together(p, latent: int) -> int:
+    """Row tiles of the same keys that CTAs walk together."""
+    group = p.num_q_heads // (1 if latent else p.num_kv_heads)
+    n = row_tile(latent, group, p.max_new_tokens)
+    most = -(-p.max_new_tokens * group // n)
+    return -(-most // -(-most // 8)) if p.total_tokens * group > p.num_reqs * (most - 1) * n else 1
+
+
 def path(p, latent: int) -> str:
     """'whole', 'cluster 2' to 'cluster 8', or 'list' with its join: 'by item, wide', 'by item', 'by cta'."""
     heads = 1 if latent else p.num_kv_heads
@@ -28,4 +36,5 @@ def path(p, latent: int) -> str:
             best, name = math.ceil(tiles / c) + 1, f"cluster {c}"
     if name != "list":
         return name
-    return "list, by cta" if items > CTAS else "list, by item, wide" if items <= 16 else "list, by item"
+    joins = heads * (p.total_tokens * group // n + p.num_reqs * together(p, latent))
+    return "list, by cta" if joins > CTAS else "list, by item, wide" if joins <= 16 else "list, by item"

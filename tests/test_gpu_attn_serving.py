@@ -9,7 +9,7 @@ import torch
 from block_sparse_long_gb300 import attn as C, kv as K
 from tests import attn_reference as ref
 from tests.attn_helpers import DEV, Paged, bits, near
-from tests.attn_paths import path
+from tests.attn_paths import path, together
 from tests.kv_helpers import bf, cu_of, i32, new_status, ok, table
 from tests.kv_reference import bf16, norm_rope, to_f64
 
@@ -50,6 +50,33 @@ PATHS = [
 def test_every_path(name, lens, new, Hq, Hkv, latent, d, slots):
     c = Paged(len(lens) + Hq, lens, new, Hq, Hkv, d, 64, latent=latent, tree=True, pitch=None if slots is None else slots // 64)
     assert path(c.p, latent) == name
+    for _ in range(2):
+        out, lse = c.buffers()
+        guard, st = out.clone(), new_status()
+        c.call(out=out, lse=lse, status=st)
+        ok(st)
+        c.check(out, lse)
+        assert torch.equal(out[c.T:], guard[c.T:])
+
+
+# path, row tiles together, lens, new, hint, q heads, kv heads, latent, tree
+TOGETHER = [
+    ("list, by item, wide", 2, [20000], [64], 64, 16, 4, 0, True),
+    ("list, by item", 2, [9000, 3000], [64, 63], 33, 16, 4, 0, True),                 # twice as many as the hint says
+    ("list, by item", 4, [9000, 3000, 700], [64, 64, 40], 64, 16, 2, 0, True),        # the last has three row tiles
+    ("list, by item", 4, [9000, 3000, 20], [7, 7, 5], 7, 32, 1, 512, True),
+    ("list, by item", 7, [19000], [330], 330, 8, 1, 0, False),                        # three rounds of seven for 21
+    ("list, by cta", 4, [1500, 700] * 25, [7] * 50, 7, 32, 1, 512, True),
+    ("list, by cta", 3, [1900, 700] * 6, [38, 48] * 6, 48, 32, 4, 0, True),
+    ("whole", 2, [200] * 60, [40] * 60, 40, 16, 4, 0, True),
+]
+
+
+@pytest.mark.parametrize("name,row_tiles,lens,new,hint,Hq,Hkv,latent,tree", TOGETHER)
+def test_row_tiles_together(name, row_tiles, lens, new, hint, Hq, Hkv, latent, tree):
+    c = Paged(len(lens) + Hq, lens, new, Hq, Hkv, 128, 64, latent=latent, tree=tree)
+    c.p.max_new_tokens = hint
+    assert (path(c.p, latent), together(c.p, latent)) == (name, row_tiles)
     for _ in range(2):
         out, lse = c.buffers()
         guard, st = out.clone(), new_status()
