@@ -66,7 +66,7 @@ struct Shape {
   static constexpr int DK = DK_, DV = DV_, N = N_;
   static constexpr bool kLatent = LATENT;
   static constexpr bool kRowLanes = N == 128;                    // a query row per TMEM lane: S = Q K^T, O = P V, P in TMEM
-  static constexpr int kGroups = N == 16 ? 1 : N == 32 ? 2 : 4;  // warpgroups of the softmax
+  static constexpr int kGroups = N == 16 ? 1 : N == 64 ? 4 : 2;  // warpgroups of the softmax
   static constexpr int NC = kRowLanes ? 1 : 16;                  // query rows of a softmax thread
   static constexpr int kThreads = 128 + 128 * kGroups;
   static constexpr int kBlocks = DV > 128 ? DV / 128 : 1;        // of 128 output values
@@ -113,6 +113,7 @@ struct Args {
   int whole;           // items are not cut: a unit is an item
   int cluster;         // CTAs that share an item by its tiles and join it themselves (whole), or 1
   int together;        // CTAs that walk the list as one, for as many row tiles of the same keys, or 1
+  int walkers;         // CTAs, or as many times so many
   float scale_log2;
   int stall;
 };
@@ -139,16 +140,33 @@ __device__ __forceinline__ Request request_of(const Args& a, int b) {
 }
 
 // An item of the list is a (request, kv head, up to `together` row tiles).
+template <int N>
+__device__ __forceinline__ int together_of(const Args& a) {
+  return N == 128 ? a.together : 1;
+}
+template <int N>
 __device__ __forceinline__ int rounds_of(const Args& a, const Request& r) {
-  return a.together == 1 ? r.row_tiles : (r.row_tiles + a.together - 1) / a.together;
+  return (r.row_tiles + together_of<N>(a) - 1) / together_of<N>(a);
 }
-__device__ __forceinline__ int units_of(const Args& a, const Request& r) { return a.num_kv_heads * rounds_of(a, r) * (a.whole ? 1 : r.tiles + 1); }
+template <int N>
+__device__ __forceinline__ int units_of(const Args& a, const Request& r) {
+  return a.num_kv_heads * rounds_of<N>(a, r) * (a.whole ? 1 : r.tiles + 1);
+}
 
-// First unit of a walker (CTA, cluster, or CTAs together).  With fewer units than walkers the first ones have one each: every one up to
-// the last with any has some.
-__device__ __forceinline__ int share(int total, int walker, int walkers) {
-  return total < walkers ? min(walker, total) : static_cast<int>(static_cast<uint64_t>(static_cast<uint32_t>(total)) * walker / walkers);
-}
+// How `total` units are shared by the walkers (CTAs, clusters, or CTAs together): the first `more` have one unit more than `each`.
+struct Shares {
+  uint32_t each, more;
+  __device__ __forceinline__ Shares(int total, int walkers) : each(0), more(total) {
+    if (total < walkers) return;
+    each = static_cast<uint32_t>(total) / walkers;
+    more = total - each * walkers;
+  }
+  __device__ __forceinline__ int first(uint32_t walker) const { return static_cast<int>(each * walker + min(walker, more)); }
+  __device__ __forceinline__ int owner(uint32_t unit) const {
+    const uint32_t all = more * (each + 1);
+    return static_cast<int>(unit < all ? unit / (each + 1) : more + (unit - all) / each);
+  }
+};
 
 // What a CTA does of one item: tiles t0 .. t1 - 1 of its row tile (none if the request has fewer row tiles).
 struct Piece {
@@ -170,20 +188,20 @@ struct Pieces {
     if (pos >= end) return false;
     while (pos >= before + units) {
       before += units;
-      items += a.num_kv_heads * rounds_of(a, r);
+      items += a.num_kv_heads * rounds_of<N>(a, r);
       r = request_of<N>(a, ++b);
-      units = units_of(a, r);
+      units = units_of<N>(a, r);
     }
     const uint32_t per = a.whole ? 1 : r.tiles + 1, item = a.whole ? pos - before : static_cast<uint32_t>(pos - before) / per;
     const int u = static_cast<int>(pos - before - item * per), take = min(static_cast<int>(per) - u, end - pos);
     p.r = r;
     p.b = b;
-    const uint32_t rounds = rounds_of(a, r);
+    const uint32_t rounds = rounds_of<N>(a, r);
     p.head = rounds == 1 ? item : item / rounds;
-    p.row_tile = (static_cast<int>(item) - p.head * static_cast<int>(rounds)) * a.together + (a.together == 1 ? 0 : blockIdx.x % a.together);
+    p.row_tile = (static_cast<int>(item) - p.head * static_cast<int>(rounds)) * together_of<N>(a) + blockIdx.x % together_of<N>(a);
     p.t0 = a.whole ? 0 : max(u - 1, 0);
     p.t1 = a.whole ? r.tiles : u + take - 1;
-    if (p.row_tile >= r.row_tiles) p.t0 = p.t1 = 0;
+    if (together_of<N>(a) > 1 && p.row_tile >= r.row_tiles) p.t0 = p.t1 = 0;
     if (a.cluster > 1) {
       const int rank = blockIdx.x % a.cluster;
       p.t1 = r.tiles * (rank + 1) / a.cluster;
@@ -210,7 +228,7 @@ struct Start {
 // By one warp, a request to a lane at a time.
 template <int N>
 __device__ __forceinline__ Start<N> find_start(const Args& a, bool report) {
-  const int walker = blockIdx.x / (a.cluster * a.together), walkers = kCtas / a.together;
+  const int per = a.cluster * together_of<N>(a), walker = per == 1 ? blockIdx.x : blockIdx.x / static_cast<unsigned>(per);
   const int lane = threadIdx.x % 32;
   Start<N> st;
   Request r{};
@@ -219,8 +237,8 @@ __device__ __forceinline__ Start<N> find_start(const Args& a, bool report) {
     units = items = 0;
     if (b >= a.num_reqs) return;
     r = request_of<N>(a, b);
-    units = units_of(a, r);
-    items = a.num_kv_heads * rounds_of(a, r);
+    units = units_of<N>(a, r);
+    items = a.num_kv_heads * rounds_of<N>(a, r);
   };
   st.total = st.items = 0;
   for (int b0 = 0; b0 < a.num_reqs; b0 += 32) {
@@ -230,8 +248,9 @@ __device__ __forceinline__ Start<N> find_start(const Args& a, bool report) {
     st.items += __reduce_add_sync(kAll, items);
   }
   Pieces<N>& w = st.rest;
-  w.first = w.pos = share(st.total, walker, walkers);
-  w.end = walker < walkers ? share(st.total, walker + 1, walkers) : w.pos;
+  const Shares shares(st.total, a.walkers);
+  w.first = w.pos = shares.first(walker);
+  w.end = walker < a.walkers ? shares.first(walker + 1) : w.pos;
   if (a.cluster > 1) w.end = min(w.end, w.pos + 1);
   w.before = w.items = w.units = 0;
   st.any = w.pos < w.end;
@@ -285,15 +304,6 @@ struct alignas(1024) Smem {
   int32_t abort_flag;
 };
 
-// The walker that has a unit.
-__device__ __forceinline__ int owner(int total, int u, int walkers) {
-  if (total < walkers) return u;
-  int c = min(walkers - 1, static_cast<int>(static_cast<uint64_t>(static_cast<uint32_t>(u)) * walkers / static_cast<uint32_t>(total)));
-  while (share(total, c + 1, walkers) <= u) ++c;
-  while (share(total, c, walkers) > u) --c;
-  return c;
-}
-
 // (d0, d1) = (a0, a1) * b + (c0, c1)
 __device__ __forceinline__ void fma2(float& d0, float& d1, float a0, float a1, float b, float c0, float c1) {
   asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %4};\n\tmov.b64 c, {%5, %6};\n\t"
@@ -313,6 +323,9 @@ __device__ __forceinline__ uint32_t remote(const void* p, int rank) {
   return r;
 }
 __device__ __forceinline__ void store_remote(uint32_t to, float x) { asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to), "f"(x) : "memory"); }
+__device__ __forceinline__ void store_remote(uint32_t to, float x, float y, float z, float w) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(to), "f"(x), "f"(y), "f"(z), "f"(w) : "memory");
+}
 __device__ __forceinline__ void store_remote(const void* to, int rank, float2 x) {
   asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(remote(to, rank)), "f"(x.x), "f"(x.y) : "memory");
 }
@@ -331,15 +344,19 @@ __device__ __forceinline__ int p_offset(int t, int c) {
 template <int NC>
 __device__ __forceinline__ void load_columns(uint32_t taddr, float (&x)[NC]) {
   uint32_t r[NC];
-  if constexpr (NC == 16) cosa::tmem_ld16(taddr, r);
-  else cosa::tmem_ld32(taddr, r);
+  if constexpr (NC == 16) {
+    cosa::tmem_ld16(taddr, r);
+  } else {
+#pragma unroll
+    for (int i = 0; i < NC; i += 32) cosa::tmem_ld32(taddr + i, *reinterpret_cast<uint32_t(*)[32]>(&r[i]));
+  }
   cosa::tmem_wait_ld();
 #pragma unroll
   for (int i = 0; i < NC; ++i) x[i] = __uint_as_float(r[i]);
 }
 
 // The first n bits.
-__device__ __forceinline__ uint32_t ones(int n) { return n <= 0 ? 0 : n >= 32 ? ~0u : (1u << n) - 1; }
+__device__ __forceinline__ uint64_t ones(int n) { return n <= 0 ? 0 : n >= 64 ? ~uint64_t{0} : (uint64_t{1} << n) - 1; }
 
 // The largest value of a warp; NaN counts as nothing.
 __device__ __forceinline__ float warp_max(float x) {
@@ -663,27 +680,28 @@ __global__ void __launch_bounds__(S::kThreads, 1)
     // =========================== what is to be joined ===========================
     if (lane == 0 && !a.whole) {
       Join none{}, mine{};
+      const Shares shares(sm.start.total, a.walkers);
       for (; more; more = pieces.next(a, pc)) {
         if (!pc.begins) continue;
         Join j{};
         j.parts = 1;
         if (pc.slot >= 0 && pc.row_tile < pc.r.row_tiles) {
-          j.parts = owner(sm.start.total, pc.item_end - 1, kCtas / a.together) - cta / a.together + 1;
+          j.parts = shares.owner(pc.item_end - 1) - cta / together_of<N>(a) + 1;
           j.first = pc.slot;
-          j.next = 2 * (cta + a.together);
-          j.step = 2 * a.together;
+          j.next = 2 * (cta + together_of<N>(a));
+          j.step = 2 * together_of<N>(a);
           j.tok0 = pc.r.tok0;
           j.rows = pc.r.n * a.group;
           j.head = pc.head;
           j.row_tile = pc.row_tile;
           mine = j;
         }
-        const int entry = pc.item * a.together + (cta - cta / a.together * a.together);
+        const int entry = pc.item * together_of<N>(a) + cta % together_of<N>(a);
         if (entry < a.join_items) a.joins[entry] = j;
       }
       if (!a.join_items) a.joins[cta] = mine;
       else if (cta == 0)
-        for (int i = sm.start.items * a.together; i < a.join_items; ++i) a.joins[i] = none;
+        for (int i = sm.start.items * together_of<N>(a); i < a.join_items; ++i) a.joins[i] = none;
     }
     __syncwarp();
   } else {
@@ -692,8 +710,10 @@ __global__ void __launch_bounds__(S::kThreads, 1)
     const int at = quarter * 32 + lane;                // TMEM lane: slot of the tile, value of an output block
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
     constexpr int kSoftmax = 128 * S::kGroups;
-    // The 128 threads that share rows: a group has 16 rows (a thread a slot of the tile), or, kRowLanes, the four warps of a quarter of
-    // the lanes have 32 (a thread a quarter of the slots).
+    // Threads that share rows: a group has 16 rows (a thread a slot of the tile), or, kRowLanes, the warps of a quarter of the lanes,
+    // one of each group, have 32 (a thread half of the slots).
+    constexpr int kSharers = S::kRowLanes ? 32 * S::kGroups : 128, kParts = kSharers / 32;
+    constexpr int kSlotsOf = kTile / S::kGroups, kWidth = DV / S::kGroups;      // kRowLanes: slots and values of a thread
     const int my_bar = 1 + (S::kRowLanes ? quarter : g);
     const int c0 = S::kRowLanes ? at : g * 16;         // first row
     const bool owns = S::kRowLanes ? g == 0 : at < 16;      // of those threads, the one that a row's reference, sum and result belong to,
@@ -727,7 +747,7 @@ __global__ void __launch_bounds__(S::kThreads, 1)
       tc_fence_after();
       if constexpr (S::kRowLanes) {
 #pragma unroll 1
-        for (int d = g * (DV / 4); d < (g + 1) * (DV / 4); d += 16) {
+        for (int d = g * kWidth; d < (g + 1) * kWidth; d += 16) {
           float o[16] = {};
           __syncwarp();
           if (pc.t0 < pc.t1) load_columns<16>(tmem + lanes + S::kTmemO + d, o);
@@ -762,7 +782,7 @@ __global__ void __launch_bounds__(S::kThreads, 1)
     for (; ok && more; more = pieces.next(a, pc)) {
       const Request& r = pc.r;
       const int rows = r.n * a.group;      // fits 32 bits: total_tokens * Hq does
-      if (pc.row_tile >= r.row_tiles) continue;
+      if (together_of<N>(a) > 1 && pc.row_tile >= r.row_tiles) continue;
       const int row0 = pc.row_tile * N;
       if (!meet()) break;                  // the last piece is done with what follows
       if (tid < N) {
@@ -798,25 +818,30 @@ __global__ void __launch_bounds__(S::kThreads, 1)
 #pragma unroll
       for (int i = 0; i < NC; ++i) l[i] = 0.f;
       float ref = kNone;                   // kRowLanes: the row's reference (log2 units)
+      // kRowLanes: pages of the thread's groups of 16 slots, one to a lane, a tile ahead
+      auto look_up = [&](int t) {
+        const int s = t * kTile + g * kSlotsOf + lane * 16;
+        return S::kRowLanes && t < pc.t1 && lane < kSlotsOf / 16 && s < r.len ? __ldg(table + (s >> a.page_shift)) : -1;
+      };
+      int phys_next = look_up(pc.t0);
       for (int t = pc.t0; t < pc.t1; ++t, ++tile) {
         const int sb = tile & 1;
-        // what the thread's slots are: one, or 32 with a bit each for those that the row sees
-        const int slot = t * kTile + (S::kRowLanes ? g * 32 : at);
+        // what the thread's slots are: one, or kSlotsOf with a bit each for those that the row sees
+        const int slot = t * kTile + (S::kRowLanes ? g * kSlotsOf : at);
         bool there = false;
-        uint32_t seen = 0;
+        uint64_t seen = 0;
         if constexpr (S::kRowLanes) {
-          const int part = slot + lane * 16;      // (pages are whole groups of 16 slots)
-          bool page = lane < 2 && part < r.len;
-          if (page) {
-            const int phys = __ldg(table + (part >> a.page_shift));
-            page = phys >= 0 && phys < a.num_pages;
-          }
-          const unsigned pages = __ballot_sync(kAll, page);
-          seen = ones(r.len - slot) & ((pages & 1 ? 0xFFFFu : 0u) | (pages & 2 ? 0xFFFF0000u : 0u));
+          const bool page = phys_next >= 0 && phys_next < a.num_pages;
+          phys_next = look_up(t + 1);
+          const unsigned pages = __ballot_sync(kAll, page);      // of groups of 16 slots (pages are whole ones)
+          seen = ones(r.len - slot);
+#pragma unroll
+          for (int k = 0; k < kSlotsOf / 16; ++k)
+            if (!(pages >> k & 1)) seen &= ~(uint64_t{0xFFFF} << 16 * k);
           const int j = slot - ctx;               // the first slot as a new token, or before them
-          if (j + 31 >= 0) {
-            uint32_t those;
-            if (a.tree_mask) those = j >= 64 ? 0u : static_cast<uint32_t>(j >= 0 ? sm.mask[at] >> j : sm.mask[at] << -j);
+          if (j + kSlotsOf > 0) {
+            uint64_t those;
+            if (a.tree_mask) those = j >= 64 ? 0 : j >= 0 ? sm.mask[at] >> j : sm.mask[at] << -j;
             else those = ones(sm.node[at] + 1 - j);
             seen &= those | ones(-j);
           }
@@ -828,17 +853,17 @@ __global__ void __launch_bounds__(S::kThreads, 1)
           }
         }
         bool fail = !warp_wait(&sm.s_full[sb], (tile / 2) & 1, abort_flag, a.status);
-        constexpr int kHave = S::kRowLanes ? 32 : 16;
-        float x[kHave];                      // logits: the thread's row's 32 slots, or its slot's 16 rows
-        uint32_t w[16];                      // kRowLanes: weights as bf16
+        constexpr int kHave = S::kRowLanes ? kSlotsOf : 16;
+        float x[kHave];                      // logits: the thread's row's slots, or its slot's 16 rows
+        uint32_t w[kHave / 2];               // kRowLanes: weights as bf16
         float sum = 0.f;                     // and their sum
         // -infinity where the row does not see the slot
         auto logits = [&] {
-          load_columns(tmem + lanes + S::kTmemS + sb * N + (S::kRowLanes ? g * 32 : c0), x);
+          load_columns(tmem + lanes + S::kTmemS + sb * N + (S::kRowLanes ? g * kSlotsOf : c0), x);
           if constexpr (S::kRowLanes) {
-            if (seen != ~0u) {
+            if (seen != ~uint64_t{0}) {
 #pragma unroll
-              for (int e = 0; e < 32; ++e)
+              for (int e = 0; e < kHave; ++e)
                 if (!(seen >> e & 1)) x[e] = -INFINITY;
             }
           } else if (!there) {
@@ -857,7 +882,7 @@ __global__ void __launch_bounds__(S::kThreads, 1)
           uint32_t high = 0;
           float s4[4] = {};
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
+          for (int e = 0; e < kHave / 2; ++e) {
             float x0, x1;
             cosa::fma2_bc(x0, x1, x[2 * e], x[2 * e + 1], scale, -ref);
             const float p0 = cosa::ex2_approx(x0), p1 = cosa::ex2_approx(x1);
@@ -891,16 +916,16 @@ __global__ void __launch_bounds__(S::kThreads, 1)
             }
             high = top > kHigh;
           }
-          redo = named_bar_red_or(my_bar, 128, high || fail);
+          redo = named_bar_red_or(my_bar, kSharers, high || fail);
         }
         if (redo) {
-          if (named_bar_red_or(my_bar, 128, fail)) { ok = false; break; }
+          if (named_bar_red_or(my_bar, kSharers, fail)) { ok = false; break; }
           // the rows' maxima over the tile become references
           float mine = S::kRowLanes ? -INFINITY : 0.f;
           if constexpr (S::kRowLanes) {
-            if (t > pc.t0) logits();       // (the weights were made of them: registers that live until here were spilled)
+            if (t > pc.t0) logits();       // (registers that live until here would be spilled)
 #pragma unroll
-            for (int e = 0; e < 32; ++e) mine = fmaxf(mine, x[e]);
+            for (int e = 0; e < kHave; ++e) mine = fmaxf(mine, x[e]);
             sm.part[g][at] = mine;
           } else {
 #pragma unroll
@@ -910,9 +935,10 @@ __global__ void __launch_bounds__(S::kThreads, 1)
             }
             if (lane < 16) sm.part[quarter][c0 + lane] = mine;
           }
-          named_bar_sync(my_bar, 128);
+          named_bar_sync(my_bar, kSharers);
           auto move = [&](int c, float was, float& alpha) {      // the new reference
-            const float top = fmaxf(fmaxf(sm.part[0][c], sm.part[1][c]), fmaxf(sm.part[2][c], sm.part[3][c]));
+            float top = fmaxf(sm.part[0][c], sm.part[1][c]);
+            if (kParts == 4) top = fmaxf(top, fmaxf(sm.part[2][c], sm.part[3][c]));
             const float now = top == -INFINITY ? was : fmaxf(was, top * scale);
             alpha = now == was ? 1.f : cosa::ex2_approx(was - now);
             return now;
@@ -924,7 +950,7 @@ __global__ void __launch_bounds__(S::kThreads, 1)
           } else if (owns) {
             sm.base[own] = -move(own, -sm.base[own], sm.alpha[own]);
           }
-          named_bar_sync(my_bar, 128);
+          named_bar_sync(my_bar, kSharers);
           if (t > pc.t0) {
             if constexpr (S::kRowLanes) l[0] *= alpha;
             else
@@ -933,10 +959,10 @@ __global__ void __launch_bounds__(S::kThreads, 1)
             fail = !warp_wait(&sm.pv_done[(tile - 1) & 1], ((tile - 1) / 2) & 1, abort_flag, a.status);
             if (!fail) {
               tc_fence_after();
-              constexpr int kTimes = S::kRowLanes ? DV / 4 / 16 : S::kBlocks;
+              constexpr int kTimes = S::kRowLanes ? kWidth / 16 : S::kBlocks;
 #pragma unroll 1
               for (int m = 0; m < kTimes; ++m) {
-                const uint32_t o = tmem + lanes + S::kTmemO + (S::kRowLanes ? g * (DV / 4) + m * 16 : m * N + c0);
+                const uint32_t o = tmem + lanes + S::kTmemO + (S::kRowLanes ? g * kWidth + m * 16 : m * N + c0);
                 uint32_t v[16];
                 cosa::tmem_ld16(o, v);
                 cosa::tmem_wait_ld();
@@ -956,7 +982,7 @@ __global__ void __launch_bounds__(S::kThreads, 1)
           if constexpr (S::kRowLanes) {
             l[0] += sum;
             tc_fence_after();
-            cosa::tmem_st16(tmem + lanes + S::kTmemP + (tile & 1) * (kTile / 2) + g * 16, w);
+            cosa::tmem_st32(tmem + lanes + S::kTmemP + (tile & 1) * (kTile / 2) + g * (kSlotsOf / 2), w);
             cosa::tmem_wait_st();
           } else {
             // exp2(x * scale - reference), summed, and as bf16 to P^T
@@ -1007,19 +1033,19 @@ __global__ void __launch_bounds__(S::kThreads, 1)
       }
       bool fail = false;
       if (pc.t0 < pc.t1) fail = !warp_wait(&sm.pv_done[(tile - 1) & 1], ((tile - 1) / 2) & 1, abort_flag, a.status);
-      if (named_bar_red_or(my_bar, 128, fail)) { ok = false; break; }
+      if (named_bar_red_or(my_bar, kSharers, fail)) { ok = false; break; }
       if (a.cluster > 1) {
         // to every CTA of the cluster; what they hold is waited for below
         if (owns) {
           const int c = own;
-          const float sum = (sm.part[0][c] + sm.part[1][c]) + (sm.part[2][c] + sm.part[3][c]), m = -sm.base[c];
+          const float sum = sm.part[0][c] + sm.part[1][c] + (kParts == 4 ? sm.part[2][c] + sm.part[3][c] : 0.f), m = -sm.base[c];
           for (int k = 0; k < a.cluster; ++k) store_remote(&sm.ml[cta % a.cluster][c], k, make_float2(m == kNone ? -INFINITY : m, sum));
         }
         break;
       }
       if (owns) {
         const int c = own;
-        const float sum = (sm.part[0][c] + sm.part[1][c]) + (sm.part[2][c] + sm.part[3][c]), m = -sm.base[c];
+        const float sum = sm.part[0][c] + sm.part[1][c] + (kParts == 4 ? sm.part[2][c] + sm.part[3][c] : 0.f), m = -sm.base[c];
         if (pc.slot >= 0) {
           float* ml = a.part_ml + (static_cast<int64_t>(pc.slot) * N + c) * 2;
           ml[0] = m == kNone ? -INFINITY : m;
@@ -1029,7 +1055,7 @@ __global__ void __launch_bounds__(S::kThreads, 1)
           if (a.lse && sm.row[c] >= 0) a.lse[sm.row[c]] = m == kNone ? -INFINITY : (m + log2f(sum)) * kLn2;
         }
       }
-      named_bar_sync(my_bar, 128);
+      named_bar_sync(my_bar, kSharers);
       const bool odd_values = pc.t0 < pc.t1 && *reinterpret_cast<volatile int*>(&sm.odd_values);
       if (pc.t0 < pc.t1 || pc.slot < 0)
         outputs(odd_values, [&](const auto& o, int c, int d) {
@@ -1086,9 +1112,15 @@ __global__ void __launch_bounds__(S::kThreads, 1)
           const bool odd_values = pc.t0 < pc.t1 && *reinterpret_cast<volatile int*>(&sm.odd_values);
           outputs(odd_values, [&](const auto& o, int c, int d) {
             const uint32_t to = remote(parts + (rank * N + c) * width + d % width, d / width);      // (8 values: of one share)
+            if constexpr (S::kRowLanes) {
+              const float f = sm.alpha[c];
+              if (sm.row[c] < 0) return;
+              store_remote(to, o[0] * f, o[1] * f, o[2] * f, o[3] * f);
+              store_remote(to + 16, o[4] * f, o[5] * f, o[6] * f, o[7] * f);
+            } else {
 #pragma unroll
-            for (int e = 0; e < (S::kRowLanes ? 8 : 16); ++e)
-              store_remote(to + e * (S::kRowLanes ? 1 : width) * 4, o[e] * sm.alpha[S::kRowLanes ? c : c + e]);
+              for (int e = 0; e < 16; ++e) store_remote(to + e * width * 4, o[e] * sm.alpha[c + e]);
+            }
           });
         }
       }
@@ -1144,7 +1176,16 @@ __global__ void __launch_bounds__(kWide ? kWideThreads : kJoinThreads) join_kern
   if (row >= j.rows) return;                                     // (kWide: the whole block)
   auto slot = [&](int i) { return i == 0 ? j.first : j.next + j.step * (i - 1); };
   const float* base = a.part_o + static_cast<int64_t>(c) * DV + seg * kSeg + lane * kVec;
-  auto load = [&](int i) { return i < parts ? *reinterpret_cast<const Vec*>(base + static_cast<int64_t>(slot(i)) * N * DV) : Vec{}; };
+  // (volatile: else the compiler moves each load to its use)
+  auto load = [&](int i) {
+    Vec x{};
+    const float* at = base + static_cast<int64_t>(slot(i)) * N * DV;
+    if (i < parts) {
+      if constexpr (kVec == 4) asm volatile("ld.global.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w) : "l"(at));
+      else asm volatile("ld.global.v2.f32 {%0, %1}, [%2];" : "=f"(x.x), "=f"(x.y) : "l"(at));
+    }
+    return x;
+  };
   const int first = kWide ? warp : 0;
   // all loads at once: the first values of the parts, and their references and sums (a part to a lane)
   Vec v[kAhead];
@@ -1211,15 +1252,13 @@ __global__ void __launch_bounds__(kWide ? kWideThreads : kJoinThreads) join_kern
 
 int rows_of_tile(const PagedLaunch& L) {
   const int64_t rows = static_cast<int64_t>(L.max_new_tokens) * (L.num_q_heads / L.num_kv_heads);
-  const int most = L.latent_dim ? 64 : 128;
-  int n = 16;
-  while (n < most && n < rows) n *= 2;
-  return n;
+  return rows <= 16 ? 16 : rows <= 32 ? 32 : L.latent_dim ? 64 : 128;
 }
 
 // Row tiles of the same keys that CTAs walk together, a CTA to a row tile, so that a tile of the cache is read from HBM once; the most
 // that a request has (up to 8) if the average one has more than one less, since a CTA idles through a request with fewer.
 int row_tiles_together(const PagedLaunch& L) {
+  if (rows_of_tile(L) < 128) return 1;
   const int64_t n = rows_of_tile(L), group = L.num_q_heads / L.num_kv_heads;
   const int64_t most = (L.max_new_tokens * group + n - 1) / n, rounds = (most + 7) / 8;
   return L.total_tokens * group > L.num_reqs * (most - 1) * n ? static_cast<int>((most + rounds - 1) / rounds) : 1;
@@ -1295,6 +1334,7 @@ cudaError_t launch_shape(const PagedLaunch& L, cudaStream_t stream) {
       a.cluster = c;
     }
   a.together = a.cluster > 1 ? 1 : row_tiles_together(L);
+  a.walkers = kCtas / a.together;
   const int64_t joins = most_items(L, a.together);
   a.join_items = joins <= kCtas ? static_cast<int>(joins) : 0;
   const unsigned ctas = static_cast<unsigned>(a.cluster > 1 ? items * a.cluster : kCtas);
@@ -1311,10 +1351,7 @@ cudaError_t launch_width(const PagedLaunch& L, cudaStream_t stream) {
   switch (rows_of_tile(L)) {
     case 16: return launch_shape<Shape<DK, DV, LATENT, 16>>(L, stream);
     case 32: return launch_shape<Shape<DK, DV, LATENT, 32>>(L, stream);
-    case 64: return launch_shape<Shape<DK, DV, LATENT, 64>>(L, stream);
-    default:
-      if constexpr (!LATENT) return launch_shape<Shape<DK, DV, LATENT, 128>>(L, stream);
-      return cudaErrorInvalidValue;
+    default: return launch_shape<Shape<DK, DV, LATENT, LATENT ? 64 : 128>>(L, stream);
   }
 }
 

@@ -6,16 +6,16 @@ CTAS = 152
 
 def row_tile(latent: int, group: int, hint: int) -> int:
     """Query rows of a row tile."""
-    most, n = (64 if latent else 128), 16
-    while n < most and n < hint * group:
-        n *= 2
-    return n
+    rows = hint * group
+    return 16 if rows <= 16 else 32 if rows <= 32 else 64 if latent else 128
 
 
 def together(p, latent: int) -> int:
     """Row tiles of the same keys that CTAs walk together."""
     group = p.num_q_heads // (1 if latent else p.num_kv_heads)
     n = row_tile(latent, group, p.max_new_tokens)
+    if n < 128:
+        return 1
     most = -(-p.max_new_tokens * group // n)
     return -(-most // -(-most // 8)) if p.total_tokens * group > p.num_reqs * (most - 1) * n else 1
 

@@ -167,6 +167,63 @@ def test_extreme_logits():
     run_and_check(Paged(14, [1500], [3], 4, latent=512, edit=falling))
 
 
+# ---- more than 32 query rows to a kv head, which lie a row to a lane
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("lens,new", [([40, 7, 300], [40, 7, 33]), ([700, 64, 130], [64, 64, 1]), ([20011, 90, 70], [64, 17, 3])])
+def test_many_rows(lens, new, d):
+    run_and_check(Paged(31, lens, new, 8, 2, d, 16, tree=True))
+    run_and_check(Paged(32, lens, new, 8, 2, d, 32, tree=True, ragged=True, missing=[(0, 0), (1, 1), (2, 2)]))
+    run_and_check(Paged(33, lens, new, 14, 2, d, 128, strided="heads"))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("bad", [np.nan, np.inf])
+@pytest.mark.parametrize("ctx", [100, 9000])
+def test_many_rows_and_what_they_do_not_see(d, bad, ctx):
+    """The values of new token 5 are not finite, nor are the keys of token 9."""
+    n = 20
+
+    def edit(ks, vs, q):
+        vs[0][ctx + 5, 0, 3] = vs[0][ctx + 5, 0, d - 1] = bad
+        ks[0][ctx + 9, 1] = np.nan
+    c, clean = (Paged(34, [ctx + n], [n], 8, 2, d, 64, tree=True, edit=e) for e in (edit, None))
+    assert c.masks == clean.masks
+    out, lse = c.buffers()
+    want, want_lse = clean.buffers()
+    c.call(out=out, lse=lse)
+    clean.call(out=want, lse=want_lse)
+    got = to_f64(out)
+    for i, m in enumerate(c.masks[0]):
+        if m >> 5 & 1:
+            assert not np.isfinite(got[i, :4, [3, d - 1]]).any()
+            keep = [e for e in range(d) if e not in (3, d - 1)]
+            assert torch.equal(out[i, :4][:, keep], want[i, :4][:, keep]) and torch.equal(lse[i, :4], want_lse[i, :4])
+        else:
+            assert torch.equal(out[i, :4], want[i, :4]) and torch.equal(lse[i, :4], want_lse[i, :4])
+        if m >> 9 & 1:
+            assert np.isnan(got[i, 4:]).all()
+        else:
+            assert torch.equal(out[i, 4:], want[i, 4:]) and torch.equal(lse[i, 4:], want_lse[i, 4:])
+
+
+def test_many_rows_of_rising_logits():
+    """References that move many times, in one CTA and in several."""
+    def edit(ks, vs, q):
+        ks[0] *= np.linspace(0.01, 40, ks[0].shape[0])[:, None, None]
+        ks[0][:] = bf16(ks[0])
+    for lens in ([1500], [12000]):
+        run_and_check(Paged(35, lens, [20], 4, 1, 128, 64, edit=edit, tree=True))
+
+
+@pytest.mark.parametrize("group", [4, 1])
+def test_bits_behind_the_last_token_count_for_nothing(group):
+    """Masks with every bit set: a row sees its request's tokens and no slot behind them."""
+    c = Paged(36, [70, 200], [20, 9], 2 * group, 2, 64, 64, tree=True)
+    c.masks = [[(1 << n) - 1] * n for n in c.new]
+    c.mask = torch.full_like(c.mask, -1)
+    run_and_check(c)
+
+
 @pytest.mark.parametrize("latent", [0, 512])
 def test_contradictions(latent):
     """A request whose lengths contradict each other has no keys; the others are as ever."""

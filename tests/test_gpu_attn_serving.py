@@ -59,24 +59,22 @@ def test_every_path(name, lens, new, Hq, Hkv, latent, d, slots):
         assert torch.equal(out[c.T:], guard[c.T:])
 
 
-# path, row tiles together, lens, new, hint, q heads, kv heads, latent, tree
+# path, row tiles together, lens, new, hint, q heads, kv heads, tree
 TOGETHER = [
-    ("list, by item, wide", 2, [20000], [64], 64, 16, 4, 0, True),
-    ("list, by item", 2, [9000, 3000], [64, 63], 33, 16, 4, 0, True),                 # twice as many as the hint says
-    ("list, by item", 4, [9000, 3000, 700], [64, 64, 40], 64, 16, 2, 0, True),        # the last has three row tiles
-    ("list, by item", 4, [9000, 3000, 20], [7, 7, 5], 7, 32, 1, 512, True),
-    ("list, by item", 7, [19000], [330], 330, 8, 1, 0, False),                        # three rounds of seven for 21
-    ("list, by cta", 4, [1500, 700] * 25, [7] * 50, 7, 32, 1, 512, True),
-    ("list, by cta", 3, [1900, 700] * 6, [38, 48] * 6, 48, 32, 4, 0, True),
-    ("whole", 2, [200] * 60, [40] * 60, 40, 16, 4, 0, True),
+    ("list, by item, wide", 2, [12000], [64], 64, 16, 4, True),
+    ("list, by item", 2, [9000, 3000], [64, 63], 33, 16, 4, True),                 # twice as many as the hint says
+    ("list, by item", 4, [9000, 3000, 700], [64, 64, 40], 64, 16, 2, True),        # the last has three row tiles
+    ("list, by item", 7, [9000], [330], 330, 8, 1, False),                         # three rounds of seven for 21
+    ("list, by cta", 3, [1900, 700] * 6, [38, 48] * 6, 48, 32, 4, True),
+    ("whole", 2, [200] * 60, [40] * 60, 40, 16, 4, True),
 ]
 
 
-@pytest.mark.parametrize("name,row_tiles,lens,new,hint,Hq,Hkv,latent,tree", TOGETHER)
-def test_row_tiles_together(name, row_tiles, lens, new, hint, Hq, Hkv, latent, tree):
-    c = Paged(len(lens) + Hq, lens, new, Hq, Hkv, 128, 64, latent=latent, tree=tree)
+@pytest.mark.parametrize("name,row_tiles,lens,new,hint,Hq,Hkv,tree", TOGETHER)
+def test_row_tiles_together(name, row_tiles, lens, new, hint, Hq, Hkv, tree):
+    c = Paged(len(lens) + Hq, lens, new, Hq, Hkv, 128, 64, tree=tree)
     c.p.max_new_tokens = hint
-    assert (path(c.p, latent), together(c.p, latent)) == (name, row_tiles)
+    assert (path(c.p, 0), together(c.p, 0)) == (name, row_tiles)
     for _ in range(2):
         out, lse = c.buffers()
         guard, st = out.clone(), new_status()
