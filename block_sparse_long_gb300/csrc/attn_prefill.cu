@@ -18,7 +18,14 @@
 //
 // Measured on the way, 16K tokens of 16 heads of 128 + 64: two tiles of 128 queries to a CTA with an issuing warp each 1.43 ms (they
 // fell into step: both softmaxes, then both products), with one issuing warp 1.37, both tiles' O before both tiles' S 1.14 (the keys'
-// slots were free for longer than a copy takes; all of TMEM and the shared memory of two tiles left no second buffer of S).
+// slots were free for longer than a copy takes; all of TMEM and the shared memory of two tiles left no second buffer of S); one tile
+// and two buffers of S 1.25 with keys and values of a block behind one barrier, 1.02 with a barrier each.  A block then takes 2050
+// cycles, the products 1340 of them as they issue (1280 at the rate of the pipe by itself) and the waits between them 700.  Not
+// better: Q in TMEM and a third slot for keys (1.04); P in columns of its own and an issuing warp for each product (1.02 to 1.03;
+// heads of 64, 8192 tokens of 16: 242 -> 231 us, 4096 of 8 heads of 128: 65 -> 67).
+//
+// What bounds it now: at 16K tokens of 16 heads of 128 + 64 1.02 ms, 1.35 PFLOP/s of the pairs that are seen; 5 prompts of 37 to 2011 tokens
+// of 6 heads of 64 45 us: 390 CTAs of up to 19 blocks on 152 SMs, each of which waits 3700 to 7300 cycles for its first loads.
 #include <cmath>
 #include <cstdint>
 
