@@ -4,24 +4,37 @@
 //     s = k . q (slot by row),  p = exp2(s * scale - m_row),  o = sum p v,  l = sum p
 //
 // A row is a (new token, query head of the kv head): R = n * Hq / Hkv of them share every key, one to some hundreds.  With so few
-// the cache is read once and the memory bounds the call, so the matrix instructions are set up for what there is plenty of:
-// the 128 slots of a tile, or 128 values of the output, are the 128 rows of a tcgen05.mma, and the N = 16 to 128 query rows
-// its columns.  S^T = K Q^T has a slot per TMEM lane, O^T = V^T P^T a value per lane; K comes as it lies in its page, and as V
-// read the other way (values contiguous), so latent vectors are loaded once for both products.
+// the cache is read once and the memory bounds the call, so the matrix instructions are set up for what there is plenty of.
+//   Up to 32 rows (of latent vectors 64 at a time): the 128 slots of a tile, or 128 values of the output, are the 128 rows of a
+//   tcgen05.mma, and the 16, 32 or 64 query rows its columns.  S^T = K Q^T has a slot per TMEM lane, O^T = V^T P^T a value per
+//   lane; K comes as it lies in its page, and as V read the other way (values contiguous), so latent vectors are loaded once for
+//   both products.  P^T goes through shared memory.
+//   More rows (kRowLanes): the 128 rows of the product are query rows, S = Q K^T, O = P V with P in TMEM, so that a softmax thread has a
+//   row (half of its slots), needs no other thread's maximum and keeps the reference in a register.  64 new tokens of 4 heads to a
+//   kv head after 128K slots: 231 us with the rows as 128 columns, 177 with a quarter of the slots to a thread, with half of them (fewer
+//   warps, none of whose registers spill) and pages looked up a tile ahead 11 % less.
 //
 // A CTA per SM.  The tiles of all (request, kv head, row tile) items stand in one list, which the CTAs share evenly, one unit per
 // tile and one per item; a CTA's piece of an item that others have too leaves m, l and o (32 bits) in the workspace and
-// join_kernel puts them together.
+// join_kernel puts them together.  Short contexts go whole to a CTA or to a cluster that joins them through distributed shared
+// memory (900 slots: list and join 12.4 us, cluster 10.5).  With several row tiles of 128 rows to the same keys as many CTAs walk the
+// list together, a CTA to a row tile, so that HBM is read once (the same 128K: 177 us apart, 140 together; then 125 as above).
+//
+// What bounds it (32 query over 8 kv heads of 128, 64-slot pages): 13-token trees of 24 ragged contexts 159 us, 5.6 TB/s; 64 tokens
+// after 128K 125 us, 4.3 TB/s and 1.1 PFLOP/s, a tile's chain of product, softmax, product (2000 cycles, of which the products run
+// 1024); one token after 900 slots 8.8 us, the chain of first loads, products and join.  Latent vectors of 512 + 64, 32 heads: one token after
+// 128K 42 us, 3.6 TB/s; 7 tokens of 24 ragged contexts 142 us: a tile (147 KB) fills shared memory, so a block of the next can only be copied
+// once the second product is done with it (6000 cycles a tile, of which the products run 3300).
 //
 // Warp roles:
 //   warp 0     producer: looks up the pages of a tile and copies them by TMA into a ring of 32 KB slots (two 128-byte wide
-//              columns of 128 slots), 160 KB in flight at most.
-//   warp 1     issues S^T of every tile into one of two TMEM buffers.
-//   warp 2     issues O^T += V^T P^T; clears rows of V that no slot has, and in the tile of the new tokens what is not finite.
-//   warp 3     owns the TMEM.
-//   warps 4-   softmax: a thread has a slot and 16 to 64 query rows.  The reference m of a row is that of an earlier tile until some
-//              logit exceeds it by 2^8, so that most tiles need no maximum over the slots: one vote, the exponentials,
-//              and P^T to shared memory as bf16 (2^-9 of each term; l sums the unrounded ones).
+//              columns of 128 slots), four to six of them.
+//   warp 1     issues the first product of every tile into one of two TMEM buffers.
+//   warp 2     issues the second; clears rows of V that no slot has, and in the tile of the new tokens what is not finite (0 times
+//              that is not 0; the rows that see it get it added at the end).
+//   warp 3     owns the TMEM; writes down what is to be joined.
+//   warps 4-   softmax.  The reference m of a row is that of an earlier tile until some weight exceeds 2^8, so that most tiles need
+//              no maximum over the slots: one vote, the exponentials, and P as bf16 (2^-9 of each term; l sums the unrounded ones).
 #include <cmath>
 #include <cstdint>
 #include <type_traits>
@@ -240,13 +253,21 @@ __device__ __forceinline__ Start<N> find_start(const Args& a, bool report) {
     units = units_of<N>(a, r);
     items = a.num_kv_heads * rounds_of<N>(a, r);
   };
-  st.total = st.items = 0;
+  st.items = 0;
+  uint64_t total = 0;
   for (int b0 = 0; b0 < a.num_reqs; b0 += 32) {
     look(b0 + lane);
     if (b0 + lane < a.num_reqs && r.bad && report) cosa::report_status(a.status, cosa::kStatusBadInput);
-    st.total += __reduce_add_sync(kAll, units);
+    const uint32_t u = units;
+    total += (static_cast<uint64_t>(__reduce_add_sync(kAll, u >> 16)) << 16) + __reduce_add_sync(kAll, u & 0xFFFFu);
     st.items += __reduce_add_sync(kAll, items);
   }
+  // Requests that share tokens (cu_seqlens that falls and rises) can have more units than the call was checked for: then nothing is done.
+  if (total > INT32_MAX) {
+    total = st.items = 0;
+    if (report && lane == 0) cosa::report_status(a.status, cosa::kStatusBadInput);
+  }
+  st.total = static_cast<int>(total);
   Pieces<N>& w = st.rest;
   const Shares shares(st.total, a.walkers);
   w.first = w.pos = shares.first(walker);
@@ -1250,6 +1271,7 @@ __global__ void __launch_bounds__(kWide ? kWideThreads : kJoinThreads) join_kern
   if (a.lse && seg == 0 && lane == 0) a.lse[to] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
 }
 
+// 24 requests of 52 rows: 168 us as 64 columns, 159 a row to a lane; of 24 rows: 152 as 32 columns, 156 a row to a lane.
 int rows_of_tile(const PagedLaunch& L) {
   const int64_t rows = static_cast<int64_t>(L.max_new_tokens) * (L.num_q_heads / L.num_kv_heads);
   return rows <= 16 ? 16 : rows <= 32 ? 32 : L.latent_dim ? 64 : 128;
@@ -1320,6 +1342,9 @@ cudaError_t launch_shape(const PagedLaunch& L, cudaStream_t stream) {
   a.cluster = 1;
   // How the items are shared, by the tiles that a CTA then has at most (lengths are known to the device only: max_seqlen's): all tiles
   // in one list, cut anywhere, and a second kernel to join (about kJoin tiles' time); whole items to a CTA; or an item to a cluster.
+  // One token each, list / whole / cluster: 1 context of 900 (32 heads over 8 of 128) 10.2 / 11.7 / 8.6 us, 4 of 900 13.8 / 12.4 / 11.0,
+  // 64 of 300 33.7 / 30.6 / -, 4 of 4000 22.5 / 29.9 / -; latent 512 of 16 heads: 9 of 900 14.6 / - / 13.1, 150 of 900 46 / 41 / -,
+  // 200 of 900 62 / 69 / -.
   constexpr double kJoin = S::kLatent ? 2.5 : 5;
   const double tiles = (L.max_seqlen + kTile - 1) / kTile;
   double best = items * (tiles + 1) / kCtas + kJoin;

@@ -24,7 +24,7 @@
  *     enqueued, or COSA_ERR_CUDA for a failed launch.  Lengths that contradict `p` or each other are found on the
  *     device: *device_status (an int32 the caller zeroes; may be NULL) becomes COSA_ERR_BAD_INPUT.  The
  *     attentions then treat the request concerned as one that has no keys (rows of cu_seqlens ranges that do not fit
- *     total_tokens are not written), the commit leaves its slots as they are, and cosa_latent_rope leaves out (writes nothing
+ *     total_tokens are not written; a cu_seqlens that falls may leave all rows unwritten), the commit leaves its slots as they are, and cosa_latent_rope leaves out (writes nothing
  *     of) the tokens of no request and those whose slot is negative or, where a cache is written, not below max_seqlen.
  *     A wait inside an attention kernel that runs out after 2 s gives COSA_ERR_DEVICE_TIMEOUT; the kernel ends
  *     once the copies in flight have landed, after 2 s more at the latest, and the outputs are then undefined.

@@ -167,6 +167,20 @@ def test_extreme_logits():
     run_and_check(Paged(14, [1500], [3], 4, latent=512, edit=falling))
 
 
+def test_more_work_than_a_batch_can_have():
+    """cu_seqlens that falls and rises again: 300 requests of all 4096 tokens, more units than 31 bits hold.  Nothing is done."""
+    T, B, slots, P = 4096, 600, 131072, 64
+    p = C.make_attn_params(num_reqs=B, num_q_heads=32, num_kv_heads=8, head_dim=64, page_size=P, total_tokens=T, max_seqlen=slots,
+                           num_pages=1, max_pages_per_req=slots // P, max_new_tokens=1)
+    q = torch.zeros(T, 32, 64, dtype=torch.bfloat16, device=DEV)
+    cache = torch.zeros(1, P, 8, 64, dtype=torch.bfloat16, device=DEV)
+    out, st = torch.full_like(q, 3.0), new_status()
+    tables = torch.full((B, slots // P), -1, dtype=torch.int32, device=DEV)
+    C.cosa_tree_attention(p, q, i32([0] + [T, 0] * (B // 2)), cache, cache, tables, i32([slots] * B), out=out, status=st)
+    torch.cuda.synchronize()
+    assert int(st) == -6 and (out == 3.0).all()
+
+
 # ---- more than 32 query rows to a kv head, which lie a row to a lane
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("lens,new", [([40, 7, 300], [40, 7, 33]), ([700, 64, 130], [64, 64, 1]), ([20011, 90, 70], [64, 17, 3])])
