@@ -14,7 +14,10 @@
 //               finite is not 0); a row that does see such a value gets it added at the end.  Warp 3 owns the TMEM.
 //   warps 4-11  softmax, a thread has half a row.  The weights are taken against the row's reference of an earlier block; only if
 //               one passes 2^8 the CTA stops for its maxima, scales O and takes them again.
-// CTAs start with the longest rows of a head and go head by head, so that a head's keys stay in L2.
+// CTAs start with the longest rows of all requests and go through them four heads at a time, so that the last to start are short and
+// those that run together read the same keys.  Head by head / 2 / 4 / 8 / 16 heads at a time, us: 4096 tokens of 8 heads of 128
+// 66 / 62 / 46 / 45 / 45, 16K of 16 1032 / 1006 / 1009 / 1022 / 1050, 8 requests of 2048 of 16 198 / 191 / 193 / 198 / 209, five ragged
+// prompts of 6 heads of 64 44.5 / 39.3 / 39.4 / 39.2 / 39.1.
 //
 // Measured on the way, 16K tokens of 16 heads of 128 + 64: two tiles of 128 queries to a CTA with an issuing warp each 1.43 ms (they
 // fell into step: both softmaxes, then both products), with one issuing warp 1.37, both tiles' O before both tiles' S 1.14 (the keys'
@@ -24,8 +27,8 @@
 // better: Q in TMEM and a third slot for keys (1.04); P in columns of its own and an issuing warp for each product (1.02 to 1.03;
 // heads of 64, 8192 tokens of 16: 242 -> 231 us, 4096 of 8 heads of 128: 65 -> 67).
 //
-// What bounds it now: at 16K tokens of 16 heads of 128 + 64 1.02 ms, 1.35 PFLOP/s of the pairs that are seen; 5 prompts of 37 to 2011 tokens
-// of 6 heads of 64 45 us: 390 CTAs of up to 19 blocks on 152 SMs, each of which waits 3700 to 7300 cycles for its first loads.
+// What bounds it now: at 16K tokens of 16 heads of 128 + 64 1.01 ms, 1.36 PFLOP/s of the pairs that are seen; 5 prompts of 37 to 2011 tokens
+// of 6 heads of 64 39 us: 390 CTAs of up to 19 blocks on 152 SMs, each of which waits 3700 to 7300 cycles for its first loads.
 #include <cmath>
 #include <cstdint>
 
@@ -54,6 +57,7 @@ constexpr int kThreads = 384;
 constexpr int kBlock = 128;                // keys
 constexpr int kRows = 128;                 // queries of a CTA
 constexpr int kColumn = kBlock * 128;      // bytes of a 64-value wide column of 128 rows
+constexpr int kHeads = 4;                  // heads whose blocks are taken together
 constexpr int kHalf = kBlock / 2;          // keys of a thread's half row
 constexpr float kNone = -3e38f;            // reference of a row that has seen nothing
 constexpr uint32_t kHigh = 0x4380;         // 2^8 in bf16
@@ -126,32 +130,51 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort_flag = &sm.abort_flag;
   cosa_kv::wait_for_stream();
 
-  const int head = blockIdx.x / a.blocks;
+  const int heads = min(kHeads, a.num_heads), group = blockIdx.x / (a.blocks * heads), in_group = min(heads, a.num_heads - group * heads);
+  const int in = blockIdx.x - group * a.blocks * heads, head = group * heads + in % in_group;
   if (warp == 0) {
-    // block `at` of the list of all requests' blocks
-    int64_t at = blockIdx.x % a.blocks;
-    int req = -1;
-    for (int b0 = 0; b0 < a.num_reqs && (req < 0 || blockIdx.x == 0); b0 += 32) {
-      const Request r = request_of(a, min(b0 + lane, a.num_reqs - 1));
+    int at = in / in_group, req = -1, block = 0;      // which of all requests' blocks
+    if (a.num_reqs <= 32) {
+      // by what lies before them, the longest rows first: block i of a request has about before + i blocks of keys
+      const Request r = request_of(a, min(lane, a.num_reqs - 1));
       if (blockIdx.x == 0 && r.bad) cosa::report_status(a.status, cosa::kStatusBadInput);
-      const int64_t mine = b0 + lane < a.num_reqs ? (r.n + kRows - 1) / kRows : 0;
-      int64_t upto = mine;
+      const int all = lane < a.num_reqs ? (r.n + kRows - 1) / kRows : 0;
+      const int before = static_cast<int>(max(r.keys - r.n + kBlock - 1, static_cast<int64_t>(0)) / kBlock);
+      auto from = [&](int v) { return static_cast<int>(__reduce_add_sync(kAll, static_cast<unsigned>(max(min(before + all - v, all), 0)))); };
+      if (from(0) > at) {
+        int v = 0;                                    // the largest with more than `at` blocks from it on
+        const unsigned most = __reduce_max_sync(kAll, static_cast<unsigned>(all ? before + all : 0));
+        for (int step = 1 << (31 - __clz(most)); step > 0; step /= 2)
+          if (from(v + step) > at) v += step;
+        at -= from(v + 1);
+        const unsigned have = __ballot_sync(kAll, v >= before && v < before + all);
+        req = __ffs(__ballot_sync(kAll, (have >> lane & 1) && __popc(have & ((1u << lane) - 1)) == at)) - 1;
+        block = v - __shfl_sync(kAll, before, max(req, 0));
+      }
+    } else {
+      // request by request
+      for (int b0 = 0; b0 < a.num_reqs && (req < 0 || blockIdx.x == 0); b0 += 32) {
+        const Request r = request_of(a, min(b0 + lane, a.num_reqs - 1));
+        if (blockIdx.x == 0 && r.bad) cosa::report_status(a.status, cosa::kStatusBadInput);
+        const int64_t mine = b0 + lane < a.num_reqs ? (r.n + kRows - 1) / kRows : 0;
+        int64_t upto = mine;
 #pragma unroll
-      for (int m = 1; m < 32; m *= 2) {
-        const int64_t x = __shfl_up_sync(kAll, upto, m);
-        if (lane >= m) upto += x;
+        for (int m = 1; m < 32; m *= 2) {
+          const int64_t x = __shfl_up_sync(kAll, upto, m);
+          if (lane >= m) upto += x;
+        }
+        const unsigned past = __ballot_sync(kAll, upto > at);
+        if (past && req < 0) {
+          const int l = __ffs(past) - 1;
+          req = b0 + l;
+          block = static_cast<int>(__shfl_sync(kAll, upto, l) - 1 - at);      // the longest rows first
+        }
+        at = static_cast<int>(max(at - __shfl_sync(kAll, upto, 31), int64_t{-1}));
       }
-      const unsigned past = __ballot_sync(kAll, upto > at);
-      if (past && req < 0) {
-        const int l = __ffs(past) - 1;
-        req = b0 + l;
-        const int64_t in = at - __shfl_sync(kAll, upto - mine, l), all = __shfl_sync(kAll, mine, l);
-        if (lane == 0) sm.block = static_cast<int>(all - 1 - in);      // the longest rows first
-      }
-      at -= __shfl_sync(kAll, upto, 31);
     }
     if (lane == 0) {
       sm.req = req;
+      sm.block = block;
       if (blockIdx.x == 0 && (a.cu_seqlens[0] != 0 || a.cu_seqlens[a.num_reqs] > a.total_tokens)) cosa::report_status(a.status, cosa::kStatusBadInput);
     }
   } else if (warp == 1 && lane == 0) {

@@ -494,6 +494,17 @@ def test_prefill_lengths(n, d):
     expand_run(expand_case(n, [n], [131], 2, d))
 
 
+@pytest.mark.parametrize("H", [1, 15, 17, 33])
+def test_prefill_of_many_heads_and_requests(H):
+    """Groups of heads with fewer in the last; requests of every length, more of them than a warp has lanes and fewer."""
+    expand_run(expand_case(H, [130, 300, 1, 257], [700, 0, 400, 129], H, 64))
+    if H < 16:
+        rng = np.random.default_rng(H)
+        for B in (31, 32, 33, 70):
+            lens = [int(x) for x in rng.integers(0, 290, B)]
+            expand_run(expand_case(B, lens, [int(x) for x in rng.integers(0, 200, B)], 2, 64))
+
+
 def test_prefill_head_by_head():
     """Keys and values as batched products leave them: tokens within a head."""
     c = expand_case(4, [40, 200], [0, 9], 3, 128)
