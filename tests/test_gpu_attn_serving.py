@@ -95,6 +95,25 @@ def test_empty_contexts_on_clusters(latent):
     assert not out[3:8].any() and torch.isneginf(lse[3:8]).all()
 
 
+@pytest.mark.parametrize("latent", [0, 512])
+def test_idle_ctas_of_clusters_again_and_again(latent):
+    """Clusters of eight of which one CTA has the only tile, the others nothing to wait for before the join, in launches that follow
+    each other closely."""
+    lens = [1, 130, 40, 128, 5, 70, 129, 30] if latent else [1, 130, 40, 128]
+    c = Paged(18, lens, [1] * len(lens), 8, 2 if not latent else 1, 128, 64, latent=latent, pitch=15)
+    assert path(c.p, latent) == "cluster 8"
+    first, first_lse = c.buffers()
+    c.call(out=first, lse=first_lse)
+    c.check(first, first_lse)
+    made = [c.buffers() for _ in range(100)]
+    st = new_status()
+    for out, lse in made:
+        c.call(out=out, lse=lse, status=st)
+    ok(st)
+    for out, lse in made:
+        assert torch.equal(out[:c.T], first[:c.T]) and torch.equal(lse[:c.T], first_lse[:c.T])
+
+
 # ---------------------------------------------------------------------------------------------------------------
 # waits that run out
 # ---------------------------------------------------------------------------------------------------------------
