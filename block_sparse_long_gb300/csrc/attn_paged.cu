@@ -809,7 +809,7 @@ __global__ void __launch_bounds__(S::kThreads, 1)
       const int rows = r.n * a.group;      // fits 32 bits: total_tokens * Hq does
       if (together_of<N>(a) > 1 && pc.row_tile >= r.row_tiles) continue;
       const int row0 = pc.row_tile * N;
-      if (!meet()) break;                  // the last piece is done with what follows
+      if (!meet()) { ok = false; break; }      // the last piece is done with what follows
       if (tid < N) {
         const int row = row0 + tid, node = static_cast<uint32_t>(min(row, rows - 1)) / static_cast<uint32_t>(a.group);
         const int head = pc.head * a.group + row - node * a.group;
@@ -822,7 +822,7 @@ __global__ void __launch_bounds__(S::kThreads, 1)
       }
       if (pc.t0 < pc.t1) {
         // queries into rows of 128 bytes per 64 values, swizzled; rows behind the last are 0
-        if (!meet()) break;
+        if (!meet()) { ok = false; break; }
         constexpr int kPieces16 = S::DK / 8;
 #pragma unroll 3
         for (int e = tid; e < N * kPieces16; e += kSoftmax) {
@@ -834,7 +834,7 @@ __global__ void __launch_bounds__(S::kThreads, 1)
         asm volatile("cp.async.wait_all;" ::: "memory");
         fence_proxy_async_smem();
       }
-      if (!meet()) break;
+      if (!meet()) { ok = false; break; }
       if (tid == 0 && pc.t0 < pc.t1) mbar_arrive(&sm.q_ready);
 
       const int32_t* table = a.page_table + static_cast<size_t>(pc.b) * a.max_pages_per_req;
@@ -1100,7 +1100,7 @@ __global__ void __launch_bounds__(S::kThreads, 1)
         });
       tc_fence_before();
       if (odd_values) {        // the other threads have read it
-        if (!meet()) break;
+        if (!meet()) { ok = false; break; }
         if (tid == 0) sm.odd_values = 0;
       }
     }

@@ -26,3 +26,12 @@ def test_a_cluster_has_started_before_its_memory_is_written():
     mine, others = softmax[1].split("a.cluster > 1 && warp < 4")
     assert barriers(mine) == barriers(others) == ["wait", "barrier", "barrier"]
     assert mine.index("cluster_wait()") < mine.index("store_remote(")
+
+
+def test_a_warp_that_gave_up_leaves_the_join_out():
+    """Behind the pieces `ok` says whether this warp knows its rows: every wait that runs out before has to clear it."""
+    softmax = re.split(r"=+ softmax =+", kernel())[1]
+    pieces = softmax[softmax.index("more = pieces.next"):softmax.index("cluster_wait()")]
+    waits = re.findall(r"if \(!meet\(\)\)([^;]*;)", pieces)
+    assert len(waits) == 4 and all("ok = false" in w for w in waits)
+    assert "sm.start.any && ok;" in softmax
