@@ -1069,7 +1069,7 @@ __global__ void __launch_bounds__(S::kThreads, 1)
           ml[1] = sum;
         } else {
           sm.alpha[c] = sum == 0.f ? 0.f : 1.f / sum;
-          if (a.lse && sm.row[c] >= 0) a.lse[sm.row[c]] = m == kNone ? -INFINITY : (m + log2f(sum)) * kLn2;
+          if (a.lse && sm.row[c] >= 0) a.lse[sm.row[c]] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
         }
       }
       named_bar_sync(my_bar, kSharers);

@@ -84,6 +84,34 @@ def test_row_tiles_together(name, row_tiles, lens, new, hint, Hq, Hkv, tree):
         assert torch.equal(out[c.T:], guard[c.T:])
 
 
+@pytest.mark.parametrize("name,lens,new,Hq,Hkv,latent,d,slots", PATHS + [(name, lens, new, Hq, Hkv, 0, 128, None)
+                                                                        for name, _, lens, new, _, Hq, Hkv, _ in TOGETHER])
+def test_queries_that_are_not_numbers(name, lens, new, Hq, Hkv, latent, d, slots):
+    """A row whose every logit is NaN gives NaN, for its lse too, on every path: it is not one that sees nothing."""
+    def edit(ks, vs, q):
+        q[::3, 0, 5] = np.nan
+    c = Paged(len(lens) + Hq + 1, lens, new, Hq, Hkv, d, 64, latent=latent, tree=max(new) <= 64, edit=edit,
+              pitch=None if slots is None else slots // 64)
+    out, lse = c.buffers()
+    c.call(out=out, lse=lse)
+    c.check(out, lse)
+    assert torch.isnan(lse[:c.T:3, 0]).all() and torch.isnan(out[:c.T:3, 0]).all()
+    rest = torch.ones(c.T, Hq, dtype=torch.bool, device=DEV)
+    rest[::3, 0] = False
+    assert torch.isfinite(lse[:c.T][rest]).all() and torch.isfinite(out[:c.T][rest]).all()
+
+
+def test_prefill_of_queries_that_are_not_numbers():
+    from tests.test_gpu_attn import expand_case, expand_run
+
+    def edit(q, kv, kr):
+        q[::3, 0, 70] = float("nan")
+    for d in (64, 128):
+        c = expand_case(21, [300, 1, 130], [0, 10, 200], 2, d, edit=edit)
+        _, lse = expand_run(c)
+        assert torch.isnan(lse[:c["T"]:3, 0]).all() and torch.isfinite(lse[:c["T"], 1]).all()
+
+
 @pytest.mark.parametrize("latent", [0, 512])
 def test_empty_contexts_on_clusters(latent):
     """Fewer tiles than CTAs of a cluster, requests without tokens or pages, in tables that ask for clusters of eight."""
