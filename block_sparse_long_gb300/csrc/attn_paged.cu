@@ -526,19 +526,21 @@ __global__ void __launch_bounds__(S::kThreads, 1)
       }
     }
     if (ok && waiting) values();
-    // every copy lands before the CTA ends: the last use of each slot (those before it have landed, or it had not been taken)
+    // every copy lands before the CTA ends: the last use of each slot (those before it have landed, or it had not been taken); all of
+    // them have one wait's time together
     if (lane == 0) {
+      const uint64_t since = cosa::global_timer_ns();
       for (; pairs > 0; --pairs) {
         ring.back();
-        wait_parity_bounded(&sm.full[ring.at * S::kStep], ring.phase, nullptr, nullptr);
+        cosa::wait_until(&sm.full[ring.at * S::kStep], ring.phase, since);
       }
       for (; vpairs > 0; --vpairs) {
         vring.back();
-        wait_parity_bounded(&sm.full[vring.at * S::kStep + 1], vring.phase, nullptr, nullptr);
+        cosa::wait_until(&sm.full[vring.at * S::kStep + 1], vring.phase, since);
       }
       for (; ropes > 0; --ropes) {
         rope.back();
-        wait_parity_bounded(&sm.rope_full[rope.at], rope.phase, nullptr, nullptr);
+        cosa::wait_until(&sm.rope_full[rope.at], rope.phase, since);
       }
     }
     __syncwarp();

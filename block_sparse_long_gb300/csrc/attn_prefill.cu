@@ -242,17 +242,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (j >= diagonal) mbar_arrive(&sm.v_sent[j - diagonal]);
         }
       }
-      // every copy lands before the CTA ends: the last use of each slot
+      // every copy lands before the CTA ends: the last use of each slot; all have one wait's time together
       if (lane == 0 && !a.stall && nb > 0) {
-        wait_parity_bounded(&sm.q_full, 0, nullptr, nullptr);
+        const uint64_t since = cosa::global_timer_ns();
+        cosa::wait_until(&sm.q_full, 0, since);
         if (keys > values) kring.next();      // (the values of the last block had no place)
         for (; keys > 0; --keys) {
           kring.back();
-          wait_parity_bounded(&sm.k_full[kring.at], kring.phase, nullptr, nullptr);
+          cosa::wait_until(&sm.k_full[kring.at], kring.phase, since);
         }
         for (; values > 0; --values) {
           vring.back();
-          wait_parity_bounded(&sm.v_full[vring.at], vring.phase, nullptr, nullptr);
+          cosa::wait_until(&sm.v_full[vring.at], vring.phase, since);
         }
       }
       __syncwarp();

@@ -219,12 +219,6 @@ __device__ __forceinline__ void copy_bulk(void* dst, const void* src, uint32_t b
                : "memory");
 }
 
-// Waits for a barrier as long as a bounded wait that began at `since` (cosa::global_timer_ns) may take.
-__device__ __forceinline__ void wait_until(uint64_t* bar, uint32_t parity, uint64_t since) {
-  while (!cosa::mbar_try_wait(bar, parity) && cosa::global_timer_ns() - since <= COSA_WAIT_BUDGET_NS) {
-  }
-}
-
 // Cache policy for bytes that a call reads once: they make room in L2 first (the logits, which are read again, stay).
 __device__ __forceinline__ uint64_t read_once() {
   uint64_t policy;
@@ -478,7 +472,7 @@ __global__ void __launch_bounds__(kThreads, Steps<NT>::kCtas) attention_kernel(c
         for (int j = 0; j < kStages; ++j) {
           const int k = (stage + j) % kStages;
           if (!a.stall && t + j * kWarps < t_end && ((there >> (k * TP)) & ((1u << TP) - 1u)))
-            wait_until(&sm.full[warp][k], (phase >> k) & 1u, since);
+            cosa::wait_until(&sm.full[warp][k], (phase >> k) & 1u, since);
         }
         alive = false;
       }

@@ -91,6 +91,13 @@ __device__ __forceinline__ bool wait_parity_bounded(uint64_t* bar, uint32_t pari
   }
 }
 
+// Waits for a barrier as long as a bounded wait that began at `since` (global_timer_ns) may take: for what is in flight when a
+// kernel ends, several barriers with one budget together.
+__device__ __forceinline__ void wait_until(uint64_t* bar, uint32_t parity, uint64_t since) {
+  while (!mbar_try_wait(bar, parity) && global_timer_ns() - since <= COSA_WAIT_BUDGET_NS) {
+  }
+}
+
 // ----------------------------------------------------------------------------
 // proxies and fences
 // ----------------------------------------------------------------------------

@@ -1,0 +1,17 @@
+"""What the attentions of libcosa_attn wait for once a wait has run out: read from the source, since no test makes a copy get lost."""
+import os
+import re
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+@pytest.mark.parametrize("name,slots", [("attn_paged.cu", 3), ("attn_prefill.cu", 3)])
+def test_copies_in_flight_have_one_budget_together(name, slots):
+    """2 s, and 2 s more for the copies: not 2 s for each slot of the rings in turn."""
+    text = open(os.path.join(ROOT, "block_sparse_long_gb300", "csrc", name)).read()
+    drain = text[text.index("every copy lands before the CTA ends"):]
+    drain = drain[:drain.index("__syncwarp();")]
+    assert "wait_parity_bounded" not in drain
+    assert len(re.findall(r"wait_until\([^;]*, since\);", drain)) == slots and drain.count("global_timer_ns()") == 1
