@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c = 0; c < VC; ++c) cosa::tma_load_4d(sm.q[c], &qmap, &sm.q_full, 0, tok, c, head);
         cosa::tma_load_4d(sm.q[VC], &qrmap, &sm.q_full, 0, tok, 0, head);
       }
-      for (int j = 0; j < nb && ok; ++j, kring.next(), vring.next()) {
+      for (int j = 0; j < nb && ok; ++j) {
         if (keys == S::kSlots) ok = warp_wait(&sm.k_empty[kring.at], kring.phase ^ 1, abort_flag, a.status);
         else ++keys;
         if (!ok) break;
@@ -233,6 +233,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int c = 0; c < VC; ++c) cosa::tma_load_4d(sm.k[kring.at][c], &kmap, &sm.k_full[kring.at], 0, key + j * kBlock, c, head);
           cosa::tma_load_4d(sm.k[kring.at][VC], &krmap, &sm.k_full[kring.at], 0, key + j * kBlock, 0, 0);
         }
+        kring.next();
         if (values == S::kSlots) ok = warp_wait(&sm.v_empty[vring.at], vring.phase ^ 1, abort_flag, a.status);
         else ++values;
         if (!ok) break;
@@ -241,12 +242,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int c = 0; c < VC; ++c) cosa::tma_load_4d(sm.v[vring.at][c], &vmap, &sm.v_full[vring.at], 0, key + j * kBlock, c, head);
           if (j >= diagonal) mbar_arrive(&sm.v_sent[j - diagonal]);
         }
+        vring.next();
       }
       // every copy lands before the CTA ends: the last use of each slot; all have one wait's time together
       if (lane == 0 && !a.stall && nb > 0) {
         const uint64_t since = cosa::global_timer_ns();
         cosa::wait_until(&sm.q_full, 0, since);
-        if (keys > values) kring.next();      // (the values of the last block had no place)
         for (; keys > 0; --keys) {
           kring.back();
           cosa::wait_until(&sm.k_full[kring.at], kring.phase, since);

@@ -15,3 +15,13 @@ def test_copies_in_flight_have_one_budget_together(name, slots):
     drain = drain[:drain.index("__syncwarp();")]
     assert "wait_parity_bounded" not in drain
     assert len(re.findall(r"wait_until\([^;]*, since\);", drain)) == slots and drain.count("global_timer_ns()") == 1
+
+
+def test_keys_count_as_in_flight_once_they_are_copied():
+    """The expanded form's producer may give up between a block's keys and its values: the ring has moved past the keys by then, so
+    that those waited for are the last ones of each slot."""
+    text = open(os.path.join(ROOT, "block_sparse_long_gb300", "csrc", "attn_prefill.cu")).read()
+    copies = text[text.index("if (keys == S::kSlots)"):text.index("every copy lands before the CTA ends")]
+    assert copies.index("&krmap") < copies.index("kring.next();") < copies.index("if (values == S::kSlots)") < copies.index("vring.next();")
+    drain = text[text.index("every copy lands before the CTA ends"):]
+    assert "next()" not in drain[:drain.index("__syncwarp();")]
