@@ -60,6 +60,11 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
   return __all_sync(kAll, cosa::wait_parity_bounded(bar, parity, abort_flag, status));
 }
 
+// Whether a wait of this call has run out already: a CTA that starts then does nothing, since its waits would take as long again.
+__device__ __forceinline__ bool gave_up(const int* status) {
+  return status != nullptr && *static_cast<const volatile int*>(status) == cosa::kStatusDeviceTimeout;
+}
+
 // Of eight bf16 values: nonzero if one is not finite (its exponent, all ones, carries into the sign's place), and zeros for those.
 __device__ __forceinline__ uint32_t odd(const uint4& x) {
   constexpr uint32_t kExp = 0x7F807F80u, kOne = 0x00800080u;

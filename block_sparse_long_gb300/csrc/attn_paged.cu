@@ -405,9 +405,11 @@ __global__ void __launch_bounds__(S::kThreads, 1)
   if (a.cluster > 1) cluster_arrive();      // (waited for before the first store to another CTA)
 
   if (warp == 0) {
+    const bool over = gave_up(a.status);
     const Start<N> st = find_start<N>(a, cta == 0);
     if (lane == 0) {
       sm.start = st;
+      if (over) sm.start.any = false;
       if (cta == 0 && (a.cu_seqlens[0] != 0 || a.cu_seqlens[a.num_reqs] > a.total_tokens)) cosa::report_status(a.status, cosa::kStatusBadInput);
     }
   } else if (warp == 1 && lane == 0) {

@@ -133,6 +133,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int heads = min(kHeads, a.num_heads), group = blockIdx.x / (a.blocks * heads), in_group = min(heads, a.num_heads - group * heads);
   const int in = blockIdx.x - group * a.blocks * heads, head = group * heads + in % in_group;
   if (warp == 0) {
+    const bool over = gave_up(a.status);
     int at = in / in_group, req = -1, block = 0;      // which of all requests' blocks
     if (a.num_reqs <= 32) {
       // by what lies before them, the longest rows first: block i of a request has about before + i blocks of keys
@@ -173,7 +174,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     if (lane == 0) {
-      sm.req = req;
+      sm.req = over ? -1 : req;
       sm.block = block;
       if (blockIdx.x == 0 && (a.cu_seqlens[0] != 0 || a.cu_seqlens[a.num_reqs] > a.total_tokens)) cosa::report_status(a.status, cosa::kStatusBadInput);
     }

@@ -27,7 +27,10 @@
  *     total_tokens are not written; a cu_seqlens that falls may leave all rows unwritten), the commit leaves its slots as they are, and cosa_latent_rope leaves out (writes nothing
  *     of) the tokens of no request and those whose slot is negative or, where a cache is written, not below max_seqlen.
  *     A wait inside an attention kernel that runs out after 2 s gives COSA_ERR_DEVICE_TIMEOUT; the kernel ends
- *     once the copies in flight have landed, after 2 s more at the latest, and the outputs are then undefined.
+ *     once the copies in flight have landed, after 2 s more at the latest, and the outputs are then undefined.  CTAs that
+ *     start after that see it in *device_status and do nothing; a status that is not zeroed after it leaves the outputs of
+ *     later attentions undefined too.  Without device_status, or where it holds another error already, every wave of
+ *     CTAs takes that long.
  *   - Requests are packed by cu_seqlens int32 [num_reqs + 1] (cu_seqlens[0] = 0, non-decreasing, last
  *     entry <= total_tokens); rows behind the last request are neither read nor written.
  *   - A cache slot is a token's place in its request: slot s of request b is row s % P of logical page

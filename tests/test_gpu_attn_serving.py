@@ -180,6 +180,35 @@ def test_prefill_waits_that_run_out():
     expand_run(c)
 
 
+@pytest.mark.parametrize("form", ["prefill", "clusters"])
+def test_ctas_that_start_after_a_timeout_end_at_once(form):
+    """More CTAs than run at a time: one wait's time for all of them, not for each wave."""
+    if form == "prefill":
+        from tests.test_gpu_attn import expand_case, expand_run
+        c = expand_case(4, [128 * 40, 128 * 30], [0, 10], 9, 64)       # 630 CTAs, one to an SM
+        p, args = c["p"], c["args"]
+        def call(**kw):
+            C.cosa_latent_prefill(p, *args, cu_kv=c["cu_kv"], **kw)
+    else:
+        c = Paged(7, [1000] * 15, [1] * 15, 4, 1, 128, 64)
+        assert path(c.p, 0) == "cluster 8"                             # 19 clusters, as many as 152 SMs would hold
+        p, call = c.p, c.call
+    call()
+    torch.cuda.synchronize()
+    p.flags |= C.COSA_ATTN_FLAG_TEST_STALL
+    st, t0 = new_status(), time.time()
+    call(status=st)
+    torch.cuda.synchronize()
+    assert int(st) == -4 and 1.5 < time.time() - t0 < 3.5
+    p.flags = 0
+    if form == "prefill":
+        expand_run(c, check=False)
+    else:
+        out, lse = c.buffers()
+        c.call(out=out, lse=lse)
+        c.check(out, lse)
+
+
 # ---------------------------------------------------------------------------------------------------------------
 # a step with drafted tokens: norm and rotation, tree attention, commit, and the next step over what was kept
 # ---------------------------------------------------------------------------------------------------------------
