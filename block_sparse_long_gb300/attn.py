@@ -100,7 +100,7 @@ def _calls():
         try:
             module = importlib.import_module("._attn_call", __package__)
         except ImportError as e:
-            raise RuntimeError("_attn_call is missing: build it with `python -m block_sparse_long_gb300.build`") from e
+            raise RuntimeError(f"_attn_call cannot be loaded ({e}): build it with `python -m block_sparse_long_gb300.build`") from e
         lib = attn_library()
         module.bind(*(ctypes.cast(getattr(lib, "cosa_" + name), ctypes.c_void_p).value for name in (
             "tree_attention", "latent_attention", "tree_commit", "latent_rope", "latent_prefill")))

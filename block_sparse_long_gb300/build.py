@@ -11,6 +11,7 @@ without a GPU (their calls then fail with COSA_ERR_CUDA).
 """
 from __future__ import annotations
 
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -53,6 +54,7 @@ def _inputs(sources, headers, public):
 # host code against PyTorch's headers: its suffix names the interpreter and the machine
 CALL = os.path.join(HERE, "_attn_call" + sysconfig.get_config_var("EXT_SUFFIX"))
 CALL_SOURCES = ["attn_binding.cpp"]
+CALL_TORCH = os.path.join(BUILD, "attn_call.torch")      # the torch that it was compiled against
 
 # library, its translation units, the headers they include
 LIBRARIES = ((LIB, SOURCES, HEADERS, ["cosa.h"]), (KV_LIB, KV_SOURCES, KV_HEADERS, ["cosa.h", "cosa_kv.h"]),
@@ -66,8 +68,22 @@ def _stale(lib, sources, headers, public) -> bool:
     return any(os.path.getmtime(f) > t for f in _inputs(sources, headers, public))
 
 
+def _torch_version() -> str:
+    """What names the torch that is there, without importing it: its version file."""
+    with open(os.path.join(os.path.dirname(importlib.util.find_spec("torch").origin), "version.py")) as f:
+        return f.read()
+
+
+def _call_stale() -> bool:
+    """The module reads tensors in place, by the headers of the torch that it was compiled against: another one needs another build."""
+    if _stale(CALL, CALL_SOURCES, [], ["cosa.h", "cosa_attn.h"]) or not os.path.exists(CALL_TORCH):
+        return True
+    with open(CALL_TORCH) as f:
+        return f.read() != _torch_version()
+
+
 def up_to_date() -> bool:
-    return not any(_stale(*entry) for entry in LIBRARIES) and not _stale(CALL, CALL_SOURCES, [], ["cosa.h", "cosa_attn.h"])
+    return not any(_stale(*entry) for entry in LIBRARIES) and not _call_stale()
 
 
 def _build_call() -> None:
@@ -84,12 +100,15 @@ def _build_call() -> None:
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on {CALL_SOURCES[0]}:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, CALL)
+    os.makedirs(BUILD, exist_ok=True)
+    with open(CALL_TORCH, "w") as f:
+        f.write(_torch_version())
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile and link the libraries whose inputs changed; returns the path of libcosa.so."""
     todo = [entry for entry in LIBRARIES if force or _stale(*entry)]
-    call = force or _stale(CALL, CALL_SOURCES, [], ["cosa.h", "cosa_attn.h"])
+    call = force or _call_stale()
     if not todo:
         if call:
             _build_call()
