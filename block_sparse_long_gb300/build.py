@@ -132,8 +132,6 @@ def build(force: bool = False, verbose: bool = False) -> str:
     with ThreadPoolExecutor(len(sources) + 1) as ex:
         other = ex.submit(_build_call) if call else None
         objs = dict(zip(sources, ex.map(compile_one, sources)))
-        if other is not None:
-            other.result()
     for lib, srcs, _, _ in todo:
         tmp = lib + ".tmp"
         cmd = [cc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *(objs[src] for src in srcs)]
@@ -141,6 +139,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, lib)
+    if other is not None:
+        other.result()      # (the libraries need nothing of it)
     return LIB
 
 

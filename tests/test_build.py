@@ -29,6 +29,21 @@ def test_the_version_is_that_of_the_torch_that_is_imported():
     assert f"'{torch.__version__}'" in B._torch_version()
 
 
+def test_libraries_are_linked_whatever_becomes_of_the_module(monkeypatch, tmp_path):
+    """A g++ that fails on the Python module is reported, and stops none of the CUDA libraries."""
+    source, lib = tmp_path / "one.cu", str(tmp_path / "libone.so")
+    source.write_text('extern "C" int one() { return 1; }\n')
+
+    def fail():
+        raise RuntimeError("g++ failed")
+    for name, value in (("CSRC", str(tmp_path)), ("BUILD", str(tmp_path)), ("LIBRARIES", ((lib, ["one.cu"], [], []),)),
+                        ("_call_stale", lambda: True), ("_build_call", fail)):
+        monkeypatch.setattr(B, name, value)
+    with pytest.raises(RuntimeError, match="g\\+\\+ failed"):
+        B.build()
+    assert os.path.exists(lib)
+
+
 def test_a_module_that_cannot_be_loaded_says_why(monkeypatch):
     from block_sparse_long_gb300 import attn
 
