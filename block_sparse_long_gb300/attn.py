@@ -57,12 +57,24 @@ COSA_ATTN_FLAG_TEST_STALL = 4   # test hook of the attentions: every in-kernel w
 
 
 class CosaAttnParams(ctypes.Structure):
-    """Mirror of ``cosa_attn_params``."""
+    """Mirror of ``cosa_attn_params``.  scale_given is False, in copies too, while sm_scale is the default of make_attn_params."""
     _fields_ = [(n, ctypes.c_int32) for n in (
         "num_reqs", "num_q_heads", "num_kv_heads", "head_dim", "latent_dim", "page_size", "total_tokens", "total_kv_tokens",
         "max_seqlen", "num_pages", "max_pages_per_req", "max_new_tokens", "flags", "reserved")] + [(n, ctypes.c_int64) for n in (
             "q_stride", "q_head_stride", "q_rope_stride", "q_rope_head_stride", "k_stride", "k_head_stride", "k_rope_stride",
             "v_stride", "v_head_stride")] + [("sm_scale", ctypes.c_double), ("norm_eps", ctypes.c_double)]
+    scale_given = True
+
+    def __setattr__(self, name, value):
+        super().__setattr__(name, value)
+        if name == "sm_scale":
+            super().__setattr__("scale_given", True)
+
+    @classmethod
+    def from_buffer_copy(cls, source, offset=0):
+        made = type(cls).from_buffer_copy(cls, source, offset)
+        made.scale_given = getattr(source, "scale_given", True)
+        return made
 
 
 _lib = None
@@ -115,13 +127,21 @@ def cosa_attn_version() -> int:
 def make_attn_params(*, num_reqs, num_q_heads, num_kv_heads=1, head_dim=128, latent_dim=512, page_size=64, total_tokens=0,
                      total_kv_tokens=0, max_seqlen=1, num_pages=1, max_pages_per_req=1, max_new_tokens=1, interleaved=False,
                      sm_scale=None, norm_eps=1e-6) -> CosaAttnParams:
-    """sm_scale defaults to 1/sqrt(head_dim), the tree attention's; latent attention's is 1/sqrt(head_dim + 64)."""
-    return CosaAttnParams(
+    """sm_scale defaults to 1/sqrt(head_dim), the tree attention's.  Both forms of latent attention, whose scale is as a rule
+    1/sqrt(d + 64) with heads of d + 64 values, refuse that default."""
+    p = CosaAttnParams(
         num_reqs=num_reqs, num_q_heads=num_q_heads, num_kv_heads=num_kv_heads, head_dim=head_dim, latent_dim=latent_dim,
         page_size=page_size, total_tokens=total_tokens, total_kv_tokens=total_kv_tokens, max_seqlen=max_seqlen,
         num_pages=num_pages, max_pages_per_req=max_pages_per_req, max_new_tokens=max_new_tokens,
         flags=COSA_ATTN_FLAG_INTERLEAVED if interleaved else 0,
         sm_scale=float(sm_scale if sm_scale is not None else 1.0 / math.sqrt(head_dim)), norm_eps=float(norm_eps))
+    p.scale_given = sm_scale is not None
+    return p
+
+
+def _latent_scale(p: CosaAttnParams) -> None:
+    if not p.scale_given:
+        raise ValueError("sm_scale is the default of make_attn_params, the tree attention's: give latent attention its own")
 
 
 def latent_cache_shape(num_pages: int, page_size: int, latent_dim: int) -> Tuple[int, int, int]:
@@ -223,7 +243,8 @@ def cosa_latent_attention(p: CosaAttnParams, q_latent: torch.Tensor, q_rope: tor
                           lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
                           status: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """Attention of the newest tokens, queries q_latent [T, Hq, latent_dim] and q_rope [T, Hq, 64], over the pages of latent
-    vectors; returns out bf16 [T, Hq, latent_dim].  The rest as in cosa_tree_attention."""
+    vectors; returns out bf16 [T, Hq, latent_dim].  p has an sm_scale of its own.  The rest as in cosa_tree_attention."""
+    _latent_scale(p)
     if out is None:
         out = _empty(q_latent, (p.total_tokens, p.num_q_heads, p.latent_dim), torch.bfloat16, stream)
     if workspace is None:
@@ -241,7 +262,9 @@ def cosa_latent_prefill(p: CosaAttnParams, q_nope: torch.Tensor, q_rope: torch.T
                         status: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """Causal attention of prompts packed by cu_seqlens: queries q_nope [T, Hq, d] and q_rope [T, Hq, 64], keys k_nope
     [Tk, Hq, d] and, shared by the heads, k_rope [Tk, 64], values v [Tk, Hq, d], packed by cu_kv (without it, by cu_seqlens; a
-    request's queries are the last of its keys); tokens and heads may lie apart.  Returns out bf16 [T, Hq, d]."""
+    request's queries are the last of its keys); tokens and heads may lie apart.  p has an sm_scale of its own.  Returns out bf16
+    [T, Hq, d]."""
+    _latent_scale(p)
     if out is None:
         out = _empty(q_nope, (p.total_tokens, p.num_q_heads, p.head_dim), torch.bfloat16, stream)
     rc = (_module or _calls()).latent_prefill(p, q_nope, q_rope, k_nope, k_rope, v, cu_seqlens, cu_kv, out, lse, status, stream)

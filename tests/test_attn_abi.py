@@ -1,4 +1,5 @@
 """libcosa_attn loads without a GPU, exports what include/cosa_attn.h declares, and refuses bad arguments on the host."""
+import copy
 import ctypes
 import os
 import re
@@ -187,3 +188,20 @@ def test_sizes(C):
     assert need["out"] == 10 * 8 * 128 and need["latent_out"] == 10 * 8 * 512 and need["k_cache"] == 40 * 64 * 2 * 128
     assert need["latent_cache"] == 40 * 64 * 576 and need["path"] == 16 and need["lse"] == 80 and need["page_table"] == 32
     assert C.latent_cache_shape(3, 16, 256) == (3, 16, 320)
+
+
+def test_latent_attention_refuses_the_default_scale(C):
+    """It is the tree attention's, 1/sqrt(head_dim): a copy of the parameters has it too, one that was set does not."""
+    given = params(C)
+    assert not given.scale_given and given.sm_scale == pytest.approx(128 ** -0.5)
+    q, r, cu, pt, n = torch.zeros(10, 8, 128, dtype=torch.bfloat16), torch.zeros(10, 8, 64, dtype=torch.bfloat16), *(torch.zeros(40, dtype=torch.int32) for _ in range(3))
+    for p in (given, C.CosaAttnParams.from_buffer_copy(given), copy.copy(given)):
+        with pytest.raises(ValueError, match="sm_scale"):
+            C.cosa_latent_attention(p, q, r, cu, q, pt, n)
+        with pytest.raises(ValueError, match="sm_scale"):
+            C.cosa_latent_prefill(p, q, r, q, r[:, 0], q, cu)
+    for p in (params(C, sm_scale=192 ** -0.5), C.make_attn_params(num_reqs=1, num_q_heads=1, sm_scale=128 ** -0.5)):
+        for p in (p, C.CosaAttnParams.from_buffer_copy(p), copy.copy(p)):
+            assert p.scale_given
+            with pytest.raises(ValueError, match="q_latent must be|must be a CUDA"):
+                C.cosa_latent_attention(p, q, r, cu, q, pt, n)
