@@ -281,6 +281,7 @@ int cosa_latent_prefill(const cosa_attn_params* p, const void* q_nope, const voi
     return COSA_ERR_INVALID_ARG;
   L.k_rope_stride = stride_of(p->k_rope_stride, kRot);
   if (L.k_rope_stride < 0) return COSA_ERR_INVALID_ARG;
+  if (!cosa_attn::prefill_fits(p->total_tokens, p->num_reqs, p->num_q_heads)) return COSA_ERR_UNSUPPORTED;
   if (p->total_tokens == 0) return COSA_OK;
   if (!q_nope || !q_rope || !cu_seqlens || !out) return COSA_ERR_INVALID_ARG;
   if (p->total_kv_tokens < 1 || !k_nope || !k_rope || !v) return COSA_ERR_INVALID_ARG;

@@ -60,6 +60,7 @@ struct PrefillLaunch {
   float scale_log2;
   bool stall;
 };
+bool prefill_fits(int total_tokens, int num_reqs, int num_heads);      // its CTAs are numbered in 31 bits
 cudaError_t launch_prefill(const PrefillLaunch& L, cudaStream_t stream);
 
 }  // namespace cosa_attn

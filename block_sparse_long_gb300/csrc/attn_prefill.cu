@@ -494,6 +494,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+// At most so many blocks of queries: what the tokens fill and a part of one for every request.
+int64_t most_blocks(int64_t total_tokens, int64_t num_reqs) { return total_tokens / kRows + num_reqs; }
+
 template <int D>
 cudaError_t launch_shape(const PrefillLaunch& L, cudaStream_t stream) {
   using S = Shape<D>;
@@ -512,9 +515,7 @@ cudaError_t launch_shape(const PrefillLaunch& L, cudaStream_t stream) {
   a.total_kv_tokens = L.total_kv_tokens;
   a.scale_log2 = L.scale_log2;
   a.stall = L.stall;
-  // at most so many blocks of queries: what the tokens fill and a part of one for every request
-  const int64_t blocks = L.total_tokens / kRows + L.num_reqs;
-  if (blocks * L.num_heads > INT32_MAX) return cudaErrorInvalidValue;
+  const int64_t blocks = most_blocks(L.total_tokens, L.num_reqs);
   a.blocks = static_cast<int>(blocks);
   // rows as (64 values, token, 64-value column, head)
   CUtensorMap maps[5];
@@ -542,6 +543,8 @@ cudaError_t launch_shape(const PrefillLaunch& L, cudaStream_t stream) {
 }
 
 }  // namespace
+
+bool prefill_fits(int total_tokens, int num_reqs, int num_heads) { return most_blocks(total_tokens, num_reqs) * num_heads <= INT32_MAX; }
 
 cudaError_t launch_prefill(const PrefillLaunch& L, cudaStream_t stream) {
   return L.head_dim == 128 ? launch_shape<128>(L, stream) : launch_shape<64>(L, stream);

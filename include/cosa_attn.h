@@ -43,7 +43,8 @@
  *     of its mask is set (itself only if bit i is), and n is at most 64; bits from n on are ignored.
  *     A row that sees nothing gives 0, and -inf for its lse.  What a row does not see, infinities and NaN among it, does
  *     not change it.
- *     A batch whose tiles of 128 slots, by max_seqlen, times row tiles pass 31 bits is refused.
+ *     A batch whose tiles of 128 slots, by max_seqlen, times row tiles pass 31 bits is refused; so is one of the expanded form
+ *     whose (total_tokens / 128 + num_reqs) * Hq do.
  *   - lse, float32 [total_tokens, Hq] or NULL: the natural logarithm of the sum of exp(logit) over what the row sees.
  *   - Tensors are bf16 unless noted, 16-byte aligned.  Strides are in elements, multiples of 8, and 0 for dense; heads lie
  *     within a token or tokens within a head, without overlap.

@@ -120,6 +120,13 @@ def test_parameters_refused(C):
         assert call(C, params(C, num_q_heads=1 << 14, total_tokens=1 << 18)) == UNS
 
 
+def test_prefill_of_more_blocks_than_a_grid_has(C):
+    """Blocks of 128 queries, one at least for a request, times heads: what a launch cannot number is refused as such."""
+    for kw in (dict(num_reqs=60000, num_q_heads=60000, total_tokens=10), dict(num_reqs=65535, num_q_heads=32769, total_tokens=65535)):
+        assert prefill(C, params(C, **kw)) == UNS
+    assert prefill(C, params(C, num_reqs=60000, num_q_heads=30000, total_tokens=0)) == 0
+
+
 def test_attention_arguments_refused(C):
     p = params(C)
     for call, names in ((tree, ("q", "k", "v", "pt", "n", "cu", "out")), (latent, ("q", "qr", "k", "pt", "n", "cu", "out")),
