@@ -303,7 +303,6 @@ int cosa_latent_prefill(const cosa_attn_params* p, const void* q_nope, const voi
   L.head_dim = p->head_dim;
   L.total_tokens = p->total_tokens;
   L.total_kv_tokens = p->total_kv_tokens;
-  L.max_new_tokens = p->max_new_tokens;
   L.scale_log2 = static_cast<float>(p->sm_scale * 1.4426950408889634074);
   L.stall = (p->flags & COSA_ATTN_FLAG_TEST_STALL) != 0;
   return done(cosa_attn::launch_prefill(L, static_cast<cudaStream_t>(stream)));

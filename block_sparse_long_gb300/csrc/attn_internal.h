@@ -56,7 +56,7 @@ struct PrefillLaunch {
   float* lse;
   int32_t* status;
   int64_t q_stride, q_head_stride, q_rope_stride, q_rope_head_stride, k_stride, k_head_stride, k_rope_stride, v_stride, v_head_stride;
-  int num_reqs, num_heads, head_dim, total_tokens, total_kv_tokens, max_new_tokens;
+  int num_reqs, num_heads, head_dim, total_tokens, total_kv_tokens;
   float scale_log2;
   bool stall;
 };

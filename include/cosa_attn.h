@@ -76,11 +76,12 @@ extern "C" {
    2 s budget, the kernel ends, *device_status becomes COSA_ERR_DEVICE_TIMEOUT and the outputs are undefined. */
 #define COSA_ATTN_FLAG_TEST_STALL 4
 
-/* Fields that a call has no use for are ignored by it. */
+/* Every call checks num_reqs, num_q_heads, total_tokens, flags and reserved, the three attentions max_new_tokens too; other fields that
+   a call has no use for are ignored by it. */
 typedef struct cosa_attn_params {
   int32_t num_reqs;          /* B >= 1                                                          */
   int32_t num_q_heads;       /* Hq >= 1                                                         */
-  int32_t num_kv_heads;      /* Hkv >= 1, Hq % Hkv == 0 (tree attention, commit)                */
+  int32_t num_kv_heads;      /* Hkv >= 1, Hq % Hkv == 0 (tree attention)                        */
   int32_t head_dim;          /* d: 64 or 128 (tree attention; prefill: values of k_nope and v)  */
   int32_t latent_dim;        /* values of a latent vector: 256 or 512                           */
   int32_t page_size;         /* P: 16, 32, 64 or 128                                            */
@@ -89,9 +90,10 @@ typedef struct cosa_attn_params {
   int32_t max_seqlen;        /* >= every context length                                         */
   int32_t num_pages;         /* pages of each cache                                             */
   int32_t max_pages_per_req; /* row pitch of the page table, >= ceil(max_seqlen / P)            */
-  int32_t max_new_tokens;    /* attentions: query tokens per request to tile for (any value >= 1
-                                is right; the largest request's is fastest); commit: row pitch
-                                of path, at most 64                                             */
+  int32_t max_new_tokens;    /* attentions over pages: query tokens per request to tile for (any
+                                value >= 1 is right; the largest request's is fastest; the
+                                expanded form, >= 1 too, does not use it); commit: row pitch of
+                                path, at most 64                                                */
   int32_t flags;             /* COSA_ATTN_FLAG_*                                                */
   int32_t reserved;          /* 0                                                               */
   int64_t q_stride;          /* between tokens of q (tree), q_latent, q_nope                    */

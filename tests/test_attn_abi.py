@@ -127,6 +127,16 @@ def test_prefill_of_more_blocks_than_a_grid_has(C):
     assert prefill(C, params(C, num_reqs=60000, num_q_heads=30000, total_tokens=0)) == 0
 
 
+def test_fields_without_use_are_ignored(C):
+    """What the header says of them, on calls without tokens, which do nothing."""
+    slots = dict(page_size=3, max_seqlen=0, num_pages=0, max_pages_per_req=0)
+    for call, junk in ((tree, dict(latent_dim=7, total_kv_tokens=-1, norm_eps=-1.0)), (latent, dict(num_kv_heads=0, head_dim=1, total_kv_tokens=-1)),
+                       (prefill, dict(slots, num_kv_heads=0, latent_dim=7, norm_eps=-1.0)),
+                       (rope, dict(num_kv_heads=0, head_dim=1, total_kv_tokens=-1, max_new_tokens=0, sm_scale=0.0))):
+        assert call(C, params(C, total_tokens=0, **junk)) == 0, call
+    assert rope(C, params(C, total_tokens=0, **slots), cache=None, pt=None) == 0
+
+
 def test_attention_arguments_refused(C):
     p = params(C)
     for call, names in ((tree, ("q", "k", "v", "pt", "n", "cu", "out")), (latent, ("q", "qr", "k", "pt", "n", "cu", "out")),
