@@ -138,7 +138,7 @@ int run_paged(const cosa_attn_params* p, bool latent, const void* q, const void*
   cosa_attn::PagedLaunch L = paged_of(p, latent);
   query_strides(p, latent, &L);
   if (!workspace || !aligned(256, workspace) || workspace_bytes < cosa_attn::paged_workspace_bytes(L)) return COSA_ERR_WORKSPACE;
-  if (out == q) return COSA_ERR_INVALID_ARG;      // CTAs that share a row's keys write it while others read its query
+  if (out == q || out == q_rope) return COSA_ERR_INVALID_ARG;      // CTAs that share a row's keys write it while others read its query
   L.q = as<uint16_t>(q);
   L.q_rope = as<uint16_t>(q_rope);
   L.k_cache = as<uint16_t>(k_cache);
@@ -193,8 +193,10 @@ int cosa_tree_commit(const cosa_attn_params* p, void* cache_a, void* cache_b, in
   if (!cache_a || !cu_seqlens || !page_table || !kv_len || !path || !path_len || !new_len) return COSA_ERR_INVALID_ARG;
   if (!aligned(16, cache_a, cache_b) || !aligned(4, cu_seqlens, page_table, kv_len, path, path_len, new_len, device_status))
     return COSA_ERR_INVALID_ARG;
-  // the CTAs of a request read the one while another writes the other; two caches in one would be moved twice
-  if (new_len == kv_len || new_len == path_len || cache_a == cache_b) return COSA_ERR_INVALID_ARG;
+  // CTAs read these while one has written new_len already; two caches in one would be moved twice
+  for (const int32_t* read : {cu_seqlens, page_table, kv_len, path, path_len})
+    if (new_len == read) return COSA_ERR_INVALID_ARG;
+  if (cache_a == cache_b) return COSA_ERR_INVALID_ARG;
   cosa_attn::CommitLaunch L{};
   L.cache_a = static_cast<uint16_t*>(cache_a);
   L.cache_b = static_cast<uint16_t*>(cache_b);

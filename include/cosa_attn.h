@@ -136,7 +136,7 @@ int cosa_tree_attention(const cosa_attn_params* p, const void* q, const int32_t*
  *   path              int32 [num_reqs, max_new_tokens]
  *   path_len          int32 [num_reqs], 0 .. min(n, max_new_tokens)
  *   new_len           out: int32 [num_reqs], kv_len[b] - n + path_len[b], or kv_len[b] for a request that contradicts
- *                     itself; not kv_len itself
+ *                     itself; none of the inputs
  */
 int cosa_tree_commit(const cosa_attn_params* p, void* cache_a, void* cache_b, int32_t row_elems, const int32_t* cu_seqlens,
                      const int32_t* page_table, const int32_t* kv_len, const int32_t* path, const int32_t* path_len,
@@ -168,7 +168,7 @@ int cosa_latent_rope(const cosa_attn_params* p, const void* kv, const void* q, c
  *   q_latent   [total_tokens, Hq, latent_dim], tokens q_stride and heads q_head_stride apart
  *   q_rope     [total_tokens, Hq, 64], tokens q_rope_stride and heads q_rope_head_stride apart
  *   tree_mask  int64 [total_tokens], or NULL
- *   out        [total_tokens, Hq, latent_dim] dense, not q_latent itself
+ *   out        [total_tokens, Hq, latent_dim] dense, neither q_latent nor q_rope itself
  *   workspace  at least cosa_latent_attention_workspace_size(p) bytes, as above
  */
 size_t cosa_latent_attention_workspace_size(const cosa_attn_params* p);

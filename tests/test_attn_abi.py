@@ -156,6 +156,13 @@ def test_attention_arguments_refused(C):
         assert prefill(C, p, **{name: G}) == INV                        # out is an input
 
 
+def test_outputs_that_other_ctas_still_read(C):
+    H = ctypes.c_void_p(16384)
+    assert latent(C, params(C), qr=G) == INV                             # out is q_rope
+    for name in ("cu", "pt", "n", "path", "m"):
+        assert commit(C, params(C), **{name: H}, new=H) == INV           # new_len is an input
+
+
 def test_commit_arguments_refused(C):
     p = params(C)
     for name in ("a", "cu", "pt", "n", "path", "m", "new"):
