@@ -12,18 +12,18 @@
 //   More rows (kRowLanes): the 128 rows of the product are query rows, S = Q K^T, O = P V with P in TMEM, so that a softmax thread has a
 //   row (half of its slots), needs no other thread's maximum and keeps the reference in a register.  64 new tokens of 4 heads to a
 //   kv head after 128K slots: 231 us with the rows as 128 columns, 177 with a quarter of the slots to a thread, with half of them (fewer
-//   warps, none of whose registers spill) and pages looked up a tile ahead 11 % less.
+//   warps, of whose 168 registers 4 to 8 bytes spill) and pages looked up a tile ahead 11 % less.
 //
 // A CTA per SM.  The tiles of all (request, kv head, row tile) items stand in one list, which the CTAs share evenly, one unit per
 // tile and one per item; a CTA's piece of an item that others have too leaves m, l and o (32 bits) in the workspace and
 // join_kernel puts them together.  Short contexts go whole to a CTA or to a cluster that joins them through distributed shared
-// memory (900 slots: list and join 12.4 us, cluster 10.5).  With several row tiles of 128 rows to the same keys as many CTAs walk the
+// memory (900 slots: list and join 10.3 us, cluster 8.9).  With several row tiles of 128 rows to the same keys as many CTAs walk the
 // list together, a CTA to a row tile, so that HBM is read once (the same 128K: 177 us apart, 140 together; then 125 as above).
 //
-// What bounds it (32 query over 8 kv heads of 128, 64-slot pages): 13-token trees of 24 ragged contexts 159 us, 5.6 TB/s; 64 tokens
-// after 128K 125 us, 4.3 TB/s and 1.1 PFLOP/s, a tile's chain of product, softmax, product (2000 cycles, of which the products run
-// 1024); one token after 900 slots 8.8 us, the chain of first loads, products and join.  Latent vectors of 512 + 64, 32 heads: one token after
-// 128K 42 us, 3.6 TB/s; 7 tokens of 24 ragged contexts 142 us: a tile (147 KB) fills shared memory, so a block of the next can only be copied
+// What bounds it (32 query over 8 kv heads of 128, 64-slot pages): 13-token trees of 24 ragged contexts 158 us, 5.7 TB/s; 64 tokens
+// after 128K 124 us, 4.3 TB/s and 1.1 PFLOP/s, a tile's chain of product, softmax, product (2000 cycles, of which the products run
+// 1024); one token after 900 slots 8.9 us, the chain of first loads, products and join.  Latent vectors of 512 + 64, 32 heads: one token after
+// 128K 43 us, 3.5 TB/s; 7 tokens of 24 ragged contexts 144 us: a tile (147 KB) fills shared memory, so a block of the next can only be copied
 // once the second product is done with it (6000 cycles a tile, of which the products run 3300).
 //
 // Warp roles:
@@ -81,6 +81,7 @@ struct Shape {
   static constexpr bool kRowLanes = N == 128;                    // a query row per TMEM lane: S = Q K^T, O = P V, P in TMEM
   static constexpr int kGroups = N == 16 ? 1 : N == 64 ? 4 : 2;  // warpgroups of the softmax
   static constexpr int NC = kRowLanes ? 1 : 16;                  // query rows of a softmax thread
+  // Row tiles of 64 have 640 threads and so 96 registers each, of which 20 bytes (latent vectors of 512) or 120 (of 256) spill.
   static constexpr int kThreads = 128 + 128 * kGroups;
   static constexpr int kBlocks = DV > 128 ? DV / 128 : 1;        // of 128 output values
   static constexpr int kPairs = LATENT ? DV / 128 : DK == 128 ? 2 : 1;      // ring slots of a tile; 64 + 64: K and V in one
@@ -354,7 +355,7 @@ __device__ __forceinline__ void store_remote(const void* to, int rank, float2 x)
 __device__ __forceinline__ void cluster_barrier() {
   asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
-// The first of them in halves: it orders no memory (900 slots of one token: 9.3 us, 9.45 with a release).
+// The first of them in halves: it orders no memory (900 slots of one token: 0.15 us less than with a release).
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 
@@ -1351,9 +1352,12 @@ cudaError_t launch_shape(const PagedLaunch& L, cudaStream_t stream) {
   a.cluster = 1;
   // How the items are shared, by the tiles that a CTA then has at most (lengths are known to the device only: max_seqlen's): all tiles
   // in one list, cut anywhere, and a second kernel to join (about kJoin tiles' time); whole items to a CTA; or an item to a cluster.
-  // One token each, list / whole / cluster: 1 context of 900 (32 heads over 8 of 128) 10.2 / 11.7 / 8.6 us, 4 of 900 13.8 / 12.4 / 11.0,
-  // 64 of 300 33.7 / 30.6 / -, 4 of 4000 22.5 / 29.9 / -; latent 512 of 16 heads: 9 of 900 14.6 / - / 13.1, 150 of 900 46 / 41 / -,
-  // 200 of 900 62 / 69 / -.
+  // One token each, list / whole / cluster: 1 context of 900 (32 heads over 8 of 128) 10.3 / 11.7 / 8.9 us, 4 of 900 13.4 / 12.1 / 10.9,
+  // 64 of 300 33.0 / 30.4 / -, 4 of 4000 22.3 / 28.3 / -; latent 512 of 16 heads: 9 of 900 14.6 / 26.2 / 13.2, 150 of 900 46.0 / 41.4 / -,
+  // 200 of 900 62 / 69 / -.  Not always the best: one latent token after 900 11.8 / 25.9 / 12.6, 64 tokens after 900 17.3 / 16.4 / 18.5.
+  // All of these have equal lengths, and what the rule knows is max_seqlen and an upper bound of the items.  A batch of other lengths can wait
+  // for few long items where it takes whole ones or clusters (counted in tiles: 31 requests, one of 128K and thirty of 1000, 2050 to a CTA
+  // where the list has 68), and where rows fill their row tile exactly the bound is twice the items, so that half of the card may idle.
   constexpr double kJoin = S::kLatent ? 2.5 : 5;
   const double tiles = (L.max_seqlen + kTile - 1) / kTile;
   double best = items * (tiles + 1) / kCtas + kJoin;

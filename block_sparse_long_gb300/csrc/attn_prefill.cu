@@ -28,7 +28,7 @@
 // heads of 64, 8192 tokens of 16: 242 -> 231 us, 4096 of 8 heads of 128: 65 -> 67).
 //
 // What bounds it now: at 16K tokens of 16 heads of 128 + 64 1.01 ms, 1.36 PFLOP/s of the pairs that are seen; 5 prompts of 37 to 2011 tokens
-// of 6 heads of 64 39 us: 390 CTAs of up to 19 blocks on 152 SMs, each of which waits 3700 to 7300 cycles for its first loads.
+// of 6 heads of 64 40 us: 390 CTAs of up to 19 blocks on 152 SMs, each of which waits 3700 to 7300 cycles for its first loads.
 #include <cmath>
 #include <cstdint>
 
