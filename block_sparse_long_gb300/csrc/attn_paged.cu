@@ -21,7 +21,7 @@
 // list together, a CTA to a row tile, so that HBM is read once (the same 128K: 177 us apart, 140 together; then 125 as above).
 //
 // What bounds it (32 query over 8 kv heads of 128, 64-slot pages): 13-token trees of 24 ragged contexts 158 us, 5.7 TB/s; 64 tokens
-// after 128K 124 us, 4.3 TB/s and 1.1 PFLOP/s, a tile's chain of product, softmax, product (2000 cycles, of which the products run
+// after 128K 125 us, 4.3 TB/s and 1.1 PFLOP/s, a tile's chain of product, softmax, product (2000 cycles, of which the products run
 // 1024); one token after 900 slots 8.9 us, the chain of first loads, products and join.  Latent vectors of 512 + 64, 32 heads: one token after
 // 128K 43 us, 3.5 TB/s; 7 tokens of 24 ragged contexts 144 us: a tile (147 KB) fills shared memory, so a block of the next can only be copied
 // once the second product is done with it (6000 cycles a tile, of which the products run 3300).
@@ -81,7 +81,7 @@ struct Shape {
   static constexpr bool kRowLanes = N == 128;                    // a query row per TMEM lane: S = Q K^T, O = P V, P in TMEM
   static constexpr int kGroups = N == 16 ? 1 : N == 64 ? 4 : 2;  // warpgroups of the softmax
   static constexpr int NC = kRowLanes ? 1 : 16;                  // query rows of a softmax thread
-  // Row tiles of 64 have 640 threads and so 96 registers each, of which 20 bytes (latent vectors of 512) or 120 (of 256) spill.
+  // Row tiles of 64 have 640 threads and so 96 registers each, of which 20 bytes (latent vectors of 512) or 116 (of 256) spill.
   static constexpr int kThreads = 128 + 128 * kGroups;
   static constexpr int kBlocks = DV > 128 ? DV / 128 : 1;        // of 128 output values
   static constexpr int kPairs = LATENT ? DV / 128 : DK == 128 ? 2 : 1;      // ring slots of a tile; 64 + 64: K and V in one
@@ -322,6 +322,7 @@ struct alignas(1024) Smem {
   float2 ml[kMaxCluster][S::N];      // references and sums of the cluster's CTAs
   Start<S::N> start;
   int32_t odd_values;                // something among the new tokens' values is not finite
+  int32_t over;                      // a wait of the call had run out before this CTA started
   uint32_t tmem_base;
   int32_t abort_flag;
 };
@@ -410,7 +411,7 @@ __global__ void __launch_bounds__(S::kThreads, 1)
     const Start<N> st = find_start<N>(a, cta == 0);
     if (lane == 0) {
       sm.start = st;
-      if (over) sm.start.any = false;
+      sm.over = over;
       if (cta == 0 && (a.cu_seqlens[0] != 0 || a.cu_seqlens[a.num_reqs] > a.total_tokens)) cosa::report_status(a.status, cosa::kStatusBadInput);
     }
   } else if (warp == 1 && lane == 0) {
@@ -443,7 +444,8 @@ __global__ void __launch_bounds__(S::kThreads, 1)
   // for (more = ...) below: the pieces of this CTA
   Pieces<N> pieces = sm.start.rest;
   Piece pc = sm.start.first;
-  bool more = sm.start.any;
+  const bool works = sm.start.any && !sm.over;
+  bool more = works;
   const int pages_per_tile = kTile >> a.page_shift;
 
   if (warp == 0) {
@@ -709,6 +711,7 @@ __global__ void __launch_bounds__(S::kThreads, 1)
   } else if (warp == 3) {
     // =========================== what is to be joined ===========================
     if (lane == 0 && !a.whole) {
+      more = sm.start.any;      // whatever became of the call: join_kernel goes by what stands there
       Join none{}, mine{};
       const Shares shares(sm.start.total, a.walkers);
       for (; more; more = pieces.next(a, pc)) {
@@ -1114,7 +1117,7 @@ __global__ void __launch_bounds__(S::kThreads, 1)
       // others send theirs, weighted.  Every thread takes all three barriers: behind the first every CTA has started, so that its
       // shared memory may be written (one without tiles would be here before), behind the second the references are there and
       // the rings are free to receive, behind the third the shares are whole.
-      const bool mine = sm.start.any && ok;
+      const bool mine = works && ok;
       const int rank = cta % a.cluster, width = DV / a.cluster;
       cluster_wait();
       if (mine && owns) {
@@ -1197,9 +1200,9 @@ __global__ void __launch_bounds__(kWide ? kWideThreads : kJoinThreads) join_kern
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   cosa_kv::wait_for_stream();
   const Join j = a.joins[blockIdx.x];
-  // (the bounds hold whatever another call might have made of the workspace)
+  // (the bounds hold whatever another call might have made of the workspace; without sign, so that the sum does not wrap)
   if (j.parts < 2 || j.parts > kCtas || j.first < 0 || j.first >= 2 * kCtas || j.next < 0 || j.step < 0 ||
-      j.step > 2 * kCtas || j.next + j.step * (j.parts - 2) >= 2 * kCtas)
+      j.step > 2 * kCtas || static_cast<uint32_t>(j.next) + j.step * (j.parts - 2) >= 2u * kCtas)
     return;
   const int parts = j.parts, seg = blockIdx.z;
   const int c = kWide ? blockIdx.y : blockIdx.y * 8 + warp;      // row of the tile

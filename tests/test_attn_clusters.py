@@ -34,4 +34,4 @@ def test_a_warp_that_gave_up_leaves_the_join_out():
     pieces = softmax[softmax.index("more = pieces.next"):softmax.index("cluster_wait()")]
     waits = re.findall(r"if \(!meet\(\)\)([^;]*;)", pieces)
     assert len(waits) == 4 and all("ok = false" in w for w in waits)
-    assert "sm.start.any && ok;" in softmax
+    assert "= works && ok;" in softmax

@@ -25,3 +25,14 @@ def test_keys_count_as_in_flight_once_they_are_copied():
     assert copies.index("&krmap") < copies.index("kring.next();") < copies.index("if (values == S::kSlots)") < copies.index("vring.next();")
     drain = text[text.index("every copy lands before the CTA ends"):]
     assert "next()" not in drain[:drain.index("__syncwarp();")]
+
+
+def test_the_list_of_joins_is_written_whatever_became_of_the_call():
+    """A CTA that does nothing, since a wait had run out before it, leaves no entry as the workspace had it; and the join does not
+    take an index that could wrap in its check."""
+    text = open(os.path.join(ROOT, "block_sparse_long_gb300", "csrc", "attn_paged.cu")).read()
+    joins = text[text.index("what is to be joined ===="):]
+    assert "more = sm.start.any;" in joins[:joins.index("for (")]
+    assert "const bool works = sm.start.any && !sm.over;" in text and "mine = works && ok;" in text
+    check = text[text.index("const Join j = a.joins[blockIdx.x];"):]
+    assert "static_cast<uint32_t>(j.next) + j.step * (j.parts - 2) >= 2u * kCtas" in check[:check.index("return;")]

@@ -209,6 +209,28 @@ def test_ctas_that_start_after_a_timeout_end_at_once(form):
         c.check(out, lse)
 
 
+@pytest.mark.parametrize("name", ["whole", "cluster 8", "list, by item, wide", "list, by item", "list, by cta"])
+def test_calls_after_a_timeout_touch_nothing_else(name):
+    """A status that still says so: no CTA works, in workspaces of any content, and nothing but the outputs' rows is written."""
+    for _, lens, new, Hq, Hkv, latent, d, slots in (e for e in PATHS if e[0] == name):
+        c = Paged(8, lens, new, Hq, Hkv, d, 64, latent=latent, tree=True, pitch=None if slots is None else slots // 64)
+        assert path(c.p, latent) == name
+        size = (C.cosa_latent_attention_workspace_size if latent else C.cosa_tree_attention_workspace_size)(c.p)
+        for fill in (0x00, 0x7F, 0xFF):
+            ws = torch.full((size + 4096,), fill, dtype=torch.uint8, device=DEV)
+            out, lse = c.buffers()
+            guard, st, t0 = out.clone(), new_status(), time.time()
+            st.fill_(-4)
+            c.call(out=out, lse=lse, workspace=ws[:size], status=st)
+            torch.cuda.synchronize()
+            assert int(st) == -4 and time.time() - t0 < 1.5
+            assert torch.equal(out[c.T:], guard[c.T:]) and (ws[size:] == fill).all()
+            st = new_status()
+            c.call(out=out, lse=lse, workspace=ws[:size], status=st)
+            ok(st)
+            c.check(out, lse)
+
+
 # ---------------------------------------------------------------------------------------------------------------
 # a step with drafted tokens: norm and rotation, tree attention, commit, and the next step over what was kept
 # ---------------------------------------------------------------------------------------------------------------
