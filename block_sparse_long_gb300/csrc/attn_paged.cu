@@ -1358,6 +1358,7 @@ cudaError_t launch_shape(const PagedLaunch& L, cudaStream_t stream) {
   // One token each, list / whole / cluster: 1 context of 900 (32 heads over 8 of 128) 10.3 / 11.7 / 8.9 us, 4 of 900 13.4 / 12.1 / 10.9,
   // 64 of 300 33.0 / 30.4 / -, 4 of 4000 22.3 / 28.3 / -; latent 512 of 16 heads: 9 of 900 14.6 / 26.2 / 13.2, 150 of 900 46.0 / 41.4 / -,
   // 200 of 900 62 / 69 / -.  Not always the best: one latent token after 900 11.8 / 25.9 / 12.6, 64 tokens after 900 17.3 / 16.4 / 18.5.
+  // (19 clusters of eight, the most that there are, run at once: a call of them whose waits run out takes one wait's time.)
   // All of these have equal lengths, and what the rule knows is max_seqlen and an upper bound of the items.  A batch of other lengths can wait
   // for few long items where it takes whole ones or clusters (counted in tiles: 31 requests, one of 128K and thirty of 1000, 2050 to a CTA
   // where the list has 68), and where rows fill their row tile exactly the bound is twice the items, so that half of the card may idle.
